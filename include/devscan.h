@@ -307,6 +307,128 @@ devscan_status radix_sort_u32(uint32_t *keys, uint32_t *tmp, size_t n, cudaStrea
 devscan_status radix_sort_digits_u32(uint32_t *keys, uint32_t *tmp, size_t n, cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Paged key/value cache: block tables and slot maps from request lengths (P1
+ * section 一: a scan of counts gives output positions; the rest is a
+ * load-balanced expansion).  The cache is made of pages of `page` tokens.  A
+ * request is a row of the block table: entry j of row i, table[i * stride +
+ * j], is the page that holds the row's tokens j * page .. (j + 1) * page - 1,
+ * and a row with c tokens has its first ceil(c / page) entries in use; the
+ * others are neither read nor written.  Token t of the cache's slot s =
+ * entry * page + t % page is a position in the cache.  The unused pages are a
+ * stack: pages[0 .. *free).
+ *
+ *   table   : device int32[rows][stride], stride >= width entries per row
+ *             (0 <= width, of which a row may use all);
+ *   rows    : at most INT32_MAX - 1; 0 is allowed (only the totals are
+ *             written);  width, page, pool : int32, page >= 1;
+ *   cached  : device int32[rows], tokens of each row already in the cache;
+ *   fresh   : device int32[rows], tokens to be added in this step (0: idle);
+ *   pages   : device int32[pool], the stack, pool < INT32_MAX entries;
+ *   free    : device int32, its height (values outside 0 .. pool count as the
+ *             nearer of the two);
+ *   left    : device int32, written with the height after the call.  It must
+ *             not be `free` itself: blocks of one launch read the one while
+ *             another writes the other.  A loop uses two words in turn.
+ *
+ * block_table_extend_i32 opens the pages that the new tokens need: row i
+ * takes need = ceil((cached + fresh) / page) - ceil(cached / page) pages from
+ * the top of the stack and appends them to its entries.  Rows are served in
+ * order while the pool lasts: with end(i) the sum of need up to and including
+ * i, row i is granted iff end(i) <= *free; a row that needs none is always
+ * granted; a row with a negative length, or whose tokens do not fit in
+ * `width` entries, is never granted and takes none.  granted: device
+ * uint8[rows], 1 or 0; a row that is not granted is left as it was.  The call
+ * reads `pages` and does not change it, so repeating it repeats its result.
+ *
+ * slot_map_i32 lists the places of the new tokens, packed in row order:
+ * starts[i] = fresh(0) + ... + fresh(i - 1), and for the token at g, the
+ * (g - starts[i])-th new one of row i:
+ *   positions[g] = cached(i) + g - starts[i],   row_ids[g] = i,
+ *   slots[g] = its slot in the cache, in 64 bits.
+ *   granted : device uint8[rows] or NULL; a row whose flag is 0 brings no
+ *             tokens (neither does one with fresh <= 0);
+ *   tokens  : length of slots, positions and row_ids (at most INT32_MAX).
+ *             Places past the last token get -1 in all three (a batch padded
+ *             to a fixed size); tokens past the last place are left out, and
+ *             starts still counts them;
+ *   starts  : device int32[rows + 1]; slots : device int64[tokens];
+ *   positions, row_ids : device int32[tokens].
+ * A token past the table's width, or whose entry is negative, gets slot -1; a
+ * position outside 0 .. INT32_MAX gets position and slot -1.
+ *
+ * block_table_release_i32 gives back the pages of rows that ended: for every
+ * row with done[i] != 0, in row order, its min(ceil(cached / page), width)
+ * entries go on top of the stack; *left = *free plus their number.  A row
+ * that would not fit in pool entries, and those after it, give back nothing.
+ * The table is not changed.  done: device uint8[rows].
+ *
+ * Sums saturate at INT32_MAX.  No buffer that is written may overlap any
+ * other (DEVSCAN_ERR_INVALID); pointers are aligned to their element size.
+ * Traffic: 8 bytes per page moved, 16 to 20 per token, 4 to 9 per row.  One
+ * launch up to 8,192 rows; above, two, with 4 bytes per row of per-stream
+ * scratch allocated stream-ordered on first use (DEVSCAN_ERR_NOMEM).
+ * ------------------------------------------------------------------------- */
+devscan_status block_table_extend_i32(int32_t *table, size_t stride, size_t rows, int width, const int32_t *cached,
+                                      const int32_t *fresh, int page, const int32_t *pages, size_t pool,
+                                      const int32_t *free, uint8_t *granted, int32_t *left, cudaStream_t stream);
+devscan_status slot_map_i32(const int32_t *table, size_t stride, size_t rows, int width, const int32_t *cached,
+                            const int32_t *fresh, const uint8_t *granted, int page, size_t tokens, int32_t *starts,
+                            int64_t *slots, int32_t *positions, int32_t *row_ids, cudaStream_t stream);
+devscan_status block_table_release_i32(const int32_t *table, size_t stride, size_t rows, int width,
+                                       const int32_t *cached, const uint8_t *done, int page, int32_t *pages,
+                                       size_t pool, const int32_t *free, int32_t *left, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Token draw: one token per row of logits, with temperature, top-k, top-p and
+ * min-p, from given random numbers (P2 section 4 uses a scan to select and to
+ * place; here a selection finds the kept tokens and a prefix of their mass
+ * cuts them off).  For a row x[0 .. vocab) with temperature T:
+ *   M = max x,  w_i = exp((x_i - M) / T),
+ * tokens ordered by logit descending, equal logits by index ascending, and
+ * kept by three rules in this order:
+ *   top-k : the first top_k of the order (top_k <= 0 or >= vocab: all);
+ *   top-p : of those, each whose mass ahead of it (the sum of w before it in
+ *           the order) is below top_p times the sum over the first rule's
+ *           tokens (top_p >= 1: all);
+ *   min-p : of those, each with w_i >= min_p;
+ * the first of the order always stays.  With noise_i > 0 drawn from Exp(1),
+ *   token = the kept i with the largest w_i / noise_i (equal: lowest index),
+ * which falls on i with probability w_i / (sum of kept w), and
+ *   logprob = (x_token - M) / T - log(sum of kept w).
+ * T <= 0 (or NaN), or noise == NULL, takes the first of the order (greedy;
+ * logprob 0).  A NaN logit counts as -inf, and -inf is never drawn; a row
+ * with nothing above -inf gets token -1 and logprob -inf.  If the largest is
+ * +inf, the draw is among those that are.
+ *
+ *   logits   : device T[rows][logits_stride] (f16 and bf16 as their 16 bits),
+ *              aligned to the element; vocab <= logits_stride;
+ *   noise    : device float[rows][noise_stride], or NULL;
+ *   temperature, top_p, min_p : device float[rows]; top_k : device
+ *              int32[rows]; each may be NULL (1, off, off, off);
+ *   tokens   : device int32[rows]; logprobs : device float[rows] or NULL;
+ *              neither may overlap another buffer (DEVSCAN_ERR_INVALID);
+ *   rows     : at most INT32_MAX; 0 is a no-op;
+ *   vocab    : 1 .. DEVSCAN_SAMPLE_MAX_VOCAB, else DEVSCAN_ERR_INVALID.
+ * Weights and their sums are fp32 or wider; the masses that top-p compares
+ * are exact sums of w rounded to 2^-31, so the kept set does not depend on
+ * the order of the adds.
+ * ------------------------------------------------------------------------- */
+#define DEVSCAN_SAMPLE_MAX_VOCAB ((size_t)1 << 18)
+
+devscan_status sample_tokens_f32(const float *logits, size_t rows, size_t vocab, size_t logits_stride,
+                                 const float *noise, size_t noise_stride, const float *temperature,
+                                 const int32_t *top_k, const float *top_p, const float *min_p, int32_t *tokens,
+                                 float *logprobs, cudaStream_t stream);
+devscan_status sample_tokens_f16(const uint16_t *logits, size_t rows, size_t vocab, size_t logits_stride,
+                                 const float *noise, size_t noise_stride, const float *temperature,
+                                 const int32_t *top_k, const float *top_p, const float *min_p, int32_t *tokens,
+                                 float *logprobs, cudaStream_t stream);
+devscan_status sample_tokens_bf16(const uint16_t *logits, size_t rows, size_t vocab, size_t logits_stride,
+                                  const float *noise, size_t noise_stride, const float *temperature,
+                                  const int32_t *top_k, const float *top_p, const float *min_p, int32_t *tokens,
+                                  float *logprobs, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Status and housekeeping.
  * ------------------------------------------------------------------------- */
 

@@ -17,6 +17,7 @@ from ._lib import DevscanError, OPS, load
 __all__ = ["scan_inclusive", "scan_exclusive", "scan_inclusive_carry", "scan_exclusive_carry", "reduce",
            "sharded_scan", "exchange_totals", "compact", "split_bit", "radix_sort", "radix_sort_digits", "scan_host",
            "compact_greater", "bracket_scan", "segmented_scan_inclusive", "segmented_scan_exclusive",
+           "sample_tokens", "block_table_extend", "slot_map", "block_table_release",
            "device_status", "set_carry_mode", "stream_release", "selftest_stalled_wait", "DevscanError",
            "load"]
 
@@ -314,6 +315,167 @@ def radix_sort_digits(keys: torch.Tensor, tmp: torch.Tensor | None = None, strea
     _lib.check(load().radix_sort_digits_u32(keys.data_ptr(), tmp.data_ptr(), keys.numel(),
                                             _stream_handle(stream)), "radix_sort_digits_u32")
     return keys
+
+
+def _check_vector(t: torch.Tensor, name: str, dtype: torch.dtype, size: int) -> None:
+    _check_cuda(t, name)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.numel() != size:
+        raise ValueError(f"{name} must hold {size} elements")
+
+
+def _check_matrix(t: torch.Tensor, name: str) -> int:
+    """A 2-d CUDA tensor whose rows are contiguous; returns its row stride."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    rows, width = t.shape
+    stride, step = t.stride()
+    if width > 1 and step != 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    if rows <= 1 or width == 0:
+        return max(width, 1)
+    if stride < width:
+        raise ValueError(f"{name}'s rows must not overlap")
+    return stride
+
+
+def _check_table(table: torch.Tensor, page_size: int) -> int:
+    stride = _check_matrix(table, "table")
+    if table.dtype != torch.int32:
+        raise TypeError("table must be int32")
+    if page_size < 1:
+        raise ValueError("page_size must be positive")
+    return stride
+
+
+def block_table_extend(table: torch.Tensor, cached: torch.Tensor, fresh: torch.Tensor, pages: torch.Tensor,
+                       free: torch.Tensor, page_size: int, granted: torch.Tensor | None = None,
+                       left: torch.Tensor | None = None, stream=None):
+    """Open the pages that each row's ``fresh`` new tokens need beyond its
+    ``cached`` ones: they are taken from the top of the stack ``pages[:free]``
+    in row order, while it lasts, and written into the rows of ``table`` (int32,
+    in place).  Returns (granted, left): uint8 per row, 1 where the row's
+    tokens have their pages, and the stack's height afterwards (one int32,
+    another tensor than ``free``)."""
+    stride = _check_table(table, page_size)
+    rows, width = table.shape
+    _check_vector(cached, "cached", torch.int32, rows)
+    _check_vector(fresh, "fresh", torch.int32, rows)
+    _check_vector(pages, "pages", torch.int32, pages.numel())
+    _check_vector(free, "free", torch.int32, 1)
+    if granted is None:
+        granted = torch.empty(rows, dtype=torch.uint8, device=table.device)
+    if left is None:
+        left = torch.empty(1, dtype=torch.int32, device=table.device)
+    _check_vector(granted, "granted", torch.uint8, rows)
+    _check_vector(left, "left", torch.int32, 1)
+    _lib.check(load().block_table_extend_i32(table.data_ptr(), stride, rows, width, cached.data_ptr(),
+                                             fresh.data_ptr(), int(page_size), pages.data_ptr(), pages.numel(),
+                                             free.data_ptr(), granted.data_ptr(), left.data_ptr(),
+                                             _stream_handle(stream)), "block_table_extend_i32")
+    return granted, left
+
+
+def slot_map(table: torch.Tensor, cached: torch.Tensor, fresh: torch.Tensor, page_size: int, tokens: int,
+             granted: torch.Tensor | None = None, out=None, stream=None):
+    """Places of the new tokens, packed in row order and padded with -1 to
+    ``tokens``.  Returns (starts, slots, positions, rows): int32 starts of
+    every row and the total, and for each token its int64 slot in the paged
+    cache, its int32 position in its row, and its row.  ``granted`` (uint8)
+    leaves out the rows whose flag is 0; ``out`` passes the four tensors."""
+    stride = _check_table(table, page_size)
+    rows, width = table.shape
+    _check_vector(cached, "cached", torch.int32, rows)
+    _check_vector(fresh, "fresh", torch.int32, rows)
+    if granted is not None:
+        _check_vector(granted, "granted", torch.uint8, rows)
+    tokens = int(tokens)
+    if tokens < 0:
+        raise ValueError("tokens must not be negative")
+    if out is None:
+        new = lambda n, dtype: torch.empty(n, dtype=dtype, device=table.device)  # noqa: E731
+        out = (new(rows + 1, torch.int32), new(tokens, torch.int64), new(tokens, torch.int32),
+               new(tokens, torch.int32))
+    starts, slots, positions, row_ids = out
+    _check_vector(starts, "starts", torch.int32, rows + 1)
+    _check_vector(slots, "slots", torch.int64, tokens)
+    _check_vector(positions, "positions", torch.int32, tokens)
+    _check_vector(row_ids, "rows", torch.int32, tokens)
+    _lib.check(load().slot_map_i32(table.data_ptr(), stride, rows, width, cached.data_ptr(), fresh.data_ptr(),
+                                   None if granted is None else granted.data_ptr(), int(page_size), tokens,
+                                   starts.data_ptr(), slots.data_ptr(), positions.data_ptr(), row_ids.data_ptr(),
+                                   _stream_handle(stream)), "slot_map_i32")
+    return starts, slots, positions, row_ids
+
+
+def block_table_release(table: torch.Tensor, cached: torch.Tensor, done: torch.Tensor, pages: torch.Tensor,
+                        free: torch.Tensor, page_size: int, left: torch.Tensor | None = None,
+                        stream=None) -> torch.Tensor:
+    """Give the pages of the rows with a nonzero ``done`` (uint8) back: their
+    entries go on top of the stack ``pages[:free]`` in row order.  Returns the
+    stack's height afterwards (one int32, another tensor than ``free``).  The
+    table is not changed; the caller sets the ended rows' lengths to 0."""
+    stride = _check_table(table, page_size)
+    rows, width = table.shape
+    _check_vector(cached, "cached", torch.int32, rows)
+    _check_vector(done, "done", torch.uint8, rows)
+    _check_vector(pages, "pages", torch.int32, pages.numel())
+    _check_vector(free, "free", torch.int32, 1)
+    if left is None:
+        left = torch.empty(1, dtype=torch.int32, device=table.device)
+    _check_vector(left, "left", torch.int32, 1)
+    _lib.check(load().block_table_release_i32(table.data_ptr(), stride, rows, width, cached.data_ptr(),
+                                              done.data_ptr(), int(page_size), pages.data_ptr(), pages.numel(),
+                                              free.data_ptr(), left.data_ptr(), _stream_handle(stream)),
+               "block_table_release_i32")
+    return left
+
+
+_LOGIT_SUFFIX = {torch.float32: "f32", torch.float16: "f16", torch.bfloat16: "bf16"}
+
+
+def sample_tokens(logits: torch.Tensor, noise: torch.Tensor | None = None, temperature: torch.Tensor | None = None,
+                  top_k: torch.Tensor | None = None, top_p: torch.Tensor | None = None,
+                  min_p: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                  logprobs: torch.Tensor | None = None, stream=None):
+    """Draw one token from each row of ``logits`` (fp32, fp16 or bf16, rows
+    contiguous) with that row's ``temperature``, ``top_k`` (int32), ``top_p``
+    and ``min_p`` (fp32, each optional), by an exponential race with the given
+    ``noise`` (fp32 of the logits' shape, positive, Exp(1)).  Without noise, or
+    where the temperature is 0, the largest logit is taken.  Returns (tokens,
+    logprobs): int32 per row (-1 for a row with nothing above -inf) and fp32
+    log-probabilities under the truncated distribution."""
+    stride = _check_matrix(logits, "logits")
+    rows, vocab = logits.shape
+    suffix = _LOGIT_SUFFIX.get(logits.dtype)
+    if suffix is None:
+        raise TypeError(f"unsupported dtype {logits.dtype} (float32, float16, bfloat16)")
+    noise_stride = vocab
+    if noise is not None:
+        noise_stride = _check_matrix(noise, "noise")
+        if noise.dtype != torch.float32:
+            raise TypeError("noise must be float32")
+        if noise.shape != logits.shape:
+            raise ValueError("noise must have the logits' shape")
+    for t, name, dtype in ((temperature, "temperature", torch.float32), (top_k, "top_k", torch.int32),
+                           (top_p, "top_p", torch.float32), (min_p, "min_p", torch.float32)):
+        if t is not None:
+            _check_vector(t, name, dtype, rows)
+    if out is None:
+        out = torch.empty(rows, dtype=torch.int32, device=logits.device)
+    if logprobs is None:
+        logprobs = torch.empty(rows, dtype=torch.float32, device=logits.device)
+    _check_vector(out, "out", torch.int32, rows)
+    _check_vector(logprobs, "logprobs", torch.float32, rows)
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    name = f"sample_tokens_{suffix}"
+    _lib.check(getattr(load(), name)(logits.data_ptr(), rows, vocab, stride, ptr(noise), noise_stride,
+                                     ptr(temperature), ptr(top_k), ptr(top_p), ptr(min_p), out.data_ptr(),
+                                     logprobs.data_ptr(), _stream_handle(stream)), name)
+    return out, logprobs
 
 
 def scan_host(x_host: torch.Tensor, inclusive: bool = False, op: str = "add", device="cuda",

@@ -24,6 +24,7 @@ CARRY_SCAN_SYMBOLS = tuple(f"scan_{d}_carry_{t}" for d in ("inclusive", "exclusi
 REDUCE_SYMBOLS = ("reduce_i32", "reduce_u32", "reduce_f32")
 SEGSCAN_SYMBOLS = tuple(f"segmented_scan_{d}_{t}" for d in ("inclusive", "exclusive")
                         for t in ("i32", "u32", "f32"))
+SAMPLE_SYMBOLS = ("sample_tokens_f32", "sample_tokens_f16", "sample_tokens_bf16")
 
 
 class DevscanError(RuntimeError):
@@ -79,6 +80,16 @@ def load() -> ctypes.CDLL:
         lib.bracket_scan_i32.restype = i
         lib.radix_sort_digits_u32.argtypes = [vp, vp, sz, vp]
         lib.radix_sort_digits_u32.restype = i
+        lib.block_table_extend_i32.argtypes = [vp, sz, sz, i, vp, vp, i, vp, sz, vp, vp, vp, vp]
+        lib.block_table_extend_i32.restype = i
+        lib.slot_map_i32.argtypes = [vp, sz, sz, i, vp, vp, vp, i, sz, vp, vp, vp, vp, vp]
+        lib.slot_map_i32.restype = i
+        lib.block_table_release_i32.argtypes = [vp, sz, sz, i, vp, vp, i, vp, sz, vp, vp, vp]
+        lib.block_table_release_i32.restype = i
+        for name in SAMPLE_SYMBOLS:
+            fn = getattr(lib, name)
+            fn.argtypes = [vp, sz, sz, sz, vp, sz, vp, vp, vp, vp, vp, vp, vp]
+            fn.restype = i
         lib.devscan_device_status.argtypes = [vp]
         lib.devscan_device_status.restype = i
         lib.devscan_status_string.argtypes = [i]

@@ -213,6 +213,93 @@ devscan_status segscan_common(ElemType type, bool inclusive, const void *in, con
                                     carry_mode(), ws, kSpinLimit, stream));
 }
 
+bool misaligned(const void *p, size_t size) { return reinterpret_cast<uintptr_t>(p) % size != 0; }
+
+// A buffer of a call; null for an optional argument, or of no bytes.
+struct Span {
+    const void *p;
+    size_t bytes;
+    bool empty() const { return p == nullptr || bytes == 0; }
+};
+
+// Whether one of the buffers that a call writes overlaps another of its
+// buffers.
+template <size_t W, size_t R>
+bool written_overlap(const Span (&written)[W], const Span (&read)[R])
+{
+    for (size_t i = 0; i < W; ++i) {
+        if (written[i].empty()) continue;
+        for (size_t j = i + 1; j < W; ++j)
+            if (!written[j].empty() && overlaps(written[i].p, written[i].bytes, written[j].p, written[j].bytes))
+                return true;
+        for (size_t j = 0; j < R; ++j)
+            if (!read[j].empty() && overlaps(written[i].p, written[i].bytes, read[j].p, read[j].bytes))
+                return true;
+    }
+    return false;
+}
+
+// Bytes of a matrix of `rows` rows, `stride` elements apart, `width` used in
+// the last; false if that passes 2^62.
+bool matrix_bytes(size_t rows, size_t stride, size_t width, size_t size, size_t *bytes)
+{
+    *bytes = 0;
+    if (rows == 0 || width == 0) return true;
+    const size_t most = (size_t(1) << 62) / size;
+    if (stride != 0 && rows - 1 > (most - width) / stride) return false;
+    *bytes = ((rows - 1) * stride + width) * size;
+    return true;
+}
+
+// What the three block table calls check alike.
+devscan_status paged_check(const void *table, size_t stride, size_t rows, int width, int page, size_t *table_bytes)
+{
+    if (width < 0 || page < 1 || rows >= static_cast<size_t>(INT32_MAX) || stride < static_cast<size_t>(width))
+        return DEVSCAN_ERR_INVALID;
+    if (!matrix_bytes(rows, stride, static_cast<size_t>(width), 4, table_bytes)) return DEVSCAN_ERR_INVALID;
+    if (*table_bytes > 0 && (table == nullptr || misaligned(table, 4))) return DEVSCAN_ERR_INVALID;
+    return DEVSCAN_OK;
+}
+
+// The workspace, and scratch for the scanned ends where they do not fit in a
+// block's shared memory.
+devscan_status paged_scratch(size_t rows, cudaStream_t stream, Workspace *ws, int32_t **scratch)
+{
+    *scratch = nullptr;
+    const devscan_status st = acquire(stream, 1, ws);
+    if (st != DEVSCAN_OK || rows <= static_cast<size_t>(kPagedSharedRows)) return st;
+    void *p = nullptr;
+    const devscan_status got = acquire_extra(stream, rows * sizeof(int32_t), &p);
+    *scratch = static_cast<int32_t *>(p);
+    return got;
+}
+
+devscan_status sample_common(LogitType type, const void *logits, size_t rows, size_t vocab, size_t stride,
+                             const float *noise, size_t noise_stride, const SampleAsk &ask, int32_t *tokens,
+                             float *logprobs, cudaStream_t stream)
+{
+    const size_t size = type == LogitType::F32 ? 4 : 2;
+    if (rows > static_cast<size_t>(INT32_MAX)) return DEVSCAN_ERR_INVALID;
+    if (vocab < 1 || vocab > DEVSCAN_SAMPLE_MAX_VOCAB || stride < vocab) return DEVSCAN_ERR_INVALID;
+    if (noise != nullptr && noise_stride < vocab) return DEVSCAN_ERR_INVALID;
+    if (rows == 0) return DEVSCAN_OK;
+    if (logits == nullptr || tokens == nullptr) return DEVSCAN_ERR_INVALID;
+    if (misaligned(logits, size) || misaligned(noise, 4) || misaligned(ask.temperature, 4) ||
+        misaligned(ask.top_k, 4) || misaligned(ask.top_p, 4) || misaligned(ask.min_p, 4) || misaligned(tokens, 4) ||
+        misaligned(logprobs, 4))
+        return DEVSCAN_ERR_INVALID;
+    size_t x_bytes = 0, q_bytes = 0;
+    if (!matrix_bytes(rows, stride, vocab, size, &x_bytes)) return DEVSCAN_ERR_INVALID;
+    if (noise != nullptr && !matrix_bytes(rows, noise_stride, vocab, 4, &q_bytes)) return DEVSCAN_ERR_INVALID;
+    const size_t each = rows * 4;
+    const Span written[] = {{tokens, each}, {logprobs, each}};
+    const Span read[] = {{logits, x_bytes},  {noise, q_bytes},  {ask.temperature, each},
+                         {ask.top_k, each},  {ask.top_p, each}, {ask.min_p, each}};
+    if (written_overlap(written, read)) return DEVSCAN_ERR_INVALID;
+    return from_cuda(launch_sample(type, logits, rows, vocab, stride, noise, noise_stride, ask, tokens, logprobs,
+                                   stream));
+}
+
 }  // namespace
 }  // namespace devscan
 
@@ -508,6 +595,105 @@ devscan_status radix_sort_digits_u32(uint32_t *keys, uint32_t *tmp, size_t n, cu
         std::swap(src, dst);
     }
     return DEVSCAN_OK;
+}
+
+devscan_status block_table_extend_i32(int32_t *table, size_t stride, size_t rows, int width, const int32_t *cached,
+                                      const int32_t *fresh, int page, const int32_t *pages, size_t pool,
+                                      const int32_t *free, uint8_t *granted, int32_t *left, cudaStream_t stream)
+{
+    size_t table_bytes = 0;
+    devscan_status st = paged_check(table, stride, rows, width, page, &table_bytes);
+    if (st != DEVSCAN_OK) return st;
+    if (pool >= static_cast<size_t>(INT32_MAX) || (pool > 0 && pages == nullptr)) return DEVSCAN_ERR_INVALID;
+    if (free == nullptr || left == nullptr) return DEVSCAN_ERR_INVALID;
+    if (rows > 0 && (cached == nullptr || fresh == nullptr || granted == nullptr)) return DEVSCAN_ERR_INVALID;
+    if (misaligned(cached, 4) || misaligned(fresh, 4) || misaligned(pages, 4) || misaligned(free, 4) ||
+        misaligned(left, 4))
+        return DEVSCAN_ERR_INVALID;
+    const Span written[] = {{table, table_bytes}, {granted, rows}, {left, 4}};
+    const Span read[] = {{cached, rows * 4}, {fresh, rows * 4}, {pages, pool * 4}, {free, 4}};
+    if (written_overlap(written, read)) return DEVSCAN_ERR_INVALID;
+    Workspace ws;
+    int32_t *scratch = nullptr;
+    st = paged_scratch(rows, stream, &ws, &scratch);
+    if (st != DEVSCAN_OK) return st;
+    return from_cuda(launch_block_table_extend(table, stride, static_cast<int>(rows), width, cached, fresh, page,
+                                               pages, static_cast<int>(pool), free, granted, left, scratch, ws,
+                                               stream));
+}
+
+devscan_status slot_map_i32(const int32_t *table, size_t stride, size_t rows, int width, const int32_t *cached,
+                            const int32_t *fresh, const uint8_t *granted, int page, size_t tokens, int32_t *starts,
+                            int64_t *slots, int32_t *positions, int32_t *row_ids, cudaStream_t stream)
+{
+    size_t table_bytes = 0;
+    devscan_status st = paged_check(table, stride, rows, width, page, &table_bytes);
+    if (st != DEVSCAN_OK) return st;
+    if (tokens > static_cast<size_t>(INT32_MAX) || starts == nullptr) return DEVSCAN_ERR_INVALID;
+    if (rows > 0 && (cached == nullptr || fresh == nullptr)) return DEVSCAN_ERR_INVALID;
+    if (tokens > 0 && (slots == nullptr || positions == nullptr || row_ids == nullptr)) return DEVSCAN_ERR_INVALID;
+    if (misaligned(cached, 4) || misaligned(fresh, 4) || misaligned(starts, 4) || misaligned(slots, 8) ||
+        misaligned(positions, 4) || misaligned(row_ids, 4))
+        return DEVSCAN_ERR_INVALID;
+    const Span written[] = {{starts, (rows + 1) * 4}, {slots, tokens * 8}, {positions, tokens * 4},
+                            {row_ids, tokens * 4}};
+    const Span read[] = {{table, table_bytes}, {cached, rows * 4}, {fresh, rows * 4}, {granted, rows}};
+    if (written_overlap(written, read)) return DEVSCAN_ERR_INVALID;
+    Workspace ws;
+    int32_t *scratch = nullptr;
+    st = paged_scratch(rows, stream, &ws, &scratch);
+    if (st != DEVSCAN_OK) return st;
+    return from_cuda(launch_slot_map(table, stride, static_cast<int>(rows), width, cached, fresh, granted, page,
+                                     static_cast<int>(tokens), starts, slots, positions, row_ids, scratch, ws,
+                                     stream));
+}
+
+devscan_status block_table_release_i32(const int32_t *table, size_t stride, size_t rows, int width,
+                                       const int32_t *cached, const uint8_t *done, int page, int32_t *pages,
+                                       size_t pool, const int32_t *free, int32_t *left, cudaStream_t stream)
+{
+    size_t table_bytes = 0;
+    devscan_status st = paged_check(table, stride, rows, width, page, &table_bytes);
+    if (st != DEVSCAN_OK) return st;
+    if (pool >= static_cast<size_t>(INT32_MAX) || (pool > 0 && pages == nullptr)) return DEVSCAN_ERR_INVALID;
+    if (free == nullptr || left == nullptr) return DEVSCAN_ERR_INVALID;
+    if (rows > 0 && (cached == nullptr || done == nullptr)) return DEVSCAN_ERR_INVALID;
+    if (misaligned(cached, 4) || misaligned(pages, 4) || misaligned(free, 4) || misaligned(left, 4))
+        return DEVSCAN_ERR_INVALID;
+    const Span written[] = {{pages, pool * 4}, {left, 4}};
+    const Span read[] = {{table, table_bytes}, {cached, rows * 4}, {done, rows}, {free, 4}};
+    if (written_overlap(written, read)) return DEVSCAN_ERR_INVALID;
+    Workspace ws;
+    int32_t *scratch = nullptr;
+    st = paged_scratch(rows, stream, &ws, &scratch);
+    if (st != DEVSCAN_OK) return st;
+    return from_cuda(launch_block_table_release(table, stride, static_cast<int>(rows), width, cached, done, page,
+                                                pages, static_cast<int>(pool), free, left, scratch, ws, stream));
+}
+
+devscan_status sample_tokens_f32(const float *logits, size_t rows, size_t vocab, size_t logits_stride,
+                                 const float *noise, size_t noise_stride, const float *temperature,
+                                 const int32_t *top_k, const float *top_p, const float *min_p, int32_t *tokens,
+                                 float *logprobs, cudaStream_t stream)
+{
+    return sample_common(LogitType::F32, logits, rows, vocab, logits_stride, noise, noise_stride,
+                         {temperature, top_k, top_p, min_p}, tokens, logprobs, stream);
+}
+devscan_status sample_tokens_f16(const uint16_t *logits, size_t rows, size_t vocab, size_t logits_stride,
+                                 const float *noise, size_t noise_stride, const float *temperature,
+                                 const int32_t *top_k, const float *top_p, const float *min_p, int32_t *tokens,
+                                 float *logprobs, cudaStream_t stream)
+{
+    return sample_common(LogitType::F16, logits, rows, vocab, logits_stride, noise, noise_stride,
+                         {temperature, top_k, top_p, min_p}, tokens, logprobs, stream);
+}
+devscan_status sample_tokens_bf16(const uint16_t *logits, size_t rows, size_t vocab, size_t logits_stride,
+                                  const float *noise, size_t noise_stride, const float *temperature,
+                                  const int32_t *top_k, const float *top_p, const float *min_p, int32_t *tokens,
+                                  float *logprobs, cudaStream_t stream)
+{
+    return sample_common(LogitType::BF16, logits, rows, vocab, logits_stride, noise, noise_stride,
+                         {temperature, top_k, top_p, min_p}, tokens, logprobs, stream);
 }
 
 devscan_status devscan_device_status(cudaStream_t stream)

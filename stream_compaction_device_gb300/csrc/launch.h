@@ -156,4 +156,32 @@ cudaError_t launch_radix_pass(const uint32_t *src, uint32_t *dst, size_t n, int 
                               const Workspace &ws, unsigned spin_limit, cudaStream_t s);
 size_t radix_hist_words(size_t n);
 
+// Block tables and slot maps.  Up to kPagedSharedRows rows every block scans
+// the row counts into its own shared memory (one launch); above, a first
+// launch leaves the scanned ends in `scratch` (rows words).
+constexpr int kPagedSharedRows = 8192;
+cudaError_t launch_block_table_extend(int32_t *table, size_t stride, int rows, int width, const int32_t *cached,
+                                      const int32_t *fresh, int page, const int32_t *pages, int pool,
+                                      const int32_t *free_count, uint8_t *granted, int32_t *left, int32_t *scratch,
+                                      const Workspace &ws, cudaStream_t s);
+cudaError_t launch_slot_map(const int32_t *table, size_t stride, int rows, int width, const int32_t *cached,
+                            const int32_t *fresh, const uint8_t *granted, int page, int tokens, int32_t *starts,
+                            int64_t *slots, int32_t *positions, int32_t *row_ids, int32_t *scratch,
+                            const Workspace &ws, cudaStream_t s);
+cudaError_t launch_block_table_release(const int32_t *table, size_t stride, int rows, int width,
+                                       const int32_t *cached, const uint8_t *done, int page, int32_t *pages, int pool,
+                                       const int32_t *free_count, int32_t *left, int32_t *scratch,
+                                       const Workspace &ws, cudaStream_t s);
+
+// Token draw.  Per-row settings in device memory, each null for "off".
+enum class LogitType { F32, F16, BF16 };
+struct SampleAsk {
+    const float *temperature;
+    const int32_t *top_k;
+    const float *top_p, *min_p;
+};
+cudaError_t launch_sample(LogitType type, const void *logits, size_t rows, size_t vocab, size_t stride,
+                          const float *noise, size_t noise_stride, const SampleAsk &ask, int32_t *tokens,
+                          float *logprobs, cudaStream_t s);
+
 }  // namespace devscan
