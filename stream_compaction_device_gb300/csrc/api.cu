@@ -296,7 +296,10 @@ devscan_status sample_common(LogitType type, const void *logits, size_t rows, si
     const Span read[] = {{logits, x_bytes},  {noise, q_bytes},  {ask.temperature, each},
                          {ask.top_k, each},  {ask.top_p, each}, {ask.min_p, each}};
     if (written_overlap(written, read)) return DEVSCAN_ERR_INVALID;
-    return from_cuda(launch_sample(type, logits, rows, vocab, stride, noise, noise_stride, ask, tokens, logprobs,
+    Workspace ws;
+    const devscan_status st = acquire(stream, 1, &ws);
+    if (st != DEVSCAN_OK) return st;
+    return from_cuda(launch_sample(type, logits, rows, vocab, stride, noise, noise_stride, ask, tokens, logprobs, ws,
                                    stream));
 }
 

@@ -182,6 +182,6 @@ struct SampleAsk {
 };
 cudaError_t launch_sample(LogitType type, const void *logits, size_t rows, size_t vocab, size_t stride,
                           const float *noise, size_t noise_stride, const SampleAsk &ask, int32_t *tokens,
-                          float *logprobs, cudaStream_t s);
+                          float *logprobs, const Workspace &ws, cudaStream_t s);
 
 }  // namespace devscan

@@ -9,35 +9,120 @@
 //   top-k : the first k;
 //   top-p : of those, tokens whose mass ahead is below p times their total;
 //   min-p : tokens with w_i >= m (the largest logit has w = 1).
-// The order is the descending order of a 64-bit key, the logit's ordered bits
-// above the complement of its index.  The last kept key is found by a radix
-// select, most significant digit first, on counts (top-k) or on masses
-// (top-p).  Masses are fixed-point integers (w in units of 2^-31, sums in 64
-// bits), so they do not depend on the order of the adds.
+//
+// One thread-block cluster draws one row, which it reads from memory once and
+// keeps in shared memory, a slice per block; the blocks meet through
+// distributed shared memory.  The passes over a row (sum, selection, race)
+// then cost no memory traffic, and the noise is read only where a token is
+// kept.
+//
+// Selection has two forms.
+//   Short list.  Every full warp's j-th largest lane maximum is taken, and the
+//     least of them is a bound with at least j tokens per warp above it: for
+//     j = ceil(k / warps) the first k are all at or above the bound.  Those
+//     tokens (a few hundred) are collected, sorted by one block as 64-bit keys
+//     (ordered logit bits above the complement of the index), and top-k, top-p
+//     (a scan of the sorted weights) and min-p are cuts of the sorted list.
+//     top-p without top-k takes the same list if its mass reaches p times the
+//     row's.
+//   Histograms.  Where the list would be too long (a wide top-k, a flat row,
+//     a tie of many tokens), the cut is bracketed by a histogram of counts or
+//     masses in shared memory, 32 bins per unit of logit, then of ordered
+//     bits, then of indices, each inside the bin where the last one crossed
+//     the mark, until the tokens inside fit the list.  Masses there are
+//     integers (w in units of 2^-31, summed in 64 bits), so no result depends
+//     on the order of the atomics.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
+#include <cfloat>
+
 #include "core.cuh"
 #include "launch.h"
+#include "pipeline.cuh"
 
 namespace devscan {
 namespace {
 
-constexpr int kSampleThreads = 512;
-constexpr int kSampleWarps = kSampleThreads / 32;
-constexpr int kIndexBits = 24;
-constexpr int kKeyDigits = (32 + kIndexBits) / 8;
-
 using u64 = unsigned long long;
 
-__device__ __forceinline__ float as_float(float v) { return v; }
-__device__ __forceinline__ float as_float(__half v) { return __half2float(v); }
-__device__ __forceinline__ float as_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr unsigned kSliceChunks = 2048;    // 16-byte chunks of a block's slice, where the row allows: 32 KB
+constexpr int kLoads = 8;                  // 16-byte loads in flight per thread
+constexpr int kList = 1024;                // tokens the short list holds
+constexpr int kKeys = kList / kThreads;    // its keys per thread in the sort
+constexpr int kBins = 1024;
+constexpr float kBinsPerUnit = 32.0f;      // first histogram: bins per unit of logit
+constexpr int kGuess = 256;                // tokens asked of the bound for top-p without top-k
 
-// Bits of x whose unsigned order is x's order; NaN counts as -inf, -0 as 0.
+__device__ __forceinline__ float inf() { return __int_as_float(0x7f800000); }
+
+// ---------------------------------------------------------------------------
+// Cluster exchange: a word of this block's shared memory in another block.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ unsigned cluster_rank()
+{
+    unsigned r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ unsigned cluster_blocks()
+{
+    unsigned r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive()
+{
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync()
+{
+    cluster_arrive();
+    cluster_wait();
+}
+__device__ __forceinline__ uint32_t remote(const void *p, unsigned rank)
+{
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void put(uint32_t *p, unsigned rank, uint32_t v)
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote(p, rank)), "r"(v) : "memory");
+}
+__device__ __forceinline__ void put(float *p, unsigned rank, float v)
+{
+    put(reinterpret_cast<uint32_t *>(p), rank, __float_as_uint(v));
+}
+__device__ __forceinline__ void put(u64 *p, unsigned rank, u64 v)
+{
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(remote(p, rank)), "l"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t get(const uint32_t *p, unsigned rank)
+{
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote(p, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t fetch_add(uint32_t *p, unsigned rank, uint32_t v)
+{
+    uint32_t old;
+    asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(remote(p, rank)), "r"(v) : "memory");
+    return old;
+}
+
+// ---------------------------------------------------------------------------
+// Values.
+// ---------------------------------------------------------------------------
+// Bits of x whose unsigned order is x's order (x not NaN; -0 counts as 0).
 __device__ __forceinline__ uint32_t ordered(float x)
 {
-    if (x != x) x = -__int_as_float(0x7f800000);
     const uint32_t b = __float_as_uint(x + 0.0f);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
@@ -47,169 +132,816 @@ __device__ __forceinline__ float unordered(uint32_t k)
 }
 constexpr uint32_t kOrderedMinusInf = 0x007fffffu;
 
-__device__ __forceinline__ u64 key_of(uint32_t ord, unsigned i)
+// A token's place in the order: larger keys first.
+__device__ __forceinline__ u64 key_of(uint32_t ord, unsigned i) { return (static_cast<u64>(ord) << 32) | ~i; }
+__device__ __forceinline__ uint32_t ord_of(u64 key) { return static_cast<uint32_t>(key >> 32); }
+__device__ __forceinline__ unsigned index_of(u64 key) { return ~static_cast<unsigned>(key); }
+
+__device__ __forceinline__ float exp2_approx(float x)
 {
-    return (static_cast<u64>(ord) << kIndexBits) | ((1u << kIndexBits) - 1 - i);
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-template <class V, class F>
-__device__ V block_fold(V v, V *s_fold, F f)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) v = f(v, __shfl_xor_sync(kFullMask, v, d));
-    __syncthreads();
-    if (lane == 0) s_fold[warp] = v;
-    __syncthreads();
-    v = s_fold[0];
-    for (int w = 1; w < kSampleWarps; ++w) v = f(v, s_fold[w]);
-    return v;
-}
-
-template <class T>
-struct Row {
-    const T *x;
-    unsigned vocab;
-    float top;      // the largest logit
-    float t;        // temperature
-    __device__ __forceinline__ uint32_t ord(unsigned i) const { return ordered(as_float(x[i])); }
-    __device__ __forceinline__ float weight(uint32_t o) const
+// A 16-byte chunk of logits: kEach values, and the larger of two chunks value
+// by value (a NaN loses to a number).
+template <class T> struct Chunk;
+template <> struct Chunk<float> {
+    static constexpr int kEach = 4;
+    static constexpr uint32_t kFill = 0xff800000u;
+    static __device__ __forceinline__ float value(const uint32_t (&q)[4], int e) { return __uint_as_float(q[e]); }
+    static __device__ __forceinline__ float most(const uint32_t (&q)[4], float m)
     {
-        const float v = unordered(o);
-        if (o == kOrderedMinusInf) return 0.0f;
-        return v == top ? 1.0f : fmaxf(expf((v - top) / t), 0.0f);   // 0 for inf / inf
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m = fmaxf(m, __uint_as_float(q[e]));
+        return m;
     }
-    __device__ __forceinline__ uint32_t mass(uint32_t o) const { return __float2uint_rn(weight(o) * 2147483648.0f); }
+};
+template <> struct Chunk<__half> {
+    static constexpr int kEach = 8;
+    static constexpr uint32_t kFill = 0xfc00fc00u;
+    static __device__ __forceinline__ float value(const uint32_t (&q)[4], int e)
+    {
+        const uint32_t b = (e & 1) ? q[e / 2] >> 16 : q[e / 2] & 0xffffu;
+        return __half2float(__ushort_as_half(static_cast<unsigned short>(b)));
+    }
+    static __device__ __forceinline__ float most(const uint32_t (&q)[4], float m)
+    {
+        __half2 h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[k] = *reinterpret_cast<const __half2 *>(&q[k]);
+        const __half2 a = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+        return fmaxf(m, fmaxf(__low2float(a), __high2float(a)));
+    }
+};
+template <> struct Chunk<__nv_bfloat16> {
+    static constexpr int kEach = 8;
+    static constexpr uint32_t kFill = 0xff80ff80u;
+    static __device__ __forceinline__ float value(const uint32_t (&q)[4], int e)
+    {
+        return __uint_as_float((e & 1) ? q[e / 2] & 0xffff0000u : q[e / 2] << 16);
+    }
+    static __device__ __forceinline__ float most(const uint32_t (&q)[4], float m)
+    {
+        __nv_bfloat162 h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[k] = *reinterpret_cast<const __nv_bfloat162 *>(&q[k]);
+        const __nv_bfloat162 a = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+        return fmaxf(m, fmaxf(__low2float(a), __high2float(a)));
+    }
 };
 
-// The largest key K such that what keys >= K hold (1 each, or their mass)
-// reaches `want`; 0 if all of them do not.  Only keys >= `floor` take part.
-template <bool MASS, class T>
-__device__ u64 select(const Row<T> &row, u64 floor, u64 want, u64 *s_hist, u64 *s_pick)
-{
-    u64 prefix = 0;
-    for (int digit = kKeyDigits - 1; digit >= 0; --digit) {
-        const int shift = digit * 8;
-        for (int b = threadIdx.x; b < 256; b += kSampleThreads) s_hist[b] = 0;
-        __syncthreads();
-        for (unsigned i = threadIdx.x; i < row.vocab; i += kSampleThreads) {
-            const uint32_t o = row.ord(i);
-            const u64 key = key_of(o, i);
-            if (key < floor || (key >> shift >> 8) != prefix || o == kOrderedMinusInf) continue;
-            atomicAdd(&s_hist[(key >> shift) & 255], MASS ? static_cast<u64>(row.mass(o)) : 1ull);
-        }
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            int b = 255;
-            while (b >= 0 && s_hist[b] < want) want -= s_hist[b--];
-            s_pick[0] = b < 0 ? ~0ull : static_cast<u64>(b);
-            s_pick[1] = want;
-        }
-        __syncthreads();
-        const u64 b = s_pick[0];
-        want = s_pick[1];
-        __syncthreads();
-        if (b == ~0ull) return 0;
-        prefix = (prefix << 8) | b;
-    }
-    return prefix;
-}
+struct Shared {
+    u64 list[kList];                 // this block's collected tokens; a buffer of the sort
+    union {
+        u64 merged[kList];           // the cluster's, in block 0
+        struct {
+            uint32_t count[kBins];   // histogram: counts, or the low words of the masses
+            uint32_t carry[kBins];   // the masses' high words
+        };
+    };
+    u64 warp64[kWarps];
+    float warpf[kWarps];
+    uint32_t warp_max[kWarps], warp_bound[kWarps], warp_n[kWarps];
+    // What the blocks tell each other, by rank.
+    uint32_t top[kMaxCluster], bound[kMaxCluster];
+    uint32_t found[2][kMaxCluster];
+    float sum[2][kMaxCluster];
+    float sum_above[kMaxCluster];
+    u64 won[kMaxCluster];
+    float rest[kMaxCluster];
+    uint32_t tops[kMaxCluster];
+    u64 mass[kMaxCluster];
+    u64 cut;
+    uint32_t merged_n[2];            // in block 0: places of its merged list that are given out
+    // Results of one block's scans.
+    u64 pick_before;
+    uint32_t pick_bin, pick_lo, pick_hi;
+    uint32_t local_n;
+};
+constexpr size_t kSharedBytes = (sizeof(Shared) + 127) / 128 * 128;
 
 template <class T>
-__global__ void __launch_bounds__(kSampleThreads)
-sample_kernel(const T *__restrict__ logits, size_t stride, unsigned vocab, const float *__restrict__ noise,
-              size_t noise_stride, SampleAsk ask, int32_t *__restrict__ tokens, float *__restrict__ logprobs)
-{
-    __shared__ u64 s_fold[kSampleWarps];
-    __shared__ u64 s_hist[256];
-    __shared__ u64 s_pick[2];
-    const unsigned r = blockIdx.x;
-    const auto larger = [](u64 a, u64 b) { return a > b ? a : b; };
-    const auto add = [](u64 a, u64 b) { return a + b; };
-    Row<T> row{logits + r * stride, vocab, 0.0f, 1.0f};
+struct Draw {
+    using C = Chunk<T>;
+    static constexpr int kEach = C::kEach;
 
-    u64 best = 0;
-    for (unsigned i = threadIdx.x; i < vocab; i += kSampleThreads) best = larger(best, key_of(row.ord(i), i));
-    best = block_fold(best, s_fold, larger);
-    const uint32_t top = static_cast<uint32_t>(best >> kIndexBits);
-    const unsigned first = (1u << kIndexBits) - 1 - static_cast<unsigned>(best & ((1u << kIndexBits) - 1));
+    Shared &s;
+    uint4 *slice;                    // this block's chunks of the row
+    unsigned tid, lane, warp, rank, blocks;
+    unsigned vocab, mine;            // tokens of the row; chunks of the slice
+    int first;                       // index of the slice's first value
+    float top, t, scale;             // the largest logit, temperature, log2(e) / T
+    int turn = 0;                    // which half of the double buffers is next
+
+    __device__ __forceinline__ Draw(Shared &shared) : s(shared) {}
+
+    static __device__ __forceinline__ void unpack(const uint4 &v, uint32_t (&q)[4])
+    {
+        q[0] = v.x, q[1] = v.y, q[2] = v.z, q[3] = v.w;
+    }
+
+    // f(value, index) for every value of this thread's chunks (each thread
+    // reads those that it wrote, so no barrier stands between).  each_above
+    // leaves out chunks without a value of at least `low`.
+    template <class F>
+    __device__ __forceinline__ void each(F f)
+    {
+        for (unsigned c = tid; c < mine; c += kThreads) {
+            uint32_t q[4];
+            unpack(slice[c], q);
+            const int i = first + static_cast<int>(c) * kEach;
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) f(C::value(q, e), i + e);
+        }
+    }
+    template <class F>
+    __device__ __forceinline__ void each_above(float low, F f)
+    {
+        for (unsigned c = tid; c < mine; c += kThreads) {
+            uint32_t q[4];
+            unpack(slice[c], q);
+            if (!(C::most(q, -inf()) >= low)) continue;
+            const int i = first + static_cast<int>(c) * kEach;
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) f(C::value(q, e), i + e);
+        }
+    }
+
+    // Reads the block's slice of the row into shared memory; returns the
+    // thread's largest value.  Rows may start anywhere: chunk 0 begins at the
+    // 16-byte boundary at or before the row, and a chunk that reaches over
+    // either end of the row is read value by value and filled with -inf.
+    __device__ __forceinline__ float load(const T *row, unsigned per)
+    {
+        const unsigned shift = static_cast<unsigned>(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(T));
+        const unsigned chunks = (vocab + shift + kEach - 1) / kEach, begin = rank * per;
+        mine = begin < chunks ? min(per, chunks - begin) : 0;
+        first = static_cast<int>(begin * kEach) - static_cast<int>(shift);
+        const uint4 *at = reinterpret_cast<const uint4 *>(row - shift) + begin;
+        // Whole chunks: [lo, hi).
+        const unsigned lo = first < 0 ? 1 : 0;
+        const bool ragged = mine > 0 && first + static_cast<int>(mine) * kEach > static_cast<int>(vocab);
+        const unsigned hi = ragged ? mine - 1 : mine;
+        float most = -inf();
+        for (unsigned c0 = tid; c0 < hi; c0 += kLoads * kThreads) {
+            uint4 v[kLoads];
+#pragma unroll
+            for (int u = 0; u < kLoads; ++u) {
+                const unsigned c = c0 + u * kThreads;
+                v[u] = c >= lo && c < hi ? ld_stream(at + c) : make_uint4(C::kFill, C::kFill, C::kFill, C::kFill);
+            }
+#pragma unroll
+            for (int u = 0; u < kLoads; ++u) {
+                const unsigned c = c0 + u * kThreads;
+                uint32_t q[4];
+                unpack(v[u], q);
+                most = C::most(q, most);
+                if (c >= lo && c < hi) slice[c] = v[u];
+            }
+        }
+        if (lo == 1 && tid == 0 && mine > 0) most = edge_chunk(row, 0, most);
+        if (ragged && !(lo == 1 && mine == 1) && tid == (mine - 1) % kThreads) most = edge_chunk(row, mine - 1, most);
+        return most;
+    }
+    __device__ float edge_chunk(const T *row, unsigned c, float most)
+    {
+        T *to = reinterpret_cast<T *>(slice + c);
+        for (int e = 0; e < kEach; ++e) {
+            const int i = first + static_cast<int>(c) * kEach + e;
+            const bool in = i >= 0 && i < static_cast<int>(vocab);
+            to[e] = in ? row[i] : T(-inf());
+            if (in) most = fmaxf(most, static_cast<float>(row[i]));
+        }
+        return most;
+    }
+
+    // Replaces every +inf by 0 and everything else by -inf.
+    __device__ void only_infinite()
+    {
+        for (unsigned c = tid; c < mine; c += kThreads) {
+            T *v = reinterpret_cast<T *>(slice + c);
+            for (int e = 0; e < kEach; ++e) v[e] = static_cast<float>(v[e]) == inf() ? T(0.0f) : T(-inf());
+        }
+    }
+
+    // Weight of any value (0 for -inf and NaN): the race and the sums over
+    // whole rows.  |error| <= (3 |d| + 3) 2^-24 relative, d = (v - top) / T.
+    __device__ __forceinline__ float weight(float v) const { return fmaxf(exp2_approx((v - top) * scale), 0.0f); }
+    // Weight of a number in the list, rounded as the definition's steps are.
+    __device__ __forceinline__ float list_weight(float v) const
+    {
+        return v == top ? 1.0f : fmaxf(expf((v - top) / t), 0.0f);
+    }
+    __device__ __forceinline__ uint32_t mass(float v) const { return __float2uint_rn(weight(v) * 2147483648.0f); }
+
+    __device__ __forceinline__ float block_sum(float v)
+    {
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(kFullMask, v, d);
+        __syncthreads();
+        if (lane == 0) s.warpf[warp] = v;
+        __syncthreads();
+        v = lane < kWarps ? s.warpf[lane] : 0.0f;
+#pragma unroll
+        for (int d = kWarps / 2; d >= 1; d >>= 1) v += __shfl_xor_sync(kFullMask, v, d);
+        return __shfl_sync(kFullMask, v, 0);
+    }
+
+    // Exclusive prefix of v over the block's threads; *all its total.
+    template <class V>
+    __device__ __forceinline__ V block_scan(V v, V *s_warp, V *all)
+    {
+        V incl = v;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const V u = __shfl_up_sync(kFullMask, incl, d);
+            if (lane >= d) incl += u;
+        }
+        __syncthreads();
+        if (lane == 31) s_warp[warp] = incl;
+        __syncthreads();
+        V ahead = 0, total = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < static_cast<int>(warp)) ahead += s_warp[w];
+            total += s_warp[w];
+        }
+        *all = total;
+        const V before = __shfl_up_sync(kFullMask, incl, 1);
+        return ahead + (lane == 0 ? V(0) : before);
+    }
+
+    // Collects the tokens for which in(v, i) holds (none below `low`) into
+    // block 0's merged list, if there are at most kList of them.  Returns their number (the same in
+    // every block).  sum: a partial sum of each thread, summed into
+    // s.sum[turn] of every block by rank.
+    template <class In>
+    __device__ uint32_t collect(float low, In in, float *sum)
+    {
+        const int now = turn;
+        turn ^= 1;
+        uint32_t found = 0;
+        each_above(low, [&](float v, int i) { found += in(v, i) ? 1u : 0u; });
+        uint32_t n = 0;
+        const uint32_t at = block_scan(found, s.warp_n, &n);
+        float total = 0.0f;
+        if (sum != nullptr) total = block_sum(*sum);
+        if (found != 0 && n <= kList) {
+            uint32_t k = at;
+            each_above(low, [&](float v, int i) {
+                if (in(v, i)) s.list[k++] = key_of(ordered(v), static_cast<unsigned>(i));
+            });
+        }
+        if (tid == 0) {
+            s.merged_n[now ^ 1] = 0;
+            s.local_n = n == 0 || n > kList ? kList + 1 : fetch_add(&s.merged_n[now], 0, n);
+        }
+        if (tid < blocks) {
+            put(&s.found[now][rank], tid, n);
+            if (sum != nullptr) put(&s.sum[now][rank], tid, total);
+        }
+        __syncthreads();
+        const uint32_t base = s.local_n;
+        if (n <= kList && base + n <= kList)
+            for (uint32_t k = tid; k < n; k += kThreads) put(&s.merged[base + k], 0, s.list[k]);
+        cluster_sync();
+        uint32_t all = 0;
+        for (unsigned b = 0; b < blocks; ++b) all += s.found[now][b];
+        return all;
+    }
+
+    __device__ __forceinline__ float cluster_sum(int which) const
+    {
+        float v = 0.0f;
+        for (unsigned b = 0; b < blocks; ++b) v += s.sum[which][b];
+        return v;
+    }
+
+    // Sorts merged[0 .. n), n <= kList, descending, by this block (a bitonic
+    // sort of 64-bit keys: strides inside a warp by shuffles, up to the block
+    // through shared memory, above inside a thread).  Thread t gets the keys
+    // at t + h * kThreads; 0 past the end.
+    __device__ void sort(uint32_t n, u64 (&a)[kKeys])
+    {
+        unsigned size2 = 32;
+        while (size2 < n) size2 *= 2;
+#pragma unroll
+        for (int h = 0; h < kKeys; ++h) a[h] = tid + h * kThreads < n ? s.merged[tid + h * kThreads] : 0;
+        const bool active = tid < size2;
+        int half = 0;
+        for (unsigned size = 2; size <= size2; size *= 2) {
+            for (unsigned stride = size / 2; stride >= 1; stride /= 2) {
+                if (stride >= kThreads) {
+#pragma unroll
+                    for (int h = 0; h < kKeys; ++h) {
+                        const int o = h ^ static_cast<int>(stride / kThreads);
+                        if (o > h) {
+                            u64 partner = 0;
+#pragma unroll
+                            for (int k = 0; k < kKeys; ++k) partner = k == o ? a[k] : partner;
+                            const bool down = ((tid + h * kThreads) & size) == 0;
+                            const u64 most = a[h] > partner ? a[h] : partner, least = a[h] > partner ? partner : a[h];
+                            a[h] = down ? most : least;
+#pragma unroll
+                            for (int k = 0; k < kKeys; ++k) a[k] = k == o ? (down ? least : most) : a[k];
+                        }
+                    }
+                    continue;
+                }
+                const bool low = (tid & stride) == 0;
+                u64 *buf = half ? s.merged : s.list;
+                if (stride >= 32) {
+                    half ^= 1;   // this half was last read two exchanges back, before the last barrier
+#pragma unroll
+                    for (int h = 0; h < kKeys; ++h)
+                        if (tid + h * kThreads < size2) buf[tid + h * kThreads] = a[h];
+                    __syncthreads();
+                }
+#pragma unroll
+                for (int h = 0; h < kKeys; ++h) {
+                    if (h > 0 ? size2 <= h * kThreads : !active) continue;
+                    const u64 p = stride >= 32 ? buf[(tid ^ stride) + h * kThreads]
+                                               : __shfl_xor_sync(kFullMask, a[h], stride);
+                    const bool down = ((tid + h * kThreads) & size) == 0;
+                    a[h] = (low == down) == (a[h] > p) ? a[h] : p;
+                }
+            }
+        }
+    }
+
+    // The race among the kept tokens that this thread has seen.
+    struct Best {
+        float score = -1.0f;
+        int at = 0x7fffffff;
+        __device__ __forceinline__ void offer(float sc, int i)
+        {
+            if (sc > score) score = sc, at = i;
+        }
+        __device__ __forceinline__ u64 key() const
+        {
+            return score < 0.0f ? 0ull : (static_cast<u64>(__float_as_uint(score)) << 32) | ~static_cast<unsigned>(at);
+        }
+    };
+
+    __device__ __forceinline__ u64 block_most(u64 v)
+    {
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) {
+            const u64 u = __shfl_xor_sync(kFullMask, v, d);
+            v = u > v ? u : v;
+        }
+        __syncthreads();
+        if (lane == 0) s.warp64[warp] = v;
+        __syncthreads();
+        v = s.warp64[lane & (kWarps - 1)];
+#pragma unroll
+        for (int d = kWarps / 2; d >= 1; d >>= 1) {
+            const u64 u = __shfl_xor_sync(kFullMask, v, d);
+            v = u > v ? u : v;
+        }
+        return v;
+    }
+
+    __device__ __forceinline__ void write(const T *row, u64 won, float rest, uint32_t tops, int32_t *token, float *logprob)
+    {
+        const unsigned i = index_of(won);
+        *token = static_cast<int32_t>(i);
+        if (logprob == nullptr) return;
+        const float v = static_cast<float>(row[i]);
+        const float d = v == inf() || v == top ? 0.0f : (v - top) / t;
+        *logprob = d - log1pf(rest + static_cast<float>(tops - 1));
+    }
+
+    // Joins the blocks' races and writes the row's answer.
+    __device__ __forceinline__ void finish(const T *row, const Best &best, float rest, uint32_t tops, int32_t *token,
+                                           float *logprob)
+    {
+        const u64 won = block_most(best.key());
+        rest = block_sum(rest);
+        tops = __reduce_add_sync(kFullMask, tops);
+        if (lane == 0) s.warp_n[warp] = tops;
+        __syncthreads();
+        if (tid == 0) {
+            uint32_t all = 0;
+            for (int w = 0; w < kWarps; ++w) all += s.warp_n[w];
+            put(&s.won[rank], 0, won);
+            put(&s.rest[rank], 0, rest);
+            put(&s.tops[rank], 0, all);
+        }
+        cluster_sync();
+        if (rank != 0 || tid != 0) return;
+        u64 w = 0;
+        float r = 0.0f;
+        uint32_t n = 0;
+        for (unsigned b = 0; b < blocks; ++b) {
+            w = s.won[b] > w ? s.won[b] : w;
+            r += s.rest[b];
+            n += s.tops[b];
+        }
+        write(row, w, r, n, token, logprob);
+    }
+
+    // The bin of the first histogram: falls as v grows.
+    __device__ __forceinline__ int bin_of(float v) const
+    {
+        return min(__float2int_rz((top - v) * kBinsPerUnit), kBins - 1);
+    }
+
+    // One histogram level: adds what each value holds, then finds the bin
+    // where the running total from bin 0 reaches `want`.  Returns false if it
+    // does not; else `bin`, and `want` less what is in the bins before it.
+    template <bool MASS, class Bin>
+    __device__ bool histogram(float low, Bin bin_in, u64 &want, uint32_t &bin)
+    {
+        for (unsigned b = tid; b < kBins; b += kThreads) s.count[b] = s.carry[b] = 0;
+        __syncthreads();
+        each_above(low, [&](float v, int i) {
+            const int b = bin_in(v, i);
+            if (b < 0) return;
+            if (MASS) {
+                const uint32_t m = mass(v);
+                if (m == 0) return;
+                const uint32_t old = atomicAdd(&s.count[b], m);
+                if (old + m < old) atomicAdd(&s.carry[b], 1u);
+            } else {
+                atomicAdd(&s.count[b], 1u);
+            }
+        });
+        cluster_sync();
+        // Thread t sums the bins from kPer * t on, of all blocks.
+        constexpr int kPer = kBins / kThreads;
+        u64 h[kPer], own = 0;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) h[k] = 0;
+        for (unsigned r = 0; r < blocks; ++r) {
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                h[k] += get(&s.count[kPer * tid + k], r);
+                if (MASS) h[k] += static_cast<u64>(get(&s.carry[kPer * tid + k], r)) << 32;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) own += h[k];
+        u64 all = 0;
+        u64 before = block_scan(own, s.warp64, &all);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            if (before < want && want <= before + h[k]) {
+                s.pick_bin = kPer * tid + k;
+                s.pick_before = before;
+            }
+            before += h[k];
+        }
+        cluster_sync();   // the histogram's memory is used again from here
+        if (all < want) return false;
+        bin = s.pick_bin;
+        want -= s.pick_before;
+        return true;
+    }
+
+    // The least ordered bits o with bin_of(o) <= b.
+    __device__ uint32_t edge(int b) const
+    {
+        uint32_t lo = ordered(-FLT_MAX), hi = ordered(top);
+        while (lo < hi) {
+            const uint32_t mid = lo + (hi - lo) / 2;
+            if (bin_of(unordered(mid)) <= b) hi = mid;
+            else lo = mid + 1;
+        }
+        return lo;
+    }
+
+    // The key of the last token, in the order, of the shortest prefix that
+    // holds `want` (tokens, or mass); 0 if all of them do not.  Only tokens
+    // with keys >= floor take part.
+    template <bool MASS>
+    __device__ u64 select(u64 floor, u64 want)
+    {
+        const float floor_v = floor == 0 ? -FLT_MAX : unordered(ord_of(floor));
+        const int floor_i = floor == 0 ? 0x7fffffff : static_cast<int>(index_of(floor));
+        const auto takes_part = [&](float v, int i) { return v > floor_v || (v == floor_v && i <= floor_i); };
+        uint32_t bin = 0;
+        if (!histogram<MASS>(floor_v, [&](float v, int i) { return takes_part(v, i) ? bin_of(v) : -1; }, want, bin)) return 0;
+        if (tid == 0) s.pick_lo = edge(static_cast<int>(bin));
+        if (tid == 32) s.pick_hi = bin == 0 ? ordered(top) : edge(static_cast<int>(bin) - 1) - 1;
+        __syncthreads();
+        uint32_t lo = s.pick_lo, hi = s.pick_hi;        // the cut's ordered bits
+        uint32_t i_lo = 0, i_hi = vocab - 1;            // and, once lo == hi, its index
+        for (;;) {
+            const float v_lo = unordered(lo), v_hi = unordered(hi);
+            const bool tie = lo == hi;
+            const auto inside = [&](float v, int i) {
+                return v >= v_lo && v <= v_hi && takes_part(v, i) &&
+                       (!tie || (static_cast<unsigned>(i) >= i_lo && static_cast<unsigned>(i) <= i_hi));
+            };
+            const uint32_t n = collect(v_lo, inside, nullptr);
+            if (n <= kList) {
+                if (rank == 0) {
+                    u64 key[kKeys], base = 0;
+                    sort(n, key);
+#pragma unroll
+                    for (int h = 0; h < kKeys; ++h) {
+                        u64 holds = 0, total = 0;
+                        if (tid + h * kThreads < n) holds = MASS ? mass(unordered(ord_of(key[h]))) : 1;
+                        const u64 ahead = base + block_scan(holds, s.warp64, &total);
+                        if (ahead < want && want <= ahead + holds) s.pick_before = key[h];
+                        base += total;
+                    }
+                    __syncthreads();
+                    if (tid < blocks) put(&s.cut, tid, s.pick_before);
+                }
+                cluster_sync();
+                return s.cut;
+            }
+            if (!tie) {
+                unsigned shift = 0;
+                while ((hi - lo) >> shift >= kBins) ++shift;
+                histogram<MASS>(v_lo, [&](float v, int i) {
+                    return inside(v, i) ? static_cast<int>((hi - ordered(v)) >> shift) : -1;
+                }, want, bin);
+                const uint32_t new_hi = hi - (bin << shift), width = (1u << shift) - 1;
+                lo = new_hi - lo > width ? new_hi - width : lo;
+                hi = new_hi;
+            } else {
+                unsigned shift = 0;
+                while ((i_hi - i_lo) >> shift >= kBins) ++shift;
+                histogram<MASS>(v_lo, [&](float v, int i) {
+                    return inside(v, i) ? static_cast<int>((static_cast<unsigned>(i) - i_lo) >> shift) : -1;
+                }, want, bin);
+                i_lo += bin << shift;
+                i_hi = min(i_hi, i_lo + ((1u << shift) - 1));
+            }
+        }
+    }
+
+    // Mass of the tokens with keys >= floor, over the cluster.
+    __device__ u64 mass_from(u64 floor)
+    {
+        const float floor_v = floor == 0 ? -FLT_MAX : unordered(ord_of(floor));
+        const int floor_i = floor == 0 ? 0x7fffffff : static_cast<int>(index_of(floor));
+        u64 sum = 0;
+        each_above(floor_v, [&](float v, int i) {
+            if (v > floor_v || (v == floor_v && i <= floor_i)) sum += mass(v);
+        });
+        u64 all = 0;
+        block_scan(sum, s.warp64, &all);
+        if (tid < blocks) put(&s.mass[rank], tid, all);
+        cluster_sync();
+        all = 0;
+        for (unsigned b = 0; b < blocks; ++b) all += s.mass[b];
+        return all;
+    }
+};
+
+template <class T>
+__global__ void __launch_bounds__(kThreads, 4)
+sample_kernel(const T *__restrict__ logits, size_t stride, unsigned vocab, unsigned per,
+              const float *__restrict__ noise, size_t noise_stride, SampleAsk ask, int32_t *__restrict__ tokens,
+              float *__restrict__ logprobs)
+{
+    extern __shared__ __align__(16) unsigned char s_bytes[];
+    Shared &s = *reinterpret_cast<Shared *>(s_bytes);
+    using D = Draw<T>;
+    D d(s);
+    d.slice = reinterpret_cast<uint4 *>(s_bytes + kSharedBytes);
+    d.tid = threadIdx.x, d.lane = d.tid & 31, d.warp = d.tid >> 5;
+    d.rank = cluster_rank(), d.blocks = cluster_blocks(), d.vocab = vocab;
+    const unsigned r = blockIdx.x / d.blocks;
+    const T *row = logits + static_cast<size_t>(r) * stride;
+    if (d.tid == 0) s.merged_n[0] = s.merged_n[1] = 0;
+    cluster_arrive();   // the blocks' shared memory is there from the matching wait on
+    const float most = d.load(row, per);
+
     const float t = ask.temperature != nullptr ? ask.temperature[r] : 1.0f;
-    if (top == kOrderedMinusInf || noise == nullptr || !(t > 0.0f)) {
-        if (threadIdx.x == 0) {
-            const bool empty = top == kOrderedMinusInf;
-            tokens[r] = empty ? -1 : static_cast<int32_t>(first);
-            if (logprobs != nullptr) logprobs[r] = empty ? -__int_as_float(0x7f800000) : 0.0f;
+    int k = ask.top_k != nullptr ? ask.top_k[r] : 0;
+    if (k <= 0 || static_cast<unsigned>(k) >= vocab) k = 0;
+    float p = ask.top_p != nullptr ? ask.top_p[r] : 1.0f;
+    const float m = ask.min_p != nullptr ? ask.min_p[r] : 0.0f;
+    // One token stays, the first of the order: no draw.
+    const bool greedy = noise == nullptr || !(t > 0.0f) || k == 1 || vocab == 1 || !(p > 0.0f) || !(m <= 1.0f);
+    const bool by_mass = !(p >= 1.0f);
+    int32_t *token = tokens + r;
+    float *logprob = logprobs != nullptr ? logprobs + r : nullptr;
+
+    // The largest logit, and the bound for the short list: the least, over the
+    // warps whose lanes all hold tokens, of the j-th largest lane maximum.
+    const uint32_t lane_top = ordered(most);
+    const uint32_t warp_top = __reduce_max_sync(kFullMask, lane_top);
+    const unsigned shift = static_cast<unsigned>(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(T));
+    const unsigned chunks = (vocab + shift + D::kEach - 1) / D::kEach, last = (chunks - 1) / per;   // last block with any
+    const unsigned full = min(d.mine / 32, static_cast<unsigned>(kWarps));
+    const unsigned warps = last * min(per / 32, static_cast<unsigned>(kWarps)) +
+                           min((chunks - last * per) / 32, static_cast<unsigned>(kWarps));
+    const int wanted = k > 0 ? k : kGuess;
+    const int j = warps > 0 ? (wanted + static_cast<int>(warps) - 1) / static_cast<int>(warps) : 33;
+    const bool bounded = !greedy && (k > 0 || by_mass) && vocab > kList && j <= 32;
+    uint32_t bound = ~0u;
+    if (bounded && d.warp < full) {
+        uint32_t left = lane_top;
+        for (int i = 0; i < j; ++i) {
+            bound = __reduce_max_sync(kFullMask, left);
+            const unsigned at = __ballot_sync(kFullMask, left == bound);
+            if (d.lane == static_cast<unsigned>(__ffs(at) - 1)) left = 0;
+        }
+    }
+    if (d.lane == 0) s.warp_max[d.warp] = warp_top, s.warp_bound[d.warp] = bound;
+    __syncthreads();
+    cluster_wait();
+    if (d.warp == 0) {
+        const uint32_t a = __reduce_max_sync(kFullMask, s.warp_max[d.lane & (kWarps - 1)]);
+        const uint32_t b = __reduce_min_sync(kFullMask, s.warp_bound[d.lane & (kWarps - 1)]);
+        if (d.lane < d.blocks) {
+            put(&s.top[d.rank], d.lane, a);
+            put(&s.bound[d.rank], d.lane, b);
+        }
+    }
+    cluster_sync();
+    uint32_t top = 0;
+    bound = ~0u;
+    for (unsigned b = 0; b < d.blocks; ++b) {
+        top = max(top, s.top[b]);
+        bound = min(bound, s.bound[b]);
+    }
+    if (top == kOrderedMinusInf) {
+        if (d.rank == 0 && d.tid == 0) {
+            *token = -1;
+            if (logprob != nullptr) *logprob = -inf();
         }
         return;
     }
-    row.top = unordered(top);
-    row.t = t;
-    const int k = ask.top_k != nullptr ? ask.top_k[r] : 0;
-    const float p = ask.top_p != nullptr ? ask.top_p[r] : 1.0f;
-    const float m = ask.min_p != nullptr ? ask.min_p[r] : 0.0f;
+    d.top = unordered(top);
+    if (d.top == inf()) {   // the draw is among the infinite ones, which weigh the same
+        d.only_infinite();
+        d.top = 0.0f;
+        bound = 0;          // all of them
+    }
+    d.t = t;
+    d.scale = fminf(1.4426950408889634f / t, FLT_MAX);
 
-    u64 last = 0;
-    if (k > 0 && static_cast<unsigned>(k) < vocab) last = select<false>(row, 0, k, s_hist, s_pick);
-    if (!(p >= 1.0f)) {
-        u64 all = 0;
-        for (unsigned i = threadIdx.x; i < vocab; i += kSampleThreads) {
-            const uint32_t o = row.ord(i);
-            if (key_of(o, i) >= last) all += row.mass(o);
+    typename D::Best best;
+    if (greedy) {
+        const float value = d.top;
+        d.each_above(value, [&](float v, int i) {
+            if (v == value) best.offer(1.0f, i);
+        });
+        d.finish(row, best, 0.0f, d.rank == 0 && d.tid == 0 ? 1 : 0, token, logprob);   // one token is kept
+        return;
+    }
+    const float *q = noise + static_cast<size_t>(r) * noise_stride;
+
+    u64 cut = 0;
+    if (k > 0 || by_mass) {
+        const float low = bounded ? fmaxf(unordered(max(bound, kOrderedMinusInf)), -FLT_MAX) : -FLT_MAX;
+        // The sums that top-p without top-k needs: the row's, and the list's.
+        const bool whole = k == 0;
+        float sum = 0.0f, above = 0.0f;
+        if (whole) {
+            d.each([&](float v, int) {
+                const float w = d.weight(v);
+                sum += w;
+                if (v >= low) above += w;
+            });
+            above = d.block_sum(above);
+            if (d.tid < d.blocks) put(&s.sum_above[d.rank], d.tid, above);
         }
-        all = block_fold(all, s_fold, add);
-        const double part = p > 0.0f ? static_cast<double>(p) * static_cast<double>(all) : 0.0;
-        const u64 want = static_cast<u64>(ceil(part));
-        last = larger(last, select<true>(row, last, want > 1 ? want : 1, s_hist, s_pick));
-    }
-    u64 won = 0;
-    float rest = 0.0f;   // the kept weights but the first's, which is 1
-    const float *q = noise + r * noise_stride;
-    for (unsigned i = threadIdx.x; i < vocab; i += kSampleThreads) {
-        const uint32_t o = row.ord(i);
-        const u64 key = key_of(o, i);
-        if (key < last || o == kOrderedMinusInf) continue;
-        const float w = row.weight(o);
-        if (i != first && !(w >= m)) continue;
-        if (i != first) rest += w;
-        const float score = w / q[i];
-        won = larger(won, (static_cast<u64>(score > 0.0f ? __float_as_uint(score) : 0u) << 32) | (0xffffffffu - i));
-    }
-    won = block_fold(won, s_fold, larger);
-    float *s_rest = reinterpret_cast<float *>(s_hist);
-    rest = block_fold(rest, s_rest, [](float a, float b) { return a + b; });
-    if (threadIdx.x == 0) {
-        const unsigned i = 0xffffffffu - static_cast<unsigned>(won);
-        tokens[r] = static_cast<int32_t>(i);
-        if (logprobs != nullptr) {
-            const float v = unordered(row.ord(i));
-            logprobs[r] = (v == row.top ? 0.0f : (v - row.top) / t) - log1pf(rest);
+        const int now = d.turn;
+        const uint32_t n = d.collect(low, [&](float v, int) { return v >= low; }, whole ? &sum : nullptr);
+        float total = 0.0f;
+        bool enough = true;
+        if (whole) {
+            total = d.cluster_sum(now);
+            above = 0.0f;
+            for (unsigned b = 0; b < d.blocks; ++b) above += s.sum_above[b];
+            enough = low == -FLT_MAX || above > p * total * (1.0f + 1.0f / 4096);
+        }
+        if (n <= kList && enough) {
+            if (d.rank != 0) return;
+            u64 key[kKeys];
+            d.sort(n, key);
+            float w[kKeys], ahead[kKeys], listed = 0.0f;
+            uint32_t tops = 0;
+            float rest = 0.0f;
+            const uint32_t limit = k > 0 ? min(static_cast<uint32_t>(k), n) : n;
+#pragma unroll
+            for (int h = 0; h < kKeys; ++h) {
+                w[h] = d.tid + h * kThreads < limit ? d.list_weight(unordered(ord_of(key[h]))) : 0.0f;
+                float all = 0.0f;
+                ahead[h] = listed + d.block_scan(w[h], s.warpf, &all);
+                listed += all;
+            }
+            const float bar = p * (whole ? total : listed);
+#pragma unroll
+            for (int h = 0; h < kKeys; ++h) {
+                const uint32_t place = d.tid + h * kThreads;
+                const bool keep = place < limit && (place == 0 || ((!by_mass || ahead[h] < bar) && w[h] >= m));
+                if (!keep) continue;
+                const int i = static_cast<int>(index_of(key[h]));
+                const float score = fmaxf(w[h] / q[i], 0.0f);
+                if (score > best.score || (score == best.score && i < best.at)) best.score = score, best.at = i;
+                if (unordered(ord_of(key[h])) == d.top) ++tops;
+                else rest += w[h];
+            }
+            const u64 won = d.block_most(best.key());
+            rest = d.block_sum(rest);
+            tops = __reduce_add_sync(kFullMask, tops);
+            if (d.lane == 0) s.warp_n[d.warp] = tops;
+            __syncthreads();
+            if (d.tid != 0) return;
+            tops = 0;
+            for (int v = 0; v < kWarps; ++v) tops += s.warp_n[v];
+            d.write(row, won, rest, tops, token, logprob);
+            return;
+        }
+        if (k > 0) cut = d.template select<false>(0, static_cast<u64>(k));
+        if (by_mass) {
+            const double part = static_cast<double>(p) * static_cast<double>(d.mass_from(cut));
+            const u64 want = static_cast<u64>(ceil(part));
+            const u64 by = d.template select<true>(cut, want > 1 ? want : 1);
+            cut = by > cut ? by : cut;
         }
     }
+
+    const float cut_v = cut == 0 ? -FLT_MAX : unordered(ord_of(cut));
+    const int cut_i = cut == 0 ? 0x7fffffff : static_cast<int>(index_of(cut));
+    float rest = 0.0f;
+    uint32_t tops = 0;
+    d.each_above(cut_v, [&](float v, int i) {
+        if (!(v > cut_v || (v == cut_v && i <= cut_i))) return;
+        const float w = d.weight(v);
+        if (!(w >= m)) return;
+        best.offer(fmaxf(__fdividef(w, q[i]), 0.0f), i);
+        if (v == d.top) ++tops;
+        else rest += w;
+    });
+    d.finish(row, best, rest, tops, token, logprob);
 }
 
 template <class T>
-cudaError_t launch(const void *logits, size_t rows, size_t vocab, size_t stride, const float *noise,
-                   size_t noise_stride, const SampleAsk &ask, int32_t *tokens, float *logprobs, cudaStream_t s)
+cudaError_t launch_typed(const void *logits, size_t rows, unsigned vocab, size_t stride, const float *noise,
+                         size_t noise_stride, const SampleAsk &ask, int32_t *tokens, float *logprobs, int num_sms,
+                         cudaStream_t s)
 {
-    sample_kernel<T><<<static_cast<unsigned>(rows), kSampleThreads, 0, s>>>(
-        static_cast<const T *>(logits), stride, static_cast<unsigned>(vocab), noise, noise_stride, ask, tokens,
-        logprobs);
-    return cudaGetLastError();
+    // Chunks of a row, and one more where it starts inside its first.
+    constexpr unsigned kEach = Chunk<T>::kEach;
+    const unsigned chunks = (vocab + kEach - 1) / kEach;
+    // As few blocks per row as keep the slices at kSliceChunks, and more while
+    // all of them still fit on the GPU at once (four per SM) and have a chunk
+    // for every thread.
+    unsigned blocks = 1;
+    while (blocks < kMaxCluster && blocks * kSliceChunks < chunks) blocks *= 2;
+    while (blocks < kMaxCluster && rows * blocks * 2 <= static_cast<size_t>(num_sms) * 4 && blocks * kThreads < chunks)
+        blocks *= 2;
+    if (rows * blocks > 0x7fffffffull) return cudaErrorInvalidValue;
+    const unsigned per = (chunks + 1 + blocks - 1) / blocks;
+    constexpr size_t kMostChunks = (static_cast<size_t>(1) << 18) / kEach;   // of the largest vocabulary
+    constexpr size_t kMostBytes = kSharedBytes + (kMostChunks / kMaxCluster + 1) * 16;
+    static_assert(kMostBytes <= 227 * 1024, "a slice of the largest vocabulary fits");
+
+    const auto kernel = sample_kernel<T>;
+    static std::atomic<unsigned long long> attribute_set{0};   // one bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if ((attribute_set.load() & bit) == 0) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMostBytes));
+        if (e != cudaSuccess) return e;
+        attribute_set.fetch_or(bit);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(rows) * blocks);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSharedBytes + static_cast<size_t>(per) * 16;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = blocks;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<const T *>(logits), stride, vocab, per, noise, noise_stride,
+                              ask, tokens, logprobs);
 }
 
 }  // namespace
 
 cudaError_t launch_sample(LogitType type, const void *logits, size_t rows, size_t vocab, size_t stride,
                           const float *noise, size_t noise_stride, const SampleAsk &ask, int32_t *tokens,
-                          float *logprobs, cudaStream_t s)
+                          float *logprobs, const Workspace &ws, cudaStream_t s)
 {
+    const unsigned v = static_cast<unsigned>(vocab);
     switch (type) {
     case LogitType::F32:
-        return launch<float>(logits, rows, vocab, stride, noise, noise_stride, ask, tokens, logprobs, s);
+        return launch_typed<float>(logits, rows, v, stride, noise, noise_stride, ask, tokens, logprobs, ws.num_sms, s);
     case LogitType::F16:
-        return launch<__half>(logits, rows, vocab, stride, noise, noise_stride, ask, tokens, logprobs, s);
+        return launch_typed<__half>(logits, rows, v, stride, noise, noise_stride, ask, tokens, logprobs, ws.num_sms,
+                                    s);
     case LogitType::BF16:
-        return launch<__nv_bfloat16>(logits, rows, vocab, stride, noise, noise_stride, ask, tokens, logprobs, s);
+        return launch_typed<__nv_bfloat16>(logits, rows, v, stride, noise, noise_stride, ask, tokens, logprobs,
+                                           ws.num_sms, s);
     }
     return cudaErrorInvalidValue;
 }
