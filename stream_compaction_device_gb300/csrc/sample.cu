@@ -269,28 +269,38 @@ struct Draw {
         }
     }
 
-    // Reads the block's slice of the row into shared memory; returns the
-    // thread's largest value.  Rows may start anywhere: chunk 0 begins at the
-    // 16-byte boundary at or before the row, and a chunk that reaches over
-    // either end of the row is read value by value and filled with -inf.
-    __device__ __forceinline__ float load(const T *row, unsigned per)
+    // The block's slice of the row.  Rows may start anywhere: chunk 0 begins
+    // at the 16-byte boundary at or before the row, and a chunk that reaches
+    // over either end of the row is read value by value and filled with -inf.
+    // [lo, hi): the slice's whole chunks; head, tail: it has such a chunk.
+    unsigned chunks, lo, hi;         // chunks of the row
+    bool head, tail;
+    const uint4 *source;
+    __device__ __forceinline__ void place(const T *row, unsigned per)
     {
         const unsigned shift = static_cast<unsigned>(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(T));
-        const unsigned chunks = (vocab + shift + kEach - 1) / kEach, begin = rank * per;
+        const unsigned begin = rank * per;
+        chunks = (vocab + shift + kEach - 1) / kEach;
         mine = begin < chunks ? min(per, chunks - begin) : 0;
         first = static_cast<int>(begin * kEach) - static_cast<int>(shift);
-        const uint4 *at = reinterpret_cast<const uint4 *>(row - shift) + begin;
-        // Whole chunks: [lo, hi).
-        const unsigned lo = first < 0 ? 1 : 0;
-        const bool ragged = mine > 0 && first + static_cast<int>(mine) * kEach > static_cast<int>(vocab);
-        const unsigned hi = ragged ? mine - 1 : mine;
+        source = reinterpret_cast<const uint4 *>(row - shift) + begin;
+        head = first < 0 && mine > 0;
+        tail = mine > 0 && first + static_cast<int>(mine) * kEach > static_cast<int>(vocab);
+        lo = head ? 1 : 0;
+        hi = tail ? mine - 1 : mine;
+        if (head && mine == 1) tail = false;   // one chunk over both ends
+    }
+
+    // Reads the slice into shared memory; returns the thread's largest value.
+    __device__ __forceinline__ float load(const T *row)
+    {
         float most = -inf();
         for (unsigned c0 = tid; c0 < hi; c0 += kLoads * kThreads) {
             uint4 v[kLoads];
 #pragma unroll
             for (int u = 0; u < kLoads; ++u) {
                 const unsigned c = c0 + u * kThreads;
-                v[u] = c >= lo && c < hi ? ld_stream(at + c) : make_uint4(C::kFill, C::kFill, C::kFill, C::kFill);
+                v[u] = c >= lo && c < hi ? ld_stream(source + c) : make_uint4(C::kFill, C::kFill, C::kFill, C::kFill);
             }
 #pragma unroll
             for (int u = 0; u < kLoads; ++u) {
@@ -301,9 +311,91 @@ struct Draw {
                 if (c >= lo && c < hi) slice[c] = v[u];
             }
         }
-        if (lo == 1 && tid == 0 && mine > 0) most = edge_chunk(row, 0, most);
-        if (ragged && !(lo == 1 && mine == 1) && tid == (mine - 1) % kThreads) most = edge_chunk(row, mine - 1, most);
+        if (head && tid == 0) most = edge_chunk(row, 0, most);
+        if (tail && tid == (mine - 1) % kThreads) most = edge_chunk(row, mine - 1, most);
         return most;
+    }
+
+    // A race of all tokens needs no selection, so it takes one pass over the
+    // logits and the noise side by side.  Weights are relative to the largest
+    // logit that the thread has seen; what it holds is scaled down when a
+    // larger one comes.
+    struct Online {
+        float most = -inf(), rest = 0.0f, score = -1.0f;
+        uint32_t tops = 0;           // weights of exactly 1; `rest` sums the others
+        int at = 0x7fffffff;
+    };
+    __device__ __forceinline__ void rescale(Online &o, float most) const
+    {
+        const float f = fmaxf(exp2_approx((o.most - most) * scale), 0.0f);
+        o.rest = (o.rest + static_cast<float>(o.tops)) * f;
+        o.tops = 0;
+        if (o.score > 0.0f) o.score *= f;
+        o.most = most;
+    }
+    template <int N>
+    __device__ __forceinline__ void race(Online &o, const float (&v)[N], const float (&q)[N], int i) const
+    {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const float w = fmaxf(exp2_approx((v[e] - o.most) * scale), 0.0f);
+            if (w == 1.0f) ++o.tops;
+            else o.rest += w;
+            const float score = __fdividef(w, q[e]);
+            if (score > o.score) o.score = score, o.at = i + e;
+        }
+    }
+    __device__ void race_edge(Online &o, const T *row, const float *q, int i0) const
+    {
+        for (int i = i0 < 0 ? 0 : i0; i < i0 + kEach && i < static_cast<int>(vocab); ++i) {
+            const float v[1] = {static_cast<float>(row[i])}, noise[1] = {q[i]};
+            if (!(v[0] > -inf())) continue;
+            if (v[0] > o.most) rescale(o, v[0]);
+            race(o, v, noise, i);
+        }
+    }
+    __device__ Online race_all(const T *row, const float *q)
+    {
+        constexpr int kRaceLoads = kEach == 4 ? 4 : 2;   // chunks in flight, beside their noise
+        Online o;
+        const float *beside = q + first;
+        if (head && tid == 0) race_edge(o, row, q, first);
+        const bool aligned = reinterpret_cast<uintptr_t>(beside) % 16 == 0;
+        for (unsigned c0 = tid; c0 < hi; c0 += kRaceLoads * kThreads) {
+            uint4 x[kRaceLoads];
+            float4 n[kRaceLoads][kEach / 4];
+#pragma unroll
+            for (int u = 0; u < kRaceLoads; ++u) {
+                const unsigned c = c0 + u * kThreads;
+                const bool in = c >= lo && c < hi;
+                x[u] = in ? ld_stream(source + c) : make_uint4(C::kFill, C::kFill, C::kFill, C::kFill);
+#pragma unroll
+                for (int k = 0; k < kEach / 4; ++k) {
+                    const float *at = beside + static_cast<size_t>(c) * kEach + 4 * k;
+                    if (!in) n[u][k] = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+                    else if (aligned) n[u][k] = __ldcs(reinterpret_cast<const float4 *>(at));
+                    else n[u][k] = make_float4(__ldcs(at), __ldcs(at + 1), __ldcs(at + 2), __ldcs(at + 3));
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kRaceLoads; ++u) {
+                uint32_t bits[4];
+                unpack(x[u], bits);
+                const float most = C::most(bits, -inf());
+                if (most == -inf()) continue;
+                if (most > o.most) rescale(o, most);
+                float v[kEach], noise[kEach];
+#pragma unroll
+                for (int e = 0; e < kEach; ++e) {
+                    v[e] = C::value(bits, e);
+                    const float4 &f = n[u][e / 4];
+                    noise[e] = e % 4 == 0 ? f.x : e % 4 == 1 ? f.y : e % 4 == 2 ? f.z : f.w;
+                }
+                race(o, v, noise, first + static_cast<int>(c0 + u * kThreads) * kEach);
+            }
+        }
+        if (tail && tid == (mine - 1) % kThreads) race_edge(o, row, q, first + static_cast<int>(mine - 1) * kEach);
+        return o;
     }
     __device__ float edge_chunk(const T *row, unsigned c, float most)
     {
@@ -506,6 +598,11 @@ struct Draw {
 
     __device__ __forceinline__ void write(const T *row, u64 won, float rest, uint32_t tops, int32_t *token, float *logprob)
     {
+        if (won == 0) {   // no score at all: noise that is not a number
+            *token = -1;
+            if (logprob != nullptr) *logprob = -inf();
+            return;
+        }
         const unsigned i = index_of(won);
         *token = static_cast<int32_t>(i);
         if (logprob == nullptr) return;
@@ -712,7 +809,7 @@ sample_kernel(const T *__restrict__ logits, size_t stride, unsigned vocab, unsig
     const T *row = logits + static_cast<size_t>(r) * stride;
     if (d.tid == 0) s.merged_n[0] = s.merged_n[1] = 0;
     cluster_arrive();   // the blocks' shared memory is there from the matching wait on
-    const float most = d.load(row, per);
+    d.place(row, per);
 
     const float t = ask.temperature != nullptr ? ask.temperature[r] : 1.0f;
     int k = ask.top_k != nullptr ? ask.top_k[r] : 0;
@@ -725,15 +822,27 @@ sample_kernel(const T *__restrict__ logits, size_t stride, unsigned vocab, unsig
     int32_t *token = tokens + r;
     float *logprob = logprobs != nullptr ? logprobs + r : nullptr;
 
+    d.t = t;
+    d.scale = fminf(1.4426950408889634f / t, FLT_MAX);
+    const float *q = noise + static_cast<size_t>(r) * noise_stride;
+    const bool plain = !greedy && k == 0 && !by_mass && !(m > 0.0f);
+    typename D::Online online;
+    float most;
+    if (plain) {
+        online = d.race_all(row, q);
+        most = online.most;
+    } else {
+        most = d.load(row);
+    }
+
     // The largest logit, and the bound for the short list: the least, over the
     // warps whose lanes all hold tokens, of the j-th largest lane maximum.
     const uint32_t lane_top = ordered(most);
     const uint32_t warp_top = __reduce_max_sync(kFullMask, lane_top);
-    const unsigned shift = static_cast<unsigned>(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(T));
-    const unsigned chunks = (vocab + shift + D::kEach - 1) / D::kEach, last = (chunks - 1) / per;   // last block with any
+    const unsigned last = (d.chunks - 1) / per;   // the last block with any
     const unsigned full = min(d.mine / 32, static_cast<unsigned>(kWarps));
     const unsigned warps = last * min(per / 32, static_cast<unsigned>(kWarps)) +
-                           min((chunks - last * per) / 32, static_cast<unsigned>(kWarps));
+                           min((d.chunks - last * per) / 32, static_cast<unsigned>(kWarps));
     const int wanted = k > 0 ? k : kGuess;
     const int j = warps > 0 ? (wanted + static_cast<int>(warps) - 1) / static_cast<int>(warps) : 33;
     const bool bounded = !greedy && (k > 0 || by_mass) && vocab > kList && j <= 32;
@@ -772,15 +881,20 @@ sample_kernel(const T *__restrict__ logits, size_t stride, unsigned vocab, unsig
         return;
     }
     d.top = unordered(top);
+    typename D::Best best;
+    if (plain && d.top != inf()) {
+        const float f = fmaxf(exp2_approx((online.most - d.top) * d.scale), 0.0f);
+        if (online.at != 0x7fffffff) best.score = online.score * f, best.at = online.at;
+        if (f != 1.0f) online.rest = (online.rest + static_cast<float>(online.tops)) * f, online.tops = 0;
+        d.finish(row, best, online.rest, online.tops, token, logprob);
+        return;
+    }
     if (d.top == inf()) {   // the draw is among the infinite ones, which weigh the same
+        if (plain) d.load(row);
         d.only_infinite();
         d.top = 0.0f;
         bound = 0;          // all of them
     }
-    d.t = t;
-    d.scale = fminf(1.4426950408889634f / t, FLT_MAX);
-
-    typename D::Best best;
     if (greedy) {
         const float value = d.top;
         d.each_above(value, [&](float v, int i) {
@@ -789,7 +903,6 @@ sample_kernel(const T *__restrict__ logits, size_t stride, unsigned vocab, unsig
         d.finish(row, best, 0.0f, d.rank == 0 && d.tid == 0 ? 1 : 0, token, logprob);   // one token is kept
         return;
     }
-    const float *q = noise + static_cast<size_t>(r) * noise_stride;
 
     u64 cut = 0;
     if (k > 0 || by_mass) {
