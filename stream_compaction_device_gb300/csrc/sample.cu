@@ -10,21 +10,24 @@
 //   top-p : of those, tokens whose mass ahead is below p times their total;
 //   min-p : tokens with w_i >= m (the largest logit has w = 1).
 //
-// One thread-block cluster draws one row, which it reads from memory once and
-// keeps in shared memory, a slice per block; the blocks meet through
-// distributed shared memory.  The passes over a row (sum, selection, race)
-// then cost no memory traffic, and the noise is read only where a token is
-// kept.
+// One thread-block cluster draws one row, a slice of it per block; with rows
+// enough to fill the GPU the cluster is one block.  A row is read from memory
+// once, for its maximum (and, for top-p alone, its sum).  That pass leaves the
+// maximum of every group of four 16-byte chunks in shared memory, an index by
+// which later passes read again, out of L2, only the groups that hold a token
+// above their bound: a few hundred tokens of a row of 100,000.  The noise is
+// read only where a token is kept.  A row without truncation takes one pass
+// over logits and noise side by side.
 //
 // Selection has two forms.
 //   Short list.  Every full warp's j-th largest lane maximum is taken, and the
 //     least of them is a bound with at least j tokens per warp above it: for
 //     j = ceil(k / warps) the first k are all at or above the bound.  Those
-//     tokens (a few hundred) are collected, sorted by one block as 64-bit keys
-//     (ordered logit bits above the complement of the index), and top-k, top-p
-//     (a scan of the sorted weights) and min-p are cuts of the sorted list.
-//     top-p without top-k takes the same list if its mass reaches p times the
-//     row's.
+//     tokens (a few hundred) are collected and sorted by one block as 64-bit
+//     keys (ordered logit bits above the complement of the index), and top-k,
+//     top-p (a scan of the sorted weights) and min-p are cuts of the sorted
+//     list.  top-p without top-k takes the same list if its mass reaches p
+//     times the row's.
 //   Histograms.  Where the list would be too long (a wide top-k, a flat row,
 //     a tie of many tokens), the cut is bracketed by a histogram of counts or
 //     masses in shared memory, 32 bins per unit of logit, then of ordered
@@ -37,6 +40,7 @@
 
 #include <atomic>
 #include <cfloat>
+#include <cstring>
 
 #include "core.cuh"
 #include "launch.h"
@@ -50,10 +54,13 @@ using u64 = unsigned long long;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr unsigned kSliceChunks = 2048;    // 16-byte chunks of a block's slice, where the row allows: 32 KB
 constexpr int kLoads = 8;                  // 16-byte loads in flight per thread
+constexpr int kGroup = 4;                  // chunks to an entry of the index
+constexpr int kQueue = 64;                 // index entries that a warp has waiting
+constexpr unsigned kLeastChunks = 512;     // of a block's slice, where rows are few
 constexpr int kList = 1024;                // tokens the short list holds
 constexpr int kKeys = kList / kThreads;    // its keys per thread in the sort
+constexpr int kRanked = 512;               // lists up to here are ordered by counting
 constexpr int kBins = 1024;
 constexpr float kBinsPerUnit = 32.0f;      // first histogram: bins per unit of logit
 constexpr int kGuess = 256;                // tokens asked of the bound for top-p without top-k
@@ -81,11 +88,6 @@ __device__ __forceinline__ void cluster_arrive()
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_sync()
-{
-    cluster_arrive();
-    cluster_wait();
-}
 __device__ __forceinline__ uint32_t remote(const void *p, unsigned rank)
 {
     uint32_t a;
@@ -201,6 +203,8 @@ struct Shared {
             uint32_t carry[kBins];   // the masses' high words
         };
     };
+    uint4 edge[2];                   // the slice's chunks over the row's ends
+    uint16_t queue[kWarps][kQueue];
     u64 warp64[kWarps];
     float warpf[kWarps];
     uint32_t warp_max[kWarps], warp_bound[kWarps], warp_n[kWarps];
@@ -208,17 +212,17 @@ struct Shared {
     uint32_t top[kMaxCluster], bound[kMaxCluster];
     uint32_t found[2][kMaxCluster];
     float sum[2][kMaxCluster];
-    float sum_above[kMaxCluster];
+    float sum_all[kMaxCluster];
     u64 won[kMaxCluster];
     float rest[kMaxCluster];
     uint32_t tops[kMaxCluster];
-    u64 mass[kMaxCluster];
     u64 cut;
     uint32_t merged_n[2];            // in block 0: places of its merged list that are given out
     // Results of one block's scans.
     u64 pick_before;
     uint32_t pick_bin, pick_lo, pick_hi;
-    uint32_t local_n;
+    uint32_t listed;                 // tokens collected by this block (counting stops above kList)
+    uint32_t local_base;
 };
 constexpr size_t kSharedBytes = (sizeof(Shared) + 127) / 128 * 128;
 
@@ -228,55 +232,40 @@ struct Draw {
     static constexpr int kEach = C::kEach;
 
     Shared &s;
-    uint4 *slice;                    // this block's chunks of the row
+    float *index;                    // maxima of this block's groups of chunks
+    const T *row;
+    const uint4 *source;             // the slice
     unsigned tid, lane, warp, rank, blocks;
-    unsigned vocab, mine;            // tokens of the row; chunks of the slice
+    unsigned vocab, chunks, mine;    // tokens and chunks of the row; chunks of the slice
+    unsigned lo, hi;                 // the slice's whole chunks
     int first;                       // index of the slice's first value
     float top, t, scale;             // the largest logit, temperature, log2(e) / T
+    bool infinite = false;           // the largest is +inf: it counts as 0, all else as -inf
     int turn = 0;                    // which half of the double buffers is next
 
     __device__ __forceinline__ Draw(Shared &shared) : s(shared) {}
+
+    // All threads of the cluster.
+    __device__ __forceinline__ void meet() const
+    {
+        if (blocks == 1) {
+            __syncthreads();
+        } else {
+            cluster_arrive();
+            cluster_wait();
+        }
+    }
 
     static __device__ __forceinline__ void unpack(const uint4 &v, uint32_t (&q)[4])
     {
         q[0] = v.x, q[1] = v.y, q[2] = v.z, q[3] = v.w;
     }
 
-    // f(value, index) for every value of this thread's chunks (each thread
-    // reads those that it wrote, so no barrier stands between).  each_above
-    // leaves out chunks without a value of at least `low`.
-    template <class F>
-    __device__ __forceinline__ void each(F f)
-    {
-        for (unsigned c = tid; c < mine; c += kThreads) {
-            uint32_t q[4];
-            unpack(slice[c], q);
-            const int i = first + static_cast<int>(c) * kEach;
-#pragma unroll
-            for (int e = 0; e < kEach; ++e) f(C::value(q, e), i + e);
-        }
-    }
-    template <class F>
-    __device__ __forceinline__ void each_above(float low, F f)
-    {
-        for (unsigned c = tid; c < mine; c += kThreads) {
-            uint32_t q[4];
-            unpack(slice[c], q);
-            if (!(C::most(q, -inf()) >= low)) continue;
-            const int i = first + static_cast<int>(c) * kEach;
-#pragma unroll
-            for (int e = 0; e < kEach; ++e) f(C::value(q, e), i + e);
-        }
-    }
-
     // The block's slice of the row.  Rows may start anywhere: chunk 0 begins
     // at the 16-byte boundary at or before the row, and a chunk that reaches
-    // over either end of the row is read value by value and filled with -inf.
-    // [lo, hi): the slice's whole chunks; head, tail: it has such a chunk.
-    unsigned chunks, lo, hi;         // chunks of the row
-    bool head, tail;
-    const uint4 *source;
-    __device__ __forceinline__ void place(const T *row, unsigned per)
+    // over either end of the row is read value by value into shared memory,
+    // filled with -inf.
+    __device__ __forceinline__ void place(unsigned per)
     {
         const unsigned shift = static_cast<unsigned>(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(T));
         const unsigned begin = rank * per;
@@ -284,36 +273,135 @@ struct Draw {
         mine = begin < chunks ? min(per, chunks - begin) : 0;
         first = static_cast<int>(begin * kEach) - static_cast<int>(shift);
         source = reinterpret_cast<const uint4 *>(row - shift) + begin;
-        head = first < 0 && mine > 0;
-        tail = mine > 0 && first + static_cast<int>(mine) * kEach > static_cast<int>(vocab);
+        const bool head = first < 0 && mine > 0;
+        const bool tail = mine > 0 && first + static_cast<int>(mine) * kEach > static_cast<int>(vocab);
         lo = head ? 1 : 0;
         hi = tail ? mine - 1 : mine;
-        if (head && mine == 1) tail = false;   // one chunk over both ends
+        // The first loads' lines are on their way to L2 before the settings
+        // have come, on which the first pass depends.
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u)
+            if (tid + u * kThreads >= lo && tid + u * kThreads < hi)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(source + tid + u * kThreads));
+        if (head || tail) {
+            if (head && tid == 0) edge_chunk(0, &s.edge[0]);
+            if (tail && !(head && mine == 1) && tid == 32) edge_chunk(mine - 1, &s.edge[1]);
+            __syncthreads();
+        }
+    }
+    __device__ void edge_chunk(unsigned c, uint4 *to)
+    {
+        T *v = reinterpret_cast<T *>(to);
+        for (int e = 0; e < kEach; ++e) {
+            const int i = first + static_cast<int>(c) * kEach + e;
+            v[e] = i >= 0 && i < static_cast<int>(vocab) ? row[i] : T(-inf());
+        }
+    }
+    static __device__ __forceinline__ uint4 fill() { return make_uint4(C::kFill, C::kFill, C::kFill, C::kFill); }
+    __device__ __forceinline__ uint4 chunk(unsigned c) const
+    {
+        if (c >= lo && c < hi) return __ldg(source + c);
+        if (c >= mine) return fill();
+        return s.edge[c == 0 && lo == 1 ? 0 : 1];
     }
 
-    // Reads the slice into shared memory; returns the thread's largest value.
-    __device__ __forceinline__ float load(const T *row)
+    // First pass: the thread's largest value, the index, and with SUM the
+    // thread's sum of weights relative to it.  Entry (k, thread) of the index
+    // is for the chunks thread + (kGroup * k + u) * kThreads.
+    template <bool SUM>
+    __device__ __forceinline__ float load(float *sum)
     {
-        float most = -inf();
-        for (unsigned c0 = tid; c0 < hi; c0 += kLoads * kThreads) {
+        float most = -inf(), held = 0.0f;
+        unsigned entry = tid;
+        for (unsigned c0 = tid; c0 < mine; c0 += kLoads * kThreads) {
             uint4 v[kLoads];
 #pragma unroll
-            for (int u = 0; u < kLoads; ++u) {
-                const unsigned c = c0 + u * kThreads;
-                v[u] = c >= lo && c < hi ? ld_stream(source + c) : make_uint4(C::kFill, C::kFill, C::kFill, C::kFill);
-            }
+            for (int u = 0; u < kLoads; ++u) v[u] = chunk(c0 + u * kThreads);
 #pragma unroll
-            for (int u = 0; u < kLoads; ++u) {
-                const unsigned c = c0 + u * kThreads;
-                uint32_t q[4];
-                unpack(v[u], q);
-                most = C::most(q, most);
-                if (c >= lo && c < hi) slice[c] = v[u];
+            for (int g = 0; g < kLoads; g += kGroup) {
+                float group = -inf();
+#pragma unroll
+                for (int u = g; u < g + kGroup; ++u) {
+                    uint32_t q[4];
+                    unpack(v[u], q);
+                    group = C::most(q, group);
+                }
+                if (g == 0 || c0 + g * kThreads < mine) index[entry] = group;
+                entry += kThreads;
+                if (SUM && group > -inf()) {
+                    if (group > most) held *= fmaxf(exp2_approx((most - group) * scale), 0.0f);
+                    const float base = fmaxf(most, group);
+#pragma unroll
+                    for (int u = g; u < g + kGroup; ++u) {
+                        uint32_t q[4];
+                        unpack(v[u], q);
+#pragma unroll
+                        for (int e = 0; e < kEach; ++e)
+                            held += fmaxf(exp2_approx((C::value(q, e) - base) * scale), 0.0f);
+                    }
+                }
+                most = fmaxf(most, group);
             }
         }
-        if (head && tid == 0) most = edge_chunk(row, 0, most);
-        if (tail && tid == (mine - 1) % kThreads) most = edge_chunk(row, mine - 1, most);
+        if (SUM) *sum = held;
         return most;
+    }
+
+    // f(value, index) for every value of at least `low` and those beside it in
+    // its chunk.  A warp queues the index entries that reach `low` and reads
+    // 32 groups at a time, one per lane.
+    template <class F>
+    __device__ __forceinline__ void each_above(float low, F f)
+    {
+        uint16_t *queue = s.queue[warp];
+        unsigned waiting = 0;
+        const unsigned entries = (mine + kGroup * kThreads - 1) / (kGroup * kThreads);
+        for (unsigned k = 0; k <= entries; ++k) {
+            if (k < entries) {
+                // A thread's first group is there if its first chunk is.
+                const bool in = tid + k * kGroup * kThreads < mine && index[k * kThreads + tid] >= low;
+                const unsigned some = __ballot_sync(kFullMask, in);
+                if (in) queue[waiting + __popc(some & ((1u << lane) - 1))] = static_cast<uint16_t>(k * 32 + lane);
+                waiting += __popc(some);
+                if (waiting < 32) continue;
+            } else if (waiting == 0) {
+                return;
+            }
+            __syncwarp();
+            const unsigned taken = min(waiting, 32u);
+            const unsigned at = lane < taken ? queue[lane] : 0;
+            const unsigned moved = lane + 32 < waiting ? queue[lane + 32] : 0;
+            __syncwarp();
+            if (lane + 32 < waiting) queue[lane] = static_cast<uint16_t>(moved);
+            waiting -= taken;
+            if (lane < taken) {
+                const unsigned c0 = (at / 32) * kGroup * kThreads + warp * 32 + at % 32;
+                uint4 v[kGroup];
+#pragma unroll
+                for (int u = 0; u < kGroup; ++u) v[u] = chunk(c0 + u * kThreads);
+#pragma unroll
+                for (int u = 0; u < kGroup; ++u) {
+                    uint32_t q[4];
+                    unpack(v[u], q);
+                    if (infinite) only_infinite(q);
+                    if (!(C::most(q, -inf()) >= low)) continue;
+                    const int i = first + static_cast<int>(c0 + u * kThreads) * kEach;
+#pragma unroll
+                    for (int e = 0; e < kEach; ++e) f(C::value(q, e), i + e);
+                }
+            }
+            __syncwarp();
+        }
+    }
+
+    // Replaces every +inf by 0 and everything else by -inf.
+    static __device__ void only_infinite(uint32_t (&q)[4])
+    {
+        T v[kEach];
+        memcpy(v, q, 16);
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) v[e] = static_cast<float>(v[e]) == inf() ? T(0.0f) : T(-inf());
+        memcpy(q, v, 16);
     }
 
     // A race of all tokens needs no selection, so it takes one pass over the
@@ -345,7 +433,7 @@ struct Draw {
             if (score > o.score) o.score = score, o.at = i + e;
         }
     }
-    __device__ void race_edge(Online &o, const T *row, const float *q, int i0) const
+    __device__ void race_edge(Online &o, const float *q, int i0) const
     {
         for (int i = i0 < 0 ? 0 : i0; i < i0 + kEach && i < static_cast<int>(vocab); ++i) {
             const float v[1] = {static_cast<float>(row[i])}, noise[1] = {q[i]};
@@ -354,12 +442,12 @@ struct Draw {
             race(o, v, noise, i);
         }
     }
-    __device__ Online race_all(const T *row, const float *q)
+    __device__ Online race_all(const float *q)
     {
         constexpr int kRaceLoads = kEach == 4 ? 4 : 2;   // chunks in flight, beside their noise
         Online o;
         const float *beside = q + first;
-        if (head && tid == 0) race_edge(o, row, q, first);
+        if (lo == 1 && tid == 0) race_edge(o, q, first);
         const bool aligned = reinterpret_cast<uintptr_t>(beside) % 16 == 0;
         for (unsigned c0 = tid; c0 < hi; c0 += kRaceLoads * kThreads) {
             uint4 x[kRaceLoads];
@@ -394,28 +482,9 @@ struct Draw {
                 race(o, v, noise, first + static_cast<int>(c0 + u * kThreads) * kEach);
             }
         }
-        if (tail && tid == (mine - 1) % kThreads) race_edge(o, row, q, first + static_cast<int>(mine - 1) * kEach);
+        if (hi < mine && mine > lo && tid == (mine - 1) % kThreads)
+            race_edge(o, q, first + static_cast<int>(mine - 1) * kEach);
         return o;
-    }
-    __device__ float edge_chunk(const T *row, unsigned c, float most)
-    {
-        T *to = reinterpret_cast<T *>(slice + c);
-        for (int e = 0; e < kEach; ++e) {
-            const int i = first + static_cast<int>(c) * kEach + e;
-            const bool in = i >= 0 && i < static_cast<int>(vocab);
-            to[e] = in ? row[i] : T(-inf());
-            if (in) most = fmaxf(most, static_cast<float>(row[i]));
-        }
-        return most;
-    }
-
-    // Replaces every +inf by 0 and everything else by -inf.
-    __device__ void only_infinite()
-    {
-        for (unsigned c = tid; c < mine; c += kThreads) {
-            T *v = reinterpret_cast<T *>(slice + c);
-            for (int e = 0; e < kEach; ++e) v[e] = static_cast<float>(v[e]) == inf() ? T(0.0f) : T(-inf());
-        }
     }
 
     // Weight of any value (0 for -inf and NaN): the race and the sums over
@@ -466,41 +535,39 @@ struct Draw {
     }
 
     // Collects the tokens for which in(v, i) holds (none below `low`) into
-    // block 0's merged list, if there are at most kList of them.  Returns their number (the same in
-    // every block).  sum: a partial sum of each thread, summed into
-    // s.sum[turn] of every block by rank.
-    template <class In>
-    __device__ uint32_t collect(float low, In in, float *sum)
+    // block 0's merged list, in any order, if there are at most kList of them.
+    // Returns their number, or more than kList (the same in every block).
+    // sum(): a partial sum of each thread, asked for after the pass, summed
+    // into s.sum[turn] of every block by rank.
+    template <class In, class Sum>
+    __device__ uint32_t collect(float low, In in, Sum sum)
     {
         const int now = turn;
         turn ^= 1;
-        uint32_t found = 0;
-        each_above(low, [&](float v, int i) { found += in(v, i) ? 1u : 0u; });
-        uint32_t n = 0;
-        const uint32_t at = block_scan(found, s.warp_n, &n);
-        float total = 0.0f;
-        if (sum != nullptr) total = block_sum(*sum);
-        if (found != 0 && n <= kList) {
-            uint32_t k = at;
-            each_above(low, [&](float v, int i) {
-                if (in(v, i)) s.list[k++] = key_of(ordered(v), static_cast<unsigned>(i));
-            });
-        }
+        if (tid == 0) s.listed = 0;
+        __syncthreads();
+        each_above(low, [&](float v, int i) {
+            if (!in(v, i) || *const_cast<volatile uint32_t *>(&s.listed) > kList) return;
+            const uint32_t k = atomicAdd(&s.listed, 1u);
+            if (k < kList) s.list[k] = key_of(ordered(v), static_cast<unsigned>(i));
+        });
+        const float total = block_sum(sum());
+        const uint32_t n = s.listed;
         if (tid == 0) {
             s.merged_n[now ^ 1] = 0;
-            s.local_n = n == 0 || n > kList ? kList + 1 : fetch_add(&s.merged_n[now], 0, n);
+            s.local_base = n == 0 || n > kList ? kList + 1 : fetch_add(&s.merged_n[now], 0, n);
         }
         if (tid < blocks) {
             put(&s.found[now][rank], tid, n);
-            if (sum != nullptr) put(&s.sum[now][rank], tid, total);
+            put(&s.sum[now][rank], tid, total);
         }
         __syncthreads();
-        const uint32_t base = s.local_n;
+        const uint32_t base = s.local_base;
         if (n <= kList && base + n <= kList)
             for (uint32_t k = tid; k < n; k += kThreads) put(&s.merged[base + k], 0, s.list[k]);
-        cluster_sync();
+        meet();
         uint32_t all = 0;
-        for (unsigned b = 0; b < blocks; ++b) all += s.found[now][b];
+        for (unsigned b = 0; b < blocks; ++b) all += min(s.found[now][b], static_cast<uint32_t>(kList + 1));
         return all;
     }
 
@@ -511,11 +578,49 @@ struct Draw {
         return v;
     }
 
-    // Sorts merged[0 .. n), n <= kList, descending, by this block (a bitonic
-    // sort of 64-bit keys: strides inside a warp by shuffles, up to the block
-    // through shared memory, above inside a thread).  Thread t gets the keys
-    // at t + h * kThreads; 0 past the end.
-    __device__ void sort(uint32_t n, u64 (&a)[kKeys])
+    // Puts the first `limit` of merged[0 .. n), n <= kList, in descending
+    // order, by this block.  Thread t gets the keys at t + h * kThreads; 0 past
+    // the end.  Up to kRanked keys, each key's place is the number of larger
+    // ones, counted in one loop without a barrier; above, a bitonic sort takes
+    // fewer steps.
+    __device__ void sort(uint32_t n, uint32_t limit, u64 (&a)[kKeys])
+    {
+        if (n > kRanked) {
+            bitonic(n, a);
+            return;
+        }
+        constexpr int kHeld = kRanked / kThreads;
+        u64 key[kHeld];
+        uint32_t place[kHeld];
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h) {
+            key[h] = tid + h * kThreads < n ? s.merged[tid + h * kThreads] : 0;
+            place[h] = 0;
+        }
+        const bool two = n > kThreads;
+        if (!two) {
+            if (warp * 32 < n)
+#pragma unroll 8
+                for (uint32_t k = 0; k < n; ++k) place[0] += s.merged[k] > key[0] ? 1u : 0u;
+        } else {
+#pragma unroll 4
+            for (uint32_t k = 0; k < n; ++k) {
+                const u64 other = s.merged[k];
+#pragma unroll
+                for (int h = 0; h < kHeld; ++h) place[h] += other > key[h] ? 1u : 0u;
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h)
+            if (key[h] != 0) s.list[place[h]] = key[h];
+        __syncthreads();
+#pragma unroll
+        for (int h = 0; h < kKeys; ++h) a[h] = tid + h * kThreads < min(n, limit) ? s.list[tid + h * kThreads] : 0;
+    }
+
+    // Bitonic sort of merged[0 .. n): strides inside a warp by shuffles, up to
+    // the block through shared memory, above inside a thread.
+    __device__ void bitonic(uint32_t n, u64 (&a)[kKeys])
     {
         unsigned size2 = 32;
         while (size2 < n) size2 *= 2;
@@ -569,7 +674,7 @@ struct Draw {
         int at = 0x7fffffff;
         __device__ __forceinline__ void offer(float sc, int i)
         {
-            if (sc > score) score = sc, at = i;
+            if (sc > score || (sc == score && i < at)) score = sc, at = i;
         }
         __device__ __forceinline__ u64 key() const
         {
@@ -577,26 +682,7 @@ struct Draw {
         }
     };
 
-    __device__ __forceinline__ u64 block_most(u64 v)
-    {
-#pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) {
-            const u64 u = __shfl_xor_sync(kFullMask, v, d);
-            v = u > v ? u : v;
-        }
-        __syncthreads();
-        if (lane == 0) s.warp64[warp] = v;
-        __syncthreads();
-        v = s.warp64[lane & (kWarps - 1)];
-#pragma unroll
-        for (int d = kWarps / 2; d >= 1; d >>= 1) {
-            const u64 u = __shfl_xor_sync(kFullMask, v, d);
-            v = u > v ? u : v;
-        }
-        return v;
-    }
-
-    __device__ __forceinline__ void write(const T *row, u64 won, float rest, uint32_t tops, int32_t *token, float *logprob)
+    __device__ __forceinline__ void write(u64 won, float rest, uint32_t tops, int32_t *token, float *logprob)
     {
         if (won == 0) {   // no score at all: noise that is not a number
             *token = -1;
@@ -611,33 +697,51 @@ struct Draw {
         *logprob = d - log1pf(rest + static_cast<float>(tops - 1));
     }
 
-    // Joins the blocks' races and writes the row's answer.
-    __device__ __forceinline__ void finish(const T *row, const Best &best, float rest, uint32_t tops, int32_t *token,
-                                           float *logprob)
+    // The block's race: thread 0 gets the winner and the sums.
+    __device__ __forceinline__ void join(u64 &won, float &rest, uint32_t &tops)
     {
-        const u64 won = block_most(best.key());
-        rest = block_sum(rest);
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) {
+            const u64 u = __shfl_xor_sync(kFullMask, won, d);
+            won = u > won ? u : won;
+            rest += __shfl_xor_sync(kFullMask, rest, d);
+        }
         tops = __reduce_add_sync(kFullMask, tops);
-        if (lane == 0) s.warp_n[warp] = tops;
         __syncthreads();
+        if (lane == 0) s.warp64[warp] = won, s.warpf[warp] = rest, s.warp_n[warp] = tops;
+        __syncthreads();
+        if (tid != 0) return;
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) {
+            won = s.warp64[w] > won ? s.warp64[w] : won;
+            rest += s.warpf[w];
+            tops += s.warp_n[w];
+        }
+    }
+
+    // Joins the blocks' races and writes the row's answer.
+    __device__ __forceinline__ void finish(const Best &best, float rest, uint32_t tops, int32_t *token, float *logprob)
+    {
+        u64 won = best.key();
+        join(won, rest, tops);
+        if (blocks == 1) {
+            if (tid == 0) write(won, rest, tops, token, logprob);
+            return;
+        }
         if (tid == 0) {
-            uint32_t all = 0;
-            for (int w = 0; w < kWarps; ++w) all += s.warp_n[w];
             put(&s.won[rank], 0, won);
             put(&s.rest[rank], 0, rest);
-            put(&s.tops[rank], 0, all);
+            put(&s.tops[rank], 0, tops);
         }
-        cluster_sync();
+        meet();
         if (rank != 0 || tid != 0) return;
-        u64 w = 0;
-        float r = 0.0f;
-        uint32_t n = 0;
+        won = 0, rest = 0.0f, tops = 0;
         for (unsigned b = 0; b < blocks; ++b) {
-            w = s.won[b] > w ? s.won[b] : w;
-            r += s.rest[b];
-            n += s.tops[b];
+            won = s.won[b] > won ? s.won[b] : won;
+            rest += s.rest[b];
+            tops += s.tops[b];
         }
-        write(row, w, r, n, token, logprob);
+        write(won, rest, tops, token, logprob);
     }
 
     // The bin of the first histogram: falls as v grows.
@@ -647,10 +751,11 @@ struct Draw {
     }
 
     // One histogram level: adds what each value holds, then finds the bin
-    // where the running total from bin 0 reaches `want`.  Returns false if it
-    // does not; else `bin`, and `want` less what is in the bins before it.
-    template <bool MASS, class Bin>
-    __device__ bool histogram(float low, Bin bin_in, u64 &want, uint32_t &bin)
+    // where the running total from bin 0 reaches want = wanted(total).  Returns
+    // false if it does not; else `bin`, and `want` less what is in the bins
+    // before it.
+    template <bool MASS, class Bin, class Want>
+    __device__ bool histogram(float low, Bin bin_in, Want wanted, u64 &want, uint32_t &bin)
     {
         for (unsigned b = tid; b < kBins; b += kThreads) s.count[b] = s.carry[b] = 0;
         __syncthreads();
@@ -666,7 +771,7 @@ struct Draw {
                 atomicAdd(&s.count[b], 1u);
             }
         });
-        cluster_sync();
+        meet();
         // Thread t sums the bins from kPer * t on, of all blocks.
         constexpr int kPer = kBins / kThreads;
         u64 h[kPer], own = 0;
@@ -683,6 +788,7 @@ struct Draw {
         for (int k = 0; k < kPer; ++k) own += h[k];
         u64 all = 0;
         u64 before = block_scan(own, s.warp64, &all);
+        want = wanted(all);
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
             if (before < want && want <= before + h[k]) {
@@ -691,7 +797,7 @@ struct Draw {
             }
             before += h[k];
         }
-        cluster_sync();   // the histogram's memory is used again from here
+        meet();   // the histogram's memory is used again from here
         if (all < want) return false;
         bin = s.pick_bin;
         want -= s.pick_before;
@@ -711,16 +817,21 @@ struct Draw {
     }
 
     // The key of the last token, in the order, of the shortest prefix that
-    // holds `want` (tokens, or mass); 0 if all of them do not.  Only tokens
-    // with keys >= floor take part.
-    template <bool MASS>
-    __device__ u64 select(u64 floor, u64 want)
+    // holds wanted(total) (tokens, or mass); 0 if all of them do not.  Only
+    // tokens with keys >= floor take part.
+    template <bool MASS, class Want>
+    __device__ u64 select(u64 floor, Want wanted)
     {
+        u64 want = 0;
+        const auto same = [&](u64) { return want; };
         const float floor_v = floor == 0 ? -FLT_MAX : unordered(ord_of(floor));
         const int floor_i = floor == 0 ? 0x7fffffff : static_cast<int>(index_of(floor));
         const auto takes_part = [&](float v, int i) { return v > floor_v || (v == floor_v && i <= floor_i); };
         uint32_t bin = 0;
-        if (!histogram<MASS>(floor_v, [&](float v, int i) { return takes_part(v, i) ? bin_of(v) : -1; }, want, bin)) return 0;
+        // Below top - 23 T a weight rounds to no mass.
+        const float least = MASS ? fmaxf(floor_v, top - 23.0f * t) : floor_v;
+        if (!histogram<MASS>(least, [&](float v, int i) { return takes_part(v, i) ? bin_of(v) : -1; }, wanted, want, bin))
+            return 0;
         if (tid == 0) s.pick_lo = edge(static_cast<int>(bin));
         if (tid == 32) s.pick_hi = bin == 0 ? ordered(top) : edge(static_cast<int>(bin) - 1) - 1;
         __syncthreads();
@@ -733,11 +844,11 @@ struct Draw {
                 return v >= v_lo && v <= v_hi && takes_part(v, i) &&
                        (!tie || (static_cast<unsigned>(i) >= i_lo && static_cast<unsigned>(i) <= i_hi));
             };
-            const uint32_t n = collect(v_lo, inside, nullptr);
+            const uint32_t n = collect(v_lo, inside, [] { return 0.0f; });
             if (n <= kList) {
                 if (rank == 0) {
                     u64 key[kKeys], base = 0;
-                    sort(n, key);
+                    sort(n, n, key);
 #pragma unroll
                     for (int h = 0; h < kKeys; ++h) {
                         u64 holds = 0, total = 0;
@@ -749,7 +860,7 @@ struct Draw {
                     __syncthreads();
                     if (tid < blocks) put(&s.cut, tid, s.pick_before);
                 }
-                cluster_sync();
+                meet();
                 return s.cut;
             }
             if (!tie) {
@@ -757,7 +868,7 @@ struct Draw {
                 while ((hi - lo) >> shift >= kBins) ++shift;
                 histogram<MASS>(v_lo, [&](float v, int i) {
                     return inside(v, i) ? static_cast<int>((hi - ordered(v)) >> shift) : -1;
-                }, want, bin);
+                }, same, want, bin);
                 const uint32_t new_hi = hi - (bin << shift), width = (1u << shift) - 1;
                 lo = new_hi - lo > width ? new_hi - width : lo;
                 hi = new_hi;
@@ -766,30 +877,13 @@ struct Draw {
                 while ((i_hi - i_lo) >> shift >= kBins) ++shift;
                 histogram<MASS>(v_lo, [&](float v, int i) {
                     return inside(v, i) ? static_cast<int>((static_cast<unsigned>(i) - i_lo) >> shift) : -1;
-                }, want, bin);
+                }, same, want, bin);
                 i_lo += bin << shift;
                 i_hi = min(i_hi, i_lo + ((1u << shift) - 1));
             }
         }
     }
 
-    // Mass of the tokens with keys >= floor, over the cluster.
-    __device__ u64 mass_from(u64 floor)
-    {
-        const float floor_v = floor == 0 ? -FLT_MAX : unordered(ord_of(floor));
-        const int floor_i = floor == 0 ? 0x7fffffff : static_cast<int>(index_of(floor));
-        u64 sum = 0;
-        each_above(floor_v, [&](float v, int i) {
-            if (v > floor_v || (v == floor_v && i <= floor_i)) sum += mass(v);
-        });
-        u64 all = 0;
-        block_scan(sum, s.warp64, &all);
-        if (tid < blocks) put(&s.mass[rank], tid, all);
-        cluster_sync();
-        all = 0;
-        for (unsigned b = 0; b < blocks; ++b) all += s.mass[b];
-        return all;
-    }
 };
 
 template <class T>
@@ -802,14 +896,14 @@ sample_kernel(const T *__restrict__ logits, size_t stride, unsigned vocab, unsig
     Shared &s = *reinterpret_cast<Shared *>(s_bytes);
     using D = Draw<T>;
     D d(s);
-    d.slice = reinterpret_cast<uint4 *>(s_bytes + kSharedBytes);
+    d.index = reinterpret_cast<float *>(s_bytes + kSharedBytes);
     d.tid = threadIdx.x, d.lane = d.tid & 31, d.warp = d.tid >> 5;
     d.rank = cluster_rank(), d.blocks = cluster_blocks(), d.vocab = vocab;
     const unsigned r = blockIdx.x / d.blocks;
-    const T *row = logits + static_cast<size_t>(r) * stride;
+    d.row = logits + static_cast<size_t>(r) * stride;
     if (d.tid == 0) s.merged_n[0] = s.merged_n[1] = 0;
-    cluster_arrive();   // the blocks' shared memory is there from the matching wait on
-    d.place(row, per);
+    if (d.blocks > 1) cluster_arrive();   // the blocks' shared memory is there from the matching wait on
+    d.place(per);
 
     const float t = ask.temperature != nullptr ? ask.temperature[r] : 1.0f;
     int k = ask.top_k != nullptr ? ask.top_k[r] : 0;
@@ -827,12 +921,15 @@ sample_kernel(const T *__restrict__ logits, size_t stride, unsigned vocab, unsig
     const float *q = noise + static_cast<size_t>(r) * noise_stride;
     const bool plain = !greedy && k == 0 && !by_mass && !(m > 0.0f);
     typename D::Online online;
-    float most;
+    const bool whole = !greedy && k == 0 && by_mass;   // top-p over the whole row
+    float most, sum = 0.0f;
     if (plain) {
-        online = d.race_all(row, q);
+        online = d.race_all(q);
         most = online.most;
+    } else if (whole) {
+        most = d.template load<true>(&sum);
     } else {
-        most = d.load(row);
+        most = d.template load<false>(nullptr);
     }
 
     // The largest logit, and the bound for the short list: the least, over the
@@ -845,7 +942,7 @@ sample_kernel(const T *__restrict__ logits, size_t stride, unsigned vocab, unsig
                            min((d.chunks - last * per) / 32, static_cast<unsigned>(kWarps));
     const int wanted = k > 0 ? k : kGuess;
     const int j = warps > 0 ? (wanted + static_cast<int>(warps) - 1) / static_cast<int>(warps) : 33;
-    const bool bounded = !greedy && (k > 0 || by_mass) && vocab > kList && j <= 32;
+    const bool bounded = !greedy && (k > 0 || by_mass) && j <= 32;
     uint32_t bound = ~0u;
     if (bounded && d.warp < full) {
         uint32_t left = lane_top;
@@ -857,7 +954,7 @@ sample_kernel(const T *__restrict__ logits, size_t stride, unsigned vocab, unsig
     }
     if (d.lane == 0) s.warp_max[d.warp] = warp_top, s.warp_bound[d.warp] = bound;
     __syncthreads();
-    cluster_wait();
+    if (d.blocks > 1) cluster_wait();
     if (d.warp == 0) {
         const uint32_t a = __reduce_max_sync(kFullMask, s.warp_max[d.lane & (kWarps - 1)]);
         const uint32_t b = __reduce_min_sync(kFullMask, s.warp_bound[d.lane & (kWarps - 1)]);
@@ -866,7 +963,7 @@ sample_kernel(const T *__restrict__ logits, size_t stride, unsigned vocab, unsig
             put(&s.bound[d.rank], d.lane, b);
         }
     }
-    cluster_sync();
+    d.meet();
     uint32_t top = 0;
     bound = ~0u;
     for (unsigned b = 0; b < d.blocks; ++b) {
@@ -886,12 +983,12 @@ sample_kernel(const T *__restrict__ logits, size_t stride, unsigned vocab, unsig
         const float f = fmaxf(exp2_approx((online.most - d.top) * d.scale), 0.0f);
         if (online.at != 0x7fffffff) best.score = online.score * f, best.at = online.at;
         if (f != 1.0f) online.rest = (online.rest + static_cast<float>(online.tops)) * f, online.tops = 0;
-        d.finish(row, best, online.rest, online.tops, token, logprob);
+        d.finish(best, online.rest, online.tops, token, logprob);
         return;
     }
     if (d.top == inf()) {   // the draw is among the infinite ones, which weigh the same
-        if (plain) d.load(row);
-        d.only_infinite();
+        if (plain) d.template load<false>(nullptr);
+        d.infinite = true;
         d.top = 0.0f;
         bound = 0;          // all of them
     }
@@ -900,49 +997,49 @@ sample_kernel(const T *__restrict__ logits, size_t stride, unsigned vocab, unsig
         d.each_above(value, [&](float v, int i) {
             if (v == value) best.offer(1.0f, i);
         });
-        d.finish(row, best, 0.0f, d.rank == 0 && d.tid == 0 ? 1 : 0, token, logprob);   // one token is kept
+        d.finish(best, 0.0f, d.rank == 0 && d.tid == 0 ? 1 : 0, token, logprob);   // one token is kept
         return;
     }
 
     u64 cut = 0;
     if (k > 0 || by_mass) {
         const float low = bounded ? fmaxf(unordered(max(bound, kOrderedMinusInf)), -FLT_MAX) : -FLT_MAX;
-        // The sums that top-p without top-k needs: the row's, and the list's.
-        const bool whole = k == 0;
-        float sum = 0.0f, above = 0.0f;
+        const float scaled = whole ? sum * fmaxf(exp2_approx((most - d.top) * d.scale), 0.0f) : 0.0f;
+        float above = 0.0f;
         if (whole) {
-            d.each([&](float v, int) {
-                const float w = d.weight(v);
-                sum += w;
-                if (v >= low) above += w;
-            });
-            above = d.block_sum(above);
-            if (d.tid < d.blocks) put(&s.sum_above[d.rank], d.tid, above);
+            const float all = d.block_sum(scaled);
+            if (d.tid < d.blocks) put(&s.sum_all[d.rank], d.tid, all);
         }
         const int now = d.turn;
-        const uint32_t n = d.collect(low, [&](float v, int) { return v >= low; }, whole ? &sum : nullptr);
+        const uint32_t n = d.collect(low, [&](float v, int) {
+            if (!(v >= low)) return false;
+            if (whole) above += d.weight(v);
+            return true;
+        }, [&] { return above; });
         float total = 0.0f;
         bool enough = true;
         if (whole) {
-            total = d.cluster_sum(now);
-            above = 0.0f;
-            for (unsigned b = 0; b < d.blocks; ++b) above += s.sum_above[b];
-            enough = low == -FLT_MAX || above > p * total * (1.0f + 1.0f / 4096);
+            for (unsigned b = 0; b < d.blocks; ++b) total += s.sum_all[b];
+            enough = !d.infinite && (low == -FLT_MAX || d.cluster_sum(now) > p * total * (1.0f + 1.0f / 4096));
         }
         if (n <= kList && enough) {
             if (d.rank != 0) return;
-            u64 key[kKeys];
-            d.sort(n, key);
-            float w[kKeys], ahead[kKeys], listed = 0.0f;
-            uint32_t tops = 0;
-            float rest = 0.0f;
             const uint32_t limit = k > 0 ? min(static_cast<uint32_t>(k), n) : n;
+            u64 key[kKeys], won = 0;
+            d.sort(n, limit, key);
+            float w[kKeys], ahead[kKeys], listed = 0.0f, rest = 0.0f;
+            uint32_t tops = 0;
 #pragma unroll
-            for (int h = 0; h < kKeys; ++h) {
+            for (int h = 0; h < kKeys; ++h)
                 w[h] = d.tid + h * kThreads < limit ? d.list_weight(unordered(ord_of(key[h]))) : 0.0f;
-                float all = 0.0f;
-                ahead[h] = listed + d.block_scan(w[h], s.warpf, &all);
-                listed += all;
+            if (by_mass) {
+#pragma unroll
+                for (int h = 0; h < kKeys; ++h) {
+                    if (h > 0 && limit <= static_cast<uint32_t>(h * kThreads)) break;
+                    float all_h = 0.0f;
+                    ahead[h] = listed + d.block_scan(w[h], s.warpf, &all_h);
+                    listed += all_h;
+                }
             }
             const float bar = p * (whole ? total : listed);
 #pragma unroll
@@ -951,27 +1048,21 @@ sample_kernel(const T *__restrict__ logits, size_t stride, unsigned vocab, unsig
                 const bool keep = place < limit && (place == 0 || ((!by_mass || ahead[h] < bar) && w[h] >= m));
                 if (!keep) continue;
                 const int i = static_cast<int>(index_of(key[h]));
-                const float score = fmaxf(w[h] / q[i], 0.0f);
-                if (score > best.score || (score == best.score && i < best.at)) best.score = score, best.at = i;
+                best.offer(fmaxf(w[h] / q[i], 0.0f), i);
                 if (unordered(ord_of(key[h])) == d.top) ++tops;
                 else rest += w[h];
             }
-            const u64 won = d.block_most(best.key());
-            rest = d.block_sum(rest);
-            tops = __reduce_add_sync(kFullMask, tops);
-            if (d.lane == 0) s.warp_n[d.warp] = tops;
-            __syncthreads();
-            if (d.tid != 0) return;
-            tops = 0;
-            for (int v = 0; v < kWarps; ++v) tops += s.warp_n[v];
-            d.write(row, won, rest, tops, token, logprob);
+            won = best.key();
+            d.join(won, rest, tops);
+            if (d.tid == 0) d.write(won, rest, tops, token, logprob);
             return;
         }
-        if (k > 0) cut = d.template select<false>(0, static_cast<u64>(k));
+        if (k > 0) cut = d.template select<false>(0, [&](u64) { return static_cast<u64>(k); });
         if (by_mass) {
-            const double part = static_cast<double>(p) * static_cast<double>(d.mass_from(cut));
-            const u64 want = static_cast<u64>(ceil(part));
-            const u64 by = d.template select<true>(cut, want > 1 ? want : 1);
+            const u64 by = d.template select<true>(cut, [&](u64 mass) {
+                const u64 want = static_cast<u64>(ceil(static_cast<double>(p) * static_cast<double>(mass)));
+                return want > 1 ? want : 1ull;
+            });
             cut = by > cut ? by : cut;
         }
     }
@@ -980,7 +1071,10 @@ sample_kernel(const T *__restrict__ logits, size_t stride, unsigned vocab, unsig
     const int cut_i = cut == 0 ? 0x7fffffff : static_cast<int>(index_of(cut));
     float rest = 0.0f;
     uint32_t tops = 0;
-    d.each_above(cut_v, [&](float v, int i) {
+    // A value that min-p leaves in, with room for the rounding of its weight.
+    const float off = m > 0.0f ? t * logf(m) : -inf();
+    const float least = fmaxf(cut_v, d.top + 1.001f * off - 1e-5f * t - fabsf(d.top) * 4e-7f);
+    d.each_above(fmaxf(least, -FLT_MAX), [&](float v, int i) {
         if (!(v > cut_v || (v == cut_v && i <= cut_i))) return;
         const float w = d.weight(v);
         if (!(w >= m)) return;
@@ -988,7 +1082,7 @@ sample_kernel(const T *__restrict__ logits, size_t stride, unsigned vocab, unsig
         if (v == d.top) ++tops;
         else rest += w;
     });
-    d.finish(row, best, rest, tops, token, logprob);
+    d.finish(best, rest, tops, token, logprob);
 }
 
 template <class T>
@@ -996,21 +1090,22 @@ cudaError_t launch_typed(const void *logits, size_t rows, unsigned vocab, size_t
                          size_t noise_stride, const SampleAsk &ask, int32_t *tokens, float *logprobs, int num_sms,
                          cudaStream_t s)
 {
-    // Chunks of a row, and one more where it starts inside its first.
+    // Chunks of a row; one more where it starts inside its first.
     constexpr unsigned kEach = Chunk<T>::kEach;
     const unsigned chunks = (vocab + kEach - 1) / kEach;
-    // As few blocks per row as keep the slices at kSliceChunks, and more while
-    // all of them still fit on the GPU at once (four per SM) and have a chunk
-    // for every thread.
+    // One block per row, and more while all of them still fit on the GPU at
+    // once (four per SM) and have enough of the row each.
     unsigned blocks = 1;
-    while (blocks < kMaxCluster && blocks * kSliceChunks < chunks) blocks *= 2;
-    while (blocks < kMaxCluster && rows * blocks * 2 <= static_cast<size_t>(num_sms) * 4 && blocks * kThreads < chunks)
+    while (blocks < kMaxCluster && rows * blocks * 2 <= static_cast<size_t>(num_sms) * 4 &&
+           blocks * kLeastChunks < chunks)
         blocks *= 2;
     if (rows * blocks > 0x7fffffffull) return cudaErrorInvalidValue;
     const unsigned per = (chunks + 1 + blocks - 1) / blocks;
-    constexpr size_t kMostChunks = (static_cast<size_t>(1) << 18) / kEach;   // of the largest vocabulary
-    constexpr size_t kMostBytes = kSharedBytes + (kMostChunks / kMaxCluster + 1) * 16;
-    static_assert(kMostBytes <= 227 * 1024, "a slice of the largest vocabulary fits");
+    constexpr unsigned kEntryChunks = kGroup * kThreads;   // chunks to kThreads entries of the index
+    constexpr size_t kMostChunks = (static_cast<size_t>(1) << 18) / kEach + 1;   // of the largest vocabulary
+    constexpr size_t kMostBytes = kSharedBytes + (kMostChunks + kEntryChunks - 1) / kEntryChunks * kThreads * 4;
+    static_assert(kMostBytes <= 227 * 1024, "the index of the largest vocabulary fits");
+    static_assert((kMostChunks + kEntryChunks - 1) / kEntryChunks * 32 <= 65536, "a warp's entries have 16-bit names");
 
     const auto kernel = sample_kernel<T>;
     static std::atomic<unsigned long long> attribute_set{0};   // one bit per device
@@ -1026,7 +1121,7 @@ cudaError_t launch_typed(const void *logits, size_t rows, unsigned vocab, size_t
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(rows) * blocks);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSharedBytes + static_cast<size_t>(per) * 16;
+    cfg.dynamicSmemBytes = kSharedBytes + static_cast<size_t>((per + kEntryChunks - 1) / kEntryChunks) * kThreads * 4;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
