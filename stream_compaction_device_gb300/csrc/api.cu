@@ -297,10 +297,15 @@ devscan_status sample_common(LogitType type, const void *logits, size_t rows, si
                          {ask.top_k, each},  {ask.top_p, each}, {ask.min_p, each}};
     if (written_overlap(written, read)) return DEVSCAN_ERR_INVALID;
     Workspace ws;
-    const devscan_status st = acquire(stream, 1, &ws);
+    devscan_status st = acquire(stream, 1, &ws);
     if (st != DEVSCAN_OK) return st;
-    return from_cuda(launch_sample(type, logits, rows, vocab, stride, noise, noise_stride, ask, tokens, logprobs, ws,
-                                   stream));
+    void *row_words = nullptr;
+    if (noise != nullptr && (ask.top_k != nullptr || ask.top_p != nullptr)) {
+        st = acquire_extra(stream, rows * sizeof(uint32_t), &row_words);
+        if (st != DEVSCAN_OK) return st;
+    }
+    return from_cuda(launch_sample(type, logits, rows, vocab, stride, noise, noise_stride, ask, tokens, logprobs,
+                                   static_cast<uint32_t *>(row_words), ws, stream));
 }
 
 }  // namespace

@@ -174,6 +174,8 @@ cudaError_t launch_block_table_release(const int32_t *table, size_t stride, int 
                                        const Workspace &ws, cudaStream_t s);
 
 // Token draw.  Per-row settings in device memory, each null for "off".
+// row_words: a word per row of per-stream scratch, for the rows that a second
+// launch draws; null where no row can need it (neither top-k nor top-p).
 enum class LogitType { F32, F16, BF16 };
 struct SampleAsk {
     const float *temperature;
@@ -182,6 +184,6 @@ struct SampleAsk {
 };
 cudaError_t launch_sample(LogitType type, const void *logits, size_t rows, size_t vocab, size_t stride,
                           const float *noise, size_t noise_stride, const SampleAsk &ask, int32_t *tokens,
-                          float *logprobs, const Workspace &ws, cudaStream_t s);
+                          float *logprobs, uint32_t *row_words, const Workspace &ws, cudaStream_t s);
 
 }  // namespace devscan

@@ -106,17 +106,14 @@ __device__ __forceinline__ void put(u64 *p, unsigned rank, u64 v)
 {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(remote(p, rank)), "l"(v) : "memory");
 }
-__device__ __forceinline__ uint32_t get(const uint32_t *p, unsigned rank)
+__device__ __forceinline__ uint4 get(const uint32_t *p, unsigned rank)   // four words, 16-byte aligned
 {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote(p, rank)) : "memory");
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(remote(p, rank))
+                 : "memory");
     return v;
-}
-__device__ __forceinline__ uint32_t fetch_add(uint32_t *p, unsigned rank, uint32_t v)
-{
-    uint32_t old;
-    asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(remote(p, rank)), "r"(v) : "memory");
-    return old;
 }
 
 // ---------------------------------------------------------------------------
@@ -196,13 +193,6 @@ template <> struct Chunk<__nv_bfloat16> {
 
 struct Shared {
     u64 list[kList];                 // this block's collected tokens; a buffer of the sort
-    union {
-        u64 merged[kList];           // the cluster's, in block 0
-        struct {
-            uint32_t count[kBins];   // histogram: counts, or the low words of the masses
-            uint32_t carry[kBins];   // the masses' high words
-        };
-    };
     uint4 edge[2];                   // the slice's chunks over the row's ends
     uint16_t queue[kWarps][kQueue];
     u64 warp64[kWarps];
@@ -217,13 +207,14 @@ struct Shared {
     float rest[kMaxCluster];
     uint32_t tops[kMaxCluster];
     u64 cut;
-    uint32_t merged_n[2];            // in block 0: places of its merged list that are given out
     // Results of one block's scans.
     u64 pick_before;
     uint32_t pick_bin, pick_lo, pick_hi;
     uint32_t listed;                 // tokens collected by this block (counting stops above kList)
-    uint32_t local_base;
 };
+// Keys that block 0's inbox has room for: a wide cluster's blocks do not all
+// bring the same number.
+__host__ __device__ constexpr unsigned inbox_keys(unsigned blocks) { return blocks == 1 ? kList : 2 * kList; }
 constexpr size_t kSharedBytes = (sizeof(Shared) + 127) / 128 * 128;
 
 template <class T>
@@ -232,7 +223,12 @@ struct Draw {
     static constexpr int kEach = C::kEach;
 
     Shared &s;
+    u64 *inbox;                      // in block 0: the cluster's tokens, a region of `region` per block
+    uint32_t *count, *carry;         // a histogram in the same memory: counts, or the masses' low words;
+                                     // the masses' high words
+    uint32_t region;
     float *index;                    // maxima of this block's groups of chunks
+    const float *noise;              // of the row
     const T *row;
     const uint4 *source;             // the slice
     unsigned tid, lane, warp, rank, blocks;
@@ -244,6 +240,20 @@ struct Draw {
     int turn = 0;                    // which half of the double buffers is next
 
     __device__ __forceinline__ Draw(Shared &shared) : s(shared) {}
+
+    // The race among the kept tokens that this thread has seen.
+    struct Best {
+        float score = -1.0f;
+        int at = 0x7fffffff;
+        __device__ __forceinline__ void offer(float sc, int i)
+        {
+            if (sc > score || (sc == score && i < at)) score = sc, at = i;
+        }
+        __device__ __forceinline__ u64 key() const
+        {
+            return score < 0.0f ? 0ull : (static_cast<u64>(__float_as_uint(score)) << 32) | ~static_cast<unsigned>(at);
+        }
+    };
 
     // All threads of the cluster.
     __device__ __forceinline__ void meet() const
@@ -347,18 +357,18 @@ struct Draw {
         return most;
     }
 
-    // f(value, index) for every value of at least `low` and those beside it in
-    // its chunk.  A warp queues the index entries that reach `low` and reads
-    // 32 groups at a time, one per lane.
+    // f(chunks, c) for every group with a value of at least `low`: its four
+    // chunks, c + u * kThreads of the slice.  A warp queues the index entries
+    // that reach `low` and reads 32 groups at a time, one per lane.
     template <class F>
-    __device__ __forceinline__ void each_above(float low, F f)
+    __device__ __forceinline__ void each_group(float low, F f)
     {
         uint16_t *queue = s.queue[warp];
         unsigned waiting = 0;
         const unsigned entries = (mine + kGroup * kThreads - 1) / (kGroup * kThreads);
         for (unsigned k = 0; k <= entries; ++k) {
             if (k < entries) {
-                // A thread's first group is there if its first chunk is.
+                // A thread's group is there if its first chunk is.
                 const bool in = tid + k * kGroup * kThreads < mine && index[k * kThreads + tid] >= low;
                 const unsigned some = __ballot_sync(kFullMask, in);
                 if (in) queue[waiting + __popc(some & ((1u << lane) - 1))] = static_cast<uint16_t>(k * 32 + lane);
@@ -375,22 +385,95 @@ struct Draw {
             if (lane + 32 < waiting) queue[lane] = static_cast<uint16_t>(moved);
             waiting -= taken;
             if (lane < taken) {
-                const unsigned c0 = (at / 32) * kGroup * kThreads + warp * 32 + at % 32;
+                const unsigned c = (at / 32) * kGroup * kThreads + warp * 32 + at % 32;
                 uint4 v[kGroup];
 #pragma unroll
-                for (int u = 0; u < kGroup; ++u) v[u] = chunk(c0 + u * kThreads);
-#pragma unroll
-                for (int u = 0; u < kGroup; ++u) {
-                    uint32_t q[4];
-                    unpack(v[u], q);
-                    if (infinite) only_infinite(q);
-                    if (!(C::most(q, -inf()) >= low)) continue;
-                    const int i = first + static_cast<int>(c0 + u * kThreads) * kEach;
-#pragma unroll
-                    for (int e = 0; e < kEach; ++e) f(C::value(q, e), i + e);
-                }
+                for (int u = 0; u < kGroup; ++u) v[u] = chunk(c + u * kThreads);
+                f(v, c);
             }
             __syncwarp();
+        }
+    }
+
+    // f(values, i) for every chunk with a value of at least `low`: its kEach
+    // values, of which the first is the row's i-th.
+    template <class F>
+    __device__ __forceinline__ void each_chunk(float low, F f)
+    {
+        each_group(low, [&](const uint4 (&v)[kGroup], unsigned c) {
+#pragma unroll
+            for (int u = 0; u < kGroup; ++u) {
+                float x[kEach];
+                if (values(v[u], x) >= low) f(x, first + static_cast<int>(c + u * kThreads) * kEach);
+            }
+        });
+    }
+    // f(value, index) for every value of those chunks.
+    template <class F>
+    __device__ __forceinline__ void each_above(float low, F f)
+    {
+        each_chunk(low, [&](const float (&x)[kEach], int i) {
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) f(x[e], i + e);
+        });
+    }
+    // A chunk's values; returns the largest.
+    __device__ __forceinline__ float values(const uint4 &v, float (&x)[kEach]) const
+    {
+        uint32_t q[4];
+        unpack(v, q);
+        if (infinite) only_infinite(q);
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) x[e] = C::value(q, e);
+        return C::most(q, -inf());
+    }
+
+    // The race of the kept tokens of two chunks at a time, so that their noise
+    // is in flight together.  keep(value, index).
+    template <class Keep>
+    __device__ __forceinline__ void race_group(const uint4 (&v)[kGroup], unsigned c, float m, Keep keep, Best &best,
+                                               float &rest, uint32_t &tops) const
+    {
+        const bool aligned = reinterpret_cast<uintptr_t>(noise + first) % 16 == 0;
+#pragma unroll
+        for (int u0 = 0; u0 < kGroup; u0 += 2) {
+            float w[2][kEach], n[2][kEach];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const unsigned at = c + (u0 + p) * kThreads;
+                const int i = first + static_cast<int>(at) * kEach;
+                float x[kEach];
+                values(v[u0 + p], x);
+                bool some = false;
+#pragma unroll
+                for (int e = 0; e < kEach; ++e) {
+                    const float weighs = weight(x[e]);
+                    w[p][e] = keep(x[e], i + e) && weighs >= m ? weighs : -1.0f;
+                    n[p][e] = 1.0f;
+                    some |= w[p][e] >= 0.0f;
+                }
+                if (some && aligned && at >= lo && at < hi) {
+#pragma unroll
+                    for (int e = 0; e < kEach; e += 4) {
+                        const float4 q = __ldcs(reinterpret_cast<const float4 *>(noise + i + e));
+                        n[p][e] = q.x, n[p][e + 1] = q.y, n[p][e + 2] = q.z, n[p][e + 3] = q.w;
+                    }
+                } else if (some) {
+#pragma unroll
+                    for (int e = 0; e < kEach; ++e) n[p][e] = w[p][e] >= 0.0f ? __ldcs(noise + i + e) : 1.0f;
+                }
+            }
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const int i = first + static_cast<int>(c + (u0 + p) * kThreads) * kEach;
+#pragma unroll
+                for (int e = 0; e < kEach; ++e) {
+                    if (w[p][e] < 0.0f) continue;
+                    best.offer(fmaxf(__fdividef(w[p][e], n[p][e]), 0.0f), i + e);
+                    if (w[p][e] == 1.0f) ++tops;
+                    else rest += w[p][e];
+                }
+            }
         }
     }
 
@@ -433,21 +516,21 @@ struct Draw {
             if (score > o.score) o.score = score, o.at = i + e;
         }
     }
-    __device__ void race_edge(Online &o, const float *q, int i0) const
+    __device__ void race_edge(Online &o, int i0) const
     {
         for (int i = i0 < 0 ? 0 : i0; i < i0 + kEach && i < static_cast<int>(vocab); ++i) {
-            const float v[1] = {static_cast<float>(row[i])}, noise[1] = {q[i]};
+            const float v[1] = {static_cast<float>(row[i])}, n[1] = {noise[i]};
             if (!(v[0] > -inf())) continue;
             if (v[0] > o.most) rescale(o, v[0]);
-            race(o, v, noise, i);
+            race(o, v, n, i);
         }
     }
-    __device__ Online race_all(const float *q)
+    __device__ Online race_all()
     {
         constexpr int kRaceLoads = kEach == 4 ? 4 : 2;   // chunks in flight, beside their noise
         Online o;
-        const float *beside = q + first;
-        if (lo == 1 && tid == 0) race_edge(o, q, first);
+        const float *beside = noise + first;
+        if (lo == 1 && tid == 0) race_edge(o, first);
         const bool aligned = reinterpret_cast<uintptr_t>(beside) % 16 == 0;
         for (unsigned c0 = tid; c0 < hi; c0 += kRaceLoads * kThreads) {
             uint4 x[kRaceLoads];
@@ -472,18 +555,18 @@ struct Draw {
                 const float most = C::most(bits, -inf());
                 if (most == -inf()) continue;
                 if (most > o.most) rescale(o, most);
-                float v[kEach], noise[kEach];
+                float v[kEach], q[kEach];
 #pragma unroll
                 for (int e = 0; e < kEach; ++e) {
                     v[e] = C::value(bits, e);
                     const float4 &f = n[u][e / 4];
-                    noise[e] = e % 4 == 0 ? f.x : e % 4 == 1 ? f.y : e % 4 == 2 ? f.z : f.w;
+                    q[e] = e % 4 == 0 ? f.x : e % 4 == 1 ? f.y : e % 4 == 2 ? f.z : f.w;
                 }
-                race(o, v, noise, first + static_cast<int>(c0 + u * kThreads) * kEach);
+                race(o, v, q, first + static_cast<int>(c0 + u * kThreads) * kEach);
             }
         }
         if (hi < mine && mine > lo && tid == (mine - 1) % kThreads)
-            race_edge(o, q, first + static_cast<int>(mine - 1) * kEach);
+            race_edge(o, first + static_cast<int>(mine - 1) * kEach);
         return o;
     }
 
@@ -534,40 +617,46 @@ struct Draw {
         return ahead + (lane == 0 ? V(0) : before);
     }
 
-    // Collects the tokens for which in(v, i) holds (none below `low`) into
-    // block 0's merged list, in any order, if there are at most kList of them.
-    // Returns their number, or more than kList (the same in every block).
-    // sum(): a partial sum of each thread, asked for after the pass, summed
-    // into s.sum[turn] of every block by rank.
-    template <class In, class Sum>
-    __device__ uint32_t collect(float low, In in, Sum sum)
+    // Tokens for the list: begin_list(), then add_token() by any thread, then
+    // merge_lists(), which returns their number over the cluster (the same in
+    // every block).  Up to kList they are then in block 0, in any order; more
+    // than kList is returned as well if a block has more than its region.
+    // sum: a partial sum of each thread, summed into s.sum[which] of every
+    // block by rank, with `which` as `turn` was before.
+    __device__ __forceinline__ void begin_list()
+    {
+        if (tid == 0) s.listed = 0;
+        __syncthreads();
+    }
+    __device__ __forceinline__ void add_token(float v, int i)
+    {
+        if (*const_cast<volatile uint32_t *>(&s.listed) > region) return;
+        const uint32_t k = atomicAdd(&s.listed, 1u);
+        if (k < region) (rank == 0 ? inbox : s.list)[k] = key_of(ordered(v), static_cast<unsigned>(i));
+    }
+    __device__ uint32_t merge_lists(float sum)
     {
         const int now = turn;
         turn ^= 1;
-        if (tid == 0) s.listed = 0;
-        __syncthreads();
-        each_above(low, [&](float v, int i) {
-            if (!in(v, i) || *const_cast<volatile uint32_t *>(&s.listed) > kList) return;
-            const uint32_t k = atomicAdd(&s.listed, 1u);
-            if (k < kList) s.list[k] = key_of(ordered(v), static_cast<unsigned>(i));
-        });
-        const float total = block_sum(sum());
+        const float total = block_sum(sum);
         const uint32_t n = s.listed;
-        if (tid == 0) {
-            s.merged_n[now ^ 1] = 0;
-            s.local_base = n == 0 || n > kList ? kList + 1 : fetch_add(&s.merged_n[now], 0, n);
-        }
         if (tid < blocks) {
-            put(&s.found[now][rank], tid, n);
+            put(&s.found[now][rank], tid, n <= region ? n : kList + 1);
             put(&s.sum[now][rank], tid, total);
         }
-        __syncthreads();
-        const uint32_t base = s.local_base;
-        if (n <= kList && base + n <= kList)
-            for (uint32_t k = tid; k < n; k += kThreads) put(&s.merged[base + k], 0, s.list[k]);
+        if (rank != 0 && n <= region)
+            for (uint32_t k = tid; k < n; k += kThreads) put(&inbox[rank * region + k], 0, s.list[k]);
         meet();
         uint32_t all = 0;
-        for (unsigned b = 0; b < blocks; ++b) all += min(s.found[now][b], static_cast<uint32_t>(kList + 1));
+        for (unsigned b = 0; b < blocks; ++b) all += s.found[now][b];
+        if (rank == 0 && blocks > 1 && all <= kList) {   // close the gaps
+            uint32_t at = 0;
+            for (unsigned b = 0; b < blocks; ++b) {
+                for (uint32_t k = tid; k < s.found[now][b]; k += kThreads) s.list[at + k] = inbox[b * region + k];
+                at += s.found[now][b];
+            }
+            __syncthreads();
+        }
         return all;
     }
 
@@ -578,15 +667,16 @@ struct Draw {
         return v;
     }
 
-    // Puts the first `limit` of merged[0 .. n), n <= kList, in descending
-    // order, by this block.  Thread t gets the keys at t + h * kThreads; 0 past
+    // Puts the first `limit` of the n <= kList merged tokens in descending
+    // order, by block 0.  Thread t gets the keys at t + h * kThreads; 0 past
     // the end.  Up to kRanked keys, each key's place is the number of larger
     // ones, counted in one loop without a barrier; above, a bitonic sort takes
     // fewer steps.
     __device__ void sort(uint32_t n, uint32_t limit, u64 (&a)[kKeys])
     {
+        u64 *from = blocks == 1 ? inbox : s.list, *to = blocks == 1 ? s.list : inbox;
         if (n > kRanked) {
-            bitonic(n, a);
+            bitonic(n, a, from, to);
             return;
         }
         constexpr int kHeld = kRanked / kThreads;
@@ -594,38 +684,38 @@ struct Draw {
         uint32_t place[kHeld];
 #pragma unroll
         for (int h = 0; h < kHeld; ++h) {
-            key[h] = tid + h * kThreads < n ? s.merged[tid + h * kThreads] : 0;
+            key[h] = tid + h * kThreads < n ? from[tid + h * kThreads] : 0;
             place[h] = 0;
         }
         const bool two = n > kThreads;
         if (!two) {
             if (warp * 32 < n)
 #pragma unroll 8
-                for (uint32_t k = 0; k < n; ++k) place[0] += s.merged[k] > key[0] ? 1u : 0u;
+                for (uint32_t k = 0; k < n; ++k) place[0] += from[k] > key[0] ? 1u : 0u;
         } else {
 #pragma unroll 4
             for (uint32_t k = 0; k < n; ++k) {
-                const u64 other = s.merged[k];
+                const u64 other = from[k];
 #pragma unroll
                 for (int h = 0; h < kHeld; ++h) place[h] += other > key[h] ? 1u : 0u;
             }
         }
 #pragma unroll
         for (int h = 0; h < kHeld; ++h)
-            if (key[h] != 0) s.list[place[h]] = key[h];
+            if (key[h] != 0) to[place[h]] = key[h];
         __syncthreads();
 #pragma unroll
-        for (int h = 0; h < kKeys; ++h) a[h] = tid + h * kThreads < min(n, limit) ? s.list[tid + h * kThreads] : 0;
+        for (int h = 0; h < kKeys; ++h) a[h] = tid + h * kThreads < min(n, limit) ? to[tid + h * kThreads] : 0;
     }
 
-    // Bitonic sort of merged[0 .. n): strides inside a warp by shuffles, up to
+    // Bitonic sort of from[0 .. n): strides inside a warp by shuffles, up to
     // the block through shared memory, above inside a thread.
-    __device__ void bitonic(uint32_t n, u64 (&a)[kKeys])
+    __device__ void bitonic(uint32_t n, u64 (&a)[kKeys], u64 *from, u64 *to)
     {
         unsigned size2 = 32;
         while (size2 < n) size2 *= 2;
 #pragma unroll
-        for (int h = 0; h < kKeys; ++h) a[h] = tid + h * kThreads < n ? s.merged[tid + h * kThreads] : 0;
+        for (int h = 0; h < kKeys; ++h) a[h] = tid + h * kThreads < n ? from[tid + h * kThreads] : 0;
         const bool active = tid < size2;
         int half = 0;
         for (unsigned size = 2; size <= size2; size *= 2) {
@@ -648,7 +738,7 @@ struct Draw {
                     continue;
                 }
                 const bool low = (tid & stride) == 0;
-                u64 *buf = half ? s.merged : s.list;
+                u64 *buf = half ? from : to;
                 if (stride >= 32) {
                     half ^= 1;   // this half was last read two exchanges back, before the last barrier
 #pragma unroll
@@ -667,20 +757,6 @@ struct Draw {
             }
         }
     }
-
-    // The race among the kept tokens that this thread has seen.
-    struct Best {
-        float score = -1.0f;
-        int at = 0x7fffffff;
-        __device__ __forceinline__ void offer(float sc, int i)
-        {
-            if (sc > score || (sc == score && i < at)) score = sc, at = i;
-        }
-        __device__ __forceinline__ u64 key() const
-        {
-            return score < 0.0f ? 0ull : (static_cast<u64>(__float_as_uint(score)) << 32) | ~static_cast<unsigned>(at);
-        }
-    };
 
     __device__ __forceinline__ void write(u64 won, float rest, uint32_t tops, int32_t *token, float *logprob)
     {
@@ -757,31 +833,39 @@ struct Draw {
     template <bool MASS, class Bin, class Want>
     __device__ bool histogram(float low, Bin bin_in, Want wanted, u64 &want, uint32_t &bin)
     {
-        for (unsigned b = tid; b < kBins; b += kThreads) s.count[b] = s.carry[b] = 0;
+        for (unsigned b = tid; b < kBins; b += kThreads) count[b] = carry[b] = 0;
         __syncthreads();
-        each_above(low, [&](float v, int i) {
-            const int b = bin_in(v, i);
-            if (b < 0) return;
+        each_chunk(low, [&](const float (&x)[kEach], int i) {
+            // All of a chunk's atomics are in flight before the first carry is
+            // looked at.
+            int b[kEach];
+            uint32_t holds[kEach], old[kEach];
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+                b[e] = bin_in(x[e], i + e);
+                holds[e] = b[e] < 0 ? 0 : MASS ? mass(x[e]) : 1;
+            }
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) old[e] = holds[e] != 0 ? atomicAdd(&count[b[e]], holds[e]) : 0;
             if (MASS) {
-                const uint32_t m = mass(v);
-                if (m == 0) return;
-                const uint32_t old = atomicAdd(&s.count[b], m);
-                if (old + m < old) atomicAdd(&s.carry[b], 1u);
-            } else {
-                atomicAdd(&s.count[b], 1u);
+#pragma unroll
+                for (int e = 0; e < kEach; ++e)
+                    if (old[e] + holds[e] < old[e]) atomicAdd(&carry[b[e]], 1u);
             }
         });
         meet();
-        // Thread t sums the bins from kPer * t on, of all blocks.
+        // Thread t sums the four bins from 4 t on, of all blocks.
         constexpr int kPer = kBins / kThreads;
-        u64 h[kPer], own = 0;
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) h[k] = 0;
+        static_assert(kPer == 4, "a thread's bins are one 16-byte read");
+        u64 h[kPer] = {0, 0, 0, 0}, own = 0;
+#pragma unroll 4
         for (unsigned r = 0; r < blocks; ++r) {
-#pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-                h[k] += get(&s.count[kPer * tid + k], r);
-                if (MASS) h[k] += static_cast<u64>(get(&s.carry[kPer * tid + k], r)) << 32;
+            const uint4 low4 = get(count + kPer * tid, r);
+            h[0] += low4.x, h[1] += low4.y, h[2] += low4.z, h[3] += low4.w;
+            if (MASS) {
+                const uint4 high4 = get(carry + kPer * tid, r);
+                h[0] += static_cast<u64>(high4.x) << 32, h[1] += static_cast<u64>(high4.y) << 32;
+                h[2] += static_cast<u64>(high4.z) << 32, h[3] += static_cast<u64>(high4.w) << 32;
             }
         }
 #pragma unroll
@@ -816,64 +900,91 @@ struct Draw {
         return lo;
     }
 
-    // The key of the last token, in the order, of the shortest prefix that
-    // holds wanted(total) (tokens, or mass); 0 if all of them do not.  Only
-    // tokens with keys >= floor take part.
+    // A cut of the order: the key of the last token of the shortest prefix
+    // that holds wanted(total), in tokens or mass.  Only tokens with keys >=
+    // floor take part.
+    struct Floor {
+        float v;
+        int i;
+        __device__ __forceinline__ explicit Floor(u64 key)
+            : v(key == 0 ? -FLT_MAX : unordered(ord_of(key))), i(key == 0 ? 0x7fffffff : static_cast<int>(index_of(key)))
+        {
+        }
+        __device__ __forceinline__ bool takes(float x, int at) const { return x > v || (x == v && at <= i); }
+    };
+
+    // The bin of the first histogram where the cut lies, and what is wanted
+    // inside it; false if all that take part hold less than wanted.
     template <bool MASS, class Want>
-    __device__ u64 select(u64 floor, Want wanted)
+    __device__ bool bracket(const Floor &floor, Want wanted, u64 &want, uint32_t &bin)
     {
-        u64 want = 0;
-        const auto same = [&](u64) { return want; };
-        const float floor_v = floor == 0 ? -FLT_MAX : unordered(ord_of(floor));
-        const int floor_i = floor == 0 ? 0x7fffffff : static_cast<int>(index_of(floor));
-        const auto takes_part = [&](float v, int i) { return v > floor_v || (v == floor_v && i <= floor_i); };
-        uint32_t bin = 0;
         // Below top - 23 T a weight rounds to no mass.
-        const float least = MASS ? fmaxf(floor_v, top - 23.0f * t) : floor_v;
-        if (!histogram<MASS>(least, [&](float v, int i) { return takes_part(v, i) ? bin_of(v) : -1; }, wanted, want, bin))
-            return 0;
+        const float least = MASS ? fmaxf(floor.v, top - 23.0f * t) : floor.v;
+        return histogram<MASS>(least, [&](float v, int i) { return floor.takes(v, i) ? bin_of(v) : -1; }, wanted, want,
+                               bin);
+    }
+
+    // Block 0 puts the n merged tokens in order, of which the first that hold
+    // `want` are kept.  Thread t gets the keys at t + h * kThreads that are
+    // kept, 0 for others; s.pick_before is the last one.
+    template <bool MASS>
+    __device__ void resolve(uint32_t n, u64 want, u64 (&key)[kKeys])
+    {
+        u64 base = 0;
+        sort(n, n, key);
+#pragma unroll
+        for (int h = 0; h < kKeys; ++h) {
+            u64 holds = 0, total = 0;
+            if (tid + h * kThreads < n) holds = MASS ? mass(unordered(ord_of(key[h]))) : 1;
+            const u64 ahead = base + block_scan(holds, s.warp64, &total);
+            if (ahead < want && want <= ahead + holds) s.pick_before = key[h];
+            if (ahead >= want) key[h] = 0;
+            base += total;
+        }
+        __syncthreads();
+    }
+
+    // The cut's key, from the bin of the first histogram where it lies.
+    template <bool MASS>
+    __device__ u64 refine(const Floor &floor, uint32_t bin, u64 want)
+    {
         if (tid == 0) s.pick_lo = edge(static_cast<int>(bin));
         if (tid == 32) s.pick_hi = bin == 0 ? ordered(top) : edge(static_cast<int>(bin) - 1) - 1;
         __syncthreads();
-        uint32_t lo = s.pick_lo, hi = s.pick_hi;        // the cut's ordered bits
-        uint32_t i_lo = 0, i_hi = vocab - 1;            // and, once lo == hi, its index
+        uint32_t lo_bits = s.pick_lo, hi_bits = s.pick_hi;   // the cut's ordered bits
+        uint32_t i_lo = 0, i_hi = vocab - 1;                 // and, once these are equal, its index
+        const auto same = [&](u64) { return want; };
         for (;;) {
-            const float v_lo = unordered(lo), v_hi = unordered(hi);
-            const bool tie = lo == hi;
+            const float v_lo = unordered(lo_bits), v_hi = unordered(hi_bits);
+            const bool tie = lo_bits == hi_bits;
             const auto inside = [&](float v, int i) {
-                return v >= v_lo && v <= v_hi && takes_part(v, i) &&
+                return v >= v_lo && v <= v_hi && floor.takes(v, i) &&
                        (!tie || (static_cast<unsigned>(i) >= i_lo && static_cast<unsigned>(i) <= i_hi));
             };
-            const uint32_t n = collect(v_lo, inside, [] { return 0.0f; });
+            begin_list();
+            each_above(v_lo, [&](float v, int i) {
+                if (inside(v, i)) add_token(v, i);
+            });
+            const uint32_t n = merge_lists(0.0f);
             if (n <= kList) {
                 if (rank == 0) {
-                    u64 key[kKeys], base = 0;
-                    sort(n, n, key);
-#pragma unroll
-                    for (int h = 0; h < kKeys; ++h) {
-                        u64 holds = 0, total = 0;
-                        if (tid + h * kThreads < n) holds = MASS ? mass(unordered(ord_of(key[h]))) : 1;
-                        const u64 ahead = base + block_scan(holds, s.warp64, &total);
-                        if (ahead < want && want <= ahead + holds) s.pick_before = key[h];
-                        base += total;
-                    }
-                    __syncthreads();
+                    u64 key[kKeys];
+                    resolve<MASS>(n, want, key);
                     if (tid < blocks) put(&s.cut, tid, s.pick_before);
                 }
                 meet();
                 return s.cut;
             }
+            unsigned shift = 0;
             if (!tie) {
-                unsigned shift = 0;
-                while ((hi - lo) >> shift >= kBins) ++shift;
+                while ((hi_bits - lo_bits) >> shift >= kBins) ++shift;
                 histogram<MASS>(v_lo, [&](float v, int i) {
-                    return inside(v, i) ? static_cast<int>((hi - ordered(v)) >> shift) : -1;
+                    return inside(v, i) ? static_cast<int>((hi_bits - ordered(v)) >> shift) : -1;
                 }, same, want, bin);
-                const uint32_t new_hi = hi - (bin << shift), width = (1u << shift) - 1;
-                lo = new_hi - lo > width ? new_hi - width : lo;
-                hi = new_hi;
+                const uint32_t new_hi = hi_bits - (bin << shift), width = (1u << shift) - 1;
+                lo_bits = new_hi - lo_bits > width ? new_hi - width : lo_bits;
+                hi_bits = new_hi;
             } else {
-                unsigned shift = 0;
                 while ((i_hi - i_lo) >> shift >= kBins) ++shift;
                 histogram<MASS>(v_lo, [&](float v, int i) {
                     return inside(v, i) ? static_cast<int>((static_cast<unsigned>(i) - i_lo) >> shift) : -1;
@@ -884,25 +995,78 @@ struct Draw {
         }
     }
 
+    // The last cut and the race in one pass: tokens in the bins before the
+    // cut's race at once, those of its bin are listed, and block 0 races the
+    // kept ones.  Returns false, with `cut` alone, if they do not fit the list
+    // or there is nothing to cut off.
+    template <bool MASS, class Want>
+    __device__ bool cut_and_race(u64 floor_key, Want wanted, float m, u64 &cut, Best &best, float &rest, uint32_t &tops)
+    {
+        const Floor floor(floor_key);
+        u64 want = 0;
+        uint32_t bin = 0;
+        cut = floor_key;
+        if (!bracket<MASS>(floor, wanted, want, bin)) return false;
+        // No value of the bin is below this.
+        const float low = bin + 1 < kBins ? top - (static_cast<float>(bin + 1) / kBinsPerUnit) * 1.0001f - fabsf(top) * 4e-7f
+                                          : floor.v;
+        begin_list();
+        each_group(fmaxf(low, floor.v), [&](const uint4 (&v)[kGroup], unsigned c) {
+            race_group(v, c, m, [&](float x, int) { return x >= floor.v && bin_of(x) < static_cast<int>(bin); }, best, rest, tops);
+#pragma unroll
+            for (int u = 0; u < kGroup; ++u) {
+                float x[kEach];
+                values(v[u], x);
+                const int i = first + static_cast<int>(c + u * kThreads) * kEach;
+#pragma unroll
+                for (int e = 0; e < kEach; ++e)
+                    if (floor.takes(x[e], i + e) && bin_of(x[e]) == static_cast<int>(bin)) add_token(x[e], i + e);
+            }
+        });
+        const uint32_t n = merge_lists(0.0f);
+        if (n > kList) {
+            best = Best();
+            rest = 0.0f, tops = 0;
+            cut = refine<MASS>(floor, bin, want);
+            return false;
+        }
+        if (rank == 0) {
+            u64 key[kKeys];
+            resolve<MASS>(n, want, key);
+#pragma unroll
+            for (int h = 0; h < kKeys; ++h) {
+                if (key[h] == 0) continue;
+                const float w = weight(unordered(ord_of(key[h])));
+                if (!(w >= m)) continue;
+                const int i = static_cast<int>(index_of(key[h]));
+                best.offer(fmaxf(__fdividef(w, noise[i]), 0.0f), i);
+                if (w == 1.0f) ++tops;
+                else rest += w;
+            }
+        }
+        return true;
+    }
 };
 
+// Rows whose cut needs histograms, left by the first launch to the second.
+struct Deferred {
+    uint32_t *rows;
+    unsigned *count, *left;          // rows put down; blocks of the second launch that are through
+};
+
+// One row by one cluster.  With `defer` a row that needs histograms is put
+// down instead.
 template <class T>
-__global__ void __launch_bounds__(kThreads, 4)
-sample_kernel(const T *__restrict__ logits, size_t stride, unsigned vocab, unsigned per,
-              const float *__restrict__ noise, size_t noise_stride, SampleAsk ask, int32_t *__restrict__ tokens,
-              float *__restrict__ logprobs)
+__device__ __forceinline__ void draw_row(Draw<T> &d, unsigned r, const T *logits, size_t stride, unsigned per,
+                                         const float *noise, size_t noise_stride, const SampleAsk &ask,
+                                         int32_t *tokens, float *logprobs, const Deferred &later, bool defer)
 {
-    extern __shared__ __align__(16) unsigned char s_bytes[];
-    Shared &s = *reinterpret_cast<Shared *>(s_bytes);
     using D = Draw<T>;
-    D d(s);
-    d.index = reinterpret_cast<float *>(s_bytes + kSharedBytes);
-    d.tid = threadIdx.x, d.lane = d.tid & 31, d.warp = d.tid >> 5;
-    d.rank = cluster_rank(), d.blocks = cluster_blocks(), d.vocab = vocab;
-    const unsigned r = blockIdx.x / d.blocks;
+    Shared &s = d.s;
+    const unsigned vocab = d.vocab;
     d.row = logits + static_cast<size_t>(r) * stride;
-    if (d.tid == 0) s.merged_n[0] = s.merged_n[1] = 0;
-    if (d.blocks > 1) cluster_arrive();   // the blocks' shared memory is there from the matching wait on
+    d.noise = noise + static_cast<size_t>(r) * noise_stride;
+    d.infinite = false;
     d.place(per);
 
     const float t = ask.temperature != nullptr ? ask.temperature[r] : 1.0f;
@@ -918,13 +1082,12 @@ sample_kernel(const T *__restrict__ logits, size_t stride, unsigned vocab, unsig
 
     d.t = t;
     d.scale = fminf(1.4426950408889634f / t, FLT_MAX);
-    const float *q = noise + static_cast<size_t>(r) * noise_stride;
     const bool plain = !greedy && k == 0 && !by_mass && !(m > 0.0f);
     typename D::Online online;
     const bool whole = !greedy && k == 0 && by_mass;   // top-p over the whole row
     float most, sum = 0.0f;
     if (plain) {
-        online = d.race_all(q);
+        online = d.race_all();
         most = online.most;
     } else if (whole) {
         most = d.template load<true>(&sum);
@@ -954,7 +1117,6 @@ sample_kernel(const T *__restrict__ logits, size_t stride, unsigned vocab, unsig
     }
     if (d.lane == 0) s.warp_max[d.warp] = warp_top, s.warp_bound[d.warp] = bound;
     __syncthreads();
-    if (d.blocks > 1) cluster_wait();
     if (d.warp == 0) {
         const uint32_t a = __reduce_max_sync(kFullMask, s.warp_max[d.lane & (kWarps - 1)]);
         const uint32_t b = __reduce_min_sync(kFullMask, s.warp_bound[d.lane & (kWarps - 1)]);
@@ -1011,11 +1173,13 @@ sample_kernel(const T *__restrict__ logits, size_t stride, unsigned vocab, unsig
             if (d.tid < d.blocks) put(&s.sum_all[d.rank], d.tid, all);
         }
         const int now = d.turn;
-        const uint32_t n = d.collect(low, [&](float v, int) {
-            if (!(v >= low)) return false;
+        d.begin_list();
+        d.each_above(low, [&](float v, int i) {
+            if (!(v >= low)) return;
             if (whole) above += d.weight(v);
-            return true;
-        }, [&] { return above; });
+            d.add_token(v, i);
+        });
+        const uint32_t n = d.merge_lists(above);
         float total = 0.0f;
         bool enough = true;
         if (whole) {
@@ -1048,7 +1212,7 @@ sample_kernel(const T *__restrict__ logits, size_t stride, unsigned vocab, unsig
                 const bool keep = place < limit && (place == 0 || ((!by_mass || ahead[h] < bar) && w[h] >= m));
                 if (!keep) continue;
                 const int i = static_cast<int>(index_of(key[h]));
-                best.offer(fmaxf(w[h] / q[i], 0.0f), i);
+                best.offer(fmaxf(w[h] / d.noise[i], 0.0f), i);
                 if (unordered(ord_of(key[h])) == d.top) ++tops;
                 else rest += w[h];
             }
@@ -1057,57 +1221,99 @@ sample_kernel(const T *__restrict__ logits, size_t stride, unsigned vocab, unsig
             if (d.tid == 0) d.write(won, rest, tops, token, logprob);
             return;
         }
-        if (k > 0) cut = d.template select<false>(0, [&](u64) { return static_cast<u64>(k); });
-        if (by_mass) {
-            const u64 by = d.template select<true>(cut, [&](u64 mass) {
-                const u64 want = static_cast<u64>(ceil(static_cast<double>(p) * static_cast<double>(mass)));
-                return want > 1 ? want : 1ull;
-            });
-            cut = by > cut ? by : cut;
+        if (defer) {
+            if (d.rank == 0 && d.tid == 0) later.rows[atomicAdd(later.count, 1u)] = r;
+            return;
+        }
+        const auto tokens_wanted = [&](u64) { return static_cast<u64>(k); };
+        const auto mass_wanted = [&](u64 mass) {
+            const u64 want = static_cast<u64>(ceil(static_cast<double>(p) * static_cast<double>(mass)));
+            return want > 1 ? want : 1ull;
+        };
+        float rest = 0.0f;
+        uint32_t tops = 0;
+        bool done;
+        if (!by_mass) {
+            done = d.template cut_and_race<false>(0, tokens_wanted, m, cut, best, rest, tops);
+        } else {
+            if (k > 0) {
+                u64 want = 0;
+                uint32_t bin = 0;
+                const typename D::Floor all(0);
+                if (d.template bracket<false>(all, tokens_wanted, want, bin)) cut = d.template refine<false>(all, bin, want);
+            }
+            done = d.template cut_and_race<true>(cut, mass_wanted, m, cut, best, rest, tops);
+        }
+        if (done) {
+            d.finish(best, rest, tops, token, logprob);
+            return;
         }
     }
 
-    const float cut_v = cut == 0 ? -FLT_MAX : unordered(ord_of(cut));
-    const int cut_i = cut == 0 ? 0x7fffffff : static_cast<int>(index_of(cut));
+    const typename D::Floor last_kept(cut);
     float rest = 0.0f;
     uint32_t tops = 0;
     // A value that min-p leaves in, with room for the rounding of its weight.
     const float off = m > 0.0f ? t * logf(m) : -inf();
-    const float least = fmaxf(cut_v, d.top + 1.001f * off - 1e-5f * t - fabsf(d.top) * 4e-7f);
-    d.each_above(fmaxf(least, -FLT_MAX), [&](float v, int i) {
-        if (!(v > cut_v || (v == cut_v && i <= cut_i))) return;
-        const float w = d.weight(v);
-        if (!(w >= m)) return;
-        best.offer(fmaxf(__fdividef(w, q[i]), 0.0f), i);
-        if (v == d.top) ++tops;
-        else rest += w;
+    const float least = fmaxf(last_kept.v, d.top + 1.001f * off - 1e-5f * t - fabsf(d.top) * 4e-7f);
+    d.each_group(fmaxf(least, -FLT_MAX), [&](const uint4 (&v)[kGroup], unsigned c) {
+        d.race_group(v, c, m, [&](float x, int i) { return last_kept.takes(x, i); }, best, rest, tops);
     });
     d.finish(best, rest, tops, token, logprob);
 }
 
-template <class T>
-cudaError_t launch_typed(const void *logits, size_t rows, unsigned vocab, size_t stride, const float *noise,
-                         size_t noise_stride, const SampleAsk &ask, int32_t *tokens, float *logprobs, int num_sms,
-                         cudaStream_t s)
+// FROM_LIST: the rows that the first launch has put down, a cluster taking
+// every so many of them; else row blockIdx.x / blocks.
+template <class T, bool FROM_LIST>
+__global__ void __launch_bounds__(kThreads, 4)
+sample_kernel(const T *__restrict__ logits, size_t stride, unsigned vocab, unsigned per,
+              const float *__restrict__ noise, size_t noise_stride, SampleAsk ask, int32_t *__restrict__ tokens,
+              float *__restrict__ logprobs, Deferred later, bool defer)
+{
+    extern __shared__ __align__(16) unsigned char s_bytes[];
+    Shared &s = *reinterpret_cast<Shared *>(s_bytes);
+    Draw<T> d(s);
+    d.tid = threadIdx.x, d.lane = d.tid & 31, d.warp = d.tid >> 5;
+    d.rank = cluster_rank(), d.blocks = cluster_blocks(), d.vocab = vocab;
+    d.inbox = reinterpret_cast<u64 *>(s_bytes + kSharedBytes);
+    d.count = reinterpret_cast<uint32_t *>(d.inbox);
+    d.carry = d.count + kBins;
+    d.region = inbox_keys(d.blocks) / d.blocks;
+    d.index = reinterpret_cast<float *>(d.inbox + inbox_keys(d.blocks));
+    if (d.blocks > 1) d.meet();   // the blocks' shared memory is there
+    if (!FROM_LIST) {
+        draw_row(d, blockIdx.x / d.blocks, logits, stride, per, noise, noise_stride, ask, tokens, logprobs, later,
+                 defer);
+        return;
+    }
+    const unsigned n = *later.count, clusters = gridDim.x / d.blocks;
+    for (unsigned w = blockIdx.x / d.blocks; w < n; w += clusters) {
+        draw_row(d, later.rows[w], logits, stride, per, noise, noise_stride, ask, tokens, logprobs, later, false);
+        d.meet();   // the shared memory is used again from here
+    }
+    if (d.tid == 0 && atomicAdd(later.left, 1u) == gridDim.x - 1) {   // every block has read the count
+        *later.count = 0;
+        *later.left = 0;
+    }
+}
+
+template <class T, bool FROM_LIST>
+cudaError_t launch_clusters(const T *logits, unsigned clusters, unsigned blocks, unsigned vocab, size_t stride,
+                            const float *noise, size_t noise_stride, const SampleAsk &ask, int32_t *tokens,
+                            float *logprobs, const Deferred &later, bool defer, cudaStream_t s)
 {
     // Chunks of a row; one more where it starts inside its first.
     constexpr unsigned kEach = Chunk<T>::kEach;
-    const unsigned chunks = (vocab + kEach - 1) / kEach;
-    // One block per row, and more while all of them still fit on the GPU at
-    // once (four per SM) and have enough of the row each.
-    unsigned blocks = 1;
-    while (blocks < kMaxCluster && rows * blocks * 2 <= static_cast<size_t>(num_sms) * 4 &&
-           blocks * kLeastChunks < chunks)
-        blocks *= 2;
-    if (rows * blocks > 0x7fffffffull) return cudaErrorInvalidValue;
-    const unsigned per = (chunks + 1 + blocks - 1) / blocks;
     constexpr unsigned kEntryChunks = kGroup * kThreads;   // chunks to kThreads entries of the index
     constexpr size_t kMostChunks = (static_cast<size_t>(1) << 18) / kEach + 1;   // of the largest vocabulary
-    constexpr size_t kMostBytes = kSharedBytes + (kMostChunks + kEntryChunks - 1) / kEntryChunks * kThreads * 4;
+    constexpr size_t kMostBytes = kSharedBytes + inbox_keys(kMaxCluster) * 8 +
+                                  (kMostChunks + kEntryChunks - 1) / kEntryChunks * kThreads * 4;
     static_assert(kMostBytes <= 227 * 1024, "the index of the largest vocabulary fits");
     static_assert((kMostChunks + kEntryChunks - 1) / kEntryChunks * 32 <= 65536, "a warp's entries have 16-bit names");
+    const unsigned chunks = (vocab + kEach - 1) / kEach;
+    const unsigned per = (chunks + 1 + blocks - 1) / blocks;
 
-    const auto kernel = sample_kernel<T>;
+    const auto kernel = sample_kernel<T, FROM_LIST>;
     static std::atomic<unsigned long long> attribute_set{0};   // one bit per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1119,9 +1325,10 @@ cudaError_t launch_typed(const void *logits, size_t rows, unsigned vocab, size_t
         attribute_set.fetch_or(bit);
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(rows) * blocks);
+    cfg.gridDim = dim3(clusters * blocks);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSharedBytes + static_cast<size_t>((per + kEntryChunks - 1) / kEntryChunks) * kThreads * 4;
+    cfg.dynamicSmemBytes = kSharedBytes + inbox_keys(blocks) * 8 +
+                           static_cast<size_t>((per + kEntryChunks - 1) / kEntryChunks) * kThreads * 4;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1130,26 +1337,52 @@ cudaError_t launch_typed(const void *logits, size_t rows, unsigned vocab, size_t
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, static_cast<const T *>(logits), stride, vocab, per, noise, noise_stride,
-                              ask, tokens, logprobs);
+    return cudaLaunchKernelEx(&cfg, kernel, logits, stride, vocab, per, noise, noise_stride, ask, tokens, logprobs,
+                              later, defer);
+}
+
+template <class T>
+cudaError_t launch_typed(const void *logits, size_t rows, unsigned vocab, size_t stride, const float *noise,
+                         size_t noise_stride, const SampleAsk &ask, int32_t *tokens, float *logprobs, const Workspace &ws,
+                         const Deferred &later, cudaStream_t s)
+{
+    const T *x = static_cast<const T *>(logits);
+    const unsigned chunks = (vocab + Chunk<T>::kEach - 1) / Chunk<T>::kEach;
+    // One block per row, and more while all of them still fit on the GPU at
+    // once (four per SM) and have enough of the row each.
+    const size_t most = static_cast<size_t>(ws.num_sms) * 4;
+    unsigned blocks = 1, wide = 1;   // wide: the most that a row of this size is worth
+    while (wide < kMaxCluster && wide * kLeastChunks < chunks) wide *= 2;
+    while (blocks < wide && rows * blocks * 2 <= most) blocks *= 2;
+    if (rows * blocks > 0x7fffffffull) return cudaErrorInvalidValue;
+    // A row that needs histograms takes many times as long as the others, so
+    // where its cluster is narrower than it could be it goes to a second
+    // launch of wide ones.
+    const bool defer = later.rows != nullptr && blocks < wide;
+    cudaError_t e = launch_clusters<T, false>(x, static_cast<unsigned>(rows), blocks, vocab, stride, noise,
+                                              noise_stride, ask, tokens, logprobs, later, defer, s);
+    if (e != cudaSuccess || !defer) return e;
+    const size_t clusters = rows < most / wide ? rows : most / wide;
+    return launch_clusters<T, true>(x, static_cast<unsigned>(clusters), wide, vocab, stride, noise, noise_stride, ask,
+                                    tokens, logprobs, later, false, s);
 }
 
 }  // namespace
 
 cudaError_t launch_sample(LogitType type, const void *logits, size_t rows, size_t vocab, size_t stride,
                           const float *noise, size_t noise_stride, const SampleAsk &ask, int32_t *tokens,
-                          float *logprobs, const Workspace &ws, cudaStream_t s)
+                          float *logprobs, uint32_t *row_words, const Workspace &ws, cudaStream_t s)
 {
     const unsigned v = static_cast<unsigned>(vocab);
+    const Deferred later{row_words, &ws.state->sample_rows, &ws.state->sample_left};
     switch (type) {
     case LogitType::F32:
-        return launch_typed<float>(logits, rows, v, stride, noise, noise_stride, ask, tokens, logprobs, ws.num_sms, s);
+        return launch_typed<float>(logits, rows, v, stride, noise, noise_stride, ask, tokens, logprobs, ws, later, s);
     case LogitType::F16:
-        return launch_typed<__half>(logits, rows, v, stride, noise, noise_stride, ask, tokens, logprobs, ws.num_sms,
-                                    s);
+        return launch_typed<__half>(logits, rows, v, stride, noise, noise_stride, ask, tokens, logprobs, ws, later, s);
     case LogitType::BF16:
-        return launch_typed<__nv_bfloat16>(logits, rows, v, stride, noise, noise_stride, ask, tokens, logprobs,
-                                           ws.num_sms, s);
+        return launch_typed<__nv_bfloat16>(logits, rows, v, stride, noise, noise_stride, ask, tokens, logprobs, ws,
+                                           later, s);
     }
     return cudaErrorInvalidValue;
 }
