@@ -274,38 +274,40 @@ devscan_status paged_scratch(size_t rows, cudaStream_t stream, Workspace *ws, in
     return got;
 }
 
-devscan_status sample_common(LogitType type, const void *logits, size_t rows, size_t vocab, size_t stride,
-                             const float *noise, size_t noise_stride, const SampleAsk &ask, int32_t *tokens,
-                             float *logprobs, cudaStream_t stream)
+// `call` as the caller gave it, vocab in `vocab`; logits of `size` bytes each.
+devscan_status sample_common(cudaError_t (*launch)(const SampleCall &, const Workspace &, cudaStream_t), size_t size,
+                             SampleCall call, size_t vocab, cudaStream_t stream)
 {
-    const size_t size = type == LogitType::F32 ? 4 : 2;
+    const size_t rows = call.rows;
     if (rows > static_cast<size_t>(INT32_MAX)) return DEVSCAN_ERR_INVALID;
-    if (vocab < 1 || vocab > DEVSCAN_SAMPLE_MAX_VOCAB || stride < vocab) return DEVSCAN_ERR_INVALID;
-    if (noise != nullptr && noise_stride < vocab) return DEVSCAN_ERR_INVALID;
+    if (vocab < 1 || vocab > DEVSCAN_SAMPLE_MAX_VOCAB || call.stride < vocab) return DEVSCAN_ERR_INVALID;
+    if (call.noise != nullptr && call.noise_stride < vocab) return DEVSCAN_ERR_INVALID;
     if (rows == 0) return DEVSCAN_OK;
-    if (logits == nullptr || tokens == nullptr) return DEVSCAN_ERR_INVALID;
-    if (misaligned(logits, size) || misaligned(noise, 4) || misaligned(ask.temperature, 4) ||
-        misaligned(ask.top_k, 4) || misaligned(ask.top_p, 4) || misaligned(ask.min_p, 4) || misaligned(tokens, 4) ||
-        misaligned(logprobs, 4))
+    if (call.logits == nullptr || call.tokens == nullptr) return DEVSCAN_ERR_INVALID;
+    if (misaligned(call.logits, size) || misaligned(call.noise, 4) || misaligned(call.temperature, 4) ||
+        misaligned(call.top_k, 4) || misaligned(call.top_p, 4) || misaligned(call.min_p, 4) ||
+        misaligned(call.tokens, 4) || misaligned(call.logprobs, 4))
         return DEVSCAN_ERR_INVALID;
     size_t x_bytes = 0, q_bytes = 0;
-    if (!matrix_bytes(rows, stride, vocab, size, &x_bytes)) return DEVSCAN_ERR_INVALID;
-    if (noise != nullptr && !matrix_bytes(rows, noise_stride, vocab, 4, &q_bytes)) return DEVSCAN_ERR_INVALID;
+    if (!matrix_bytes(rows, call.stride, vocab, size, &x_bytes)) return DEVSCAN_ERR_INVALID;
+    if (call.noise != nullptr && !matrix_bytes(rows, call.noise_stride, vocab, 4, &q_bytes))
+        return DEVSCAN_ERR_INVALID;
     const size_t each = rows * 4;
-    const Span written[] = {{tokens, each}, {logprobs, each}};
-    const Span read[] = {{logits, x_bytes},  {noise, q_bytes},  {ask.temperature, each},
-                         {ask.top_k, each},  {ask.top_p, each}, {ask.min_p, each}};
+    const Span written[] = {{call.tokens, each}, {call.logprobs, each}};
+    const Span read[] = {{call.logits, x_bytes}, {call.noise, q_bytes}, {call.temperature, each},
+                         {call.top_k, each},     {call.top_p, each},    {call.min_p, each}};
     if (written_overlap(written, read)) return DEVSCAN_ERR_INVALID;
+    call.vocab = static_cast<unsigned>(vocab);
     Workspace ws;
     devscan_status st = acquire(stream, 1, &ws);
     if (st != DEVSCAN_OK) return st;
-    void *row_words = nullptr;
-    if (noise != nullptr && (ask.top_k != nullptr || ask.top_p != nullptr)) {
+    if (call.noise != nullptr && (call.top_k != nullptr || call.top_p != nullptr)) {
+        void *row_words = nullptr;
         st = acquire_extra(stream, rows * sizeof(uint32_t), &row_words);
         if (st != DEVSCAN_OK) return st;
+        call.row_words = static_cast<uint32_t *>(row_words);
     }
-    return from_cuda(launch_sample(type, logits, rows, vocab, stride, noise, noise_stride, ask, tokens, logprobs,
-                                   static_cast<uint32_t *>(row_words), ws, stream));
+    return from_cuda(launch(call, ws, stream));
 }
 
 }  // namespace
@@ -684,24 +686,30 @@ devscan_status sample_tokens_f32(const float *logits, size_t rows, size_t vocab,
                                  const int32_t *top_k, const float *top_p, const float *min_p, int32_t *tokens,
                                  float *logprobs, cudaStream_t stream)
 {
-    return sample_common(LogitType::F32, logits, rows, vocab, logits_stride, noise, noise_stride,
-                         {temperature, top_k, top_p, min_p}, tokens, logprobs, stream);
+    return sample_common(launch_sample_f32, 4,
+                         {logits, rows, logits_stride, 0, noise, noise_stride, temperature, top_k, top_p, min_p, tokens,
+                          logprobs, nullptr},
+                         vocab, stream);
 }
 devscan_status sample_tokens_f16(const uint16_t *logits, size_t rows, size_t vocab, size_t logits_stride,
                                  const float *noise, size_t noise_stride, const float *temperature,
                                  const int32_t *top_k, const float *top_p, const float *min_p, int32_t *tokens,
                                  float *logprobs, cudaStream_t stream)
 {
-    return sample_common(LogitType::F16, logits, rows, vocab, logits_stride, noise, noise_stride,
-                         {temperature, top_k, top_p, min_p}, tokens, logprobs, stream);
+    return sample_common(launch_sample_f16, 2,
+                         {logits, rows, logits_stride, 0, noise, noise_stride, temperature, top_k, top_p, min_p, tokens,
+                          logprobs, nullptr},
+                         vocab, stream);
 }
 devscan_status sample_tokens_bf16(const uint16_t *logits, size_t rows, size_t vocab, size_t logits_stride,
                                   const float *noise, size_t noise_stride, const float *temperature,
                                   const int32_t *top_k, const float *top_p, const float *min_p, int32_t *tokens,
                                   float *logprobs, cudaStream_t stream)
 {
-    return sample_common(LogitType::BF16, logits, rows, vocab, logits_stride, noise, noise_stride,
-                         {temperature, top_k, top_p, min_p}, tokens, logprobs, stream);
+    return sample_common(launch_sample_bf16, 2,
+                         {logits, rows, logits_stride, 0, noise, noise_stride, temperature, top_k, top_p, min_p, tokens,
+                          logprobs, nullptr},
+                         vocab, stream);
 }
 
 devscan_status devscan_device_status(cudaStream_t stream)

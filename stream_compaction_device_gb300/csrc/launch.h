@@ -176,14 +176,21 @@ cudaError_t launch_block_table_release(const int32_t *table, size_t stride, int 
 // Token draw.  Per-row settings in device memory, each null for "off".
 // row_words: a word per row of per-stream scratch, for the rows that a second
 // launch draws; null where no row can need it (neither top-k nor top-p).
-enum class LogitType { F32, F16, BF16 };
-struct SampleAsk {
+struct SampleCall {
+    const void *logits;
+    size_t rows, stride;
+    unsigned vocab;
+    const float *noise;
+    size_t noise_stride;
     const float *temperature;
     const int32_t *top_k;
     const float *top_p, *min_p;
+    int32_t *tokens;
+    float *logprobs;
+    uint32_t *row_words;
 };
-cudaError_t launch_sample(LogitType type, const void *logits, size_t rows, size_t vocab, size_t stride,
-                          const float *noise, size_t noise_stride, const SampleAsk &ask, int32_t *tokens,
-                          float *logprobs, uint32_t *row_words, const Workspace &ws, cudaStream_t s);
+cudaError_t launch_sample_f32(const SampleCall &call, const Workspace &ws, cudaStream_t s);
+cudaError_t launch_sample_f16(const SampleCall &call, const Workspace &ws, cudaStream_t s);
+cudaError_t launch_sample_bf16(const SampleCall &call, const Workspace &ws, cudaStream_t s);
 
 }  // namespace devscan

@@ -30,11 +30,13 @@
 //     times the row's.
 //   Histograms.  Where the list would be too long (a wide top-k, a flat row,
 //     a tie of many tokens), the cut is bracketed by a histogram of counts or
-//     masses in shared memory, 32 bins per unit of logit, then of ordered
+//     masses in shared memory, 64 bins per unit of logit, then of ordered
 //     bits, then of indices, each inside the bin where the last one crossed
 //     the mark, until the tokens inside fit the list.  Masses there are
 //     integers (w in units of 2^-31, summed in 64 bits), so no result depends
 //     on the order of the atomics.
+#pragma once
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -60,10 +62,9 @@ constexpr int kQueue = 64;                 // index entries that a warp has wait
 constexpr unsigned kLeastChunks = 512;     // of a block's slice, where rows are few
 constexpr int kList = 1024;                // tokens the short list holds
 constexpr int kKeys = kList / kThreads;    // its keys per thread in the sort
-constexpr int kRanked = 512;               // lists up to here are ordered by counting
 constexpr int kBins = 1024;
-constexpr float kBinsPerUnit = 32.0f;      // first histogram: bins per unit of logit
-constexpr int kGuess = 256;                // tokens asked of the bound for top-p without top-k
+constexpr float kBinsPerUnit = 64.0f;      // first histogram: bins per unit of logit
+constexpr int kGuess = 256, kGuessEach = 16;   // tokens asked of the bound for top-p without top-k: in all, per warp at most
 
 __device__ __forceinline__ float inf() { return __int_as_float(0x7f800000); }
 
@@ -116,6 +117,13 @@ __device__ __forceinline__ uint4 get(const uint32_t *p, unsigned rank)   // four
     return v;
 }
 
+__device__ __forceinline__ uint32_t shared_add(uint32_t *p, uint32_t v)
+{
+    uint32_t old;
+    asm volatile("atom.shared::cta.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(smem_u32(p)), "r"(v) : "memory");
+    return old;
+}
+
 // ---------------------------------------------------------------------------
 // Values.
 // ---------------------------------------------------------------------------
@@ -147,7 +155,7 @@ __device__ __forceinline__ float exp2_approx(float x)
 // by value (a NaN loses to a number).
 template <class T> struct Chunk;
 template <> struct Chunk<float> {
-    static constexpr int kEach = 4;
+    static constexpr int kEach = 4, kSpare = 0;   // kSpare: low bits of ordered() that no value uses
     static constexpr uint32_t kFill = 0xff800000u;
     static __device__ __forceinline__ float value(const uint32_t (&q)[4], int e) { return __uint_as_float(q[e]); }
     static __device__ __forceinline__ float most(const uint32_t (&q)[4], float m)
@@ -158,7 +166,7 @@ template <> struct Chunk<float> {
     }
 };
 template <> struct Chunk<__half> {
-    static constexpr int kEach = 8;
+    static constexpr int kEach = 8, kSpare = 13;
     static constexpr uint32_t kFill = 0xfc00fc00u;
     static __device__ __forceinline__ float value(const uint32_t (&q)[4], int e)
     {
@@ -175,7 +183,7 @@ template <> struct Chunk<__half> {
     }
 };
 template <> struct Chunk<__nv_bfloat16> {
-    static constexpr int kEach = 8;
+    static constexpr int kEach = 8, kSpare = 16;
     static constexpr uint32_t kFill = 0xff80ff80u;
     static __device__ __forceinline__ float value(const uint32_t (&q)[4], int e)
     {
@@ -195,9 +203,10 @@ struct Shared {
     u64 list[kList];                 // this block's collected tokens; a buffer of the sort
     uint4 edge[2];                   // the slice's chunks over the row's ends
     uint16_t queue[kWarps][kQueue];
+    uint32_t bins[kBins];            // of the list's sort
     u64 warp64[kWarps];
     float warpf[kWarps];
-    uint32_t warp_max[kWarps], warp_bound[kWarps], warp_n[kWarps];
+    uint32_t warp_max[kWarps], warp_bound[kWarps], warp_n[kWarps], warp_least[kWarps];
     // What the blocks tell each other, by rank.
     uint32_t top[kMaxCluster], bound[kMaxCluster];
     uint32_t found[2][kMaxCluster];
@@ -217,7 +226,8 @@ struct Shared {
 __host__ __device__ constexpr unsigned inbox_keys(unsigned blocks) { return blocks == 1 ? kList : 2 * kList; }
 constexpr size_t kSharedBytes = (sizeof(Shared) + 127) / 128 * 128;
 
-template <class T>
+// KEEP: the first pass leaves the slice in shared memory for the later ones.
+template <class T, bool KEEP>
 struct Draw {
     using C = Chunk<T>;
     static constexpr int kEach = C::kEach;
@@ -231,6 +241,7 @@ struct Draw {
     const float *noise;              // of the row
     const T *row;
     const uint4 *source;             // the slice
+    uint4 *kept;                     // with KEEP its copy in shared memory
     unsigned tid, lane, warp, rank, blocks;
     unsigned vocab, chunks, mine;    // tokens and chunks of the row; chunks of the slice
     unsigned lo, hi;                 // the slice's whole chunks
@@ -247,7 +258,7 @@ struct Draw {
         int at = 0x7fffffff;
         __device__ __forceinline__ void offer(float sc, int i)
         {
-            if (sc > score || (sc == score && i < at)) score = sc, at = i;
+            if (sc >= score && (sc > score || i < at)) score = sc, at = i;
         }
         __device__ __forceinline__ u64 key() const
         {
@@ -310,6 +321,11 @@ struct Draw {
     static __device__ __forceinline__ uint4 fill() { return make_uint4(C::kFill, C::kFill, C::kFill, C::kFill); }
     __device__ __forceinline__ uint4 chunk(unsigned c) const
     {
+        if (KEEP) return c < mine ? kept[c] : fill();
+        return fetch(c);
+    }
+    __device__ __forceinline__ uint4 fetch(unsigned c) const
+    {
         if (c >= lo && c < hi) return __ldg(source + c);
         if (c >= mine) return fill();
         return s.edge[c == 0 && lo == 1 ? 0 : 1];
@@ -326,7 +342,12 @@ struct Draw {
         for (unsigned c0 = tid; c0 < mine; c0 += kLoads * kThreads) {
             uint4 v[kLoads];
 #pragma unroll
-            for (int u = 0; u < kLoads; ++u) v[u] = chunk(c0 + u * kThreads);
+            for (int u = 0; u < kLoads; ++u) v[u] = fetch(c0 + u * kThreads);
+            if (KEEP) {
+#pragma unroll
+                for (int u = 0; u < kLoads; ++u)
+                    if (c0 + u * kThreads < mine) kept[c0 + u * kThreads] = v[u];
+            }
 #pragma unroll
             for (int g = 0; g < kLoads; g += kGroup) {
                 float group = -inf();
@@ -389,6 +410,10 @@ struct Draw {
                 uint4 v[kGroup];
 #pragma unroll
                 for (int u = 0; u < kGroup; ++u) v[u] = chunk(c + u * kThreads);
+                if (infinite) {
+#pragma unroll
+                    for (int u = 0; u < kGroup; ++u) v[u] = only_infinite(v[u]);
+                }
                 f(v, c);
             }
             __syncwarp();
@@ -422,7 +447,6 @@ struct Draw {
     {
         uint32_t q[4];
         unpack(v, q);
-        if (infinite) only_infinite(q);
 #pragma unroll
         for (int e = 0; e < kEach; ++e) x[e] = C::value(q, e);
         return C::most(q, -inf());
@@ -477,14 +501,20 @@ struct Draw {
         }
     }
 
-    // Replaces every +inf by 0 and everything else by -inf.
-    static __device__ void only_infinite(uint32_t (&q)[4])
+    // The chunk with 0 in place of every +inf, and -inf of everything else.
+    static __device__ __forceinline__ uint4 only_infinite(const uint4 &v)
     {
-        T v[kEach];
-        memcpy(v, q, 16);
+        uint32_t q[4];
+        unpack(v, q);
 #pragma unroll
-        for (int e = 0; e < kEach; ++e) v[e] = static_cast<float>(v[e]) == inf() ? T(0.0f) : T(-inf());
-        memcpy(q, v, 16);
+        for (int k = 0; k < 4; ++k) {
+            uint32_t r = 0;
+#pragma unroll
+            for (int e = 0; e < kEach / 4; ++e)
+                if (C::value(q, k * (kEach / 4) + e) != inf()) r |= kEach == 4 ? C::kFill : C::kFill & (0xffffu << (16 * e));
+            q[k] = r;
+        }
+        return make_uint4(q[0], q[1], q[2], q[3]);
     }
 
     // A race of all tokens needs no selection, so it takes one pass over the
@@ -617,7 +647,7 @@ struct Draw {
         return ahead + (lane == 0 ? V(0) : before);
     }
 
-    // Tokens for the list: begin_list(), then add_token() by any thread, then
+    // Tokens for the list: begin_list(), then add_tokens() by any thread, then
     // merge_lists(), which returns their number over the cluster (the same in
     // every block).  Up to kList they are then in block 0, in any order; more
     // than kList is returned as well if a block has more than its region.
@@ -628,11 +658,34 @@ struct Draw {
         if (tid == 0) s.listed = 0;
         __syncthreads();
     }
-    __device__ __forceinline__ void add_token(float v, int i)
+    // The group's tokens for which in(value, index) holds.  One atomic for a
+    // thread's tokens of a group, then stores that wait for nothing.
+    template <class In>
+    __device__ __forceinline__ void add_tokens(const uint4 (&v)[kGroup], unsigned c, In in)
     {
-        if (*const_cast<volatile uint32_t *>(&s.listed) > region) return;
-        const uint32_t k = atomicAdd(&s.listed, 1u);
-        if (k < region) (rank == 0 ? inbox : s.list)[k] = key_of(ordered(v), static_cast<unsigned>(i));
+        uint32_t which = 0;
+#pragma unroll
+        for (int u = 0; u < kGroup; ++u) {
+            float x[kEach];
+            values(v[u], x);
+            const int i = first + static_cast<int>(c + u * kThreads) * kEach;
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) which |= in(x[e], i + e) ? 1u << (u * kEach + e) : 0u;
+        }
+        if (which == 0 || *const_cast<volatile uint32_t *>(&s.listed) > region) return;
+        uint32_t k = shared_add(&s.listed, __popc(which));
+        if (k + __popc(which) > region) return;
+        u64 *list = rank == 0 ? inbox : s.list;
+#pragma unroll
+        for (int u = 0; u < kGroup; ++u) {
+            if ((which >> (u * kEach) & ((1u << kEach) - 1)) == 0) continue;
+            float x[kEach];
+            values(v[u], x);
+            const int i = first + static_cast<int>(c + u * kThreads) * kEach;
+#pragma unroll
+            for (int e = 0; e < kEach; ++e)
+                if (which >> (u * kEach + e) & 1) list[k++] = key_of(ordered(x[e]), static_cast<unsigned>(i + e));
+        }
     }
     __device__ uint32_t merge_lists(float sum)
     {
@@ -650,10 +703,11 @@ struct Draw {
         uint32_t all = 0;
         for (unsigned b = 0; b < blocks; ++b) all += s.found[now][b];
         if (rank == 0 && blocks > 1 && all <= kList) {   // close the gaps
-            uint32_t at = 0;
-            for (unsigned b = 0; b < blocks; ++b) {
-                for (uint32_t k = tid; k < s.found[now][b]; k += kThreads) s.list[at + k] = inbox[b * region + k];
-                at += s.found[now][b];
+            static_assert(kWarps >= kMaxCluster, "a warp per block's region");
+            if (warp < blocks) {
+                uint32_t at = 0;
+                for (unsigned b = 0; b < warp; ++b) at += s.found[now][b];
+                for (uint32_t k = lane; k < s.found[now][warp]; k += 32) s.list[at + k] = inbox[warp * region + k];
             }
             __syncthreads();
         }
@@ -669,93 +723,69 @@ struct Draw {
 
     // Puts the first `limit` of the n <= kList merged tokens in descending
     // order, by block 0.  Thread t gets the keys at t + h * kThreads; 0 past
-    // the end.  Up to kRanked keys, each key's place is the number of larger
-    // ones, counted in one loop without a barrier; above, a bitonic sort takes
-    // fewer steps.
+    // the end.  A counting sort in bins of equal width from the largest down to
+    // the least, then by key inside a bin, where there are one or two as a
+    // rule: a fixed number of barriers, where a sort by comparisons took two to
+    // three times as long (300 tokens: 6,300 to 10,900 cycles).
     __device__ void sort(uint32_t n, uint32_t limit, u64 (&a)[kKeys])
     {
         u64 *from = blocks == 1 ? inbox : s.list, *to = blocks == 1 ? s.list : inbox;
-        if (n > kRanked) {
-            bitonic(n, a, from, to);
-            return;
-        }
-        constexpr int kHeld = kRanked / kThreads;
-        u64 key[kHeld];
-        uint32_t place[kHeld];
+        constexpr int kPer = kBins / kThreads;
+        u64 key[kKeys];
+        uint32_t most = 0, least = ~0u;
 #pragma unroll
-        for (int h = 0; h < kHeld; ++h) {
+        for (int h = 0; h < kKeys; ++h) {
             key[h] = tid + h * kThreads < n ? from[tid + h * kThreads] : 0;
-            place[h] = 0;
+            if (key[h] == 0) continue;
+            most = max(most, ord_of(key[h]));
+            least = min(least, ord_of(key[h]));
         }
-        const bool two = n > kThreads;
-        if (!two) {
-            if (warp * 32 < n)
-#pragma unroll 8
-                for (uint32_t k = 0; k < n; ++k) place[0] += from[k] > key[0] ? 1u : 0u;
-        } else {
-#pragma unroll 4
-            for (uint32_t k = 0; k < n; ++k) {
-                const u64 other = from[k];
-#pragma unroll
-                for (int h = 0; h < kHeld; ++h) place[h] += other > key[h] ? 1u : 0u;
-            }
-        }
-#pragma unroll
-        for (int h = 0; h < kHeld; ++h)
-            if (key[h] != 0) to[place[h]] = key[h];
+        most = __reduce_max_sync(kFullMask, most);
+        least = __reduce_min_sync(kFullMask, least);
+        if (lane == 0) s.warp_max[warp] = most, s.warp_least[warp] = least;
+        static_assert(kPer == 4, "a thread's bins are one 16-byte access");
+        reinterpret_cast<uint4 *>(s.bins)[tid] = make_uint4(0, 0, 0, 0);
         __syncthreads();
 #pragma unroll
-        for (int h = 0; h < kKeys; ++h) a[h] = tid + h * kThreads < min(n, limit) ? to[tid + h * kThreads] : 0;
-    }
-
-    // Bitonic sort of from[0 .. n): strides inside a warp by shuffles, up to
-    // the block through shared memory, above inside a thread.
-    __device__ void bitonic(uint32_t n, u64 (&a)[kKeys], u64 *from, u64 *to)
-    {
-        unsigned size2 = 32;
-        while (size2 < n) size2 *= 2;
-#pragma unroll
-        for (int h = 0; h < kKeys; ++h) a[h] = tid + h * kThreads < n ? from[tid + h * kThreads] : 0;
-        const bool active = tid < size2;
-        int half = 0;
-        for (unsigned size = 2; size <= size2; size *= 2) {
-            for (unsigned stride = size / 2; stride >= 1; stride /= 2) {
-                if (stride >= kThreads) {
-#pragma unroll
-                    for (int h = 0; h < kKeys; ++h) {
-                        const int o = h ^ static_cast<int>(stride / kThreads);
-                        if (o > h) {
-                            u64 partner = 0;
-#pragma unroll
-                            for (int k = 0; k < kKeys; ++k) partner = k == o ? a[k] : partner;
-                            const bool down = ((tid + h * kThreads) & size) == 0;
-                            const u64 most = a[h] > partner ? a[h] : partner, least = a[h] > partner ? partner : a[h];
-                            a[h] = down ? most : least;
-#pragma unroll
-                            for (int k = 0; k < kKeys; ++k) a[k] = k == o ? (down ? least : most) : a[k];
-                        }
-                    }
-                    continue;
-                }
-                const bool low = (tid & stride) == 0;
-                u64 *buf = half ? from : to;
-                if (stride >= 32) {
-                    half ^= 1;   // this half was last read two exchanges back, before the last barrier
-#pragma unroll
-                    for (int h = 0; h < kKeys; ++h)
-                        if (tid + h * kThreads < size2) buf[tid + h * kThreads] = a[h];
-                    __syncthreads();
-                }
-#pragma unroll
-                for (int h = 0; h < kKeys; ++h) {
-                    if (h > 0 ? size2 <= h * kThreads : !active) continue;
-                    const u64 p = stride >= 32 ? buf[(tid ^ stride) + h * kThreads]
-                                               : __shfl_xor_sync(kFullMask, a[h], stride);
-                    const bool down = ((tid + h * kThreads) & size) == 0;
-                    a[h] = (low == down) == (a[h] > p) ? a[h] : p;
-                }
-            }
+        for (int w = 0; w < kWarps; ++w) {
+            most = max(most, s.warp_max[w]);
+            least = min(least, s.warp_least[w]);
         }
+        // Places by value, then by index: ties fill their range evenly too.
+        const u64 high = static_cast<u64>(most >> C::kSpare) * vocab + vocab - 1;
+        const float scaled = kBins / static_cast<float>(high - static_cast<u64>(least >> C::kSpare) * vocab + 1);
+        uint32_t bin[kKeys], order[kKeys];
+#pragma unroll
+        for (int h = 0; h < kKeys; ++h) {
+            if (key[h] == 0) continue;
+            const u64 at = static_cast<u64>(ord_of(key[h]) >> C::kSpare) * vocab + (vocab - 1 - index_of(key[h]));
+            bin[h] = min(static_cast<uint32_t>(static_cast<float>(high - at) * scaled), kBins - 1u);
+            order[h] = shared_add(&s.bins[bin[h]], 1);
+        }
+        __syncthreads();
+        uint4 begin = reinterpret_cast<uint4 *>(s.bins)[tid];
+        uint32_t all = 0;
+        const uint32_t before = block_scan(begin.x + begin.y + begin.z + begin.w, s.warp_n, &all);
+        const uint32_t n0 = begin.x, n1 = begin.y, n2 = begin.z;
+        begin = make_uint4(before, before + n0, before + n0 + n1, before + n0 + n1 + n2);
+        reinterpret_cast<uint4 *>(s.bins)[tid] = begin;
+        __syncthreads();
+#pragma unroll
+        for (int h = 0; h < kKeys; ++h)
+            if (key[h] != 0) to[s.bins[bin[h]] + order[h]] = key[h];
+        __syncthreads();
+#pragma unroll
+        for (int h = 0; h < kKeys; ++h) {
+            if (key[h] == 0) continue;
+            const uint32_t first_of = s.bins[bin[h]], end = bin[h] + 1 < kBins ? s.bins[bin[h] + 1] : n;
+            uint32_t place = first_of;
+            if (end - first_of > 1)
+                for (uint32_t k = first_of; k < end; ++k) place += to[k] > key[h] ? 1u : 0u;
+            from[place] = key[h];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int h = 0; h < kKeys; ++h) a[h] = tid + h * kThreads < min(n, limit) ? from[tid + h * kThreads] : 0;
     }
 
     __device__ __forceinline__ void write(u64 won, float rest, uint32_t tops, int32_t *token, float *logprob)
@@ -823,7 +853,9 @@ struct Draw {
     // The bin of the first histogram: falls as v grows.
     __device__ __forceinline__ int bin_of(float v) const
     {
-        return min(__float2int_rz((top - v) * kBinsPerUnit), kBins - 1);
+        // The sum's last bit is worth 1: its low bits are the rounded bin.
+        const float most = static_cast<float>(kBins - 1) / kBinsPerUnit;
+        return __float_as_int(fmaf(fminf(top - v, most), kBinsPerUnit, 8388608.0f)) - 0x4b000000;
     }
 
     // One histogram level: adds what each value holds, then finds the bin
@@ -846,11 +878,11 @@ struct Draw {
                 holds[e] = b[e] < 0 ? 0 : MASS ? mass(x[e]) : 1;
             }
 #pragma unroll
-            for (int e = 0; e < kEach; ++e) old[e] = holds[e] != 0 ? atomicAdd(&count[b[e]], holds[e]) : 0;
+            for (int e = 0; e < kEach; ++e) old[e] = holds[e] != 0 ? shared_add(&count[b[e]], holds[e]) : 0;
             if (MASS) {
 #pragma unroll
                 for (int e = 0; e < kEach; ++e)
-                    if (old[e] + holds[e] < old[e]) atomicAdd(&carry[b[e]], 1u);
+                    if (old[e] + holds[e] < old[e]) shared_add(&carry[b[e]], 1);
             }
         });
         meet();
@@ -888,16 +920,23 @@ struct Draw {
         return true;
     }
 
-    // The least ordered bits o with bin_of(o) <= b.
+    // The least ordered bits o with bin_of(o) <= b, by one warp: 32 probes cut
+    // the range to a 32nd.
     __device__ uint32_t edge(int b) const
     {
-        uint32_t lo = ordered(-FLT_MAX), hi = ordered(top);
-        while (lo < hi) {
-            const uint32_t mid = lo + (hi - lo) / 2;
-            if (bin_of(unordered(mid)) <= b) hi = mid;
-            else lo = mid + 1;
+        uint32_t from = ordered(-FLT_MAX), to = ordered(top);
+        while (from < to) {
+            const uint32_t step = (to - from) / 32 + 1;
+            const uint32_t probe = min(from + min(lane * step, to - from), to);
+            const unsigned in = __ballot_sync(kFullMask, bin_of(unordered(probe)) <= b);
+            const uint32_t at = in == 0 ? 31 : __ffs(in) - 1;   // the first probe inside, or the last outside
+            const uint32_t found = __shfl_sync(kFullMask, probe, at);
+            const uint32_t before = __shfl_sync(kFullMask, probe, at == 0 ? 0 : at - 1);
+            if (in == 0) from = found + 1;
+            else if (at == 0) return found;
+            else from = before + 1, to = found;
         }
-        return lo;
+        return to;
     }
 
     // A cut of the order: the key of the last token of the shortest prefix
@@ -913,15 +952,28 @@ struct Draw {
         __device__ __forceinline__ bool takes(float x, int at) const { return x > v || (x == v && at <= i); }
     };
 
-    // The bin of the first histogram where the cut lies, and what is wanted
-    // inside it; false if all that take part hold less than wanted.
+    // The range of ordered bits of the first histogram's bin where the cut
+    // lies, and what is wanted inside it; false if all that take part hold less
+    // than wanted.
     template <bool MASS, class Want>
-    __device__ bool bracket(const Floor &floor, Want wanted, u64 &want, uint32_t &bin)
+    __device__ bool bracket(const Floor &floor, Want wanted, u64 &want, uint32_t &lo_bits, uint32_t &hi_bits)
     {
+        uint32_t bin = 0;
         // Below top - 23 T a weight rounds to no mass.
         const float least = MASS ? fmaxf(floor.v, top - 23.0f * t) : floor.v;
-        return histogram<MASS>(least, [&](float v, int i) { return floor.takes(v, i) ? bin_of(v) : -1; }, wanted, want,
-                               bin);
+        if (!histogram<MASS>(least, [&](float v, int i) { return floor.takes(v, i) ? bin_of(v) : -1; }, wanted, want,
+                             bin))
+            return false;
+        if (warp == 0) {
+            const uint32_t o = edge(static_cast<int>(bin));
+            if (lane == 0) s.pick_lo = o;
+        } else if (warp == 1) {
+            const uint32_t o = bin == 0 ? ordered(top) : edge(static_cast<int>(bin) - 1) - 1;
+            if (lane == 0) s.pick_hi = o;
+        }
+        __syncthreads();
+        lo_bits = s.pick_lo, hi_bits = s.pick_hi;
+        return true;
     }
 
     // Block 0 puts the n merged tokens in order, of which the first that hold
@@ -944,15 +996,11 @@ struct Draw {
         __syncthreads();
     }
 
-    // The cut's key, from the bin of the first histogram where it lies.
+    // The cut's key, from the range of ordered bits where it lies.
     template <bool MASS>
-    __device__ u64 refine(const Floor &floor, uint32_t bin, u64 want)
+    __device__ u64 refine(const Floor &floor, uint32_t lo_bits, uint32_t hi_bits, u64 want)
     {
-        if (tid == 0) s.pick_lo = edge(static_cast<int>(bin));
-        if (tid == 32) s.pick_hi = bin == 0 ? ordered(top) : edge(static_cast<int>(bin) - 1) - 1;
-        __syncthreads();
-        uint32_t lo_bits = s.pick_lo, hi_bits = s.pick_hi;   // the cut's ordered bits
-        uint32_t i_lo = 0, i_hi = vocab - 1;                 // and, once these are equal, its index
+        uint32_t bin = 0, i_lo = 0, i_hi = vocab - 1;   // its index's range, once lo_bits == hi_bits
         const auto same = [&](u64) { return want; };
         for (;;) {
             const float v_lo = unordered(lo_bits), v_hi = unordered(hi_bits);
@@ -962,9 +1010,7 @@ struct Draw {
                        (!tie || (static_cast<unsigned>(i) >= i_lo && static_cast<unsigned>(i) <= i_hi));
             };
             begin_list();
-            each_above(v_lo, [&](float v, int i) {
-                if (inside(v, i)) add_token(v, i);
-            });
+            each_group(v_lo, [&](const uint4 (&v)[kGroup], unsigned c) { add_tokens(v, c, inside); });
             const uint32_t n = merge_lists(0.0f);
             if (n <= kList) {
                 if (rank == 0) {
@@ -1004,30 +1050,20 @@ struct Draw {
     {
         const Floor floor(floor_key);
         u64 want = 0;
-        uint32_t bin = 0;
+        uint32_t lo_bits = 0, hi_bits = 0;
         cut = floor_key;
-        if (!bracket<MASS>(floor, wanted, want, bin)) return false;
-        // No value of the bin is below this.
-        const float low = bin + 1 < kBins ? top - (static_cast<float>(bin + 1) / kBinsPerUnit) * 1.0001f - fabsf(top) * 4e-7f
-                                          : floor.v;
+        if (!bracket<MASS>(floor, wanted, want, lo_bits, hi_bits)) return false;
+        const float v_lo = unordered(lo_bits), v_hi = unordered(hi_bits);
         begin_list();
-        each_group(fmaxf(low, floor.v), [&](const uint4 (&v)[kGroup], unsigned c) {
-            race_group(v, c, m, [&](float x, int) { return x >= floor.v && bin_of(x) < static_cast<int>(bin); }, best, rest, tops);
-#pragma unroll
-            for (int u = 0; u < kGroup; ++u) {
-                float x[kEach];
-                values(v[u], x);
-                const int i = first + static_cast<int>(c + u * kThreads) * kEach;
-#pragma unroll
-                for (int e = 0; e < kEach; ++e)
-                    if (floor.takes(x[e], i + e) && bin_of(x[e]) == static_cast<int>(bin)) add_token(x[e], i + e);
-            }
+        each_group(fmaxf(v_lo, floor.v), [&](const uint4 (&v)[kGroup], unsigned c) {
+            race_group(v, c, m, [&](float x, int) { return x > v_hi; }, best, rest, tops);
+            add_tokens(v, c, [&](float x, int i) { return x >= v_lo && x <= v_hi && floor.takes(x, i); });
         });
         const uint32_t n = merge_lists(0.0f);
         if (n > kList) {
             best = Best();
             rest = 0.0f, tops = 0;
-            cut = refine<MASS>(floor, bin, want);
+            cut = refine<MASS>(floor, lo_bits, hi_bits, want);
             return false;
         }
         if (rank == 0) {
@@ -1054,31 +1090,30 @@ struct Deferred {
     unsigned *count, *left;          // rows put down; blocks of the second launch that are through
 };
 
-// One row by one cluster.  With `defer` a row that needs histograms is put
-// down instead.
-template <class T>
-__device__ __forceinline__ void draw_row(Draw<T> &d, unsigned r, const T *logits, size_t stride, unsigned per,
-                                         const float *noise, size_t noise_stride, const SampleAsk &ask,
-                                         int32_t *tokens, float *logprobs, const Deferred &later, bool defer)
+// One row by one cluster.  Without HISTOGRAMS a row that needs them is put
+// down for later.
+template <class T, bool HISTOGRAMS>
+__device__ __forceinline__ void draw_row(Draw<T, HISTOGRAMS> &d, unsigned r, const SampleCall &call, unsigned per,
+                                         const Deferred &later)
 {
-    using D = Draw<T>;
+    using D = Draw<T, HISTOGRAMS>;
     Shared &s = d.s;
     const unsigned vocab = d.vocab;
-    d.row = logits + static_cast<size_t>(r) * stride;
-    d.noise = noise + static_cast<size_t>(r) * noise_stride;
+    d.row = static_cast<const T *>(call.logits) + static_cast<size_t>(r) * call.stride;
+    d.noise = call.noise + static_cast<size_t>(r) * call.noise_stride;
     d.infinite = false;
     d.place(per);
 
-    const float t = ask.temperature != nullptr ? ask.temperature[r] : 1.0f;
-    int k = ask.top_k != nullptr ? ask.top_k[r] : 0;
+    const float t = call.temperature != nullptr ? call.temperature[r] : 1.0f;
+    int k = call.top_k != nullptr ? call.top_k[r] : 0;
     if (k <= 0 || static_cast<unsigned>(k) >= vocab) k = 0;
-    float p = ask.top_p != nullptr ? ask.top_p[r] : 1.0f;
-    const float m = ask.min_p != nullptr ? ask.min_p[r] : 0.0f;
+    float p = call.top_p != nullptr ? call.top_p[r] : 1.0f;
+    const float m = call.min_p != nullptr ? call.min_p[r] : 0.0f;
     // One token stays, the first of the order: no draw.
-    const bool greedy = noise == nullptr || !(t > 0.0f) || k == 1 || vocab == 1 || !(p > 0.0f) || !(m <= 1.0f);
+    const bool greedy = call.noise == nullptr || !(t > 0.0f) || k == 1 || vocab == 1 || !(p > 0.0f) || !(m <= 1.0f);
     const bool by_mass = !(p >= 1.0f);
-    int32_t *token = tokens + r;
-    float *logprob = logprobs != nullptr ? logprobs + r : nullptr;
+    int32_t *token = call.tokens + r;
+    float *logprob = call.logprobs != nullptr ? call.logprobs + r : nullptr;
 
     d.t = t;
     d.scale = fminf(1.4426950408889634f / t, FLT_MAX);
@@ -1103,7 +1138,7 @@ __device__ __forceinline__ void draw_row(Draw<T> &d, unsigned r, const T *logits
     const unsigned full = min(d.mine / 32, static_cast<unsigned>(kWarps));
     const unsigned warps = last * min(per / 32, static_cast<unsigned>(kWarps)) +
                            min((d.chunks - last * per) / 32, static_cast<unsigned>(kWarps));
-    const int wanted = k > 0 ? k : kGuess;
+    const int wanted = k > 0 ? k : min(kGuess, kGuessEach * static_cast<int>(warps));
     const int j = warps > 0 ? (wanted + static_cast<int>(warps) - 1) / static_cast<int>(warps) : 33;
     const bool bounded = !greedy && (k > 0 || by_mass) && j <= 32;
     uint32_t bound = ~0u;
@@ -1174,10 +1209,11 @@ __device__ __forceinline__ void draw_row(Draw<T> &d, unsigned r, const T *logits
         }
         const int now = d.turn;
         d.begin_list();
-        d.each_above(low, [&](float v, int i) {
-            if (!(v >= low)) return;
-            if (whole) above += d.weight(v);
-            d.add_token(v, i);
+        d.each_group(low, [&](const uint4 (&v)[kGroup], unsigned c) {
+            d.add_tokens(v, c, [&](float x, int) {
+                if (whole && x >= low) above += d.weight(x);
+                return x >= low;
+            });
         });
         const uint32_t n = d.merge_lists(above);
         float total = 0.0f;
@@ -1221,10 +1257,10 @@ __device__ __forceinline__ void draw_row(Draw<T> &d, unsigned r, const T *logits
             if (d.tid == 0) d.write(won, rest, tops, token, logprob);
             return;
         }
-        if (defer) {
+        if constexpr (!HISTOGRAMS) {
             if (d.rank == 0 && d.tid == 0) later.rows[atomicAdd(later.count, 1u)] = r;
             return;
-        }
+        } else {
         const auto tokens_wanted = [&](u64) { return static_cast<u64>(k); };
         const auto mass_wanted = [&](u64 mass) {
             const u64 want = static_cast<u64>(ceil(static_cast<double>(p) * static_cast<double>(mass)));
@@ -1238,15 +1274,17 @@ __device__ __forceinline__ void draw_row(Draw<T> &d, unsigned r, const T *logits
         } else {
             if (k > 0) {
                 u64 want = 0;
-                uint32_t bin = 0;
+                uint32_t lo_bits = 0, hi_bits = 0;
                 const typename D::Floor all(0);
-                if (d.template bracket<false>(all, tokens_wanted, want, bin)) cut = d.template refine<false>(all, bin, want);
+                if (d.template bracket<false>(all, tokens_wanted, want, lo_bits, hi_bits))
+                    cut = d.template refine<false>(all, lo_bits, hi_bits, want);
             }
             done = d.template cut_and_race<true>(cut, mass_wanted, m, cut, best, rest, tops);
         }
         if (done) {
             d.finish(best, rest, tops, token, logprob);
             return;
+        }
         }
     }
 
@@ -1262,58 +1300,64 @@ __device__ __forceinline__ void draw_row(Draw<T> &d, unsigned r, const T *logits
     d.finish(best, rest, tops, token, logprob);
 }
 
-// FROM_LIST: the rows that the first launch has put down, a cluster taking
-// every so many of them; else row blockIdx.x / blocks.
-template <class T, bool FROM_LIST>
-__global__ void __launch_bounds__(kThreads, 4)
-sample_kernel(const T *__restrict__ logits, size_t stride, unsigned vocab, unsigned per,
-              const float *__restrict__ noise, size_t noise_stride, SampleAsk ask, int32_t *__restrict__ tokens,
-              float *__restrict__ logprobs, Deferred later, bool defer)
+// What a launch does: every row, leaving out those that need histograms; every
+// row; the rows that the first kind has left out, a cluster taking every so
+// many of them.  Four blocks per SM for the first, whose rows are many and
+// wait for memory; two for the others, whose passes want registers.
+enum class Pass { Plain, Whole, Left };
+template <Pass PASS> constexpr int kBlocksPerSm = PASS == Pass::Plain ? 4 : 2;
+
+template <class T, Pass PASS>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm<PASS>)
+sample_kernel(const SampleCall call, unsigned per, const Deferred later)
 {
     extern __shared__ __align__(16) unsigned char s_bytes[];
     Shared &s = *reinterpret_cast<Shared *>(s_bytes);
-    Draw<T> d(s);
+    constexpr bool kKeep = PASS != Pass::Plain;
+    Draw<T, kKeep> d(s);
     d.tid = threadIdx.x, d.lane = d.tid & 31, d.warp = d.tid >> 5;
-    d.rank = cluster_rank(), d.blocks = cluster_blocks(), d.vocab = vocab;
+    d.rank = cluster_rank(), d.blocks = cluster_blocks(), d.vocab = call.vocab;
     d.inbox = reinterpret_cast<u64 *>(s_bytes + kSharedBytes);
     d.count = reinterpret_cast<uint32_t *>(d.inbox);
     d.carry = d.count + kBins;
     d.region = inbox_keys(d.blocks) / d.blocks;
-    d.index = reinterpret_cast<float *>(d.inbox + inbox_keys(d.blocks));
+    d.kept = reinterpret_cast<uint4 *>(d.inbox + inbox_keys(d.blocks));
+    d.index = reinterpret_cast<float *>(d.kept + (kKeep ? per : 0));
     if (d.blocks > 1) d.meet();   // the blocks' shared memory is there
-    if (!FROM_LIST) {
-        draw_row(d, blockIdx.x / d.blocks, logits, stride, per, noise, noise_stride, ask, tokens, logprobs, later,
-                 defer);
-        return;
-    }
-    const unsigned n = *later.count, clusters = gridDim.x / d.blocks;
-    for (unsigned w = blockIdx.x / d.blocks; w < n; w += clusters) {
-        draw_row(d, later.rows[w], logits, stride, per, noise, noise_stride, ask, tokens, logprobs, later, false);
-        d.meet();   // the shared memory is used again from here
-    }
-    if (d.tid == 0 && atomicAdd(later.left, 1u) == gridDim.x - 1) {   // every block has read the count
-        *later.count = 0;
-        *later.left = 0;
+    if constexpr (PASS != Pass::Left) {
+        draw_row<T, kKeep>(d, blockIdx.x / d.blocks, call, per, later);
+    } else {
+        const unsigned n = *later.count, clusters = gridDim.x / d.blocks;
+        for (unsigned w = blockIdx.x / d.blocks; w < n; w += clusters) {
+            draw_row<T, kKeep>(d, later.rows[w], call, per, later);
+            d.meet();   // the shared memory is used again from here
+        }
+        if (d.tid == 0 && atomicAdd(later.left, 1u) == gridDim.x - 1) {   // every block has read the count
+            *later.count = 0;
+            *later.left = 0;
+        }
     }
 }
 
-template <class T, bool FROM_LIST>
-cudaError_t launch_clusters(const T *logits, unsigned clusters, unsigned blocks, unsigned vocab, size_t stride,
-                            const float *noise, size_t noise_stride, const SampleAsk &ask, int32_t *tokens,
-                            float *logprobs, const Deferred &later, bool defer, cudaStream_t s)
+template <class T, Pass PASS>
+cudaError_t launch_clusters(const SampleCall &call, unsigned clusters, unsigned blocks, const Deferred &later,
+                            cudaStream_t s)
 {
     // Chunks of a row; one more where it starts inside its first.
     constexpr unsigned kEach = Chunk<T>::kEach;
     constexpr unsigned kEntryChunks = kGroup * kThreads;   // chunks to kThreads entries of the index
     constexpr size_t kMostChunks = (static_cast<size_t>(1) << 18) / kEach + 1;   // of the largest vocabulary
-    constexpr size_t kMostBytes = kSharedBytes + inbox_keys(kMaxCluster) * 8 +
-                                  (kMostChunks + kEntryChunks - 1) / kEntryChunks * kThreads * 4;
-    static_assert(kMostBytes <= 227 * 1024, "the index of the largest vocabulary fits");
+    constexpr bool kKeep = PASS != Pass::Plain;
+    constexpr size_t kMostEntries = (kMostChunks + kEntryChunks - 1) / kEntryChunks * kThreads;
+    constexpr size_t kMostKept = kKeep ? (kMostChunks + kMaxCluster - 1) / kMaxCluster * 16 : 0;
+    constexpr size_t kMostBytes = kSharedBytes + inbox_keys(kMaxCluster) * 8 + kMostKept +
+                                  (kKeep ? kMostEntries / kMaxCluster + kThreads : kMostEntries) * 4;
+    static_assert(kMostBytes <= 227 * 1024, "the largest vocabulary fits");
     static_assert((kMostChunks + kEntryChunks - 1) / kEntryChunks * 32 <= 65536, "a warp's entries have 16-bit names");
-    const unsigned chunks = (vocab + kEach - 1) / kEach;
+    const unsigned chunks = (call.vocab + kEach - 1) / kEach;
     const unsigned per = (chunks + 1 + blocks - 1) / blocks;
 
-    const auto kernel = sample_kernel<T, FROM_LIST>;
+    const auto kernel = sample_kernel<T, PASS>;
     static std::atomic<unsigned long long> attribute_set{0};   // one bit per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1327,7 +1371,7 @@ cudaError_t launch_clusters(const T *logits, unsigned clusters, unsigned blocks,
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(clusters * blocks);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSharedBytes + inbox_keys(blocks) * 8 +
+    cfg.dynamicSmemBytes = kSharedBytes + inbox_keys(blocks) * 8 + (kKeep ? static_cast<size_t>(per) * 16 : 0) +
                            static_cast<size_t>((per + kEntryChunks - 1) / kEntryChunks) * kThreads * 4;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -1337,54 +1381,32 @@ cudaError_t launch_clusters(const T *logits, unsigned clusters, unsigned blocks,
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, logits, stride, vocab, per, noise, noise_stride, ask, tokens, logprobs,
-                              later, defer);
+    return cudaLaunchKernelEx(&cfg, kernel, call, per, later);
 }
 
 template <class T>
-cudaError_t launch_typed(const void *logits, size_t rows, unsigned vocab, size_t stride, const float *noise,
-                         size_t noise_stride, const SampleAsk &ask, int32_t *tokens, float *logprobs, const Workspace &ws,
-                         const Deferred &later, cudaStream_t s)
+cudaError_t launch_typed(const SampleCall &call, const Workspace &ws, cudaStream_t s)
 {
-    const T *x = static_cast<const T *>(logits);
-    const unsigned chunks = (vocab + Chunk<T>::kEach - 1) / Chunk<T>::kEach;
+    const Deferred later{call.row_words, &ws.state->sample_rows, &ws.state->sample_left};
+    const size_t rows = call.rows;
+    const unsigned chunks = (call.vocab + Chunk<T>::kEach - 1) / Chunk<T>::kEach;
     // One block per row, and more while all of them still fit on the GPU at
-    // once (four per SM) and have enough of the row each.
-    const size_t most = static_cast<size_t>(ws.num_sms) * 4;
+    // once and have enough of the row each.
+    const size_t sms = static_cast<size_t>(ws.num_sms);
     unsigned blocks = 1, wide = 1;   // wide: the most that a row of this size is worth
     while (wide < kMaxCluster && wide * kLeastChunks < chunks) wide *= 2;
-    while (blocks < wide && rows * blocks * 2 <= most) blocks *= 2;
+    while (blocks < wide && rows * blocks * 2 <= sms * kBlocksPerSm<Pass::Plain>) blocks *= 2;
     if (rows * blocks > 0x7fffffffull) return cudaErrorInvalidValue;
-    // A row that needs histograms takes many times as long as the others, so
-    // where its cluster is narrower than it could be it goes to a second
-    // launch of wide ones.
-    const bool defer = later.rows != nullptr && blocks < wide;
-    cudaError_t e = launch_clusters<T, false>(x, static_cast<unsigned>(rows), blocks, vocab, stride, noise,
-                                              noise_stride, ask, tokens, logprobs, later, defer, s);
-    if (e != cudaSuccess || !defer) return e;
-    const size_t clusters = rows < most / wide ? rows : most / wide;
-    return launch_clusters<T, true>(x, static_cast<unsigned>(clusters), wide, vocab, stride, noise, noise_stride, ask,
-                                    tokens, logprobs, later, false, s);
+    const unsigned n = static_cast<unsigned>(rows);
+    const size_t most = sms * kBlocksPerSm<Pass::Whole> / wide;   // wide clusters on the GPU at once
+    if (later.rows != nullptr && rows <= most)
+        return launch_clusters<T, Pass::Whole>(call, n, wide, later, s);
+    const cudaError_t e = launch_clusters<T, Pass::Plain>(call, n, blocks, later, s);
+    if (e != cudaSuccess || later.rows == nullptr) return e;
+    // A row that needs histograms takes many times as long as the others:
+    // these go to a second launch of wide clusters.
+    return launch_clusters<T, Pass::Left>(call, static_cast<unsigned>(rows < most ? rows : most), wide, later, s);
 }
 
 }  // namespace
-
-cudaError_t launch_sample(LogitType type, const void *logits, size_t rows, size_t vocab, size_t stride,
-                          const float *noise, size_t noise_stride, const SampleAsk &ask, int32_t *tokens,
-                          float *logprobs, uint32_t *row_words, const Workspace &ws, cudaStream_t s)
-{
-    const unsigned v = static_cast<unsigned>(vocab);
-    const Deferred later{row_words, &ws.state->sample_rows, &ws.state->sample_left};
-    switch (type) {
-    case LogitType::F32:
-        return launch_typed<float>(logits, rows, v, stride, noise, noise_stride, ask, tokens, logprobs, ws, later, s);
-    case LogitType::F16:
-        return launch_typed<__half>(logits, rows, v, stride, noise, noise_stride, ask, tokens, logprobs, ws, later, s);
-    case LogitType::BF16:
-        return launch_typed<__nv_bfloat16>(logits, rows, v, stride, noise, noise_stride, ask, tokens, logprobs, ws,
-                                           later, s);
-    }
-    return cudaErrorInvalidValue;
-}
-
 }  // namespace devscan
