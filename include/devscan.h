@@ -365,7 +365,7 @@ devscan_status radix_sort_digits_u32(uint32_t *keys, uint32_t *tmp, size_t n, cu
  * Sums saturate at INT32_MAX.  No buffer that is written may overlap any
  * other (DEVSCAN_ERR_INVALID); pointers are aligned to their element size.
  * Traffic: 8 bytes per page moved, 16 to 20 per token, 4 to 9 per row.  One
- * launch up to 8,192 rows; above, two, with 4 bytes per row of per-stream
+ * launch up to 4,096 rows; above, two, with 8 bytes per row of per-stream
  * scratch allocated stream-ordered on first use (DEVSCAN_ERR_NOMEM).
  * ------------------------------------------------------------------------- */
 devscan_status block_table_extend_i32(int32_t *table, size_t stride, size_t rows, int width, const int32_t *cached,

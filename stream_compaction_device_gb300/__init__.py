@@ -26,8 +26,15 @@ if hasattr(torch, "uint32"):
     _SUFFIX[torch.uint32] = "u32"
 
 
+_RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_handle(stream) -> int:
     if stream is None:
+        # The current device's current stream without a Stream object: the
+        # object takes longer to make than a small call's launch.
+        if _RAW_STREAM is not None:
+            return _RAW_STREAM(torch._C._cuda_getDevice())
         stream = torch.cuda.current_stream()
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -317,12 +324,14 @@ def radix_sort_digits(keys: torch.Tensor, tmp: torch.Tensor | None = None, strea
     return keys
 
 
-def _check_vector(t: torch.Tensor, name: str, dtype: torch.dtype, size: int) -> None:
+def _check_vector(t: torch.Tensor, name: str, dtype: torch.dtype, size: int) -> int:
+    """A contiguous CUDA tensor of that type and size; returns its address."""
+    if t.is_cuda and t.dtype is dtype and t.numel() == size and t.is_contiguous():
+        return t.data_ptr()
     _check_cuda(t, name)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if t.numel() != size:
-        raise ValueError(f"{name} must hold {size} elements")
+    raise ValueError(f"{name} must hold {size} elements")
 
 
 def _check_matrix(t: torch.Tensor, name: str) -> int:
@@ -362,20 +371,19 @@ def block_table_extend(table: torch.Tensor, cached: torch.Tensor, fresh: torch.T
     another tensor than ``free``)."""
     stride = _check_table(table, page_size)
     rows, width = table.shape
-    _check_vector(cached, "cached", torch.int32, rows)
-    _check_vector(fresh, "fresh", torch.int32, rows)
-    _check_vector(pages, "pages", torch.int32, pages.numel())
-    _check_vector(free, "free", torch.int32, 1)
+    pool = pages.numel()
     if granted is None:
         granted = torch.empty(rows, dtype=torch.uint8, device=table.device)
     if left is None:
         left = torch.empty(1, dtype=torch.int32, device=table.device)
-    _check_vector(granted, "granted", torch.uint8, rows)
-    _check_vector(left, "left", torch.int32, 1)
-    _lib.check(load().block_table_extend_i32(table.data_ptr(), stride, rows, width, cached.data_ptr(),
-                                             fresh.data_ptr(), int(page_size), pages.data_ptr(), pages.numel(),
-                                             free.data_ptr(), granted.data_ptr(), left.data_ptr(),
-                                             _stream_handle(stream)), "block_table_extend_i32")
+    status = load().block_table_extend_i32(
+        table.data_ptr(), stride, rows, width, _check_vector(cached, "cached", torch.int32, rows),
+        _check_vector(fresh, "fresh", torch.int32, rows), int(page_size),
+        _check_vector(pages, "pages", torch.int32, pool), pool, _check_vector(free, "free", torch.int32, 1),
+        _check_vector(granted, "granted", torch.uint8, rows), _check_vector(left, "left", torch.int32, 1),
+        _stream_handle(stream))
+    if status:
+        _lib.check(status, "block_table_extend_i32")
     return granted, left
 
 
@@ -388,10 +396,6 @@ def slot_map(table: torch.Tensor, cached: torch.Tensor, fresh: torch.Tensor, pag
     leaves out the rows whose flag is 0; ``out`` passes the four tensors."""
     stride = _check_table(table, page_size)
     rows, width = table.shape
-    _check_vector(cached, "cached", torch.int32, rows)
-    _check_vector(fresh, "fresh", torch.int32, rows)
-    if granted is not None:
-        _check_vector(granted, "granted", torch.uint8, rows)
     tokens = int(tokens)
     if tokens < 0:
         raise ValueError("tokens must not be negative")
@@ -400,14 +404,15 @@ def slot_map(table: torch.Tensor, cached: torch.Tensor, fresh: torch.Tensor, pag
         out = (new(rows + 1, torch.int32), new(tokens, torch.int64), new(tokens, torch.int32),
                new(tokens, torch.int32))
     starts, slots, positions, row_ids = out
-    _check_vector(starts, "starts", torch.int32, rows + 1)
-    _check_vector(slots, "slots", torch.int64, tokens)
-    _check_vector(positions, "positions", torch.int32, tokens)
-    _check_vector(row_ids, "rows", torch.int32, tokens)
-    _lib.check(load().slot_map_i32(table.data_ptr(), stride, rows, width, cached.data_ptr(), fresh.data_ptr(),
-                                   None if granted is None else granted.data_ptr(), int(page_size), tokens,
-                                   starts.data_ptr(), slots.data_ptr(), positions.data_ptr(), row_ids.data_ptr(),
-                                   _stream_handle(stream)), "slot_map_i32")
+    status = load().slot_map_i32(
+        table.data_ptr(), stride, rows, width, _check_vector(cached, "cached", torch.int32, rows),
+        _check_vector(fresh, "fresh", torch.int32, rows),
+        None if granted is None else _check_vector(granted, "granted", torch.uint8, rows), int(page_size), tokens,
+        _check_vector(starts, "starts", torch.int32, rows + 1), _check_vector(slots, "slots", torch.int64, tokens),
+        _check_vector(positions, "positions", torch.int32, tokens), _check_vector(row_ids, "rows", torch.int32, tokens),
+        _stream_handle(stream))
+    if status:
+        _lib.check(status, "slot_map_i32")
     return starts, slots, positions, row_ids
 
 
@@ -420,21 +425,21 @@ def block_table_release(table: torch.Tensor, cached: torch.Tensor, done: torch.T
     table is not changed; the caller sets the ended rows' lengths to 0."""
     stride = _check_table(table, page_size)
     rows, width = table.shape
-    _check_vector(cached, "cached", torch.int32, rows)
-    _check_vector(done, "done", torch.uint8, rows)
-    _check_vector(pages, "pages", torch.int32, pages.numel())
-    _check_vector(free, "free", torch.int32, 1)
+    pool = pages.numel()
     if left is None:
         left = torch.empty(1, dtype=torch.int32, device=table.device)
-    _check_vector(left, "left", torch.int32, 1)
-    _lib.check(load().block_table_release_i32(table.data_ptr(), stride, rows, width, cached.data_ptr(),
-                                              done.data_ptr(), int(page_size), pages.data_ptr(), pages.numel(),
-                                              free.data_ptr(), left.data_ptr(), _stream_handle(stream)),
-               "block_table_release_i32")
+    status = load().block_table_release_i32(
+        table.data_ptr(), stride, rows, width, _check_vector(cached, "cached", torch.int32, rows),
+        _check_vector(done, "done", torch.uint8, rows), int(page_size),
+        _check_vector(pages, "pages", torch.int32, pool), pool, _check_vector(free, "free", torch.int32, 1),
+        _check_vector(left, "left", torch.int32, 1), _stream_handle(stream))
+    if status:
+        _lib.check(status, "block_table_release_i32")
     return left
 
 
-_LOGIT_SUFFIX = {torch.float32: "f32", torch.float16: "f16", torch.bfloat16: "bf16"}
+_SAMPLE_SYMBOL = {torch.float32: "sample_tokens_f32", torch.float16: "sample_tokens_f16",
+                  torch.bfloat16: "sample_tokens_bf16"}
 
 
 def sample_tokens(logits: torch.Tensor, noise: torch.Tensor | None = None, temperature: torch.Tensor | None = None,
@@ -450,8 +455,7 @@ def sample_tokens(logits: torch.Tensor, noise: torch.Tensor | None = None, tempe
     log-probabilities under the truncated distribution."""
     stride = _check_matrix(logits, "logits")
     rows, vocab = logits.shape
-    suffix = _LOGIT_SUFFIX.get(logits.dtype)
-    if suffix is None:
+    if logits.dtype not in _SAMPLE_SYMBOL:
         raise TypeError(f"unsupported dtype {logits.dtype} (float32, float16, bfloat16)")
     noise_stride = vocab
     if noise is not None:
@@ -460,21 +464,20 @@ def sample_tokens(logits: torch.Tensor, noise: torch.Tensor | None = None, tempe
             raise TypeError("noise must be float32")
         if noise.shape != logits.shape:
             raise ValueError("noise must have the logits' shape")
-    for t, name, dtype in ((temperature, "temperature", torch.float32), (top_k, "top_k", torch.int32),
-                           (top_p, "top_p", torch.float32), (min_p, "min_p", torch.float32)):
-        if t is not None:
-            _check_vector(t, name, dtype, rows)
     if out is None:
         out = torch.empty(rows, dtype=torch.int32, device=logits.device)
     if logprobs is None:
         logprobs = torch.empty(rows, dtype=torch.float32, device=logits.device)
-    _check_vector(out, "out", torch.int32, rows)
-    _check_vector(logprobs, "logprobs", torch.float32, rows)
-    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    name = f"sample_tokens_{suffix}"
-    _lib.check(getattr(load(), name)(logits.data_ptr(), rows, vocab, stride, ptr(noise), noise_stride,
-                                     ptr(temperature), ptr(top_k), ptr(top_p), ptr(min_p), out.data_ptr(),
-                                     logprobs.data_ptr(), _stream_handle(stream)), name)
+    f32, i32 = torch.float32, torch.int32
+    status = getattr(load(), _SAMPLE_SYMBOL[logits.dtype])(
+        logits.data_ptr(), rows, vocab, stride, None if noise is None else noise.data_ptr(), noise_stride,
+        None if temperature is None else _check_vector(temperature, "temperature", f32, rows),
+        None if top_k is None else _check_vector(top_k, "top_k", i32, rows),
+        None if top_p is None else _check_vector(top_p, "top_p", f32, rows),
+        None if min_p is None else _check_vector(min_p, "min_p", f32, rows),
+        _check_vector(out, "out", i32, rows), _check_vector(logprobs, "logprobs", f32, rows), _stream_handle(stream))
+    if status:
+        _lib.check(status, _SAMPLE_SYMBOL[logits.dtype])
     return out, logprobs
 
 

@@ -40,6 +40,8 @@ _lib = None
 def load() -> ctypes.CDLL:
     """Load libdevscan.so once and declare every entry point's signature."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

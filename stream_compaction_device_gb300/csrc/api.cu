@@ -269,7 +269,7 @@ devscan_status paged_scratch(size_t rows, cudaStream_t stream, Workspace *ws, in
     const devscan_status st = acquire(stream, 1, ws);
     if (st != DEVSCAN_OK || rows <= static_cast<size_t>(kPagedSharedRows)) return st;
     void *p = nullptr;
-    const devscan_status got = acquire_extra(stream, rows * sizeof(int32_t), &p);
+    const devscan_status got = acquire_extra(stream, 2 * rows * sizeof(int32_t), &p);
     *scratch = static_cast<int32_t *>(p);
     return got;
 }

@@ -158,8 +158,8 @@ size_t radix_hist_words(size_t n);
 
 // Block tables and slot maps.  Up to kPagedSharedRows rows every block scans
 // the row counts into its own shared memory (one launch); above, a first
-// launch leaves the scanned ends in `scratch` (rows words).
-constexpr int kPagedSharedRows = 8192;
+// launch leaves the scanned rows in `scratch` (2 * rows words).
+constexpr int kPagedSharedRows = 4096;
 cudaError_t launch_block_table_extend(int32_t *table, size_t stride, int rows, int width, const int32_t *cached,
                                       const int32_t *fresh, int page, const int32_t *pages, int pool,
                                       const int32_t *free_count, uint8_t *granted, int32_t *left, int32_t *scratch,

@@ -17,7 +17,9 @@
 // Split: the row counts are 4 to 9 bytes each while an output element moves 8
 // to 20, so every block scans all the counts for itself (out of L2, into its
 // shared memory) and takes an equal share of the output: one launch, no block
-// waits for another, and one long row is spread over the whole GPU.
+// waits for another, and one long row is spread over the whole GPU.  A warp
+// takes 256 neighbouring outputs and looks for the rows of the first and the
+// last; the others search between these two, and in a long row not at all.
 // Sums run in 64 bits and are stored saturated to INT32_MAX, so that lengths
 // whose sum passes 32 bits cannot wrap into positions that look valid.
 #include "core.cuh"
@@ -28,92 +30,139 @@ namespace {
 
 constexpr int kPagedThreads = 512;
 constexpr int kPagedWarps = kPagedThreads / 32;
+constexpr int kChunk = 256;   // consecutive outputs that a warp takes at a time
 
-__device__ __forceinline__ long long blocks_of(long long tokens, int page) { return (tokens + page - 1) / page; }
+// Division of any uint32 by the page size, by a multiplication with its
+// reciprocal rounded up to 33 bits (Granlund and Montgomery, "Division by
+// invariant integers using multiplication", 1994, figure 4.1).
+struct Pages {
+    uint32_t page, magic, shift;
+    explicit Pages(uint32_t p) : page(p), magic(0), shift(0)
+    {
+        while ((1ull << shift) < p) ++shift;   // ceil(log2 p)
+        magic = static_cast<uint32_t>(((1ull << 32) * ((1ull << shift) - p)) / p + 1);
+    }
+    __device__ __forceinline__ uint32_t div(uint32_t x) const
+    {
+        const uint32_t t = __umulhi(magic, x);
+        return shift == 0 ? x : (t + ((x - t) >> 1)) >> (shift - 1);
+    }
+    __device__ __forceinline__ uint32_t blocks_of(uint32_t tokens) const
+    {
+        const uint32_t q = div(tokens);
+        return q + (q * page != tokens ? 1u : 0u);
+    }
+};
 
-// Pages that row `r` needs beyond those it has; false for a row that cannot
-// be served whatever the pool holds (negative lengths, or wider than the
-// table).
+// What a row brings: its number of outputs, and the place of its first one
+// (in the row's table entries or tokens).
+struct RowPart {
+    int count, place;
+};
+
+// Pages that a row needs beyond those it has, and how many those are.  A row
+// that cannot be served whatever the pool holds (negative lengths, or wider
+// than the table) needs none; its place is -1.
 struct ExtendCount {
     const int32_t *cached, *fresh;
-    int page, width;
-    __device__ __forceinline__ bool count(int r, int &have, int &need) const
+    Pages pages;
+    int width;
+    __device__ __forceinline__ RowPart operator()(int r) const
     {
-        const long long c = cached[r], n = fresh[r];
-        have = need = 0;
-        if (c < 0 || n < 0) return false;
-        const long long h = blocks_of(c, page), w = blocks_of(c + n, page);
-        if (w > width) return false;
-        have = static_cast<int>(h);
-        need = static_cast<int>(w - h);
-        return true;
-    }
-    __device__ __forceinline__ int operator()(int r) const
-    {
-        int have, need;
-        count(r, have, need);
-        return need;
+        const int c = cached[r], n = fresh[r];
+        if (c < 0 || n < 0) return {0, -1};
+        const uint32_t have = pages.blocks_of(c), want = pages.blocks_of(static_cast<uint32_t>(c) + static_cast<uint32_t>(n));
+        if (want > static_cast<uint32_t>(width)) return {0, -1};
+        return {static_cast<int>(want - have), static_cast<int>(have)};
     }
 };
 
 struct SlotCount {
-    const int32_t *fresh;
+    const int32_t *cached, *fresh;
     const uint8_t *granted;   // null: every row runs
-    __device__ __forceinline__ int operator()(int r) const
+    __device__ __forceinline__ RowPart operator()(int r) const
     {
-        if (granted != nullptr && granted[r] == 0) return 0;
-        const int n = fresh[r];
-        return n > 0 ? n : 0;
+        const int n = granted != nullptr && granted[r] == 0 ? 0 : fresh[r];
+        return {n > 0 ? n : 0, cached[r]};
     }
 };
 
 struct ReleaseCount {
     const int32_t *cached;
     const uint8_t *done;
-    int page, width;
-    __device__ __forceinline__ int operator()(int r) const
+    Pages pages;
+    int width;
+    __device__ __forceinline__ RowPart operator()(int r) const
     {
-        if (done[r] == 0 || cached[r] <= 0) return 0;
-        const long long b = blocks_of(cached[r], page);
-        return static_cast<int>(b < width ? b : width);
+        const int c = cached[r];
+        if (done[r] == 0 || c <= 0) return {0, 0};
+        const uint32_t b = pages.blocks_of(c);
+        return {static_cast<int>(b < static_cast<uint32_t>(width) ? b : static_cast<uint32_t>(width)), 0};
     }
 };
 
-// ends[r] = min(count(0) + ... + count(r), INT32_MAX) for all rows, by one
-// block; ends in shared or global memory.  Ends with a block barrier.
+// The scanned rows: ends[r] = min(count(0) + ... + count(r), INT32_MAX), and
+// places[r] as the row gave it.  In shared memory, or in global scratch.
+struct Ends {
+    int32_t *ends, *places;
+};
+
+// Scans the rows by one block.  Every tile's counts are read before any is
+// summed (one wait for memory), then a thread sums a run of neighbours.  Ends
+// with a block barrier.
 template <class Count>
-__device__ void scan_rows(const Count &count, int rows, int32_t *ends)
+__device__ void scan_rows(const Count &count, int rows, const Ends &out)
 {
+    constexpr int kRun = 8, kTile = kPagedThreads * kRun;
     __shared__ long long s_warp[kPagedWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     long long base = 0;
-    for (int r0 = 0; r0 < rows; r0 += kPagedThreads) {
-        const int r = r0 + tid;
-        long long v = r < rows ? count(r) : 0;
+    for (int r0 = 0; r0 < rows; r0 += kTile) {
+        const int n = rows - r0 < kTile ? rows - r0 : kTile;
+        RowPart part[kRun];
+#pragma unroll
+        for (int k = 0; k < kRun; ++k)
+            if (k * kPagedThreads + tid < n) part[k] = count(r0 + k * kPagedThreads + tid);
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) {
+            if (k * kPagedThreads + tid >= n) continue;
+            out.ends[r0 + k * kPagedThreads + tid] = part[k].count;
+            out.places[r0 + k * kPagedThreads + tid] = part[k].place;
+        }
+        __syncthreads();
+        const int per = (n + kPagedThreads - 1) / kPagedThreads, first = tid * per;
+        long long sum = 0;
+        for (int k = 0; k < per; ++k)
+            if (first + k < n) sum += out.ends[r0 + first + k];
+        long long incl = sum;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const long long u = __shfl_up_sync(kFullMask, v, d);
-            if (lane >= d) v += u;
+            const long long u = __shfl_up_sync(kFullMask, incl, d);
+            if (lane >= d) incl += u;
         }
-        if (lane == 31) s_warp[warp] = v;
+        if (lane == 31) s_warp[warp] = incl;
         __syncthreads();
-        long long ahead = 0, all = 0;
+        long long parts = s_warp[lane & (kPagedWarps - 1)];
 #pragma unroll
-        for (int w = 0; w < kPagedWarps; ++w) {
-            if (w < warp) ahead += s_warp[w];
-            all += s_warp[w];
+        for (int d = 1; d < kPagedWarps; d <<= 1) {
+            const long long u = __shfl_up_sync(kFullMask, parts, d);
+            if ((lane & (kPagedWarps - 1)) >= d) parts += u;
         }
-        const long long end = base + ahead + v;
-        if (r < rows) ends[r] = static_cast<int32_t>(end < INT32_MAX ? end : INT32_MAX);
-        base += all;
+        const long long ahead = __shfl_sync(kFullMask, parts, (warp - 1) & 31);
+        long long end = base + (warp > 0 ? ahead : 0) + incl - sum;
+        for (int k = 0; k < per; ++k) {
+            if (first + k >= n) break;
+            end += out.ends[r0 + first + k];
+            out.ends[r0 + first + k] = static_cast<int32_t>(end < INT32_MAX ? end : INT32_MAX);
+        }
+        base += __shfl_sync(kFullMask, parts, kPagedWarps - 1);
         __syncthreads();
     }
 }
 
-// First row whose end is above g; `rows` if none.
-__device__ __forceinline__ int row_of(const int32_t *ends, int rows, int g)
+// First row in [lo, hi) whose end is above g; hi if none.
+__device__ __forceinline__ int row_of(const int32_t *ends, int lo, int hi, int g)
 {
-    int lo = 0, hi = rows;
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
         if (ends[mid] > g) hi = mid;
@@ -121,22 +170,56 @@ __device__ __forceinline__ int row_of(const int32_t *ends, int rows, int g)
     }
     return lo;
 }
+// The same over [lo, hi) by a whole warp: 32 probes a step.
+__device__ __forceinline__ int warp_row_of(const int32_t *ends, int lo, int hi, int g)
+{
+    const int lane = threadIdx.x & 31;
+    while (lo < hi) {
+        const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+        const unsigned above = __ballot_sync(kFullMask, at >= hi || ends[at] > g);
+        const int k = above == 0 ? 32 : __ffs(above) - 1;   // the first probe above; the one before it is not
+        if (k < 32 && lo + k * step < hi) hi = lo + k * step;
+        if (k > 0) lo = lo + (k - 1) * step + 1;
+    }
+    return lo;
+}
 
 template <class Count>
-__global__ void __launch_bounds__(kPagedThreads) row_ends_kernel(Count count, int rows, int32_t *ends)
+__global__ void __launch_bounds__(kPagedThreads) row_ends_kernel(Count count, int rows, Ends out)
 {
-    scan_rows(count, rows, ends);
+    scan_rows(count, rows, out);
 }
 
 // IN_SHARED: the block scans the counts into its own shared memory; else
-// row_ends_kernel has left the ends in `g_ends`.
+// row_ends_kernel has left them in `scratch`.
 template <bool IN_SHARED, class Count>
-__device__ __forceinline__ const int32_t *row_ends(const Count &count, int rows, const int32_t *g_ends)
+__device__ __forceinline__ Ends row_ends(const Count &count, int rows, const Ends &scratch)
 {
-    extern __shared__ int32_t s_ends[];
-    if (!IN_SHARED) return g_ends;
-    scan_rows(count, rows, s_ends);
-    return s_ends;
+    extern __shared__ int32_t s_rows[];
+    if (!IN_SHARED) return scratch;
+    const Ends e{s_rows, s_rows + rows};
+    scan_rows(count, rows, e);
+    return e;
+}
+
+// f(g, row, index in the row) for the outputs 0 .. total, dealt to the warps
+// of the grid a chunk of neighbours at a time; row == rows past the last one.
+template <class F>
+__device__ __forceinline__ void each_output(const Ends &e, int rows, int total, F f)
+{
+    const int lane = threadIdx.x & 31;
+    const long long warps = static_cast<long long>(gridDim.x) * kPagedWarps;
+    for (long long c = static_cast<long long>(blockIdx.x) * kPagedWarps + (threadIdx.x >> 5); c * kChunk < total;
+         c += warps) {
+        const int g0 = static_cast<int>(c) * kChunk, g1 = total - g0 < kChunk ? total : g0 + kChunk;
+        const int lo = warp_row_of(e.ends, 0, rows, g0);
+        const int hi = lo < rows && e.ends[lo] >= g1 ? lo : warp_row_of(e.ends, lo, rows, g1 - 1);
+#pragma unroll 4
+        for (int g = g0 + lane; g < g1; g += 32) {
+            const int r = lo == hi ? lo : row_of(e.ends, lo, hi, g);
+            f(g, r, g - (r > 0 ? e.ends[r - 1] : 0));
+        }
+    }
 }
 
 __device__ __forceinline__ int clamp_free(const int32_t *free_count, int pool)
@@ -146,98 +229,91 @@ __device__ __forceinline__ int clamp_free(const int32_t *free_count, int pool)
 }
 
 template <bool IN_SHARED>
-__global__ void __launch_bounds__(kPagedThreads)
+__global__ void __launch_bounds__(kPagedThreads, 2)
 extend_kernel(int32_t *__restrict__ table, size_t stride, int rows, ExtendCount count,
               const int32_t *__restrict__ pages, int pool, const int32_t *__restrict__ free_count,
-              uint8_t *__restrict__ granted, int32_t *__restrict__ left, const int32_t *g_ends)
+              uint8_t *__restrict__ granted, int32_t *__restrict__ left, Ends scratch)
 {
-    const int32_t *ends = row_ends<IN_SHARED>(count, rows, g_ends);
     const int free = clamp_free(free_count, pool);
+    const Ends e = row_ends<IN_SHARED>(count, rows, scratch);
     // Rows are served in order while the pool lasts: those whose end is within it.
-    const int served = row_of(ends, rows, free);
-    const int total = served > 0 ? ends[served - 1] : 0;
+    const int served = warp_row_of(e.ends, 0, rows, free);
+    const int total = served > 0 ? e.ends[served - 1] : 0;
     const int tid = blockIdx.x * kPagedThreads + threadIdx.x, threads = gridDim.x * kPagedThreads;
     for (int r = tid; r < rows; r += threads) {
-        int have, need;
-        const bool valid = count.count(r, have, need);
-        granted[r] = valid && (need == 0 || ends[r] <= free);
+        const int end = e.ends[r];
+        const bool needs = end == INT32_MAX ? count(r).count != 0 : end != (r > 0 ? e.ends[r - 1] : 0);
+        granted[r] = e.places[r] >= 0 && (!needs || end <= free);
     }
     if (tid == 0) *left = free - total;
-    for (long long g = tid; g < total; g += threads) {
-        const int r = row_of(ends, rows, static_cast<int>(g));
-        int have, need;
-        count.count(r, have, need);
-        const int j = static_cast<int>(g) - (ends[r] - need);
-        table[static_cast<size_t>(r) * stride + have + j] = pages[free - 1 - static_cast<int>(g)];
-    }
+    each_output(e, rows, total, [&](int g, int r, int j) {
+        table[static_cast<size_t>(r) * stride + e.places[r] + j] = __ldcs(pages + (free - 1 - g));
+    });
 }
 
 template <bool IN_SHARED>
-__global__ void __launch_bounds__(kPagedThreads)
-slot_kernel(const int32_t *__restrict__ table, size_t stride, int rows, int width,
-            const int32_t *__restrict__ cached, SlotCount count, int page, int tokens,
-            int32_t *__restrict__ starts, long long *__restrict__ slots, int32_t *__restrict__ positions,
-            int32_t *__restrict__ row_ids, const int32_t *g_ends)
+__global__ void __launch_bounds__(kPagedThreads, 2)
+slot_kernel(const int32_t *__restrict__ table, size_t stride, int rows, int width, SlotCount count, Pages page,
+            int tokens, int32_t *__restrict__ starts, long long *__restrict__ slots, int32_t *__restrict__ positions,
+            int32_t *__restrict__ row_ids, Ends scratch)
 {
-    const int32_t *ends = row_ends<IN_SHARED>(count, rows, g_ends);
+    const Ends e = row_ends<IN_SHARED>(count, rows, scratch);
     const int tid = blockIdx.x * kPagedThreads + threadIdx.x, threads = gridDim.x * kPagedThreads;
-    for (int r = tid; r < rows; r += threads) starts[r + 1] = ends[r];
+    for (int r = tid; r < rows; r += threads) starts[r + 1] = e.ends[r];
     if (tid == 0) starts[0] = 0;
-    for (long long g = tid; g < tokens; g += threads) {
-        const int r = row_of(ends, rows, static_cast<int>(g));
+    each_output(e, rows, tokens, [&](int g, int r, int j) {
         long long slot = -1;
         int pos = -1, id = -1;
         if (r < rows) {
-            const int first = r > 0 ? ends[r - 1] : 0;
-            const long long at = static_cast<long long>(cached[r]) + (g - first);
+            const long long at = static_cast<long long>(e.places[r]) + j;
             id = r;
-            const bool valid = at >= 0 && at <= INT32_MAX;
-            pos = valid ? static_cast<int>(at) : -1;
-            const long long b = at / page;
-            if (valid && b < width) {
-                const int entry = table[static_cast<size_t>(r) * stride + b];
-                if (entry >= 0) slot = static_cast<long long>(entry) * page + at % page;
+            if (at >= 0 && at <= INT32_MAX) {
+                pos = static_cast<int>(at);
+                const uint32_t b = page.div(pos);
+                if (b < static_cast<uint32_t>(width)) {
+                    const int entry = __ldg(table + static_cast<size_t>(r) * stride + b);
+                    if (entry >= 0) slot = static_cast<long long>(entry) * page.page + (pos - b * page.page);
+                }
             }
         }
-        slots[g] = slot;
-        positions[g] = pos;
-        row_ids[g] = id;
-    }
+        __stcs(slots + g, slot);
+        __stcs(positions + g, pos);
+        __stcs(row_ids + g, id);
+    });
 }
 
 template <bool IN_SHARED>
-__global__ void __launch_bounds__(kPagedThreads)
+__global__ void __launch_bounds__(kPagedThreads, 2)
 release_kernel(const int32_t *__restrict__ table, size_t stride, int rows, ReleaseCount count,
                int32_t *__restrict__ pages, int pool, const int32_t *__restrict__ free_count,
-               int32_t *__restrict__ left, const int32_t *g_ends)
+               int32_t *__restrict__ left, Ends scratch)
 {
-    const int32_t *ends = row_ends<IN_SHARED>(count, rows, g_ends);
     const int free = clamp_free(free_count, pool);
-    const int served = row_of(ends, rows, pool - free);   // rows whose pages fit the pool array
-    const int total = served > 0 ? ends[served - 1] : 0;
-    const int tid = blockIdx.x * kPagedThreads + threadIdx.x, threads = gridDim.x * kPagedThreads;
-    if (tid == 0) *left = free + total;
-    for (long long g = tid; g < total; g += threads) {
-        const int r = row_of(ends, rows, static_cast<int>(g));
-        const int first = r > 0 ? ends[r - 1] : 0;
-        pages[free + static_cast<int>(g)] = table[static_cast<size_t>(r) * stride + (static_cast<int>(g) - first)];
-    }
+    const Ends e = row_ends<IN_SHARED>(count, rows, scratch);
+    const int served = warp_row_of(e.ends, 0, rows, pool - free);   // rows whose pages fit the pool array
+    const int total = served > 0 ? e.ends[served - 1] : 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *left = free + total;
+    each_output(e, rows, total, [&](int g, int r, int j) {
+        pages[free + g] = __ldcs(table + static_cast<size_t>(r) * stride + j);
+    });
 }
 
 // Blocks for `most` output elements at the most.
 unsigned paged_blocks(unsigned long long most, const Workspace &ws)
 {
-    const unsigned long long b = (most + kPagedThreads - 1) / kPagedThreads;
+    const unsigned long long b = (most + kPagedWarps * kChunk - 1) / (kPagedWarps * kChunk);
     const unsigned long long cap = static_cast<unsigned long long>(ws.num_sms) * 2;
     return static_cast<unsigned>(b < 1 ? 1 : (b < cap ? b : cap));
 }
 
+// Where the rows are too many for a block's shared memory, the launch that
+// scans them into `scratch`.
 template <class Count>
-cudaError_t prepare_ends(const Count &count, int rows, int32_t *scratch, size_t *shared_bytes, cudaStream_t s)
+cudaError_t prepare_ends(const Count &count, int rows, const Ends &scratch, size_t *shared_bytes, cudaStream_t s)
 {
     *shared_bytes = 0;
     if (rows <= kPagedSharedRows) {
-        *shared_bytes = static_cast<size_t>(rows) * sizeof(int32_t);
+        *shared_bytes = static_cast<size_t>(rows) * 2 * sizeof(int32_t);
         return cudaSuccess;
     }
     row_ends_kernel<Count><<<1, kPagedThreads, 0, s>>>(count, rows, scratch);
@@ -251,19 +327,20 @@ cudaError_t launch_block_table_extend(int32_t *table, size_t stride, int rows, i
                                       const int32_t *free_count, uint8_t *granted, int32_t *left, int32_t *scratch,
                                       const Workspace &ws, cudaStream_t s)
 {
-    const ExtendCount count{cached, fresh, page, width};
+    const ExtendCount count{cached, fresh, Pages(page), width};
+    const Ends ends{scratch, scratch + rows};
     size_t shared = 0;
-    cudaError_t e = prepare_ends(count, rows, scratch, &shared, s);
+    cudaError_t e = prepare_ends(count, rows, ends, &shared, s);
     if (e != cudaSuccess) return e;
     unsigned long long most = static_cast<unsigned long long>(rows) * width;
     if (most > static_cast<unsigned long long>(pool)) most = pool;
     const unsigned blocks = paged_blocks(most, ws);
     if (rows <= kPagedSharedRows)
         extend_kernel<true><<<blocks, kPagedThreads, shared, s>>>(table, stride, rows, count, pages, pool, free_count,
-                                                                  granted, left, nullptr);
+                                                                  granted, left, ends);
     else
         extend_kernel<false><<<blocks, kPagedThreads, 0, s>>>(table, stride, rows, count, pages, pool, free_count,
-                                                              granted, left, scratch);
+                                                              granted, left, ends);
     return cudaGetLastError();
 }
 
@@ -272,18 +349,19 @@ cudaError_t launch_slot_map(const int32_t *table, size_t stride, int rows, int w
                             int64_t *slots, int32_t *positions, int32_t *row_ids, int32_t *scratch,
                             const Workspace &ws, cudaStream_t s)
 {
-    const SlotCount count{fresh, granted};
+    const SlotCount count{cached, fresh, granted};
+    const Ends ends{scratch, scratch + rows};
     size_t shared = 0;
-    cudaError_t e = prepare_ends(count, rows, scratch, &shared, s);
+    cudaError_t e = prepare_ends(count, rows, ends, &shared, s);
     if (e != cudaSuccess) return e;
     const unsigned blocks = paged_blocks(static_cast<unsigned long long>(tokens), ws);
     long long *out = reinterpret_cast<long long *>(slots);
     if (rows <= kPagedSharedRows)
-        slot_kernel<true><<<blocks, kPagedThreads, shared, s>>>(table, stride, rows, width, cached, count, page,
-                                                                tokens, starts, out, positions, row_ids, nullptr);
+        slot_kernel<true><<<blocks, kPagedThreads, shared, s>>>(table, stride, rows, width, count, Pages(page), tokens,
+                                                                starts, out, positions, row_ids, ends);
     else
-        slot_kernel<false><<<blocks, kPagedThreads, 0, s>>>(table, stride, rows, width, cached, count, page, tokens,
-                                                            starts, out, positions, row_ids, scratch);
+        slot_kernel<false><<<blocks, kPagedThreads, 0, s>>>(table, stride, rows, width, count, Pages(page), tokens,
+                                                            starts, out, positions, row_ids, ends);
     return cudaGetLastError();
 }
 
@@ -292,19 +370,20 @@ cudaError_t launch_block_table_release(const int32_t *table, size_t stride, int 
                                        const int32_t *free_count, int32_t *left, int32_t *scratch,
                                        const Workspace &ws, cudaStream_t s)
 {
-    const ReleaseCount count{cached, done, page, width};
+    const ReleaseCount count{cached, done, Pages(page), width};
+    const Ends ends{scratch, scratch + rows};
     size_t shared = 0;
-    cudaError_t e = prepare_ends(count, rows, scratch, &shared, s);
+    cudaError_t e = prepare_ends(count, rows, ends, &shared, s);
     if (e != cudaSuccess) return e;
     unsigned long long most = static_cast<unsigned long long>(rows) * width;
     if (most > static_cast<unsigned long long>(pool)) most = pool;
     const unsigned blocks = paged_blocks(most, ws);
     if (rows <= kPagedSharedRows)
         release_kernel<true><<<blocks, kPagedThreads, shared, s>>>(table, stride, rows, count, pages, pool,
-                                                                   free_count, left, nullptr);
+                                                                   free_count, left, ends);
     else
         release_kernel<false><<<blocks, kPagedThreads, 0, s>>>(table, stride, rows, count, pages, pool, free_count,
-                                                               left, scratch);
+                                                               left, ends);
     return cudaGetLastError();
 }
 

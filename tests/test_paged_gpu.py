@@ -46,7 +46,7 @@ def batch(rows, width, page, seed, most=None):
 
 
 SHAPES = [(1, 1, 1), (1, 300, 16), (3, 40, 16), (64, 33, 5), (511, 20, 16), (513, 9, 64), (4096, 3, 1), (2000, 70, 24),
-          (8192, 4, 16), (8193, 4, 16), (20001, 3, 7)]
+          (4097, 4, 16), (8192, 4, 16), (8193, 4, 16), (20001, 3, 7)]
 
 
 @pytest.mark.parametrize("rows,width,page", SHAPES)
