@@ -60,6 +60,32 @@ struct RowPart {
     int count, place;
 };
 
+constexpr int kRun = 8;   // neighbouring rows that a thread scans
+
+// v[k] = p[r + k] for the rows before `rows`; 0 for the others.
+__device__ __forceinline__ void load_run(const int32_t *p, int r, int rows, int (&v)[kRun])
+{
+    if (r + kRun <= rows && reinterpret_cast<uintptr_t>(p + r) % 16 == 0) {
+        const int4 a = __ldg(reinterpret_cast<const int4 *>(p + r)), b = __ldg(reinterpret_cast<const int4 *>(p + r) + 1);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) v[k] = r + k < rows ? __ldg(p + r + k) : 0;
+    }
+}
+// The same of flags; null: 1 for every row.
+__device__ __forceinline__ void load_run(const uint8_t *p, int r, int rows, int (&v)[kRun])
+{
+    if (p != nullptr && r + kRun <= rows && reinterpret_cast<uintptr_t>(p + r) % 8 == 0) {
+        const uint2 a = __ldg(reinterpret_cast<const uint2 *>(p + r));
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) v[k] = ((k < 4 ? a.x : a.y) >> (k % 4 * 8)) & 255;
+    } else {
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) v[k] = r + k >= rows ? 0 : p == nullptr ? 1 : __ldg(p + r + k);
+    }
+}
+
 // Pages that a row needs beyond those it has, and how many those are.  A row
 // that cannot be served whatever the pool holds (negative lengths, or wider
 // than the table) needs none; its place is -1.
@@ -67,24 +93,33 @@ struct ExtendCount {
     const int32_t *cached, *fresh;
     Pages pages;
     int width;
-    __device__ __forceinline__ RowPart operator()(int r) const
+    __device__ __forceinline__ void load(int r, int rows, int (&a)[kRun], int (&b)[kRun]) const
     {
-        const int c = cached[r], n = fresh[r];
-        if (c < 0 || n < 0) return {0, -1};
+        load_run(cached, r, rows, a);
+        load_run(fresh, r, rows, b);
+    }
+    __device__ __forceinline__ RowPart part(int c, int n) const
+    {
         const uint32_t have = pages.blocks_of(c), want = pages.blocks_of(static_cast<uint32_t>(c) + static_cast<uint32_t>(n));
-        if (want > static_cast<uint32_t>(width)) return {0, -1};
+        if (c < 0 || n < 0 || want > static_cast<uint32_t>(width)) return {0, -1};
         return {static_cast<int>(want - have), static_cast<int>(have)};
     }
 };
 
+// Tokens of a row, from its length; without a flag it brings none.
 struct SlotCount {
     const int32_t *cached, *fresh;
     const uint8_t *granted;   // null: every row runs
-    __device__ __forceinline__ RowPart operator()(int r) const
+    __device__ __forceinline__ void load(int r, int rows, int (&a)[kRun], int (&b)[kRun]) const
     {
-        const int n = granted != nullptr && granted[r] == 0 ? 0 : fresh[r];
-        return {n > 0 ? n : 0, cached[r]};
+        int runs[kRun];
+        load_run(cached, r, rows, a);
+        load_run(fresh, r, rows, b);
+        load_run(granted, r, rows, runs);
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) b[k] = runs[k] != 0 && b[k] > 0 ? b[k] : 0;
     }
+    __device__ __forceinline__ RowPart part(int c, int n) const { return {n, c}; }
 };
 
 struct ReleaseCount {
@@ -92,11 +127,15 @@ struct ReleaseCount {
     const uint8_t *done;
     Pages pages;
     int width;
-    __device__ __forceinline__ RowPart operator()(int r) const
+    __device__ __forceinline__ void load(int r, int rows, int (&a)[kRun], int (&b)[kRun]) const
     {
-        const int c = cached[r];
-        if (done[r] == 0 || c <= 0) return {0, 0};
+        load_run(cached, r, rows, a);
+        load_run(done, r, rows, b);
+    }
+    __device__ __forceinline__ RowPart part(int c, int ended) const
+    {
         const uint32_t b = pages.blocks_of(c);
+        if (ended == 0 || c <= 0) return {0, 0};
         return {static_cast<int>(b < static_cast<uint32_t>(width) ? b : static_cast<uint32_t>(width)), 0};
     }
 };
@@ -107,42 +146,35 @@ struct Ends {
     int32_t *ends, *places;
 };
 
-// Scans the rows by one block.  Every tile's counts are read before any is
-// summed (one wait for memory), then a thread sums a run of neighbours.  Ends
-// with a block barrier.
+// Scans the rows by one block, a run of neighbours per thread: one wait for
+// memory and one for the other warps in 4,096 rows.  Ends with a block barrier.
 template <class Count>
 __device__ void scan_rows(const Count &count, int rows, const Ends &out)
 {
-    constexpr int kRun = 8, kTile = kPagedThreads * kRun;
-    __shared__ long long s_warp[kPagedWarps];
+    __shared__ long long s_warp[2][kPagedWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     long long base = 0;
-    for (int r0 = 0; r0 < rows; r0 += kTile) {
-        const int n = rows - r0 < kTile ? rows - r0 : kTile;
-        RowPart part[kRun];
-#pragma unroll
-        for (int k = 0; k < kRun; ++k)
-            if (k * kPagedThreads + tid < n) part[k] = count(r0 + k * kPagedThreads + tid);
+    int turn = 0;
+    for (int r0 = 0; r0 < rows; r0 += kPagedThreads * kRun, turn ^= 1) {
+        const int r = r0 + tid * kRun;
+        int a[kRun], b[kRun];
+        long long sum = 0;
+        count.load(r, rows, a, b);
 #pragma unroll
         for (int k = 0; k < kRun; ++k) {
-            if (k * kPagedThreads + tid >= n) continue;
-            out.ends[r0 + k * kPagedThreads + tid] = part[k].count;
-            out.places[r0 + k * kPagedThreads + tid] = part[k].place;
+            const RowPart p = count.part(a[k], b[k]);
+            a[k] = p.count, b[k] = p.place;
+            sum += p.count;
         }
-        __syncthreads();
-        const int per = (n + kPagedThreads - 1) / kPagedThreads, first = tid * per;
-        long long sum = 0;
-        for (int k = 0; k < per; ++k)
-            if (first + k < n) sum += out.ends[r0 + first + k];
         long long incl = sum;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const long long u = __shfl_up_sync(kFullMask, incl, d);
             if (lane >= d) incl += u;
         }
-        if (lane == 31) s_warp[warp] = incl;
+        if (lane == 31) s_warp[turn][warp] = incl;
         __syncthreads();
-        long long parts = s_warp[lane & (kPagedWarps - 1)];
+        long long parts = s_warp[turn][lane & (kPagedWarps - 1)];
 #pragma unroll
         for (int d = 1; d < kPagedWarps; d <<= 1) {
             const long long u = __shfl_up_sync(kFullMask, parts, d);
@@ -150,14 +182,16 @@ __device__ void scan_rows(const Count &count, int rows, const Ends &out)
         }
         const long long ahead = __shfl_sync(kFullMask, parts, (warp - 1) & 31);
         long long end = base + (warp > 0 ? ahead : 0) + incl - sum;
-        for (int k = 0; k < per; ++k) {
-            if (first + k >= n) break;
-            end += out.ends[r0 + first + k];
-            out.ends[r0 + first + k] = static_cast<int32_t>(end < INT32_MAX ? end : INT32_MAX);
-        }
         base += __shfl_sync(kFullMask, parts, kPagedWarps - 1);
-        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) {
+            end += a[k];
+            if (r + k >= rows) continue;
+            out.ends[r + k] = static_cast<int32_t>(end < INT32_MAX ? end : INT32_MAX);
+            out.places[r + k] = b[k];
+        }
     }
+    __syncthreads();
 }
 
 // First row in [lo, hi) whose end is above g; hi if none.
@@ -255,7 +289,8 @@ extend_kernel(int32_t *__restrict__ table, size_t stride, int rows, ExtendCount 
     const int tid = blockIdx.x * kPagedThreads + threadIdx.x, threads = gridDim.x * kPagedThreads;
     for (int r = tid; r < rows; r += threads) {
         const int end = e.ends[r];
-        const bool needs = end == INT32_MAX ? count(r).count != 0 : end != (r > 0 ? e.ends[r - 1] : 0);
+        const bool needs = end == INT32_MAX ? count.part(count.cached[r], count.fresh[r]).count != 0
+                                            : end != (r > 0 ? e.ends[r - 1] : 0);
         granted[r] = e.places[r] >= 0 && (!needs || end <= free);
     }
     if (tid == 0) *left = free - total;

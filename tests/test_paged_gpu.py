@@ -113,6 +113,33 @@ def test_slot_map(ds, rows, width, page, pad):
             assert np.array_equal(g.cpu().numpy(), w)
 
 
+@pytest.mark.parametrize("offset", [0, 1])
+def test_slot_map_of_many_tokens(ds, offset):
+    """A million tokens in rows from none up to thousands, and outputs that do
+    not start on 16 bytes."""
+    rng = np.random.default_rng(77)
+    rows, width, page = 500, 300, 24
+    fresh = rng.integers(0, 4500, rows)
+    fresh[rng.random(rows) < 0.3] = rng.integers(0, 3, (rng.random(rows) < 0.3).sum())[0]
+    cached = rng.integers(0, width * page - 4500, rows)
+    table = rng.permutation(rows * width).reshape(rows, width).astype(np.int32)
+    table[::7, 5] = -1
+    tokens = int(fresh.sum()) + 3
+    assert tokens > 700_000
+    out = [torch.zeros(rows + 1, dtype=torch.int32, device="cuda")] + [
+        torch.zeros(tokens + offset, dtype=d, device="cuda")[offset:] for d in (torch.int64, torch.int32, torch.int32)]
+    ds.slot_map(dev(table), dev(cached), dev(fresh), page, tokens, out=out)
+    starts = np.concatenate([[0], np.cumsum(fresh)])
+    row = np.repeat(np.arange(rows), fresh)
+    pos = cached[row] + np.arange(len(row)) - starts[row]
+    entry = table[row, pos // page].astype(np.int64)
+    pad = np.full(3, -1)
+    assert np.array_equal(out[0].cpu().numpy(), starts)
+    assert np.array_equal(out[1].cpu().numpy(), np.concatenate([np.where(entry < 0, -1, entry * page + pos % page), pad]))
+    assert np.array_equal(out[2].cpu().numpy(), np.concatenate([pos, pad]))
+    assert np.array_equal(out[3].cpu().numpy(), np.concatenate([row, pad]))
+
+
 def test_slots_past_32_bits(ds):
     """Pages whose slots pass 2^31 and 2^32, and lengths whose sums do."""
     table = np.array([[2**31 - 1, 2**30], [7, -1]], np.int32)
