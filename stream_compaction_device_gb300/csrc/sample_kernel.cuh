@@ -57,7 +57,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kGroup = 4;                  // chunks that a thread loads at once: an entry of the index
-constexpr int kQueue = 64;                 // index entries that a warp has waiting
+constexpr int kQueue = 64;                 // entries that a warp has waiting
 constexpr unsigned kLeastChunks = 512;     // of a block's slice, where rows are few
 constexpr int kList = 1024;                // tokens the short list holds
 constexpr int kBins = 1024;
@@ -222,7 +222,7 @@ struct Shared {
 };
 // Keys that block 0's inbox has room for: a wide cluster's blocks do not all
 // bring the same number.
-__host__ __device__ constexpr unsigned inbox_keys(unsigned blocks) { return blocks == 1 ? kList : 2 * kList; }
+__host__ __device__ constexpr unsigned inbox_keys(unsigned blocks) { return blocks == 1 ? kList + 32 : 2 * kList; }
 constexpr size_t kSharedBytes = (sizeof(Shared) + 127) / 128 * 128;
 
 // The race among the kept tokens that a thread has seen, and their weights'
@@ -381,41 +381,52 @@ struct Draw {
         return most;
     }
 
+    // A warp's queue: lanes put numbers in, and whenever 32 wait, or at the end
+    // (`all`), each lane takes one and calls f(number).
+    template <class F>
+    __device__ __forceinline__ void queue_up(unsigned &waiting, bool in, unsigned number, bool all, F f)
+    {
+        uint16_t *queue = s.queue[warp];
+        const unsigned some = __ballot_sync(kFullMask, in);
+        if (in) queue[waiting + __popc(some & ((1u << lane) - 1))] = static_cast<uint16_t>(number);
+        waiting += __popc(some);
+        if (waiting < 32 && !(all && waiting > 0)) return;
+        __syncwarp();
+        const unsigned taken = min(waiting, 32u);
+        const unsigned at = lane < taken ? queue[lane] : 0, moved = lane + 32 < waiting ? queue[lane + 32] : 0;
+        __syncwarp();
+        if (lane + 32 < waiting) queue[lane] = static_cast<uint16_t>(moved);
+        waiting -= taken;
+        if (lane < taken) f(at);
+        __syncwarp();
+    }
+
     // f(values, c) for every chunk c of the slice with a value of at least
-    // `low`.  From the kept slice, each thread its own chunks; else a warp
-    // queues the index entries that reach `low` and reads 32 groups at a time,
-    // one per lane.
+    // `low`, where these are few: they are queued, a chunk of the kept slice or
+    // an entry of the index at a time.
     template <class F>
     __device__ __forceinline__ void each_chunk(float low, F f)
     {
-        if constexpr (KEEP) {
+        constexpr unsigned kStep = KEEP ? kThreads : kGroup * kThreads;   // chunks to a round of entries
+        unsigned waiting = 0;
+        const unsigned rounds = (mine + kStep - 1) / kStep;
 #pragma unroll 1
-            for (unsigned c = tid; c < mine; c += kThreads) visit(kept[c], low, c, f);
-        } else {
-            uint16_t *queue = s.queue[warp];
-            unsigned waiting = 0;
-            const unsigned entries = (mine + kGroup * kThreads - 1) / (kGroup * kThreads);
-#pragma unroll 1
-            for (unsigned k = 0; k <= entries; ++k) {
-                if (k < entries) {
-                    // A thread's group is there if its first chunk is.
-                    const bool in = tid + k * kGroup * kThreads < mine && index[k * kThreads + tid] >= low;
-                    const unsigned some = __ballot_sync(kFullMask, in);
-                    if (in) queue[waiting + __popc(some & ((1u << lane) - 1))] = static_cast<uint16_t>(k * 32 + lane);
-                    waiting += __popc(some);
-                    if (waiting < 32) continue;
-                } else if (waiting == 0) {
-                    return;
+        for (unsigned k = 0; k <= rounds; ++k) {
+            bool in = k < rounds && tid + k * kStep < mine;   // an entry is there if its first chunk is
+            if (KEEP) {
+                if (in) {
+                    uint32_t q[4];
+                    unpack(kept[tid + k * kStep], q);
+                    in = C::most(q, -inf()) >= low;
                 }
-                __syncwarp();
-                const unsigned taken = min(waiting, 32u);
-                const unsigned at = lane < taken ? queue[lane] : 0;
-                const unsigned moved = lane + 32 < waiting ? queue[lane + 32] : 0;
-                __syncwarp();
-                if (lane + 32 < waiting) queue[lane] = static_cast<uint16_t>(moved);
-                waiting -= taken;
-                if (lane < taken) {
-                    const unsigned c = (at / 32) * kGroup * kThreads + warp * 32 + at % 32;
+            } else {
+                in = in && index[k * kThreads + tid] >= low;
+            }
+            queue_up(waiting, in, k * 32 + lane, k == rounds, [&](unsigned at) {
+                const unsigned c = (at / 32) * kStep + warp * 32 + at % 32;
+                if (KEEP) {
+                    visit(kept[c], low, c, f);
+                } else {
                     uint4 v[kGroup];
 #pragma unroll
                     for (int u = 0; u < kGroup; ++u) v[u] = fetch(c + u * kThreads);
@@ -426,12 +437,19 @@ struct Draw {
                         for (int k2 = 1; k2 < kGroup; ++k2) v[k2 - 1] = v[k2];
                     }
                 }
-                __syncwarp();
-            }
+            });
         }
     }
+    // The same where they are most of a kept slice: every thread its own, in
+    // the order of their indices.
     template <class F>
-    __device__ __forceinline__ void visit(const uint4 &v, float low, unsigned c, F &f)
+    __device__ __forceinline__ void each_own_chunk(float low, F f)
+    {
+#pragma unroll 1
+        for (unsigned c = tid; c < mine; c += kThreads) visit(kept[c], low, c, f);
+    }
+    template <class F>
+    __device__ __forceinline__ void visit(const uint4 &v, float low, unsigned c, F &&f)
     {
         uint32_t q[4];
         unpack(v, q);
@@ -535,8 +553,9 @@ struct Draw {
     }
 
     // The race of a chunk's tokens for which keep(value, index) holds and
-    // whose weight is at least m.
-    template <class Keep>
+    // whose weight is at least m.  RISING: this thread's indices rise, so the
+    // first of equal scores stays.
+    template <bool RISING, class Keep>
     __device__ __forceinline__ void race_chunk(const float (&x)[kEach], unsigned c, bool aligned, float m, Keep keep,
                                                Race &o) const
     {
@@ -546,19 +565,29 @@ struct Draw {
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
             w[e] = weight(x[e]);
-            if (!(keep(x[e], i + e) && w[e] >= m)) w[e] = -1.0f;
-            some |= w[e] >= 0.0f;
+            const bool in = keep(x[e], i + e) & (w[e] >= m);
+            w[e] = in ? w[e] : -1.0f;   // its score is below every other's
+            some |= in;
         }
         if (!some) return;
         load_noise(c, aligned, n);
 #pragma unroll
-        for (int e = 0; e < kEach; ++e)
-            if (w[e] >= 0.0f) o.offer(w[e], n[e], i + e);
+        for (int e = 0; e < kEach; ++e) {
+            const float sc = w[e] < 0.0f ? -1.0f : __fdividef(w[e], n[e]);
+            if (RISING) {
+                o.at = sc > o.score ? i + e : o.at;
+                o.score = sc > o.score ? sc : o.score;
+            } else if (sc >= o.score && (sc > o.score || i + e < o.at)) {
+                o.score = sc, o.at = i + e;
+            }
+            o.tops += w[e] == 1.0f ? 1u : 0u;
+            o.rest += w[e] == 1.0f ? 0.0f : fmaxf(w[e], 0.0f);
+        }
     }
     // Starts the noise of the chunks with a value of at least `low` towards L2.
     __device__ __forceinline__ void prefetch_noise(float low)
     {
-        each_chunk(low, [&](const float (&)[kEach], unsigned c) {
+        each_own_chunk(low, [&](const float (&)[kEach], unsigned c) {
             asm volatile("prefetch.global.L2 [%0];" ::"l"(noise + max(index_at(c), 0)));
         });
     }
@@ -770,37 +799,42 @@ struct Draw {
     // One histogram level: adds what each value holds, then finds the bin
     // where the running total from bin 0 reaches want = wanted(total).  Returns
     // false if it does not; else `bin`, and `want` less what is in the bins
-    // before it.  The last bin, in which most of a peaked row may fall, is
-    // summed in registers: its atomics would wait for one another.
+    // before it.  The last bin of counts, in which most of a peaked row may
+    // fall, is summed in registers: its atomics would wait for one another.
     template <bool MASS, class Bin, class Want>
     __device__ __forceinline__ bool histogram(float low, Bin bin_in, Want wanted, u64 &want, uint32_t &bin)
     {
         reinterpret_cast<uint4 *>(count)[tid] = make_uint4(0, 0, 0, 0);
         reinterpret_cast<uint4 *>(carry)[tid] = make_uint4(0, 0, 0, 0);
         __syncthreads();
-        u64 last = 0;
-        each_chunk(low, [&](const float (&x)[kEach], unsigned c) {
-            // All of a chunk's atomics are in flight before the first carry is
-            // looked at.
-            int b[kEach];
-            uint32_t holds[kEach], old[kEach];
+        uint32_t last = 0;
+        each_own_chunk(low, [&](const float (&x)[kEach], unsigned c) {
+            // Nothing branches before the chunk's atomics are all in flight: a
+            // value that takes no part adds 0 to a word of its lane's own.
+            uint32_t *at[kEach], holds[kEach], old[kEach], carried = 0;
 #pragma unroll
             for (int e = 0; e < kEach; ++e) {
-                b[e] = bin_in(x[e], index_at(c) + e);
-                holds[e] = b[e] < 0 ? 0 : MASS ? mass(x[e]) : 1;
-                if (b[e] == kBins - 1) last += holds[e], holds[e] = 0;
+                const int b = bin_in(x[e], index_at(c) + e);
+                const bool in = b >= 0 & (MASS | b != kBins - 1);
+                last += !MASS & b == kBins - 1 ? 1u : 0u;
+                at[e] = count + (in ? b : kBins + static_cast<int>(lane));
+                holds[e] = in ? (MASS ? mass(x[e]) : 1u) : 0u;
             }
 #pragma unroll
-            for (int e = 0; e < kEach; ++e) old[e] = holds[e] != 0 ? shared_add(&count[b[e]], holds[e]) : 0;
+            for (int e = 0; e < kEach; ++e) old[e] = shared_add(at[e], holds[e]);
             if (MASS) {
 #pragma unroll
-                for (int e = 0; e < kEach; ++e)
-                    if (old[e] + holds[e] < old[e]) shared_add(&carry[b[e]], 1);
+                for (int e = 0; e < kEach; ++e) carried |= old[e] + holds[e] < old[e] ? 1u << e : 0u;
+                if (carried != 0) {
+#pragma unroll
+                    for (int e = 0; e < kEach; ++e)
+                        if (carried >> e & 1) shared_add(at[e] + (kBins + 32), 1);
+                }
             }
         });
-        if (last != 0) {
-            const uint32_t low32 = static_cast<uint32_t>(last), old = shared_add(&count[kBins - 1], low32);
-            shared_add(&carry[kBins - 1], static_cast<uint32_t>(last >> 32) + (old + low32 < old ? 1u : 0u));
+        if (!MASS) {
+            last = __reduce_add_sync(kFullMask, last);
+            if (lane == 0 && last != 0) shared_add(&count[kBins - 1], last);
         }
         meet();
         // Thread t sums the four bins from 4 t on, of all blocks.
@@ -857,7 +891,7 @@ struct Draw {
             : v(key == 0 ? -FLT_MAX : unordered(ord_of(key))), i(key == 0 ? 0x7fffffff : static_cast<int>(index_of(key)))
         {
         }
-        __device__ __forceinline__ bool takes(float x, int at) const { return x > v || (x == v && at <= i); }
+        __device__ __forceinline__ bool takes(float x, int at) const { return x > v | (x == v & at <= i); }
     };
 
     // The range of ordered bits of the first histogram's bin where the cut
@@ -870,8 +904,8 @@ struct Draw {
         const float span = MASS ? kMassSpan * t : kCountSpan;
         bins_per_unit = fmaxf((kBins - 1) / span, 1e-30f);
         const float least = MASS ? fmaxf(floor.v, top - span) : floor.v;
-        if (!histogram<MASS>(least, [&](float v, int i) { return floor.takes(v, i) ? bin_of(v) : -1; }, wanted, want,
-                             bin))
+        if (!histogram<MASS>(least, [&](float v, int i) { return floor.takes(v, i) & v >= least ? bin_of(v) : -1; },
+                             wanted, want, bin))
             return false;
         if (warp < 2) {   // bin -1 would begin above the largest
             const uint32_t o = bin < warp ? ordered(top) + 1 : edge(static_cast<int>(bin - warp));
@@ -915,8 +949,8 @@ struct Draw {
             const float v_lo = unordered(lo_bits), v_hi = unordered(hi_bits);
             const bool tie = lo_bits == hi_bits;
             const auto inside = [&](float v, int i) {
-                return v >= v_lo && v <= v_hi && floor.takes(v, i) &&
-                       (!tie || (static_cast<unsigned>(i) >= i_lo && static_cast<unsigned>(i) <= i_hi));
+                return v >= v_lo & v <= v_hi & floor.takes(v, i) &
+                       (!tie | (static_cast<unsigned>(i) >= i_lo & static_cast<unsigned>(i) <= i_hi));
             };
             begin_list();
             each_chunk(v_lo, [&](const float (&x)[kEach], unsigned c) {
@@ -977,14 +1011,29 @@ struct Draw {
         prefetch_noise(low);
         begin_list();
         const bool aligned = reinterpret_cast<uintptr_t>(noise + first) % 16 == 0;
-        each_chunk(low, [&](const float (&x)[kEach], unsigned c) {
+        unsigned waiting = 0;
+        const unsigned rounds = (mine + kThreads - 1) / kThreads;
+        const auto listed = [&](const float (&x)[kEach], unsigned c) {
             uint32_t which = 0;
 #pragma unroll
             for (int e = 0; e < kEach; ++e)
-                which |= x[e] >= v_lo && x[e] <= v_hi && floor.takes(x[e], index_at(c) + e) ? 1u << e : 0u;
-            add_tokens(x, c, which);
-            race_chunk(x, c, aligned, m, [&](float v, int) { return v > v_hi; }, o);
-        });
+                which |= x[e] >= v_lo & x[e] <= v_hi & floor.takes(x[e], index_at(c) + e) ? 1u << e : 0u;
+            return which;
+        };
+#pragma unroll 1
+        for (unsigned k = 0; k <= rounds; ++k) {
+            const unsigned c = k * kThreads + tid;
+            bool some = false;
+            if (c < mine && k < rounds)
+                visit(kept[c], low, c, [&](const float (&x)[kEach], unsigned) {
+                    race_chunk<true>(x, c, aligned, m, [&](float v, int) { return v > v_hi; }, o);
+                    some = listed(x, c) != 0;
+                });
+            queue_up(waiting, some, k * 32 + lane, k == rounds, [&](unsigned at) {
+                const unsigned from = (at / 32) * kThreads + warp * 32 + at % 32;
+                visit(kept[from], low, from, [&](const float (&x)[kEach], unsigned) { add_tokens(x, from, listed(x, from)); });
+            });
+        }
         const uint32_t n = merge_lists(nullptr);
         if (n > kList) {
             o = Race();
@@ -1203,7 +1252,7 @@ __device__ __forceinline__ void draw_row(Draw<T, HISTOGRAMS> &d, unsigned r, con
     const float least = fmaxf(last_kept.v, d.top + 1.001f * off - 1e-5f * t - fabsf(d.top) * 4e-7f);
     const bool aligned = reinterpret_cast<uintptr_t>(d.noise + d.first) % 16 == 0;
     d.each_chunk(fmaxf(least, -FLT_MAX), [&](const float (&x)[D::kEach], unsigned c) {
-        d.race_chunk(x, c, aligned, m, [&](float v, int i) { return last_kept.takes(v, i); }, race);
+        d.template race_chunk<false>(x, c, aligned, m, [&](float v, int i) { return last_kept.takes(v, i); }, race);
     });
     d.template finish<true>(race, token, logprob);
 }
@@ -1227,8 +1276,8 @@ sample_kernel(const SampleCall call, unsigned per, const Deferred later)
     d.rank = cluster_rank(), d.blocks = cluster_blocks(), d.vocab = call.vocab;
     d.inbox = reinterpret_cast<u64 *>(s_bytes + kSharedBytes);
     d.count = reinterpret_cast<uint32_t *>(d.inbox);
-    d.carry = d.count + kBins;
-    d.region = inbox_keys(d.blocks) / d.blocks;
+    d.carry = d.count + kBins + 32;
+    d.region = d.blocks == 1 ? kList : inbox_keys(d.blocks) / d.blocks;
     d.kept = reinterpret_cast<uint4 *>(d.inbox + inbox_keys(d.blocks));
     d.index = reinterpret_cast<float *>(d.kept);
     if (d.blocks > 1) d.meet();   // the blocks' shared memory is there
