@@ -106,16 +106,12 @@ __device__ __forceinline__ void put(u64 *p, unsigned rank, u64 v)
 {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(remote(p, rank)), "l"(v) : "memory");
 }
-__device__ __forceinline__ uint4 get(const uint32_t *p, unsigned rank)   // four words, 16-byte aligned
+__device__ __forceinline__ void put(uint4 *p, unsigned rank, const uint4 &v)
 {
-    uint4 v;
-    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(remote(p, rank))
+    asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(remote(p, rank)), "r"(v.x), "r"(v.y),
+                 "r"(v.z), "r"(v.w)
                  : "memory");
-    return v;
 }
-
 __device__ __forceinline__ uint32_t shared_add(uint32_t *p, uint32_t v)
 {
     uint32_t old;
@@ -214,15 +210,20 @@ struct Shared {
     u64 won[kMaxCluster];
     float rest[kMaxCluster];
     uint32_t tops[kMaxCluster];
-    u64 cut;
+    u64 mass[kMaxCluster];           // of their parts of a histogram
+    u64 cut, pick_want;
+    uint32_t pick_bin;
     // Results of one block's scans.
-    u64 pick_before;
-    uint32_t pick_bin, pick_edge[2];
+    u64 pick_key;
+    uint32_t pick_edge[2];
     uint32_t listed;                 // tokens collected by this block (counting stops above its region)
 };
 // Keys that block 0's inbox has room for: a wide cluster's blocks do not all
 // bring the same number.
-__host__ __device__ constexpr unsigned inbox_keys(unsigned blocks) { return blocks == 1 ? kList + 32 : 2 * kList; }
+template <bool KEEP>
+__host__ __device__ constexpr unsigned inbox_keys(unsigned blocks) { return blocks == 1 && !KEEP ? kList : 2 * kList; }
+// Words of the histogram's parts that the blocks send each other.
+template <bool KEEP> constexpr unsigned kPartWords = KEEP ? 2 * kBins : 0;
 constexpr size_t kSharedBytes = (sizeof(Shared) + 127) / 128 * 128;
 
 // The race among the kept tokens that a thread has seen, and their weights'
@@ -261,6 +262,7 @@ struct Draw {
     u64 *inbox;                      // in block 0: the cluster's tokens, a region of `region` per block
     uint32_t *count, *carry;         // a histogram in the same memory: counts, or the masses' low words;
                                      // the masses' high words
+    uint32_t *low_parts, *high_parts;   // every block's part of the bins that are this block's to sum
     uint32_t region;
     uint4 *kept;                     // with KEEP the slice
     float *index;                    // else the maxima of its groups of chunks
@@ -412,16 +414,9 @@ struct Draw {
         const unsigned rounds = (mine + kStep - 1) / kStep;
 #pragma unroll 1
         for (unsigned k = 0; k <= rounds; ++k) {
-            bool in = k < rounds && tid + k * kStep < mine;   // an entry is there if its first chunk is
-            if (KEEP) {
-                if (in) {
-                    uint32_t q[4];
-                    unpack(kept[tid + k * kStep], q);
-                    in = C::most(q, -inf()) >= low;
-                }
-            } else {
-                in = in && index[k * kThreads + tid] >= low;
-            }
+            // An entry of the index is there if its first chunk is.
+            const bool in = k < rounds && tid + k * kStep < mine &&
+                            (KEEP ? reaches(tid + k * kStep, low) : index[k * kThreads + tid] >= low);
             queue_up(waiting, in, k * 32 + lane, k == rounds, [&](unsigned at) {
                 const unsigned c = (at / 32) * kStep + warp * 32 + at % 32;
                 if (KEEP) {
@@ -439,6 +434,15 @@ struct Draw {
                 }
             });
         }
+    }
+    // Whether chunk c of the kept slice has a value of at least `low`.
+    __device__ __forceinline__ bool reaches(unsigned c, float low) const
+    {
+        if (c >= mine) return false;
+        uint32_t q[4];
+        unpack(kept[c], q);
+        if (infinite) only_infinite(q);
+        return C::most(q, -inf()) >= low;
     }
     // The same where they are most of a kept slice: every thread its own, in
     // the order of their indices.
@@ -556,32 +560,23 @@ struct Draw {
     // whose weight is at least m.  RISING: this thread's indices rise, so the
     // first of equal scores stays.
     template <bool RISING, class Keep>
-    __device__ __forceinline__ void race_chunk(const float (&x)[kEach], unsigned c, bool aligned, float m, Keep keep,
-                                               Race &o) const
+    __device__ __forceinline__ void race_chunk(const float (&x)[kEach], const float (&n)[kEach], unsigned c, float m,
+                                               Keep keep, Race &o) const
     {
         const int i = index_at(c);
-        float w[kEach], n[kEach];
-        bool some = false;
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
-            w[e] = weight(x[e]);
-            const bool in = keep(x[e], i + e) & (w[e] >= m);
-            w[e] = in ? w[e] : -1.0f;   // its score is below every other's
-            some |= in;
-        }
-        if (!some) return;
-        load_noise(c, aligned, n);
-#pragma unroll
-        for (int e = 0; e < kEach; ++e) {
-            const float sc = w[e] < 0.0f ? -1.0f : __fdividef(w[e], n[e]);
+            float w = weight(x[e]);
+            w = keep(x[e], i + e) & (w >= m) ? w : -1.0f;   // its score is below every other's
+            const float sc = w < 0.0f ? -1.0f : __fdividef(w, n[e]);
             if (RISING) {
                 o.at = sc > o.score ? i + e : o.at;
                 o.score = sc > o.score ? sc : o.score;
             } else if (sc >= o.score && (sc > o.score || i + e < o.at)) {
                 o.score = sc, o.at = i + e;
             }
-            o.tops += w[e] == 1.0f ? 1u : 0u;
-            o.rest += w[e] == 1.0f ? 0.0f : fmaxf(w[e], 0.0f);
+            o.tops += w == 1.0f ? 1u : 0u;
+            o.rest += w == 1.0f ? 0.0f : fmaxf(w, 0.0f);
         }
     }
     // Starts the noise of the chunks with a value of at least `low` towards L2.
@@ -733,33 +728,33 @@ struct Draw {
     }
 
     // Puts the n <= kList merged tokens in descending order, by block 0, and
-    // returns them.  A counting sort in bins of equal width from the largest
-    // down to the least (by value, then by index, so that ties fill their range
+    // returns them; their ordered bits are in least .. most.  A counting sort in
+    // bins of equal width from the largest down to the least (by value, then by index, so that ties fill their range
     // evenly too), then by key inside a bin, where there are one or two as a
     // rule: a fixed number of barriers, where a sort by comparisons took two to
     // three times as long.
-    __device__ __forceinline__ const u64 *sort(uint32_t n)
+    __device__ __forceinline__ const u64 *sort(uint32_t n, uint32_t most, uint32_t least)
     {
         u64 *from = blocks == 1 ? inbox : s.list, *to = blocks == 1 ? s.list : inbox;
-        uint32_t most = 0, least = ~0u;
-#pragma unroll 1
-        for (uint32_t k = tid; k < n; k += kThreads) {
-            most = max(most, ord_of(from[k]));
-            least = min(least, ord_of(from[k]));
-        }
-        most = __reduce_max_sync(kFullMask, most);
-        least = __reduce_min_sync(kFullMask, least);
-        if (lane == 0) s.warp_a[warp] = most, s.warp_b[warp] = least;
         static_assert(kBins == 4 * kThreads, "a thread's bins are one 16-byte access");
         reinterpret_cast<uint4 *>(s.bins)[tid] = make_uint4(0, 0, 0, 0);
+        if (least <= ordered(-FLT_MAX)) {   // no bound: the least token's
+            least = most;
+#pragma unroll 1
+            for (uint32_t k = tid; k < n; k += kThreads) least = min(least, ord_of(from[k]));
+            least = __reduce_min_sync(kFullMask, least);
+            if (lane == 0) s.warp_b[warp] = least;
+            __syncthreads();
+            least = __reduce_min_sync(kFullMask, s.warp_b[lane & (kWarps - 1)]);
+        }
         __syncthreads();
-        most = __reduce_max_sync(kFullMask, s.warp_a[lane & (kWarps - 1)]);
-        least = __reduce_min_sync(kFullMask, s.warp_b[lane & (kWarps - 1)]);
-        const u64 high = static_cast<u64>(most >> C::kSpare) * vocab + vocab - 1;
-        const float scaled = kBins / static_cast<float>(high - static_cast<u64>(least >> C::kSpare) * vocab + 1);
+        // Steps of value below the largest, and the index as a fraction of one:
+        // rounded, but never out of order.
+        const float step = 1.0f / static_cast<float>(vocab);
+        const float scaled = kBins / (static_cast<float>((most >> C::kSpare) - (least >> C::kSpare)) + 1.0f);
         const auto bin_of_key = [&](u64 key) {
-            const u64 at = static_cast<u64>(ord_of(key) >> C::kSpare) * vocab + (vocab - 1 - index_of(key));
-            return min(static_cast<uint32_t>(static_cast<float>(high - at) * scaled), kBins - 1u);
+            const float below = static_cast<float>((most >> C::kSpare) - (ord_of(key) >> C::kSpare));
+            return min(static_cast<uint32_t>(fmaf(static_cast<float>(index_of(key)), step, below) * scaled), kBins - 1u);
         };
 #pragma unroll 1
         for (uint32_t k = tid; k < n; k += kThreads) shared_add(&s.bins[bin_of_key(from[k])], 1);
@@ -836,30 +831,58 @@ struct Draw {
             last = __reduce_add_sync(kFullMask, last);
             if (lane == 0 && last != 0) shared_add(&count[kBins - 1], last);
         }
+        __syncthreads();
+        // Every block sums an equal part of the bins.  The others send it
+        // theirs before the barrier: stores that nobody waits for, where reading each other's counts took 8,000 cycles.
+        const uint4 low4 = reinterpret_cast<uint4 *>(count)[tid], high4 = reinterpret_cast<uint4 *>(carry)[tid];
+        const unsigned part = kBins / blocks, owner = 4 * tid / part, at = rank * part + 4 * tid % part;
+        put(reinterpret_cast<uint4 *>(low_parts + at), owner, low4);
+        put(reinterpret_cast<uint4 *>(high_parts + at), owner, high4);
         meet();
-        // Thread t sums the four bins from 4 t on, of all blocks.
-        u64 h[4] = {0, 0, 0, 0};
-#pragma unroll 2
-        for (unsigned r = 0; r < blocks; ++r) {
-            const uint4 low4 = get(count + 4 * tid, r), high4 = get(carry + 4 * tid, r);
-            h[0] += low4.x | static_cast<u64>(high4.x) << 32, h[1] += low4.y | static_cast<u64>(high4.y) << 32;
-            h[2] += low4.z | static_cast<u64>(high4.z) << 32, h[3] += low4.w | static_cast<u64>(high4.w) << 32;
+        // Thread t sums the part's bins from per * t on.
+        const unsigned per = (part + kThreads - 1) / kThreads;
+        u64 h[kBins / kThreads], own = 0;
+#pragma unroll
+        for (unsigned k = 0; k < kBins / kThreads; ++k) {
+            h[k] = 0;
+            if (k < per && per * tid + k < part) {
+#pragma unroll 1
+                for (unsigned r = 0; r < blocks; ++r) {
+                    const unsigned b = r * part + per * tid + k;
+                    h[k] += low_parts[b] | static_cast<u64>(high_parts[b]) << 32;
+                }
+            }
+            own += h[k];
         }
         u64 all = 0;
-        u64 before = block_scan(h[0] + h[1] + h[2] + h[3], s.warp64, &all);
+        u64 before = block_scan(own, s.warp64, &all);
+        if (blocks > 1) {
+            if (tid < blocks) put(&s.mass[rank], tid, all);
+            meet();
+            const unsigned r0 = rank;
+            all = 0;
+#pragma unroll 1
+            for (unsigned r = 0; r < blocks; ++r) {
+                if (r == r0) before += all;
+                all += s.mass[r];
+            }
+        }
         want = wanted(all);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (unsigned k = 0; k < kBins / kThreads; ++k) {
             if (before < want && want <= before + h[k]) {
-                s.pick_bin = 4 * tid + k;
-                s.pick_before = before;
+#pragma unroll 1
+                for (unsigned r = 0; r < blocks; ++r) {
+                    put(&s.pick_bin, r, rank * part + per * tid + k);
+                    put(&s.pick_want, r, want - before);
+                }
             }
             before += h[k];
         }
         meet();   // the histogram's memory is used again from here
         if (all < want) return false;
         bin = s.pick_bin;
-        want -= s.pick_before;
+        want = s.pick_want;
         return true;
     }
 
@@ -918,11 +941,11 @@ struct Draw {
 
     // Block 0 puts the n merged tokens in order, of which the first that hold
     // `want` are kept, calls kept(key) for each of those, and leaves the last
-    // one's key in s.pick_before.
+    // one's key in s.pick_key.
     template <bool MASS, class Kept>
-    __device__ __forceinline__ void resolve(uint32_t n, u64 want, Kept keep)
+    __device__ __forceinline__ void resolve(uint32_t n, uint32_t hi_bits, uint32_t lo_bits, u64 want, Kept keep)
     {
-        const u64 *sorted = sort(n);
+        const u64 *sorted = sort(n, hi_bits, lo_bits);
         u64 base = 0;
 #pragma unroll 1
         for (uint32_t k0 = 0; k0 < n; k0 += kThreads) {
@@ -932,7 +955,7 @@ struct Draw {
                 holds = MASS ? mass(unordered(ord_of(key))) : 1;
             }
             const u64 ahead = base + block_scan(holds, s.warp64, &all);
-            if (ahead < want && want <= ahead + holds) s.pick_before = key;
+            if (ahead < want && want <= ahead + holds) s.pick_key = key;
             if (ahead < want && key != 0) keep(key);
             base += all;
         }
@@ -962,8 +985,8 @@ struct Draw {
             const uint32_t n = merge_lists(nullptr);
             if (n <= kList) {
                 if (rank == 0) {
-                    resolve<MASS>(n, want, [](u64) {});
-                    if (tid < blocks) put(&s.cut, tid, s.pick_before);
+                    resolve<MASS>(n, hi_bits, lo_bits, want, [](u64) {});
+                    if (tid < blocks) put(&s.cut, tid, s.pick_key);
                 }
                 meet();
                 return s.cut;
@@ -1020,28 +1043,38 @@ struct Draw {
                 which |= x[e] >= v_lo & x[e] <= v_hi & floor.takes(x[e], index_at(c) + e) ? 1u << e : 0u;
             return which;
         };
+        // A chunk's noise is on its way while the chunk before it races.
+        bool in = reaches(tid, low);
+        float n[kEach];
+        if (in) load_noise(tid, aligned, n);
 #pragma unroll 1
         for (unsigned k = 0; k <= rounds; ++k) {
-            const unsigned c = k * kThreads + tid;
+            const unsigned c = k * kThreads + tid, then = c + kThreads;
+            const bool in_then = reaches(then, low);
+            float n_then[kEach];
+            if (in_then) load_noise(then, aligned, n_then);
             bool some = false;
-            if (c < mine && k < rounds)
+            if (in)
                 visit(kept[c], low, c, [&](const float (&x)[kEach], unsigned) {
-                    race_chunk<true>(x, c, aligned, m, [&](float v, int) { return v > v_hi; }, o);
+                    race_chunk<true>(x, n, c, m, [&](float v, int) { return v > v_hi; }, o);
                     some = listed(x, c) != 0;
                 });
             queue_up(waiting, some, k * 32 + lane, k == rounds, [&](unsigned at) {
                 const unsigned from = (at / 32) * kThreads + warp * 32 + at % 32;
                 visit(kept[from], low, from, [&](const float (&x)[kEach], unsigned) { add_tokens(x, from, listed(x, from)); });
             });
+            in = in_then;
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) n[e] = n_then[e];
         }
-        const uint32_t n = merge_lists(nullptr);
-        if (n > kList) {
+        const uint32_t tokens = merge_lists(nullptr);
+        if (tokens > kList) {
             o = Race();
             cut = refined<MASS>(floor, lo_bits, hi_bits, want);
             return false;
         }
         if (rank == 0)
-            resolve<MASS>(n, want, [&](u64 key) {
+            resolve<MASS>(tokens, hi_bits, lo_bits, want, [&](u64 key) {
                 const float w = weight(unordered(ord_of(key)));
                 const int i = static_cast<int>(index_of(key));
                 if (w >= m) o.offer(w, noise[i], i);
@@ -1190,7 +1223,7 @@ __device__ __forceinline__ void draw_row(Draw<T, HISTOGRAMS> &d, unsigned r, con
         if (n <= kList && enough) {
             if (d.rank != 0) return;
             const uint32_t limit = k > 0 ? min(static_cast<uint32_t>(k), n) : n;
-            const u64 *sorted = d.sort(n);
+            const u64 *sorted = d.sort(n, ordered(d.top), ordered(low));
             if (by_mass && !whole) {   // the first k's mass
                 float part = 0.0f;
 #pragma unroll 1
@@ -1252,7 +1285,9 @@ __device__ __forceinline__ void draw_row(Draw<T, HISTOGRAMS> &d, unsigned r, con
     const float least = fmaxf(last_kept.v, d.top + 1.001f * off - 1e-5f * t - fabsf(d.top) * 4e-7f);
     const bool aligned = reinterpret_cast<uintptr_t>(d.noise + d.first) % 16 == 0;
     d.each_chunk(fmaxf(least, -FLT_MAX), [&](const float (&x)[D::kEach], unsigned c) {
-        d.template race_chunk<false>(x, c, aligned, m, [&](float v, int i) { return last_kept.takes(v, i); }, race);
+        float n[D::kEach];
+        d.load_noise(c, aligned, n);
+        d.template race_chunk<false>(x, n, c, m, [&](float v, int i) { return last_kept.takes(v, i); }, race);
     });
     d.template finish<true>(race, token, logprob);
 }
@@ -1277,9 +1312,12 @@ sample_kernel(const SampleCall call, unsigned per, const Deferred later)
     d.inbox = reinterpret_cast<u64 *>(s_bytes + kSharedBytes);
     d.count = reinterpret_cast<uint32_t *>(d.inbox);
     d.carry = d.count + kBins + 32;
-    d.region = d.blocks == 1 ? kList : inbox_keys(d.blocks) / d.blocks;
-    d.kept = reinterpret_cast<uint4 *>(d.inbox + inbox_keys(d.blocks));
+    d.region = d.blocks == 1 ? kList : inbox_keys<kKeep>(d.blocks) / d.blocks;
+    d.low_parts = reinterpret_cast<uint32_t *>(d.inbox + inbox_keys<kKeep>(d.blocks));
+    d.high_parts = d.low_parts + kBins;
+    d.kept = reinterpret_cast<uint4 *>(d.low_parts + kPartWords<kKeep>);
     d.index = reinterpret_cast<float *>(d.kept);
+    if constexpr (PASS == Pass::Left) asm volatile("griddepcontrol.wait;" ::: "memory");
     if (d.blocks > 1) d.meet();   // the blocks' shared memory is there
     if constexpr (PASS != Pass::Left) {
         draw_row<T, kKeep>(d, blockIdx.x / d.blocks, call, per, later);
@@ -1308,7 +1346,8 @@ cudaError_t launch_clusters(const SampleCall &call, unsigned clusters, unsigned 
     constexpr bool kKeep = PASS != Pass::Plain;
     constexpr size_t kMostEntries = (kMostChunks + kEntryChunks - 1) / kEntryChunks * kThreads;
     constexpr size_t kMostKept = (kMostChunks + kMaxCluster - 1) / kMaxCluster * 16;
-    constexpr size_t kMostBytes = kSharedBytes + inbox_keys(kMaxCluster) * 8 + (kKeep ? kMostKept : kMostEntries * 4);
+    constexpr size_t kMostBytes = kSharedBytes + inbox_keys<kKeep>(kMaxCluster) * 8 + kPartWords<kKeep> * 4 +
+                                  (kKeep ? kMostKept : kMostEntries * 4);
     static_assert(kMostBytes <= 227 * 1024, "the largest vocabulary fits");
     static_assert((kMostChunks + kEntryChunks - 1) / kEntryChunks * 32 <= 65536, "a warp's entries have 16-bit names");
     const unsigned chunks = (call.vocab + kEach - 1) / kEach;
@@ -1329,15 +1368,19 @@ cudaError_t launch_clusters(const SampleCall &call, unsigned clusters, unsigned 
     cfg.gridDim = dim3(clusters * blocks);
     cfg.blockDim = dim3(kThreads);
     const size_t entries = (per + kEntryChunks - 1) / kEntryChunks * kThreads;
-    cfg.dynamicSmemBytes = kSharedBytes + inbox_keys(blocks) * 8 + (kKeep ? static_cast<size_t>(per) * 16 : entries * 4);
+    cfg.dynamicSmemBytes = kSharedBytes + inbox_keys<kKeep>(blocks) * 8 + kPartWords<kKeep> * 4 + (kKeep ? static_cast<size_t>(per) * 16 : entries * 4);
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = blocks;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    // The second launch is set up while the first runs, and waits for its end
+    // before it reads anything.
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = PASS == Pass::Left ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, call, per, later);
 }
 
