@@ -146,6 +146,13 @@ __device__ __forceinline__ float exp2_approx(float x)
     return y;
 }
 
+__device__ __forceinline__ float reciprocal(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // A 16-byte chunk of logits: kEach values, and the larger of two chunks value
 // by value (a NaN loses to a number).
 template <class T> struct Chunk;
@@ -235,7 +242,7 @@ struct Race {
     uint32_t tops = 0;
     __device__ __forceinline__ void offer(float w, float q, int i)
     {
-        const float sc = fmaxf(__fdividef(w, q), 0.0f);
+        const float sc = fmaxf(w * reciprocal(q), 0.0f);
         if (sc >= score && (sc > score || i < at)) score = sc, at = i;
         if (w == 1.0f) ++tops;
         else rest += w;
@@ -425,11 +432,22 @@ struct Draw {
                     uint4 v[kGroup];
 #pragma unroll
                     for (int u = 0; u < kGroup; ++u) v[u] = fetch(c + u * kThreads);
-#pragma unroll 1
-                    for (int u = 0; u < kGroup; ++u) {
-                        visit(v[0], low, c + u * kThreads, f);
+                    // Mostly one of the four reaches it: as many turns as the
+                    // most that a lane has, not four.
+                    uint32_t hits = 0;
 #pragma unroll
-                        for (int k2 = 1; k2 < kGroup; ++k2) v[k2 - 1] = v[k2];
+                    for (int u = 0; u < kGroup; ++u) {
+                        uint32_t q[4];
+                        unpack(v[u], q);
+                        hits |= infinite || C::most(q, -inf()) >= low ? 1u << u : 0u;
+                    }
+#pragma unroll 1
+                    for (; hits != 0; hits &= hits - 1) {
+                        const unsigned u = __ffs(hits) - 1;
+                        uint4 x = v[0];
+#pragma unroll
+                        for (int o = 1; o < kGroup; ++o) x = u == o ? v[o] : x;
+                        visit(x, low, c + u * kThreads, f);
                     }
                 }
             });
@@ -528,10 +546,11 @@ struct Draw {
                 for (int e = 0; e < kEach; ++e) {
                     // Indices rise within a thread, so the first of equals stays.
                     const float w = fmaxf(exp2_approx((C::value(q, e) - most) * scale), 0.0f);
-                    const float sc = __fdividef(w, n[u][e]);
-                    if (sc > o.score) o.score = sc, o.at = i + e;
-                    if (w == 1.0f) ++o.tops;
-                    else o.rest += w;
+                    const float sc = w * reciprocal(n[u][e]);
+                    o.at = sc > o.score ? i + e : o.at;
+                    o.score = sc > o.score ? sc : o.score;
+                    o.tops += w == 1.0f ? 1u : 0u;
+                    o.rest += w == 1.0f ? 0.0f : w;
                 }
             }
         }
@@ -568,7 +587,7 @@ struct Draw {
         for (int e = 0; e < kEach; ++e) {
             float w = weight(x[e]);
             w = keep(x[e], i + e) & (w >= m) ? w : -1.0f;   // its score is below every other's
-            const float sc = w < 0.0f ? -1.0f : __fdividef(w, n[e]);
+            const float sc = w < 0.0f ? -1.0f : w * reciprocal(n[e]);
             if (RISING) {
                 o.at = sc > o.score ? i + e : o.at;
                 o.score = sc > o.score ? sc : o.score;
