@@ -99,7 +99,7 @@ template <> __device__ __forceinline__ float from_bits<float>(uint32_t b) { retu
 //   zeros  : zero counts per bit for the split / radix sort.
 //   capture_abort / capture_wait : the fused-predicate compaction's
 //            one-pass capture, and the back-off after a capture gave up.
-//   sample_rows / sample_left : the token draw's second launch.
+//   sample_rows / sample_decided / sample_next / sample_left : the token draw's second launch.
 // ---------------------------------------------------------------------------
 struct DevState {
     unsigned epoch;
@@ -111,9 +111,11 @@ struct DevState {
     unsigned grid_depart;   // blocks that left it; the last one resets both
     unsigned capture_abort; // a fused-predicate capture gave up (reset by its last block to leave)
     unsigned capture_wait;  // calls still to skip the capture after one gave up (a back-off)
-    unsigned sample_rows;   // token draw: rows left to its second launch, which resets both
-    unsigned sample_left;   // blocks of that launch that are through
-    unsigned pad[6];
+    unsigned sample_rows;   // token draw: rows left to its second launch, which resets the four
+    unsigned sample_decided;   // rows that are left to it or will not be
+    unsigned sample_next;   // rows that this launch has taken up beyond its clusters' first ones
+    unsigned sample_left;   // its blocks that are through
+    unsigned pad[4];
     unsigned zeros[48];
 };
 static_assert(sizeof(DevState) == 256, "DevState is 256 bytes in every workspace layout");

@@ -219,7 +219,7 @@ struct Shared {
     uint32_t tops[kMaxCluster];
     u64 mass[kMaxCluster];           // of their parts of a histogram
     u64 cut, pick_want;
-    uint32_t pick_bin;
+    uint32_t pick_bin, next[2];
     // Results of one block's scans.
     u64 pick_key;
     uint32_t pick_edge[2];
@@ -1103,9 +1103,43 @@ struct Draw {
 };
 
 // Rows whose cut needs histograms, left by the first launch to the second.
+// The second starts when every row of the first is either drawn, put down
+// here, or in a race of all its tokens: these take longest, and go on beside it.
 struct Deferred {
     uint32_t *rows;
-    unsigned *count, *left;          // rows put down; blocks of the second launch that are through
+    unsigned *count, *decided;       // rows put down; rows that are put down or will not be
+    unsigned *next, *left;           // rows that the second launch has taken up; its blocks that are through
+    unsigned *error;
+    unsigned limit;                  // polls of the second launch before it gives up
+
+    // By one thread of the row's cluster, once.
+    __device__ __forceinline__ void decide(bool put_down, unsigned row) const
+    {
+        if (rows == nullptr) return;
+        if (put_down) rows[atomicAdd(count, 1u)] = row;
+        __threadfence();   // the row before the word that counts it
+        atomicAdd(decided, 1u);
+    }
+};
+
+// What a row asks for.
+struct Setting {
+    float t, p, m;
+    int k;                           // 0: all
+    bool greedy, by_mass, plain, whole;
+    __device__ __forceinline__ Setting(const SampleCall &call, unsigned r)
+    {
+        t = call.temperature != nullptr ? call.temperature[r] : 1.0f;
+        k = call.top_k != nullptr ? call.top_k[r] : 0;
+        if (k <= 0 || static_cast<unsigned>(k) >= call.vocab) k = 0;
+        p = call.top_p != nullptr ? call.top_p[r] : 1.0f;
+        m = call.min_p != nullptr ? call.min_p[r] : 0.0f;
+        // One token stays, the first of the order: no draw.
+        greedy = call.noise == nullptr || !(t > 0.0f) || k == 1 || call.vocab == 1 || !(p > 0.0f) || !(m <= 1.0f);
+        by_mass = !(p >= 1.0f);
+        plain = !greedy && k == 0 && !by_mass && !(m > 0.0f);   // a race of all tokens
+        whole = !greedy && k == 0 && by_mass;                   // top-p over the whole row
+    }
 };
 
 // One row by one cluster.  Without HISTOGRAMS a row that needs them is put
@@ -1122,16 +1156,13 @@ __device__ __forceinline__ void draw_row(Draw<T, HISTOGRAMS> &d, unsigned r, con
     d.infinite = false;
     d.place(per);
 
-    const float t = call.temperature != nullptr ? call.temperature[r] : 1.0f;
-    int k = call.top_k != nullptr ? call.top_k[r] : 0;
-    if (k <= 0 || static_cast<unsigned>(k) >= vocab) k = 0;
-    const float p = call.top_p != nullptr ? call.top_p[r] : 1.0f;
-    const float m = call.min_p != nullptr ? call.min_p[r] : 0.0f;
-    // One token stays, the first of the order: no draw.
-    const bool greedy = call.noise == nullptr || !(t > 0.0f) || k == 1 || vocab == 1 || !(p > 0.0f) || !(m <= 1.0f);
-    const bool by_mass = !(p >= 1.0f);
-    const bool plain = !greedy && k == 0 && !by_mass && !(m > 0.0f);
-    const bool whole = !greedy && k == 0 && by_mass;   // top-p over the whole row
+    const Setting ask(call, r);
+    const float t = ask.t, p = ask.p, m = ask.m;
+    const int k = ask.k;
+    const bool greedy = ask.greedy, by_mass = ask.by_mass, plain = ask.plain, whole = ask.whole;
+    const bool listed = !greedy && (k > 0 || by_mass), first_thread = d.rank == 0 && d.tid == 0;
+    if (!HISTOGRAMS && !listed && first_thread) later.decide(false, r);
+    if (!HISTOGRAMS && plain) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int32_t *token = call.tokens + r;
     float *logprob = call.logprobs != nullptr ? call.logprobs + r : nullptr;
     d.t = t;
@@ -1148,7 +1179,7 @@ __device__ __forceinline__ void draw_row(Draw<T, HISTOGRAMS> &d, unsigned r, con
     const uint32_t warp_top = __reduce_max_sync(kFullMask, lane_top);
     uint32_t bound = ~0u;
     bool bounded = false;
-    if (!greedy && (k > 0 || by_mass)) {
+    if (listed) {
         const unsigned last = (d.chunks - 1) / per;   // the last block with any
         const unsigned full = min(d.mine / 32, static_cast<unsigned>(kWarps));
         const unsigned warps = last * min(per / 32, static_cast<unsigned>(kWarps)) +
@@ -1181,10 +1212,11 @@ __device__ __forceinline__ void draw_row(Draw<T, HISTOGRAMS> &d, unsigned r, con
         bound = __reduce_min_sync(kFullMask, s.bound[b]);
     }
     if (top == kOrderedMinusInf) {
-        if (d.rank == 0 && d.tid == 0) {
+        if (first_thread) {
             *token = -1;
             if (logprob != nullptr) *logprob = -inf();
         }
+        if (!HISTOGRAMS && listed && first_thread) later.decide(false, r);
         return;
     }
     d.top = unordered(top);
@@ -1206,11 +1238,11 @@ __device__ __forceinline__ void draw_row(Draw<T, HISTOGRAMS> &d, unsigned r, con
             for (int e = 0; e < D::kEach; ++e)
                 if (x[e] == d.top) race.score = 1.0f, race.at = min(race.at, d.index_at(c) + e);
         });
-        race.tops = d.rank == 0 && d.tid == 0 ? 1 : 0;   // one token is kept
+        race.tops = first_thread ? 1 : 0;   // one token is kept
         d.template finish<true>(race, token, logprob);
         return;
     }
-    if (k > 0 || by_mass) {
+    if (listed) {
         const float low = bounded ? fmaxf(unordered(max(bound, kOrderedMinusInf)), -FLT_MAX) : -FLT_MAX;
         float above = 0.0f, total = 0.0f;
         if (whole) {
@@ -1239,7 +1271,9 @@ __device__ __forceinline__ void draw_row(Draw<T, HISTOGRAMS> &d, unsigned r, con
             for (unsigned b = 0; b < d.blocks; ++b) total += s.sum_all[b];
             enough = !d.infinite && (low == -FLT_MAX || above > p * total * (1.0f + 1.0f / 4096));
         }
-        if (n <= kList && enough) {
+        const bool fits = n <= kList && enough;
+        if (!HISTOGRAMS && first_thread) later.decide(!fits, r);
+        if (fits) {
             if (d.rank != 0) return;
             const uint32_t limit = k > 0 ? min(static_cast<uint32_t>(k), n) : n;
             const u64 *sorted = d.sort(n, ordered(d.top), ordered(low));
@@ -1269,7 +1303,6 @@ __device__ __forceinline__ void draw_row(Draw<T, HISTOGRAMS> &d, unsigned r, con
             return;
         }
         if constexpr (!HISTOGRAMS) {
-            if (d.rank == 0 && d.tid == 0) later.rows[atomicAdd(later.count, 1u)] = r;
             return;
         } else {
             const auto tokens_wanted = [&](u64) { return static_cast<u64>(k); };
@@ -1336,19 +1369,38 @@ sample_kernel(const SampleCall call, unsigned per, const Deferred later)
     d.high_parts = d.low_parts + kBins;
     d.kept = reinterpret_cast<uint4 *>(d.low_parts + kPartWords<kKeep>);
     d.index = reinterpret_cast<float *>(d.kept);
-    if constexpr (PASS == Pass::Left) asm volatile("griddepcontrol.wait;" ::: "memory");
     if (d.blocks > 1) d.meet();   // the blocks' shared memory is there
     if constexpr (PASS != Pass::Left) {
         draw_row<T, kKeep>(d, blockIdx.x / d.blocks, call, per, later);
     } else {
-        const unsigned n = *later.count, clusters = gridDim.x / d.blocks;
+        unsigned decided = 0;
+        for (unsigned polls = 0; polls < later.limit; ++polls) {
+            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(decided) : "l"(later.decided) : "memory");
+            if (decided == call.rows) break;
+            __nanosleep(64);
+        }
+        const bool ready = __syncthreads_and(decided == call.rows) != 0;
+        if (!ready && d.tid == 0) atomicOr(later.error, kErrTimeout);
+        // A cluster's first row by its place, then whichever is next; asked for
+        // while the row before it is drawn.
+        const unsigned n = ready ? *later.count : 0, clusters = gridDim.x / d.blocks;
 #pragma unroll 1
-        for (unsigned w = blockIdx.x / d.blocks; w < n; w += clusters) {
+        for (unsigned w = blockIdx.x / d.blocks, turn = 0; w < n; w = s.next[turn], turn ^= 1) {
+            unsigned next = 0;
+            if (d.rank == 0 && d.tid == 0) next = clusters + atomicAdd(later.next, 1u);
             draw_row<T, kKeep>(d, later.rows[w], call, per, later);
+            if (d.rank == 0 && d.tid == 0) {
+#pragma unroll 1
+                for (unsigned b = 0; b < d.blocks; ++b) put(&s.next[turn], b, next);
+            }
             d.meet();   // the shared memory is used again from here
         }
-        if (d.tid == 0 && atomicAdd(later.left, 1u) == gridDim.x - 1) {   // every block has read the count
+        // Not over before the first launch is.
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (d.tid == 0 && atomicAdd(later.left, 1u) == gridDim.x - 1) {   // every block is through
             *later.count = 0;
+            *later.decided = 0;
+            *later.next = 0;
             *later.left = 0;
         }
     }
@@ -1395,8 +1447,7 @@ cudaError_t launch_clusters(const SampleCall &call, unsigned clusters, unsigned 
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    // The second launch is set up while the first runs, and waits for its end
-    // before it reads anything.
+    // The second launch may start before the first is over.
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.numAttrs = PASS == Pass::Left ? 2 : 1;
@@ -1406,7 +1457,6 @@ cudaError_t launch_clusters(const SampleCall &call, unsigned clusters, unsigned 
 template <class T>
 cudaError_t launch_typed(const SampleCall &call, const Workspace &ws, cudaStream_t s)
 {
-    const Deferred later{call.row_words, &ws.state->sample_rows, &ws.state->sample_left};
     const size_t rows = call.rows;
     const unsigned chunks = (call.vocab + Chunk<T>::kEach - 1) / Chunk<T>::kEach;
     // One block per row, and more while all of them still fit on the GPU at
@@ -1417,13 +1467,13 @@ cudaError_t launch_typed(const SampleCall &call, const Workspace &ws, cudaStream
     while (blocks < wide && rows * blocks * 2 <= sms * kBlocksPerSm<Pass::Plain>) blocks *= 2;
     if (rows * blocks > 0x7fffffffull) return cudaErrorInvalidValue;
     const unsigned n = static_cast<unsigned>(rows);
+    const Deferred later{call.row_words,         &ws.state->sample_rows, &ws.state->sample_decided, &ws.state->sample_next,
+                         &ws.state->sample_left, &ws.state->error,       call.spin_limit};
     const size_t most = sms * kBlocksPerSm<Pass::Whole> / wide;   // wide clusters on the GPU at once
     if (later.rows != nullptr && rows <= most)
         return launch_clusters<T, Pass::Whole>(call, n, wide, later, s);
     const cudaError_t e = launch_clusters<T, Pass::Plain>(call, n, blocks, later, s);
     if (e != cudaSuccess || later.rows == nullptr) return e;
-    // A row that needs histograms takes many times as long as the others:
-    // these go to a second launch of wide clusters.
     return launch_clusters<T, Pass::Left>(call, static_cast<unsigned>(rows < most ? rows : most), wide, later, s);
 }
 
