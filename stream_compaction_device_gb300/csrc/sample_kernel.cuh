@@ -59,6 +59,7 @@ constexpr int kMaxCluster = 8;
 constexpr int kGroup = 4;                  // chunks that a thread loads at once: an entry of the index
 constexpr int kQueue = 64;                 // entries that a warp has waiting
 constexpr unsigned kLeastChunks = 512;     // of a block's slice, where rows are few
+constexpr unsigned kKeptChunks = 4096;     // of a kept slice, for two blocks per SM: 64 KB
 constexpr int kList = 1024;                // tokens the short list holds
 constexpr int kBins = 1024;
 constexpr float kCountSpan = 16.0f;        // first histogram of counts: logits below the largest that it resolves
@@ -1459,21 +1460,32 @@ cudaError_t launch_typed(const SampleCall &call, const Workspace &ws, cudaStream
 {
     const size_t rows = call.rows;
     const unsigned chunks = (call.vocab + Chunk<T>::kEach - 1) / Chunk<T>::kEach;
-    // One block per row, and more while all of them still fit on the GPU at
-    // once and have enough of the row each.
-    const size_t sms = static_cast<size_t>(ws.num_sms);
-    unsigned blocks = 1, wide = 1;   // wide: the most that a row of this size is worth
+    const size_t sms = static_cast<size_t>(ws.num_sms), room = sms * kBlocksPerSm<Pass::Whole>;
+    unsigned wide = 1;               // the most blocks that a row of this size is worth
     while (wide < kMaxCluster && wide * kLeastChunks < chunks) wide *= 2;
-    while (blocks < wide && rows * blocks * 2 <= sms * kBlocksPerSm<Pass::Plain>) blocks *= 2;
-    if (rows * blocks > 0x7fffffffull) return cudaErrorInvalidValue;
+    if (rows > 0x7fffffffull / kMaxCluster) return cudaErrorInvalidValue;
     const unsigned n = static_cast<unsigned>(rows);
     const Deferred later{call.row_words,         &ws.state->sample_rows, &ws.state->sample_decided, &ws.state->sample_next,
                          &ws.state->sample_left, &ws.state->error,       call.spin_limit};
-    const size_t most = sms * kBlocksPerSm<Pass::Whole> / wide;   // wide clusters on the GPU at once
-    if (later.rows != nullptr && rows <= most)
-        return launch_clusters<T, Pass::Whole>(call, n, wide, later, s);
+    // One launch of blocks that keep their slices, as many to a row as fit on
+    // the GPU at once (clusters of eight leave gaps: fewer of them fit), where
+    // the slices are small enough for two blocks per SM.  Against two launches
+    // (us, one : two): 64 x 131072 bf16 top-k and top-p 12.4 : 16.9, of mixed
+    // settings 35 : 46; 100 x 50001 f16 31 : 39; 300 x 8000 bf16 19 : 37; 512 x
+    // 30000 bf16 top-p 53 : 116, top-k and top-p 18.8 : 16.8.
+    unsigned blocks = 1;
+    while (blocks < wide && rows * blocks * 2 <= (blocks * 2 == kMaxCluster ? room / 32 * 27 : room)) blocks *= 2;
+    if (later.rows != nullptr && chunks <= blocks * kKeptChunks)
+        return launch_clusters<T, Pass::Whole>(call, n, blocks, later, s);
+    // Else a launch of blocks that do not, for the rows that need one or two
+    // passes, and one of wide clusters for the others (512 x 131072 bf16 of
+    // mixed settings: 82 us, in one launch of two or four blocks per row that
+    // keep their slices 173 and 127).
+    blocks = 1;
+    while (blocks < wide && rows * blocks * 2 <= sms * kBlocksPerSm<Pass::Plain>) blocks *= 2;
     const cudaError_t e = launch_clusters<T, Pass::Plain>(call, n, blocks, later, s);
     if (e != cudaSuccess || later.rows == nullptr) return e;
+    const size_t most = room / wide;
     return launch_clusters<T, Pass::Left>(call, static_cast<unsigned>(rows < most ? rows : most), wide, later, s);
 }
 
