@@ -1143,12 +1143,20 @@ struct Setting {
     }
 };
 
-// One row by one cluster.  Without HISTOGRAMS a row that needs them is put
-// down for later.
-template <class T, bool HISTOGRAMS>
-__device__ __forceinline__ void draw_row(Draw<T, HISTOGRAMS> &d, unsigned r, const SampleCall &call, unsigned per,
+// What a launch does: every row, leaving out those that need histograms; every
+// row; the rows that the first kind has left out, a cluster taking every so
+// many of them.  Four blocks per SM for the first, whose rows are many and
+// wait for memory; two for the others, whose passes want registers.
+enum class Pass { Plain, Whole, Left };
+template <Pass PASS> constexpr int kBlocksPerSm = PASS == Pass::Plain ? 4 : 2;
+template <Pass PASS> constexpr bool kKeeps = PASS != Pass::Plain;
+
+// One row by one cluster.
+template <class T, Pass PASS>
+__device__ __forceinline__ void draw_row(Draw<T, kKeeps<PASS>> &d, unsigned r, const SampleCall &call, unsigned per,
                                          const Deferred &later)
 {
+    constexpr bool HISTOGRAMS = kKeeps<PASS>;
     using D = Draw<T, HISTOGRAMS>;
     Shared &s = d.s;
     const unsigned vocab = d.vocab;
@@ -1161,7 +1169,8 @@ __device__ __forceinline__ void draw_row(Draw<T, HISTOGRAMS> &d, unsigned r, con
     const float t = ask.t, p = ask.p, m = ask.m;
     const int k = ask.k;
     const bool greedy = ask.greedy, by_mass = ask.by_mass, plain = ask.plain, whole = ask.whole;
-    const bool listed = !greedy && (k > 0 || by_mass), first_thread = d.rank == 0 && d.tid == 0;
+    const bool cuts = !greedy && (k > 0 || by_mass), first_thread = d.rank == 0 && d.tid == 0;
+    const bool listed = cuts && PASS != Pass::Left;   // rows are left because a list does not do
     if (!HISTOGRAMS && !listed && first_thread) later.decide(false, r);
     if (!HISTOGRAMS && plain) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int32_t *token = call.tokens + r;
@@ -1171,7 +1180,7 @@ __device__ __forceinline__ void draw_row(Draw<T, HISTOGRAMS> &d, unsigned r, con
     Race race;
     float most, sum = 0.0f;
     if (plain) most = d.race_all(race);
-    else if (whole) most = d.template load<true>(&sum);
+    else if (whole && listed) most = d.template load<true>(&sum);
     else most = d.template load<false>(nullptr);
 
     // The largest logit, and the bound for the short list: the least, over the
@@ -1243,65 +1252,67 @@ __device__ __forceinline__ void draw_row(Draw<T, HISTOGRAMS> &d, unsigned r, con
         d.template finish<true>(race, token, logprob);
         return;
     }
-    if (listed) {
-        const float low = bounded ? fmaxf(unordered(max(bound, kOrderedMinusInf)), -FLT_MAX) : -FLT_MAX;
-        float above = 0.0f, total = 0.0f;
-        if (whole) {
-            float part;
-            d.block_scan(sum * fmaxf(exp2_approx((most - d.top) * d.scale), 0.0f), s.warpf, &part);
-            if (d.tid < d.blocks) put(&s.sum_all[d.rank], d.tid, part);
-        }
-        const bool near = d.blocks > 1;   // few rows: the list's noise is fetched before it is known to be needed
-        d.begin_list();
-        d.each_chunk(low, [&](const float (&x)[D::kEach], unsigned c) {
-            uint32_t which = 0;
-#pragma unroll
-            for (int e = 0; e < D::kEach; ++e) which |= x[e] >= low ? 1u << e : 0u;
+    if (cuts) {
+        if (listed) {
+            const float low = bounded ? fmaxf(unordered(max(bound, kOrderedMinusInf)), -FLT_MAX) : -FLT_MAX;
+            float above = 0.0f, total = 0.0f;
             if (whole) {
+                float part;
+                d.block_scan(sum * fmaxf(exp2_approx((most - d.top) * d.scale), 0.0f), s.warpf, &part);
+                if (d.tid < d.blocks) put(&s.sum_all[d.rank], d.tid, part);
+            }
+            const bool near = d.blocks > 1;   // few rows: the list's noise is fetched before it is known to be needed
+            d.begin_list();
+            d.each_chunk(low, [&](const float (&x)[D::kEach], unsigned c) {
+                uint32_t which = 0;
 #pragma unroll
-                for (int e = 0; e < D::kEach; ++e) above += x[e] >= low ? d.weight(x[e]) : 0.0f;
-            }
-            if (near && which != 0)
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(d.noise + d.index_at(c) + __ffs(which) - 1));
-            d.add_tokens(x, c, which);
-        });
-        const uint32_t n = d.merge_lists(&above);
-        bool enough = true;
-        if (whole) {
-#pragma unroll 1
-            for (unsigned b = 0; b < d.blocks; ++b) total += s.sum_all[b];
-            enough = !d.infinite && (low == -FLT_MAX || above > p * total * (1.0f + 1.0f / 4096));
-        }
-        const bool fits = n <= kList && enough;
-        if (!HISTOGRAMS && first_thread) later.decide(!fits, r);
-        if (fits) {
-            if (d.rank != 0) return;
-            const uint32_t limit = k > 0 ? min(static_cast<uint32_t>(k), n) : n;
-            const u64 *sorted = d.sort(n, ordered(d.top), ordered(low));
-            if (by_mass && !whole) {   // the first k's mass
-                float part = 0.0f;
-#pragma unroll 1
-                for (uint32_t at = d.tid; at < limit; at += kThreads) part += d.list_weight(unordered(ord_of(sorted[at])));
-                d.block_scan(part, s.warpf, &total);
-            }
-            const float bar = p * total;
-            float listed = 0.0f;
-#pragma unroll 1
-            for (uint32_t at0 = 0; at0 < limit; at0 += kThreads) {
-                const uint32_t at = at0 + d.tid;
-                float w = 0.0f, all = 0.0f, ahead = 0.0f;
-                u64 key = 0;
-                if (at < limit) {
-                    key = sorted[at];
-                    w = d.list_weight(unordered(ord_of(key)));
+                for (int e = 0; e < D::kEach; ++e) which |= x[e] >= low ? 1u << e : 0u;
+                if (whole) {
+#pragma unroll
+                    for (int e = 0; e < D::kEach; ++e) above += x[e] >= low ? d.weight(x[e]) : 0.0f;
                 }
-                if (by_mass) ahead = listed + d.block_scan(w, s.warpf, &all);
-                listed += all;
-                if (at < limit && (at == 0 || ((!by_mass || ahead < bar) && w >= m)))
-                    race.offer(w, d.noise[index_of(key)], static_cast<int>(index_of(key)));
+                if (near && which != 0)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(d.noise + d.index_at(c) + __ffs(which) - 1));
+                d.add_tokens(x, c, which);
+            });
+            const uint32_t n = d.merge_lists(&above);
+            bool enough = true;
+            if (whole) {
+#pragma unroll 1
+                for (unsigned b = 0; b < d.blocks; ++b) total += s.sum_all[b];
+                enough = !d.infinite && (low == -FLT_MAX || above > p * total * (1.0f + 1.0f / 4096));
             }
-            d.template finish<false>(race, token, logprob);
-            return;
+            const bool fits = n <= kList && enough;
+            if (!HISTOGRAMS && first_thread) later.decide(!fits, r);
+            if (fits) {
+                if (d.rank != 0) return;
+                const uint32_t limit = k > 0 ? min(static_cast<uint32_t>(k), n) : n;
+                const u64 *sorted = d.sort(n, ordered(d.top), ordered(low));
+                if (by_mass && !whole) {   // the first k's mass
+                    float part = 0.0f;
+#pragma unroll 1
+                    for (uint32_t at = d.tid; at < limit; at += kThreads) part += d.list_weight(unordered(ord_of(sorted[at])));
+                    d.block_scan(part, s.warpf, &total);
+                }
+                const float bar = p * total;
+                float listed = 0.0f;
+#pragma unroll 1
+                for (uint32_t at0 = 0; at0 < limit; at0 += kThreads) {
+                    const uint32_t at = at0 + d.tid;
+                    float w = 0.0f, all = 0.0f, ahead = 0.0f;
+                    u64 key = 0;
+                    if (at < limit) {
+                        key = sorted[at];
+                        w = d.list_weight(unordered(ord_of(key)));
+                    }
+                    if (by_mass) ahead = listed + d.block_scan(w, s.warpf, &all);
+                    listed += all;
+                    if (at < limit && (at == 0 || ((!by_mass || ahead < bar) && w >= m)))
+                        race.offer(w, d.noise[index_of(key)], static_cast<int>(index_of(key)));
+                }
+                d.template finish<false>(race, token, logprob);
+                return;
+            }
         }
         if constexpr (!HISTOGRAMS) {
             return;
@@ -1345,20 +1356,13 @@ __device__ __forceinline__ void draw_row(Draw<T, HISTOGRAMS> &d, unsigned r, con
     d.template finish<true>(race, token, logprob);
 }
 
-// What a launch does: every row, leaving out those that need histograms; every
-// row; the rows that the first kind has left out, a cluster taking every so
-// many of them.  Four blocks per SM for the first, whose rows are many and
-// wait for memory; two for the others, whose passes want registers.
-enum class Pass { Plain, Whole, Left };
-template <Pass PASS> constexpr int kBlocksPerSm = PASS == Pass::Plain ? 4 : 2;
-
 template <class T, Pass PASS>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm<PASS>)
 sample_kernel(const SampleCall call, unsigned per, const Deferred later)
 {
     extern __shared__ __align__(16) unsigned char s_bytes[];
     Shared &s = *reinterpret_cast<Shared *>(s_bytes);
-    constexpr bool kKeep = PASS != Pass::Plain;
+    constexpr bool kKeep = kKeeps<PASS>;
     Draw<T, kKeep> d(s);
     d.tid = threadIdx.x, d.lane = d.tid & 31, d.warp = d.tid >> 5;
     d.rank = cluster_rank(), d.blocks = cluster_blocks(), d.vocab = call.vocab;
@@ -1372,7 +1376,7 @@ sample_kernel(const SampleCall call, unsigned per, const Deferred later)
     d.index = reinterpret_cast<float *>(d.kept);
     if (d.blocks > 1) d.meet();   // the blocks' shared memory is there
     if constexpr (PASS != Pass::Left) {
-        draw_row<T, kKeep>(d, blockIdx.x / d.blocks, call, per, later);
+        draw_row<T, PASS>(d, blockIdx.x / d.blocks, call, per, later);
     } else {
         unsigned decided = 0;
         for (unsigned polls = 0; polls < later.limit; ++polls) {
@@ -1389,7 +1393,7 @@ sample_kernel(const SampleCall call, unsigned per, const Deferred later)
         for (unsigned w = blockIdx.x / d.blocks, turn = 0; w < n; w = s.next[turn], turn ^= 1) {
             unsigned next = 0;
             if (d.rank == 0 && d.tid == 0) next = clusters + atomicAdd(later.next, 1u);
-            draw_row<T, kKeep>(d, later.rows[w], call, per, later);
+            draw_row<T, PASS>(d, later.rows[w], call, per, later);
             if (d.rank == 0 && d.tid == 0) {
 #pragma unroll 1
                 for (unsigned b = 0; b < d.blocks; ++b) put(&s.next[turn], b, next);
@@ -1415,7 +1419,7 @@ cudaError_t launch_clusters(const SampleCall &call, unsigned clusters, unsigned 
     constexpr unsigned kEach = Chunk<T>::kEach;
     constexpr unsigned kEntryChunks = kGroup * kThreads;   // chunks to kThreads entries of the index
     constexpr size_t kMostChunks = (static_cast<size_t>(1) << 18) / kEach + 1;   // of the largest vocabulary
-    constexpr bool kKeep = PASS != Pass::Plain;
+    constexpr bool kKeep = kKeeps<PASS>;
     constexpr size_t kMostEntries = (kMostChunks + kEntryChunks - 1) / kEntryChunks * kThreads;
     constexpr size_t kMostKept = (kMostChunks + kMaxCluster - 1) / kMaxCluster * 16;
     constexpr size_t kMostBytes = kSharedBytes + inbox_keys<kKeep>(kMaxCluster) * 8 + kPartWords<kKeep> * 4 +
