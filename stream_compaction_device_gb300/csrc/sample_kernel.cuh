@@ -945,7 +945,7 @@ struct Draw {
     {
         uint32_t bin = 0;
         const float span = MASS ? kMassSpan * t : kCountSpan;
-        bins_per_unit = fmaxf((kBins - 1) / span, 1e-30f);
+        bins_per_unit = fminf(fmaxf((kBins - 1) / span, 1e-30f), 1e30f);
         const float least = MASS ? fmaxf(floor.v, top - span) : floor.v;
         if (!histogram<MASS>(least, [&](float v, int i) { return floor.takes(v, i) & v >= least ? bin_of(v) : -1; },
                              wanted, want, bin))

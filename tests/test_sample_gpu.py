@@ -252,6 +252,56 @@ def test_graph_replay(ds):
     ds.stream_release(s)
 
 
+def test_rows_left_to_a_second_launch(ds):
+    """More rows than fit at once with their slices: flat rows whose cut needs
+    histograms beside peaked ones and races of all tokens, again and again on
+    one stream and in a graph."""
+    rows, vocab = 330, 40000
+    kinds = [(1.0, 0, 0.9, 0.0), (0.8, 50, 0.9, 0.0), (1.0, 0, 1.0, 0.0), (1.0, 3000, 0.95, 0.0), (0.0, 0, 1.0, 0.0),
+             (1.0, 2000, 1.0, 0.001), (3.0, 0, 0.5, 0.0)]
+    asks = [kinds[r % len(kinds)] for r in range(rows)]
+    kw = asked(asks)
+    for seed, dtype in ((21, torch.float32), (22, torch.bfloat16)):
+        x, q = peaked(rows, vocab, seed)
+        x = x.to(dtype)
+        xd, qd = x.cuda(), q.cuda()
+        first = [t.clone() for t in ds.sample_tokens(xd, qd, **kw)]
+        check(x, q, *first, asks)
+        for _ in range(4):
+            assert all(torch.equal(a, b) for a, b in zip(first, ds.sample_tokens(xd, qd, **kw)))
+        assert ds.device_status() == 0
+        out, logprobs = torch.empty(rows, dtype=torch.int32, device="cuda"), torch.empty(rows, device="cuda")
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            ds.sample_tokens(xd, qd, **kw, out=out, logprobs=logprobs)
+        s.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            for _ in range(2):
+                ds.sample_tokens(xd, qd, **kw, out=out, logprobs=logprobs)
+        out.fill_(-5)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, first[0]) and torch.equal(logprobs, first[1])
+        assert ds.device_status(s) == 0
+        ds.stream_release(s)
+
+
+@pytest.mark.parametrize("rows", [2, 330])
+def test_wide_cuts(ds, rows):
+    """Cuts far down the order, in rows of ties and of masked tokens."""
+    vocab = 36001
+    rng = np.random.default_rng(23)
+    x, q = peaked(rows, vocab, 24)
+    x[0] = torch.from_numpy(rng.integers(-3, 3, vocab).astype(np.float32))
+    x[1, rng.random(vocab) < 0.7] = -INF
+    for ask in [(1.0, 20000, 1.0, 0.0), (1.0, 5000, 0.99, 0.0), (0.5, 0, 0.9999, 0.0), (1e-3, 0, 0.9, 0.0),
+                (30.0, 0, 0.97, 0.0), (1.0, 9999, 0.3, 0.01), (1.0, 36000, 0.999, 0.0), (1e-30, 30000, 0.9, 0.0)]:
+        tokens, logprobs = ds.sample_tokens(x.cuda(), q.cuda(), **asked([ask] * rows))
+        check(x[:8], q[:8], tokens[:8], logprobs[:8], [ask] * min(rows, 8))
+
+
 def test_refusals(ds):
     x, q = torch.zeros(4, 64, device="cuda"), torch.ones(4, 64, device="cuda")
     i32 = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
