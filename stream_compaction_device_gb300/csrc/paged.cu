@@ -18,8 +18,8 @@
 // to 20, so every block scans all the counts for itself (out of L2, into its
 // shared memory) and takes an equal share of the output: one launch, no block
 // waits for another, and one long row is spread over the whole GPU.  A warp
-// takes up to 256 neighbouring outputs and looks for the rows of the first and the
-// last; the others search between these two, and in a long row not at all.
+// takes up to 4,096 neighbouring outputs and looks for the rows of the first and the
+// last of them.
 // Sums run in 64 bits and are stored saturated to INT32_MAX, so that lengths
 // whose sum passes 32 bits cannot wrap into positions that look valid.
 #include "core.cuh"
@@ -30,7 +30,7 @@ namespace {
 
 constexpr int kPagedThreads = 512;
 constexpr int kPagedWarps = kPagedThreads / 32;
-constexpr int kChunk = 256;   // consecutive outputs that a warp takes at a time, at most
+constexpr int kChunk = 4096;   // consecutive outputs that a warp takes at a time, at most
 
 // Division of any uint32 by the page size, by a multiplication with its
 // reciprocal rounded up to 33 bits (Granlund and Montgomery, "Division by
@@ -236,35 +236,45 @@ __device__ __forceinline__ Ends row_ends(const Count &count, int rows, const End
     return e;
 }
 
-// store(g, row, load(g, row, index in the row)) for the outputs 0 .. total,
-// dealt to the warps of the grid a chunk of neighbours at a time; row == rows
-// past the last one.  The loads of a chunk's part are in flight together.
-template <class Load, class Store>
-__device__ __forceinline__ void each_output(const Ends &e, int rows, int total, Load load, Store store)
+// store(c, g, load(c, g)) with c = of_row(row, the row's first output) for the
+// outputs 0 .. total, dealt to the warps of the grid a chunk of neighbours at a
+// time; row == rows past the last one.  A chunk of few rows goes row by row,
+// with no search and one c for a run; one of many rows (a decode step brings
+// one output a row, or none) searches for every output's.
+template <class OfRow, class Load, class Store>
+__device__ __forceinline__ void each_output(const Ends &e, int rows, int total, OfRow of_row, Load load, Store store)
 {
-    constexpr int kAtOnce = 4;
+    constexpr int kAtOnce = 4, kFewRows = 4;
     const int lane = threadIdx.x & 31;
     const int warps = static_cast<int>(gridDim.x) * kPagedWarps;
-    // As many outputs to a chunk as give every warp one, within bounds.
-    const int share = (total / warps + 31) / 32 * 32, chunk = share < 32 ? 32 : (share > kChunk ? kChunk : share);
+    // One chunk per warp: every chunk costs two searches and its own waits.
+    const int share = (total / warps + 32) / 32 * 32, chunk = share > kChunk ? kChunk : share;
+    const auto start_of = [&](int r) { return r > 0 ? e.ends[r - 1] : 0; };
     for (long long first = (static_cast<long long>(blockIdx.x) * kPagedWarps + (threadIdx.x >> 5)) * chunk;
          first < total; first += static_cast<long long>(warps) * chunk) {
         const int g0 = static_cast<int>(first), g1 = total - g0 < chunk ? total : g0 + chunk;
         const int lo = warp_row_of(e.ends, 0, rows, g0);
         const int hi = lo < rows && e.ends[lo] >= g1 ? lo : warp_row_of(e.ends, lo, rows, g1 - 1);
-        for (int g = g0 + lane; g < g1; g += 32 * kAtOnce) {
-            int row[kAtOnce];
-            decltype(load(0, 0, 0)) v[kAtOnce];
+        if (hi - lo < kFewRows) {
+            for (int r = lo; r <= hi; ++r) {
+                const int start = start_of(r), end = r < rows && e.ends[r] < g1 ? e.ends[r] : g1;
+                const auto c = of_row(r, start);
+                for (int g = (start > g0 ? start : g0) + lane; g < end; g += 32 * kAtOnce) {
+                    decltype(load(c, 0)) v[kAtOnce];
 #pragma unroll
-            for (int u = 0; u < kAtOnce; ++u) {
-                const int at = g + 32 * u;
-                if (at >= g1) continue;
-                row[u] = lo == hi ? lo : row_of(e.ends, lo, hi, at);
-                v[u] = load(at, row[u], at - (row[u] > 0 ? e.ends[row[u] - 1] : 0));
+                    for (int u = 0; u < kAtOnce; ++u)
+                        if (g + 32 * u < end) v[u] = load(c, g + 32 * u);
+#pragma unroll
+                    for (int u = 0; u < kAtOnce; ++u)
+                        if (g + 32 * u < end) store(c, g + 32 * u, v[u]);
+                }
             }
-#pragma unroll
-            for (int u = 0; u < kAtOnce; ++u)
-                if (g + 32 * u < g1) store(g + 32 * u, row[u], v[u]);
+        } else {
+            for (int g = g0 + lane; g < g1; g += 32) {
+                const int r = row_of(e.ends, lo, hi, g);
+                const auto c = of_row(r, start_of(r));
+                store(c, g, load(c, g));
+            }
         }
     }
 }
@@ -294,13 +304,10 @@ extend_kernel(int32_t *__restrict__ table, size_t stride, int rows, ExtendCount 
         granted[r] = e.places[r] >= 0 && (!needs || end <= free);
     }
     if (tid == 0) *left = free - total;
-    struct Page {
-        size_t at;
-        int id;
-    };
-    each_output(e, rows, total, [&](int g, int r, int j) {
-        return Page{static_cast<size_t>(r) * stride + e.places[r] + j, __ldcs(pages + (free - 1 - g))};
-    }, [&](int, int, const Page &p) { table[p.at] = p.id; });
+    each_output(e, rows, total,
+                [&](int r, int start) { return static_cast<long long>(r) * static_cast<long long>(stride) + e.places[r] - start; },
+                [&](long long, int g) { return __ldcs(pages + (free - 1 - g)); },
+                [&](long long row, int g, int id) { table[row + g] = id; });
 }
 
 template <bool IN_SHARED>
@@ -313,24 +320,34 @@ slot_kernel(const int32_t *__restrict__ table, size_t stride, int rows, int widt
     const int tid = blockIdx.x * kPagedThreads + threadIdx.x, threads = gridDim.x * kPagedThreads;
     for (int r = tid; r < rows; r += threads) starts[r + 1] = e.ends[r];
     if (tid == 0) starts[0] = 0;
+    struct Row {
+        const int32_t *entries;
+        long long before;         // position of output g: before + g
+        int id;                   // -1: past the last row
+    };
     struct Place {
         int pos, entry, offset;   // -1: none
     };
-    each_output(e, rows, tokens, [&](int, int r, int j) {
-        Place p{-1, -1, 0};
-        if (r >= rows) return p;
-        const long long at = static_cast<long long>(e.places[r]) + j;
-        if (at < 0 || at > INT32_MAX) return p;
-        p.pos = static_cast<int>(at);
-        const uint32_t b = page.div(p.pos);
-        p.offset = static_cast<int>(p.pos - b * page.page);
-        if (b < static_cast<uint32_t>(width)) p.entry = __ldg(table + static_cast<size_t>(r) * stride + b);
-        return p;
-    }, [&](int g, int r, const Place &p) {
-        __stcs(slots + g, p.entry < 0 ? -1ll : static_cast<long long>(p.entry) * page.page + p.offset);
-        __stcs(positions + g, p.pos);
-        __stcs(row_ids + g, r < rows ? r : -1);
-    });
+    each_output(e, rows, tokens,
+                [&](int r, int start) {
+                    return r < rows ? Row{table + static_cast<size_t>(r) * stride, static_cast<long long>(e.places[r]) - start, r}
+                                    : Row{nullptr, 0, -1};
+                },
+                [&](const Row &row, int g) {
+                    Place p{-1, -1, 0};
+                    const long long at = row.before + g;
+                    if (row.id < 0 || at < 0 || at > INT32_MAX) return p;
+                    p.pos = static_cast<int>(at);
+                    const uint32_t b = page.div(p.pos);
+                    p.offset = static_cast<int>(p.pos - b * page.page);
+                    if (b < static_cast<uint32_t>(width)) p.entry = __ldg(row.entries + b);
+                    return p;
+                },
+                [&](const Row &row, int g, const Place &p) {
+                    __stcs(slots + g, p.entry < 0 ? -1ll : static_cast<long long>(p.entry) * page.page + p.offset);
+                    __stcs(positions + g, p.pos);
+                    __stcs(row_ids + g, row.id);
+                });
 }
 
 template <bool IN_SHARED>
@@ -344,8 +361,10 @@ release_kernel(const int32_t *__restrict__ table, size_t stride, int rows, Relea
     const int served = warp_row_of(e.ends, 0, rows, pool - free);   // rows whose pages fit the pool array
     const int total = served > 0 ? e.ends[served - 1] : 0;
     if (blockIdx.x == 0 && threadIdx.x == 0) *left = free + total;
-    each_output(e, rows, total, [&](int, int r, int j) { return __ldcs(table + static_cast<size_t>(r) * stride + j); },
-                [&](int g, int, int id) { pages[free + g] = id; });
+    each_output(e, rows, total,
+                [&](int r, int start) { return static_cast<long long>(r) * static_cast<long long>(stride) - start; },
+                [&](long long row, int g) { return __ldcs(table + row + g); },
+                [&](long long, int g, int id) { pages[free + g] = id; });
 }
 
 // Blocks for `most` output elements at the most.
