@@ -218,12 +218,11 @@ struct Shared {
     u64 won[kMaxCluster];
     float rest[kMaxCluster];
     uint32_t tops[kMaxCluster];
-    u64 mass[kMaxCluster];           // of their parts of a histogram
-    u64 cut, pick_want;
-    uint32_t pick_bin, next[2];
+    u64 cut;
+    uint32_t next[2];
     // Results of one block's scans.
-    u64 pick_key;
-    uint32_t pick_edge[2];
+    u64 pick_key, pick_want;
+    uint32_t pick_bin, pick_edge[2];
     uint32_t listed;                 // tokens collected by this block (counting stops above its region)
 };
 // Keys that block 0's inbox has room for: a wide cluster's blocks do not all
@@ -265,6 +264,7 @@ template <class T, bool KEEP>
 struct Draw {
     using C = Chunk<T>;
     static constexpr int kEach = C::kEach;
+    static constexpr int kPair = 8 / kEach, kOwn = kPair * kEach;   // chunks, and values, that a dense pass takes at once
 
     Shared &s;
     u64 *inbox;                      // in block 0: the cluster's tokens, a region of `region` per block
@@ -463,13 +463,36 @@ struct Draw {
         if (infinite) only_infinite(q);
         return C::most(q, -inf()) >= low;
     }
-    // The same where they are most of a kept slice: every thread its own, in
-    // the order of their indices.
-    template <class F>
-    __device__ __forceinline__ void each_own_chunk(float low, F f)
+    // Dense passes of a kept slice: every thread its own chunks, kPair at a
+    // time (c and c + kThreads), in the order of their indices.  Whether one of
+    // the pair at c has a value of at least `low`; its values.
+    __device__ __forceinline__ bool own(unsigned c, float low, float (&x)[kOwn]) const
     {
-#pragma unroll 1
-        for (unsigned c = tid; c < mine; c += kThreads) visit(kept[c], low, c, f);
+        float most = -inf();
+#pragma unroll
+        for (int u = 0; u < kPair; ++u) {
+            uint32_t q[4];
+            unpack(c + u * kThreads < mine ? kept[c + u * kThreads] : fill(), q);
+            if (infinite) only_infinite(q);
+            most = C::most(q, most);
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) x[u * kEach + e] = C::value(q, e);
+        }
+        return most >= low;
+    }
+    __device__ __forceinline__ int own_index(unsigned c, int e) const
+    {
+        return index_at(c + e / kEach * kThreads) + e % kEach;
+    }
+    __device__ __forceinline__ void own_noise(unsigned c, bool aligned, float (&n)[kOwn]) const
+    {
+#pragma unroll
+        for (int u = 0; u < kPair; ++u) {
+            float part[kEach];
+            load_noise(c + u * kThreads, aligned, part);
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) n[u * kEach + e] = part[e];
+        }
     }
     template <class F>
     __device__ __forceinline__ void visit(const uint4 &v, float low, unsigned c, F &&f)
@@ -579,21 +602,21 @@ struct Draw {
     // The race of a chunk's tokens for which keep(value, index) holds and
     // whose weight is at least m.  RISING: this thread's indices rise, so the
     // first of equal scores stays.
-    template <bool RISING, class Keep>
-    __device__ __forceinline__ void race_chunk(const float (&x)[kEach], const float (&n)[kEach], unsigned c, float m,
-                                               Keep keep, Race &o) const
+    template <bool RISING, int N, class Keep>
+    __device__ __forceinline__ void race_chunk(const float (&x)[N], const float (&n)[N], unsigned c, float m, Keep keep,
+                                               Race &o) const
     {
-        const int i = index_at(c);
 #pragma unroll
-        for (int e = 0; e < kEach; ++e) {
+        for (int e = 0; e < N; ++e) {
+            const int i = own_index(c, e);
             float w = weight(x[e]);
-            w = keep(x[e], i + e) & (w >= m) ? w : -1.0f;   // its score is below every other's
+            w = keep(x[e], i) & (w >= m) ? w : -1.0f;   // its score is below every other's
             const float sc = w < 0.0f ? -1.0f : w * reciprocal(n[e]);
             if (RISING) {
-                o.at = sc > o.score ? i + e : o.at;
+                o.at = sc > o.score ? i : o.at;
                 o.score = sc > o.score ? sc : o.score;
-            } else if (sc >= o.score && (sc > o.score || i + e < o.at)) {
-                o.score = sc, o.at = i + e;
+            } else if (sc >= o.score && (sc > o.score || i < o.at)) {
+                o.score = sc, o.at = i;
             }
             o.tops += w == 1.0f ? 1u : 0u;
             o.rest += w == 1.0f ? 0.0f : fmaxf(w, 0.0f);
@@ -602,9 +625,9 @@ struct Draw {
     // Starts the noise of the chunks with a value of at least `low` towards L2.
     __device__ __forceinline__ void prefetch_noise(float low)
     {
-        each_own_chunk(low, [&](const float (&)[kEach], unsigned c) {
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(noise + max(index_at(c), 0)));
-        });
+#pragma unroll 1
+        for (unsigned c = tid; c < mine; c += kThreads)
+            if (reaches(c, low)) asm volatile("prefetch.global.L2 [%0];" ::"l"(noise + max(index_at(c), 0)));
     }
 
     __device__ __forceinline__ void write(u64 won, const Race &o, int32_t *token, float *logprob) const
@@ -823,30 +846,33 @@ struct Draw {
         reinterpret_cast<uint4 *>(carry)[tid] = make_uint4(0, 0, 0, 0);
         __syncthreads();
         uint32_t last = 0;
-        each_own_chunk(low, [&](const float (&x)[kEach], unsigned c) {
+#pragma unroll 1
+        for (unsigned c = tid; c < mine; c += kPair * kThreads) {
+            float x[kOwn];
+            if (!own(c, low, x)) continue;
             // Nothing branches before the chunk's atomics are all in flight: a
             // value that takes no part adds 0 to a word of its lane's own.
-            uint32_t *at[kEach], holds[kEach], old[kEach], carried = 0;
+            uint32_t *at[kOwn], holds[kOwn], old[kOwn], carried = 0;
 #pragma unroll
-            for (int e = 0; e < kEach; ++e) {
-                const int b = bin_in(x[e], index_at(c) + e);
+            for (int e = 0; e < kOwn; ++e) {
+                const int b = bin_in(x[e], own_index(c, e));
                 const bool in = b >= 0 & (MASS | b != kBins - 1);
                 last += !MASS & b == kBins - 1 ? 1u : 0u;
                 at[e] = count + (in ? b : kBins + static_cast<int>(lane));
                 holds[e] = in ? (MASS ? mass(x[e]) : 1u) : 0u;
             }
 #pragma unroll
-            for (int e = 0; e < kEach; ++e) old[e] = shared_add(at[e], holds[e]);
+            for (int e = 0; e < kOwn; ++e) old[e] = shared_add(at[e], holds[e]);
             if (MASS) {
 #pragma unroll
-                for (int e = 0; e < kEach; ++e) carried |= old[e] + holds[e] < old[e] ? 1u << e : 0u;
+                for (int e = 0; e < kOwn; ++e) carried |= old[e] + holds[e] < old[e] ? 1u << e : 0u;
                 if (carried != 0) {
 #pragma unroll
-                    for (int e = 0; e < kEach; ++e)
+                    for (int e = 0; e < kOwn; ++e)
                         if (carried >> e & 1) shared_add(at[e] + (kBins + 32), 1);
                 }
             }
-        });
+        }
         if (!MASS) {
             last = __reduce_add_sync(kFullMask, last);
             if (lane == 0 && last != 0) shared_add(&count[kBins - 1], last);
@@ -859,47 +885,30 @@ struct Draw {
         put(reinterpret_cast<uint4 *>(low_parts + at), owner, low4);
         put(reinterpret_cast<uint4 *>(high_parts + at), owner, high4);
         meet();
-        // Thread t sums the part's bins from per * t on.
-        const unsigned per = (part + kThreads - 1) / kThreads;
-        u64 h[kBins / kThreads], own = 0;
-#pragma unroll
-        for (unsigned k = 0; k < kBins / kThreads; ++k) {
-            h[k] = 0;
-            if (k < per && per * tid + k < part) {
+        // Its sums go to every block, into the memory of its own list, which is
+        // not in use between merge_lists() and begin_list(); each block then
+        // finds the bin for itself.
+        u64 *sums = s.list;
 #pragma unroll 1
-                for (unsigned r = 0; r < blocks; ++r) {
-                    const unsigned b = r * part + per * tid + k;
-                    h[k] += low_parts[b] | static_cast<u64>(high_parts[b]) << 32;
-                }
-            }
-            own += h[k];
-        }
-        u64 all = 0;
-        u64 before = block_scan(own, s.warp64, &all);
-        if (blocks > 1) {
-            if (tid < blocks) put(&s.mass[rank], tid, all);
-            meet();
-            const unsigned r0 = rank;
-            all = 0;
+        for (unsigned b = tid; b < part; b += kThreads) {
+            u64 h = 0;
 #pragma unroll 1
-            for (unsigned r = 0; r < blocks; ++r) {
-                if (r == r0) before += all;
-                all += s.mass[r];
-            }
+            for (unsigned r = 0; r < blocks; ++r) h += low_parts[r * part + b] | static_cast<u64>(high_parts[r * part + b]) << 32;
+#pragma unroll 1
+            for (unsigned r = 0; r < blocks; ++r) put(&sums[rank * part + b], r, h);
         }
+        meet();
+        const ulonglong2 h01 = reinterpret_cast<const ulonglong2 *>(sums)[2 * tid];
+        const ulonglong2 h23 = reinterpret_cast<const ulonglong2 *>(sums)[2 * tid + 1];
+        const u64 h[4] = {h01.x, h01.y, h23.x, h23.y};
+        u64 all = 0, before = block_scan(h[0] + h[1] + h[2] + h[3], s.warp64, &all);
         want = wanted(all);
 #pragma unroll
-        for (unsigned k = 0; k < kBins / kThreads; ++k) {
-            if (before < want && want <= before + h[k]) {
-#pragma unroll 1
-                for (unsigned r = 0; r < blocks; ++r) {
-                    put(&s.pick_bin, r, rank * part + per * tid + k);
-                    put(&s.pick_want, r, want - before);
-                }
-            }
+        for (int k = 0; k < 4; ++k) {
+            if (before < want && want <= before + h[k]) s.pick_bin = 4 * tid + k, s.pick_want = want - before;
             before += h[k];
         }
-        meet();   // the histogram's memory is used again from here
+        __syncthreads();
         if (all < want) return false;
         bin = s.pick_bin;
         want = s.pick_want;
@@ -911,6 +920,10 @@ struct Draw {
     __device__ __forceinline__ uint32_t edge(int b) const
     {
         uint32_t from = ordered(-FLT_MAX), to = ordered(top);
+        // As a rule within a few roundings of where the bin ends.
+        const uint32_t near = max(min(ordered(top - (static_cast<float>(b) + 0.5f) / bins_per_unit), to), from + 16) - 16;
+        const unsigned probed = __ballot_sync(kFullMask, bin_of(unordered(min(near + lane, to))) <= b);
+        if ((probed & 1) == 0 && probed != 0) return near + __ffs(probed) - 1;
 #pragma unroll 1
         while (from < to) {
             const uint32_t step = (to - from) / 32 + 1;
@@ -1055,37 +1068,41 @@ struct Draw {
         begin_list();
         const bool aligned = reinterpret_cast<uintptr_t>(noise + first) % 16 == 0;
         unsigned waiting = 0;
-        const unsigned rounds = (mine + kThreads - 1) / kThreads;
-        const auto listed = [&](const float (&x)[kEach], unsigned c) {
-            uint32_t which = 0;
-#pragma unroll
-            for (int e = 0; e < kEach; ++e)
-                which |= x[e] >= v_lo & x[e] <= v_hi & floor.takes(x[e], index_at(c) + e) ? 1u << e : 0u;
-            return which;
-        };
-        // A chunk's noise is on its way while the chunk before it races.
-        bool in = reaches(tid, low);
-        float n[kEach];
-        if (in) load_noise(tid, aligned, n);
+        const unsigned rounds = (mine + kPair * kThreads - 1) / (kPair * kThreads);
+        const auto in_range = [&](float v, int i) { return v >= v_lo & v <= v_hi & floor.takes(v, i); };
+        // A pair's noise is on its way while the pair before it races.
+        float x[kOwn], n[kOwn];
+        bool in = own(tid, low, x);
+        if (in) own_noise(tid, aligned, n);
 #pragma unroll 1
         for (unsigned k = 0; k <= rounds; ++k) {
-            const unsigned c = k * kThreads + tid, then = c + kThreads;
-            const bool in_then = reaches(then, low);
-            float n_then[kEach];
-            if (in_then) load_noise(then, aligned, n_then);
+            const unsigned c = k * kPair * kThreads + tid, then = c + kPair * kThreads;
+            float x_then[kOwn], n_then[kOwn];
+            const bool in_then = own(then, low, x_then);
+            if (in_then) own_noise(then, aligned, n_then);
             bool some = false;
-            if (in)
-                visit(kept[c], low, c, [&](const float (&x)[kEach], unsigned) {
-                    race_chunk<true>(x, n, c, m, [&](float v, int) { return v > v_hi; }, o);
-                    some = listed(x, c) != 0;
-                });
+            if (in) {
+                race_chunk<true>(x, n, c, m, [&](float v, int) { return v > v_hi; }, o);
+#pragma unroll
+                for (int e = 0; e < kOwn; ++e) some |= in_range(x[e], own_index(c, e));
+            }
             queue_up(waiting, some, k * 32 + lane, k == rounds, [&](unsigned at) {
-                const unsigned from = (at / 32) * kThreads + warp * 32 + at % 32;
-                visit(kept[from], low, from, [&](const float (&x)[kEach], unsigned) { add_tokens(x, from, listed(x, from)); });
+                const unsigned from = (at / 32) * kPair * kThreads + warp * 32 + at % 32;
+#pragma unroll 1
+                for (int u = 0; u < kPair; ++u) {
+                    const unsigned f = from + u * kThreads;
+                    if (f >= mine) continue;
+                    visit(kept[f], low, f, [&](const float (&v)[kEach], unsigned) {
+                        uint32_t which = 0;
+#pragma unroll
+                        for (int e = 0; e < kEach; ++e) which |= in_range(v[e], index_at(f) + e) ? 1u << e : 0u;
+                        add_tokens(v, f, which);
+                    });
+                }
             });
             in = in_then;
 #pragma unroll
-            for (int e = 0; e < kEach; ++e) n[e] = n_then[e];
+            for (int e = 0; e < kOwn; ++e) x[e] = x_then[e], n[e] = n_then[e];
         }
         const uint32_t tokens = merge_lists(nullptr);
         if (tokens > kList) {
