@@ -62,7 +62,7 @@ constexpr unsigned kLeastChunks = 512;     // of a block's slice, where rows are
 constexpr unsigned kKeptChunks = 4096;     // of a kept slice, for two blocks per SM: 64 KB
 constexpr int kList = 1024;                // tokens the short list holds
 constexpr int kBins = 1024;
-constexpr float kCountSpan = 16.0f;        // first histogram of counts: logits below the largest that it resolves
+constexpr float kCountSpan = 16.0f;        // first histogram of counts: logits below the largest, where nothing says how far
 constexpr float kMassSpan = 23.0f;         // of masses: in temperatures; below, a weight rounds to no mass
 constexpr int kGuess = 256, kGuessEach = 16;   // tokens asked of the bound for top-p without top-k: in all, per warp at most
 
@@ -283,6 +283,7 @@ struct Draw {
     int first;                       // index of the slice's first value
     float top, t, scale;             // the largest logit, temperature, log2(e) / T
     float bins_per_unit;             // of the first histogram
+    float reach;                     // logits below the largest where the first k are expected to end
     bool infinite = false;           // the largest is +inf: it counts as 0, all else as -inf
     int turn = 0;                    // which half of the double buffers is next
 
@@ -957,7 +958,7 @@ struct Draw {
     __device__ __forceinline__ bool bracket(const Floor &floor, Want wanted, u64 &want, uint32_t &lo_bits, uint32_t &hi_bits)
     {
         uint32_t bin = 0;
-        const float span = MASS ? kMassSpan * t : kCountSpan;
+        const float span = MASS ? kMassSpan * t : reach;
         bins_per_unit = fminf(fmaxf((kBins - 1) / span, 1e-30f), 1e30f);
         const float least = MASS ? fmaxf(floor.v, top - span) : floor.v;
         if (!histogram<MASS>(least, [&](float v, int i) { return floor.takes(v, i) & v >= least ? bin_of(v) : -1; },
@@ -1224,6 +1225,9 @@ __device__ __forceinline__ void draw_row(Draw<T, kKeeps<PASS>> &d, unsigned r, c
             }
         }
     }
+    // For a histogram of counts, the least lane maximum: as many tokens as
+    // there are lanes are at or above it.
+    if (HISTOGRAMS && cuts && !bounded) bound = __reduce_min_sync(kFullMask, d.tid < d.mine ? lane_top : ~0u);
     if (d.lane == 0) s.warp_a[d.warp] = warp_top, s.warp_b[d.warp] = bound;
     __syncthreads();
     uint32_t top = __reduce_max_sync(kFullMask, s.warp_a[d.lane & (kWarps - 1)]);
@@ -1258,6 +1262,11 @@ __device__ __forceinline__ void draw_row(Draw<T, kKeeps<PASS>> &d, unsigned r, c
         return;
     }
 
+    // A little further than the bound, and twice as far for more tokens than
+    // lanes; what lies further still is in the histogram's last bin.
+    d.reach = (d.top - unordered(max(bound, kOrderedMinusInf))) * (bounded || static_cast<unsigned>(k) <= d.blocks * kThreads ? 1.02f : 2.0f);
+    if (!(d.reach > 0.0f && d.reach < FLT_MAX)) d.reach = kCountSpan;
+
     u64 cut = 0;
     if (greedy) {
         d.each_chunk(d.top, [&](const float (&x)[D::kEach], unsigned c) {
@@ -1270,7 +1279,9 @@ __device__ __forceinline__ void draw_row(Draw<T, kKeeps<PASS>> &d, unsigned r, c
         return;
     }
     if (cuts) {
-        if (listed) {
+        if (listed && !bounded && vocab > kList) {   // more tokens than the list holds
+            if (!HISTOGRAMS && first_thread) later.decide(true, r);
+        } else if (listed) {
             const float low = bounded ? fmaxf(unordered(max(bound, kOrderedMinusInf)), -FLT_MAX) : -FLT_MAX;
             float above = 0.0f, total = 0.0f;
             if (whole) {
