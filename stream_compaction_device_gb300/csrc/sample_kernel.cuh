@@ -1416,12 +1416,12 @@ sample_kernel(const SampleCall call, unsigned per, const Deferred later)
         if (!ready && d.tid == 0) atomicOr(later.error, kErrTimeout);
         // A cluster's first row by its place, then whichever is next; asked for
         // while the row before it is drawn.
-        const unsigned n = ready ? *later.count : 0, clusters = gridDim.x / d.blocks;
+        const unsigned n = ready ? __ldcg(later.count) : 0, clusters = gridDim.x / d.blocks;
 #pragma unroll 1
         for (unsigned w = blockIdx.x / d.blocks, turn = 0; w < n; w = s.next[turn], turn ^= 1) {
             unsigned next = 0;
             if (d.rank == 0 && d.tid == 0) next = clusters + atomicAdd(later.next, 1u);
-            draw_row<T, PASS>(d, later.rows[w], call, per, later);
+            draw_row<T, PASS>(d, __ldcg(later.rows + w), call, per, later);
             if (d.rank == 0 && d.tid == 0) {
 #pragma unroll 1
                 for (unsigned b = 0; b < d.blocks; ++b) put(&s.next[turn], b, next);
