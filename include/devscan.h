@@ -1,6 +1,7 @@
 /*
  * devscan -- device-wide parallel prefix scan, stream compaction and radix
- * one-bit split for one NVIDIA GB300 GPU (sm_103a).
+ * one-bit split for one NVIDIA GB300 GPU (sm_103a), and the selections and
+ * bookkeeping of a model's serving step that are made of them.
  *
  * C ABI.  Every pointer argument of a compute call is a DEVICE pointer owned
  * by the caller; the library never frees, retains or reallocates it.  Every
@@ -395,10 +396,12 @@ devscan_status block_table_release_i32(const int32_t *table, size_t stride, size
  *   token = the kept i with the largest w_i / noise_i (equal: lowest index),
  * which falls on i with probability w_i / (sum of kept w), and
  *   logprob = (x_token - M) / T - log(sum of kept w).
- * T <= 0 (or NaN), or noise == NULL, takes the first of the order (greedy;
- * logprob 0).  A NaN logit counts as -inf, and -inf is never drawn; a row
- * with nothing above -inf gets token -1 and logprob -inf.  If the largest is
- * +inf, the draw is among those that are.
+ * T <= 0, min_p > 1, a setting that is NaN, or noise == NULL takes the first
+ * of the order (greedy; logprob 0).  A NaN logit counts as -inf, and -inf is
+ * never drawn; a row with nothing above -inf gets token -1 and logprob -inf.
+ * If the largest is +inf, the draw is among those that are.  Noise that is
+ * not positive and finite loses; where all of a row's kept tokens have such,
+ * the token is one of the row or -1.
  *
  *   logits   : device T[rows][logits_stride] (f16 and bf16 as their 16 bits),
  *              aligned to the element; vocab <= logits_stride;
@@ -409,9 +412,18 @@ devscan_status block_table_release_i32(const int32_t *table, size_t stride, size
  *              neither may overlap another buffer (DEVSCAN_ERR_INVALID);
  *   rows     : at most INT32_MAX; 0 is a no-op;
  *   vocab    : 1 .. DEVSCAN_SAMPLE_MAX_VOCAB, else DEVSCAN_ERR_INVALID.
- * Weights and their sums are fp32 or wider; the masses that top-p compares
- * are exact sums of w rounded to 2^-31, so the kept set does not depend on
- * the order of the adds.
+ * Weights are fp32 (below 2^-126 they count as 0); sums are fp32 in a fixed
+ * order, or integers of w in units of 2^-31 in 64 bits, so that the same call
+ * gives the same bits.  A token at the edge of top-p may fall on either side
+ * where its mass ahead is within rounding of the mark.
+ * Traffic: each row once, the noise of the kept tokens (all of it where
+ * nothing truncates); rows whose cut is far down the order (a top-k above a
+ * few hundred, or a nearly flat row with top-p) are read once more.  One
+ * launch, or two where the rows are many and large, the second for those rows;
+ * 4 bytes per row of per-stream scratch are allocated stream-ordered on first
+ * use if top_k or top_p is given (DEVSCAN_ERR_NOMEM).  The second launch
+ * waits, for a bounded time, for the first to have seen every row; if that
+ * runs out, devscan_device_status() reports DEVSCAN_ERR_TIMEOUT.
  * ------------------------------------------------------------------------- */
 #define DEVSCAN_SAMPLE_MAX_VOCAB ((size_t)1 << 18)
 

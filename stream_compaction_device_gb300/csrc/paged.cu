@@ -18,8 +18,15 @@
 // to 20, so every block scans all the counts for itself (out of L2, into its
 // shared memory) and takes an equal share of the output: one launch, no block
 // waits for another, and one long row is spread over the whole GPU.  A warp
-// takes up to 4,096 neighbouring outputs and looks for the rows of the first and the
-// last of them.
+// takes up to 128 or 256 neighbouring outputs and looks for the rows of the
+// first and the last of them.
+//
+// What bounds it: a call of few rows its launch and one wait for memory (64
+// rows 4.9 us, 256 rows 3.9 us by device time, of which an empty kernel takes
+// more than half); 4,096 rows the scan in front (6.4 us with nothing to move)
+// and then memory: with nothing in L2 they extend by 2.8 M pages in 16 us and
+// release 2.1 M in 15 us (22 and 17 MB, 3.3 and 2.5 us at the copy rate), and
+// 2.7 M slots of 1,000 rows take 12 us (44 MB, 6.5 us).
 // Sums run in 64 bits and are stored saturated to INT32_MAX, so that lengths
 // whose sum passes 32 bits cannot wrap into positions that look valid.
 #include "core.cuh"
@@ -30,7 +37,11 @@ namespace {
 
 constexpr int kPagedThreads = 512;
 constexpr int kPagedWarps = kPagedThreads / 32;
-constexpr int kChunk = 4096;   // consecutive outputs that a warp takes at a time, at most
+// Consecutive outputs that a warp takes at a time, at most.  Small chunks keep
+// what the grid touches at one time close together in memory: 4,096 rows with
+// nothing in L2 took (us, chunks of 128 : 256 : 512) 15.1 : 17.6 : 17.8 to
+// release, 15.8 : 15.7 : 20.4 to extend, and 2.7 M slots 14.1 : 12.1 : 12.6.
+constexpr int kMoveChunk = 128, kSlotChunk = 256;
 
 // Division of any uint32 by the page size, by a multiplication with its
 // reciprocal rounded up to 33 bits (Granlund and Montgomery, "Division by
@@ -241,14 +252,14 @@ __device__ __forceinline__ Ends row_ends(const Count &count, int rows, const End
 // time; row == rows past the last one.  A chunk of few rows goes row by row,
 // with no search and one c for a run; one of many rows (a decode step brings
 // one output a row, or none) searches for every output's.
-template <class OfRow, class Load, class Store>
+template <int CHUNK, class OfRow, class Load, class Store>
 __device__ __forceinline__ void each_output(const Ends &e, int rows, int total, OfRow of_row, Load load, Store store)
 {
     constexpr int kAtOnce = 4, kFewRows = 4;
     const int lane = threadIdx.x & 31;
     const int warps = static_cast<int>(gridDim.x) * kPagedWarps;
-    // One chunk per warp: every chunk costs two searches and its own waits.
-    const int share = (total / warps + 32) / 32 * 32, chunk = share > kChunk ? kChunk : share;
+    // Fewer to a chunk where that gives every warp one.
+    const int share = (total / warps + 32) / 32 * 32, chunk = share > CHUNK ? CHUNK : share;
     const auto start_of = [&](int r) { return r > 0 ? e.ends[r - 1] : 0; };
     for (long long first = (static_cast<long long>(blockIdx.x) * kPagedWarps + (threadIdx.x >> 5)) * chunk;
          first < total; first += static_cast<long long>(warps) * chunk) {
@@ -304,10 +315,10 @@ extend_kernel(int32_t *__restrict__ table, size_t stride, int rows, ExtendCount 
         granted[r] = e.places[r] >= 0 && (!needs || end <= free);
     }
     if (tid == 0) *left = free - total;
-    each_output(e, rows, total,
-                [&](int r, int start) { return static_cast<long long>(r) * static_cast<long long>(stride) + e.places[r] - start; },
-                [&](long long, int g) { return __ldcs(pages + (free - 1 - g)); },
-                [&](long long row, int g, int id) { table[row + g] = id; });
+    each_output<kMoveChunk>(e, rows, total,
+                            [&](int r, int start) { return r * static_cast<long long>(stride) + e.places[r] - start; },
+                            [&](long long, int g) { return __ldcs(pages + (free - 1 - g)); },
+                            [&](long long row, int g, int id) { table[row + g] = id; });
 }
 
 template <bool IN_SHARED>
@@ -328,26 +339,25 @@ slot_kernel(const int32_t *__restrict__ table, size_t stride, int rows, int widt
     struct Place {
         int pos, entry, offset;   // -1: none
     };
-    each_output(e, rows, tokens,
-                [&](int r, int start) {
-                    return r < rows ? Row{table + static_cast<size_t>(r) * stride, static_cast<long long>(e.places[r]) - start, r}
-                                    : Row{nullptr, 0, -1};
-                },
-                [&](const Row &row, int g) {
-                    Place p{-1, -1, 0};
-                    const long long at = row.before + g;
-                    if (row.id < 0 || at < 0 || at > INT32_MAX) return p;
-                    p.pos = static_cast<int>(at);
-                    const uint32_t b = page.div(p.pos);
-                    p.offset = static_cast<int>(p.pos - b * page.page);
-                    if (b < static_cast<uint32_t>(width)) p.entry = __ldg(row.entries + b);
-                    return p;
-                },
-                [&](const Row &row, int g, const Place &p) {
-                    __stcs(slots + g, p.entry < 0 ? -1ll : static_cast<long long>(p.entry) * page.page + p.offset);
-                    __stcs(positions + g, p.pos);
-                    __stcs(row_ids + g, row.id);
-                });
+    const auto row_at = [&](int r, int start) {
+        return r < rows ? Row{table + static_cast<size_t>(r) * stride, static_cast<long long>(e.places[r]) - start, r}
+                        : Row{nullptr, 0, -1};
+    };
+    const auto place_of = [&](const Row &row, int g) {
+        Place p{-1, -1, 0};
+        const long long at = row.before + g;
+        if (row.id < 0 || at < 0 || at > INT32_MAX) return p;
+        p.pos = static_cast<int>(at);
+        const uint32_t b = page.div(p.pos);
+        p.offset = static_cast<int>(p.pos - b * page.page);
+        if (b < static_cast<uint32_t>(width)) p.entry = __ldg(row.entries + b);
+        return p;
+    };
+    each_output<kSlotChunk>(e, rows, tokens, row_at, place_of, [&](const Row &row, int g, const Place &p) {
+        __stcs(slots + g, p.entry < 0 ? -1ll : static_cast<long long>(p.entry) * page.page + p.offset);
+        __stcs(positions + g, p.pos);
+        __stcs(row_ids + g, row.id);
+    });
 }
 
 template <bool IN_SHARED>
@@ -361,10 +371,10 @@ release_kernel(const int32_t *__restrict__ table, size_t stride, int rows, Relea
     const int served = warp_row_of(e.ends, 0, rows, pool - free);   // rows whose pages fit the pool array
     const int total = served > 0 ? e.ends[served - 1] : 0;
     if (blockIdx.x == 0 && threadIdx.x == 0) *left = free + total;
-    each_output(e, rows, total,
-                [&](int r, int start) { return static_cast<long long>(r) * static_cast<long long>(stride) - start; },
-                [&](long long row, int g) { return __ldcs(table + row + g); },
-                [&](long long, int g, int id) { pages[free + g] = id; });
+    each_output<kMoveChunk>(e, rows, total,
+                            [&](int r, int start) { return r * static_cast<long long>(stride) - start; },
+                            [&](long long row, int g) { return __ldcs(table + row + g); },
+                            [&](long long, int g, int id) { pages[free + g] = id; });
 }
 
 // Blocks for `most` output elements at the most.
