@@ -28,7 +28,9 @@
 // release 2.1 M in 15 us (22 and 17 MB, 3.3 and 2.5 us at the copy rate), and
 // 2.7 M slots of 1,000 rows take 12 us (44 MB, 6.5 us).
 // Sums run in 64 bits and are stored saturated to INT32_MAX, so that lengths
-// whose sum passes 32 bits cannot wrap into positions that look valid.
+// whose sum passes 32 bits cannot wrap into positions that look valid.  Rows
+// and outputs are counted without sign: there may be nearly 2^31 of either,
+// and a step past the last one must not wrap.
 #include "core.cuh"
 #include "launch.h"
 
@@ -74,10 +76,11 @@ struct RowPart {
 constexpr int kRun = 8;   // neighbouring rows that a thread scans
 
 // v[k] = p[r + k] for the rows before `rows`; 0 for the others.
-__device__ __forceinline__ void load_run(const int32_t *p, int r, int rows, int (&v)[kRun])
+__device__ __forceinline__ void load_run(const int32_t *p, unsigned r, unsigned rows, int (&v)[kRun])
 {
     if (r + kRun <= rows && reinterpret_cast<uintptr_t>(p + r) % 16 == 0) {
-        const int4 a = __ldg(reinterpret_cast<const int4 *>(p + r)), b = __ldg(reinterpret_cast<const int4 *>(p + r) + 1);
+        const int4 *q = reinterpret_cast<const int4 *>(p + r);
+        const int4 a = __ldg(q), b = __ldg(q + 1);
         v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
     } else {
 #pragma unroll
@@ -85,7 +88,7 @@ __device__ __forceinline__ void load_run(const int32_t *p, int r, int rows, int 
     }
 }
 // The same of flags; null: 1 for every row.
-__device__ __forceinline__ void load_run(const uint8_t *p, int r, int rows, int (&v)[kRun])
+__device__ __forceinline__ void load_run(const uint8_t *p, unsigned r, unsigned rows, int (&v)[kRun])
 {
     if (p != nullptr && r + kRun <= rows && reinterpret_cast<uintptr_t>(p + r) % 8 == 0) {
         const uint2 a = __ldg(reinterpret_cast<const uint2 *>(p + r));
@@ -104,14 +107,15 @@ struct ExtendCount {
     const int32_t *cached, *fresh;
     Pages pages;
     int width;
-    __device__ __forceinline__ void load(int r, int rows, int (&a)[kRun], int (&b)[kRun]) const
+    __device__ __forceinline__ void load(unsigned r, unsigned rows, int (&a)[kRun], int (&b)[kRun]) const
     {
         load_run(cached, r, rows, a);
         load_run(fresh, r, rows, b);
     }
     __device__ __forceinline__ RowPart part(int c, int n) const
     {
-        const uint32_t have = pages.blocks_of(c), want = pages.blocks_of(static_cast<uint32_t>(c) + static_cast<uint32_t>(n));
+        const uint32_t have = pages.blocks_of(c);
+        const uint32_t want = pages.blocks_of(static_cast<uint32_t>(c) + static_cast<uint32_t>(n));
         if (c < 0 || n < 0 || want > static_cast<uint32_t>(width)) return {0, -1};
         return {static_cast<int>(want - have), static_cast<int>(have)};
     }
@@ -121,7 +125,7 @@ struct ExtendCount {
 struct SlotCount {
     const int32_t *cached, *fresh;
     const uint8_t *granted;   // null: every row runs
-    __device__ __forceinline__ void load(int r, int rows, int (&a)[kRun], int (&b)[kRun]) const
+    __device__ __forceinline__ void load(unsigned r, unsigned rows, int (&a)[kRun], int (&b)[kRun]) const
     {
         int runs[kRun];
         load_run(cached, r, rows, a);
@@ -138,7 +142,7 @@ struct ReleaseCount {
     const uint8_t *done;
     Pages pages;
     int width;
-    __device__ __forceinline__ void load(int r, int rows, int (&a)[kRun], int (&b)[kRun]) const
+    __device__ __forceinline__ void load(unsigned r, unsigned rows, int (&a)[kRun], int (&b)[kRun]) const
     {
         load_run(cached, r, rows, a);
         load_run(done, r, rows, b);
@@ -154,20 +158,21 @@ struct ReleaseCount {
 // The scanned rows: ends[r] = min(count(0) + ... + count(r), INT32_MAX), and
 // places[r] as the row gave it.  In shared memory, or in global scratch.
 struct Ends {
-    int32_t *ends, *places;
+    uint32_t *ends;
+    int32_t *places;
 };
 
 // Scans the rows by one block, a run of neighbours per thread: one wait for
 // memory and one for the other warps in 4,096 rows.  Ends with a block barrier.
 template <class Count>
-__device__ void scan_rows(const Count &count, int rows, const Ends &out)
+__device__ void scan_rows(const Count &count, unsigned rows, const Ends &out)
 {
     __shared__ long long s_warp[2][kPagedWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     long long base = 0;
     int turn = 0;
-    for (int r0 = 0; r0 < rows; r0 += kPagedThreads * kRun, turn ^= 1) {
-        const int r = r0 + tid * kRun;
+    for (unsigned r0 = 0; r0 < rows; r0 += kPagedThreads * kRun, turn ^= 1) {
+        const unsigned r = r0 + tid * kRun;
         int a[kRun], b[kRun];
         long long sum = 0;
         count.load(r, rows, a, b);
@@ -198,7 +203,7 @@ __device__ void scan_rows(const Count &count, int rows, const Ends &out)
         for (int k = 0; k < kRun; ++k) {
             end += a[k];
             if (r + k >= rows) continue;
-            out.ends[r + k] = static_cast<int32_t>(end < INT32_MAX ? end : INT32_MAX);
+            out.ends[r + k] = static_cast<uint32_t>(end < INT32_MAX ? end : INT32_MAX);
             out.places[r + k] = b[k];
         }
     }
@@ -206,23 +211,23 @@ __device__ void scan_rows(const Count &count, int rows, const Ends &out)
 }
 
 // First row in [lo, hi) whose end is above g; hi if none.
-__device__ __forceinline__ int row_of(const int32_t *ends, int lo, int hi, int g)
+__device__ __forceinline__ unsigned row_of(const uint32_t *ends, unsigned lo, unsigned hi, unsigned g)
 {
     while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
+        const unsigned mid = (lo + hi) >> 1;
         if (ends[mid] > g) hi = mid;
         else lo = mid + 1;
     }
     return lo;
 }
 // The same over [lo, hi) by a whole warp: 32 probes a step.
-__device__ __forceinline__ int warp_row_of(const int32_t *ends, int lo, int hi, int g)
+__device__ __forceinline__ unsigned warp_row_of(const uint32_t *ends, unsigned lo, unsigned hi, unsigned g)
 {
-    const int lane = threadIdx.x & 31;
+    const unsigned lane = threadIdx.x & 31;
     while (lo < hi) {
-        const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+        const unsigned step = (hi - lo + 31) / 32, at = lo + lane * step;
         const unsigned above = __ballot_sync(kFullMask, at >= hi || ends[at] > g);
-        const int k = above == 0 ? 32 : __ffs(above) - 1;   // the first probe above; the one before it is not
+        const unsigned k = above == 0 ? 32 : __ffs(above) - 1;   // the first probe above; the one before it is not
         if (k < 32 && lo + k * step < hi) hi = lo + k * step;
         if (k > 0) lo = lo + (k - 1) * step + 1;
     }
@@ -230,7 +235,7 @@ __device__ __forceinline__ int warp_row_of(const int32_t *ends, int lo, int hi, 
 }
 
 template <class Count>
-__global__ void __launch_bounds__(kPagedThreads) row_ends_kernel(Count count, int rows, Ends out)
+__global__ void __launch_bounds__(kPagedThreads) row_ends_kernel(Count count, unsigned rows, Ends out)
 {
     scan_rows(count, rows, out);
 }
@@ -238,11 +243,11 @@ __global__ void __launch_bounds__(kPagedThreads) row_ends_kernel(Count count, in
 // IN_SHARED: the block scans the counts into its own shared memory; else
 // row_ends_kernel has left them in `scratch`.
 template <bool IN_SHARED, class Count>
-__device__ __forceinline__ Ends row_ends(const Count &count, int rows, const Ends &scratch)
+__device__ __forceinline__ Ends row_ends(const Count &count, unsigned rows, const Ends &scratch)
 {
-    extern __shared__ int32_t s_rows[];
+    extern __shared__ uint32_t s_rows[];
     if (!IN_SHARED) return scratch;
-    const Ends e{s_rows, s_rows + rows};
+    const Ends e{s_rows, reinterpret_cast<int32_t *>(s_rows + rows)};
     scan_rows(count, rows, e);
     return e;
 }
@@ -253,36 +258,35 @@ __device__ __forceinline__ Ends row_ends(const Count &count, int rows, const End
 // with no search and one c for a run; one of many rows (a decode step brings
 // one output a row, or none) searches for every output's.
 template <int CHUNK, class OfRow, class Load, class Store>
-__device__ __forceinline__ void each_output(const Ends &e, int rows, int total, OfRow of_row, Load load, Store store)
+__device__ __forceinline__ void each_output(const Ends &e, unsigned rows, unsigned total, OfRow of_row, Load load, Store store)
 {
-    constexpr int kAtOnce = 4, kFewRows = 4;
-    const int lane = threadIdx.x & 31;
-    const int warps = static_cast<int>(gridDim.x) * kPagedWarps;
+    constexpr unsigned kAtOnce = 4, kFewRows = 4;
+    const unsigned lane = threadIdx.x & 31;
+    const unsigned warps = gridDim.x * kPagedWarps;
     // Fewer to a chunk where that gives every warp one.
-    const int share = (total / warps + 32) / 32 * 32, chunk = share > CHUNK ? CHUNK : share;
-    const auto start_of = [&](int r) { return r > 0 ? e.ends[r - 1] : 0; };
-    for (long long first = (static_cast<long long>(blockIdx.x) * kPagedWarps + (threadIdx.x >> 5)) * chunk;
-         first < total; first += static_cast<long long>(warps) * chunk) {
-        const int g0 = static_cast<int>(first), g1 = total - g0 < chunk ? total : g0 + chunk;
-        const int lo = warp_row_of(e.ends, 0, rows, g0);
-        const int hi = lo < rows && e.ends[lo] >= g1 ? lo : warp_row_of(e.ends, lo, rows, g1 - 1);
+    const unsigned share = (total / warps + 32) / 32 * 32, chunk = share > CHUNK ? CHUNK : share;
+    const auto start_of = [&](unsigned r) { return r > 0 ? e.ends[r - 1] : 0u; };
+    for (unsigned g0 = (blockIdx.x * kPagedWarps + (threadIdx.x >> 5)) * chunk; g0 < total; g0 += warps * chunk) {
+        const unsigned g1 = total - g0 < chunk ? total : g0 + chunk;
+        const unsigned lo = warp_row_of(e.ends, 0, rows, g0);
+        const unsigned hi = lo < rows && e.ends[lo] >= g1 ? lo : warp_row_of(e.ends, lo, rows, g1 - 1);
         if (hi - lo < kFewRows) {
-            for (int r = lo; r <= hi; ++r) {
-                const int start = start_of(r), end = r < rows && e.ends[r] < g1 ? e.ends[r] : g1;
+            for (unsigned r = lo; r <= hi; ++r) {
+                const unsigned start = start_of(r), end = r < rows && e.ends[r] < g1 ? e.ends[r] : g1;
                 const auto c = of_row(r, start);
-                for (int g = (start > g0 ? start : g0) + lane; g < end; g += 32 * kAtOnce) {
+                for (unsigned g = (start > g0 ? start : g0) + lane; g < end; g += 32 * kAtOnce) {
                     decltype(load(c, 0)) v[kAtOnce];
 #pragma unroll
-                    for (int u = 0; u < kAtOnce; ++u)
+                    for (unsigned u = 0; u < kAtOnce; ++u)
                         if (g + 32 * u < end) v[u] = load(c, g + 32 * u);
 #pragma unroll
-                    for (int u = 0; u < kAtOnce; ++u)
+                    for (unsigned u = 0; u < kAtOnce; ++u)
                         if (g + 32 * u < end) store(c, g + 32 * u, v[u]);
                 }
             }
         } else {
-            for (int g = g0 + lane; g < g1; g += 32) {
-                const int r = row_of(e.ends, lo, hi, g);
+            for (unsigned g = g0 + lane; g < g1; g += 32) {
+                const unsigned r = row_of(e.ends, lo, hi, g);
                 const auto c = of_row(r, start_of(r));
                 store(c, g, load(c, g));
             }
@@ -298,38 +302,40 @@ __device__ __forceinline__ int clamp_free(const int32_t *free_count, int pool)
 
 template <bool IN_SHARED>
 __global__ void __launch_bounds__(kPagedThreads, 2)
-extend_kernel(int32_t *__restrict__ table, size_t stride, int rows, ExtendCount count,
+extend_kernel(int32_t *__restrict__ table, size_t stride, unsigned rows, ExtendCount count,
               const int32_t *__restrict__ pages, int pool, const int32_t *__restrict__ free_count,
               uint8_t *__restrict__ granted, int32_t *__restrict__ left, Ends scratch)
 {
-    const int free = clamp_free(free_count, pool);
+    const unsigned free = clamp_free(free_count, pool);
     const Ends e = row_ends<IN_SHARED>(count, rows, scratch);
     // Rows are served in order while the pool lasts: those whose end is within it.
-    const int served = warp_row_of(e.ends, 0, rows, free);
-    const int total = served > 0 ? e.ends[served - 1] : 0;
-    const int tid = blockIdx.x * kPagedThreads + threadIdx.x, threads = gridDim.x * kPagedThreads;
-    for (int r = tid; r < rows; r += threads) {
-        const int end = e.ends[r];
+    const unsigned served = warp_row_of(e.ends, 0, rows, free);
+    const unsigned total = served > 0 ? e.ends[served - 1] : 0;
+    const unsigned tid = blockIdx.x * kPagedThreads + threadIdx.x, threads = gridDim.x * kPagedThreads;
+    for (unsigned r = tid; r < rows; r += threads) {
+        const unsigned end = e.ends[r];
         const bool needs = end == INT32_MAX ? count.part(count.cached[r], count.fresh[r]).count != 0
-                                            : end != (r > 0 ? e.ends[r - 1] : 0);
+                                            : end != (r > 0 ? e.ends[r - 1] : 0u);
         granted[r] = e.places[r] >= 0 && (!needs || end <= free);
     }
     if (tid == 0) *left = free - total;
     each_output<kMoveChunk>(e, rows, total,
-                            [&](int r, int start) { return r * static_cast<long long>(stride) + e.places[r] - start; },
-                            [&](long long, int g) { return __ldcs(pages + (free - 1 - g)); },
-                            [&](long long row, int g, int id) { table[row + g] = id; });
+                            [&](unsigned r, unsigned start) {
+                                return r * static_cast<long long>(stride) + e.places[r] - start;
+                            },
+                            [&](long long, unsigned g) { return __ldcs(pages + (free - 1 - g)); },
+                            [&](long long row, unsigned g, int id) { table[row + g] = id; });
 }
 
 template <bool IN_SHARED>
 __global__ void __launch_bounds__(kPagedThreads, 2)
-slot_kernel(const int32_t *__restrict__ table, size_t stride, int rows, int width, SlotCount count, Pages page,
-            int tokens, int32_t *__restrict__ starts, long long *__restrict__ slots, int32_t *__restrict__ positions,
+slot_kernel(const int32_t *__restrict__ table, size_t stride, unsigned rows, int width, SlotCount count, Pages page,
+            unsigned tokens, int32_t *__restrict__ starts, long long *__restrict__ slots, int32_t *__restrict__ positions,
             int32_t *__restrict__ row_ids, Ends scratch)
 {
     const Ends e = row_ends<IN_SHARED>(count, rows, scratch);
-    const int tid = blockIdx.x * kPagedThreads + threadIdx.x, threads = gridDim.x * kPagedThreads;
-    for (int r = tid; r < rows; r += threads) starts[r + 1] = e.ends[r];
+    const unsigned tid = blockIdx.x * kPagedThreads + threadIdx.x, threads = gridDim.x * kPagedThreads;
+    for (unsigned r = tid; r < rows; r += threads) starts[r + 1] = static_cast<int32_t>(e.ends[r]);
     if (tid == 0) starts[0] = 0;
     struct Row {
         const int32_t *entries;
@@ -339,11 +345,12 @@ slot_kernel(const int32_t *__restrict__ table, size_t stride, int rows, int widt
     struct Place {
         int pos, entry, offset;   // -1: none
     };
-    const auto row_at = [&](int r, int start) {
-        return r < rows ? Row{table + static_cast<size_t>(r) * stride, static_cast<long long>(e.places[r]) - start, r}
+    const auto row_at = [&](unsigned r, unsigned start) {
+        return r < rows ? Row{table + static_cast<size_t>(r) * stride, static_cast<long long>(e.places[r]) - start,
+                              static_cast<int>(r)}
                         : Row{nullptr, 0, -1};
     };
-    const auto place_of = [&](const Row &row, int g) {
+    const auto place_of = [&](const Row &row, unsigned g) {
         Place p{-1, -1, 0};
         const long long at = row.before + g;
         if (row.id < 0 || at < 0 || at > INT32_MAX) return p;
@@ -353,7 +360,7 @@ slot_kernel(const int32_t *__restrict__ table, size_t stride, int rows, int widt
         if (b < static_cast<uint32_t>(width)) p.entry = __ldg(row.entries + b);
         return p;
     };
-    each_output<kSlotChunk>(e, rows, tokens, row_at, place_of, [&](const Row &row, int g, const Place &p) {
+    each_output<kSlotChunk>(e, rows, tokens, row_at, place_of, [&](const Row &row, unsigned g, const Place &p) {
         __stcs(slots + g, p.entry < 0 ? -1ll : static_cast<long long>(p.entry) * page.page + p.offset);
         __stcs(positions + g, p.pos);
         __stcs(row_ids + g, row.id);
@@ -362,19 +369,19 @@ slot_kernel(const int32_t *__restrict__ table, size_t stride, int rows, int widt
 
 template <bool IN_SHARED>
 __global__ void __launch_bounds__(kPagedThreads, 2)
-release_kernel(const int32_t *__restrict__ table, size_t stride, int rows, ReleaseCount count,
+release_kernel(const int32_t *__restrict__ table, size_t stride, unsigned rows, ReleaseCount count,
                int32_t *__restrict__ pages, int pool, const int32_t *__restrict__ free_count,
                int32_t *__restrict__ left, Ends scratch)
 {
-    const int free = clamp_free(free_count, pool);
+    const unsigned free = clamp_free(free_count, pool);
     const Ends e = row_ends<IN_SHARED>(count, rows, scratch);
-    const int served = warp_row_of(e.ends, 0, rows, pool - free);   // rows whose pages fit the pool array
-    const int total = served > 0 ? e.ends[served - 1] : 0;
+    const unsigned served = warp_row_of(e.ends, 0, rows, pool - free);   // rows whose pages fit the pool array
+    const unsigned total = served > 0 ? e.ends[served - 1] : 0;
     if (blockIdx.x == 0 && threadIdx.x == 0) *left = free + total;
     each_output<kMoveChunk>(e, rows, total,
-                            [&](int r, int start) { return r * static_cast<long long>(stride) - start; },
-                            [&](long long row, int g) { return __ldcs(table + row + g); },
-                            [&](long long, int g, int id) { pages[free + g] = id; });
+                            [&](unsigned r, unsigned start) { return r * static_cast<long long>(stride) - start; },
+                            [&](long long row, unsigned g) { return __ldcs(table + row + g); },
+                            [&](long long, unsigned g, int id) { pages[free + g] = id; });
 }
 
 // Blocks for `most` output elements at the most.
@@ -388,7 +395,7 @@ unsigned paged_blocks(unsigned long long most, const Workspace &ws)
 // Where the rows are too many for a block's shared memory, the launch that
 // scans them into `scratch`.
 template <class Count>
-cudaError_t prepare_ends(const Count &count, int rows, const Ends &scratch, size_t *shared_bytes, cudaStream_t s)
+cudaError_t prepare_ends(const Count &count, unsigned rows, const Ends &scratch, size_t *shared_bytes, cudaStream_t s)
 {
     *shared_bytes = 0;
     if (rows <= kPagedSharedRows) {
@@ -407,7 +414,7 @@ cudaError_t launch_block_table_extend(int32_t *table, size_t stride, int rows, i
                                       const Workspace &ws, cudaStream_t s)
 {
     const ExtendCount count{cached, fresh, Pages(page), width};
-    const Ends ends{scratch, scratch + rows};
+    const Ends ends{reinterpret_cast<uint32_t *>(scratch), scratch + rows};
     size_t shared = 0;
     cudaError_t e = prepare_ends(count, rows, ends, &shared, s);
     if (e != cudaSuccess) return e;
@@ -429,7 +436,7 @@ cudaError_t launch_slot_map(const int32_t *table, size_t stride, int rows, int w
                             const Workspace &ws, cudaStream_t s)
 {
     const SlotCount count{cached, fresh, granted};
-    const Ends ends{scratch, scratch + rows};
+    const Ends ends{reinterpret_cast<uint32_t *>(scratch), scratch + rows};
     size_t shared = 0;
     cudaError_t e = prepare_ends(count, rows, ends, &shared, s);
     if (e != cudaSuccess) return e;
@@ -450,7 +457,7 @@ cudaError_t launch_block_table_release(const int32_t *table, size_t stride, int 
                                        const Workspace &ws, cudaStream_t s)
 {
     const ReleaseCount count{cached, done, Pages(page), width};
-    const Ends ends{scratch, scratch + rows};
+    const Ends ends{reinterpret_cast<uint32_t *>(scratch), scratch + rows};
     size_t shared = 0;
     cudaError_t e = prepare_ends(count, rows, ends, &shared, s);
     if (e != cudaSuccess) return e;
