@@ -26,6 +26,7 @@ if hasattr(torch, "uint32"):
     _SUFFIX[torch.uint32] = "u32"
 
 
+_INT32_MAX = 2**31 - 1
 _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
@@ -355,8 +356,10 @@ def _check_table(table: torch.Tensor, page_size: int) -> int:
     stride = _check_matrix(table, "table")
     if table.dtype != torch.int32:
         raise TypeError("table must be int32")
-    if page_size < 1:
-        raise ValueError("page_size must be positive")
+    if not 1 <= page_size <= _INT32_MAX:
+        raise ValueError("page_size must be positive and fit in int32")
+    if table.shape[1] > _INT32_MAX:
+        raise ValueError("table's rows must have at most INT32_MAX entries")
     return stride
 
 

@@ -120,3 +120,18 @@ def test_2_31_rows(ds, room):
         assert pages.tolist() == [-1, -1] + list(range(100 + n - 1, 99, -1)) + [-1]
     s.synchronize()
     ds.stream_release(s)
+
+
+def test_sizes_that_do_not_fit_in_int32_are_refused(ds):
+    four, one = i32(0, 0, 0, 0), i32(0)
+    table, pages = torch.zeros(4, 8, dtype=torch.int32, device="cuda"), i32(1, 2, 3)
+    flags = torch.zeros(4, dtype=torch.uint8, device="cuda")
+    wide = torch.zeros(0, 2**32 + 8, dtype=torch.int32, device="cuda")
+    none = i32()
+    for t, lengths, done, page in ((table, four, flags, 2**32 + 16), (wide, none, flags[:0], 16)):
+        with pytest.raises(ValueError):
+            ds.block_table_extend(t, lengths, lengths, pages, one, page)
+        with pytest.raises(ValueError):
+            ds.slot_map(t, lengths, lengths, page, 5)
+        with pytest.raises(ValueError):
+            ds.block_table_release(t, lengths, done, pages, one, page)
