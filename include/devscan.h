@@ -421,9 +421,7 @@ devscan_status block_table_release_i32(const int32_t *table, size_t stride, size
  * few hundred, or a nearly flat row with top-p) are read once more.  One
  * launch, or two where the rows are many and large, the second for those rows;
  * 4 bytes per row of per-stream scratch are allocated stream-ordered on first
- * use if top_k or top_p is given (DEVSCAN_ERR_NOMEM).  The second launch
- * waits, for a bounded time, for the first to have seen every row; if that
- * runs out, devscan_device_status() reports DEVSCAN_ERR_TIMEOUT.
+ * use if top_k or top_p is given (DEVSCAN_ERR_NOMEM).
  * ------------------------------------------------------------------------- */
 #define DEVSCAN_SAMPLE_MAX_VOCAB ((size_t)1 << 18)
 

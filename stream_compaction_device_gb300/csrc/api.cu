@@ -688,7 +688,7 @@ devscan_status sample_tokens_f32(const float *logits, size_t rows, size_t vocab,
 {
     return sample_common(launch_sample_f32, 4,
                          {logits, rows, logits_stride, 0, noise, noise_stride, temperature, top_k, top_p, min_p, tokens,
-                          logprobs, nullptr, kSpinLimit},
+                          logprobs, nullptr},
                          vocab, stream);
 }
 devscan_status sample_tokens_f16(const uint16_t *logits, size_t rows, size_t vocab, size_t logits_stride,
@@ -698,7 +698,7 @@ devscan_status sample_tokens_f16(const uint16_t *logits, size_t rows, size_t voc
 {
     return sample_common(launch_sample_f16, 2,
                          {logits, rows, logits_stride, 0, noise, noise_stride, temperature, top_k, top_p, min_p, tokens,
-                          logprobs, nullptr, kSpinLimit},
+                          logprobs, nullptr},
                          vocab, stream);
 }
 devscan_status sample_tokens_bf16(const uint16_t *logits, size_t rows, size_t vocab, size_t logits_stride,
@@ -708,7 +708,7 @@ devscan_status sample_tokens_bf16(const uint16_t *logits, size_t rows, size_t vo
 {
     return sample_common(launch_sample_bf16, 2,
                          {logits, rows, logits_stride, 0, noise, noise_stride, temperature, top_k, top_p, min_p, tokens,
-                          logprobs, nullptr, kSpinLimit},
+                          logprobs, nullptr},
                          vocab, stream);
 }
 

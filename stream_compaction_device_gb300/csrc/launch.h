@@ -188,7 +188,6 @@ struct SampleCall {
     int32_t *tokens;
     float *logprobs;
     uint32_t *row_words;
-    unsigned spin_limit;
 };
 cudaError_t launch_sample_f32(const SampleCall &call, const Workspace &ws, cudaStream_t s);
 cudaError_t launch_sample_f16(const SampleCall &call, const Workspace &ws, cudaStream_t s);

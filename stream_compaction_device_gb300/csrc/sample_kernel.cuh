@@ -81,6 +81,7 @@ constexpr int kQueue = 64;                 // entries that a warp has waiting
 // and 16 us in one, two, four and eight (top-p).
 constexpr unsigned kLoneChunks = 2048, kLeastChunks = 512;
 constexpr unsigned kKeptChunks = 4096;     // of a kept slice, for two blocks per SM: 64 KB
+constexpr unsigned kPolls = 1024;          // of the second launch for the first's rows, 64 ns apart
 constexpr int kList = 1024;                // tokens the short list holds
 constexpr int kBins = 1024;
 constexpr float kCountSpan = 16.0f;        // first histogram of counts: logits below the largest, where nothing says how far
@@ -536,7 +537,8 @@ struct Draw {
             uint32_t r = 0;
 #pragma unroll
             for (int e = 0; e < kEach / 4; ++e)
-                if (C::value(q, k * (kEach / 4) + e) != inf()) r |= kEach == 4 ? C::kFill : C::kFill & (0xffffu << (16 * e));
+                if (C::value(q, k * (kEach / 4) + e) != inf())
+                    r |= kEach == 4 ? C::kFill : C::kFill & (0xffffu << (16 * e));
             q[k] = r;
         }
     }
@@ -915,7 +917,8 @@ struct Draw {
         for (unsigned b = tid; b < part; b += kThreads) {
             u64 h = 0;
 #pragma unroll 1
-            for (unsigned r = 0; r < blocks; ++r) h += low_parts[r * part + b] | static_cast<u64>(high_parts[r * part + b]) << 32;
+            for (unsigned r = 0; r < blocks; ++r)
+                h += low_parts[r * part + b] | static_cast<u64>(high_parts[r * part + b]) << 32;
 #pragma unroll 1
             for (unsigned r = 0; r < blocks; ++r) put(&sums[rank * part + b], r, h);
         }
@@ -1051,7 +1054,8 @@ struct Draw {
             unsigned shift = 0;
             while (width >> shift >= kBins) ++shift;
             histogram<MASS>(v_lo, [&](float v, int i) {
-                return inside(v, i) ? static_cast<int>((tie ? static_cast<unsigned>(i) - i_lo : hi_bits - ordered(v)) >> shift) : -1;
+                if (!inside(v, i)) return -1;
+                return static_cast<int>((tie ? static_cast<unsigned>(i) - i_lo : hi_bits - ordered(v)) >> shift);
             }, same, want, bin);
             if (tie) {
                 i_lo += bin << shift;
@@ -1149,8 +1153,6 @@ struct Deferred {
     uint32_t *rows;
     unsigned *count, *decided;       // rows put down; rows that are put down or will not be
     unsigned *next, *left;           // rows that the second launch has taken up; its blocks that are through
-    unsigned *error;
-    unsigned limit;                  // polls of the second launch before it gives up
 
     // By one thread of the row's cluster, once.
     __device__ __forceinline__ void decide(bool put_down, unsigned row) const
@@ -1285,7 +1287,8 @@ __device__ __forceinline__ void draw_row(Draw<T, kKeeps<PASS>> &d, unsigned r, c
 
     // A little further than the bound, and twice as far for more tokens than
     // lanes; what lies further still is in the histogram's last bin.
-    d.reach = (d.top - unordered(max(bound, kOrderedMinusInf))) * (bounded || static_cast<unsigned>(k) <= d.blocks * kThreads ? 1.02f : 2.0f);
+    d.reach = d.top - unordered(max(bound, kOrderedMinusInf));
+    d.reach *= bounded || static_cast<unsigned>(k) <= d.blocks * kThreads ? 1.02f : 2.0f;
     if (!(d.reach > 0.0f && d.reach < FLT_MAX)) d.reach = kCountSpan;
 
     u64 cut = 0;
@@ -1340,7 +1343,8 @@ __device__ __forceinline__ void draw_row(Draw<T, kKeeps<PASS>> &d, unsigned r, c
                 if (by_mass && !whole) {   // the first k's mass
                     float part = 0.0f;
 #pragma unroll 1
-                    for (uint32_t at = d.tid; at < limit; at += kThreads) part += d.list_weight(unordered(ord_of(sorted[at])));
+                    for (uint32_t at = d.tid; at < limit; at += kThreads)
+                        part += d.list_weight(unordered(ord_of(sorted[at])));
                     d.block_scan(part, s.warpf, &total);
                 }
                 const float bar = p * total;
@@ -1427,17 +1431,18 @@ sample_kernel(const SampleCall call, unsigned per, const Deferred later)
     if constexpr (PASS != Pass::Left) {
         draw_row<T, PASS>(d, blockIdx.x / d.blocks, call, per, later);
     } else {
+        // Every row of the first launch is decided when its blocks let this one
+        // start, or about then; if that is not seen soon, at its end.
         unsigned decided = 0;
-        for (unsigned polls = 0; polls < later.limit; ++polls) {
+        for (unsigned polls = 0; polls < kPolls && decided != call.rows; ++polls) {
             asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(decided) : "l"(later.decided) : "memory");
-            if (decided == call.rows) break;
-            __nanosleep(64);
+            if (decided != call.rows) __nanosleep(64);
         }
-        const bool ready = __syncthreads_and(decided == call.rows) != 0;
-        if (!ready && d.tid == 0) atomicOr(later.error, kErrTimeout);
+        if (decided != call.rows) asm volatile("griddepcontrol.wait;" ::: "memory");
+        __syncthreads();
         // A cluster's first row by its place, then whichever is next; asked for
         // while the row before it is drawn.
-        const unsigned n = ready ? __ldcg(later.count) : 0, clusters = gridDim.x / d.blocks;
+        const unsigned n = __ldcg(later.count), clusters = gridDim.x / d.blocks;
 #pragma unroll 1
         for (unsigned w = blockIdx.x / d.blocks, turn = 0; w < n; w = s.next[turn], turn ^= 1) {
             unsigned next = 0;
@@ -1493,7 +1498,8 @@ cudaError_t launch_clusters(const SampleCall &call, unsigned clusters, unsigned 
     cfg.gridDim = dim3(clusters * blocks);
     cfg.blockDim = dim3(kThreads);
     const size_t entries = (per + kEntryChunks - 1) / kEntryChunks * kThreads;
-    cfg.dynamicSmemBytes = kSharedBytes + inbox_keys<kKeep>(blocks) * 8 + kPartWords<kKeep> * 4 + (kKeep ? static_cast<size_t>(per) * 16 : entries * 4);
+    cfg.dynamicSmemBytes = kSharedBytes + inbox_keys<kKeep>(blocks) * 8 + kPartWords<kKeep> * 4 +
+                           (kKeep ? static_cast<size_t>(per) * 16 : entries * 4);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1517,10 +1523,10 @@ cudaError_t launch_typed(const SampleCall &call, const Workspace &ws, cudaStream
     unsigned wide = 1;               // the most blocks that a row of this size is worth
     if (chunks > kLoneChunks)
         while (wide < kMaxCluster && wide * kLeastChunks < chunks) wide *= 2;
-    if (rows > 0x7fffffffull / kMaxCluster) return cudaErrorInvalidValue;
     const unsigned n = static_cast<unsigned>(rows);
-    const Deferred later{call.row_words,         &ws.state->sample_rows, &ws.state->sample_decided, &ws.state->sample_next,
-                         &ws.state->sample_left, &ws.state->error,       call.spin_limit};
+    DevState &state = *ws.state;
+    const Deferred later{call.row_words, &state.sample_rows, &state.sample_decided, &state.sample_next,
+                         &state.sample_left};
     // One launch of blocks that keep their slices, as many to a row as fit on
     // the GPU at once (clusters of eight leave gaps: fewer of them fit), where
     // the slices are small enough for two blocks per SM.  Against two launches
@@ -1537,10 +1543,13 @@ cudaError_t launch_typed(const SampleCall &call, const Workspace &ws, cudaStream
     // keep their slices 173 and 127).
     blocks = 1;
     while (blocks < wide && rows * blocks * 2 <= sms * kBlocksPerSm<Pass::Plain>) blocks *= 2;
-    const cudaError_t e = launch_clusters<T, Pass::Plain>(call, n, blocks, later, s);
+    cudaError_t e = launch_clusters<T, Pass::Plain>(call, n, blocks, later, s);
     if (e != cudaSuccess || later.rows == nullptr) return e;
     const size_t most = room / wide;
-    return launch_clusters<T, Pass::Left>(call, static_cast<unsigned>(rows < most ? rows : most), wide, later, s);
+    e = launch_clusters<T, Pass::Left>(call, static_cast<unsigned>(rows < most ? rows : most), wide, later, s);
+    // The words that the second would have reset.
+    if (e != cudaSuccess) (void)cudaMemsetAsync(&state.sample_rows, 0, 4 * sizeof(unsigned), s);
+    return e;
 }
 
 }  // namespace

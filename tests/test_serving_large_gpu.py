@@ -122,6 +122,21 @@ def test_2_31_rows(ds, room):
     ds.stream_release(s)
 
 
+def test_draw_of_2_28_rows(ds, room):
+    room(20)
+    rows = 2**28 + 3
+    logits = torch.empty(rows, 3, dtype=torch.bfloat16, device="cuda")
+    for lo, hi in parts(rows):
+        logits[lo:hi] = torch.randint(-3, 4, (hi - lo, 3), device="cuda", dtype=torch.int8).to(torch.bfloat16)
+    tokens, logprobs = ds.sample_tokens(logits)
+    for lo, hi in parts(rows):
+        x = logits[lo:hi]
+        top = x.amax(1)
+        want = torch.where(x[:, 0] == top, 0, torch.where(x[:, 1] == top, 1, 2))
+        assert torch.equal(tokens[lo:hi].long(), want)
+    assert not bool(logprobs.any())
+
+
 def test_sizes_that_do_not_fit_in_int32_are_refused(ds):
     four, one = i32(0, 0, 0, 0), i32(0)
     table, pages = torch.zeros(4, 8, dtype=torch.int32, device="cuda"), i32(1, 2, 3)
