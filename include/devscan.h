@@ -399,9 +399,11 @@ devscan_status block_table_release_i32(const int32_t *table, size_t stride, size
  * T <= 0, min_p > 1, a setting that is NaN, or noise == NULL takes the first
  * of the order (greedy; logprob 0).  A NaN logit counts as -inf, and -inf is
  * never drawn; a row with nothing above -inf gets token -1 and logprob -inf.
- * If the largest is +inf, the draw is among those that are.  Noise that is
- * not positive and finite loses; where all of a row's kept tokens have such,
- * the token is one of the row or -1.
+ * If the largest is +inf, the draw is among those that are.  Noise counts by
+ * its value, from the smallest denormal to 2^64.  Noise that is zero,
+ * negative, infinite or NaN loses, and larger noise may; a row of which no kept
+ * token has noise that counts gets token -1 and logprob -inf, as may one
+ * whose w_i / noise_i are all below 2^-64.
  *
  *   logits   : device T[rows][logits_stride] (f16 and bf16 as their 16 bits),
  *              aligned to the element; vocab <= logits_stride;

@@ -255,16 +255,30 @@ __host__ __device__ constexpr unsigned inbox_keys(unsigned blocks) { return bloc
 template <bool KEEP> constexpr unsigned kPartWords = KEEP ? 2 * kBins : 0;
 constexpr size_t kSharedBytes = (sizeof(Shared) + 127) / 128 * 128;
 
+// 2^-48 over a token's noise; for noise that loses not above 0, or no number.
+// The reciprocal flushes denormal numbers, and that of 0 would beat every other:
+// so the noise is scaled first, and moved by 2^-126, which makes 0 and -0 lose as
+// negative noise does and is below a number's last digit otherwise (the smallest
+// denormal is 2^-101 here).  Noise from 2^78 on gives 0.  With weights of up to 1
+// no score overflows, and a quotient of weight and noise of 2^-78 or more keeps
+// its digits.  One multiply-add: 512 x 131072 bf16 of mixed settings take 76.3
+// us, with a comparison and a select in its place 79.4.
+__device__ __forceinline__ float pace(float q)
+{
+    return reciprocal(fmaf(q, 0x1p48f, -0x1p-126f));
+}
+
 // The race among the kept tokens that a thread has seen, and their weights'
 // sum: `tops` of exactly 1, the others in `rest`, so that a small rest keeps
-// its digits beside them.
+// its digits beside them.  Only a score above 0 can be drawn: what lies outside
+// the row, is masked, or has noise that loses never is, whatever else there is.
 struct Race {
-    float score = -1.0f, rest = 0.0f;
+    float score = 0.0f, rest = 0.0f;
     int at = 0x7fffffff;
     uint32_t tops = 0;
     __device__ __forceinline__ void offer(float w, float q, int i)
     {
-        const float sc = fmaxf(w * reciprocal(q), 0.0f);
+        const float sc = w * pace(q);
         if (sc >= score && (sc > score || i < at)) score = sc, at = i;
         if (w == 1.0f) ++tops;
         else rest += w;
@@ -272,7 +286,7 @@ struct Race {
     // Order of scores, the lowest index first among equals.
     __device__ __forceinline__ u64 key() const
     {
-        return score < 0.0f ? 0ull : (static_cast<u64>(__float_as_uint(score)) << 32) | ~static_cast<unsigned>(at);
+        return score > 0.0f ? (static_cast<u64>(__float_as_uint(score)) << 32) | ~static_cast<unsigned>(at) : 0ull;
     }
 };
 
@@ -564,7 +578,7 @@ struct Draw {
     {
         const float f = fmaxf(exp2_approx((most - to) * scale), 0.0f);
         if (f != 1.0f) o.rest = (o.rest + static_cast<float>(o.tops)) * f, o.tops = 0;
-        if (o.score > 0.0f) o.score *= f;
+        o.score *= f;
         most = to;
     }
     __device__ __forceinline__ float race_all(Race &o)
@@ -594,7 +608,7 @@ struct Draw {
                 for (int e = 0; e < kEach; ++e) {
                     // Indices rise within a thread, so the first of equals stays.
                     const float w = fmaxf(exp2_approx((C::value(q, e) - most) * scale), 0.0f);
-                    const float sc = w * reciprocal(n[u][e]);
+                    const float sc = w * pace(n[u][e]);
                     o.at = sc > o.score ? i + e : o.at;
                     o.score = sc > o.score ? sc : o.score;
                     o.tops += w == 1.0f ? 1u : 0u;
@@ -634,8 +648,8 @@ struct Draw {
         for (int e = 0; e < N; ++e) {
             const int i = own_index(c, e);
             float w = weight(x[e]);
-            w = keep(x[e], i) & (w >= m) ? w : -1.0f;   // its score is below every other's
-            const float sc = w < 0.0f ? -1.0f : w * reciprocal(n[e]);
+            w = keep(x[e], i) & (w >= m) ? w : 0.0f;   // its score is not above 0
+            const float sc = w * pace(n[e]);
             if (RISING) {
                 o.at = sc > o.score ? i : o.at;
                 o.score = sc > o.score ? sc : o.score;
@@ -643,7 +657,7 @@ struct Draw {
                 o.score = sc, o.at = i;
             }
             o.tops += w == 1.0f ? 1u : 0u;
-            o.rest += w == 1.0f ? 0.0f : fmaxf(w, 0.0f);
+            o.rest += w == 1.0f ? 0.0f : w;
         }
     }
     // Starts the noise of the chunks with a value of at least `low` towards L2.
@@ -656,7 +670,7 @@ struct Draw {
 
     __device__ __forceinline__ void write(u64 won, const Race &o, int32_t *token, float *logprob) const
     {
-        if (won == 0) {   // no score at all: noise that is not a number
+        if (won == 0) {   // no score above 0: the kept tokens' noise loses
             *token = -1;
             if (logprob != nullptr) *logprob = -inf();
             return;
