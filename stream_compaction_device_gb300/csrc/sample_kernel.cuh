@@ -156,6 +156,7 @@ __device__ __forceinline__ float unordered(uint32_t k)
     return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 constexpr uint32_t kOrderedMinusInf = 0x007fffffu;
+constexpr uint32_t kOrderedMinusZero = 0x7fffffffu;   // of no value: unordered() compares equal to 0 there
 
 // A token's place in the order: larger keys first.
 __device__ __forceinline__ u64 key_of(uint32_t ord, unsigned i) { return (static_cast<u64>(ord) << 32) | ~i; }
@@ -1041,6 +1042,10 @@ struct Draw {
         uint32_t bin = 0, i_lo = 0, i_hi = vocab - 1;   // its index's range, once lo_bits == hi_bits
         const auto same = [&](u64) { return want; };
         for (;;) {
+            // A range that ends at -0 ends below it: 0 compares equal, but its
+            // bits are above the range, and its place in a histogram would be
+            // far outside.
+            if (hi_bits == kOrderedMinusZero) --hi_bits;
             const float v_lo = unordered(lo_bits), v_hi = unordered(hi_bits);
             const bool tie = lo_bits == hi_bits;
             const auto inside = [&](float v, int i) {
