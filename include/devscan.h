@@ -15,8 +15,10 @@
  * (one 8-byte status word per tile of the largest input seen, plus a few
  * counters) that the library allocates stream-ordered on first use
  * (cudaMallocAsync) and reuses for later calls on the same stream.  Calls on
- * one stream never race on it; calls on different streams use different
- * workspaces.  devscan_stream_release() frees a stream's workspace.
+ * one stream never race on it, from whichever host threads they come: a call
+ * queues all of its launches before another on that stream queues any.  Calls
+ * on different streams use different workspaces.  devscan_stream_release() frees
+ * a stream's workspace.
  *
  * Pages the operations follow:
  *   [P1] geek-doc.cn/chip-design/intermediate/parallel-prefix-scan,

@@ -4,7 +4,9 @@
 #include <atomic>
 #include <cstdint>
 #include <map>
+#include <memory>
 #include <mutex>
+#include <new>
 #include <utility>
 
 #include "../../include/devscan.h"
@@ -36,13 +38,44 @@ struct Slot {
     void *base = nullptr;
     size_t bytes = 0;
     Workspace ws;
-    void *extra = nullptr;   // per-stream scratch of the digit sort (its histograms)
+    void *extra = nullptr;   // per-stream scratch, of what the largest call so far asked for
     size_t extra_bytes = 0;
+    std::shared_ptr<std::mutex> calls = std::make_shared<std::mutex>();   // held by one call at a time
 };
 
-std::mutex g_mutex;
-std::map<std::pair<int, uintptr_t>, Slot> g_slots;
+using SlotKey = std::pair<int, uintptr_t>;   // device, stream
+
+std::mutex g_mutex;   // of the maps
+std::map<SlotKey, Slot> g_slots;
 std::map<int, int> g_num_sms;
+
+// A call's hold on its stream's slot, from finding it to the call's last
+// launch.  A call's launches hand each other what is in the workspace and the
+// scratch, so another thread's call on the same stream must not come between
+// them, nor free a scratch that it outgrows before they are queued.
+struct Hold {
+    std::shared_ptr<std::mutex> calls;   // outlives the slot, which another thread may release
+    std::unique_lock<std::mutex> lock;
+};
+
+// Holds the slot of `key` and returns it; null if there is none and none is
+// to be made.
+Slot *hold_slot(const SlotKey &key, bool make, Hold *hold)
+{
+    for (;;) {
+        hold->lock = {};
+        {
+            std::lock_guard<std::mutex> lock(g_mutex);
+            const auto it = make ? g_slots.try_emplace(key).first : g_slots.find(key);
+            if (it == g_slots.end()) return nullptr;
+            hold->calls = it->second.calls;
+        }
+        hold->lock = std::unique_lock<std::mutex>(*hold->calls);
+        std::lock_guard<std::mutex> lock(g_mutex);
+        const auto it = g_slots.find(key);
+        if (it != g_slots.end() && it->second.calls == hold->calls) return &it->second;   // else released meanwhile
+    }
+}
 
 constexpr size_t kStateBytes = 256;
 
@@ -58,12 +91,16 @@ devscan_status from_cuda(cudaError_t e) { return e == cudaSuccess ? DEVSCAN_OK :
 // Finds (or grows) the workspace of (current device, stream) so that it holds
 // at least `tiles` tile slots.  Growth frees the old block and allocates a
 // new one stream-ordered, then zeroes it on the stream, so calls already
-// queued on the stream finish with the old block first.
-devscan_status acquire(cudaStream_t stream, unsigned tiles, Workspace *out)
-{
+// queued on the stream finish with the old block first.  The workspace is the
+// call's while it has `hold`.
+devscan_status acquire(cudaStream_t stream, unsigned tiles, Workspace *out, Hold *hold)
+try {
     static_assert(sizeof(DevState) <= kStateBytes, "device state must fit its slot");
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return DEVSCAN_ERR_CUDA;
+    if (tiles > kMaxTiles) return DEVSCAN_ERR_INVALID;
+    const SlotKey key{dev, reinterpret_cast<uintptr_t>(stream)};
+    Slot &slot = *hold_slot(key, true, hold);
     std::lock_guard<std::mutex> lock(g_mutex);
     auto sms = g_num_sms.find(dev);
     if (sms == g_num_sms.end()) {
@@ -72,8 +109,6 @@ devscan_status acquire(cudaStream_t stream, unsigned tiles, Workspace *out)
             return DEVSCAN_ERR_CUDA;
         sms = g_num_sms.emplace(dev, count).first;
     }
-    if (tiles > kMaxTiles) return DEVSCAN_ERR_INVALID;
-    Slot &slot = g_slots[{dev, reinterpret_cast<uintptr_t>(stream)}];
     if (slot.base == nullptr || slot.ws.capacity < tiles) {
         size_t cap = 1024;
         while (cap < tiles) cap *= 2;   // at most kMaxTiles = 2^31
@@ -87,7 +122,7 @@ devscan_status acquire(cudaStream_t stream, unsigned tiles, Workspace *out)
         const cudaError_t e = cudaMallocAsync(&base, bytes, stream);
         if (e != cudaSuccess) {
             (void)cudaGetLastError();
-            g_slots.erase({dev, reinterpret_cast<uintptr_t>(stream)});
+            g_slots.erase(key);
             return e == cudaErrorMemoryAllocation ? DEVSCAN_ERR_NOMEM : DEVSCAN_ERR_CUDA;
         }
         if (cudaMemsetAsync(base, 0, bytes, stream) != cudaSuccess) return DEVSCAN_ERR_CUDA;
@@ -103,10 +138,12 @@ devscan_status acquire(cudaStream_t stream, unsigned tiles, Workspace *out)
     slot.ws.num_sms = sms->second;
     *out = slot.ws;
     return DEVSCAN_OK;
+} catch (const std::bad_alloc &) {
+    return DEVSCAN_ERR_NOMEM;
 }
 
 // Per-stream scratch of at least `bytes`, grown stream-ordered like the
-// workspace (the slot must exist: call acquire() first).
+// workspace (by a call that holds the slot: call acquire() first).
 devscan_status acquire_extra(cudaStream_t stream, size_t bytes, void **out)
 {
     int dev = 0;
@@ -153,7 +190,8 @@ devscan_status scan_common(ElemType type, bool inclusive, const void *in, void *
         return DEVSCAN_ERR_INVALID;
     const unsigned tiles = tiles_for(n, kScanTile);
     Workspace ws;
-    const devscan_status st = acquire(stream, tiles, &ws);
+    Hold hold;
+    const devscan_status st = acquire(stream, tiles, &ws, &hold);
     if (st != DEVSCAN_OK) return st;
     const bool aligned = reinterpret_cast<uintptr_t>(in) % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
     const int carry = carry_mode();
@@ -190,7 +228,8 @@ devscan_status reduce_common(ElemType type, const void *in, size_t n, devscan_op
     if (n > 0 && (in == nullptr || reinterpret_cast<uintptr_t>(in) % 4 != 0 || overlaps(total, 4, in, n * 4)))
         return DEVSCAN_ERR_INVALID;
     Workspace ws;
-    const devscan_status st = acquire(stream, 1, &ws);
+    Hold hold;
+    const devscan_status st = acquire(stream, 1, &ws, &hold);
     if (st != DEVSCAN_OK) return st;
     return from_cuda(launch_reduce(type, static_cast<int>(op), in, n, total, ws, stream));
 }
@@ -207,7 +246,8 @@ devscan_status segscan_common(ElemType type, bool inclusive, const void *in, con
     if (n > kMaxScanN) return DEVSCAN_ERR_INVALID;
     if (overlaps(heads, n, out, n * 4) || (in != out && overlaps(in, n * 4, out, n * 4))) return DEVSCAN_ERR_INVALID;
     Workspace ws;
-    const devscan_status st = acquire(stream, tiles_for(n, kScanTile), &ws);
+    Hold hold;
+    const devscan_status st = acquire(stream, tiles_for(n, kScanTile), &ws, &hold);
     if (st != DEVSCAN_OK) return st;
     return from_cuda(launch_segscan(type, static_cast<int>(op), inclusive, in, heads, out, n,
                                     carry_mode(), ws, kSpinLimit, stream));
@@ -263,10 +303,10 @@ devscan_status paged_check(const void *table, size_t stride, size_t rows, int wi
 
 // The workspace, and scratch for the scanned ends where they do not fit in a
 // block's shared memory.
-devscan_status paged_scratch(size_t rows, cudaStream_t stream, Workspace *ws, int32_t **scratch)
+devscan_status paged_scratch(size_t rows, cudaStream_t stream, Workspace *ws, Hold *hold, int32_t **scratch)
 {
     *scratch = nullptr;
-    const devscan_status st = acquire(stream, 1, ws);
+    const devscan_status st = acquire(stream, 1, ws, hold);
     if (st != DEVSCAN_OK || rows <= static_cast<size_t>(kPagedSharedRows)) return st;
     void *p = nullptr;
     const devscan_status got = acquire_extra(stream, 2 * rows * sizeof(int32_t), &p);
@@ -299,7 +339,8 @@ devscan_status sample_common(cudaError_t (*launch)(const SampleCall &, const Wor
     if (written_overlap(written, read)) return DEVSCAN_ERR_INVALID;
     call.vocab = static_cast<unsigned>(vocab);
     Workspace ws;
-    devscan_status st = acquire(stream, 1, &ws);
+    Hold hold;
+    devscan_status st = acquire(stream, 1, &ws, &hold);
     if (st != DEVSCAN_OK) return st;
     if (call.noise != nullptr && (call.top_k != nullptr || call.top_p != nullptr)) {
         void *row_words = nullptr;
@@ -465,7 +506,8 @@ devscan_status compact_i32(const int32_t *in, const uint8_t *flags, int32_t *out
     if (n == 0) return from_cuda(cudaMemsetAsync(count, 0, sizeof(int32_t), stream));
     const unsigned tiles = tiles_for(n, kCompactTile);
     Workspace ws;
-    devscan_status st = acquire(stream, tiles, &ws);
+    Hold hold;
+    devscan_status st = acquire(stream, tiles, &ws, &hold);
     if (st != DEVSCAN_OK) return st;
     const int carry = carry_mode();
     void *part_words = nullptr;   // the two-launch path's part counts and offsets
@@ -491,7 +533,8 @@ devscan_status compact_gt_i32(const int32_t *in, int32_t threshold, int32_t *out
     }
     if (n == 0) return from_cuda(cudaMemsetAsync(count, 0, sizeof(int32_t), stream));
     Workspace ws;
-    devscan_status st = acquire(stream, tiles_for(n, kCompactTile), &ws);
+    Hold hold;
+    devscan_status st = acquire(stream, tiles_for(n, kCompactTile), &ws, &hold);
     if (st != DEVSCAN_OK) return st;
     const int carry = carry_mode();
     void *part_words = nullptr;   // the two-launch path's part masks, counts and offsets
@@ -514,8 +557,9 @@ devscan_status bracket_scan_i32(const int32_t *in, int32_t *out, int32_t *result
             return DEVSCAN_ERR_INVALID;
     }
     Workspace ws;
+    Hold hold;
     if (n > 0) {
-        const devscan_status st = acquire(stream, tiles_for(n, kScanTile), &ws);
+        const devscan_status st = acquire(stream, tiles_for(n, kScanTile), &ws, &hold);
         if (st != DEVSCAN_OK) return st;
     }
     return from_cuda(launch_bracket(in, out, result, n, carry_mode(), ws,
@@ -533,7 +577,8 @@ devscan_status split_bit_u32(const uint32_t *keys, uint32_t *out, int bit, size_
     if (overlaps(keys, n * 4, out, n * 4)) return DEVSCAN_ERR_INVALID;
     const unsigned tiles = tiles_for(n, kSplitTile);
     Workspace ws;
-    devscan_status st = acquire(stream, tiles, &ws);
+    Hold hold;
+    devscan_status st = acquire(stream, tiles, &ws, &hold);
     if (st != DEVSCAN_OK) return st;
     unsigned *z = &ws.state->zeros[40];
     const int carry = carry_mode();
@@ -560,7 +605,8 @@ devscan_status radix_sort_u32(uint32_t *keys, uint32_t *tmp, size_t n, cudaStrea
     if (overlaps(keys, n * 4, tmp, n * 4)) return DEVSCAN_ERR_INVALID;
     const unsigned tiles = tiles_for(n, kSplitTile);
     Workspace ws;
-    devscan_status st = acquire(stream, tiles, &ws);
+    Hold hold;
+    devscan_status st = acquire(stream, tiles, &ws, &hold);
     if (st != DEVSCAN_OK) return st;
     unsigned *z = ws.state->zeros;   // z[b] = zero count of bit b
     const int carry = carry_mode();
@@ -593,7 +639,8 @@ devscan_status radix_sort_digits_u32(uint32_t *keys, uint32_t *tmp, size_t n, cu
     if (overlaps(keys, n * 4, tmp, n * 4)) return DEVSCAN_ERR_INVALID;
     const size_t hist_words = radix_hist_words(n);
     Workspace ws;
-    devscan_status st = acquire(stream, tiles_for(hist_words, kScanTile), &ws);
+    Hold hold;
+    devscan_status st = acquire(stream, tiles_for(hist_words, kScanTile), &ws, &hold);
     if (st != DEVSCAN_OK) return st;
     void *hist = nullptr;
     st = acquire_extra(stream, hist_words * sizeof(uint32_t), &hist);
@@ -624,8 +671,9 @@ devscan_status block_table_extend_i32(int32_t *table, size_t stride, size_t rows
     const Span read[] = {{cached, rows * 4}, {fresh, rows * 4}, {pages, pool * 4}, {free, 4}};
     if (written_overlap(written, read)) return DEVSCAN_ERR_INVALID;
     Workspace ws;
+    Hold hold;
     int32_t *scratch = nullptr;
-    st = paged_scratch(rows, stream, &ws, &scratch);
+    st = paged_scratch(rows, stream, &ws, &hold, &scratch);
     if (st != DEVSCAN_OK) return st;
     return from_cuda(launch_block_table_extend(table, stride, static_cast<int>(rows), width, cached, fresh, page,
                                                pages, static_cast<int>(pool), free, granted, left, scratch, ws,
@@ -650,8 +698,9 @@ devscan_status slot_map_i32(const int32_t *table, size_t stride, size_t rows, in
     const Span read[] = {{table, table_bytes}, {cached, rows * 4}, {fresh, rows * 4}, {granted, rows}};
     if (written_overlap(written, read)) return DEVSCAN_ERR_INVALID;
     Workspace ws;
+    Hold hold;
     int32_t *scratch = nullptr;
-    st = paged_scratch(rows, stream, &ws, &scratch);
+    st = paged_scratch(rows, stream, &ws, &hold, &scratch);
     if (st != DEVSCAN_OK) return st;
     return from_cuda(launch_slot_map(table, stride, static_cast<int>(rows), width, cached, fresh, granted, page,
                                      static_cast<int>(tokens), starts, slots, positions, row_ids, scratch, ws,
@@ -674,8 +723,9 @@ devscan_status block_table_release_i32(const int32_t *table, size_t stride, size
     const Span read[] = {{table, table_bytes}, {cached, rows * 4}, {done, rows}, {free, 4}};
     if (written_overlap(written, read)) return DEVSCAN_ERR_INVALID;
     Workspace ws;
+    Hold hold;
     int32_t *scratch = nullptr;
-    st = paged_scratch(rows, stream, &ws, &scratch);
+    st = paged_scratch(rows, stream, &ws, &hold, &scratch);
     if (st != DEVSCAN_OK) return st;
     return from_cuda(launch_block_table_release(table, stride, static_cast<int>(rows), width, cached, done, page,
                                                 pages, static_cast<int>(pool), free, left, scratch, ws, stream));
@@ -717,23 +767,15 @@ devscan_status devscan_device_status(cudaStream_t stream)
     if (cudaStreamSynchronize(stream) != cudaSuccess) return DEVSCAN_ERR_CUDA;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return DEVSCAN_ERR_CUDA;
-    DevState *state = nullptr;
-    void *base = nullptr;
-    size_t bytes = 0;
-    {
-        std::lock_guard<std::mutex> lock(g_mutex);
-        auto it = g_slots.find({dev, reinterpret_cast<uintptr_t>(stream)});
-        if (it == g_slots.end()) return DEVSCAN_OK;
-        state = it->second.ws.state;
-        base = it->second.base;
-        bytes = it->second.bytes;
-    }
+    Hold hold;
+    const Slot *slot = hold_slot({dev, reinterpret_cast<uintptr_t>(stream)}, false, &hold);
+    if (slot == nullptr || slot->base == nullptr) return DEVSCAN_OK;
     unsigned err = 0;
-    if (cudaMemcpy(&err, &state->error, sizeof(unsigned), cudaMemcpyDeviceToHost) != cudaSuccess)
+    if (cudaMemcpy(&err, &slot->ws.state->error, sizeof(unsigned), cudaMemcpyDeviceToHost) != cudaSuccess)
         return DEVSCAN_ERR_CUDA;
     // A launch that gave up may have left its tile counter, epoch and status
     // words half-way; the stream is idle now, so start the workspace afresh.
-    if (err != 0 && cudaMemset(base, 0, bytes) != cudaSuccess) return DEVSCAN_ERR_CUDA;
+    if (err != 0 && cudaMemset(slot->base, 0, slot->bytes) != cudaSuccess) return DEVSCAN_ERR_CUDA;
     return (err & kErrTimeout) ? DEVSCAN_ERR_TIMEOUT : DEVSCAN_OK;
 }
 
@@ -754,14 +796,18 @@ devscan_status devscan_stream_release(cudaStream_t stream)
 {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return DEVSCAN_ERR_CUDA;
-    std::lock_guard<std::mutex> lock(g_mutex);
-    auto it = g_slots.find({dev, reinterpret_cast<uintptr_t>(stream)});
-    if (it == g_slots.end()) return DEVSCAN_OK;
-    void *base = it->second.base;
-    void *extra = it->second.extra;
-    g_slots.erase(it);
+    const SlotKey key{dev, reinterpret_cast<uintptr_t>(stream)};
+    Hold hold;
+    const Slot *slot = hold_slot(key, false, &hold);
+    if (slot == nullptr) return DEVSCAN_OK;
+    void *base = slot->base;
+    void *extra = slot->extra;
+    {
+        std::lock_guard<std::mutex> lock(g_mutex);
+        g_slots.erase(key);
+    }
     if (extra != nullptr && cudaFreeAsync(extra, stream) != cudaSuccess) return DEVSCAN_ERR_CUDA;
-    return from_cuda(cudaFreeAsync(base, stream));
+    return base == nullptr ? DEVSCAN_OK : from_cuda(cudaFreeAsync(base, stream));
 }
 
 devscan_status devscan_measure_set_carry_mode(int mode)
@@ -777,7 +823,8 @@ devscan_status devscan_selftest_stalled_wait(unsigned int spin_limit, cudaStream
 {
     if (spin_limit == 0) return DEVSCAN_ERR_INVALID;
     Workspace ws;
-    const devscan_status st = acquire(stream, 1, &ws);
+    Hold hold;
+    const devscan_status st = acquire(stream, 1, &ws, &hold);
     if (st != DEVSCAN_OK) return st;
     return from_cuda(launch_stalled_wait(ws, spin_limit, stream));
 }
