@@ -416,10 +416,12 @@ devscan_status block_table_release_i32(const int32_t *table, size_t stride, size
  *              neither may overlap another buffer (DEVSCAN_ERR_INVALID);
  *   rows     : at most INT32_MAX; 0 is a no-op;
  *   vocab    : 1 .. DEVSCAN_SAMPLE_MAX_VOCAB, else DEVSCAN_ERR_INVALID.
- * Weights are fp32 (below 2^-126 they count as 0); sums are fp32 in a fixed
- * order, or integers of w in units of 2^-31 in 64 bits, so that the same call
- * gives the same bits.  A token at the edge of top-p may fall on either side
- * where its mass ahead is within rounding of the mark.
+ * Weights are fp32 (below 2^-126 they count as 0).  Sums are fp32 in a fixed
+ * order or, where a cut needs a histogram, of integers in 64 bits (a weight is
+ * rounded to 23 bits there, below 2^-32 to units of 2^-54, and the sum of a bin of
+ * weights down to units of 2^-45), so that the same call gives the same bits.  A
+ * token at the edge of top-p may fall on either side where its mass ahead is
+ * within rounding of the mark.
  * Traffic: each row once, the noise of the kept tokens (all of it where
  * nothing truncates); rows whose cut is far down the order (a top-k above a
  * few hundred, or a nearly flat row with top-p) are read once more.  One

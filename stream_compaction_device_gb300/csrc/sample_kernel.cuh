@@ -34,8 +34,9 @@
 //     masses in shared memory, of equal bins of logits, then of ordered
 //     bits, then of indices, each inside the bin where the last one crossed
 //     the mark, until the tokens inside fit the list.  Masses there are
-//     integers (w in units of 2^-31, summed in 64 bits), so no result depends
-//     on the order of the atomics.  Without kept slices such a row is left to
+//     integers, summed in 64 bits, so no result depends on the order of the
+//     atomics; each bin counts in a unit of its own, so that small weights keep
+//     their digits as well.  Without kept slices such a row is left to
 //     a second launch of wide clusters with them: read again by 2,048 threads
 //     it takes 25 us, where one block of 256 took 350.
 // Other sums are in fp32: a thread's in the order of its tokens, then over the
@@ -85,7 +86,19 @@ constexpr unsigned kPolls = 1024;          // of the second launch for the first
 constexpr int kList = 1024;                // tokens the short list holds
 constexpr int kBins = 1024;
 constexpr float kCountSpan = 16.0f;        // first histogram of counts: logits below the largest, where nothing says how far
-constexpr float kMassSpan = 23.0f;         // of masses: in temperatures; below, a weight rounds to no mass
+// First histogram of masses: kBinsPerBit bins to a factor of two in weight.  As
+// many neighbouring bins share a unit, about 2^-kMassBits of the weight at which
+// they begin: a weight, whose own error is 3 to 200 times 2^-24, is rounded to 23
+// bits, which a float's addition does, and a word takes 500 masses without a
+// carry.  (16 x 65536 f32 top-p: 23.6 us; 24 bits by a conversion 24.5; 31 bits,
+// with a carry at every third, 25.3.)  The last bin holds all that lies further,
+// in units of 2^-kDeepest.  Bins are added up in units of 2^-kMassUnit, in which
+// 2^18 weights of 1 fit 64 bits.  With one unit of 2^-31 for all bins, a cut among
+// weights of 2^-32 was off by a seventh of its tokens (131072 tokens 22
+// temperatures below the largest).
+constexpr int kUnitShift = 5, kBinsPerBit = 1 << kUnitShift, kMassBits = 23, kMassUnit = 45,
+              kDeepest = kMassBits + (kBins - 1) / kBinsPerBit;
+constexpr float kMassOfOne = 63.0f / 64.0f * (1 << kMassBits);
 constexpr int kGuess = 256, kGuessEach = 16;   // tokens asked of the bound for top-p without top-k: in all, per warp at most
 
 __device__ __forceinline__ float inf() { return __int_as_float(0x7f800000); }
@@ -320,6 +333,7 @@ struct Draw {
     int first;                       // index of the slice's first value
     float top, t, scale;             // the largest logit, temperature, log2(e) / T
     float bins_per_unit;             // of the first histogram
+    float per_weight;                // masses to a weight of 1, in the bin where a cut lies
     float reach;                     // logits below the largest where the first k are expected to end
     bool infinite = false;           // the largest is +inf: it counts as 0, all else as -inf
     int turn = 0;                    // which half of the double buffers is next
@@ -566,7 +580,30 @@ struct Draw {
     {
         return v == top ? 1.0f : fmaxf(expf((v - top) / t), 0.0f);
     }
-    __device__ __forceinline__ uint32_t mass(float v) const { return __float2uint_rn(weight(v) * 2147483648.0f); }
+    // Masses to a weight of 1 in a bin of the first histogram: 63/64 of 2^(23 +
+    // b / 32).  The bin's weights are at most 2^(1/64 - b / 32), so that a mass is
+    // below 2^23, and in all bins but the last above half of that.
+    static __device__ __forceinline__ float per_weight_in(int b)
+    {
+        return __int_as_float(__float_as_int(kMassOfOne) + (b >> kUnitShift << 23));
+    }
+    // w * per, rounded: the sum's last bit is worth 1.
+    static __device__ __forceinline__ uint32_t mass_of(float w, float per)
+    {
+        return static_cast<uint32_t>(__float_as_int(fmaf(w, per, 8388608.0f)) - 0x4b000000);
+    }
+    // A bin's masses in units of 2^-kMassUnit, rounded down; and masses wanted in
+    // that unit as masses of the bin, rounded up.  Both pass by 2^-kMassUnit of
+    // the unit's first weight, where 2^18 masses still fit 64 bits.
+    static __device__ __forceinline__ u64 common(u64 masses, unsigned b)
+    {
+        return masses << (kMassUnit - kMassBits) >> (b >> kUnitShift);
+    }
+    static __device__ __forceinline__ u64 in_bin(u64 wanted, unsigned b)
+    {
+        return ((wanted << (b >> kUnitShift)) + ((1u << (kMassUnit - kMassBits)) - 1)) >> (kMassUnit - kMassBits);
+    }
+    __device__ __forceinline__ uint32_t mass(float v) const { return mass_of(exp2_approx((v - top) * scale), per_weight); }
 
     // -----------------------------------------------------------------------
     // Races.
@@ -878,7 +915,10 @@ struct Draw {
     // false if it does not; else `bin`, and `want` less what is in the bins
     // before it.  The last bin of counts, in which most of a peaked row may
     // fall, is summed in registers: its atomics would wait for one another.
-    template <bool MASS, class Bin, class Want>
+    // (That of masses fills up only where a cut is wanted far down a tail.)
+    // FIRST: masses in the bins' own units, totals in the common one; else both
+    // in the unit of per_weight.
+    template <bool MASS, bool FIRST, class Bin, class Want>
     __device__ __forceinline__ bool histogram(float low, Bin bin_in, Want wanted, u64 &want, uint32_t &bin)
     {
         reinterpret_cast<uint4 *>(count)[tid] = make_uint4(0, 0, 0, 0);
@@ -898,7 +938,7 @@ struct Draw {
                 const bool in = b >= 0 & (MASS | b != kBins - 1);
                 last += !MASS & b == kBins - 1 ? 1u : 0u;
                 at[e] = count + (in ? b : kBins + static_cast<int>(lane));
-                holds[e] = in ? (MASS ? mass(x[e]) : 1u) : 0u;
+                holds[e] = !in ? 0u : !MASS ? 1u : mass_of(exp2_approx((x[e] - top) * scale), FIRST ? per_weight_in(b) : per_weight);
             }
 #pragma unroll
             for (int e = 0; e < kOwn; ++e) old[e] = shared_add(at[e], holds[e]);
@@ -934,6 +974,7 @@ struct Draw {
 #pragma unroll 1
             for (unsigned r = 0; r < blocks; ++r)
                 h += low_parts[r * part + b] | static_cast<u64>(high_parts[r * part + b]) << 32;
+            if (MASS && FIRST) h = common(h, rank * part + b);
 #pragma unroll 1
             for (unsigned r = 0; r < blocks; ++r) put(&sums[rank * part + b], r, h);
         }
@@ -991,18 +1032,22 @@ struct Draw {
     };
 
     // The range of ordered bits of the first histogram's bin where the cut
-    // lies, and what is wanted inside it; false if all that take part hold less
-    // than wanted.
+    // lies, and what is wanted inside it (masses in the bin's unit); false if all
+    // that take part hold less than wanted.
     template <bool MASS, class Want>
     __device__ __forceinline__ bool bracket(const Floor &floor, Want wanted, u64 &want, uint32_t &lo_bits, uint32_t &hi_bits)
     {
         uint32_t bin = 0;
-        const float span = MASS ? kMassSpan * t : reach;
-        bins_per_unit = fminf(fmaxf((kBins - 1) / span, 1e-30f), 1e30f);
-        const float least = MASS ? fmaxf(floor.v, top - span) : floor.v;
-        if (!histogram<MASS>(least, [&](float v, int i) { return floor.takes(v, i) & v >= least ? bin_of(v) : -1; },
-                             wanted, want, bin))
+        bins_per_unit = fminf(MASS ? kBinsPerBit * scale : fmaxf((kBins - 1) / reach, 1e-30f), 1e30f);
+        // A weight of less has no mass.
+        const float least = MASS ? fmaxf(floor.v, top - (kDeepest + 1) / scale) : floor.v;
+        if (!histogram<MASS, true>(least, [&](float v, int i) { return floor.takes(v, i) & v >= least ? bin_of(v) : -1; },
+                                   wanted, want, bin))
             return false;
+        if (MASS) {
+            per_weight = per_weight_in(static_cast<int>(bin));
+            want = in_bin(want, bin);
+        }
         if (warp < 2) {   // bin -1 would begin above the largest
             const uint32_t o = bin < warp ? ordered(top) + 1 : edge(static_cast<int>(bin - warp));
             if (lane == 0) s.pick_edge[warp] = o;
@@ -1072,7 +1117,7 @@ struct Draw {
             const uint32_t width = tie ? i_hi - i_lo : hi_bits - lo_bits;
             unsigned shift = 0;
             while (width >> shift >= kBins) ++shift;
-            histogram<MASS>(v_lo, [&](float v, int i) {
+            histogram<MASS, false>(v_lo, [&](float v, int i) {
                 if (!inside(v, i)) return -1;
                 return static_cast<int>((tie ? static_cast<unsigned>(i) - i_lo : hi_bits - ordered(v)) >> shift);
             }, same, want, bin);
@@ -1236,7 +1281,7 @@ __device__ __forceinline__ void draw_row(Draw<T, kKeeps<PASS>> &d, unsigned r, c
     int32_t *token = call.tokens + r;
     float *logprob = call.logprobs != nullptr ? call.logprobs + r : nullptr;
     d.t = t;
-    d.scale = fminf(1.4426950408889634f / t, FLT_MAX);
+    d.scale = fminf(fmaxf(1.4426950408889634f / t, FLT_TRUE_MIN), FLT_MAX);   // 0 times an infinite distance is none
     Race race;
     float most, sum = 0.0f;
     if (plain) most = d.race_all(race);
