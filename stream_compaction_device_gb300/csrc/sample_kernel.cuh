@@ -77,10 +77,10 @@ constexpr int kGroup = 4;                  // chunks that a thread loads at once
 constexpr int kQueue = 64;                 // entries that a warp has waiting
 // A row of at most kLoneChunks 16-byte chunks is one block's: 8,000 tokens took
 // 7.3 us in one block and 8.3 in two (bf16, top-k and top-p), 8.6 and 10.0 in
-// four (fp32, top-p).  Larger ones are dealt to more blocks, of at least
-// kLeastChunks each, while rows are few: 32,768 tokens of bf16 took 29, 24, 18
-// and 16 us in one, two, four and eight (top-p).
-constexpr unsigned kLoneChunks = 2048, kLeastChunks = 512;
+// four (fp32, top-p).  Larger ones are dealt to up to kMaxCluster blocks while
+// rows are few: 32,768 tokens of bf16 took 29, 24, 18 and 16 us in one, two, four
+// and eight (top-p).
+constexpr unsigned kLoneChunks = 2048;
 constexpr unsigned kKeptChunks = 4096;     // of a kept slice, for two blocks per SM: 64 KB
 constexpr unsigned kPolls = 1024;          // of the second launch for the first's rows, 64 ns apart
 constexpr int kList = 1024;                // tokens the short list holds
@@ -1584,9 +1584,7 @@ cudaError_t launch_typed(const SampleCall &call, const Workspace &ws, cudaStream
     const size_t rows = call.rows;
     const unsigned chunks = (call.vocab + Chunk<T>::kEach - 1) / Chunk<T>::kEach;
     const size_t sms = static_cast<size_t>(ws.num_sms), room = sms * kBlocksPerSm<Pass::Whole>;
-    unsigned wide = 1;               // the most blocks that a row of this size is worth
-    if (chunks > kLoneChunks)
-        while (wide < kMaxCluster && wide * kLeastChunks < chunks) wide *= 2;
+    const unsigned wide = chunks > kLoneChunks ? kMaxCluster : 1;   // the most blocks that a row of this size is worth
     const unsigned n = static_cast<unsigned>(rows);
     DevState &state = *ws.state;
     const Deferred later{call.row_words, &state.sample_rows, &state.sample_decided, &state.sample_next,
