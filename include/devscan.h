@@ -420,6 +420,8 @@ devscan_status block_table_release_i32(const int32_t *table, size_t stride, size
  * order or, where a cut needs a histogram, of integers in 64 bits (a weight is
  * rounded to 23 bits there, below 2^-32 to units of 2^-54, and the sum of a bin of
  * weights down to units of 2^-45), so that the same call gives the same bits.  A
+ * row alone or in another batch may differ in the last ones: how many blocks
+ * share a row, and so the order of its sums, follows from the number of rows.  A
  * token at the edge of top-p may fall on either side where its mass ahead is
  * within rounding of the mark.
  * Traffic: each row once, the noise of the kept tokens (all of it where

@@ -611,7 +611,11 @@ struct Draw {
     // A race of all tokens needs no selection, so it takes one pass over the
     // logits and the noise side by side.  Weights are relative to the largest
     // logit that the thread has seen; what it holds is scaled down when a
-    // larger one comes.
+    // larger one comes.  That adds up to 5 * 2^-24 relative each time (the
+    // distances add up to the token's own), once per chunk in a row that rises
+    // throughout: 262,144 such fp32 tokens in one block, 256 chunks per thread,
+    // gave log-probabilities of -12 with errors of up to 2.6e-6, rows that fall
+    // of up to 2.5e-6.
     __device__ __forceinline__ void rescale(Race &o, float &most, float to) const
     {
         const float f = fmaxf(exp2_approx((most - to) * scale), 0.0f);
