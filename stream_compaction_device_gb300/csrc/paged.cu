@@ -22,8 +22,9 @@
 // first and the last of them.
 //
 // What bounds it: a call of few rows its launch and one wait for memory (64
-// rows 4.9 us, 256 rows 3.9 us by device time, of which an empty kernel takes
-// more than half); 4,096 rows the scan in front (6.4 us with nothing to move)
+// rows 4.9 us, 256 rows 3.6 us by device time, of which an empty kernel takes
+// more than half); more than 4,096 rows the one block that scans them (900 rows
+// per us); 4,096 rows the scan in front (6.4 us with nothing to move)
 // and then memory: with nothing in L2 they extend by 2.8 M pages in 16 us and
 // release 2.1 M in 15 us (22 and 17 MB, 3.3 and 2.5 us at the copy rate), and
 // 2.7 M slots of 1,000 rows take 12 us (44 MB, 6.5 us).

@@ -40,18 +40,19 @@
 //     a second launch of wide clusters with them: read again by 2,048 threads
 //     it takes 25 us, where one block of 256 took 350.
 // Other sums are in fp32: a thread's in the order of its tokens, then over the
-// threads and blocks in a fixed tree.  Weights below 2^-126 count as 0.
+// threads and blocks in a fixed tree.  Weights below 2^-126 may count as 0.
 //
 // What bounds it (device time): rows that need no histogram, memory -- 256 x
 // 131072 fp32 with temperature alone 46 us for 268 MB (5.9 TB/s, 86% of the
-// copy rate), 512 x 131072 bf16 greedy 30 us for 134 MB, with top-k and top-p
+// copy rate), 512 x 131072 bf16 greedy 31 us for 134 MB, with top-k and top-p
 // 35 us.  Few rows, the chain of cluster barriers (about 1,200 cycles each)
 // and of steps in one block: 1 x 32768 bf16 with top-k and top-p 8.3 us, of
 // which the pass over the row is 0.6, the bound 1.5, collecting 2.9, the sort
 // 1.9, the cut and the race 1.4.  Flat rows, the two dense passes: 16 x 65536
-// fp32 with top-p 24 us, of which the histogram takes 2.5, its exchange 3.5,
-// the race 4.0.  512 x 131072 bf16 of mixed settings take 75 us: 35 for the
-// rows that a list does for, 30 for the others beside the longest races.
+// fp32 with top-p 20 to 24 us, by the rows, of which the histogram takes 2.5, its
+// exchange 3.5, the race 4.0.  512 x 131072 bf16 of mixed settings take 72 to 77
+// us: 35 for the rows that a list does for, 30 for the others beside the longest
+// races.
 #pragma once
 
 #include <cuda_bf16.h>
