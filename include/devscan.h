@@ -17,8 +17,9 @@
  * (cudaMallocAsync) and reuses for later calls on the same stream.  Calls on
  * one stream never race on it, from whichever host threads they come: a call
  * queues all of its launches before another on that stream queues any.  Calls
- * on different streams use different workspaces.  devscan_stream_release() frees
- * a stream's workspace.
+ * on different streams use different workspaces.  (cudaStreamPerThread is a
+ * stream per thread under one handle, and so one workspace: use it in one thread
+ * only.)  devscan_stream_release() frees a stream's workspace.
  *
  * Pages the operations follow:
  *   [P1] geek-doc.cn/chip-design/intermediate/parallel-prefix-scan,
