@@ -1,7 +1,8 @@
 /*
  * devscan -- device-wide parallel prefix scan, stream compaction and radix
- * one-bit split for one NVIDIA GB300 GPU (sm_103a), and the selections and
- * bookkeeping of a model's serving step that are made of them.
+ * one-bit split for one NVIDIA GB300 GPU (sm_103a), and what is made of them
+ * for language models: the selections and bookkeeping of a serving step, the
+ * gated recurrence, tokens sorted by expert, and the norm of all gradients.
  *
  * C ABI.  Every pointer argument of a compute call is a DEVICE pointer owned
  * by the caller; the library never frees, retains or reallocates it.  Every
@@ -450,6 +451,211 @@ devscan_status sample_tokens_bf16(const uint16_t *logits, size_t rows, size_t vo
                                   const float *noise, size_t noise_stride, const float *temperature,
                                   const int32_t *top_k, const float *top_p, const float *min_p, int32_t *tokens,
                                   float *logprobs, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Gated linear recurrence, and its gradient (P1 section 一: any associative
+ * operator can be scanned; here the maps h -> a h + b, channel by channel).
+ * In every row of tokens, from the row's first to its last,
+ *   h_t = a_t h_{t-1} + b_t:
+ *   DEVSCAN_GATE_DECAY   : a = gate,                    b = x;
+ *   DEVSCAN_GATE_LOG     : a = exp(gate),               b = x;
+ *   DEVSCAN_GATE_SIGMOID : a = 1 / (1 + exp(-gate)),    b = (1 - a) x.
+ * out is h in x's type; the recurrence itself runs in fp32.  Gates are meant
+ * to have |a| <= 1: products of up to 1,024 of them are formed, and where one
+ * overflows so may what is 0 times it.
+ *
+ *   x, gate, out : device arrays of rows of tokens of `channels` neighbouring
+ *             values; token t of row r is at r * row_stride + t * stride
+ *             (in elements; inputs may repeat themselves with a stride of 0,
+ *             outputs' tokens must not overlap).  gate has x's type, or with
+ *             gate_f32 != 0 is fp32 (always so in the f32 calls).
+ *   rows, tokens : rows of `tokens` each; tokens == 1 is a decode step (one
+ *             launch without any exchange).  rows * tokens < INT32_MAX - 1;
+ *   starts  : NULL, or device int32[rows + 1], not decreasing: the rows lie
+ *             packed behind each other (slot_map's starts are such), token t of
+ *             the packing at t * stride, row r being the tokens starts[r] ..
+ *             starts[r + 1] - 1 of the `tokens` that there are.  Rows may be
+ *             empty.  Tokens in no row (a padded batch) get 0 and are not
+ *             otherwise looked at; row_strides are not used;
+ *   initial : device float[pool][channels] or NULL (0): h before a row's
+ *             first token.  The first token's gate counts only with it;
+ *   final   : device float[pool][channels] or NULL: gets h after a row's last
+ *             token; for an empty row, initial.  It may be `initial` itself;
+ *   slots   : device int32[rows] or NULL: row r's state is at slots[r] in
+ *             both.  A row whose slot lies outside 0 .. pool - 1 has no state:
+ *             it starts from 0 and leaves none.  States of other slots stay as
+ *             they are.  Slots of two rows should differ; if not, which row's
+ *             state remains is not defined.  NULL: r itself, pool >= rows.
+ * out may be x itself, with its strides; otherwise it overlaps no other array,
+ * except that arrays of the same strides may lie side by side in each
+ * token (DEVSCAN_ERR_INVALID).  Pointers are aligned to their element.
+ *
+ * gated_scan_backward_T, from the gradients of out (grad, in its type) and of
+ * final (grad_final, float[rows][channels] or NULL), gives those of x, gate
+ * (each in its type) and initial (grad_initial, float[rows][channels] or
+ * NULL).  y is what the forward call wrote to out.  With f = grad_final (or 0)
+ * behind a row's last token and w = grad_t + f, from the last token to the
+ * first:
+ *   grad_x = w (sigmoid: (1 - a) w),   f = a w (at last: grad_initial),
+ *   grad_gate = w h' (decay), w h' a (log), w (h' - x) a (1 - a) (sigmoid),
+ * h' being y of the token before, or initial.  x is read for sigmoid only (else
+ * it may be NULL).  States lie by row (no slots); tokens in no row get 0;
+ * outputs overlap nothing but as above.
+ *
+ * Traffic: each value once.  No scratch; the same call gives the same bits.
+ * ------------------------------------------------------------------------- */
+typedef enum devscan_gate { DEVSCAN_GATE_DECAY = 0, DEVSCAN_GATE_LOG = 1, DEVSCAN_GATE_SIGMOID = 2 } devscan_gate;
+
+devscan_status gated_scan_f32(const float *x, size_t x_row_stride, size_t x_stride, const void *gate,
+                             size_t gate_row_stride, size_t gate_stride, int gate_f32, size_t rows, size_t tokens,
+                             size_t channels, const int32_t *starts, const float *initial, const int32_t *slots,
+                             size_t pool, devscan_gate kind, float *out, size_t out_row_stride, size_t out_stride,
+                             float *final, cudaStream_t stream);
+devscan_status gated_scan_f16(const uint16_t *x, size_t x_row_stride, size_t x_stride, const void *gate,
+                             size_t gate_row_stride, size_t gate_stride, int gate_f32, size_t rows, size_t tokens,
+                             size_t channels, const int32_t *starts, const float *initial, const int32_t *slots,
+                             size_t pool, devscan_gate kind, uint16_t *out, size_t out_row_stride, size_t out_stride,
+                             float *final, cudaStream_t stream);
+devscan_status gated_scan_bf16(const uint16_t *x, size_t x_row_stride, size_t x_stride, const void *gate,
+                             size_t gate_row_stride, size_t gate_stride, int gate_f32, size_t rows, size_t tokens,
+                             size_t channels, const int32_t *starts, const float *initial, const int32_t *slots,
+                             size_t pool, devscan_gate kind, uint16_t *out, size_t out_row_stride, size_t out_stride,
+                             float *final, cudaStream_t stream);
+devscan_status gated_scan_backward_f32(const float *grad, size_t grad_row_stride, size_t grad_stride, const float *x,
+                                      size_t x_row_stride, size_t x_stride, const void *gate, size_t gate_row_stride,
+                                      size_t gate_stride, int gate_f32, const float *y, size_t y_row_stride,
+                                      size_t y_stride, size_t rows, size_t tokens, size_t channels,
+                                      const int32_t *starts, const float *initial, const float *grad_final,
+                                      devscan_gate kind, float *grad_x, size_t grad_x_row_stride, size_t grad_x_stride,
+                                      void *grad_gate, size_t grad_gate_row_stride, size_t grad_gate_stride,
+                                      float *grad_initial, cudaStream_t stream);
+devscan_status gated_scan_backward_f16(const uint16_t *grad, size_t grad_row_stride, size_t grad_stride, const uint16_t *x,
+                                      size_t x_row_stride, size_t x_stride, const void *gate, size_t gate_row_stride,
+                                      size_t gate_stride, int gate_f32, const uint16_t *y, size_t y_row_stride,
+                                      size_t y_stride, size_t rows, size_t tokens, size_t channels,
+                                      const int32_t *starts, const float *initial, const float *grad_final,
+                                      devscan_gate kind, uint16_t *grad_x, size_t grad_x_row_stride, size_t grad_x_stride,
+                                      void *grad_gate, size_t grad_gate_row_stride, size_t grad_gate_stride,
+                                      float *grad_initial, cudaStream_t stream);
+devscan_status gated_scan_backward_bf16(const uint16_t *grad, size_t grad_row_stride, size_t grad_stride, const uint16_t *x,
+                                      size_t x_row_stride, size_t x_stride, const void *gate, size_t gate_row_stride,
+                                      size_t gate_stride, int gate_f32, const uint16_t *y, size_t y_row_stride,
+                                      size_t y_stride, size_t rows, size_t tokens, size_t channels,
+                                      const int32_t *starts, const float *initial, const float *grad_final,
+                                      devscan_gate kind, uint16_t *grad_x, size_t grad_x_row_stride, size_t grad_x_stride,
+                                      void *grad_gate, size_t grad_gate_row_stride, size_t grad_gate_stride,
+                                      float *grad_initial, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Tokens sorted by expert, and back (P2 section 4.2: counts per digit, a
+ * prefix over them, a stable scatter; the expert is the only digit).  Each of
+ * `tokens` tokens goes to `choices` experts: pair i = t * choices + k has the
+ * expert ids[i], and a place, a row among the rows of its expert.
+ *
+ * expert_sort_T: expert e's rows are starts[e] .. starts[e + 1] - 1, of which
+ * the first counts[e] hold its pairs in the order of i, and the rest round
+ * their number up to a multiple of `align`.
+ *   places[i] : pair i's row, or -1: its id is outside 0 .. experts - 1 (it
+ *               is not counted), or its row is not below `rows`;
+ *   order[r]  : the pair of row r, -1 for a row that rounds up a segment, -2
+ *               behind the last segment, for r below `rows`.
+ *   ids : device int32 or int64 [tokens * choices];  starts : device
+ *   int32[experts + 1];  counts : device int32[experts];  order : device
+ *   int32[rows];  places : device int32[tokens * choices].
+ *   experts : 1 .. DEVSCAN_MAX_EXPERTS;  tokens * choices + experts * (align -
+ *   1) <= INT32_MAX, and that many rows always suffice.
+ *
+ * expert_dispatch: row places[i] of out becomes row i / choices of x, byte for
+ * byte; with `order` (or NULL), rows of which order says -1 become 0.  Other
+ * rows are left as they were.  x: device, `tokens` rows of row_bytes bytes,
+ * x_stride bytes apart; out: `rows` rows, out_stride bytes apart.  Its
+ * gradient is expert_combine without weights.
+ *
+ * expert_combine_T: out[t] = sum over k of weights[i] y[places[i]], i = t *
+ * choices + k, in fp32 in the order of k, rounded once; a pair without a place
+ * adds nothing.  weights: device float[tokens * choices] or NULL (1).
+ * Strides in elements.
+ *
+ * expert_combine_backward_T: grad_y[places[i]] = weights[i] grad[t], and
+ * grad_weights[i] = <grad[t], y[places[i]]> in fp32 (0 without a place);
+ * grad_weights may be NULL, and then y too.  Rows of which `order` (or NULL)
+ * says -1 become 0, others are left as they were.
+ *
+ * Places outside 0 .. rows - 1 count as none; two pairs with the same place
+ * (expert_sort gives none) leave either's row.  No buffer that is written may
+ * overlap another (DEVSCAN_ERR_INVALID).  No scratch; the same call gives the
+ * same bits.  Rows that begin on 16 bytes and are a multiple of 16 bytes long
+ * move fastest.
+ * ------------------------------------------------------------------------- */
+#define DEVSCAN_MAX_EXPERTS 1024
+
+devscan_status expert_sort_i32(const int32_t *ids, size_t tokens, size_t choices, size_t experts, size_t align,
+                              size_t rows, int32_t *starts, int32_t *counts, int32_t *order, int32_t *places,
+                              cudaStream_t stream);
+devscan_status expert_sort_i64(const int64_t *ids, size_t tokens, size_t choices, size_t experts, size_t align,
+                              size_t rows, int32_t *starts, int32_t *counts, int32_t *order, int32_t *places,
+                              cudaStream_t stream);
+devscan_status expert_dispatch(const void *x, size_t x_stride, size_t row_bytes, size_t tokens, size_t choices,
+                               const int32_t *places, size_t rows, const int32_t *order, void *out, size_t out_stride,
+                               cudaStream_t stream);
+devscan_status expert_combine_f32(const float *y, size_t y_stride, size_t rows, size_t tokens, size_t choices,
+                                 size_t width, const int32_t *places, const float *weights, float *out,
+                                 size_t out_stride, cudaStream_t stream);
+devscan_status expert_combine_f16(const uint16_t *y, size_t y_stride, size_t rows, size_t tokens, size_t choices,
+                                 size_t width, const int32_t *places, const float *weights, uint16_t *out,
+                                 size_t out_stride, cudaStream_t stream);
+devscan_status expert_combine_bf16(const uint16_t *y, size_t y_stride, size_t rows, size_t tokens, size_t choices,
+                                 size_t width, const int32_t *places, const float *weights, uint16_t *out,
+                                 size_t out_stride, cudaStream_t stream);
+devscan_status expert_combine_backward_f32(const float *grad, size_t grad_stride, const float *y, size_t y_stride,
+                                          size_t rows, size_t tokens, size_t choices, size_t width,
+                                          const int32_t *places, const float *weights, const int32_t *order,
+                                          float *grad_y, size_t grad_y_stride, float *grad_weights, cudaStream_t stream);
+devscan_status expert_combine_backward_f16(const uint16_t *grad, size_t grad_stride, const uint16_t *y, size_t y_stride,
+                                          size_t rows, size_t tokens, size_t choices, size_t width,
+                                          const int32_t *places, const float *weights, const int32_t *order,
+                                          uint16_t *grad_y, size_t grad_y_stride, float *grad_weights, cudaStream_t stream);
+devscan_status expert_combine_backward_bf16(const uint16_t *grad, size_t grad_stride, const uint16_t *y, size_t y_stride,
+                                          size_t rows, size_t tokens, size_t choices, size_t width,
+                                          const int32_t *places, const float *weights, const int32_t *order,
+                                          uint16_t *grad_y, size_t grad_y_stride, float *grad_weights, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The 2-norm over many tensors, and their clipping (the fold of P1 section
+ * 四 over arrays that lie anywhere):
+ *   *norm = sqrt(sum over all tensors and elements of in^2),
+ *   out   = in min(1, max_norm / (norm + 1e-6)), rounded once.
+ * A norm that is infinite or NaN clips nothing (out = in): the caller, who
+ * reads it, decides.  Squares neither overflow nor vanish, whatever the
+ * values' size; sums are fp32 for 64 values and fp64 above, in a fixed order, so
+ * that the same call gives the same bits.
+ *
+ *   tensors : HOST array of `count` (at most 2^24), read during the call; each
+ *             has n elements of `type` at the device pointers in and out,
+ *             aligned to the element.  out may be in, otherwise it overlaps
+ *             nothing; the outs of two tensors must not overlap (not checked).
+ *             grad_norm does not use out.
+ *   norm    : device float; max_norm: at least 0;
+ *   work    : device scratch of the caller's, 8-byte aligned, of work_bytes >=
+ *             DEVSCAN_NORM_WORK_BYTES(count); its content before and after
+ *             means nothing, and two calls that may run at once need one each.
+ * Two launches (for every 512 tensors).  Traffic: each tensor once for the
+ * norm; to clip, once more and written, unless nothing is to be done in place.
+ * ------------------------------------------------------------------------- */
+typedef enum devscan_type { DEVSCAN_TYPE_F32 = 0, DEVSCAN_TYPE_F16 = 1, DEVSCAN_TYPE_BF16 = 2 } devscan_type;
+typedef struct devscan_tensor {
+    const void *in;
+    void *out;
+    size_t n;
+    devscan_type type;
+} devscan_tensor;
+#define DEVSCAN_NORM_WORK_TENSORS 512
+#define DEVSCAN_NORM_WORK_BYTES(count) (((size_t)(count) / DEVSCAN_NORM_WORK_TENSORS + 1) * 8192)
+
+devscan_status grad_norm(const devscan_tensor *tensors, size_t count, float *norm, void *work, size_t work_bytes,
+                         cudaStream_t stream);
+devscan_status clip_grad_norm(const devscan_tensor *tensors, size_t count, float max_norm, float *norm, void *work,
+                              size_t work_bytes, cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Status and housekeeping.

@@ -18,6 +18,8 @@ __all__ = ["scan_inclusive", "scan_exclusive", "scan_inclusive_carry", "scan_exc
            "sharded_scan", "exchange_totals", "compact", "split_bit", "radix_sort", "radix_sort_digits", "scan_host",
            "compact_greater", "bracket_scan", "segmented_scan_inclusive", "segmented_scan_exclusive",
            "sample_tokens", "block_table_extend", "slot_map", "block_table_release",
+           "gated_scan", "gated_scan_backward", "expert_sort", "expert_dispatch", "expert_combine",
+           "expert_combine_backward", "grad_norm", "clip_grad_norm",
            "device_status", "set_carry_mode", "stream_release", "selftest_stalled_wait", "DevscanError",
            "load"]
 
@@ -482,6 +484,372 @@ def sample_tokens(logits: torch.Tensor, noise: torch.Tensor | None = None, tempe
     if status:
         _lib.check(status, _SAMPLE_SYMBOL[logits.dtype])
     return out, logprobs
+
+
+_VALUES = {torch.float32: "f32", torch.float16: "f16", torch.bfloat16: "bf16"}
+
+
+def _value_suffix(t: torch.Tensor) -> str:
+    suffix = _VALUES.get(t.dtype)
+    if suffix is None:
+        raise TypeError(f"unsupported dtype {t.dtype} (float32, float16, bfloat16)")
+    return suffix
+
+
+def _here(t: torch.Tensor, name: str) -> torch.Tensor:
+    """A CUDA tensor of the current device, whose stream the call takes."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} must be on the current device")
+    return t
+
+
+def _token_array(t: torch.Tensor, name: str, shape, dtype):
+    """(address, row stride, token stride) of a tensor [rows, tokens, channels]
+    or [tokens, channels] with neighbouring channels."""
+    _here(t, name)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    strides = t.stride()
+    if strides[-1] != 1 and shape[-1] != 1:
+        raise ValueError(f"{name}'s channels must be contiguous")
+    return t.data_ptr(), strides[0] if len(strides) == 3 else 0, strides[-2]
+
+
+def _gated_rows(x: torch.Tensor, gate: torch.Tensor, starts, kind: str):
+    """(rows, tokens, channels, whether the gates are fp32 beside 16 bits)."""
+    if kind not in _lib.GATES:
+        raise ValueError(f"unknown kind {kind!r} (decay, log, sigmoid)")
+    if gate.dtype != x.dtype and gate.dtype != torch.float32:
+        raise TypeError("gate must be float32 or of x's type")
+    if x.dim() == 3:
+        if starts is not None:
+            raise ValueError("packed rows (starts) need [tokens, channels]")
+        rows, tokens, channels = x.shape
+    elif x.dim() == 2:
+        tokens, channels = x.shape
+        rows = 1
+        if starts is not None:
+            if starts.numel() < 1:
+                raise ValueError("starts must hold rows + 1 elements")
+            rows = starts.numel() - 1
+    else:
+        raise ValueError("x must be [rows, tokens, channels] or [tokens, channels]")
+    if channels < 1:
+        raise ValueError("x must have channels")
+    return rows, tokens, channels, gate.dtype != x.dtype
+
+
+def _states(t, name: str, channels: int, pool=None):
+    """Address of fp32 states [pool, channels]; None for None."""
+    if t is None:
+        return None
+    _here(t, name)
+    if t.dim() != 2 or t.shape[1] != channels or (pool is not None and t.shape[0] != pool) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [{'states' if pool is None else pool}, {channels}]")
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be float32")
+    return t.data_ptr()
+
+
+def gated_scan(x: torch.Tensor, gate: torch.Tensor, starts: torch.Tensor | None = None,
+               initial: torch.Tensor | None = None, slots: torch.Tensor | None = None, kind: str = "decay",
+               out: torch.Tensor | None = None, final: torch.Tensor | None = None, stream=None):
+    """Gated linear recurrence h_t = a_t h_{t-1} + b_t over every row's tokens,
+    channel by channel, in fp32: ``kind`` "decay" (a = gate, b = x), "log" (a =
+    exp(gate), b = x) or "sigmoid" (a = sigmoid(gate), b = (1 - a) x).
+
+    ``x`` (float32, float16 or bfloat16) is [rows, tokens, channels], or
+    [tokens, channels]: one row, or with ``starts`` (int32, rows + 1, as
+    ``slot_map`` gives them) packed rows; tokens in no row get 0.  ``gate`` has
+    x's shape, and its type or float32.  Only the channels need to be
+    contiguous.  ``initial`` (fp32 [states, channels]) holds the rows' h before
+    their first token; ``slots`` (int32 per row) says where in it, and in
+    ``final``, which takes h after their last token.  One token per row is the
+    decode step.
+
+    Returns (out, final).  ``out`` may be ``x`` itself and ``final`` may be
+    ``initial`` itself; without ``final``, rows with slots leave their states in
+    ``initial``, and others in a new tensor."""
+    suffix = _value_suffix(x)
+    rows, tokens, channels, wide = _gated_rows(x, gate, starts, kind)
+    if final is None:
+        if slots is None:
+            final = torch.empty(rows, channels, dtype=torch.float32, device=x.device)
+        elif initial is None:
+            raise ValueError("slots need initial or final to point into")
+        else:
+            final = initial
+    pool = final.shape[0] if final.dim() else 0
+    if slots is None and pool != rows:
+        raise ValueError(f"final must hold {rows} states")
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    shape, i32 = x.shape, torch.int32
+    name = "gated_scan_" + suffix
+    status = getattr(load(), name)(
+        *_token_array(x, "x", shape, x.dtype), *_token_array(gate, "gate", shape, gate.dtype), wide, rows, tokens,
+        channels, None if starts is None else _check_vector(_here(starts, "starts"), "starts", i32, rows + 1),
+        _states(initial, "initial", channels, pool),
+        None if slots is None else _check_vector(_here(slots, "slots"), "slots", i32, rows), pool, _lib.GATES[kind],
+        *_token_array(out, "out", shape, x.dtype), _states(final, "final", channels), _stream_handle(stream))
+    if status:
+        _lib.check(status, name)
+    return out, final
+
+
+def gated_scan_backward(grad: torch.Tensor, x: torch.Tensor | None, gate: torch.Tensor, y: torch.Tensor,
+                        starts: torch.Tensor | None = None, initial: torch.Tensor | None = None,
+                        grad_final: torch.Tensor | None = None, kind: str = "decay",
+                        grad_x: torch.Tensor | None = None, grad_gate: torch.Tensor | None = None,
+                        grad_initial: torch.Tensor | None = None, stream=None):
+    """Gradients of :func:`gated_scan` (without slots): from those of its
+    outputs, ``grad`` and ``grad_final`` (fp32 [rows, channels], optional), and
+    from what it was given and gave (``y``, its ``out``), those of ``x`` and
+    ``gate`` in their types and of ``initial``.  ``x`` is read for "sigmoid"
+    only, and may be None otherwise.  Returns (grad_x, grad_gate,
+    grad_initial), the last None where there is neither ``initial`` nor a
+    tensor for it."""
+    suffix = _value_suffix(y)
+    rows, tokens, channels, wide = _gated_rows(y, gate, starts, kind)
+    shape = y.shape
+    if kind == "sigmoid" and x is None:
+        raise ValueError("sigmoid needs x")
+    new = lambda *size, dtype: torch.empty(*size, dtype=dtype, device=y.device)  # noqa: E731
+    if grad_x is None:
+        grad_x = new(shape, dtype=y.dtype)
+    if grad_gate is None:
+        grad_gate = new(shape, dtype=gate.dtype)
+    if grad_initial is None and initial is not None:
+        grad_initial = new(rows, channels, dtype=torch.float32)
+    name = "gated_scan_backward_" + suffix
+    status = getattr(load(), name)(
+        *_token_array(grad, "grad", shape, y.dtype),
+        *((None, 0, 0) if x is None else _token_array(x, "x", shape, y.dtype)),
+        *_token_array(gate, "gate", shape, gate.dtype), wide, *_token_array(y, "y", shape, y.dtype), rows, tokens,
+        channels, None if starts is None else _check_vector(_here(starts, "starts"), "starts", torch.int32, rows + 1),
+        _states(initial, "initial", channels, rows), _states(grad_final, "grad_final", channels, rows),
+        _lib.GATES[kind], *_token_array(grad_x, "grad_x", shape, y.dtype),
+        *_token_array(grad_gate, "grad_gate", shape, gate.dtype),
+        _states(grad_initial, "grad_initial", channels, rows), _stream_handle(stream))
+    if status:
+        _lib.check(status, name)
+    return grad_x, grad_gate, grad_initial
+
+
+_IDS = {torch.int32: "expert_sort_i32", torch.int64: "expert_sort_i64"}
+
+
+def expert_sort(experts: torch.Tensor, num_experts: int, align: int = 1, rows: int | None = None,
+                starts: torch.Tensor | None = None, counts: torch.Tensor | None = None,
+                order: torch.Tensor | None = None, places: torch.Tensor | None = None, stream=None):
+    """Sort the pairs (token, choice) of ``experts`` (int32 or int64 [tokens,
+    choices], as a top-k gives them) stably by expert, every expert's rows
+    rounded up to a multiple of ``align``.  Returns (starts, counts, order,
+    places), all int32: each expert's first row and the number of rows
+    [num_experts + 1], its number of pairs [num_experts], for every row the pair
+    that lies there (-1: rounds up, -2: behind the last segment), and for
+    every pair its row (-1 where its id is outside 0 .. num_experts - 1).
+    ``rows`` is the number of rows that there are (by default what the pairs
+    can need at most); pairs beyond have no place."""
+    _here(experts, "experts")
+    name = _IDS.get(experts.dtype)
+    if name is None:
+        raise TypeError("experts must be int32 or int64")
+    if experts.dim() != 2 or not experts.is_contiguous():
+        raise ValueError("experts must be a contiguous [tokens, choices]")
+    tokens, choices = experts.shape
+    num_experts, align = int(num_experts), int(align)
+    if num_experts < 1 or align < 1 or choices < 1:
+        raise ValueError("num_experts, align and choices must be positive")
+    pairs = tokens * choices
+    if rows is None:
+        rows = order.numel() if order is not None else pairs + min(num_experts, pairs) * (align - 1)
+    rows = int(rows)
+    if rows < 0:
+        raise ValueError("rows must not be negative")
+    i32 = torch.int32
+    new = lambda *size: torch.empty(size, dtype=i32, device=experts.device)  # noqa: E731
+    starts = new(num_experts + 1) if starts is None else starts
+    counts = new(num_experts) if counts is None else counts
+    order = new(rows) if order is None else order
+    places = new(tokens, choices) if places is None else places
+    if places.shape != experts.shape:
+        raise ValueError("places must have the shape of experts")
+    status = getattr(load(), name)(
+        experts.data_ptr(), tokens, choices, num_experts, align, rows,
+        _check_vector(_here(starts, "starts"), "starts", i32, num_experts + 1),
+        _check_vector(_here(counts, "counts"), "counts", i32, num_experts),
+        _check_vector(_here(order, "order"), "order", i32, rows),
+        _check_vector(_here(places, "places"), "places", i32, pairs), _stream_handle(stream))
+    if status:
+        _lib.check(status, name)
+    return starts, counts, order, places
+
+
+def _check_rows(t: torch.Tensor, name: str, rows: int, width: int, dtype: torch.dtype) -> int:
+    """A matrix of that size on the current device; returns its row stride."""
+    stride = _check_matrix(_here(t, name), name)
+    if t.shape[0] != rows or t.shape[1] != width:
+        raise ValueError(f"{name} must be [{rows}, {width}]")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    return stride
+
+
+def _check_places(places: torch.Tensor):
+    _here(places, "places")
+    if places.dim() != 2 or not places.is_contiguous() or places.dtype != torch.int32:
+        raise ValueError("places must be a contiguous int32 [tokens, choices]")
+    if places.shape[1] < 1:
+        raise ValueError("places must hold a choice per token")
+    return places.shape
+
+
+def expert_dispatch(x: torch.Tensor, places: torch.Tensor, order: torch.Tensor, out: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """Copy every token's row of ``x`` (any type, [tokens, width]) to its
+    ``places``; rows that round up a segment (``order`` -1) become 0, those
+    behind the last segment are left as they were (in a new tensor: whatever is
+    there).  Returns ``out`` [rows, width].  The gradient of x is
+    ``expert_combine`` of out's, without weights."""
+    tokens, choices = _check_places(places)
+    if x.dim() != 2 or x.shape[1] < 1:
+        raise ValueError("x must be [tokens, width]")
+    width, rows, size = x.shape[1], order.numel(), x.element_size()
+    stride = _check_rows(x, "x", tokens, width, x.dtype)
+    if out is None:
+        out = torch.empty(rows, width, dtype=x.dtype, device=x.device)
+    status = load().expert_dispatch(
+        x.data_ptr(), stride * size, width * size, tokens, choices, places.data_ptr(), rows,
+        _check_vector(_here(order, "order"), "order", torch.int32, rows), out.data_ptr(),
+        _check_rows(out, "out", rows, width, x.dtype) * size, _stream_handle(stream))
+    if status:
+        _lib.check(status, "expert_dispatch")
+    return out
+
+
+def expert_combine(y: torch.Tensor, places: torch.Tensor, weights: torch.Tensor | None = None,
+                   out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Bring the experts' rows back: out[t] = sum over its choices of
+    ``weights`` (fp32 like ``places``; None: 1) times the rows of ``y`` [rows,
+    width] (float32, float16 or bfloat16) at its ``places``, summed in fp32.  A
+    token without any place gets 0."""
+    suffix = _value_suffix(y)
+    tokens, choices = _check_places(places)
+    if y.dim() != 2 or y.shape[1] < 1:
+        raise ValueError("y must be [rows, width]")
+    rows, width = y.shape
+    stride = _check_rows(y, "y", rows, width, y.dtype)
+    if out is None:
+        out = torch.empty(tokens, width, dtype=y.dtype, device=y.device)
+    name = "expert_combine_" + suffix
+    status = getattr(load(), name)(
+        y.data_ptr(), stride, rows, tokens, choices, width, places.data_ptr(),
+        None if weights is None else _check_vector(_here(weights, "weights"), "weights", torch.float32,
+                                                   tokens * choices),
+        out.data_ptr(), _check_rows(out, "out", tokens, width, y.dtype), _stream_handle(stream))
+    if status:
+        _lib.check(status, name)
+    return out
+
+
+def expert_combine_backward(grad: torch.Tensor, y: torch.Tensor, places: torch.Tensor,
+                            weights: torch.Tensor | None = None, order: torch.Tensor | None = None,
+                            grad_y: torch.Tensor | None = None, grad_weights: torch.Tensor | None = None,
+                            stream=None):
+    """Gradients of :func:`expert_combine`: from ``grad`` [tokens, width] those
+    of ``y`` and of the weights (fp32 like ``places``).  With ``order``, rows of
+    grad_y that round up a segment become 0; rows without a pair are otherwise
+    left as they were.  Returns (grad_y, grad_weights), the second None where
+    there are neither ``weights`` nor a tensor for it."""
+    suffix = _value_suffix(y)
+    tokens, choices = _check_places(places)
+    if y.dim() != 2 or y.shape[1] < 1:
+        raise ValueError("y must be [rows, width]")
+    rows, width = y.shape
+    if grad_y is None:
+        grad_y = torch.empty(rows, width, dtype=y.dtype, device=y.device)
+    if grad_weights is None and weights is not None:
+        grad_weights = torch.empty(tokens, choices, dtype=torch.float32, device=y.device)
+    f32 = torch.float32
+    vector = lambda t, what, dtype, size: None if t is None else _check_vector(_here(t, what), what, dtype, size)  # noqa: E731
+    name = "expert_combine_backward_" + suffix
+    status = getattr(load(), name)(
+        grad.data_ptr(), _check_rows(grad, "grad", tokens, width, y.dtype), y.data_ptr(),
+        _check_rows(y, "y", rows, width, y.dtype), rows, tokens, choices, width, places.data_ptr(),
+        vector(weights, "weights", f32, tokens * choices), vector(order, "order", torch.int32, rows),
+        grad_y.data_ptr(), _check_rows(grad_y, "grad_y", rows, width, y.dtype),
+        vector(grad_weights, "grad_weights", f32, tokens * choices), _stream_handle(stream))
+    if status:
+        _lib.check(status, name)
+    return grad_y, grad_weights
+
+
+_TENSOR_TYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+def _norm(tensors, out, max_norm, norm, work, stream):
+    tensors = list(tensors)
+    outs = tensors if out is None else list(out)
+    if len(outs) != len(tensors):
+        raise ValueError("out must hold a tensor for each of tensors")
+    count, here = len(tensors), torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
+    table = (_lib.Tensor * max(count, 1))()
+    for i, t in enumerate(tensors):
+        kind, o = _TENSOR_TYPE.get(t.dtype), outs[i]
+        if kind is None:
+            raise TypeError(f"unsupported dtype {t.dtype} (float32, float16, bfloat16)")
+        n = t.numel()
+        if not t.is_cuda or t.get_device() != here or not t.is_contiguous():
+            raise ValueError("tensors must be contiguous, on the current CUDA device")
+        if o is not t and (o.dtype != t.dtype or o.numel() != n or not o.is_cuda or o.get_device() != here
+                           or not o.is_contiguous()):
+            raise ValueError("each of out must match its tensor in type, size and device, and be contiguous")
+        entry = table[i]
+        entry.data, entry.out, entry.n, entry.type = t.data_ptr(), o.data_ptr(), n, kind
+    if norm is None:
+        norm = torch.empty(1, dtype=torch.float32, device="cuda")
+    need = _lib.norm_work_bytes(count)
+    if work is None:
+        work = torch.empty(need, dtype=torch.uint8, device="cuda")
+        if stream is not None:   # the allocator may give it away once that stream is through with it
+            work.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+    _check_cuda(_here(work, "work"), "work")
+    if work.numel() * work.element_size() < need:
+        raise ValueError(f"work must hold {need} bytes")
+    at = _check_vector(_here(norm, "norm"), "norm", torch.float32, 1)
+    size = work.numel() * work.element_size()
+    if max_norm is None:
+        _lib.check(load().grad_norm(table, count, at, work.data_ptr(), size, _stream_handle(stream)), "grad_norm")
+    else:
+        _lib.check(load().clip_grad_norm(table, count, max_norm, at, work.data_ptr(), size, _stream_handle(stream)),
+                   "clip_grad_norm")
+    return norm, outs
+
+
+def grad_norm(tensors, norm: torch.Tensor | None = None, work: torch.Tensor | None = None,
+              stream=None) -> torch.Tensor:
+    """2-norm over all elements of ``tensors`` (contiguous float32, float16 or
+    bfloat16, mixed as they come): one fp32 on the device.  Squares neither
+    overflow nor vanish.  ``work`` may pass the scratch (any type,
+    ``_lib.norm_work_bytes(len(tensors))`` bytes)."""
+    return _norm(tensors, None, None, norm, work, stream)[0]
+
+
+def clip_grad_norm(tensors, max_norm: float, out=None, norm: torch.Tensor | None = None,
+                   work: torch.Tensor | None = None, stream=None):
+    """Scale ``tensors`` by min(1, max_norm / (norm + 1e-6)), norm being that of
+    :func:`grad_norm` over all of them; in place, or into the tensors of
+    ``out``.  A norm that is infinite or NaN clips nothing.  Returns (norm, the
+    list of clipped tensors); nothing is read back to the host."""
+    max_norm = float(max_norm)
+    if not max_norm >= 0:
+        raise ValueError("max_norm must not be negative")
+    return _norm(tensors, out, max_norm, norm, work, stream)
 
 
 def scan_host(x_host: torch.Tensor, inclusive: bool = False, op: str = "add", device="cuda",

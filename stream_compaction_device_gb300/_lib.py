@@ -24,7 +24,24 @@ CARRY_SCAN_SYMBOLS = tuple(f"scan_{d}_carry_{t}" for d in ("inclusive", "exclusi
 REDUCE_SYMBOLS = ("reduce_i32", "reduce_u32", "reduce_f32")
 SEGSCAN_SYMBOLS = tuple(f"segmented_scan_{d}_{t}" for d in ("inclusive", "exclusive")
                         for t in ("i32", "u32", "f32"))
+GATED_SYMBOLS = ("gated_scan_f32", "gated_scan_f16", "gated_scan_bf16")
+GATED_BACKWARD_SYMBOLS = ("gated_scan_backward_f32", "gated_scan_backward_f16", "gated_scan_backward_bf16")
+EXPERT_SORT_SYMBOLS = ("expert_sort_i32", "expert_sort_i64")
+EXPERT_COMBINE_SYMBOLS = ("expert_combine_f32", "expert_combine_f16", "expert_combine_bf16")
+EXPERT_COMBINE_BACKWARD_SYMBOLS = ("expert_combine_backward_f32", "expert_combine_backward_f16",
+                                   "expert_combine_backward_bf16")
+GATES = {"decay": 0, "log": 1, "sigmoid": 2}
 SAMPLE_SYMBOLS = ("sample_tokens_f32", "sample_tokens_f16", "sample_tokens_bf16")
+
+
+class Tensor(ctypes.Structure):
+    """``devscan_tensor``."""
+    _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_size_t), ("type", ctypes.c_int)]
+
+
+def norm_work_bytes(count: int) -> int:
+    """``DEVSCAN_NORM_WORK_BYTES``."""
+    return (count // 512 + 1) * 8192
 
 
 class DevscanError(RuntimeError):
@@ -92,6 +109,33 @@ def load() -> ctypes.CDLL:
             fn = getattr(lib, name)
             fn.argtypes = [vp, sz, sz, sz, vp, sz, vp, vp, vp, vp, vp, vp, vp]
             fn.restype = i
+        for name in GATED_SYMBOLS:
+            fn = getattr(lib, name)
+            fn.argtypes = [vp, sz, sz, vp, sz, sz, i, sz, sz, sz, vp, vp, vp, sz, i, vp, sz, sz, vp, vp]
+            fn.restype = i
+        for name in GATED_BACKWARD_SYMBOLS:
+            fn = getattr(lib, name)
+            fn.argtypes = [vp, sz, sz, vp, sz, sz, vp, sz, sz, i, vp, sz, sz, sz, sz, sz, vp, vp, vp, i, vp, sz, sz,
+                           vp, sz, sz, vp, vp]
+            fn.restype = i
+        for name in EXPERT_SORT_SYMBOLS:
+            fn = getattr(lib, name)
+            fn.argtypes = [vp, sz, sz, sz, sz, sz, vp, vp, vp, vp, vp]
+            fn.restype = i
+        lib.expert_dispatch.argtypes = [vp, sz, sz, sz, sz, vp, sz, vp, vp, sz, vp]
+        lib.expert_dispatch.restype = i
+        for name in EXPERT_COMBINE_SYMBOLS:
+            fn = getattr(lib, name)
+            fn.argtypes = [vp, sz, sz, sz, sz, sz, vp, vp, vp, sz, vp]
+            fn.restype = i
+        for name in EXPERT_COMBINE_BACKWARD_SYMBOLS:
+            fn = getattr(lib, name)
+            fn.argtypes = [vp, sz, vp, sz, sz, sz, sz, sz, vp, vp, vp, vp, sz, vp, vp]
+            fn.restype = i
+        lib.grad_norm.argtypes = [vp, sz, vp, vp, sz, vp]
+        lib.grad_norm.restype = i
+        lib.clip_grad_norm.argtypes = [vp, sz, ctypes.c_float, vp, vp, sz, vp]
+        lib.clip_grad_norm.restype = i
         lib.devscan_device_status.argtypes = [vp]
         lib.devscan_device_status.restype = i
         lib.devscan_status_string.argtypes = [i]

@@ -8,6 +8,7 @@
 #include <mutex>
 #include <new>
 #include <utility>
+#include <vector>
 
 #include "../../include/devscan.h"
 #include "../../include/devscan_measure.h"
@@ -349,6 +350,273 @@ devscan_status sample_common(cudaError_t (*launch)(const SampleCall &, const Wor
         call.row_words = static_cast<uint32_t *>(row_words);
     }
     return from_cuda(launch(call, ws, stream));
+}
+
+// A call's array of values: rows of tokens of neighbouring channels, strides
+// in elements of `size` bytes.
+struct Values {
+    GatedArray array;
+    size_t size;
+    size_t bytes;   // from the first to behind the last
+};
+
+// Fills `bytes`; false where an argument is no good.  An output's tokens must
+// not overlap each other.
+bool check_values(Values *v, const GatedRows &rows, bool output)
+{
+    const size_t r = rows.starts != nullptr ? 1 : static_cast<size_t>(rows.rows), t = rows.tokens;
+    const size_t c = static_cast<size_t>(rows.channels);
+    v->bytes = 0;
+    if (r == 0 || t == 0) return true;
+    if (v->array.data == nullptr || misaligned(v->array.data, v->size)) return false;
+    const size_t most = (size_t(1) << 61) / v->size;
+    size_t rs = r > 1 ? v->array.row_stride : 0, ts = t > 1 ? v->array.stride : 0;
+    if ((rs != 0 && r - 1 > most / rs) || (ts != 0 && t - 1 > most / ts) || c > most) return false;
+    if (output) {
+        const bool rows_apart = r == 1 || rs >= (t - 1) * ts + c, tokens_apart = t == 1 || ts >= (r - 1) * rs + c;
+        if ((t > 1 && ts < c) || (r > 1 && rs < c) || !(rows_apart || tokens_apart)) return false;
+    }
+    v->bytes = ((r - 1) * rs + (t - 1) * ts + c) * v->size;
+    return true;
+}
+
+// Whether an output and another array may share memory: not where they lie
+// apart, nor where both have the same strides and their channels lie side by
+// side within a token's.
+bool values_overlap(const Values &a, const Values &b, const GatedRows &rows)
+{
+    if (a.bytes == 0 || b.bytes == 0 || !overlaps(a.array.data, a.bytes, b.array.data, b.bytes)) return false;
+    const size_t stride = a.array.stride * a.size, row = a.array.row_stride * a.size;
+    const bool one_row = rows.starts != nullptr || rows.rows == 1;
+    if (rows.tokens < 2 || stride == 0 || stride != b.array.stride * b.size) return true;
+    if (!one_row && (row != b.array.row_stride * b.size || row % stride != 0)) return true;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.array.data), y = reinterpret_cast<uintptr_t>(b.array.data);
+    const size_t shift = x <= y ? (y - x) % stride : (stride - (x - y) % stride) % stride;   // of b within a's token
+    const size_t c = static_cast<size_t>(rows.channels);
+    return shift < c * a.size || shift + c * b.size > stride;
+}
+
+// What forward and backward check alike.
+devscan_status gated_check(size_t rows, size_t tokens, size_t channels, const int32_t *starts, const int32_t *slots,
+                           size_t pool, devscan_gate kind, GatedRows *out)
+{
+    if (kind != DEVSCAN_GATE_DECAY && kind != DEVSCAN_GATE_LOG && kind != DEVSCAN_GATE_SIGMOID)
+        return DEVSCAN_ERR_INVALID;
+    constexpr size_t kMost = static_cast<size_t>(INT32_MAX) - 1;
+    if (rows > kMost || tokens > kMost || channels > kMost || pool > kMost || channels < 1) return DEVSCAN_ERR_INVALID;
+    if (starts == nullptr && rows * tokens > kMost) return DEVSCAN_ERR_INVALID;
+    if (misaligned(starts, 4) || misaligned(slots, 4)) return DEVSCAN_ERR_INVALID;
+    *out = {starts, slots, static_cast<int>(rows), static_cast<int>(channels), static_cast<int>(pool),
+            static_cast<unsigned>(tokens), 0, 0, 0};
+    return DEVSCAN_OK;
+}
+
+devscan_status current_sms(int *sms)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return DEVSCAN_ERR_CUDA;
+    return DEVSCAN_OK;
+}
+
+using GatedScanLaunch = cudaError_t (*)(const GatedScanCall &, bool, int, cudaStream_t);
+using GatedBackwardLaunch = cudaError_t (*)(const GatedBackwardCall &, bool, int, cudaStream_t);
+
+devscan_status gated_scan_common(GatedScanLaunch launch, size_t size, GatedScanCall call, int gate_f32, size_t rows,
+                                 size_t tokens, size_t channels, size_t pool, devscan_gate kind, cudaStream_t stream)
+{
+    devscan_status st = gated_check(rows, tokens, channels, call.rows.starts, call.rows.slots, pool, kind, &call.rows);
+    if (st != DEVSCAN_OK) return st;
+    call.kind = kind;
+    if (rows == 0 && call.rows.starts == nullptr) return DEVSCAN_OK;
+    const bool wide = size == 2 && gate_f32 != 0;
+    Values x = {call.x, size, 0}, gate = {call.gate, wide ? 4 : size, 0}, out = {call.out, size, 0};
+    if (!check_values(&x, call.rows, false) || !check_values(&gate, call.rows, false) || !check_values(&out, call.rows, true))
+        return DEVSCAN_ERR_INVALID;
+    if (misaligned(call.initial, 4) || misaligned(call.final, 4)) return DEVSCAN_ERR_INVALID;
+    if (call.rows.slots == nullptr && (call.initial != nullptr || call.final != nullptr) && pool < rows)
+        return DEVSCAN_ERR_INVALID;
+    size_t states = 0;
+    if (!matrix_bytes(pool, channels, channels, 4, &states)) return DEVSCAN_ERR_INVALID;
+    const bool in_place = out.array.data == x.array.data && out.array.stride == x.array.stride &&
+                          out.array.row_stride == x.array.row_stride;
+    if ((!in_place && values_overlap(out, x, call.rows)) || values_overlap(out, gate, call.rows)) return DEVSCAN_ERR_INVALID;
+    const size_t starts = call.rows.starts != nullptr ? (rows + 1) * 4 : 0, slots = rows * 4;
+    const Span written[] = {{out.array.data, out.bytes}, {call.final, states}};
+    const Span read[] = {{call.rows.starts, starts}, {call.rows.slots, slots}};
+    if (written_overlap(written, read)) return DEVSCAN_ERR_INVALID;
+    if (call.initial != call.final) {   // the states in place are the same pool
+        const Span next[] = {{call.final, states}}, last[] = {{call.initial, states}};
+        if (written_overlap(next, last)) return DEVSCAN_ERR_INVALID;
+    }
+    const Span result[] = {{out.array.data, out.bytes}}, before[] = {{call.initial, states}};
+    const Span next[] = {{call.final, states}}, values[] = {{x.array.data, x.bytes}, {gate.array.data, gate.bytes}};
+    if (written_overlap(result, before) || written_overlap(next, values)) return DEVSCAN_ERR_INVALID;
+    int sms = 0;
+    st = current_sms(&sms);
+    return st != DEVSCAN_OK ? st : from_cuda(launch(call, wide, sms, stream));
+}
+
+devscan_status gated_backward_common(GatedBackwardLaunch launch, size_t size, GatedBackwardCall call, int gate_f32,
+                                     size_t rows, size_t tokens, size_t channels, devscan_gate kind, cudaStream_t stream)
+{
+    devscan_status st = gated_check(rows, tokens, channels, call.rows.starts, nullptr, rows, kind, &call.rows);
+    if (st != DEVSCAN_OK) return st;
+    call.kind = kind;
+    if (rows == 0 && call.rows.starts == nullptr) return DEVSCAN_OK;
+    const bool wide = size == 2 && gate_f32 != 0, sigmoid = kind == DEVSCAN_GATE_SIGMOID;
+    const size_t gate_size = wide ? 4 : size;
+    Values in[] = {{call.grad, size, 0}, {call.gate, gate_size, 0}, {call.y, size, 0}, {call.x, size, 0}};
+    Values out[] = {{call.grad_x, size, 0}, {call.grad_gate, gate_size, 0}};
+    const int ins = sigmoid ? 4 : 3;
+    for (int i = 0; i < ins; ++i)
+        if (!check_values(&in[i], call.rows, false)) return DEVSCAN_ERR_INVALID;
+    for (Values &v : out)
+        if (!check_values(&v, call.rows, true)) return DEVSCAN_ERR_INVALID;
+    if (misaligned(call.initial, 4) || misaligned(call.grad_final, 4) || misaligned(call.grad_initial, 4))
+        return DEVSCAN_ERR_INVALID;
+    for (const Values &v : out)
+        for (int i = 0; i < ins; ++i)
+            if (values_overlap(v, in[i], call.rows)) return DEVSCAN_ERR_INVALID;
+    if (values_overlap(out[0], out[1], call.rows)) return DEVSCAN_ERR_INVALID;
+    size_t states = 0;
+    if (!matrix_bytes(rows, channels, channels, 4, &states)) return DEVSCAN_ERR_INVALID;
+    const size_t starts = call.rows.starts != nullptr ? (rows + 1) * 4 : 0;
+    const Span more[] = {{call.rows.starts, starts}, {call.initial, states}, {call.grad_final, states}};
+    for (const Values &v : out) {
+        const Span written[] = {{v.array.data, v.bytes}, {call.grad_initial, states}};
+        if (written_overlap(written, more)) return DEVSCAN_ERR_INVALID;
+    }
+    for (int i = 0; i < ins; ++i) {
+        const Span written[] = {{call.grad_initial, states}}, read[] = {{in[i].array.data, in[i].bytes}};
+        if (written_overlap(written, read)) return DEVSCAN_ERR_INVALID;
+    }
+    int sms = 0;
+    st = current_sms(&sms);
+    return st != DEVSCAN_OK ? st : from_cuda(launch(call, wide, sms, stream));
+}
+
+devscan_status expert_sort_common(const void *ids, size_t id_size, size_t tokens, size_t choices, size_t experts,
+                                  size_t align, size_t rows, int32_t *starts, int32_t *counts, int32_t *order,
+                                  int32_t *places, cudaStream_t stream)
+{
+    constexpr size_t kMost = INT32_MAX;
+    if (experts < 1 || experts > static_cast<size_t>(kMostExperts) || align < 1 || choices < 1) return DEVSCAN_ERR_INVALID;
+    if (tokens > kMost || choices > kMost || tokens * choices > kMost || rows > kMost || align > kMost)
+        return DEVSCAN_ERR_INVALID;
+    const size_t pairs = tokens * choices;
+    if (pairs + experts * (align - 1) > kMost) return DEVSCAN_ERR_INVALID;
+    if (starts == nullptr || counts == nullptr || (rows > 0 && order == nullptr) ||
+        (pairs > 0 && (ids == nullptr || places == nullptr)))
+        return DEVSCAN_ERR_INVALID;
+    if (misaligned(ids, id_size) || misaligned(starts, 4) || misaligned(counts, 4) || misaligned(order, 4) ||
+        misaligned(places, 4))
+        return DEVSCAN_ERR_INVALID;
+    const Span written[] = {{starts, (experts + 1) * 4}, {counts, experts * 4}, {order, rows * 4}, {places, pairs * 4}};
+    const Span read[] = {{ids, pairs * id_size}};
+    if (written_overlap(written, read)) return DEVSCAN_ERR_INVALID;
+    return from_cuda(launch_expert_sort({ids, static_cast<unsigned>(pairs), static_cast<unsigned>(rows),
+                                         static_cast<unsigned>(align), static_cast<int>(experts), starts, counts, order,
+                                         places},
+                                        id_size == 8, stream));
+}
+
+// What the calls on rows of experts check alike: sizes, and the places.
+bool expert_sizes(size_t tokens, size_t choices, size_t rows, size_t width)
+{
+    constexpr size_t kMost = INT32_MAX;
+    return choices >= 1 && width >= 1 && tokens <= kMost && choices <= kMost && rows <= kMost && width <= kMost &&
+           tokens * choices <= kMost;
+}
+
+devscan_status expert_combine_common(ValueType type, const ExpertCombineCall &call, size_t rows, size_t tokens,
+                                     size_t choices, size_t width, cudaStream_t stream)
+{
+    const size_t size = type == ValueType::F32 ? 4 : 2;
+    if (!expert_sizes(tokens, choices, rows, width)) return DEVSCAN_ERR_INVALID;
+    if ((rows > 1 && call.y_stride < width) || (tokens > 1 && call.out_stride < width)) return DEVSCAN_ERR_INVALID;
+    if (tokens == 0) return DEVSCAN_OK;
+    if (call.places == nullptr || call.out == nullptr || (rows > 0 && call.y == nullptr)) return DEVSCAN_ERR_INVALID;
+    if (misaligned(call.y, size) || misaligned(call.out, size) || misaligned(call.places, 4) || misaligned(call.weights, 4))
+        return DEVSCAN_ERR_INVALID;
+    size_t y_bytes = 0, out_bytes = 0;
+    if (!matrix_bytes(rows, call.y_stride, width, size, &y_bytes) ||
+        !matrix_bytes(tokens, call.out_stride, width, size, &out_bytes))
+        return DEVSCAN_ERR_INVALID;
+    const Span written[] = {{call.out, out_bytes}};
+    const Span read[] = {{call.y, y_bytes}, {call.places, tokens * choices * 4}, {call.weights, tokens * choices * 4}};
+    if (written_overlap(written, read)) return DEVSCAN_ERR_INVALID;
+    ExpertCombineCall c = call;
+    c.rows = static_cast<unsigned>(rows), c.tokens = static_cast<unsigned>(tokens);
+    c.width = static_cast<unsigned>(width), c.choices = static_cast<int>(choices);
+    return from_cuda(launch_expert_combine(type, c, stream));
+}
+
+devscan_status expert_combine_backward_common(ValueType type, const ExpertCombineBackwardCall &call, size_t rows,
+                                              size_t tokens, size_t choices, size_t width, cudaStream_t stream)
+{
+    const size_t size = type == ValueType::F32 ? 4 : 2;
+    if (!expert_sizes(tokens, choices, rows, width)) return DEVSCAN_ERR_INVALID;
+    if ((rows > 1 && (call.y_stride < width || call.grad_y_stride < width)) || (tokens > 1 && call.grad_stride < width))
+        return DEVSCAN_ERR_INVALID;
+    if (tokens > 0 && (call.places == nullptr || call.grad == nullptr)) return DEVSCAN_ERR_INVALID;
+    if (rows > 0 && (call.grad_y == nullptr || (call.grad_weights != nullptr && call.y == nullptr)))
+        return DEVSCAN_ERR_INVALID;
+    if (misaligned(call.grad, size) || misaligned(call.y, size) || misaligned(call.grad_y, size) ||
+        misaligned(call.places, 4) || misaligned(call.order, 4) || misaligned(call.weights, 4) ||
+        misaligned(call.grad_weights, 4))
+        return DEVSCAN_ERR_INVALID;
+    size_t grad_bytes = 0, y_bytes = 0, grad_y_bytes = 0;
+    if (!matrix_bytes(tokens, call.grad_stride, width, size, &grad_bytes) ||
+        !matrix_bytes(rows, call.y_stride, width, size, &y_bytes) ||
+        !matrix_bytes(rows, call.grad_y_stride, width, size, &grad_y_bytes))
+        return DEVSCAN_ERR_INVALID;
+    const size_t pairs = tokens * choices * 4;
+    const Span written[] = {{call.grad_y, grad_y_bytes}, {call.grad_weights, pairs}};
+    const Span read[] = {{call.grad, grad_bytes}, {call.y, y_bytes},   {call.places, pairs},
+                         {call.order, rows * 4},  {call.weights, pairs}};
+    if (written_overlap(written, read)) return DEVSCAN_ERR_INVALID;
+    ExpertCombineBackwardCall c = call;
+    c.rows = static_cast<unsigned>(rows), c.tokens = static_cast<unsigned>(tokens);
+    c.width = static_cast<unsigned>(width), c.choices = static_cast<int>(choices);
+    return from_cuda(launch_expert_combine_backward(type, c, stream));
+}
+
+devscan_status norm_common(const devscan_tensor *tensors, size_t count, bool clip, float max_norm, float *norm, void *work,
+                           size_t work_bytes, cudaStream_t stream)
+try {
+    static_assert(DEVSCAN_NORM_WORK_TENSORS == kNormTensors && DEVSCAN_NORM_WORK_BYTES(1) == kNormBlocks * sizeof(double),
+                  "the header's scratch is the launch's");
+    constexpr size_t kMostTensors = size_t(1) << 24;
+    if (norm == nullptr || misaligned(norm, 4) || work == nullptr || misaligned(work, 8)) return DEVSCAN_ERR_INVALID;
+    if (count > kMostTensors || (count > 0 && tensors == nullptr)) return DEVSCAN_ERR_INVALID;
+    if (clip && !(max_norm >= 0.0f)) return DEVSCAN_ERR_INVALID;
+    const size_t need = DEVSCAN_NORM_WORK_BYTES(count);
+    if (work_bytes < need) return DEVSCAN_ERR_INVALID;
+    const Span written[] = {{norm, 4}, {work, need}};
+    std::vector<NormTensor> list(count);
+    for (size_t i = 0; i < count; ++i) {
+        const devscan_tensor &t = tensors[i];
+        if (t.type != DEVSCAN_TYPE_F32 && t.type != DEVSCAN_TYPE_F16 && t.type != DEVSCAN_TYPE_BF16)
+            return DEVSCAN_ERR_INVALID;
+        const size_t size = t.type == DEVSCAN_TYPE_F32 ? 4 : 2;
+        if (t.n > (size_t(1) << 60)) return DEVSCAN_ERR_INVALID;
+        list[i] = {t.in, clip ? t.out : nullptr, t.n, static_cast<ValueType>(t.type)};
+        if (t.n == 0) continue;
+        if (t.in == nullptr || misaligned(t.in, size)) return DEVSCAN_ERR_INVALID;
+        const Span in[] = {{t.in, t.n * size}};
+        if (written_overlap(written, in)) return DEVSCAN_ERR_INVALID;
+        if (!clip) continue;
+        if (t.out == nullptr || misaligned(t.out, size)) return DEVSCAN_ERR_INVALID;
+        const Span out[] = {{t.out, t.n * size}}, others[] = {{norm, 4}, {work, need}};
+        if (written_overlap(out, others) || (t.out != t.in && written_overlap(out, in))) return DEVSCAN_ERR_INVALID;
+    }
+    int sms = 0;
+    const devscan_status st = current_sms(&sms);
+    if (st != DEVSCAN_OK) return st;
+    return from_cuda(launch_grad_norm(list.data(), count, clip, max_norm, norm, static_cast<double *>(work), sms, stream));
+} catch (const std::bad_alloc &) {
+    return DEVSCAN_ERR_NOMEM;
 }
 
 }  // namespace
@@ -760,6 +1028,220 @@ devscan_status sample_tokens_bf16(const uint16_t *logits, size_t rows, size_t vo
                          {logits, rows, logits_stride, 0, noise, noise_stride, temperature, top_k, top_p, min_p, tokens,
                           logprobs, nullptr},
                          vocab, stream);
+}
+
+devscan_status gated_scan_f32(const float *x, size_t x_row_stride, size_t x_stride, const void *gate,
+                             size_t gate_row_stride, size_t gate_stride, int gate_f32, size_t rows, size_t tokens,
+                             size_t channels, const int32_t *starts, const float *initial, const int32_t *slots,
+                             size_t pool, devscan_gate kind, float *out, size_t out_row_stride, size_t out_stride,
+                             float *final, cudaStream_t stream)
+{
+    GatedScanCall call = {};
+    call.rows.starts = starts, call.rows.slots = slots;
+    call.x = {const_cast<float *>(x), x_row_stride, x_stride};
+    call.gate = {const_cast<void *>(gate), gate_row_stride, gate_stride};
+    call.out = {out, out_row_stride, out_stride};
+    call.initial = const_cast<float *>(initial), call.final = final;
+    return gated_scan_common(launch_gated_scan_f32, 4, call, gate_f32, rows, tokens, channels, pool, kind, stream);
+}
+
+devscan_status gated_scan_backward_f32(const float *grad, size_t grad_row_stride, size_t grad_stride, const float *x,
+                                      size_t x_row_stride, size_t x_stride, const void *gate, size_t gate_row_stride,
+                                      size_t gate_stride, int gate_f32, const float *y, size_t y_row_stride,
+                                      size_t y_stride, size_t rows, size_t tokens, size_t channels,
+                                      const int32_t *starts, const float *initial, const float *grad_final,
+                                      devscan_gate kind, float *grad_x, size_t grad_x_row_stride, size_t grad_x_stride,
+                                      void *grad_gate, size_t grad_gate_row_stride, size_t grad_gate_stride,
+                                      float *grad_initial, cudaStream_t stream)
+{
+    GatedBackwardCall call = {};
+    call.rows.starts = starts;
+    call.grad = {const_cast<float *>(grad), grad_row_stride, grad_stride};
+    call.x = {const_cast<float *>(x), x_row_stride, x_stride};
+    call.gate = {const_cast<void *>(gate), gate_row_stride, gate_stride};
+    call.y = {const_cast<float *>(y), y_row_stride, y_stride};
+    call.grad_x = {grad_x, grad_x_row_stride, grad_x_stride};
+    call.grad_gate = {grad_gate, grad_gate_row_stride, grad_gate_stride};
+    call.initial = const_cast<float *>(initial), call.grad_final = grad_final, call.grad_initial = grad_initial;
+    return gated_backward_common(launch_gated_backward_f32, 4, call, gate_f32, rows, tokens, channels, kind, stream);
+}
+
+devscan_status gated_scan_f16(const uint16_t *x, size_t x_row_stride, size_t x_stride, const void *gate,
+                             size_t gate_row_stride, size_t gate_stride, int gate_f32, size_t rows, size_t tokens,
+                             size_t channels, const int32_t *starts, const float *initial, const int32_t *slots,
+                             size_t pool, devscan_gate kind, uint16_t *out, size_t out_row_stride, size_t out_stride,
+                             float *final, cudaStream_t stream)
+{
+    GatedScanCall call = {};
+    call.rows.starts = starts, call.rows.slots = slots;
+    call.x = {const_cast<uint16_t *>(x), x_row_stride, x_stride};
+    call.gate = {const_cast<void *>(gate), gate_row_stride, gate_stride};
+    call.out = {out, out_row_stride, out_stride};
+    call.initial = const_cast<float *>(initial), call.final = final;
+    return gated_scan_common(launch_gated_scan_f16, 2, call, gate_f32, rows, tokens, channels, pool, kind, stream);
+}
+
+devscan_status gated_scan_backward_f16(const uint16_t *grad, size_t grad_row_stride, size_t grad_stride, const uint16_t *x,
+                                      size_t x_row_stride, size_t x_stride, const void *gate, size_t gate_row_stride,
+                                      size_t gate_stride, int gate_f32, const uint16_t *y, size_t y_row_stride,
+                                      size_t y_stride, size_t rows, size_t tokens, size_t channels,
+                                      const int32_t *starts, const float *initial, const float *grad_final,
+                                      devscan_gate kind, uint16_t *grad_x, size_t grad_x_row_stride, size_t grad_x_stride,
+                                      void *grad_gate, size_t grad_gate_row_stride, size_t grad_gate_stride,
+                                      float *grad_initial, cudaStream_t stream)
+{
+    GatedBackwardCall call = {};
+    call.rows.starts = starts;
+    call.grad = {const_cast<uint16_t *>(grad), grad_row_stride, grad_stride};
+    call.x = {const_cast<uint16_t *>(x), x_row_stride, x_stride};
+    call.gate = {const_cast<void *>(gate), gate_row_stride, gate_stride};
+    call.y = {const_cast<uint16_t *>(y), y_row_stride, y_stride};
+    call.grad_x = {grad_x, grad_x_row_stride, grad_x_stride};
+    call.grad_gate = {grad_gate, grad_gate_row_stride, grad_gate_stride};
+    call.initial = const_cast<float *>(initial), call.grad_final = grad_final, call.grad_initial = grad_initial;
+    return gated_backward_common(launch_gated_backward_f16, 2, call, gate_f32, rows, tokens, channels, kind, stream);
+}
+
+devscan_status gated_scan_bf16(const uint16_t *x, size_t x_row_stride, size_t x_stride, const void *gate,
+                             size_t gate_row_stride, size_t gate_stride, int gate_f32, size_t rows, size_t tokens,
+                             size_t channels, const int32_t *starts, const float *initial, const int32_t *slots,
+                             size_t pool, devscan_gate kind, uint16_t *out, size_t out_row_stride, size_t out_stride,
+                             float *final, cudaStream_t stream)
+{
+    GatedScanCall call = {};
+    call.rows.starts = starts, call.rows.slots = slots;
+    call.x = {const_cast<uint16_t *>(x), x_row_stride, x_stride};
+    call.gate = {const_cast<void *>(gate), gate_row_stride, gate_stride};
+    call.out = {out, out_row_stride, out_stride};
+    call.initial = const_cast<float *>(initial), call.final = final;
+    return gated_scan_common(launch_gated_scan_bf16, 2, call, gate_f32, rows, tokens, channels, pool, kind, stream);
+}
+
+devscan_status gated_scan_backward_bf16(const uint16_t *grad, size_t grad_row_stride, size_t grad_stride, const uint16_t *x,
+                                      size_t x_row_stride, size_t x_stride, const void *gate, size_t gate_row_stride,
+                                      size_t gate_stride, int gate_f32, const uint16_t *y, size_t y_row_stride,
+                                      size_t y_stride, size_t rows, size_t tokens, size_t channels,
+                                      const int32_t *starts, const float *initial, const float *grad_final,
+                                      devscan_gate kind, uint16_t *grad_x, size_t grad_x_row_stride, size_t grad_x_stride,
+                                      void *grad_gate, size_t grad_gate_row_stride, size_t grad_gate_stride,
+                                      float *grad_initial, cudaStream_t stream)
+{
+    GatedBackwardCall call = {};
+    call.rows.starts = starts;
+    call.grad = {const_cast<uint16_t *>(grad), grad_row_stride, grad_stride};
+    call.x = {const_cast<uint16_t *>(x), x_row_stride, x_stride};
+    call.gate = {const_cast<void *>(gate), gate_row_stride, gate_stride};
+    call.y = {const_cast<uint16_t *>(y), y_row_stride, y_stride};
+    call.grad_x = {grad_x, grad_x_row_stride, grad_x_stride};
+    call.grad_gate = {grad_gate, grad_gate_row_stride, grad_gate_stride};
+    call.initial = const_cast<float *>(initial), call.grad_final = grad_final, call.grad_initial = grad_initial;
+    return gated_backward_common(launch_gated_backward_bf16, 2, call, gate_f32, rows, tokens, channels, kind, stream);
+}
+
+devscan_status expert_sort_i32(const int32_t *ids, size_t tokens, size_t choices, size_t experts, size_t align,
+                              size_t rows, int32_t *starts, int32_t *counts, int32_t *order, int32_t *places,
+                              cudaStream_t stream)
+{
+    return expert_sort_common(ids, sizeof(int32_t), tokens, choices, experts, align, rows, starts, counts, order, places,
+                              stream);
+}
+
+devscan_status expert_sort_i64(const int64_t *ids, size_t tokens, size_t choices, size_t experts, size_t align,
+                              size_t rows, int32_t *starts, int32_t *counts, int32_t *order, int32_t *places,
+                              cudaStream_t stream)
+{
+    return expert_sort_common(ids, sizeof(int64_t), tokens, choices, experts, align, rows, starts, counts, order, places,
+                              stream);
+}
+
+devscan_status expert_dispatch(const void *x, size_t x_stride, size_t row_bytes, size_t tokens, size_t choices,
+                               const int32_t *places, size_t rows, const int32_t *order, void *out, size_t out_stride,
+                               cudaStream_t stream)
+{
+    if (!expert_sizes(tokens, choices, rows, row_bytes)) return DEVSCAN_ERR_INVALID;
+    if ((tokens > 1 && x_stride < row_bytes) || (rows > 1 && out_stride < row_bytes)) return DEVSCAN_ERR_INVALID;
+    if (rows == 0) return DEVSCAN_OK;
+    if (out == nullptr || (tokens > 0 && (x == nullptr || places == nullptr))) return DEVSCAN_ERR_INVALID;
+    if (misaligned(places, 4) || misaligned(order, 4)) return DEVSCAN_ERR_INVALID;
+    size_t x_bytes = 0, out_bytes = 0;
+    if (!matrix_bytes(tokens, x_stride, row_bytes, 1, &x_bytes) || !matrix_bytes(rows, out_stride, row_bytes, 1, &out_bytes))
+        return DEVSCAN_ERR_INVALID;
+    const Span written[] = {{out, out_bytes}};
+    const Span read[] = {{x, x_bytes}, {places, tokens * choices * 4}, {order, rows * 4}};
+    if (written_overlap(written, read)) return DEVSCAN_ERR_INVALID;
+    return from_cuda(launch_expert_dispatch({x, x_stride, row_bytes, static_cast<unsigned>(tokens),
+                                             static_cast<unsigned>(rows), static_cast<int>(choices), places, order, out,
+                                             out_stride},
+                                            stream));
+}
+
+devscan_status expert_combine_f32(const float *y, size_t y_stride, size_t rows, size_t tokens, size_t choices,
+                                 size_t width, const int32_t *places, const float *weights, float *out,
+                                 size_t out_stride, cudaStream_t stream)
+{
+    return expert_combine_common(ValueType::F32, {y, y_stride, 0, 0, 0, 0, places, weights, out, out_stride}, rows, tokens,
+                                 choices, width, stream);
+}
+
+devscan_status expert_combine_backward_f32(const float *grad, size_t grad_stride, const float *y, size_t y_stride,
+                                          size_t rows, size_t tokens, size_t choices, size_t width,
+                                          const int32_t *places, const float *weights, const int32_t *order,
+                                          float *grad_y, size_t grad_y_stride, float *grad_weights, cudaStream_t stream)
+{
+    return expert_combine_backward_common(ValueType::F32,
+                                          {grad, grad_stride, y, y_stride, 0, 0, 0, 0, places, order, weights, grad_y,
+                                           grad_y_stride, grad_weights},
+                                          rows, tokens, choices, width, stream);
+}
+
+devscan_status expert_combine_f16(const uint16_t *y, size_t y_stride, size_t rows, size_t tokens, size_t choices,
+                                 size_t width, const int32_t *places, const float *weights, uint16_t *out,
+                                 size_t out_stride, cudaStream_t stream)
+{
+    return expert_combine_common(ValueType::F16, {y, y_stride, 0, 0, 0, 0, places, weights, out, out_stride}, rows, tokens,
+                                 choices, width, stream);
+}
+
+devscan_status expert_combine_backward_f16(const uint16_t *grad, size_t grad_stride, const uint16_t *y, size_t y_stride,
+                                          size_t rows, size_t tokens, size_t choices, size_t width,
+                                          const int32_t *places, const float *weights, const int32_t *order,
+                                          uint16_t *grad_y, size_t grad_y_stride, float *grad_weights, cudaStream_t stream)
+{
+    return expert_combine_backward_common(ValueType::F16,
+                                          {grad, grad_stride, y, y_stride, 0, 0, 0, 0, places, order, weights, grad_y,
+                                           grad_y_stride, grad_weights},
+                                          rows, tokens, choices, width, stream);
+}
+
+devscan_status expert_combine_bf16(const uint16_t *y, size_t y_stride, size_t rows, size_t tokens, size_t choices,
+                                 size_t width, const int32_t *places, const float *weights, uint16_t *out,
+                                 size_t out_stride, cudaStream_t stream)
+{
+    return expert_combine_common(ValueType::BF16, {y, y_stride, 0, 0, 0, 0, places, weights, out, out_stride}, rows, tokens,
+                                 choices, width, stream);
+}
+
+devscan_status expert_combine_backward_bf16(const uint16_t *grad, size_t grad_stride, const uint16_t *y, size_t y_stride,
+                                          size_t rows, size_t tokens, size_t choices, size_t width,
+                                          const int32_t *places, const float *weights, const int32_t *order,
+                                          uint16_t *grad_y, size_t grad_y_stride, float *grad_weights, cudaStream_t stream)
+{
+    return expert_combine_backward_common(ValueType::BF16,
+                                          {grad, grad_stride, y, y_stride, 0, 0, 0, 0, places, order, weights, grad_y,
+                                           grad_y_stride, grad_weights},
+                                          rows, tokens, choices, width, stream);
+}
+
+devscan_status grad_norm(const devscan_tensor *tensors, size_t count, float *norm, void *work, size_t work_bytes,
+                         cudaStream_t stream)
+{
+    return norm_common(tensors, count, false, 0.0f, norm, work, work_bytes, stream);
+}
+
+devscan_status clip_grad_norm(const devscan_tensor *tensors, size_t count, float max_norm, float *norm, void *work,
+                              size_t work_bytes, cudaStream_t stream)
+{
+    return norm_common(tensors, count, true, max_norm, norm, work, work_bytes, stream);
 }
 
 devscan_status devscan_device_status(cudaStream_t stream)

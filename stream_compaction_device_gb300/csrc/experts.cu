@@ -1,0 +1,418 @@
+// Tokens sorted by expert and back (sm_103a): every token goes to `choices`
+// experts, and a pair (token, choice) to a place among its expert's rows.
+//
+// sort     : the stable counting sort of the pairs by expert -- lpnh.cn
+//            "并行扫描" section 4.2's counts per digit, a prefix over them and a
+//            scatter, with the expert as the only digit.  A segment of rows per
+//            expert, each rounded up to a multiple of `align`.
+// dispatch : xs[place(t, k)] = x[t]
+// combine  : y[t] = sum over k of w(t, k) ys[place(t, k)]
+// and the gradient of combine: dys[place] = w dy[t], dw = <dy[t], ys[place]>.
+// The gradient of dispatch is combine without weights.
+#include "cluster.cuh"
+#include "convert.cuh"
+#include "grid_sync.cuh"
+#include "launch.h"
+
+namespace devscan {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Sort.  One cluster of up to eight blocks: its blocks take equal runs of the
+// pairs, and their warps equal runs of those, so that the order of warps is
+// the order of pairs.  Every warp counts its pairs per expert in shared memory;
+// a column of counts is scanned over the warps by one thread, over the blocks
+// through distributed shared memory, and over the experts by the block.  Then
+// each warp goes through its pairs again: lanes with the same expert find each
+// other (match), their ranks are counted from the mask, and the warp's counter
+// moves on.  No scratch, no global atomics, one launch.
+// ---------------------------------------------------------------------------
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortMostBlocks = 8;
+constexpr size_t kSortPairsPerBlock = 4096;   // from where another block is worth it
+
+template <typename Id>
+__global__ void __launch_bounds__(kSortThreads, 1) expert_sort_kernel(const __grid_constant__ ExpertSortCall p)
+{
+    extern __shared__ unsigned s_counts[];            // [warp][expert], then the experts' totals and bases
+    unsigned *const s_total = s_counts + kSortWarps * p.experts;
+    unsigned *const s_base = s_total + p.experts;     // first row of a segment
+    unsigned *const s_filled = s_base + p.experts;    // behind the last row with a pair
+    __shared__ unsigned s_warp[kSortWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const unsigned rank = cluster_rank(), blocks = gridDim.x;
+    const Id *ids = static_cast<const Id *>(p.ids);
+    const unsigned experts = static_cast<unsigned>(p.experts);
+    const unsigned each = (p.pairs + blocks * kSortThreads - 1) / (blocks * kSortThreads) * 32;   // pairs of a warp
+    const unsigned begin = (rank * kSortWarps + warp) * each;
+    const unsigned end = begin < p.pairs ? (p.pairs - begin < each ? p.pairs : begin + each) : begin;
+    unsigned *const mine = s_counts + warp * experts;
+    auto expert_of = [&](unsigned i) {   // `experts` where there is none
+        if (i >= end) return experts;
+        const long long id = static_cast<long long>(ids[i]);
+        return id >= 0 && id < static_cast<long long>(experts) ? static_cast<unsigned>(id) : experts;
+    };
+
+    for (unsigned e = lane; e < experts; e += 32) mine[e] = 0;
+    __syncwarp();
+    for (unsigned i = begin + lane; i < end; i += 32) {
+        const unsigned e = expert_of(i);
+        if (e < experts) atomicAdd(&mine[e], 1u);
+    }
+    __syncthreads();
+    unsigned total = 0;
+    const bool column = static_cast<unsigned>(tid) < experts;
+    if (column) {
+#pragma unroll 8
+        for (int w = 0; w < kSortWarps; ++w) {
+            const unsigned c = s_counts[w * experts + tid];
+            s_counts[w * experts + tid] = total;
+            total += c;
+        }
+        s_total[tid] = total;
+    }
+    unsigned before = 0, all = total;
+    if (blocks > 1) {
+        cluster_sync();   // the totals are there
+        if (column) {
+            all = 0;
+            for (unsigned q = 0; q < blocks; ++q) {
+                const unsigned c = ld_cluster(cluster_addr(&s_total[tid], q));
+                before += q < rank ? c : 0u;
+                all += c;
+            }
+        }
+    }
+    // the segments' first rows: a scan of the rounded counts over the experts
+    const unsigned room = (all + p.align - 1) / p.align * p.align;
+    unsigned upto = room;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const unsigned u = __shfl_up_sync(kFullMask, upto, d);
+        if (lane >= d) upto += u;
+    }
+    if (lane == 31) s_warp[warp] = upto;
+    __syncthreads();
+    unsigned wt = s_warp[lane], wi = wt;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const unsigned u = __shfl_up_sync(kFullMask, wi, d);
+        if (lane >= d) wi += u;
+    }
+    const unsigned used = __shfl_sync(kFullMask, wi, 31);
+    const unsigned base = __shfl_sync(kFullMask, wi - wt, warp) + upto - room;
+    if (column) {
+        s_base[tid] = base;
+        s_filled[tid] = base + all;
+#pragma unroll 8
+        for (int w = 0; w < kSortWarps; ++w) s_counts[w * experts + tid] += base + before;
+        if (rank == 0) p.starts[tid] = static_cast<int32_t>(base), p.counts[tid] = static_cast<int32_t>(all);
+    }
+    if (rank == 0 && tid == 0) p.starts[experts] = static_cast<int32_t>(used);
+    __syncthreads();
+
+    for (unsigned i0 = begin; i0 < end; i0 += 32) {
+        const unsigned i = i0 + lane, e = expert_of(i);
+        const unsigned same = __match_any_sync(kFullMask, e);
+        const unsigned ahead = __popc(same & ((1u << lane) - 1u));
+        const unsigned place = e < experts ? mine[e] + ahead : p.rows;
+        __syncwarp();
+        if (e < experts && ahead == 0) mine[e] += __popc(same);
+        __syncwarp();
+        if (i < end) p.places[i] = place < p.rows ? static_cast<int32_t>(place) : -1;
+        if (place < p.rows) p.order[place] = static_cast<int32_t>(i);
+    }
+    // rows without a pair: up to the end of their segment, and behind the last one
+    for (unsigned e = rank * kSortWarps + warp; e < experts; e += blocks * kSortWarps) {
+        unsigned to = e + 1 < experts ? s_base[e + 1] : used;
+        to = to < p.rows ? to : p.rows;
+        for (unsigned r = s_filled[e] + lane; r < to; r += 32) p.order[r] = kOrderPadding;
+    }
+    for (unsigned r = used + rank * kSortThreads + tid; r < p.rows; r += blocks * kSortThreads) p.order[r] = kOrderBehind;
+    if (blocks > 1) cluster_sync();   // nobody leaves while its totals may be read
+}
+
+// ---------------------------------------------------------------------------
+// Dispatch.  A warp takes a token's run of 32 * U vectors, reads it once and
+// writes it to each of the token's places, so that x is read once and not once
+// per choice; the warps behind those look through `order`, 32 rows each, for
+// rows of padding and clear them.  Bound by memory.
+// ---------------------------------------------------------------------------
+constexpr int kMoveWarps = 8;
+
+// The rows among order[r0 .. r0 + 32) that are padding, a bit each.
+__device__ __forceinline__ unsigned padding_rows(const int32_t *order, unsigned r0, unsigned rows, int lane)
+{
+    const unsigned r = r0 + lane;
+    return __ballot_sync(kFullMask, r < rows && order[r] == kOrderPadding);
+}
+
+template <typename V, int U>
+__global__ void __launch_bounds__(32 * kMoveWarps) expert_dispatch_kernel(const __grid_constant__ ExpertMoveCall p,
+                                                                          unsigned vectors, unsigned runs)
+{
+    const int lane = threadIdx.x & 31;
+    const size_t item = static_cast<size_t>(blockIdx.x) * kMoveWarps + (threadIdx.x >> 5);
+    const size_t moves = static_cast<size_t>(p.tokens) * runs;
+    if (item < moves) {
+        const unsigned t = static_cast<unsigned>(item / runs), run = static_cast<unsigned>(item % runs);
+        const V *from = reinterpret_cast<const V *>(static_cast<const char *>(p.from) + t * p.from_stride);
+        const unsigned v0 = run * (32 * U) + lane;
+        V v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (v0 + 32 * u < vectors) v[u] = __ldcs(from + v0 + 32 * u);
+        const int32_t *places = p.places + static_cast<size_t>(t) * p.choices;
+        for (int k0 = 0; k0 < p.choices; k0 += 32) {
+            const int here = k0 + lane < p.choices ? places[k0 + lane] : -1;
+            const int many = min(32, p.choices - k0);
+            for (int k = 0; k < many; ++k) {
+                const unsigned place = static_cast<unsigned>(__shfl_sync(kFullMask, here, k));
+                if (place >= p.rows) continue;
+                V *to = reinterpret_cast<V *>(static_cast<char *>(p.to) + place * p.to_stride);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (v0 + 32 * u < vectors) __stcs(to + v0 + 32 * u, v[u]);
+            }
+        }
+        return;
+    }
+    const size_t r0 = (item - moves) * 32;
+    if (p.order == nullptr || r0 >= p.rows) return;
+    for (unsigned found = padding_rows(p.order, static_cast<unsigned>(r0), p.rows, lane); found != 0; found &= found - 1) {
+        V *to = reinterpret_cast<V *>(static_cast<char *>(p.to) + (r0 + __ffs(found) - 1) * p.to_stride);
+        for (unsigned i = lane; i < vectors; i += 32) to[i] = V{};
+    }
+}
+
+template <typename V, int U>
+cudaError_t dispatch(const ExpertMoveCall &call, cudaStream_t s)
+{
+    const unsigned vectors = static_cast<unsigned>(call.row_bytes / sizeof(V));
+    const unsigned runs = (vectors + 32 * U - 1) / (32 * U);
+    const size_t items = static_cast<size_t>(call.tokens) * runs + (call.order != nullptr ? (call.rows + 31u) / 32 : 0);
+    if (items == 0) return cudaSuccess;
+    const size_t blocks = (items + kMoveWarps - 1) / kMoveWarps;
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    expert_dispatch_kernel<V, U><<<static_cast<unsigned>(blocks), 32 * kMoveWarps, 0, s>>>(call, vectors, runs);
+    return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Combine.  A warp takes 32 * V columns of a token and adds the rows of its
+// choices in their order, eight loads in flight, in fp32; one rounding.
+// ---------------------------------------------------------------------------
+constexpr int kAtOnce = 8;   // choices whose rows are in flight together
+
+template <typename T, int V>
+__global__ void __launch_bounds__(32 * kMoveWarps) expert_combine_kernel(const __grid_constant__ ExpertCombineCall p,
+                                                                         unsigned runs)
+{
+    using R = typename Raw<T, V>::type;
+    const int lane = threadIdx.x & 31;
+    const size_t item = static_cast<size_t>(blockIdx.x) * kMoveWarps + (threadIdx.x >> 5);
+    if (item >= static_cast<size_t>(p.tokens) * runs) return;
+    const unsigned t = static_cast<unsigned>(item / runs), run = static_cast<unsigned>(item % runs);
+    const unsigned c = (run * 32 + lane) * V;
+    const bool live = c < p.width;   // a whole number of lanes is
+    const T *y = static_cast<const T *>(p.y) + c;
+    const size_t pair0 = static_cast<size_t>(t) * p.choices;
+    float sum[V] = {};
+    for (int k0 = 0; k0 < p.choices; k0 += kAtOnce) {
+        const bool have = lane < kAtOnce && k0 + lane < p.choices;
+        const int place_here = have ? p.places[pair0 + k0 + lane] : -1;
+        const float weight_here = have && p.weights != nullptr ? p.weights[pair0 + k0 + lane] : 1.0f;
+        R r[kAtOnce];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            const unsigned place = static_cast<unsigned>(__shfl_sync(kFullMask, place_here, j));
+            if (place < p.rows && live) r[j] = *reinterpret_cast<const R *>(y + place * p.y_stride);
+        }
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            const unsigned place = static_cast<unsigned>(__shfl_sync(kFullMask, place_here, j));
+            const float w = __shfl_sync(kFullMask, weight_here, j);
+            if (place >= p.rows || !live) continue;
+            float v[V];
+            unpack<T, V>(r[j], v);
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum[i] = fmaf(w, v[i], sum[i]);
+        }
+    }
+    if (live) *reinterpret_cast<R *>(static_cast<T *>(p.out) + t * p.out_stride + c) = pack<T, V>(sum);
+}
+
+// ---------------------------------------------------------------------------
+// The gradient of combine.  A block of four warps takes a token: its row of
+// gradients is read once per eight choices, each choice's row of y gives a
+// piece of the weight's gradient, and the row's gradient is written.  The
+// pieces are added lane, warp, block, in a fixed order.
+// ---------------------------------------------------------------------------
+constexpr int kBackWarps = 4;
+
+template <typename T, int V>
+__global__ void __launch_bounds__(32 * kBackWarps) expert_combine_backward_kernel(
+    const __grid_constant__ ExpertCombineBackwardCall p)
+{
+    using R = typename Raw<T, V>::type;
+    __shared__ float s_sum[kBackWarps][kAtOnce];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (blockIdx.x >= p.tokens) {   // rows of padding
+        const size_t r0 = (static_cast<size_t>(blockIdx.x - p.tokens) * kBackWarps + warp) * 32;
+        if (r0 >= p.rows) return;
+        for (unsigned found = padding_rows(p.order, static_cast<unsigned>(r0), p.rows, lane); found != 0;
+             found &= found - 1) {
+            T *to = static_cast<T *>(p.grad_y) + (r0 + __ffs(found) - 1) * p.grad_y_stride;
+            for (unsigned c = lane * V; c < p.width; c += 32 * V) *reinterpret_cast<R *>(to + c) = R{};
+        }
+        return;
+    }
+    const unsigned t = blockIdx.x;
+    const T *grad = static_cast<const T *>(p.grad) + t * p.grad_stride;
+    const size_t pair0 = static_cast<size_t>(t) * p.choices;
+    for (int k0 = 0; k0 < p.choices; k0 += kAtOnce) {
+        const bool have = lane < kAtOnce && k0 + lane < p.choices;
+        const int place_here = have ? p.places[pair0 + k0 + lane] : -1;
+        const float weight_here = have && p.weights != nullptr ? p.weights[pair0 + k0 + lane] : 1.0f;
+        unsigned place[kAtOnce];
+        float weight[kAtOnce], sum[kAtOnce] = {};
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            place[j] = static_cast<unsigned>(__shfl_sync(kFullMask, place_here, j));
+            weight[j] = __shfl_sync(kFullMask, weight_here, j);
+        }
+        for (unsigned c = threadIdx.x * V; c < p.width; c += 32 * kBackWarps * V) {
+            float g[V];
+            R r[kAtOnce];
+            if (p.grad_weights != nullptr)
+#pragma unroll
+                for (int j = 0; j < kAtOnce; ++j)
+                    if (place[j] < p.rows)
+                        r[j] = __ldcs(reinterpret_cast<const R *>(static_cast<const T *>(p.y) + place[j] * p.y_stride + c));
+            unpack<T, V>(*reinterpret_cast<const R *>(grad + c), g);
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+                if (place[j] >= p.rows) continue;
+                float v[V];
+                if (p.grad_weights != nullptr) {
+                    unpack<T, V>(r[j], v);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) sum[j] = fmaf(g[i], v[i], sum[j]);
+                }
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[i] = weight[j] * g[i];
+                __stcs(reinterpret_cast<R *>(static_cast<T *>(p.grad_y) + place[j] * p.grad_y_stride + c), pack<T, V>(v));
+            }
+        }
+        if (p.grad_weights == nullptr) continue;
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j)
+#pragma unroll
+            for (int d = 16; d >= 1; d >>= 1) sum[j] += __shfl_xor_sync(kFullMask, sum[j], d);
+        __syncthreads();   // the sums before have been read
+        if (lane == 0)
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) s_sum[warp][j] = sum[j];
+        __syncthreads();
+        if (warp == 0 && have) {
+            float all = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kBackWarps; ++w) all += s_sum[w][lane];
+            p.grad_weights[pair0 + k0 + lane] = static_cast<unsigned>(place_here) < p.rows ? all : 0.0f;
+        }
+    }
+}
+
+bool wide_rows(const void *p, size_t stride, size_t width, size_t size)
+{
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * size % 16 == 0 && width * size % 16 == 0;
+}
+
+template <typename T, int V>
+cudaError_t combine(const ExpertCombineCall &call, cudaStream_t s)
+{
+    const unsigned runs = (call.width + 32 * V - 1) / (32 * V);
+    const size_t blocks = (static_cast<size_t>(call.tokens) * runs + kMoveWarps - 1) / kMoveWarps;
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    expert_combine_kernel<T, V><<<static_cast<unsigned>(blocks), 32 * kMoveWarps, 0, s>>>(call, runs);
+    return cudaGetLastError();
+}
+template <typename T>
+cudaError_t combine_any(const ExpertCombineCall &call, cudaStream_t s)
+{
+    constexpr int V = 16 / sizeof(T);
+    if (wide_rows(call.y, call.y_stride, call.width, sizeof(T)) && wide_rows(call.out, call.out_stride, call.width, sizeof(T)))
+        return combine<T, V>(call, s);
+    return combine<T, 1>(call, s);
+}
+
+template <typename T, int V>
+cudaError_t combine_backward(const ExpertCombineBackwardCall &call, cudaStream_t s)
+{
+    const size_t blocks = static_cast<size_t>(call.tokens) +
+                          (call.order != nullptr ? (call.rows + 32u * kBackWarps - 1) / (32 * kBackWarps) : 0);
+    if (blocks == 0) return cudaSuccess;
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    expert_combine_backward_kernel<T, V><<<static_cast<unsigned>(blocks), 32 * kBackWarps, 0, s>>>(call);
+    return cudaGetLastError();
+}
+template <typename T>
+cudaError_t combine_backward_any(const ExpertCombineBackwardCall &call, cudaStream_t s)
+{
+    constexpr int V = 16 / sizeof(T);
+    const size_t w = call.width;
+    if (wide_rows(call.grad, call.grad_stride, w, sizeof(T)) && wide_rows(call.y, call.y_stride, w, sizeof(T)) &&
+        wide_rows(call.grad_y, call.grad_y_stride, w, sizeof(T)))
+        return combine_backward<T, V>(call, s);
+    return combine_backward<T, 1>(call, s);
+}
+
+}  // namespace
+
+cudaError_t launch_expert_sort(const ExpertSortCall &call, bool wide_ids, cudaStream_t s)
+{
+    static std::atomic<unsigned long long> done[2];
+    const int smem = static_cast<int>((kSortWarps + 3) * static_cast<size_t>(call.experts) * sizeof(unsigned));
+    const int most = static_cast<int>((kSortWarps + 3) * static_cast<size_t>(kMostExperts) * sizeof(unsigned));
+    auto *kernel = wide_ids ? expert_sort_kernel<int64_t> : expert_sort_kernel<int32_t>;
+    const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), most, done[wide_ids]);
+    if (e != cudaSuccess) return e;
+    unsigned blocks = 1;
+    while (blocks < kSortMostBlocks && static_cast<size_t>(call.pairs) > blocks * kSortPairsPerBlock) blocks *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = blocks;   // one cluster spans the grid
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, call);
+}
+
+cudaError_t launch_expert_dispatch(const ExpertMoveCall &call, cudaStream_t s)
+{
+    const size_t all = reinterpret_cast<uintptr_t>(call.from) | reinterpret_cast<uintptr_t>(call.to) | call.row_bytes |
+                       call.from_stride | call.to_stride;
+    if (all % 16 == 0) return dispatch<uint4, 4>(call, s);
+    if (all % 4 == 0) return dispatch<unsigned, 4>(call, s);
+    if (all % 2 == 0) return dispatch<unsigned short, 4>(call, s);
+    return dispatch<unsigned char, 4>(call, s);
+}
+
+cudaError_t launch_expert_combine(ValueType type, const ExpertCombineCall &call, cudaStream_t s)
+{
+    if (type == ValueType::F32) return combine_any<float>(call, s);
+    return type == ValueType::F16 ? combine_any<__half>(call, s) : combine_any<__nv_bfloat16>(call, s);
+}
+
+cudaError_t launch_expert_combine_backward(ValueType type, const ExpertCombineBackwardCall &call, cudaStream_t s)
+{
+    if (type == ValueType::F32) return combine_backward_any<float>(call, s);
+    return type == ValueType::F16 ? combine_backward_any<__half>(call, s) : combine_backward_any<__nv_bfloat16>(call, s);
+}
+
+}  // namespace devscan

@@ -193,4 +193,107 @@ cudaError_t launch_sample_f32(const SampleCall &call, const Workspace &ws, cudaS
 cudaError_t launch_sample_f16(const SampleCall &call, const Workspace &ws, cudaStream_t s);
 cudaError_t launch_sample_bf16(const SampleCall &call, const Workspace &ws, cudaStream_t s);
 
+// Gated recurrence.  The rows of tokens that all of a call's arrays share, and
+// how the launch splits them (groups of channels, spans of rows, blocks of a
+// cluster; set by the launch).
+constexpr int kGateDecay = 0, kGateLog = 1, kGateSigmoid = 2;
+struct GatedRows {
+    const int32_t *starts;   // packed rows; null: `tokens` in each
+    const int32_t *slots;    // of the rows in the states; null: their own index
+    int rows, channels, pool;
+    unsigned tokens;         // per row, or packed in all
+    unsigned groups, spans;
+    int blocks;
+    __host__ __device__ unsigned all() const { return starts != nullptr ? tokens : tokens * static_cast<unsigned>(rows); }
+};
+struct GatedArray {
+    void *data;                  // read only where the call reads it
+    size_t row_stride, stride;   // in elements, of rows and tokens
+};
+struct GatedScanCall {
+    GatedRows rows;
+    GatedArray x, gate, out;
+    float *initial, *final;      // initial is read only
+    int kind;
+};
+struct GatedBackwardCall {
+    GatedRows rows;
+    GatedArray grad, x, gate, y, grad_x, grad_gate;
+    float *initial;              // read only
+    const float *grad_final;
+    float *grad_initial;
+    int kind;
+};
+// `wide`: the gates and their gradients in fp32 beside 16-bit values.
+cudaError_t launch_gated_scan_f32(const GatedScanCall &call, bool wide, int sms, cudaStream_t s);
+cudaError_t launch_gated_scan_f16(const GatedScanCall &call, bool wide, int sms, cudaStream_t s);
+cudaError_t launch_gated_scan_bf16(const GatedScanCall &call, bool wide, int sms, cudaStream_t s);
+cudaError_t launch_gated_backward_f32(const GatedBackwardCall &call, bool wide, int sms, cudaStream_t s);
+cudaError_t launch_gated_backward_f16(const GatedBackwardCall &call, bool wide, int sms, cudaStream_t s);
+cudaError_t launch_gated_backward_bf16(const GatedBackwardCall &call, bool wide, int sms, cudaStream_t s);
+
+enum class ValueType : unsigned char { F32, F16, BF16 };
+
+// Tokens sorted by expert.  order[row]: the pair that lies there, or one of
+// the two below.
+constexpr int32_t kOrderPadding = -1;   // a row that rounds up a segment
+constexpr int32_t kOrderBehind = -2;    // behind the last segment
+constexpr int kMostExperts = 1024;
+struct ExpertSortCall {
+    const void *ids;
+    unsigned pairs, rows, align;
+    int experts;
+    int32_t *starts, *counts, *order, *places;
+};
+struct ExpertMoveCall {   // strides in bytes
+    const void *from;
+    size_t from_stride, row_bytes;
+    unsigned tokens, rows;
+    int choices;
+    const int32_t *places, *order;
+    void *to;
+    size_t to_stride;
+};
+struct ExpertCombineCall {   // strides in elements
+    const void *y;
+    size_t y_stride;
+    unsigned rows, tokens, width;
+    int choices;
+    const int32_t *places;
+    const float *weights;
+    void *out;
+    size_t out_stride;
+};
+struct ExpertCombineBackwardCall {
+    const void *grad;
+    size_t grad_stride;
+    const void *y;
+    size_t y_stride;
+    unsigned rows, tokens, width;
+    int choices;
+    const int32_t *places, *order;
+    const float *weights;
+    void *grad_y;
+    size_t grad_y_stride;
+    float *grad_weights;
+};
+cudaError_t launch_expert_sort(const ExpertSortCall &call, bool wide_ids, cudaStream_t s);
+cudaError_t launch_expert_dispatch(const ExpertMoveCall &call, cudaStream_t s);
+cudaError_t launch_expert_combine(ValueType type, const ExpertCombineCall &call, cudaStream_t s);
+cudaError_t launch_expert_combine_backward(ValueType type, const ExpertCombineBackwardCall &call, cudaStream_t s);
+
+// The 2-norm over tensors, and with `clip` their clipping.  work: kNormBlocks
+// doubles for every kNormTensors tensors or part of them.
+constexpr int kNormTensors = 512;
+constexpr unsigned kNormBlocks = 1024;
+constexpr double kClipEps = 1e-6;
+struct NormTensor {
+    const void *in;
+    void *out;
+    size_t n;
+    ValueType type;
+};
+cudaError_t launch_grad_norm(const NormTensor *tensors, size_t count, bool clip, float max_norm, float *norm, double *work,
+                             int sms, cudaStream_t s);
+
 }  // namespace devscan
