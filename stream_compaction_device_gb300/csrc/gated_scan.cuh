@@ -16,11 +16,14 @@
 // zero, so that an infinity or NaN of one row stays in that row.
 //
 // Layout.  Channels are contiguous, so lanes are channels (4 bytes of x each,
-// 128 bytes per warp and token) and nothing is shuffled; a warp takes kTokens
+// 128 bytes per warp and token) and nothing is shuffled; a warp takes
 // consecutive tokens, a block's eight warps lie behind each other.  Every
-// value is read once and kept in registers while the carry comes: the maps of
-// its tokens are folded, handed on, and then the tokens are run again from
-// the right h.  The next round's loads are issued before the exchange.
+// value is read once: a warp's tokens of the next rounds come into its own ring
+// of shared memory by asynchronous copies (no registers, no block barrier),
+// the maps of a round's tokens are folded, handed on, and then the tokens are
+// run again, from registers, from the right h.  Pairs of channels go through
+// the two-wide fp32 instructions.  Tokens at odd multiples of 2 bytes cannot
+// be copied that way; they are loaded into registers a round ahead.
 //
 // Split.  A cluster takes 32 lanes' channels of one span of whole rows.  Rows
 // are handed out first, since rows need no exchange; a row is spread over up to
@@ -31,6 +34,7 @@
 
 #include "cluster.cuh"
 #include "convert.cuh"
+#include "grid_sync.cuh"
 #include "launch.h"
 
 namespace devscan {
@@ -40,6 +44,50 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMostBlocks = 8;   // of a cluster (the portable size)
 constexpr int kForwardTokens = 16, kBackwardTokens = 8;   // per warp and round
+constexpr int kRingBytes = 96 << 10;                      // of a block, so that an SM holds two
+
+// ---------------------------------------------------------------------------
+// V neighbouring channels in fp32.  Two go through one instruction.
+// ---------------------------------------------------------------------------
+template <int V> struct alignas(4 * V) Lanes { float v[V]; };
+
+__device__ __forceinline__ unsigned long long bits(const Lanes<2> &a) { return __builtin_bit_cast(unsigned long long, a); }
+__device__ __forceinline__ Lanes<2> lanes(unsigned long long a) { return __builtin_bit_cast(Lanes<2>, a); }
+
+__device__ __forceinline__ Lanes<1> fma(Lanes<1> a, Lanes<1> b, Lanes<1> c) { return {fmaf(a.v[0], b.v[0], c.v[0])}; }
+__device__ __forceinline__ Lanes<1> operator*(Lanes<1> a, Lanes<1> b) { return {a.v[0] * b.v[0]}; }
+__device__ __forceinline__ Lanes<1> operator+(Lanes<1> a, Lanes<1> b) { return {a.v[0] + b.v[0]}; }
+__device__ __forceinline__ Lanes<2> fma(Lanes<2> a, Lanes<2> b, Lanes<2> c)
+{
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+    return lanes(d);
+}
+__device__ __forceinline__ Lanes<2> operator*(Lanes<2> a, Lanes<2> b)
+{
+    unsigned long long d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
+    return lanes(d);
+}
+__device__ __forceinline__ Lanes<2> operator+(Lanes<2> a, Lanes<2> b)
+{
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
+    return lanes(d);
+}
+template <int V> __device__ __forceinline__ Lanes<V> all(float x)
+{
+    Lanes<V> a;
+#pragma unroll
+    for (int k = 0; k < V; ++k) a.v[k] = x;
+    return a;
+}
+template <typename T, int V> __device__ __forceinline__ Lanes<V> lanes_of(typename Raw<T, V>::type raw)
+{
+    Lanes<V> a;
+    unpack<T, V>(raw, a.v);
+    return a;
+}
 
 // ---------------------------------------------------------------------------
 // Gates.  A decay next to 1 acts thousands of times, so its error must not
@@ -49,19 +97,29 @@ constexpr int kForwardTokens = 16, kBackwardTokens = 8;   // per warp and round
 // exp(g): near 0 as 1 + (its series to the fifth power, off by less than
 // g^6 / 720 < 2^-27); elsewhere the hardware's, off by 2^-22 of values that act
 // less than ten times.
-__device__ __forceinline__ float exp_decay(float g)
+template <int V> __device__ __forceinline__ Lanes<V> exp_decay(Lanes<V> g)
 {
-    const float s = g * fmaf(g, fmaf(g, fmaf(g, fmaf(g, 1.0f / 120, 1.0f / 24), 1.0f / 6), 0.5f), 1.0f);
-    return fabsf(g) < 0.125f ? 1.0f + s : __expf(g);
+    Lanes<V> s = fma(g, all<V>(1.0f / 120), all<V>(1.0f / 24));
+    s = fma(g, s, all<V>(1.0f / 6));
+    s = fma(g, s, all<V>(0.5f));
+    s = fma(g, s, all<V>(1.0f));
+    s = g * s;
+    s = s + all<V>(1.0f);
+#pragma unroll
+    for (int k = 0; k < V; ++k) s.v[k] = fabsf(g.v[k]) < 0.125f ? s.v[k] : __expf(g.v[k]);
+    return s;
 }
 
 // a = 1 / (1 + exp(-g)) and r = 1 - a, the smaller of the two from the quotient.
-__device__ __forceinline__ void sigmoid_decay(float g, float &a, float &r)
+template <int V> __device__ __forceinline__ void sigmoid_decay(Lanes<V> g, Lanes<V> &a, Lanes<V> &r)
 {
-    const float t = __expf(-fabsf(g));
-    const float small = __fdividef(t, 1.0f + t), large = 1.0f - small;
-    a = g >= 0.0f ? large : small;
-    r = g >= 0.0f ? small : large;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        const float t = __expf(-fabsf(g.v[k]));
+        const float small = __fdividef(t, 1.0f + t), large = 1.0f - small;
+        a.v[k] = g.v[k] >= 0.0f ? large : small;
+        r.v[k] = g.v[k] >= 0.0f ? small : large;
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -139,36 +197,99 @@ __device__ __forceinline__ float *state_of(const GatedRows &rows, float *states,
                : nullptr;
 }
 
-// The elements of consecutive tokens of a strided array: fn(i, element) for
-// i = 0 .. count - 1, beginning with token n and going on (DOWN: back).
-template <int COUNT, bool DOWN, typename Fn>
-__device__ __forceinline__ void walk(const GatedRows &rows, const GatedArray &array, unsigned n, int count, Fn &&fn)
+// ---------------------------------------------------------------------------
+// A warp's consecutive tokens n, n + 1, ... (DOWN: n, n - 1, ...).
+// ---------------------------------------------------------------------------
+struct Run {
+    unsigned n, row, t;   // the first token, its row of an array and its place there
+    int count;
+    bool whole;           // all there, and in one row of an array
+};
+template <int L, bool DOWN> __device__ __forceinline__ Run run_of(const GatedRows &rows, unsigned n, int count)
 {
-    const unsigned r = n / rows.tokens;
-    unsigned t = n - r * rows.tokens;
-    size_t at = r * array.row_stride + t * array.stride;
-    if (count == COUNT && (DOWN ? t + 1 >= COUNT : t + COUNT <= rows.tokens)) {   // all in one row: no turns
+    Run r;
+    r.n = n, r.count = count;
+    r.row = rows.starts == nullptr && rows.rows > 1 && count > 0 ? n / rows.tokens : 0u;
+    r.t = n - r.row * rows.tokens;
+    r.whole = count == L && (DOWN ? r.t + 1 >= L : r.t + L <= rows.tokens);
+    return r;
+}
+__device__ __forceinline__ size_t element(const GatedArray &array, unsigned row, unsigned t)
+{
+    return row * array.row_stride + t * array.stride;
+}
+
+// fn(i, element) for each of the run's tokens.
+template <int L, bool DOWN, typename Fn>
+__device__ __forceinline__ void walk(const GatedRows &rows, const GatedArray &array, const Run &r, Fn &&fn)
+{
+    size_t at = element(array, r.row, r.t);
+    if (r.whole) {
 #pragma unroll
-        for (int i = 0; i < COUNT; ++i) {
-            fn(i, at, DOWN ? t - i : t + i);
+        for (int i = 0; i < L; ++i) {
+            fn(i, at);
             at = DOWN ? at - array.stride : at + array.stride;
         }
         return;
     }
     const size_t turn = array.row_stride - (rows.tokens - 1) * array.stride;   // modulo 2^64
+    unsigned t = r.t;
 #pragma unroll
-    for (int i = 0; i < COUNT; ++i) {
-        if (i < count) fn(i, at, t);
+    for (int i = 0; i < L; ++i) {
+        if (i < r.count) fn(i, at);
+        const bool wrap = DOWN ? t == 0 : t + 1 == rows.tokens;
         if (DOWN) {
-            const bool wrap = t == 0;
             at -= wrap ? turn : array.stride;
             t = wrap ? rows.tokens - 1 : t - 1;
         } else {
-            const bool wrap = t + 1 == rows.tokens;
             at += wrap ? turn : array.stride;
             t = wrap ? 0 : t + 1;
         }
     }
+}
+
+// Asynchronous copy of up to W bytes (the rest become 0).
+template <int W> __device__ __forceinline__ void copy_async(uint32_t to, const void *from, int bytes)
+{
+    if constexpr (W == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Copies the warp's channels (`bytes` of them, at `base`) of the run's tokens,
+// BACK tokens before each, to `to`: 32 words of WORD bytes per token, W bytes
+// at a time.
+template <int L, bool DOWN, int BACK, int WORD, int W>
+__device__ __forceinline__ void copy_tokens(const GatedRows &rows, const GatedArray &array, const Run &r, const char *base,
+                                            size_t size, int bytes, uint32_t to, int lane)
+{
+    constexpr int kPieces = 32 * WORD / W;                        // of a token
+    constexpr int kAtOnce = kPieces < 32 ? 32 / kPieces : 1;      // tokens per instruction
+    constexpr int kParts = kPieces > 32 ? kPieces / 32 : 1;       // instructions per token
+#pragma unroll
+    for (int j = 0; j < L / kAtOnce; ++j)
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) {
+            const int piece = kPieces > 32 ? q * 32 + lane : lane % kPieces;
+            const int i = j * kAtOnce + (kPieces < 32 ? lane / kPieces : 0);
+            const int left = bytes - piece * W;
+            if (i >= r.count || left <= 0) continue;
+            unsigned row = r.row, t = r.t;
+            if (r.whole) {
+                t = DOWN ? t - i : t + i;
+            } else if (rows.starts == nullptr) {
+                const unsigned n = DOWN ? r.n - i : r.n + i;
+                row = n / rows.tokens, t = n - row * rows.tokens;
+            } else {
+                t = DOWN ? r.n - i : r.n + i;
+            }
+            if (BACK > 0 && t < BACK) continue;   // nothing before it: not looked at
+            copy_async<W>(to + i * (32 * WORD) + piece * W, base + element(array, row, t - BACK) * size + piece * W,
+                          left < W ? left : W);
+        }
 }
 
 // ---------------------------------------------------------------------------
@@ -176,90 +297,75 @@ __device__ __forceinline__ void walk(const GatedRows &rows, const GatedArray &ar
 // that comes into it.
 // ---------------------------------------------------------------------------
 template <int V> struct Exchange {
-    float a[2][kWarps][32 * V], h[2][kWarps][32 * V];             // this block's warps
-    float all_a[2][kMostBlocks][32 * V], all_h[2][kMostBlocks][32 * V];   // the cluster's blocks
-    unsigned cut[2][kWarps], all_cut[2][kMostBlocks];             // nonzero: the map forgets what comes in
+    Lanes<V> a[2][kWarps][32], h[2][kWarps][32];                       // this block's warps
+    Lanes<V> all_a[2][kMostBlocks][32], all_h[2][kMostBlocks][32];     // the cluster's blocks
+    unsigned cut[2][kWarps], all_cut[2][kMostBlocks];                  // nonzero: the map forgets what comes in
 };
+
+template <int V> __device__ __forceinline__ Lanes<V> follow(bool cut, Lanes<V> a, Lanes<V> in, Lanes<V> h)
+{
+    const Lanes<V> next = fma(a, in, h);
+#pragma unroll
+    for (int k = 0; k < V; ++k) h.v[k] = cut ? h.v[k] : next.v[k];
+    return h;
+}
+template <int V> __device__ __forceinline__ void st_lanes(uint32_t to, Lanes<V> a)
+{
+    if constexpr (V == 2)
+        asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(to), "l"(bits(a)) : "memory");
+    else
+        st_cluster(to, a.v[0]);
+}
 
 // Two buffers in turn are enough: a block writes a round's buffer after the
 // barrier of the round before, at which every reader of the round before that
 // has arrived.
 template <int V>
-__device__ __forceinline__ void exchange(Exchange<V> &x, int turn, int blocks, int rank, int warp, int lane,
-                                         const float (&a)[V], const float (&h)[V], bool cut, float (&carry)[V],
-                                         float (&in)[V])
+__device__ __forceinline__ Lanes<V> exchange(Exchange<V> &x, int turn, int blocks, int rank, int warp, int lane,
+                                             Lanes<V> a, Lanes<V> h, bool cut, Lanes<V> &carry)
 {
-#pragma unroll
-    for (int k = 0; k < V; ++k) x.a[turn][warp][lane * V + k] = a[k], x.h[turn][warp][lane * V + k] = h[k];
+    x.a[turn][warp][lane] = a, x.h[turn][warp][lane] = h;
     if (lane == 0) x.cut[turn][warp] = cut;
     __syncthreads();
+    Lanes<V> run = carry;
     if (blocks > 1) {
         if (warp == 0) {
-            float fa[V], fh[V];
+            Lanes<V> fa = all<V>(1.0f), fh = all<V>(0.0f);
             unsigned any = 0;
 #pragma unroll
-            for (int k = 0; k < V; ++k) fa[k] = 1.0f, fh[k] = 0.0f;
-#pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const bool c = x.cut[turn][w] != 0;
+                const unsigned c = x.cut[turn][w];
+                const Lanes<V> wa = x.a[turn][w][lane];
+                fh = follow(c != 0, wa, fh, x.h[turn][w][lane]);
+                fa = c != 0 ? wa : wa * fa;
                 any |= c;
-#pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    const float wa = x.a[turn][w][lane * V + k], wh = x.h[turn][w][lane * V + k];
-                    fh[k] = c ? wh : fmaf(wa, fh[k], wh);
-                    fa[k] = c ? wa : wa * fa[k];
-                }
             }
             for (int q = 0; q < blocks; ++q) {
-#pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    st_cluster(cluster_addr(&x.all_a[turn][rank][lane * V + k], q), fa[k]);
-                    st_cluster(cluster_addr(&x.all_h[turn][rank][lane * V + k], q), fh[k]);
-                }
+                st_lanes<V>(cluster_addr(&x.all_a[turn][rank][lane], q), fa);
+                st_lanes<V>(cluster_addr(&x.all_h[turn][rank][lane], q), fh);
                 if (lane == 0) st_cluster(cluster_addr(&x.all_cut[turn][rank], q), any);
             }
         }
         cluster_sync();
-        float run[V];
-#pragma unroll
-        for (int k = 0; k < V; ++k) run[k] = carry[k];
+        Lanes<V> into = run;
         for (int q = 0; q < blocks; ++q) {
-            const bool c = x.all_cut[turn][q] != 0;
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                if (q == rank) in[k] = run[k];
-                const float qh = x.all_h[turn][q][lane * V + k];
-                run[k] = c ? qh : fmaf(x.all_a[turn][q][lane * V + k], run[k], qh);
-            }
+            if (q == rank) into = run;
+            run = follow(x.all_cut[turn][q] != 0, x.all_a[turn][q][lane], run, x.all_h[turn][q][lane]);
         }
-#pragma unroll
-        for (int k = 0; k < V; ++k) carry[k] = run[k];
-    } else {
-#pragma unroll
-        for (int k = 0; k < V; ++k) in[k] = carry[k];
+        carry = run, run = into;
     }
     // the block's warps before this one; where the block is alone, all of them for the next round
-    float run[V];
-#pragma unroll
-    for (int k = 0; k < V; ++k) run[k] = in[k];
+    Lanes<V> in = run;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-        if (w >= warp && blocks > 1) break;
-        const bool c = x.cut[turn][w] != 0;
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-            if (w == warp) in[k] = run[k];
-            const float wh = x.h[turn][w][lane * V + k];
-            run[k] = c ? wh : fmaf(x.a[turn][w][lane * V + k], run[k], wh);
+        if (w == warp) {
+            in = run;
+            if (blocks > 1) break;
         }
+        run = follow(x.cut[turn][w] != 0, x.a[turn][w][lane], run, x.h[turn][w][lane]);
     }
-    if (blocks > 1) {
-#pragma unroll
-        for (int k = 0; k < V; ++k) in[k] = run[k];
-    } else {
-#pragma unroll
-        for (int k = 0; k < V; ++k) carry[k] = run[k];
-    }
+    if (blocks == 1) carry = run;
+    return in;
 }
 
 // What a block of the grid works on.
@@ -279,6 +385,48 @@ __device__ __forceinline__ Work work_of(const GatedRows &rows, int per_lane)
     return w;
 }
 
+// Rows that begin or end among a warp's tokens, a bit per token; lane i knows
+// token i's row.
+struct Edges {
+    unsigned first, last, outside;
+    int row;
+    __device__ int row_of(int i) const { return __shfl_sync(kFullMask, row, i); }
+};
+
+// What a warp remembers of the row that it was in last, so that it looks for
+// rows only where there may be edges.
+struct InRow {
+    unsigned begin = 1, end = 0;
+};
+
+template <int L, bool DOWN>
+__device__ __forceinline__ Edges edges_of(const GatedRows &rows, const Run &r, int lane, InRow &in)
+{
+    Edges e = {0, 0, 0, 0};
+    const unsigned low = DOWN ? r.n - (L - 1) : r.n;   // where count == L
+    if (rows.starts == nullptr) {
+        if (r.whole && (DOWN ? r.t + 1 > L && r.t + 1 < rows.tokens : r.t > 0 && r.t + L < rows.tokens)) return e;
+    } else if (r.count == L && low > in.begin && low + L < in.end) {
+        return e;
+    }
+    const bool mine = lane < r.count;
+    TokenPlace p = {0, true, false, false};
+    if (mine) p = place_of(rows, DOWN ? r.n - lane : r.n + lane);
+    e.first = __ballot_sync(kFullMask, mine && p.first);
+    e.last = __ballot_sync(kFullMask, mine && p.last);
+    e.outside = __ballot_sync(kFullMask, mine && !p.inside);
+    e.row = p.row;
+    if (rows.starts != nullptr && r.count > 0) {
+        const bool some = __shfl_sync(kFullMask, p.inside, r.count - 1);   // the row that goes on
+        const int row = __shfl_sync(kFullMask, p.row, r.count - 1);
+        if (some) {
+            in.begin = static_cast<unsigned>(__ldg(rows.starts + row));
+            in.end = min(static_cast<unsigned>(__ldg(rows.starts + row + 1)), rows.all());
+        }
+    }
+    return e;
+}
+
 // Rows without tokens: what goes in comes out, 0 where nothing does.  fn(row)
 // is called by a warp for each.
 template <typename Fn>
@@ -293,21 +441,60 @@ __device__ __forceinline__ void empty_rows(const GatedRows &rows, const Work &w,
 }
 
 // ---------------------------------------------------------------------------
+// A warp's ring: stages of a round's tokens, array after array, 32 lanes' words
+// per token.  COPY: bytes of an asynchronous copy (16 or 4); 0: the round ahead
+// waits in registers, and there is one stage.
+// ---------------------------------------------------------------------------
+template <typename X, typename G, int V, int L, int VALUES, int COPY> struct Ring {
+    using RX = typename Raw<X, V>::type;
+    using RG = typename Raw<G, V>::type;
+    static constexpr int kX = static_cast<int>(sizeof(RX)), kG = static_cast<int>(sizeof(RG));
+    static constexpr int kPart = L * 32 * kX, kGates = VALUES * kPart, kStage = kGates + L * 32 * kG;   // bytes
+    static constexpr int kFit = kRingBytes / (kWarps * kStage), kStages = COPY == 0 ? 1 : kFit < 4 ? kFit : 4;
+    static constexpr int kBytes = kWarps * kStages * kStage;
+    static_assert(COPY == 0 || kStages >= 2, "a round is copied while another is read");
+    static __device__ __forceinline__ Lanes<V> value(const char *stage, int array, int i, int lane)
+    {
+        return lanes_of<X, V>(reinterpret_cast<const RX *>(stage + array * kPart)[i * 32 + lane]);
+    }
+    static __device__ __forceinline__ Lanes<V> gate(const char *stage, int i, int lane)
+    {
+        return lanes_of<G, V>(reinterpret_cast<const RG *>(stage + kGates)[i * 32 + lane]);
+    }
+};
+
+// ---------------------------------------------------------------------------
 // Forward.
 // ---------------------------------------------------------------------------
-template <typename X, typename G, int V>
+template <int KIND, int V> __device__ __forceinline__ void coefficients(Lanes<V> gate, Lanes<V> x, Lanes<V> &a, Lanes<V> &b)
+{
+    a = gate, b = x;
+    if constexpr (KIND == kGateLog) a = exp_decay(gate);
+    if constexpr (KIND == kGateSigmoid) {
+        Lanes<V> r;
+        sigmoid_decay(gate, a, r);
+        b = r * x;
+    }
+}
+
+template <typename X, typename G, int V, int KIND, int COPY>
 __global__ void __launch_bounds__(kThreads, 2) gated_scan_kernel(const __grid_constant__ GatedScanCall p)
 {
     constexpr int L = kForwardTokens;
-    using RX = typename Raw<X, V>::type;
-    using RG = typename Raw<G, V>::type;
+    using R = Ring<X, G, V, L, 1, COPY>;
+    using RX = typename R::RX;
+    using RG = typename R::RG;
+    extern __shared__ __align__(16) char s_ring[];
     __shared__ Exchange<V> s_x;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Work w = work_of(p.rows, V);
     const bool live = w.channel < p.rows.channels;   // a whole number of lanes is
-    const X *x = static_cast<const X *>(p.x.data) + w.channel;
-    const G *gate = static_cast<const G *>(p.gate.data) + w.channel;
+    const int first_channel = w.channel - lane * V;
+    const int wide = min(p.rows.channels - first_channel, 32 * V);   // channels of the warp
+    const X *x = static_cast<const X *>(p.x.data);
+    const G *gate = static_cast<const G *>(p.gate.data);
     X *out = static_cast<X *>(p.out.data) + w.channel;
+    char *const ring = s_ring + warp * R::kStages * R::kStage;
 
     if (p.final != nullptr)
         empty_rows(p.rows, w, [&](int r) {
@@ -319,101 +506,106 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_kernel(const __grid_co
 
     const unsigned round = static_cast<unsigned>(w.blocks * kWarps * L);
     const unsigned rounds = (w.end - w.begin + round - 1) / round;
-    RX rx[L];
-    RG rg[L];
-    int count = 0;
-    unsigned n = w.begin + static_cast<unsigned>((w.rank * kWarps + warp) * L);   // this warp's first token
-    auto load = [&]() {
-        count = n < w.end ? static_cast<int>(min(w.end - n, static_cast<unsigned>(L))) : 0;
-        if (!live || count == 0) return;
-        walk<L, false>(p.rows, p.x, n, count, [&](int i, size_t at, unsigned) {
-            rx[i] = *reinterpret_cast<const RX *>(x + at);
-        });
-        walk<L, false>(p.rows, p.gate, n, count, [&](int i, size_t at, unsigned) {
-            rg[i] = *reinterpret_cast<const RG *>(gate + at);
-        });
+    const unsigned start = w.begin + static_cast<unsigned>((w.rank * kWarps + warp) * L);
+    auto run_at = [&](unsigned step) {
+        const unsigned n = start + step * round;
+        const bool some = step < rounds && n < w.end;
+        return run_of<L, false>(p.rows, some ? n : w.begin, some ? static_cast<int>(min(w.end - n, static_cast<unsigned>(L))) : 0);
     };
-#pragma unroll
-    for (int i = 0; i < L; ++i) rx[i] = RX{}, rg[i] = RG{};
-    load();
-    if (w.blocks > 1) cluster_sync();   // every block is there before another writes to it
-    float carry[V] = {};
-    for (unsigned step = 0; step < rounds; ++step) {
-        float a[L][V], b[L][V];
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-            float xv[V], gv[V];
-            unpack<X, V>(rx[i], xv);
-            unpack<G, V>(rg[i], gv);
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                a[i][k] = gv[k], b[i][k] = xv[k];
-                if (p.kind == kGateLog) a[i][k] = exp_decay(gv[k]);
-                if (p.kind == kGateSigmoid) {
-                    float r;
-                    sigmoid_decay(gv[k], a[i][k], r);
-                    b[i][k] *= r;
-                }
-                if (i >= count) a[i][k] = 1.0f, b[i][k] = 0.0f;
+    constexpr int kKept = COPY > 0 ? 1 : L;
+    RX rx[kKept] = {};
+    RG rg[kKept] = {};
+    auto fetch = [&](unsigned step) {
+        const Run r = run_at(step);
+        if constexpr (COPY > 0) {
+            if (r.count > 0) {
+                const uint32_t to = smem_u32(ring + step % R::kStages * R::kStage);
+                copy_tokens<L, false, 0, R::kX, COPY>(p.rows, p.x, r, reinterpret_cast<const char *>(x + first_channel),
+                                                      sizeof(X), wide * static_cast<int>(sizeof(X)), to, lane);
+                copy_tokens<L, false, 0, R::kG, COPY>(p.rows, p.gate, r, reinterpret_cast<const char *>(gate + first_channel),
+                                                      sizeof(G), wide * static_cast<int>(sizeof(G)), to + R::kGates, lane);
             }
+            copies_commit();
+        } else if (live && r.count > 0) {
+            walk<L, false>(p.rows, p.x, r, [&](int i, size_t at) { rx[i % kKept] = *reinterpret_cast<const RX *>(x + w.channel + at); });
+            walk<L, false>(p.rows, p.gate, r, [&](int i, size_t at) { rg[i % kKept] = *reinterpret_cast<const RG *>(gate + w.channel + at); });
         }
-        // Rows that begin or end among these tokens, a bit per token.
-        TokenPlace place = {0, true, false, false};
-        const bool mine = lane < count;
-        if (mine) place = place_of(p.rows, n + lane);
-        const unsigned first = __ballot_sync(kFullMask, mine && place.first);
-        const unsigned last = __ballot_sync(kFullMask, mine && place.last);
-        const unsigned outside = __ballot_sync(kFullMask, mine && !place.inside);
-        const unsigned cut = first | outside;
-        if (cut != 0) {
+    };
+    for (unsigned step = 0; step == 0 || step + 1 < R::kStages; ++step) fetch(step);
+    if (w.blocks > 1) cluster_sync();   // every block is there before another writes to it
+    Lanes<V> carry = all<V>(0.0f);
+    InRow in_row;
+    for (unsigned step = 0; step < rounds; ++step) {
+        const Run r = run_at(step);
+        char *const stage = ring + step % R::kStages * R::kStage;
+        if constexpr (COPY > 0) {
+            fetch(step + R::kStages - 1);   // into the stage that the round before has read
+            copies_wait<R::kStages - 1>();
+            __syncwarp();
+        } else {
 #pragma unroll
             for (int i = 0; i < L; ++i) {
-                if ((first >> i) & 1u) {
-                    const float *from = state_of(p.rows, p.initial, __shfl_sync(kFullMask, place.row, i));
+                reinterpret_cast<RX *>(stage)[i * 32 + lane] = rx[i % kKept];
+                reinterpret_cast<RG *>(stage + R::kGates)[i * 32 + lane] = rg[i % kKept];
+            }
+            fetch(step + 1);
+        }
+        Lanes<V> a[L], b[L];
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+            coefficients<KIND, V>(R::gate(stage, i, lane), R::value(stage, 0, i, lane), a[i], b[i]);
+        __syncwarp();   // the stage has been read
+        const Edges e = edges_of<L, false>(p.rows, r, lane, in_row);
+        const unsigned cut = e.first | e.outside;
+        const bool plain = r.whole && (cut | e.last) == 0;
+        Lanes<V> fa = all<V>(1.0f), h = all<V>(0.0f);
+        if (plain) {
+#pragma unroll
+            for (int i = 0; i < L; ++i) h = fma(a[i], h, b[i]), fa = fa * a[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                if (i >= r.count) a[i] = all<V>(1.0f), b[i] = all<V>(0.0f);
+                if ((e.outside >> i) & 1u) b[i] = all<V>(0.0f);
+                if ((e.first >> i) & 1u) {
+                    const float *from = state_of(p.rows, p.initial, e.row_of(i));
                     if (from != nullptr && live)
 #pragma unroll
-                        for (int k = 0; k < V; ++k) b[i][k] = fmaf(a[i][k], from[w.channel + k], b[i][k]);
+                        for (int k = 0; k < V; ++k) b[i].v[k] = fmaf(a[i].v[k], from[w.channel + k], b[i].v[k]);
                 }
-                if ((outside >> i) & 1u)
-#pragma unroll
-                    for (int k = 0; k < V; ++k) b[i][k] = 0.0f;
+                const bool c = (cut >> i) & 1u;
+                h = follow(c, a[i], h, b[i]);
+                fa = c ? all<V>(0.0f) : fa * a[i];
             }
         }
-        float fa[V], h[V];
+        h = exchange<V>(s_x, step & 1, w.blocks, w.rank, warp, lane, fa, h, cut != 0, carry);
+        if (plain) {
+            if (live) {
+                X *to = out + element(p.out, r.row, r.t);
 #pragma unroll
-        for (int k = 0; k < V; ++k) fa[k] = 1.0f, h[k] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < L; ++i)
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                const bool c = (cut >> i) & 1u;
-                h[k] = c ? b[i][k] : fmaf(a[i][k], h[k], b[i][k]);
-                fa[k] = c ? 0.0f : fa[k] * a[i][k];
+                for (int i = 0; i < L; ++i) {
+                    h = fma(a[i], h, b[i]);
+                    *reinterpret_cast<RX *>(to) = pack<X, V>(h.v);
+                    to += p.out.stride;
+                }
             }
-        const unsigned here = n;
-        const int had = count;
-        n += round;
-        load();
-        exchange<V>(s_x, step & 1, w.blocks, w.rank, warp, lane, fa, h, cut != 0, carry, h);
+            continue;
+        }
 #pragma unroll
-        for (int i = 0; i < L; ++i)
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                h[k] = (cut >> i) & 1u ? b[i][k] : fmaf(a[i][k], h[k], b[i][k]);
-                b[i][k] = h[k];
-            }
-        if (live && had > 0)
-            walk<L, false>(p.rows, p.out, here, had, [&](int i, size_t at, unsigned) {
-                *reinterpret_cast<RX *>(out + at) = pack<X, V>(b[i]);
-            });
-        if (last != 0 && p.final != nullptr) {
+        for (int i = 0; i < L; ++i) {
+            h = follow((cut >> i) & 1u, a[i], h, b[i]);
+            b[i] = h;
+        }
+        if (live && r.count > 0)
+            walk<L, false>(p.rows, p.out, r, [&](int i, size_t at) { *reinterpret_cast<RX *>(out + at) = pack<X, V>(b[i].v); });
+        if (p.final != nullptr) {
 #pragma unroll
             for (int i = 0; i < L; ++i) {
-                if (((last >> i) & 1u) == 0) continue;
-                float *to = state_of(p.rows, p.final, __shfl_sync(kFullMask, place.row, i));
+                if (((e.last >> i) & 1u) == 0) continue;
+                float *to = state_of(p.rows, p.final, e.row_of(i));
                 if (to != nullptr && live)
 #pragma unroll
-                    for (int k = 0; k < V; ++k) to[w.channel + k] = b[i][k];
+                    for (int k = 0; k < V; ++k) to[w.channel + k] = b[i].v[k];
             }
         }
     }
@@ -426,24 +618,31 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_kernel(const __grid_co
 // which is the same recurrence from the last token to the first, and
 //   dx_t = w_t (sigmoid: r_t w_t),  da_t = w_t h_{t-1},  dinitial = f_first;
 //   da / dgate = 1, a, or a r (h_{t-1} - x_t in place of h_{t-1}).
-// h_{t-1} is what the forward call wrote, in its type.
+// h_{t-1} is what the forward call wrote, in its type.  It (and x) is taken
+// from the ring after the exchange, so that registers hold a, dh and r only.
 // ---------------------------------------------------------------------------
-template <typename X, typename G, int V, bool SIGMOID>
+template <typename X, typename G, int V, int KIND, int COPY>
 __global__ void __launch_bounds__(kThreads, 2) gated_scan_backward_kernel(const __grid_constant__ GatedBackwardCall p)
 {
     constexpr int L = kBackwardTokens;
-    using RX = typename Raw<X, V>::type;
-    using RG = typename Raw<G, V>::type;
+    constexpr bool SIGMOID = KIND == kGateSigmoid;
+    using R = Ring<X, G, V, L, SIGMOID ? 3 : 2, COPY>;   // grad, y, x
+    using RX = typename R::RX;
+    using RG = typename R::RG;
+    extern __shared__ __align__(16) char s_ring[];
     __shared__ Exchange<V> s_x;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Work w = work_of(p.rows, V);
     const bool live = w.channel < p.rows.channels;
-    const X *grad = static_cast<const X *>(p.grad.data) + w.channel;
-    const X *y = static_cast<const X *>(p.y.data) + w.channel;
-    const X *x = SIGMOID ? static_cast<const X *>(p.x.data) + w.channel : nullptr;
-    const G *gate = static_cast<const G *>(p.gate.data) + w.channel;
+    const int first_channel = w.channel - lane * V;
+    const int wide = min(p.rows.channels - first_channel, 32 * V);
+    const X *grad = static_cast<const X *>(p.grad.data);
+    const X *y = static_cast<const X *>(p.y.data);
+    const X *x = static_cast<const X *>(p.x.data);
+    const G *gate = static_cast<const G *>(p.gate.data);
     X *grad_x = static_cast<X *>(p.grad_x.data) + w.channel;
     G *grad_gate = static_cast<G *>(p.grad_gate.data) + w.channel;
+    char *const ring = s_ring + warp * R::kStages * R::kStage;
 
     if (p.grad_initial != nullptr)
         empty_rows(p.rows, w, [&](int r) {
@@ -454,167 +653,208 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_backward_kernel(const 
 
     const unsigned round = static_cast<unsigned>(w.blocks * kWarps * L);
     const unsigned tokens = w.end - w.begin, rounds = (tokens + round - 1) / round;
-    RX rd[L], ry[L], rx[SIGMOID ? L : 1];
-    RG rg[L];
-    int count = 0;
-    unsigned done = static_cast<unsigned>((w.rank * kWarps + warp) * L);   // tokens of the span behind this warp's
-    auto load = [&]() {
-        count = done < tokens ? static_cast<int>(min(tokens - done, static_cast<unsigned>(L))) : 0;
-        if (!live || count == 0) return;
-        const unsigned n = w.end - 1 - done;   // going back from here
-        walk<L, true>(p.rows, p.grad, n, count, [&](int i, size_t at, unsigned) {
-            rd[i] = *reinterpret_cast<const RX *>(grad + at);
-        });
-        walk<L, true>(p.rows, p.gate, n, count, [&](int i, size_t at, unsigned) {
-            rg[i] = *reinterpret_cast<const RG *>(gate + at);
-        });
-        walk<L, true>(p.rows, p.y, n, count, [&](int i, size_t at, unsigned t) {
-            if (t > 0) ry[i] = *reinterpret_cast<const RX *>(y + (at - p.y.stride));
-        });
-        if constexpr (SIGMOID)
-            walk<L, true>(p.rows, p.x, n, count, [&](int i, size_t at, unsigned) {
-                rx[i] = *reinterpret_cast<const RX *>(x + at);
-            });
+    const unsigned start = static_cast<unsigned>((w.rank * kWarps + warp) * L);   // tokens of the span behind this warp's
+    auto run_at = [&](unsigned step) {
+        const unsigned done = start + step * round;
+        const bool some = step < rounds && done < tokens;
+        return run_of<L, true>(p.rows, some ? w.end - 1 - done : w.begin,
+                               some ? static_cast<int>(min(tokens - done, static_cast<unsigned>(L))) : 0);
     };
-#pragma unroll
-    for (int i = 0; i < L; ++i) rd[i] = RX{}, ry[i] = RX{}, rx[SIGMOID ? i : 0] = RX{}, rg[i] = RG{};
-    load();
+    constexpr int kKept = COPY > 0 ? 1 : L;
+    RX rd[kKept] = {}, ry[kKept] = {}, rx[SIGMOID ? kKept : 1] = {};
+    RG rg[kKept] = {};
+    auto fetch = [&](unsigned step) {
+        const Run r = run_at(step);
+        if constexpr (COPY > 0) {
+            if (r.count > 0) {
+                constexpr int size = static_cast<int>(sizeof(X)), gate_size = static_cast<int>(sizeof(G));
+                const uint32_t to = smem_u32(ring + step % R::kStages * R::kStage);
+                copy_tokens<L, true, 0, R::kX, COPY>(p.rows, p.grad, r, reinterpret_cast<const char *>(grad + first_channel),
+                                                     size, wide * size, to, lane);
+                copy_tokens<L, true, 1, R::kX, COPY>(p.rows, p.y, r, reinterpret_cast<const char *>(y + first_channel),
+                                                     size, wide * size, to + R::kPart, lane);
+                if constexpr (SIGMOID)
+                    copy_tokens<L, true, 0, R::kX, COPY>(p.rows, p.x, r, reinterpret_cast<const char *>(x + first_channel),
+                                                         size, wide * size, to + 2 * R::kPart, lane);
+                copy_tokens<L, true, 0, R::kG, COPY>(p.rows, p.gate, r, reinterpret_cast<const char *>(gate + first_channel),
+                                                     gate_size, wide * gate_size, to + R::kGates, lane);
+            }
+            copies_commit();
+        } else if (live && r.count > 0) {
+            unsigned t = r.t;
+            walk<L, true>(p.rows, p.grad, r, [&](int i, size_t at) { rd[i % kKept] = *reinterpret_cast<const RX *>(grad + w.channel + at); });
+            walk<L, true>(p.rows, p.gate, r, [&](int i, size_t at) { rg[i % kKept] = *reinterpret_cast<const RG *>(gate + w.channel + at); });
+            walk<L, true>(p.rows, p.y, r, [&](int i, size_t at) {
+                if (t > 0) ry[i % kKept] = *reinterpret_cast<const RX *>(y + w.channel + (at - p.y.stride));
+                t = t == 0 ? p.rows.tokens - 1 : t - 1;
+            });
+            if constexpr (SIGMOID)
+                walk<L, true>(p.rows, p.x, r, [&](int i, size_t at) { rx[i % kKept] = *reinterpret_cast<const RX *>(x + w.channel + at); });
+        }
+    };
+    for (unsigned step = 0; step == 0 || step + 1 < R::kStages; ++step) fetch(step);
     if (w.blocks > 1) cluster_sync();   // every block is there before another writes to it
-    float carry[V] = {};
+    Lanes<V> carry = all<V>(0.0f);
+    InRow in_row;
     for (unsigned step = 0; step < rounds; ++step) {
-        const unsigned here = w.end - 1 - done;
-        TokenPlace place = {0, true, false, false};
-        const bool mine = lane < count;
-        if (mine) place = place_of(p.rows, here - lane);
-        const unsigned first = __ballot_sync(kFullMask, mine && place.first);
-        const unsigned last = __ballot_sync(kFullMask, mine && place.last);
-        const unsigned outside = __ballot_sync(kFullMask, mine && !place.inside);
-        const unsigned cut = last | outside;
-        // d: dh, then w; e: what w is multiplied by for the gate; m: for x
-        float a[L][V], d[L][V], e[L][V], m[SIGMOID ? L : 1][V];
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-            float gv[V], xv[V];
-            unpack<X, V>(rd[i], d[i]);
-            unpack<X, V>(ry[i], e[i]);
-            unpack<X, V>(rx[SIGMOID ? i : 0], xv);
-            unpack<G, V>(rg[i], gv);
-            if ((first >> i) & 1u) {
-                const float *from = state_of(p.rows, p.initial, __shfl_sync(kFullMask, place.row, i));
-#pragma unroll
-                for (int k = 0; k < V; ++k) e[i][k] = from != nullptr && live ? from[w.channel + k] : 0.0f;
-            }
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                if constexpr (SIGMOID) {
-                    float r;
-                    sigmoid_decay(gv[k], a[i][k], r);
-                    m[i][k] = r;
-                    e[i][k] = (e[i][k] - xv[k]) * (a[i][k] * r);
-                } else {
-                    a[i][k] = p.kind == kGateLog ? exp_decay(gv[k]) : gv[k];
-                    if (p.kind == kGateLog) e[i][k] *= a[i][k];
-                }
-                if (i >= count) a[i][k] = 1.0f, d[i][k] = 0.0f;
-                if ((outside >> i) & 1u) {
-                    a[i][k] = d[i][k] = e[i][k] = 0.0f;
-                    if constexpr (SIGMOID) m[i][k] = 0.0f;
-                }
-            }
-            if (((last >> i) & 1u) != 0 && p.grad_final != nullptr) {
-                const int r = __shfl_sync(kFullMask, place.row, i);
-                const size_t at = static_cast<size_t>(r) * p.rows.channels + w.channel;
-#pragma unroll
-                for (int k = 0; k < V; ++k) d[i][k] += live ? p.grad_final[at + k] : 0.0f;
-            }
-        }
-        float fa[V], f[V];
-#pragma unroll
-        for (int k = 0; k < V; ++k) fa[k] = 1.0f, f[k] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < L; ++i)
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                const bool c = (cut >> i) & 1u;
-                f[k] = a[i][k] * (c ? d[i][k] : d[i][k] + f[k]);
-                fa[k] = c ? 0.0f : fa[k] * a[i][k];
-            }
-        const int had = count;
-        done += round;
-        load();
-        exchange<V>(s_x, step & 1, w.blocks, w.rank, warp, lane, fa, f, cut != 0, carry, f);
-#pragma unroll
-        for (int i = 0; i < L; ++i)
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                const float v = (cut >> i) & 1u ? d[i][k] : d[i][k] + f[k];
-                f[k] = a[i][k] * v;
-                e[i][k] *= v;
-                d[i][k] = SIGMOID ? v * m[SIGMOID ? i : 0][k] : v;
-                a[i][k] = f[k];
-            }
-        if (live && had > 0) {
-            walk<L, true>(p.rows, p.grad_x, here, had, [&](int i, size_t at, unsigned) {
-                *reinterpret_cast<RX *>(grad_x + at) = pack<X, V>(d[i]);
-            });
-            walk<L, true>(p.rows, p.grad_gate, here, had, [&](int i, size_t at, unsigned) {
-                *reinterpret_cast<RG *>(grad_gate + at) = pack<G, V>(e[i]);
-            });
-        }
-        if (first != 0 && p.grad_initial != nullptr) {
+        const Run r = run_at(step);
+        char *const stage = ring + step % R::kStages * R::kStage;
+        if constexpr (COPY > 0) {
+            fetch(step + R::kStages - 1);   // into the stage that the round before has read
+            copies_wait<R::kStages - 1>();
+            __syncwarp();
+        } else {
 #pragma unroll
             for (int i = 0; i < L; ++i) {
-                if (((first >> i) & 1u) == 0) continue;
-                const int r = __shfl_sync(kFullMask, place.row, i);
-                if (live)
+                reinterpret_cast<RX *>(stage)[i * 32 + lane] = rd[i % kKept];
+                reinterpret_cast<RX *>(stage + R::kPart)[i * 32 + lane] = ry[i % kKept];
+                if constexpr (SIGMOID) reinterpret_cast<RX *>(stage + 2 * R::kPart)[i * 32 + lane] = rx[i % kKept];
+                reinterpret_cast<RG *>(stage + R::kGates)[i * 32 + lane] = rg[i % kKept];
+            }
+            fetch(step + 1);
+        }
+        Lanes<V> a[L], d[L], m[SIGMOID ? L : 1];   // decay, dh, r
 #pragma unroll
-                    for (int k = 0; k < V; ++k)
-                        p.grad_initial[static_cast<size_t>(r) * p.rows.channels + w.channel + k] = a[i][k];
+        for (int i = 0; i < L; ++i) {
+            const Lanes<V> g = R::gate(stage, i, lane);
+            d[i] = R::value(stage, 0, i, lane);
+            a[i] = g;
+            if constexpr (KIND == kGateLog) a[i] = exp_decay(g);
+            if constexpr (SIGMOID) sigmoid_decay(g, a[i], m[i]);
+        }
+        const Edges e = edges_of<L, true>(p.rows, r, lane, in_row);
+        const unsigned cut = e.last | e.outside;
+        const bool plain = r.whole && (cut | e.first) == 0;
+        Lanes<V> fa = all<V>(1.0f), f = all<V>(0.0f);
+        if (plain) {
+#pragma unroll
+            for (int i = 0; i < L; ++i) f = a[i] * (d[i] + f), fa = fa * a[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                if (i >= r.count) a[i] = all<V>(1.0f), d[i] = all<V>(0.0f);
+                if ((e.outside >> i) & 1u) {
+                    a[i] = d[i] = all<V>(0.0f);
+                    if constexpr (SIGMOID) m[i] = all<V>(0.0f);
+                }
+                if (((e.last >> i) & 1u) != 0 && p.grad_final != nullptr) {
+                    const size_t at = static_cast<size_t>(e.row_of(i)) * p.rows.channels + w.channel;
+                    if (live)
+#pragma unroll
+                        for (int k = 0; k < V; ++k) d[i].v[k] += p.grad_final[at + k];
+                }
+                const bool c = (cut >> i) & 1u;
+                const Lanes<V> sum = d[i] + f;
+#pragma unroll
+                for (int k = 0; k < V; ++k) f.v[k] = c ? d[i].v[k] : sum.v[k];
+                f = a[i] * f;
+                fa = c ? all<V>(0.0f) : fa * a[i];
             }
         }
+        f = exchange<V>(s_x, step & 1, w.blocks, w.rank, warp, lane, fa, f, cut != 0, carry);
+        // the gradients of token i from w = v and h_{t-1}
+        auto gradients = [&](int i, Lanes<V> v, Lanes<V> before, Lanes<V> &gx, Lanes<V> &gg) {
+            gx = v;
+            if constexpr (SIGMOID) {
+                const Lanes<V> xv = R::value(stage, 2, i, lane);
+                gx = v * m[SIGMOID ? i : 0];
+                gg = (fma(xv, all<V>(-1.0f), before) * (a[i] * m[SIGMOID ? i : 0])) * v;
+            } else {
+                gg = (KIND == kGateLog ? before * a[i] : before) * v;
+            }
+        };
+        if (plain) {
+            if (live) {
+                X *to_x = grad_x + element(p.grad_x, r.row, r.t);
+                G *to_gate = grad_gate + element(p.grad_gate, r.row, r.t);
+#pragma unroll
+                for (int i = 0; i < L; ++i) {
+                    const Lanes<V> v = d[i] + f;
+                    f = a[i] * v;
+                    Lanes<V> gx, gg;
+                    gradients(i, v, R::value(stage, 1, i, lane), gx, gg);
+                    *reinterpret_cast<RX *>(to_x) = pack<X, V>(gx.v);
+                    *reinterpret_cast<RG *>(to_gate) = pack<G, V>(gg.v);
+                    to_x -= p.grad_x.stride, to_gate -= p.grad_gate.stride;
+                }
+            }
+            __syncwarp();   // the stage has been read
+            continue;
+        }
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            const bool out = (e.outside >> i) & 1u;
+            Lanes<V> v = d[i] + f, before = R::value(stage, 1, i, lane), gx, gg;
+#pragma unroll
+            for (int k = 0; k < V; ++k) v.v[k] = (cut >> i) & 1u ? d[i].v[k] : v.v[k];
+            f = a[i] * v;
+            if ((e.first >> i) & 1u) {
+                const int row = e.row_of(i);
+                const float *from = state_of(p.rows, p.initial, row);
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    before.v[k] = from != nullptr && live ? from[w.channel + k] : 0.0f;
+                    if (p.grad_initial != nullptr && live)
+                        p.grad_initial[static_cast<size_t>(row) * p.rows.channels + w.channel + k] = f.v[k];
+                }
+            }
+            gradients(i, v, before, gx, gg);
+            a[i] = out ? all<V>(0.0f) : gx, d[i] = out ? all<V>(0.0f) : gg;
+        }
+        if (live && r.count > 0) {
+            walk<L, true>(p.rows, p.grad_x, r, [&](int i, size_t at) { *reinterpret_cast<RX *>(grad_x + at) = pack<X, V>(a[i].v); });
+            walk<L, true>(p.rows, p.grad_gate, r, [&](int i, size_t at) { *reinterpret_cast<RG *>(grad_gate + at) = pack<G, V>(d[i].v); });
+        }
+        __syncwarp();   // the stage has been read
     }
 }
 
 // ---------------------------------------------------------------------------
 // One token per row: a thread per V channels of a row.
 // ---------------------------------------------------------------------------
-template <typename X, typename G, int V>
+template <typename X, typename G, int V, int KIND>
 __global__ void __launch_bounds__(256) gated_step_kernel(const __grid_constant__ GatedScanCall p, unsigned lanes)
 {
     const size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
     const int r = static_cast<int>(i / lanes), c = static_cast<int>(i % lanes) * V;
     if (r >= p.rows.rows) return;
     X *out = static_cast<X *>(p.out.data) + r * p.out.row_stride + c;
-    float a[V], b[V];
-    unpack<X, V>(*reinterpret_cast<const typename Raw<X, V>::type *>(static_cast<const X *>(p.x.data) +
-                                                                      r * p.x.row_stride + c), b);
-    unpack<G, V>(*reinterpret_cast<const typename Raw<G, V>::type *>(static_cast<const G *>(p.gate.data) +
-                                                                      r * p.gate.row_stride + c), a);
+    const X *x = static_cast<const X *>(p.x.data) + r * p.x.row_stride + c;
+    const G *gate = static_cast<const G *>(p.gate.data) + r * p.gate.row_stride + c;
+    Lanes<V> a, b;
+    coefficients<KIND, V>(lanes_of<G, V>(*reinterpret_cast<const typename Raw<G, V>::type *>(gate)),
+                          lanes_of<X, V>(*reinterpret_cast<const typename Raw<X, V>::type *>(x)), a, b);
     const float *from = state_of(p.rows, p.initial, r);
     float *to = state_of(p.rows, p.final, r);
+    if (from != nullptr)
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-        if (p.kind == kGateLog) a[k] = exp_decay(a[k]);
-        if (p.kind == kGateSigmoid) {
-            float rest;
-            sigmoid_decay(a[k], a[k], rest);
-            b[k] *= rest;
-        }
-        if (from != nullptr) b[k] = fmaf(a[k], from[c + k], b[k]);
-    }
-    *reinterpret_cast<typename Raw<X, V>::type *>(out) = pack<X, V>(b);
+        for (int k = 0; k < V; ++k) b.v[k] = fmaf(a.v[k], from[c + k], b.v[k]);
+    *reinterpret_cast<typename Raw<X, V>::type *>(out) = pack<X, V>(b.v);
     if (to != nullptr)
 #pragma unroll
-        for (int k = 0; k < V; ++k) to[c + k] = b[k];
+        for (int k = 0; k < V; ++k) to[c + k] = b.v[k];
 }
 
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
-inline bool pairs(const GatedArray &a, size_t size)
-{
-    return reinterpret_cast<uintptr_t>(a.data) % (2 * size) == 0 && a.stride % 2 == 0 && a.row_stride % 2 == 0;
-}
+
+// The widest copies that a call's arrays allow: 16 or 4 bytes, or 0 where a
+// lane's `per_lane` values are not aligned as one.
+struct Width {
+    int per_lane;
+    size_t all = 0;
+    bool whole = true;
+    void add(const GatedArray &a, const GatedRows &rows, size_t size)
+    {
+        size_t bits = reinterpret_cast<uintptr_t>(a.data) | static_cast<size_t>(rows.channels) * size;
+        if (rows.tokens > 1) bits |= a.stride * size;
+        if (rows.starts == nullptr && rows.rows > 1) bits |= a.row_stride * size;
+        whole = whole && bits % (per_lane * size) == 0;
+        all |= bits;
+    }
+    int copy() const { return !whole ? 0 : all % 16 == 0 ? 16 : 4; }
+};
 
 // Spans and blocks per cluster.  Rows are spread first; a span's rows are then
 // spread over more blocks while the grid leaves places on the GPU empty and
@@ -634,63 +874,96 @@ inline void plan(GatedRows &rows, int per_lane, int tokens_per_warp, int sms)
     rows.blocks = static_cast<int>(blocks);
 }
 
-template <typename... Params, typename... Args>
-cudaError_t launch_clusters(void (*kernel)(Params...), const GatedRows &rows, cudaStream_t s, Args... args)
+template <typename Call>
+cudaError_t launch_clusters(void (*kernel)(Call), const Call &call, int ring, std::atomic<unsigned long long> &done, cudaStream_t s)
 {
+    const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), ring, done);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(rows.groups * rows.spans * static_cast<unsigned>(rows.blocks));
+    cfg.gridDim = dim3(call.rows.groups * call.rows.spans * static_cast<unsigned>(call.rows.blocks));
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(ring);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(rows.blocks);
+    attr[0].val.clusterDim.x = static_cast<unsigned>(call.rows.blocks);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+    return cudaLaunchKernelEx(&cfg, kernel, call);
 }
 
-template <typename X, typename G, int V>
+template <typename X, typename G, int V, int KIND, int COPY>
 cudaError_t forward(GatedScanCall call, int sms, cudaStream_t s)
 {
-    if (call.rows.starts == nullptr && call.rows.tokens == 1) {
-        const unsigned lanes = static_cast<unsigned>(call.rows.channels / V);
-        const size_t threads = static_cast<size_t>(call.rows.rows) * lanes;
-        gated_step_kernel<X, G, V><<<static_cast<unsigned>((threads + 255) / 256), 256, 0, s>>>(call, lanes);
-        return cudaGetLastError();
-    }
+    static std::atomic<unsigned long long> done;
     plan(call.rows, V, kForwardTokens, sms);
-    return launch_clusters(gated_scan_kernel<X, G, V>, call.rows, s, call);
+    return launch_clusters(gated_scan_kernel<X, G, V, KIND, COPY>, call, Ring<X, G, V, kForwardTokens, 1, COPY>::kBytes, done, s);
 }
-
+template <typename X, typename G, int V, int KIND>
+cudaError_t step(const GatedScanCall &call, cudaStream_t s)
+{
+    const unsigned lanes = static_cast<unsigned>(call.rows.channels / V);
+    const size_t threads = static_cast<size_t>(call.rows.rows) * lanes;
+    gated_step_kernel<X, G, V, KIND><<<static_cast<unsigned>((threads + 255) / 256), 256, 0, s>>>(call, lanes);
+    return cudaGetLastError();
+}
+template <typename X, typename G, int KIND>
+cudaError_t forward_kind(const GatedScanCall &call, int sms, cudaStream_t s)
+{
+    constexpr int V = 4 / sizeof(X);
+    Width width = {V};
+    width.add(call.x, call.rows, sizeof(X));
+    width.add(call.gate, call.rows, sizeof(G));
+    width.add(call.out, call.rows, sizeof(X));
+    const int copy = width.copy();
+    if (call.rows.starts == nullptr && call.rows.tokens == 1)
+        return copy > 0 ? step<X, G, V, KIND>(call, s) : step<X, G, 1, KIND>(call, s);
+    if (copy == 16) return forward<X, G, V, KIND, 16>(call, sms, s);
+    if (copy == 4) return forward<X, G, V, KIND, 4>(call, sms, s);
+    if constexpr (V > 1) return forward<X, G, 1, KIND, 0>(call, sms, s);
+    return cudaErrorInvalidValue;   // fp32 is aligned
+}
 template <typename X, typename G>
 cudaError_t forward_any(const GatedScanCall &call, int sms, cudaStream_t s)
 {
-    if constexpr (sizeof(X) == 2)
-        if (call.rows.channels % 2 == 0 && pairs(call.x, 2) && pairs(call.gate, sizeof(G)) && pairs(call.out, 2))
-            return forward<X, G, 2>(call, sms, s);
-    return forward<X, G, 1>(call, sms, s);
+    if (call.kind == kGateDecay) return forward_kind<X, G, kGateDecay>(call, sms, s);
+    if (call.kind == kGateLog) return forward_kind<X, G, kGateLog>(call, sms, s);
+    return forward_kind<X, G, kGateSigmoid>(call, sms, s);
 }
 
-template <typename X, typename G, int V>
+template <typename X, typename G, int V, int KIND, int COPY>
 cudaError_t backward(GatedBackwardCall call, int sms, cudaStream_t s)
 {
+    static std::atomic<unsigned long long> done;
     plan(call.rows, V, kBackwardTokens, sms);
-    if (call.kind == kGateSigmoid)
-        return launch_clusters(gated_scan_backward_kernel<X, G, V, true>, call.rows, s, call);
-    return launch_clusters(gated_scan_backward_kernel<X, G, V, false>, call.rows, s, call);
+    return launch_clusters(gated_scan_backward_kernel<X, G, V, KIND, COPY>, call,
+                           Ring<X, G, V, kBackwardTokens, KIND == kGateSigmoid ? 3 : 2, COPY>::kBytes, done, s);
 }
-
+template <typename X, typename G, int KIND>
+cudaError_t backward_kind(const GatedBackwardCall &call, int sms, cudaStream_t s)
+{
+    constexpr int V = 4 / sizeof(X);
+    Width width = {V};
+    width.add(call.grad, call.rows, sizeof(X));
+    width.add(call.y, call.rows, sizeof(X));
+    if (KIND == kGateSigmoid) width.add(call.x, call.rows, sizeof(X));
+    width.add(call.gate, call.rows, sizeof(G));
+    width.add(call.grad_x, call.rows, sizeof(X));
+    width.add(call.grad_gate, call.rows, sizeof(G));
+    const int copy = width.copy();
+    if (copy == 16) return backward<X, G, V, KIND, 16>(call, sms, s);
+    if (copy == 4) return backward<X, G, V, KIND, 4>(call, sms, s);
+    if constexpr (V > 1) return backward<X, G, 1, KIND, 0>(call, sms, s);
+    return cudaErrorInvalidValue;
+}
 template <typename X, typename G>
 cudaError_t backward_any(const GatedBackwardCall &call, int sms, cudaStream_t s)
 {
-    if constexpr (sizeof(X) == 2)
-        if (call.rows.channels % 2 == 0 && pairs(call.grad, 2) && (call.kind != kGateSigmoid || pairs(call.x, 2)) &&
-            pairs(call.gate, sizeof(G)) && pairs(call.y, 2) && pairs(call.grad_x, 2) &&
-            pairs(call.grad_gate, sizeof(G)))
-            return backward<X, G, 2>(call, sms, s);
-    return backward<X, G, 1>(call, sms, s);
+    if (call.kind == kGateDecay) return backward_kind<X, G, kGateDecay>(call, sms, s);
+    if (call.kind == kGateLog) return backward_kind<X, G, kGateLog>(call, sms, s);
+    return backward_kind<X, G, kGateSigmoid>(call, sms, s);
 }
 
 }  // namespace gated

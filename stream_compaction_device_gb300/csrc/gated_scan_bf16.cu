@@ -1,4 +1,5 @@
-// The gated recurrence on bf16 values (a translation unit per type, compiled in parallel).
+// The gated recurrence on bf16 values (a translation unit per type and direction,
+// compiled in parallel).
 #include "gated_scan.cuh"
 
 namespace devscan {
@@ -6,11 +7,6 @@ namespace devscan {
 cudaError_t launch_gated_scan_bf16(const GatedScanCall &call, bool wide, int sms, cudaStream_t s)
 {
     return wide ? gated::forward_any<__nv_bfloat16, float>(call, sms, s) : gated::forward_any<__nv_bfloat16, __nv_bfloat16>(call, sms, s);
-}
-
-cudaError_t launch_gated_backward_bf16(const GatedBackwardCall &call, bool wide, int sms, cudaStream_t s)
-{
-    return wide ? gated::backward_any<__nv_bfloat16, float>(call, sms, s) : gated::backward_any<__nv_bfloat16, __nv_bfloat16>(call, sms, s);
 }
 
 }  // namespace devscan

@@ -1,4 +1,5 @@
-// The gated recurrence on f16 values (a translation unit per type, compiled in parallel).
+// The gated recurrence on f16 values (a translation unit per type and direction,
+// compiled in parallel).
 #include "gated_scan.cuh"
 
 namespace devscan {
@@ -6,11 +7,6 @@ namespace devscan {
 cudaError_t launch_gated_scan_f16(const GatedScanCall &call, bool wide, int sms, cudaStream_t s)
 {
     return wide ? gated::forward_any<__half, float>(call, sms, s) : gated::forward_any<__half, __half>(call, sms, s);
-}
-
-cudaError_t launch_gated_backward_f16(const GatedBackwardCall &call, bool wide, int sms, cudaStream_t s)
-{
-    return wide ? gated::backward_any<__half, float>(call, sms, s) : gated::backward_any<__half, __half>(call, sms, s);
 }
 
 }  // namespace devscan

@@ -1,4 +1,5 @@
-// The gated recurrence on f32 values (a translation unit per type, compiled in parallel).
+// The gated recurrence on f32 values (a translation unit per type and direction,
+// compiled in parallel).
 #include "gated_scan.cuh"
 
 namespace devscan {
@@ -6,11 +7,6 @@ namespace devscan {
 cudaError_t launch_gated_scan_f32(const GatedScanCall &call, bool , int sms, cudaStream_t s)
 {
     return gated::forward_any<float, float>(call, sms, s);
-}
-
-cudaError_t launch_gated_backward_f32(const GatedBackwardCall &call, bool , int sms, cudaStream_t s)
-{
-    return gated::backward_any<float, float>(call, sms, s);
 }
 
 }  // namespace devscan

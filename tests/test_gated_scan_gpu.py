@@ -184,6 +184,26 @@ def test_strides(ds, dtype):
     assert ds.gated_scan(into, gate, kind="log", out=into)[0] is into and torch.equal(into, want)
 
 
+@pytest.mark.parametrize("tokens", [1, 200])
+def test_wide_gates_at_any_address(ds, tokens):
+    """fp32 gates and their gradients on 4 bytes beside pairs of 16-bit values, and 4-byte-aligned rows."""
+    rng = np.random.default_rng(9)
+    x = cuda(rng.standard_normal((3, tokens, 70)), BF16)
+    gate = cuda(rng.standard_normal((3, tokens, 75)))
+    at = gate[..., 1:71]
+    spans = ref.rows_of(None, tokens, 3)
+    out, final = ds.gated_scan(x, at, kind="sigmoid")
+    h, room, last, last_room = ref.scan(flat(x), flat(at), "sigmoid", spans)
+    ref.close(out.reshape(-1, 70), h, room, "out")
+    ref.close(final, last, last_room, "final")
+    wide = torch.zeros(3, tokens, 76, device="cuda")
+    gx, _, _ = ds.gated_scan_backward(x, x, at, out, kind="sigmoid", grad_gate=wide[..., 3:73])
+    want = ref.scan_backward(flat(x), flat(x), flat(at), flat(out), "sigmoid", spans)
+    ref.close(gx.reshape(-1, 70), *want["x"], "grad_x")
+    ref.close(wide[..., 3:73].reshape(-1, 70), *want["gate"], "grad_gate")
+    assert not wide[..., :3].any() and not wide[..., 73:].any()
+
+
 def test_what_is_not_a_number_stays_in_its_row(ds):
     """Rows after one that ends in infinity or NaN are what they are without it, forward and back."""
     rng = np.random.default_rng(6)
