@@ -35,14 +35,27 @@ __device__ __forceinline__ void unpack(typename Raw<T, V>::type raw, float (&v)[
 #pragma unroll
     for (int k = 0; k < V; ++k) v[k] = to_float(e[k]);
 }
+__device__ __forceinline__ void pair_from_floats(__half2 &p, float a, float b) { p = __floats2half2_rn(a, b); }
+__device__ __forceinline__ void pair_from_floats(__nv_bfloat162 &p, float a, float b) { p = __floats2bfloat162_rn(a, b); }
+template <typename T> struct PairOf;
+template <> struct PairOf<__half> { using type = __half2; };
+template <> struct PairOf<__nv_bfloat16> { using type = __nv_bfloat162; };
+
 template <typename T, int V>
 __device__ __forceinline__ typename Raw<T, V>::type pack(const float (&v)[V])
 {
-    T e[V];
-#pragma unroll
-    for (int k = 0; k < V; ++k) e[k] = from_float<T>(v[k]);
     typename Raw<T, V>::type raw;
-    __builtin_memcpy(&raw, e, sizeof(e));
+    if constexpr (sizeof(T) == 2 && V % 2 == 0) {   // one conversion for two
+        typename PairOf<T>::type e[V / 2];
+#pragma unroll
+        for (int k = 0; k < V / 2; ++k) pair_from_floats(e[k], v[2 * k], v[2 * k + 1]);
+        __builtin_memcpy(&raw, e, sizeof(e));
+    } else {
+        T e[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) e[k] = from_float<T>(v[k]);
+        __builtin_memcpy(&raw, e, sizeof(e));
+    }
     return raw;
 }
 

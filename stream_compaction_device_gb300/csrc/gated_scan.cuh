@@ -94,19 +94,32 @@ template <typename T, int V> __device__ __forceinline__ Lanes<V> lanes_of(typena
 // lean to one side there: it is 1 plus or minus something small, rounded once.
 // ---------------------------------------------------------------------------
 
-// exp(g): near 0 as 1 + (its series to the fifth power, off by less than
-// g^6 / 720 < 2^-27); elsewhere the hardware's, off by 2^-22 of values that act
-// less than ten times.
+// The hardware's 2^x and 1 / x (results below 2^-126 are 0).
+__device__ __forceinline__ float hard_exp(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+    return y;
+}
+__device__ __forceinline__ float hard_reciprocal(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// exp(g): near 0 as 1 + (its series to the fourth power, off by less than
+// g^5 / 120 < 2^-26); elsewhere the hardware's, off by 2^-22 of values that act
+// less than twenty times.
 template <int V> __device__ __forceinline__ Lanes<V> exp_decay(Lanes<V> g)
 {
-    Lanes<V> s = fma(g, all<V>(1.0f / 120), all<V>(1.0f / 24));
-    s = fma(g, s, all<V>(1.0f / 6));
+    Lanes<V> s = fma(g, all<V>(1.0f / 24), all<V>(1.0f / 6));
     s = fma(g, s, all<V>(0.5f));
     s = fma(g, s, all<V>(1.0f));
     s = g * s;
     s = s + all<V>(1.0f);
 #pragma unroll
-    for (int k = 0; k < V; ++k) s.v[k] = fabsf(g.v[k]) < 0.125f ? s.v[k] : __expf(g.v[k]);
+    for (int k = 0; k < V; ++k) s.v[k] = fabsf(g.v[k]) < 0.0625f ? s.v[k] : hard_exp(g.v[k]);
     return s;
 }
 
@@ -115,8 +128,8 @@ template <int V> __device__ __forceinline__ void sigmoid_decay(Lanes<V> g, Lanes
 {
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-        const float t = __expf(-fabsf(g.v[k]));
-        const float small = __fdividef(t, 1.0f + t), large = 1.0f - small;
+        const float t = hard_exp(-fabsf(g.v[k]));
+        const float small = t * hard_reciprocal(1.0f + t), large = 1.0f - small;
         a.v[k] = g.v[k] >= 0.0f ? large : small;
         r.v[k] = g.v[k] >= 0.0f ? small : large;
     }
@@ -269,36 +282,45 @@ __device__ __forceinline__ void copy_tokens(const GatedRows &rows, const GatedAr
     constexpr int kPieces = 32 * WORD / W;                        // of a token
     constexpr int kAtOnce = kPieces < 32 ? 32 / kPieces : 1;      // tokens per instruction
     constexpr int kParts = kPieces > 32 ? kPieces / 32 : 1;       // instructions per token
+    const int i0 = kPieces < 32 ? lane / kPieces : 0, piece = kPieces < 32 ? lane % kPieces : lane;
+    const int left = bytes - piece * W;
+    to += i0 * (32 * WORD) + piece * W;
+    if (r.whole && (BACK == 0 || r.t >= L)) {
+        const size_t stride = array.stride * size;
+        const char *from = base + element(array, r.row, r.t - BACK) * size + piece * W;
+        from = DOWN ? from - i0 * stride : from + i0 * stride;
 #pragma unroll
-    for (int j = 0; j < L / kAtOnce; ++j)
+        for (int j = 0; j < L / kAtOnce; ++j) {
 #pragma unroll
-        for (int q = 0; q < kParts; ++q) {
-            const int piece = kPieces > 32 ? q * 32 + lane : lane % kPieces;
-            const int i = j * kAtOnce + (kPieces < 32 ? lane / kPieces : 0);
-            const int left = bytes - piece * W;
-            if (i >= r.count || left <= 0) continue;
-            unsigned row = r.row, t = r.t;
-            if (r.whole) {
-                t = DOWN ? t - i : t + i;
-            } else if (rows.starts == nullptr) {
-                const unsigned n = DOWN ? r.n - i : r.n + i;
-                row = n / rows.tokens, t = n - row * rows.tokens;
-            } else {
-                t = DOWN ? r.n - i : r.n + i;
-            }
-            if (BACK > 0 && t < BACK) continue;   // nothing before it: not looked at
-            copy_async<W>(to + i * (32 * WORD) + piece * W, base + element(array, row, t - BACK) * size + piece * W,
-                          left < W ? left : W);
+            for (int q = 0; q < kParts; ++q)
+                if (left > q * 32 * W) copy_async<W>(to + (j * kAtOnce * 32 * WORD + q * 32 * W), from + q * 32 * W, min(left - q * 32 * W, W));
+            from = DOWN ? from - kAtOnce * stride : from + kAtOnce * stride;
         }
+        return;
+    }
+#pragma unroll 1
+    for (int j = 0; j < L / kAtOnce; ++j) {
+        const int i = j * kAtOnce + i0;
+        if (i >= r.count) break;
+        const unsigned n = DOWN ? r.n - i : r.n + i;
+        const unsigned row = rows.starts == nullptr ? n / rows.tokens : 0u, t = n - row * rows.tokens;
+        if (BACK > 0 && t < BACK) continue;   // nothing before it: not looked at
+        const char *from = base + element(array, row, t - BACK) * size + piece * W;
+#pragma unroll
+        for (int q = 0; q < kParts; ++q)
+            if (left > q * 32 * W) copy_async<W>(to + j * (kAtOnce * 32 * WORD) + q * 32 * W, from + q * 32 * W, min(left - q * 32 * W, W));
+    }
 }
 
 // ---------------------------------------------------------------------------
 // The exchange of one round: every warp hands in its map, and gets the value
-// that comes into it.
+// that comes into it.  The cluster's last warp hands on what goes out of it as
+// the next round's carry.
 // ---------------------------------------------------------------------------
 template <int V> struct Exchange {
     Lanes<V> a[2][kWarps][32], h[2][kWarps][32];                       // this block's warps
     Lanes<V> all_a[2][kMostBlocks][32], all_h[2][kMostBlocks][32];     // the cluster's blocks
+    Lanes<V> carry[2][32];
     unsigned cut[2][kWarps], all_cut[2][kMostBlocks];                  // nonzero: the map forgets what comes in
 };
 
@@ -322,50 +344,65 @@ template <int V> __device__ __forceinline__ void st_lanes(uint32_t to, Lanes<V> 
 // has arrived.
 template <int V>
 __device__ __forceinline__ Lanes<V> exchange(Exchange<V> &x, int turn, int blocks, int rank, int warp, int lane,
-                                             Lanes<V> a, Lanes<V> h, bool cut, Lanes<V> &carry)
+                                             Lanes<V> a, Lanes<V> h, bool cut)
 {
     x.a[turn][warp][lane] = a, x.h[turn][warp][lane] = h;
     if (lane == 0) x.cut[turn][warp] = cut;
     __syncthreads();
-    Lanes<V> run = carry;
-    if (blocks > 1) {
-        if (warp == 0) {
-            Lanes<V> fa = all<V>(1.0f), fh = all<V>(0.0f);
-            unsigned any = 0;
+    // the map of the block's warps before this one, and of all of them
+    Lanes<V> ba = all<V>(1.0f), bh = all<V>(0.0f), fa = ba, fh = bh;
+    const unsigned cuts = __ballot_sync(kFullMask, lane < kWarps && x.cut[turn][lane & (kWarps - 1)] != 0);
+    if (cuts == 0) {
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const unsigned c = x.cut[turn][w];
-                const Lanes<V> wa = x.a[turn][w][lane];
-                fh = follow(c != 0, wa, fh, x.h[turn][w][lane]);
-                fa = c != 0 ? wa : wa * fa;
-                any |= c;
-            }
-            for (int q = 0; q < blocks; ++q) {
-                st_lanes<V>(cluster_addr(&x.all_a[turn][rank][lane], q), fa);
-                st_lanes<V>(cluster_addr(&x.all_h[turn][rank][lane], q), fh);
-                if (lane == 0) st_cluster(cluster_addr(&x.all_cut[turn][rank], q), any);
-            }
+        for (int w = 0; w < kWarps; ++w) {
+            if (w == warp) ba = fa, bh = fh;
+            if (w >= warp && blocks == 1) break;
+            const Lanes<V> wa = x.a[turn][w][lane];
+            fh = fma(wa, fh, x.h[turn][w][lane]);
+            fa = wa * fa;
         }
-        cluster_sync();
-        Lanes<V> into = run;
-        for (int q = 0; q < blocks; ++q) {
-            if (q == rank) into = run;
-            run = follow(x.all_cut[turn][q] != 0, x.all_a[turn][q][lane], run, x.all_h[turn][q][lane]);
+    } else {
+#pragma unroll 1
+        for (int w = 0; w < kWarps; ++w) {
+            if (w == warp) ba = fa, bh = fh;
+            const bool c = (cuts >> w) & 1u;
+            const Lanes<V> wa = x.a[turn][w][lane];
+            fh = follow(c, wa, fh, x.h[turn][w][lane]);
+            fa = c ? wa : wa * fa;
         }
-        carry = run, run = into;
     }
-    // the block's warps before this one; where the block is alone, all of them for the next round
-    Lanes<V> in = run;
+    if (blocks == 1) return follow((cuts & ((1u << warp) - 1u)) != 0, ba, x.carry[turn][lane], bh);
+    if (warp < blocks) {   // warp q tells block q
+        st_lanes<V>(cluster_addr(&x.all_a[turn][rank][lane], warp), fa);
+        st_lanes<V>(cluster_addr(&x.all_h[turn][rank][lane], warp), fh);
+        if (lane == 0) st_cluster(cluster_addr(&x.all_cut[turn][rank], warp), cuts);
+    }
+    cluster_sync();
+    Lanes<V> in = x.carry[turn][lane];
+    const unsigned all_cuts = __ballot_sync(kFullMask, lane < blocks && x.all_cut[turn][lane & (kMostBlocks - 1)] != 0);
+    if (all_cuts == 0) {
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w == warp) {
-            in = run;
-            if (blocks > 1) break;
-        }
-        run = follow(x.cut[turn][w] != 0, x.a[turn][w][lane], run, x.h[turn][w][lane]);
+        for (int q = 0; q < kMostBlocks - 1; ++q)
+            if (q < rank) in = fma(x.all_a[turn][q][lane], in, x.all_h[turn][q][lane]);
+    } else {
+#pragma unroll 1
+        for (int q = 0; q < rank; ++q)
+            in = follow((all_cuts >> q) & 1u, x.all_a[turn][q][lane], in, x.all_h[turn][q][lane]);
     }
-    if (blocks == 1) carry = run;
-    return in;
+    return follow((cuts & ((1u << warp) - 1u)) != 0, ba, in, bh);
+}
+
+// What goes out of the cluster's last warp.  Not after the last round: another
+// block may have left by then.
+template <int V>
+__device__ __forceinline__ void hand_on(Exchange<V> &x, int turn, int blocks, int rank, int warp, int lane, Lanes<V> h)
+{
+    if (rank != blocks - 1 || warp != kWarps - 1) return;
+    if (blocks == 1) {
+        x.carry[turn][lane] = h;
+    } else {
+        for (int q = 0; q < blocks; ++q) st_lanes<V>(cluster_addr(&x.carry[turn][lane], q), h);
+    }
 }
 
 // What a block of the grid works on.
@@ -486,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_kernel(const __grid_co
     using RG = typename R::RG;
     extern __shared__ __align__(16) char s_ring[];
     __shared__ Exchange<V> s_x;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(kFullMask, threadIdx.x >> 5, 0);
     const Work w = work_of(p.rows, V);
     const bool live = w.channel < p.rows.channels;   // a whole number of lanes is
     const int first_channel = w.channel - lane * V;
@@ -532,8 +569,8 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_kernel(const __grid_co
         }
     };
     for (unsigned step = 0; step == 0 || step + 1 < R::kStages; ++step) fetch(step);
+    if (warp == 0) s_x.carry[0][lane] = all<V>(0.0f);
     if (w.blocks > 1) cluster_sync();   // every block is there before another writes to it
-    Lanes<V> carry = all<V>(0.0f);
     InRow in_row;
     for (unsigned step = 0; step < rounds; ++step) {
         const Run r = run_at(step);
@@ -578,17 +615,16 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_kernel(const __grid_co
                 fa = c ? all<V>(0.0f) : fa * a[i];
             }
         }
-        h = exchange<V>(s_x, step & 1, w.blocks, w.rank, warp, lane, fa, h, cut != 0, carry);
+        h = exchange<V>(s_x, step & 1, w.blocks, w.rank, warp, lane, fa, h, cut != 0);
         if (plain) {
-            if (live) {
-                X *to = out + element(p.out, r.row, r.t);
+            X *to = out + element(p.out, r.row, r.t);
 #pragma unroll
-                for (int i = 0; i < L; ++i) {
-                    h = fma(a[i], h, b[i]);
-                    *reinterpret_cast<RX *>(to) = pack<X, V>(h.v);
-                    to += p.out.stride;
-                }
+            for (int i = 0; i < L; ++i) {
+                h = fma(a[i], h, b[i]);
+                if (live) *reinterpret_cast<RX *>(to) = pack<X, V>(h.v);
+                to += p.out.stride;
             }
+            if (step + 1 < rounds) hand_on<V>(s_x, (step + 1) & 1, w.blocks, w.rank, warp, lane, h);
             continue;
         }
 #pragma unroll
@@ -596,6 +632,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_kernel(const __grid_co
             h = follow((cut >> i) & 1u, a[i], h, b[i]);
             b[i] = h;
         }
+        if (step + 1 < rounds) hand_on<V>(s_x, (step + 1) & 1, w.blocks, w.rank, warp, lane, h);
         if (live && r.count > 0)
             walk<L, false>(p.rows, p.out, r, [&](int i, size_t at) { *reinterpret_cast<RX *>(out + at) = pack<X, V>(b[i].v); });
         if (p.final != nullptr) {
@@ -631,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_backward_kernel(const 
     using RG = typename R::RG;
     extern __shared__ __align__(16) char s_ring[];
     __shared__ Exchange<V> s_x;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(kFullMask, threadIdx.x >> 5, 0);
     const Work w = work_of(p.rows, V);
     const bool live = w.channel < p.rows.channels;
     const int first_channel = w.channel - lane * V;
@@ -693,8 +730,8 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_backward_kernel(const 
         }
     };
     for (unsigned step = 0; step == 0 || step + 1 < R::kStages; ++step) fetch(step);
+    if (warp == 0) s_x.carry[0][lane] = all<V>(0.0f);
     if (w.blocks > 1) cluster_sync();   // every block is there before another writes to it
-    Lanes<V> carry = all<V>(0.0f);
     InRow in_row;
     for (unsigned step = 0; step < rounds; ++step) {
         const Run r = run_at(step);
@@ -751,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_backward_kernel(const 
                 fa = c ? all<V>(0.0f) : fa * a[i];
             }
         }
-        f = exchange<V>(s_x, step & 1, w.blocks, w.rank, warp, lane, fa, f, cut != 0, carry);
+        f = exchange<V>(s_x, step & 1, w.blocks, w.rank, warp, lane, fa, f, cut != 0);
         // the gradients of token i from w = v and h_{t-1}
         auto gradients = [&](int i, Lanes<V> v, Lanes<V> before, Lanes<V> &gx, Lanes<V> &gg) {
             gx = v;
@@ -764,20 +801,21 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_backward_kernel(const 
             }
         };
         if (plain) {
-            if (live) {
-                X *to_x = grad_x + element(p.grad_x, r.row, r.t);
-                G *to_gate = grad_gate + element(p.grad_gate, r.row, r.t);
+            X *to_x = grad_x + element(p.grad_x, r.row, r.t);
+            G *to_gate = grad_gate + element(p.grad_gate, r.row, r.t);
 #pragma unroll
-                for (int i = 0; i < L; ++i) {
-                    const Lanes<V> v = d[i] + f;
-                    f = a[i] * v;
-                    Lanes<V> gx, gg;
-                    gradients(i, v, R::value(stage, 1, i, lane), gx, gg);
+            for (int i = 0; i < L; ++i) {
+                const Lanes<V> v = d[i] + f;
+                f = a[i] * v;
+                Lanes<V> gx, gg;
+                gradients(i, v, R::value(stage, 1, i, lane), gx, gg);
+                if (live) {
                     *reinterpret_cast<RX *>(to_x) = pack<X, V>(gx.v);
                     *reinterpret_cast<RG *>(to_gate) = pack<G, V>(gg.v);
-                    to_x -= p.grad_x.stride, to_gate -= p.grad_gate.stride;
                 }
+                to_x -= p.grad_x.stride, to_gate -= p.grad_gate.stride;
             }
+            if (step + 1 < rounds) hand_on<V>(s_x, (step + 1) & 1, w.blocks, w.rank, warp, lane, f);
             __syncwarp();   // the stage has been read
             continue;
         }
@@ -801,6 +839,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_backward_kernel(const 
             gradients(i, v, before, gx, gg);
             a[i] = out ? all<V>(0.0f) : gx, d[i] = out ? all<V>(0.0f) : gg;
         }
+        if (step + 1 < rounds) hand_on<V>(s_x, (step + 1) & 1, w.blocks, w.rank, warp, lane, f);
         if (live && r.count > 0) {
             walk<L, true>(p.rows, p.grad_x, r, [&](int i, size_t at) { *reinterpret_cast<RX *>(grad_x + at) = pack<X, V>(a[i].v); });
             walk<L, true>(p.rows, p.grad_gate, r, [&](int i, size_t at) { *reinterpret_cast<RG *>(grad_gate + at) = pack<G, V>(d[i].v); });
