@@ -43,8 +43,19 @@ namespace gated {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMostBlocks = 8;   // of a cluster (the portable size)
-constexpr int kForwardTokens = 16, kBackwardTokens = 8;   // per warp and round
-constexpr int kRingBytes = 96 << 10;                      // of a block, so that an SM holds two
+constexpr int kMostPerSm = 3;   // blocks, where two stages of the ring fit
+// Shared memory for a block's ring where an SM holds `blocks`: of its 228 KB,
+// 1 KB and the exchange go off for each.
+constexpr int ring_bytes(int blocks) { return (228 << 10) / blocks - (18 << 10); }
+// Tokens of a warp and round where the values of a lane and token have `bytes`
+// bytes: as many as two blocks per SM hold twice (long rows: fewer rounds), or
+// fewer, where rows are short.
+constexpr int tokens_per_round(int bytes, int copy, bool many)
+{
+    const int most = ring_bytes(2) / (2 * kWarps * 32 * bytes) / 4 * 4;
+    const int some = bytes <= 8 && copy > 0 ? 12 : 8;
+    return copy == 0 || !many ? some : most;
+}
 
 // ---------------------------------------------------------------------------
 // V neighbouring channels in fp32.  Two go through one instruction.
@@ -95,12 +106,13 @@ template <typename T, int V> __device__ __forceinline__ Lanes<V> lanes_of(typena
 // ---------------------------------------------------------------------------
 
 // The hardware's 2^x and 1 / x (results below 2^-126 are 0).
-__device__ __forceinline__ float hard_exp(float x)
+__device__ __forceinline__ float hard_exp2(float x)
 {
     float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+constexpr float kLog2E = 1.4426950408889634f;
 __device__ __forceinline__ float hard_reciprocal(float x)
 {
     float y;
@@ -118,22 +130,46 @@ template <int V> __device__ __forceinline__ Lanes<V> exp_decay(Lanes<V> g)
     s = fma(g, s, all<V>(1.0f));
     s = g * s;
     s = s + all<V>(1.0f);
+    const Lanes<V> t = g * all<V>(kLog2E);
 #pragma unroll
-    for (int k = 0; k < V; ++k) s.v[k] = fabsf(g.v[k]) < 0.0625f ? s.v[k] : hard_exp(g.v[k]);
+    for (int k = 0; k < V; ++k) s.v[k] = fabsf(g.v[k]) < 0.0625f ? s.v[k] : hard_exp2(t.v[k]);
     return s;
 }
 
-// a = 1 / (1 + exp(-g)) and r = 1 - a, the smaller of the two from the quotient.
-template <int V> __device__ __forceinline__ void sigmoid_decay(Lanes<V> g, Lanes<V> &a, Lanes<V> &r)
+// a = 1 / (1 + exp(-g)) and r = 1 - a: the smaller of the two is the quotient
+// t / (1 + t), t = exp(-|g|).  Both are kept as it, with g's sign.
+template <int V> __device__ __forceinline__ Lanes<V> sigmoid_kept(Lanes<V> g)
 {
+    const Lanes<V> scaled = g * all<V>(kLog2E);
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-        const float t = hard_exp(-fabsf(g.v[k]));
-        const float small = t * hard_reciprocal(1.0f + t), large = 1.0f - small;
-        a.v[k] = g.v[k] >= 0.0f ? large : small;
-        r.v[k] = g.v[k] >= 0.0f ? small : large;
+        const float t = hard_exp2(-fabsf(scaled.v[k]));
+        g.v[k] = copysignf(t * hard_reciprocal(1.0f + t), g.v[k]);
+    }
+    return g;
+}
+
+// What a token's gate is kept as, a from it, and what x is multiplied by.
+template <int KIND, int V> __device__ __forceinline__ Lanes<V> kept_of(Lanes<V> gate)
+{
+    if constexpr (KIND == kGateLog) return exp_decay(gate);
+    if constexpr (KIND == kGateSigmoid) return sigmoid_kept(gate);
+    return gate;
+}
+template <int KIND, int V> __device__ __forceinline__ void coefficients(Lanes<V> kept, Lanes<V> &a, Lanes<V> &r)
+{
+    a = kept;
+    if constexpr (KIND == kGateSigmoid) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const float small = fabsf(kept.v[k]), large = 1.0f - small;
+            const bool open = static_cast<int>(__float_as_uint(kept.v[k])) >= 0;   // g at least 0 (or a NaN)
+            a.v[k] = open ? large : small;
+            r.v[k] = open ? small : large;
+        }
     }
 }
+template <int KIND> constexpr float kHold = KIND == kGateSigmoid ? 0.0f : 1.0f;   // kept for a = 1
 
 // ---------------------------------------------------------------------------
 // Rows and spans.
@@ -485,9 +521,11 @@ __device__ __forceinline__ void empty_rows(const GatedRows &rows, const Work &w,
 template <typename X, typename G, int V, int L, int VALUES, int COPY> struct Ring {
     using RX = typename Raw<X, V>::type;
     using RG = typename Raw<G, V>::type;
+    static constexpr int kTokens = L;
     static constexpr int kX = static_cast<int>(sizeof(RX)), kG = static_cast<int>(sizeof(RG));
     static constexpr int kPart = L * 32 * kX, kGates = VALUES * kPart, kStage = kGates + L * 32 * kG;   // bytes
-    static constexpr int kFit = kRingBytes / (kWarps * kStage), kStages = COPY == 0 ? 1 : kFit < 4 ? kFit : 4;
+    static constexpr int kPerSm = COPY > 0 && 2 * kWarps * kStage <= ring_bytes(kMostPerSm) ? kMostPerSm : 2;
+    static constexpr int kFit = ring_bytes(kPerSm) / (kWarps * kStage), kStages = COPY == 0 ? 1 : kFit < 4 ? kFit : 4;
     static constexpr int kBytes = kWarps * kStages * kStage;
     static_assert(COPY == 0 || kStages >= 2, "a round is copied while another is read");
     static __device__ __forceinline__ Lanes<V> value(const char *stage, int array, int i, int lane)
@@ -498,27 +536,54 @@ template <typename X, typename G, int V, int L, int VALUES, int COPY> struct Rin
     {
         return lanes_of<G, V>(reinterpret_cast<const RG *>(stage + kGates)[i * 32 + lane]);
     }
+    // fp32 values in the place of a lane's own first value and gate
+    static __device__ __forceinline__ void put(char *stage, int i, int lane, Lanes<V> b)
+    {
+        char *value = stage + (i * 32 + lane) * kX, *gate = stage + kGates + (i * 32 + lane) * kG;
+        if constexpr (kG >= 4 * V) {
+            *reinterpret_cast<Lanes<V> *>(gate) = b;
+        } else {   // half of it in each
+            __builtin_memcpy(value, &b, 2 * V);
+            __builtin_memcpy(gate, reinterpret_cast<const char *>(&b) + 2 * V, 2 * V);
+        }
+    }
+    static __device__ __forceinline__ Lanes<V> get(const char *stage, int i, int lane)
+    {
+        const char *value = stage + (i * 32 + lane) * kX, *gate = stage + kGates + (i * 32 + lane) * kG;
+        Lanes<V> b;
+        if constexpr (kG >= 4 * V) {
+            b = *reinterpret_cast<const Lanes<V> *>(gate);
+        } else {
+            __builtin_memcpy(&b, value, 2 * V);
+            __builtin_memcpy(reinterpret_cast<char *>(&b) + 2 * V, gate, 2 * V);
+        }
+        return b;
+    }
 };
+
+template <typename X, typename G, int V, int VALUES> constexpr int kLaneBytes = V * (VALUES * static_cast<int>(sizeof(X)) + static_cast<int>(sizeof(G)));
+template <typename X, typename G, int V, int VALUES, int COPY, bool MANY>
+using RingOf = Ring<X, G, V, tokens_per_round(kLaneBytes<X, G, V, VALUES>, COPY, MANY), VALUES, COPY>;
+template <typename X, typename G, int V, int COPY, bool MANY> using ForwardRing = RingOf<X, G, V, 1, COPY, MANY>;
+template <typename X, typename G, int V, int KIND, int COPY, bool MANY>
+using BackwardRing = RingOf<X, G, V, KIND == kGateSigmoid ? 3 : 2, COPY, MANY>;
 
 // ---------------------------------------------------------------------------
 // Forward.
 // ---------------------------------------------------------------------------
-template <int KIND, int V> __device__ __forceinline__ void coefficients(Lanes<V> gate, Lanes<V> x, Lanes<V> &a, Lanes<V> &b)
+// b of a token from x.
+template <int KIND, int V> __device__ __forceinline__ Lanes<V> given(Lanes<V> r, Lanes<V> x)
 {
-    a = gate, b = x;
-    if constexpr (KIND == kGateLog) a = exp_decay(gate);
-    if constexpr (KIND == kGateSigmoid) {
-        Lanes<V> r;
-        sigmoid_decay(gate, a, r);
-        b = r * x;
-    }
+    if constexpr (KIND == kGateSigmoid) return r * x;
+    return x;
 }
 
-template <typename X, typename G, int V, int KIND, int COPY>
-__global__ void __launch_bounds__(kThreads, 2) gated_scan_kernel(const __grid_constant__ GatedScanCall p)
+template <typename X, typename G, int V, int KIND, int COPY, bool MANY>
+__global__ void __launch_bounds__(kThreads, (ForwardRing<X, G, V, COPY, MANY>::kPerSm))
+ gated_scan_kernel(const __grid_constant__ GatedScanCall p)
 {
-    constexpr int L = kForwardTokens;
-    using R = Ring<X, G, V, L, 1, COPY>;
+    using R = ForwardRing<X, G, V, COPY, MANY>;
+    constexpr int L = R::kTokens;
     using RX = typename R::RX;
     using RG = typename R::RG;
     extern __shared__ __align__(16) char s_ring[];
@@ -587,32 +652,38 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_kernel(const __grid_co
             }
             fetch(step + 1);
         }
-        Lanes<V> a[L], b[L];
-#pragma unroll
-        for (int i = 0; i < L; ++i)
-            coefficients<KIND, V>(R::gate(stage, i, lane), R::value(stage, 0, i, lane), a[i], b[i]);
-        __syncwarp();   // the stage has been read
         const Edges e = edges_of<L, false>(p.rows, r, lane, in_row);
         const unsigned cut = e.first | e.outside;
         const bool plain = r.whole && (cut | e.last) == 0;
-        Lanes<V> fa = all<V>(1.0f), h = all<V>(0.0f);
+        Lanes<V> kept[L], fa = all<V>(1.0f), h = all<V>(0.0f);
+#pragma unroll
+        for (int i = 0; i < L; ++i) kept[i] = kept_of<KIND, V>(R::gate(stage, i, lane));
         if (plain) {
 #pragma unroll
-            for (int i = 0; i < L; ++i) h = fma(a[i], h, b[i]), fa = fa * a[i];
-        } else {
+            for (int i = 0; i < L; ++i) {
+                Lanes<V> a, rest;
+                coefficients<KIND, V>(kept[i], a, rest);
+                h = fma(a, h, given<KIND, V>(rest, R::value(stage, 0, i, lane)));
+                fa = fa * a;
+            }
+        } else {   // b is left in the ring: what it was made of may be overwritten before it is used again
 #pragma unroll
             for (int i = 0; i < L; ++i) {
-                if (i >= r.count) a[i] = all<V>(1.0f), b[i] = all<V>(0.0f);
-                if ((e.outside >> i) & 1u) b[i] = all<V>(0.0f);
+                Lanes<V> a, rest;
+                if (i >= r.count) kept[i] = all<V>(kHold<KIND>);
+                coefficients<KIND, V>(kept[i], a, rest);
+                Lanes<V> b = given<KIND, V>(rest, R::value(stage, 0, i, lane));
+                if (i >= r.count || ((e.outside >> i) & 1u)) b = all<V>(0.0f);
                 if ((e.first >> i) & 1u) {
                     const float *from = state_of(p.rows, p.initial, e.row_of(i));
                     if (from != nullptr && live)
 #pragma unroll
-                        for (int k = 0; k < V; ++k) b[i].v[k] = fmaf(a[i].v[k], from[w.channel + k], b[i].v[k]);
+                        for (int k = 0; k < V; ++k) b.v[k] = fmaf(a.v[k], from[w.channel + k], b.v[k]);
                 }
+                R::put(stage, i, lane, b);
                 const bool c = (cut >> i) & 1u;
-                h = follow(c, a[i], h, b[i]);
-                fa = c ? all<V>(0.0f) : fa * a[i];
+                h = follow(c, a, h, b);
+                fa = c ? all<V>(0.0f) : fa * a;
             }
         }
         h = exchange<V>(s_x, step & 1, w.blocks, w.rank, warp, lane, fa, h, cut != 0);
@@ -620,21 +691,27 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_kernel(const __grid_co
             X *to = out + element(p.out, r.row, r.t);
 #pragma unroll
             for (int i = 0; i < L; ++i) {
-                h = fma(a[i], h, b[i]);
+                Lanes<V> a, rest;
+                coefficients<KIND, V>(kept[i], a, rest);
+                h = fma(a, h, given<KIND, V>(rest, R::value(stage, 0, i, lane)));
                 if (live) *reinterpret_cast<RX *>(to) = pack<X, V>(h.v);
                 to += p.out.stride;
             }
             if (step + 1 < rounds) hand_on<V>(s_x, (step + 1) & 1, w.blocks, w.rank, warp, lane, h);
+            __syncwarp();   // the stage has been read
             continue;
         }
 #pragma unroll
         for (int i = 0; i < L; ++i) {
-            h = follow((cut >> i) & 1u, a[i], h, b[i]);
-            b[i] = h;
+            Lanes<V> a, rest;
+            coefficients<KIND, V>(kept[i], a, rest);
+            h = follow((cut >> i) & 1u, a, h, R::get(stage, i, lane));
+            kept[i] = h;
         }
         if (step + 1 < rounds) hand_on<V>(s_x, (step + 1) & 1, w.blocks, w.rank, warp, lane, h);
+        __syncwarp();   // the stage has been read
         if (live && r.count > 0)
-            walk<L, false>(p.rows, p.out, r, [&](int i, size_t at) { *reinterpret_cast<RX *>(out + at) = pack<X, V>(b[i].v); });
+            walk<L, false>(p.rows, p.out, r, [&](int i, size_t at) { *reinterpret_cast<RX *>(out + at) = pack<X, V>(kept[i].v); });
         if (p.final != nullptr) {
 #pragma unroll
             for (int i = 0; i < L; ++i) {
@@ -642,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_kernel(const __grid_co
                 float *to = state_of(p.rows, p.final, e.row_of(i));
                 if (to != nullptr && live)
 #pragma unroll
-                    for (int k = 0; k < V; ++k) to[w.channel + k] = b[i].v[k];
+                    for (int k = 0; k < V; ++k) to[w.channel + k] = kept[i].v[k];
             }
         }
     }
@@ -658,12 +735,13 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_kernel(const __grid_co
 // h_{t-1} is what the forward call wrote, in its type.  It (and x) is taken
 // from the ring after the exchange, so that registers hold a, dh and r only.
 // ---------------------------------------------------------------------------
-template <typename X, typename G, int V, int KIND, int COPY>
-__global__ void __launch_bounds__(kThreads, 2) gated_scan_backward_kernel(const __grid_constant__ GatedBackwardCall p)
+template <typename X, typename G, int V, int KIND, int COPY, bool MANY>
+__global__ void __launch_bounds__(kThreads, (BackwardRing<X, G, V, KIND, COPY, MANY>::kPerSm))
+ gated_scan_backward_kernel(const __grid_constant__ GatedBackwardCall p)
 {
-    constexpr int L = kBackwardTokens;
     constexpr bool SIGMOID = KIND == kGateSigmoid;
-    using R = Ring<X, G, V, L, SIGMOID ? 3 : 2, COPY>;   // grad, y, x
+    using R = BackwardRing<X, G, V, KIND, COPY, MANY>;   // grad, y, x
+    constexpr int L = R::kTokens;
     using RX = typename R::RX;
     using RG = typename R::RG;
     extern __shared__ __align__(16) char s_ring[];
@@ -750,14 +828,11 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_backward_kernel(const 
             }
             fetch(step + 1);
         }
-        Lanes<V> a[L], d[L], m[SIGMOID ? L : 1];   // decay, dh, r
+        Lanes<V> a[L], rest[SIGMOID ? L : 1], d[L];
 #pragma unroll
         for (int i = 0; i < L; ++i) {
-            const Lanes<V> g = R::gate(stage, i, lane);
+            coefficients<KIND, V>(kept_of<KIND, V>(R::gate(stage, i, lane)), a[i], rest[SIGMOID ? i : 0]);
             d[i] = R::value(stage, 0, i, lane);
-            a[i] = g;
-            if constexpr (KIND == kGateLog) a[i] = exp_decay(g);
-            if constexpr (SIGMOID) sigmoid_decay(g, a[i], m[i]);
         }
         const Edges e = edges_of<L, true>(p.rows, r, lane, in_row);
         const unsigned cut = e.last | e.outside;
@@ -769,11 +844,10 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_backward_kernel(const 
         } else {
 #pragma unroll
             for (int i = 0; i < L; ++i) {
-                if (i >= r.count) a[i] = all<V>(1.0f), d[i] = all<V>(0.0f);
-                if ((e.outside >> i) & 1u) {
-                    a[i] = d[i] = all<V>(0.0f);
-                    if constexpr (SIGMOID) m[i] = all<V>(0.0f);
-                }
+                const bool out = (e.outside >> i) & 1u;
+                if (i >= r.count) a[i] = all<V>(1.0f);
+                if (out) a[i] = all<V>(0.0f);
+                if (i >= r.count || out) d[i] = all<V>(0.0f);
                 if (((e.last >> i) & 1u) != 0 && p.grad_final != nullptr) {
                     const size_t at = static_cast<size_t>(e.row_of(i)) * p.rows.channels + w.channel;
                     if (live)
@@ -793,9 +867,9 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_backward_kernel(const 
         auto gradients = [&](int i, Lanes<V> v, Lanes<V> before, Lanes<V> &gx, Lanes<V> &gg) {
             gx = v;
             if constexpr (SIGMOID) {
-                const Lanes<V> xv = R::value(stage, 2, i, lane);
-                gx = v * m[SIGMOID ? i : 0];
-                gg = (fma(xv, all<V>(-1.0f), before) * (a[i] * m[SIGMOID ? i : 0])) * v;
+                const Lanes<V> x_here = R::value(stage, 2, i, lane), share = rest[SIGMOID ? i : 0];
+                gx = v * share;
+                gg = (fma(x_here, all<V>(-1.0f), before) * (a[i] * share)) * v;
             } else {
                 gg = (KIND == kGateLog ? before * a[i] : before) * v;
             }
@@ -805,9 +879,9 @@ __global__ void __launch_bounds__(kThreads, 2) gated_scan_backward_kernel(const 
             G *to_gate = grad_gate + element(p.grad_gate, r.row, r.t);
 #pragma unroll
             for (int i = 0; i < L; ++i) {
+                Lanes<V> gx, gg;
                 const Lanes<V> v = d[i] + f;
                 f = a[i] * v;
-                Lanes<V> gx, gg;
                 gradients(i, v, R::value(stage, 1, i, lane), gx, gg);
                 if (live) {
                     *reinterpret_cast<RX *>(to_x) = pack<X, V>(gx.v);
@@ -860,9 +934,9 @@ __global__ void __launch_bounds__(256) gated_step_kernel(const __grid_constant__
     X *out = static_cast<X *>(p.out.data) + r * p.out.row_stride + c;
     const X *x = static_cast<const X *>(p.x.data) + r * p.x.row_stride + c;
     const G *gate = static_cast<const G *>(p.gate.data) + r * p.gate.row_stride + c;
-    Lanes<V> a, b;
-    coefficients<KIND, V>(lanes_of<G, V>(*reinterpret_cast<const typename Raw<G, V>::type *>(gate)),
-                          lanes_of<X, V>(*reinterpret_cast<const typename Raw<X, V>::type *>(x)), a, b);
+    Lanes<V> a, rest;
+    coefficients<KIND, V>(kept_of<KIND, V>(lanes_of<G, V>(*reinterpret_cast<const typename Raw<G, V>::type *>(gate))), a, rest);
+    Lanes<V> b = given<KIND, V>(rest, lanes_of<X, V>(*reinterpret_cast<const typename Raw<X, V>::type *>(x)));
     const float *from = state_of(p.rows, p.initial, r);
     float *to = state_of(p.rows, p.final, r);
     if (from != nullptr)
@@ -898,10 +972,10 @@ struct Width {
 // Spans and blocks per cluster.  Rows are spread first; a span's rows are then
 // spread over more blocks while the grid leaves places on the GPU empty and
 // every block has a round's tokens.
-inline void plan(GatedRows &rows, int per_lane, int tokens_per_warp, int sms)
+inline void plan(GatedRows &rows, int per_lane, int tokens_per_warp, int places_per_sm, int sms)
 {
     const size_t all = rows.all(), groups = (static_cast<size_t>(rows.channels) + 32 * per_lane - 1) / (32 * per_lane);
-    const size_t places = static_cast<size_t>(sms) * 2, tile = static_cast<size_t>(kWarps) * tokens_per_warp;
+    const size_t places = static_cast<size_t>(sms) * places_per_sm, tile = static_cast<size_t>(kWarps) * tokens_per_warp;
     size_t spans = (4 * places + groups - 1) / groups;
     spans = spans < static_cast<size_t>(rows.rows) ? spans : static_cast<size_t>(rows.rows);
     const size_t most = (all + tile - 1) / tile;   // spans of a round at least
@@ -912,6 +986,9 @@ inline void plan(GatedRows &rows, int per_lane, int tokens_per_warp, int sms)
     rows.groups = static_cast<unsigned>(groups), rows.spans = static_cast<unsigned>(spans);
     rows.blocks = static_cast<int>(blocks);
 }
+
+// Whether rows are long enough for many tokens per round.
+inline bool many_tokens(const GatedRows &rows) { return rows.all() / static_cast<unsigned>(rows.rows > 0 ? rows.rows : 1) >= 1024; }
 
 template <typename Call>
 cudaError_t launch_clusters(void (*kernel)(Call), const Call &call, int ring, std::atomic<unsigned long long> &done, cudaStream_t s)
@@ -933,12 +1010,20 @@ cudaError_t launch_clusters(void (*kernel)(Call), const Call &call, int ring, st
     return cudaLaunchKernelEx(&cfg, kernel, call);
 }
 
-template <typename X, typename G, int V, int KIND, int COPY>
-cudaError_t forward(GatedScanCall call, int sms, cudaStream_t s)
+template <typename X, typename G, int V, int KIND, int COPY, bool MANY>
+cudaError_t forward_of(GatedScanCall call, int sms, cudaStream_t s)
 {
     static std::atomic<unsigned long long> done;
-    plan(call.rows, V, kForwardTokens, sms);
-    return launch_clusters(gated_scan_kernel<X, G, V, KIND, COPY>, call, Ring<X, G, V, kForwardTokens, 1, COPY>::kBytes, done, s);
+    using R = ForwardRing<X, G, V, COPY, MANY>;
+    plan(call.rows, V, R::kTokens, R::kPerSm, sms);
+    return launch_clusters(gated_scan_kernel<X, G, V, KIND, COPY, MANY>, call, R::kBytes, done, s);
+}
+template <typename X, typename G, int V, int KIND, int COPY>
+cudaError_t forward(const GatedScanCall &call, int sms, cudaStream_t s)
+{
+    if constexpr (COPY > 0)
+        if (many_tokens(call.rows)) return forward_of<X, G, V, KIND, COPY, true>(call, sms, s);
+    return forward_of<X, G, V, KIND, COPY, false>(call, sms, s);
 }
 template <typename X, typename G, int V, int KIND>
 cudaError_t step(const GatedScanCall &call, cudaStream_t s)
@@ -972,13 +1057,20 @@ cudaError_t forward_any(const GatedScanCall &call, int sms, cudaStream_t s)
     return forward_kind<X, G, kGateSigmoid>(call, sms, s);
 }
 
-template <typename X, typename G, int V, int KIND, int COPY>
-cudaError_t backward(GatedBackwardCall call, int sms, cudaStream_t s)
+template <typename X, typename G, int V, int KIND, int COPY, bool MANY>
+cudaError_t backward_of(GatedBackwardCall call, int sms, cudaStream_t s)
 {
     static std::atomic<unsigned long long> done;
-    plan(call.rows, V, kBackwardTokens, sms);
-    return launch_clusters(gated_scan_backward_kernel<X, G, V, KIND, COPY>, call,
-                           Ring<X, G, V, kBackwardTokens, KIND == kGateSigmoid ? 3 : 2, COPY>::kBytes, done, s);
+    using R = BackwardRing<X, G, V, KIND, COPY, MANY>;
+    plan(call.rows, V, R::kTokens, R::kPerSm, sms);
+    return launch_clusters(gated_scan_backward_kernel<X, G, V, KIND, COPY, MANY>, call, R::kBytes, done, s);
+}
+template <typename X, typename G, int V, int KIND, int COPY>
+cudaError_t backward(const GatedBackwardCall &call, int sms, cudaStream_t s)
+{
+    if constexpr (COPY > 0)
+        if (many_tokens(call.rows)) return backward_of<X, G, V, KIND, COPY, true>(call, sms, s);
+    return backward_of<X, G, V, KIND, COPY, false>(call, sms, s);
 }
 template <typename X, typename G, int KIND>
 cudaError_t backward_kind(const GatedBackwardCall &call, int sms, cudaStream_t s)
