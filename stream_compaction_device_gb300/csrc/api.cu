@@ -517,7 +517,7 @@ devscan_status expert_sort_common(const void *ids, size_t id_size, size_t tokens
     if (written_overlap(written, read)) return DEVSCAN_ERR_INVALID;
     return from_cuda(launch_expert_sort({ids, static_cast<unsigned>(pairs), static_cast<unsigned>(rows),
                                          static_cast<unsigned>(align), static_cast<int>(experts), starts, counts, order,
-                                         places},
+                                         places, false},
                                         id_size == 8, stream));
 }
 

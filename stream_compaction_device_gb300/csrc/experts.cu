@@ -18,116 +18,170 @@ namespace devscan {
 namespace {
 
 // ---------------------------------------------------------------------------
-// Sort.  One cluster of up to eight blocks: its blocks take equal runs of the
+// Sort.  One cluster of up to sixteen blocks: its blocks take equal runs of the
 // pairs, and their warps equal runs of those, so that the order of warps is
 // the order of pairs.  Every warp counts its pairs per expert in shared memory;
 // a column of counts is scanned over the warps by one thread, over the blocks
 // through distributed shared memory, and over the experts by the block.  Then
 // each warp goes through its pairs again: lanes with the same expert find each
-// other (match), their ranks are counted from the mask, and the warp's counter
-// moves on.  No scratch, no global atomics, one launch.
+// other by a ballot per bit of the id, their ranks are counted from the mask,
+// and the warp's counter moves on.  Ids come four per lane at once; where a
+// warp has no more than those, they are read once.  `order` is put together in
+// shared memory and written an expert's run at a time: written pair by pair, 32
+// sectors per instruction, it was what bounded the call.  (Where a block's
+// pairs do not fit there it is written so all the same.)  No scratch, no global
+// atomics, one launch.
 // ---------------------------------------------------------------------------
-constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortMostBlocks = 8;
+constexpr int kSortMostBlocks = 16;
+constexpr int kSortWarps = 32, kSortFewWarps = 8;   // of a block; few, where there are few pairs and experts
+constexpr int kSortAtOnce = 4;   // ids of a lane
 constexpr size_t kSortPairsPerBlock = 4096;   // from where another block is worth it
+constexpr size_t kSortDirect = 2048;          // pairs of a block that are written one by one
+constexpr int kSortSmem = 224 << 10;
 
-template <typename Id>
-__global__ void __launch_bounds__(kSortThreads, 1) expert_sort_kernel(const __grid_constant__ ExpertSortCall p)
+template <typename Id, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, 1) expert_sort_kernel(const __grid_constant__ ExpertSortCall p)
 {
-    extern __shared__ unsigned s_counts[];            // [warp][expert], then the experts' totals and bases
-    unsigned *const s_total = s_counts + kSortWarps * p.experts;
+    constexpr int kThreads = 32 * WARPS;
+    extern __shared__ unsigned s_counts[];            // [warp][expert], then by expert:
+    unsigned *const s_total = s_counts + WARPS * p.experts;
     unsigned *const s_base = s_total + p.experts;     // first row of a segment
     unsigned *const s_filled = s_base + p.experts;    // behind the last row with a pair
-    __shared__ unsigned s_warp[kSortWarps];
+    unsigned *const s_here = s_filled + p.experts;    // first row of this block's pairs
+    unsigned *const s_local = s_here + p.experts;     // their first place in s_order
+    unsigned short *const s_order = reinterpret_cast<unsigned short *>(s_local + p.experts);   // the block's pairs by expert
+    __shared__ unsigned s_warp[WARPS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const unsigned rank = cluster_rank(), blocks = gridDim.x;
+    const bool local = p.local;   // the block's pairs fit in s_order
     const Id *ids = static_cast<const Id *>(p.ids);
     const unsigned experts = static_cast<unsigned>(p.experts);
-    const unsigned each = (p.pairs + blocks * kSortThreads - 1) / (blocks * kSortThreads) * 32;   // pairs of a warp
-    const unsigned begin = (rank * kSortWarps + warp) * each;
+    const unsigned each = (p.pairs + blocks * kThreads - 1) / (blocks * kThreads) * 32;   // pairs of a warp
+    const unsigned begin = (rank * WARPS + warp) * each;
     const unsigned end = begin < p.pairs ? (p.pairs - begin < each ? p.pairs : begin + each) : begin;
     unsigned *const mine = s_counts + warp * experts;
-    auto expert_of = [&](unsigned i) {   // `experts` where there is none
-        if (i >= end) return experts;
-        const long long id = static_cast<long long>(ids[i]);
-        return id >= 0 && id < static_cast<long long>(experts) ? static_cast<unsigned>(id) : experts;
+    unsigned e[kSortAtOnce];   // experts of pairs i0 + 32 j + lane; `experts` where there is none
+    auto load = [&](unsigned i0) {
+        Id id[kSortAtOnce];
+#pragma unroll
+        for (int j = 0; j < kSortAtOnce; ++j) {
+            const unsigned i = i0 + 32 * j + lane;
+            id[j] = i < end ? ids[i] : static_cast<Id>(-1);
+        }
+#pragma unroll
+        for (int j = 0; j < kSortAtOnce; ++j)
+            e[j] = id[j] >= 0 && id[j] < static_cast<Id>(experts) ? static_cast<unsigned>(id[j]) : experts;
     };
 
-    for (unsigned e = lane; e < experts; e += 32) mine[e] = 0;
+    for (unsigned k = lane; k < experts; k += 32) mine[k] = 0;
     __syncwarp();
-    for (unsigned i = begin + lane; i < end; i += 32) {
-        const unsigned e = expert_of(i);
-        if (e < experts) atomicAdd(&mine[e], 1u);
-    }
-    __syncthreads();
-    unsigned total = 0;
-    const bool column = static_cast<unsigned>(tid) < experts;
-    if (column) {
-#pragma unroll 8
-        for (int w = 0; w < kSortWarps; ++w) {
-            const unsigned c = s_counts[w * experts + tid];
-            s_counts[w * experts + tid] = total;
-            total += c;
-        }
-        s_total[tid] = total;
-    }
-    unsigned before = 0, all = total;
-    if (blocks > 1) {
-        cluster_sync();   // the totals are there
-        if (column) {
-            all = 0;
-            for (unsigned q = 0; q < blocks; ++q) {
-                const unsigned c = ld_cluster(cluster_addr(&s_total[tid], q));
-                before += q < rank ? c : 0u;
-                all += c;
+    const bool once = each <= 32 * kSortAtOnce;
+    unsigned used = 0;
+    // One copy of the loop for counting and for placing: this is code that runs
+    // a few times, and fetching it for the first time is what small calls pay.
+#pragma unroll 1
+    for (int placing = 0; placing < 2; ++placing) {
+#pragma unroll 1
+        for (unsigned i0 = begin; i0 < end; i0 += 32 * kSortAtOnce) {
+            if (!placing || !once) load(i0);
+            if (!placing) {
+#pragma unroll
+                for (int j = 0; j < kSortAtOnce; ++j)
+                    if (e[j] < experts) atomicAdd(&mine[e[j]], 1u);
+                continue;
+            }
+            unsigned all_same[kSortAtOnce];
+#pragma unroll
+            for (int j = 0; j < kSortAtOnce; ++j) all_same[j] = kFullMask;
+#pragma unroll 1
+            for (unsigned bit = 1; bit <= experts; bit *= 2)
+#pragma unroll
+                for (int j = 0; j < kSortAtOnce; ++j) {
+                    const unsigned with = __ballot_sync(kFullMask, (e[j] & bit) != 0);
+                    all_same[j] &= (e[j] & bit) != 0 ? with : ~with;
+                }
+#pragma unroll
+            for (int j = 0; j < kSortAtOnce; ++j) {
+                const unsigned i = i0 + 32 * j + lane, same = all_same[j];
+                if (i0 + 32 * j >= end) break;
+                const unsigned ahead = __popc(same & ((1u << lane) - 1u));
+                const unsigned place = e[j] < experts ? mine[e[j]] + ahead : p.rows;
+                __syncwarp();
+                if (e[j] < experts && ahead == 0) mine[e[j]] += __popc(same);
+                __syncwarp();
+                if (i < end) p.places[i] = place < p.rows ? static_cast<int32_t>(place) : -1;
+                if (local) {
+                    if (e[j] < experts) s_order[place - s_here[e[j]] + s_local[e[j]]] = static_cast<unsigned short>(i - rank * WARPS * each);
+                } else if (place < p.rows) {
+                    p.order[place] = static_cast<int32_t>(i);
+                }
             }
         }
-    }
-    // the segments' first rows: a scan of the rounded counts over the experts
-    const unsigned room = (all + p.align - 1) / p.align * p.align;
-    unsigned upto = room;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const unsigned u = __shfl_up_sync(kFullMask, upto, d);
-        if (lane >= d) upto += u;
-    }
-    if (lane == 31) s_warp[warp] = upto;
-    __syncthreads();
-    unsigned wt = s_warp[lane], wi = wt;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const unsigned u = __shfl_up_sync(kFullMask, wi, d);
-        if (lane >= d) wi += u;
-    }
-    const unsigned used = __shfl_sync(kFullMask, wi, 31);
-    const unsigned base = __shfl_sync(kFullMask, wi - wt, warp) + upto - room;
-    if (column) {
-        s_base[tid] = base;
-        s_filled[tid] = base + all;
+        if (placing) break;
+        __syncthreads();
+        // a thread has an expert's counts; there are no more experts than threads
+        const bool column = static_cast<unsigned>(tid) < experts;
+        unsigned total = 0, before = 0;
 #pragma unroll 8
-        for (int w = 0; w < kSortWarps; ++w) s_counts[w * experts + tid] += base + before;
-        if (rank == 0) p.starts[tid] = static_cast<int32_t>(base), p.counts[tid] = static_cast<int32_t>(all);
+        for (int w = 0; w < WARPS; ++w) total += column ? s_counts[w * experts + tid] : 0u;
+        unsigned all = total;
+        if (column) s_total[tid] = total;
+        if (blocks > 1) {
+            cluster_sync();   // the totals are there
+            all = 0;
+#pragma unroll 4
+            for (unsigned q = 0; q < blocks; ++q) {
+                const unsigned theirs = column ? ld_cluster(cluster_addr(&s_total[tid], q)) : 0u;
+                before += q < rank ? theirs : 0u;
+                all += theirs;
+            }
+        }
+        // the segments' first rows, and the block's own: scans over the experts
+        const unsigned room = (all + p.align - 1) / p.align * p.align;
+        const unsigned base = block_excl_scan<kThreads>(room, s_warp, tid, used);
+        unsigned place0 = 0;
+        if (local) {
+            unsigned in_block = 0;
+            __syncthreads();
+            place0 = block_excl_scan<kThreads>(total, s_warp, tid, in_block);
+        }
+        if (column) {
+            s_base[tid] = base;
+            s_filled[tid] = base + all;
+            s_here[tid] = base + before;
+            s_local[tid] = place0;
+            unsigned upto = base + before;
+#pragma unroll 1
+            for (int w0 = 0; w0 < WARPS; w0 += 8) {
+                unsigned count[8];
+#pragma unroll
+                for (int w = 0; w < 8; ++w) count[w] = s_counts[(w0 + w) * experts + tid];
+#pragma unroll
+                for (int w = 0; w < 8; ++w) {
+                    s_counts[(w0 + w) * experts + tid] = upto;
+                    upto += count[w];
+                }
+            }
+            if (rank == 0) p.starts[tid] = static_cast<int32_t>(base), p.counts[tid] = static_cast<int32_t>(all);
+        }
+        if (rank == 0 && tid == 0) p.starts[experts] = static_cast<int32_t>(used);
+        __syncthreads();
     }
-    if (rank == 0 && tid == 0) p.starts[experts] = static_cast<int32_t>(used);
-    __syncthreads();
-
-    for (unsigned i0 = begin; i0 < end; i0 += 32) {
-        const unsigned i = i0 + lane, e = expert_of(i);
-        const unsigned same = __match_any_sync(kFullMask, e);
-        const unsigned ahead = __popc(same & ((1u << lane) - 1u));
-        const unsigned place = e < experts ? mine[e] + ahead : p.rows;
-        __syncwarp();
-        if (e < experts && ahead == 0) mine[e] += __popc(same);
-        __syncwarp();
-        if (i < end) p.places[i] = place < p.rows ? static_cast<int32_t>(place) : -1;
-        if (place < p.rows) p.order[place] = static_cast<int32_t>(i);
+    if (local) {
+        __syncthreads();
+        for (unsigned k = warp; k < experts; k += WARPS)
+            for (unsigned i = lane; i < s_total[k]; i += 32) {
+                const unsigned row = s_here[k] + i;
+                if (row < p.rows) p.order[row] = static_cast<int32_t>(rank * WARPS * each + s_order[s_local[k] + i]);
+            }
     }
     // rows without a pair: up to the end of their segment, and behind the last one
-    for (unsigned e = rank * kSortWarps + warp; e < experts; e += blocks * kSortWarps) {
+    for (unsigned e = rank * WARPS + warp; e < experts; e += blocks * WARPS) {
         unsigned to = e + 1 < experts ? s_base[e + 1] : used;
         to = to < p.rows ? to : p.rows;
         for (unsigned r = s_filled[e] + lane; r < to; r += 32) p.order[r] = kOrderPadding;
     }
-    for (unsigned r = used + rank * kSortThreads + tid; r < p.rows; r += blocks * kSortThreads) p.order[r] = kOrderBehind;
+    for (unsigned r = used + rank * kThreads + tid; r < p.rows; r += blocks * kThreads) p.order[r] = kOrderBehind;
     if (blocks > 1) cluster_sync();   // nobody leaves while its totals may be read
 }
 
@@ -287,7 +341,7 @@ __global__ void __launch_bounds__(32 * kBackWarps) expert_combine_backward_kerne
 #pragma unroll
                 for (int j = 0; j < kAtOnce; ++j)
                     if (place[j] < p.rows)
-                        r[j] = __ldcs(reinterpret_cast<const R *>(static_cast<const T *>(p.y) + place[j] * p.y_stride + c));
+                        r[j] = *reinterpret_cast<const R *>(static_cast<const T *>(p.y) + place[j] * p.y_stride + c);
             unpack<T, V>(*reinterpret_cast<const R *>(grad + c), g);
 #pragma unroll
             for (int j = 0; j < kAtOnce; ++j) {
@@ -300,7 +354,7 @@ __global__ void __launch_bounds__(32 * kBackWarps) expert_combine_backward_kerne
                 }
 #pragma unroll
                 for (int i = 0; i < V; ++i) v[i] = weight[j] * g[i];
-                __stcs(reinterpret_cast<R *>(static_cast<T *>(p.grad_y) + place[j] * p.grad_y_stride + c), pack<T, V>(v));
+                *reinterpret_cast<R *>(static_cast<T *>(p.grad_y) + place[j] * p.grad_y_stride + c) = pack<T, V>(v);
             }
         }
         if (p.grad_weights == nullptr) continue;
@@ -320,6 +374,41 @@ __global__ void __launch_bounds__(32 * kBackWarps) expert_combine_backward_kerne
             p.grad_weights[pair0 + k0 + lane] = static_cast<unsigned>(place_here) < p.rows ? all : 0.0f;
         }
     }
+}
+
+template <typename Id, int WARPS> cudaError_t sort(ExpertSortCall call, cudaStream_t s)
+{
+    static std::atomic<unsigned long long> done, wide;
+    auto *kernel = expert_sort_kernel<Id, WARPS>;
+    cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), kSortSmem, done);
+    if (e != cudaSuccess) return e;
+    unsigned blocks = 1;
+    while (blocks < kSortMostBlocks && static_cast<size_t>(call.pairs) > blocks * kSortPairsPerBlock) blocks *= 2;
+    if (blocks > 8) {   // more than the portable size
+        int dev = 0;
+        if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+        if ((wide.load() >> (dev & 63) & 1) == 0) {
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e != cudaSuccess) return e;
+            wide.fetch_or(1ull << (dev & 63));
+        }
+    }
+    const size_t threads = 32 * WARPS, counts = (WARPS + 5) * static_cast<size_t>(call.experts) * sizeof(unsigned);
+    const size_t each = (static_cast<size_t>(call.pairs) + blocks * threads - 1) / (blocks * threads) * threads;   // a block's
+    call.local = each > kSortDirect && each <= 65536 && counts + 2 * each <= static_cast<size_t>(kSortSmem);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = counts + (call.local ? 2 * each : 0);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = blocks;   // one cluster spans the grid
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, call);
 }
 
 bool wide_rows(const void *p, size_t stride, size_t width, size_t size)
@@ -368,29 +457,12 @@ cudaError_t combine_backward_any(const ExpertCombineBackwardCall &call, cudaStre
 
 }  // namespace
 
-cudaError_t launch_expert_sort(const ExpertSortCall &call, bool wide_ids, cudaStream_t s)
+cudaError_t launch_expert_sort(ExpertSortCall call, bool wide_ids, cudaStream_t s)
 {
-    static std::atomic<unsigned long long> done[2];
-    const int smem = static_cast<int>((kSortWarps + 3) * static_cast<size_t>(call.experts) * sizeof(unsigned));
-    const int most = static_cast<int>((kSortWarps + 3) * static_cast<size_t>(kMostExperts) * sizeof(unsigned));
-    auto *kernel = wide_ids ? expert_sort_kernel<int64_t> : expert_sort_kernel<int32_t>;
-    const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), most, done[wide_ids]);
-    if (e != cudaSuccess) return e;
-    unsigned blocks = 1;
-    while (blocks < kSortMostBlocks && static_cast<size_t>(call.pairs) > blocks * kSortPairsPerBlock) blocks *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(kSortThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = blocks;   // one cluster spans the grid
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, call);
+    constexpr size_t few_pairs = 32 * kSortFewWarps * kSortAtOnce;
+    const bool few = call.pairs <= few_pairs && call.experts <= 32 * kSortFewWarps;
+    if (wide_ids) return few ? sort<int64_t, kSortFewWarps>(call, s) : sort<int64_t, kSortWarps>(call, s);
+    return few ? sort<int32_t, kSortFewWarps>(call, s) : sort<int32_t, kSortWarps>(call, s);
 }
 
 cudaError_t launch_expert_dispatch(const ExpertMoveCall &call, cudaStream_t s)

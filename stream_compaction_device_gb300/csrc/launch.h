@@ -244,6 +244,7 @@ struct ExpertSortCall {
     unsigned pairs, rows, align;
     int experts;
     int32_t *starts, *counts, *order, *places;
+    bool local;   // set by the launch
 };
 struct ExpertMoveCall {   // strides in bytes
     const void *from;
@@ -277,7 +278,7 @@ struct ExpertCombineBackwardCall {
     size_t grad_y_stride;
     float *grad_weights;
 };
-cudaError_t launch_expert_sort(const ExpertSortCall &call, bool wide_ids, cudaStream_t s);
+cudaError_t launch_expert_sort(ExpertSortCall call, bool wide_ids, cudaStream_t s);
 cudaError_t launch_expert_dispatch(const ExpertMoveCall &call, cudaStream_t s);
 cudaError_t launch_expert_combine(ValueType type, const ExpertCombineCall &call, cudaStream_t s);
 cudaError_t launch_expert_combine_backward(ValueType type, const ExpertCombineBackwardCall &call, cudaStream_t s);
