@@ -9,6 +9,8 @@ array to the device, scans it and copies the result back.
 """
 from __future__ import annotations
 
+import array
+
 import torch
 
 from . import _lib
@@ -487,6 +489,7 @@ def sample_tokens(logits: torch.Tensor, noise: torch.Tensor | None = None, tempe
 
 
 _VALUES = {torch.float32: "f32", torch.float16: "f16", torch.bfloat16: "bf16"}
+_F32, _I32 = torch.float32, torch.int32
 
 
 def _value_suffix(t: torch.Tensor) -> str:
@@ -496,34 +499,52 @@ def _value_suffix(t: torch.Tensor) -> str:
     return suffix
 
 
-def _here(t: torch.Tensor, name: str) -> torch.Tensor:
-    """A CUDA tensor of the current device, whose stream the call takes."""
-    if not t.is_cuda:
+def _device_of(t: torch.Tensor, name: str) -> int:
+    """The device of a call that begins with that tensor: the current one,
+    whose stream it takes."""
+    here = t.get_device()
+    if here < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.get_device() != torch._C._cuda_getDevice():
+    if here != torch._C._cuda_getDevice():
         raise ValueError(f"{name} must be on the current device")
-    return t
+    return here
 
 
-def _token_array(t: torch.Tensor, name: str, shape, dtype):
+def _vector(t, name: str, dtype: torch.dtype, size: int, here: int):
+    """Address of a contiguous tensor of that type, size and device; None for
+    None."""
+    if t is None:
+        return None
+    if t.get_device() == here and t.dtype is dtype and t.numel() == size and t.is_contiguous():
+        return t.data_ptr()
+    _device_of(t, name)
+    _check_vector(t, name, dtype, size)
+    raise ValueError(f"{name} must be on the current device")
+
+
+def _token_array(t: torch.Tensor, name: str, shape, dtype, here: int):
     """(address, row stride, token stride) of a tensor [rows, tokens, channels]
     or [tokens, channels] with neighbouring channels."""
-    _here(t, name)
+    strides = t.stride()
+    if t.get_device() != here:
+        raise ValueError(f"{name} must be a CUDA tensor on the current device")
     if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
-    strides = t.stride()
     if strides[-1] != 1 and shape[-1] != 1:
         raise ValueError(f"{name}'s channels must be contiguous")
     return t.data_ptr(), strides[0] if len(strides) == 3 else 0, strides[-2]
 
 
 def _gated_rows(x: torch.Tensor, gate: torch.Tensor, starts, kind: str):
-    """(rows, tokens, channels, whether the gates are fp32 beside 16 bits)."""
-    if kind not in _lib.GATES:
+    """(rows, tokens, channels, the kind's number, whether the gates are fp32
+    beside 16 bits)."""
+    number = _lib.GATES.get(kind)
+    if number is None:
         raise ValueError(f"unknown kind {kind!r} (decay, log, sigmoid)")
-    if gate.dtype != x.dtype and gate.dtype != torch.float32:
+    wide = gate.dtype is not x.dtype
+    if wide and gate.dtype is not _F32:
         raise TypeError("gate must be float32 or of x's type")
     if x.dim() == 3:
         if starts is not None:
@@ -540,17 +561,18 @@ def _gated_rows(x: torch.Tensor, gate: torch.Tensor, starts, kind: str):
         raise ValueError("x must be [rows, tokens, channels] or [tokens, channels]")
     if channels < 1:
         raise ValueError("x must have channels")
-    return rows, tokens, channels, gate.dtype != x.dtype
+    return rows, tokens, channels, number, wide
 
 
-def _states(t, name: str, channels: int, pool=None):
+def _states(t, name: str, channels: int, pool: int, here: int):
     """Address of fp32 states [pool, channels]; None for None."""
     if t is None:
         return None
-    _here(t, name)
-    if t.dim() != 2 or t.shape[1] != channels or (pool is not None and t.shape[0] != pool) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous [{'states' if pool is None else pool}, {channels}]")
-    if t.dtype != torch.float32:
+    if t.get_device() != here:
+        raise ValueError(f"{name} must be a CUDA tensor on the current device")
+    if t.dim() != 2 or t.shape[0] != pool or t.shape[1] != channels or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [{pool}, {channels}]")
+    if t.dtype is not _F32:
         raise TypeError(f"{name} must be float32")
     return t.data_ptr()
 
@@ -575,10 +597,11 @@ def gated_scan(x: torch.Tensor, gate: torch.Tensor, starts: torch.Tensor | None 
     ``initial`` itself; without ``final``, rows with slots leave their states in
     ``initial``, and others in a new tensor."""
     suffix = _value_suffix(x)
-    rows, tokens, channels, wide = _gated_rows(x, gate, starts, kind)
+    here = _device_of(x, "x")
+    rows, tokens, channels, number, wide = _gated_rows(x, gate, starts, kind)
     if final is None:
         if slots is None:
-            final = torch.empty(rows, channels, dtype=torch.float32, device=x.device)
+            final = torch.empty(rows, channels, dtype=_F32, device=x.device)
         elif initial is None:
             raise ValueError("slots need initial or final to point into")
         else:
@@ -586,18 +609,17 @@ def gated_scan(x: torch.Tensor, gate: torch.Tensor, starts: torch.Tensor | None 
     pool = final.shape[0] if final.dim() else 0
     if slots is None and pool != rows:
         raise ValueError(f"final must hold {rows} states")
+    shape, dtype = x.shape, x.dtype
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    shape, i32 = x.shape, torch.int32
-    name = "gated_scan_" + suffix
-    status = getattr(load(), name)(
-        *_token_array(x, "x", shape, x.dtype), *_token_array(gate, "gate", shape, gate.dtype), wide, rows, tokens,
-        channels, None if starts is None else _check_vector(_here(starts, "starts"), "starts", i32, rows + 1),
-        _states(initial, "initial", channels, pool),
-        None if slots is None else _check_vector(_here(slots, "slots"), "slots", i32, rows), pool, _lib.GATES[kind],
-        *_token_array(out, "out", shape, x.dtype), _states(final, "final", channels), _stream_handle(stream))
+        out = torch.empty(shape, dtype=dtype, device=x.device)
+    status = getattr(load(), "gated_scan_" + suffix)(
+        *_token_array(x, "x", shape, dtype, here), *_token_array(gate, "gate", shape, gate.dtype, here), wide, rows,
+        tokens, channels, _vector(starts, "starts", _I32, rows + 1, here),
+        _states(initial, "initial", channels, pool, here), _vector(slots, "slots", _I32, rows, here), pool, number,
+        *_token_array(out, "out", shape, dtype, here), _states(final, "final", channels, pool, here),
+        _stream_handle(stream))
     if status:
-        _lib.check(status, name)
+        _lib.check(status, "gated_scan_" + suffix)
     return out, final
 
 
@@ -614,29 +636,28 @@ def gated_scan_backward(grad: torch.Tensor, x: torch.Tensor | None, gate: torch.
     grad_initial), the last None where there is neither ``initial`` nor a
     tensor for it."""
     suffix = _value_suffix(y)
-    rows, tokens, channels, wide = _gated_rows(y, gate, starts, kind)
-    shape = y.shape
+    here = _device_of(y, "y")
+    rows, tokens, channels, number, wide = _gated_rows(y, gate, starts, kind)
+    shape, dtype, device = y.shape, y.dtype, y.device
     if kind == "sigmoid" and x is None:
         raise ValueError("sigmoid needs x")
-    new = lambda *size, dtype: torch.empty(*size, dtype=dtype, device=y.device)  # noqa: E731
     if grad_x is None:
-        grad_x = new(shape, dtype=y.dtype)
+        grad_x = torch.empty(shape, dtype=dtype, device=device)
     if grad_gate is None:
-        grad_gate = new(shape, dtype=gate.dtype)
+        grad_gate = torch.empty(shape, dtype=gate.dtype, device=device)
     if grad_initial is None and initial is not None:
-        grad_initial = new(rows, channels, dtype=torch.float32)
-    name = "gated_scan_backward_" + suffix
-    status = getattr(load(), name)(
-        *_token_array(grad, "grad", shape, y.dtype),
-        *((None, 0, 0) if x is None else _token_array(x, "x", shape, y.dtype)),
-        *_token_array(gate, "gate", shape, gate.dtype), wide, *_token_array(y, "y", shape, y.dtype), rows, tokens,
-        channels, None if starts is None else _check_vector(_here(starts, "starts"), "starts", torch.int32, rows + 1),
-        _states(initial, "initial", channels, rows), _states(grad_final, "grad_final", channels, rows),
-        _lib.GATES[kind], *_token_array(grad_x, "grad_x", shape, y.dtype),
-        *_token_array(grad_gate, "grad_gate", shape, gate.dtype),
-        _states(grad_initial, "grad_initial", channels, rows), _stream_handle(stream))
+        grad_initial = torch.empty(rows, channels, dtype=_F32, device=device)
+    status = getattr(load(), "gated_scan_backward_" + suffix)(
+        *_token_array(grad, "grad", shape, dtype, here),
+        *((None, 0, 0) if x is None else _token_array(x, "x", shape, dtype, here)),
+        *_token_array(gate, "gate", shape, gate.dtype, here), wide, *_token_array(y, "y", shape, dtype, here), rows,
+        tokens, channels, _vector(starts, "starts", _I32, rows + 1, here),
+        _states(initial, "initial", channels, rows, here), _states(grad_final, "grad_final", channels, rows, here),
+        number, *_token_array(grad_x, "grad_x", shape, dtype, here),
+        *_token_array(grad_gate, "grad_gate", shape, gate.dtype, here),
+        _states(grad_initial, "grad_initial", channels, rows, here), _stream_handle(stream))
     if status:
-        _lib.check(status, name)
+        _lib.check(status, "gated_scan_backward_" + suffix)
     return grad_x, grad_gate, grad_initial
 
 
@@ -655,7 +676,7 @@ def expert_sort(experts: torch.Tensor, num_experts: int, align: int = 1, rows: i
     every pair its row (-1 where its id is outside 0 .. num_experts - 1).
     ``rows`` is the number of rows that there are (by default what the pairs
     can need at most); pairs beyond have no place."""
-    _here(experts, "experts")
+    here = _device_of(experts, "experts")
     name = _IDS.get(experts.dtype)
     if name is None:
         raise TypeError("experts must be int32 or int64")
@@ -671,42 +692,48 @@ def expert_sort(experts: torch.Tensor, num_experts: int, align: int = 1, rows: i
     rows = int(rows)
     if rows < 0:
         raise ValueError("rows must not be negative")
-    i32 = torch.int32
-    new = lambda *size: torch.empty(size, dtype=i32, device=experts.device)  # noqa: E731
-    starts = new(num_experts + 1) if starts is None else starts
-    counts = new(num_experts) if counts is None else counts
-    order = new(rows) if order is None else order
-    places = new(tokens, choices) if places is None else places
-    if places.shape != experts.shape:
+    device, empty = experts.device, torch.empty
+    if starts is None:
+        starts = empty(num_experts + 1, dtype=_I32, device=device)
+    if counts is None:
+        counts = empty(num_experts, dtype=_I32, device=device)
+    if order is None:
+        order = empty(rows, dtype=_I32, device=device)
+    if places is None:
+        places = empty(tokens, choices, dtype=_I32, device=device)
+    elif places.shape != experts.shape:
         raise ValueError("places must have the shape of experts")
     status = getattr(load(), name)(
         experts.data_ptr(), tokens, choices, num_experts, align, rows,
-        _check_vector(_here(starts, "starts"), "starts", i32, num_experts + 1),
-        _check_vector(_here(counts, "counts"), "counts", i32, num_experts),
-        _check_vector(_here(order, "order"), "order", i32, rows),
-        _check_vector(_here(places, "places"), "places", i32, pairs), _stream_handle(stream))
+        _vector(starts, "starts", _I32, num_experts + 1, here), _vector(counts, "counts", _I32, num_experts, here),
+        _vector(order, "order", _I32, rows, here), _vector(places, "places", _I32, pairs, here),
+        _stream_handle(stream))
     if status:
         _lib.check(status, name)
     return starts, counts, order, places
 
 
-def _check_rows(t: torch.Tensor, name: str, rows: int, width: int, dtype: torch.dtype) -> int:
-    """A matrix of that size on the current device; returns its row stride."""
-    stride = _check_matrix(_here(t, name), name)
+def _check_rows(t: torch.Tensor, name: str, rows: int, width: int, dtype: torch.dtype, here: int) -> int:
+    """A matrix of that size and device; returns its row stride."""
+    if t.get_device() != here:
+        raise ValueError(f"{name} must be a CUDA tensor on the current device")
+    stride = _check_matrix(t, name)
     if t.shape[0] != rows or t.shape[1] != width:
         raise ValueError(f"{name} must be [{rows}, {width}]")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
     return stride
 
 
-def _check_places(places: torch.Tensor):
-    _here(places, "places")
-    if places.dim() != 2 or not places.is_contiguous() or places.dtype != torch.int32:
+def _check_places(places: torch.Tensor, here: int):
+    if places.dim() != 2 or places.dtype is not _I32 or not places.is_contiguous():
         raise ValueError("places must be a contiguous int32 [tokens, choices]")
-    if places.shape[1] < 1:
+    if places.get_device() != here:
+        raise ValueError("places must be on the current device")
+    tokens, choices = places.shape
+    if choices < 1:
         raise ValueError("places must hold a choice per token")
-    return places.shape
+    return tokens, choices
 
 
 def expert_dispatch(x: torch.Tensor, places: torch.Tensor, order: torch.Tensor, out: torch.Tensor | None = None,
@@ -716,17 +743,17 @@ def expert_dispatch(x: torch.Tensor, places: torch.Tensor, order: torch.Tensor, 
     behind the last segment are left as they were (in a new tensor: whatever is
     there).  Returns ``out`` [rows, width].  The gradient of x is
     ``expert_combine`` of out's, without weights."""
-    tokens, choices = _check_places(places)
+    here = _device_of(x, "x")
+    tokens, choices = _check_places(places, here)
     if x.dim() != 2 or x.shape[1] < 1:
         raise ValueError("x must be [tokens, width]")
-    width, rows, size = x.shape[1], order.numel(), x.element_size()
-    stride = _check_rows(x, "x", tokens, width, x.dtype)
+    width, rows, size, dtype = x.shape[1], order.numel(), x.element_size(), x.dtype
     if out is None:
-        out = torch.empty(rows, width, dtype=x.dtype, device=x.device)
+        out = torch.empty(rows, width, dtype=dtype, device=x.device)
     status = load().expert_dispatch(
-        x.data_ptr(), stride * size, width * size, tokens, choices, places.data_ptr(), rows,
-        _check_vector(_here(order, "order"), "order", torch.int32, rows), out.data_ptr(),
-        _check_rows(out, "out", rows, width, x.dtype) * size, _stream_handle(stream))
+        x.data_ptr(), _check_rows(x, "x", tokens, width, dtype, here) * size, width * size, tokens, choices,
+        places.data_ptr(), rows, _vector(order, "order", _I32, rows, here), out.data_ptr(),
+        _check_rows(out, "out", rows, width, dtype, here) * size, _stream_handle(stream))
     if status:
         _lib.check(status, "expert_dispatch")
     return out
@@ -739,21 +766,20 @@ def expert_combine(y: torch.Tensor, places: torch.Tensor, weights: torch.Tensor 
     width] (float32, float16 or bfloat16) at its ``places``, summed in fp32.  A
     token without any place gets 0."""
     suffix = _value_suffix(y)
-    tokens, choices = _check_places(places)
+    here = _device_of(y, "y")
+    tokens, choices = _check_places(places, here)
     if y.dim() != 2 or y.shape[1] < 1:
         raise ValueError("y must be [rows, width]")
     rows, width = y.shape
-    stride = _check_rows(y, "y", rows, width, y.dtype)
+    dtype = y.dtype
     if out is None:
-        out = torch.empty(tokens, width, dtype=y.dtype, device=y.device)
-    name = "expert_combine_" + suffix
-    status = getattr(load(), name)(
-        y.data_ptr(), stride, rows, tokens, choices, width, places.data_ptr(),
-        None if weights is None else _check_vector(_here(weights, "weights"), "weights", torch.float32,
-                                                   tokens * choices),
-        out.data_ptr(), _check_rows(out, "out", tokens, width, y.dtype), _stream_handle(stream))
+        out = torch.empty(tokens, width, dtype=dtype, device=y.device)
+    status = getattr(load(), "expert_combine_" + suffix)(
+        y.data_ptr(), _check_rows(y, "y", rows, width, dtype, here), rows, tokens, choices, width, places.data_ptr(),
+        _vector(weights, "weights", _F32, tokens * choices, here), out.data_ptr(),
+        _check_rows(out, "out", tokens, width, dtype, here), _stream_handle(stream))
     if status:
-        _lib.check(status, name)
+        _lib.check(status, "expert_combine_" + suffix)
     return out
 
 
@@ -767,25 +793,24 @@ def expert_combine_backward(grad: torch.Tensor, y: torch.Tensor, places: torch.T
     left as they were.  Returns (grad_y, grad_weights), the second None where
     there are neither ``weights`` nor a tensor for it."""
     suffix = _value_suffix(y)
-    tokens, choices = _check_places(places)
+    here = _device_of(y, "y")
+    tokens, choices = _check_places(places, here)
     if y.dim() != 2 or y.shape[1] < 1:
         raise ValueError("y must be [rows, width]")
     rows, width = y.shape
+    dtype, pairs = y.dtype, tokens * choices
     if grad_y is None:
-        grad_y = torch.empty(rows, width, dtype=y.dtype, device=y.device)
+        grad_y = torch.empty(rows, width, dtype=dtype, device=y.device)
     if grad_weights is None and weights is not None:
-        grad_weights = torch.empty(tokens, choices, dtype=torch.float32, device=y.device)
-    f32 = torch.float32
-    vector = lambda t, what, dtype, size: None if t is None else _check_vector(_here(t, what), what, dtype, size)  # noqa: E731
-    name = "expert_combine_backward_" + suffix
-    status = getattr(load(), name)(
-        grad.data_ptr(), _check_rows(grad, "grad", tokens, width, y.dtype), y.data_ptr(),
-        _check_rows(y, "y", rows, width, y.dtype), rows, tokens, choices, width, places.data_ptr(),
-        vector(weights, "weights", f32, tokens * choices), vector(order, "order", torch.int32, rows),
-        grad_y.data_ptr(), _check_rows(grad_y, "grad_y", rows, width, y.dtype),
-        vector(grad_weights, "grad_weights", f32, tokens * choices), _stream_handle(stream))
+        grad_weights = torch.empty(tokens, choices, dtype=_F32, device=y.device)
+    status = getattr(load(), "expert_combine_backward_" + suffix)(
+        grad.data_ptr(), _check_rows(grad, "grad", tokens, width, dtype, here), y.data_ptr(),
+        _check_rows(y, "y", rows, width, dtype, here), rows, tokens, choices, width, places.data_ptr(),
+        _vector(weights, "weights", _F32, pairs, here), _vector(order, "order", _I32, rows, here), grad_y.data_ptr(),
+        _check_rows(grad_y, "grad_y", rows, width, dtype, here),
+        _vector(grad_weights, "grad_weights", _F32, pairs, here), _stream_handle(stream))
     if status:
-        _lib.check(status, name)
+        _lib.check(status, "expert_combine_backward_" + suffix)
     return grad_y, grad_weights
 
 
@@ -795,39 +820,46 @@ _TENSOR_TYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 def _norm(tensors, out, max_norm, norm, work, stream):
     tensors = list(tensors)
     outs = tensors if out is None else list(out)
-    if len(outs) != len(tensors):
+    count = len(tensors)
+    if len(outs) != count:
         raise ValueError("out must hold a tensor for each of tensors")
-    count, here = len(tensors), torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
-    table = (_lib.Tensor * max(count, 1))()
-    for i, t in enumerate(tensors):
-        kind, o = _TENSOR_TYPE.get(t.dtype), outs[i]
-        if kind is None:
-            raise TypeError(f"unsupported dtype {t.dtype} (float32, float16, bfloat16)")
-        n = t.numel()
-        if not t.is_cuda or t.get_device() != here or not t.is_contiguous():
-            raise ValueError("tensors must be contiguous, on the current CUDA device")
-        if o is not t and (o.dtype != t.dtype or o.numel() != n or not o.is_cuda or o.get_device() != here
-                           or not o.is_contiguous()):
+    here = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
+    kinds = [_TENSOR_TYPE.get(t.dtype) for t in tensors]
+    if None in kinds:
+        raise TypeError(f"unsupported dtype {tensors[kinds.index(None)].dtype} (float32, float16, bfloat16)")
+    of = torch.Tensor                              # a method for all tensors at once: there may be hundreds
+    sizes = list(map(of.numel, tensors))
+    at = list(map(of.data_ptr, tensors))
+    if count and (set(map(of.get_device, tensors)) != {here} or here < 0 or not all(map(of.is_contiguous, tensors))):
+        raise ValueError("tensors must be contiguous, on the current CUDA device")
+    to = at
+    if out is not None:
+        if (count and set(map(of.get_device, outs)) != {here} or not all(map(of.is_contiguous, outs))
+                or list(map(of.numel, outs)) != sizes or [_TENSOR_TYPE.get(o.dtype) for o in outs] != kinds):
             raise ValueError("each of out must match its tensor in type, size and device, and be contiguous")
-        entry = table[i]
-        entry.data, entry.out, entry.n, entry.type = t.data_ptr(), o.data_ptr(), n, kind
+        to = list(map(of.data_ptr, outs))
+    table = array.array("Q", bytes(32 * max(count, 1)))   # of devscan_tensor, four words each
+    for word, values in enumerate((at, to, sizes, kinds)):
+        table[word:4 * count:4] = array.array("Q", values)
     if norm is None:
-        norm = torch.empty(1, dtype=torch.float32, device="cuda")
+        norm = torch.empty(1, dtype=_F32, device="cuda")
     need = _lib.norm_work_bytes(count)
     if work is None:
         work = torch.empty(need, dtype=torch.uint8, device="cuda")
         if stream is not None:   # the allocator may give it away once that stream is through with it
             work.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
-    _check_cuda(_here(work, "work"), "work")
-    if work.numel() * work.element_size() < need:
-        raise ValueError(f"work must hold {need} bytes")
-    at = _check_vector(_here(norm, "norm"), "norm", torch.float32, 1)
+    here = _device_of(work, "work")
+    if not work.is_contiguous():
+        raise ValueError("work must be contiguous")
     size = work.numel() * work.element_size()
+    if size < need:
+        raise ValueError(f"work must hold {need} bytes")
+    address, result = table.buffer_info()[0], _vector(norm, "norm", _F32, 1, here)
     if max_norm is None:
-        _lib.check(load().grad_norm(table, count, at, work.data_ptr(), size, _stream_handle(stream)), "grad_norm")
+        _lib.check(load().grad_norm(address, count, result, work.data_ptr(), size, _stream_handle(stream)), "grad_norm")
     else:
-        _lib.check(load().clip_grad_norm(table, count, max_norm, at, work.data_ptr(), size, _stream_handle(stream)),
-                   "clip_grad_norm")
+        _lib.check(load().clip_grad_norm(address, count, max_norm, result, work.data_ptr(), size,
+                                         _stream_handle(stream)), "clip_grad_norm")
     return norm, outs
 
 

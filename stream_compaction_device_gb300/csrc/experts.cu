@@ -73,6 +73,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) expert_sort_kernel(const __grid
             e[j] = id[j] >= 0 && id[j] < static_cast<Id>(experts) ? static_cast<unsigned>(id[j]) : experts;
     };
 
+    allow_dependent_launch();   // dispatch, which waits for this launch's end
     for (unsigned k = lane; k < experts; k += 32) mine[k] = 0;
     __syncwarp();
     const bool once = each <= 32 * kSortAtOnce;
@@ -189,9 +190,11 @@ __global__ void __launch_bounds__(32 * WARPS, 1) expert_sort_kernel(const __grid
 // Dispatch.  A warp takes a token's run of 32 * U vectors, reads it once and
 // writes it to each of the token's places, so that x is read once and not once
 // per choice; the warps behind those look through `order`, 32 rows each, for
-// rows of padding and clear them.  Bound by memory.
+// rows of padding and clear them.  Every warp is a block: it ends, and makes room
+// for the next, when its own writes are out (16,384 x 8 rows of 4 KB: 115 us
+// with four warps to a block, 109 with one, 6.1 TB/s).
 // ---------------------------------------------------------------------------
-constexpr int kMoveWarps = 8;
+constexpr int kMoveWarps = 4;   // of a block that combines
 
 // The rows among order[r0 .. r0 + 32) that are padding, a bit each.
 __device__ __forceinline__ unsigned padding_rows(const int32_t *order, unsigned r0, unsigned rows, int lane)
@@ -201,11 +204,12 @@ __device__ __forceinline__ unsigned padding_rows(const int32_t *order, unsigned 
 }
 
 template <typename V, int U>
-__global__ void __launch_bounds__(32 * kMoveWarps) expert_dispatch_kernel(const __grid_constant__ ExpertMoveCall p,
+__global__ void __launch_bounds__(32) expert_dispatch_kernel(const __grid_constant__ ExpertMoveCall p,
                                                                           unsigned vectors, unsigned runs)
 {
-    const int lane = threadIdx.x & 31;
-    const size_t item = static_cast<size_t>(blockIdx.x) * kMoveWarps + (threadIdx.x >> 5);
+    wait_primary_grid();   // a sort before this lets it start early
+    const int lane = threadIdx.x;
+    const size_t item = blockIdx.x;
     const size_t moves = static_cast<size_t>(p.tokens) * runs;
     if (item < moves) {
         const unsigned t = static_cast<unsigned>(item / runs), run = static_cast<unsigned>(item % runs);
@@ -245,20 +249,21 @@ cudaError_t dispatch(const ExpertMoveCall &call, cudaStream_t s)
     const unsigned runs = (vectors + 32 * U - 1) / (32 * U);
     const size_t items = static_cast<size_t>(call.tokens) * runs + (call.order != nullptr ? (call.rows + 31u) / 32 : 0);
     if (items == 0) return cudaSuccess;
-    const size_t blocks = (items + kMoveWarps - 1) / kMoveWarps;
-    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    expert_dispatch_kernel<V, U><<<static_cast<unsigned>(blocks), 32 * kMoveWarps, 0, s>>>(call, vectors, runs);
-    return cudaGetLastError();
+    if (items > INT32_MAX) return cudaErrorInvalidValue;
+    return launch_dependent(expert_dispatch_kernel<V, U>, static_cast<unsigned>(items), 32, s, call, vectors, runs);
 }
 
 // ---------------------------------------------------------------------------
 // Combine.  A warp takes 32 * V columns of a token and adds the rows of its
-// choices in their order, eight loads in flight, in fp32; one rounding.
+// choices in their order, eight loads in flight, in fp32; one rounding.  Bound
+// by the two loads behind each other, of places and of rows: 32 warps to an SM
+// and small blocks (8,191 x 6 rows of 4 KB: 47 us with eight warps to a block
+// and 24 to an SM, 40 so, 5.8 TB/s).
 // ---------------------------------------------------------------------------
 constexpr int kAtOnce = 8;   // choices whose rows are in flight together
 
 template <typename T, int V>
-__global__ void __launch_bounds__(32 * kMoveWarps) expert_combine_kernel(const __grid_constant__ ExpertCombineCall p,
+__global__ void __launch_bounds__(32 * kMoveWarps, 8) expert_combine_kernel(const __grid_constant__ ExpertCombineCall p,
                                                                          unsigned runs)
 {
     using R = typename Raw<T, V>::type;
@@ -304,7 +309,7 @@ __global__ void __launch_bounds__(32 * kMoveWarps) expert_combine_kernel(const _
 constexpr int kBackWarps = 4;
 
 template <typename T, int V>
-__global__ void __launch_bounds__(32 * kBackWarps) expert_combine_backward_kernel(
+__global__ void __launch_bounds__(32 * kBackWarps, 6) expert_combine_backward_kernel(
     const __grid_constant__ ExpertCombineBackwardCall p)
 {
     using R = typename Raw<T, V>::type;
@@ -469,7 +474,13 @@ cudaError_t launch_expert_dispatch(const ExpertMoveCall &call, cudaStream_t s)
 {
     const size_t all = reinterpret_cast<uintptr_t>(call.from) | reinterpret_cast<uintptr_t>(call.to) | call.row_bytes |
                        call.from_stride | call.to_stride;
-    if (all % 16 == 0) return dispatch<uint4, 4>(call, s);
+    // Large calls move most per warp (16,384 x 8 rows of 4 KB: 118 us at 4 vectors a lane, 115 at 8), small ones
+    // have the most warps (16 x 8 rows: 2.8 and 2.3 us at 4 and 1).
+    if (all % 16 == 0) {
+        const size_t lanes = static_cast<size_t>(call.tokens) * (call.row_bytes / 16);
+        if (lanes >= size_t(1) << 20) return dispatch<uint4, 8>(call, s);
+        return lanes >= size_t(1) << 17 ? dispatch<uint4, 4>(call, s) : dispatch<uint4, 1>(call, s);
+    }
     if (all % 4 == 0) return dispatch<unsigned, 4>(call, s);
     if (all % 2 == 0) return dispatch<unsigned short, 4>(call, s);
     return dispatch<unsigned char, 4>(call, s);

@@ -3,27 +3,31 @@
 //   out  = g min(1, max_norm / (norm + 1e-6)).
 //
 // The fold of geek-doc.cn "并行前缀和 scan ..." section 四 over arrays that lie
-// anywhere: the tensors are cut into chunks of 32 KB, block b takes the chunks
+// anywhere: the tensors are cut into chunks of 16 KB, block b takes the chunks
 // b, b + blocks, ... and leaves one partial sum; whoever needs the norm folds
 // the partial sums, in their order, so that the same call gives the same bits.
 // The tensors' table is a kernel parameter, so a launch holds up to
-// kNormTensors of them and nothing is copied to the device first.
+// kNormTensors of them and nothing is copied to the device first.  The second
+// launch is a programmatic dependent: its blocks start as the first one's end
+// and load their first chunk before they wait for the norm.
 //
 // Sums: a thread adds the squares of a chunk's share (64 values at most) in
 // fp32 and its shares in fp64.  Where a share's fp32 sum leaves the range in
 // which no square that matters is lost or overflows, the share is added again
-// in fp64 from its registers.
+// in fp64 from its registers.  fp64 goes at two a clock and SM here, so one
+// warp folds what a block has, and one thread takes the root.
 #include <algorithm>
 
 #include "convert.cuh"
 #include "core.cuh"
+#include "grid_sync.cuh"
 #include "launch.h"
 
 namespace devscan {
 namespace {
 
-constexpr int kNormThreads = 512, kNormUnroll = 4;
-constexpr int kNormPerSm = 2;   // blocks of an SM
+constexpr int kNormThreads = 256, kNormUnroll = 4;
+constexpr int kNormPerSm = 4;   // blocks of an SM
 constexpr unsigned kChunkBytes = kNormThreads * kNormUnroll * 16;
 
 struct NormTable {
@@ -138,23 +142,22 @@ template <typename T> __device__ __forceinline__ double chunk_squares(const Norm
     return total;
 }
 
-// The block's sum, in a fixed order, to every thread.
-__device__ __forceinline__ double block_sum(double v, double *s_w, int tid)
+// The sum of s_v[0 .. count), each lane's share in order and the lanes by a
+// tree, to all lanes of the one warp that calls this.
+__device__ __forceinline__ double warp_sum(const double *v, unsigned count, int lane)
 {
+    double sum = 0.0;
+    for (unsigned i = lane; i < count; i += 32) sum += v[i];
 #pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(kFullMask, v, d);
-    if ((tid & 31) == 0) s_w[tid >> 5] = v;
-    __syncthreads();
-    double all = 0.0;
-#pragma unroll
-    for (int w = 0; w < kNormThreads / 32; ++w) all += s_w[w];
-    return all;
+    for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(kFullMask, sum, d);
+    return sum;
 }
 
 __global__ void __launch_bounds__(kNormThreads, kNormPerSm) norm_partials_kernel(const __grid_constant__ NormTable t, double *partials)
 {
-    __shared__ double s_w[kNormThreads / 32];
+    __shared__ double s_v[kNormThreads];
     const int tid = threadIdx.x;
+    allow_dependent_launch();
     double total = 0.0;
     for (unsigned chunk = blockIdx.x; chunk < t.chunks; chunk += gridDim.x) {
         const int tensor = tensor_of(t, chunk);
@@ -165,47 +168,50 @@ __global__ void __launch_bounds__(kNormThreads, kNormPerSm) norm_partials_kernel
         case ValueType::BF16: total += chunk_squares<__nv_bfloat16>(t, tensor, index, tid); break;
         }
     }
-    total = block_sum(total, s_w, tid);
+    s_v[tid] = total;
+    __syncthreads();
+    if (tid >= 32) return;
+    total = warp_sum(s_v, kNormThreads, tid);
     if (tid == 0) partials[blockIdx.x] = total;
 }
 
 // The norm from the partial sums of all launches.
-__device__ __forceinline__ double norm_of(const double *partials, unsigned count, double *s_w, int tid)
+__global__ void __launch_bounds__(32) norm_kernel(const double *partials, unsigned count, float *norm)
 {
-    double v = 0.0;
-    for (unsigned i = tid; i < count; i += kNormThreads) v += __ldcg(partials + i);
-    return sqrt(block_sum(v, s_w, tid));
-}
-
-__global__ void __launch_bounds__(kNormThreads) norm_kernel(const double *partials, unsigned count, float *norm)
-{
-    __shared__ double s_w[kNormThreads / 32];
-    const double v = norm_of(partials, count, s_w, threadIdx.x);
+    wait_primary_grid();
+    const double v = sqrt(warp_sum(partials, count, threadIdx.x));
     if (threadIdx.x == 0) *norm = static_cast<float>(v);
 }
 
-template <typename T>
-__device__ __forceinline__ void chunk_scale(const NormTable &t, int tensor, unsigned index, float scale, int tid)
-{
-    constexpr int E = 16 / sizeof(T);
-    const Chunk c = chunk_at<sizeof(T)>(t, tensor, index);
-    const T *base = static_cast<const T *>(t.in[tensor]);
-    T *out = static_cast<T *>(t.out[tensor]);
-    const uint4 *vectors = reinterpret_cast<const uint4 *>(base + c.head) + c.first;
-    T *to = out + c.head + c.first * E;
-    const bool aligned = reinterpret_cast<uintptr_t>(to) % 16 == 0;
+// A chunk on its way through: loaded, then scaled and stored.
+struct Loaded {
+    Chunk c;
     uint4 q[kNormUnroll];
+};
+template <unsigned size> __device__ __forceinline__ void chunk_load(const NormTable &t, int tensor, unsigned index, int tid, Loaded &l)
+{
+    l.c = chunk_at<size>(t, tensor, index);
+    const uint4 *vectors = reinterpret_cast<const uint4 *>(static_cast<const char *>(t.in[tensor]) + l.c.head * size) + l.c.first;
 #pragma unroll
     for (int u = 0; u < kNormUnroll; ++u) {
         const unsigned i = u * kNormThreads + tid;
-        if (i < c.vectors) q[u] = vectors[i];
+        if (i < l.c.vectors) l.q[u] = vectors[i];
     }
+}
+template <typename T> __device__ __forceinline__ void chunk_store(const NormTable &t, const Loaded &l, float scale, int tid)
+{
+    constexpr int E = 16 / sizeof(T);
+    const Chunk &c = l.c;
+    const T *base = static_cast<const T *>(t.in[c.tensor]);
+    T *out = static_cast<T *>(t.out[c.tensor]);
+    T *to = out + c.head + c.first * E;
+    const bool aligned = reinterpret_cast<uintptr_t>(to) % 16 == 0;
 #pragma unroll
     for (int u = 0; u < kNormUnroll; ++u) {
         const unsigned i = u * kNormThreads + tid;
         if (i >= c.vectors) continue;
         float v[E];
-        values_of<T>(q[u], v);
+        values_of<T>(l.q[u], v);
 #pragma unroll
         for (int e = 0; e < E; ++e) v[e] *= scale;
         if (aligned) {
@@ -216,35 +222,64 @@ __device__ __forceinline__ void chunk_scale(const NormTable &t, int tensor, unsi
         }
     }
     if (c.lead && static_cast<unsigned>(tid) < c.head) out[tid] = from_float<T>(to_float(base[tid]) * scale);
-    if (c.trail && c.tail + tid < t.n[tensor]) out[c.tail + tid] = from_float<T>(to_float(base[c.tail + tid]) * scale);
+    if (c.trail && c.tail + tid < t.n[c.tensor]) out[c.tail + tid] = from_float<T>(to_float(base[c.tail + tid]) * scale);
 }
 
 // Blocks go through the chunks from the last to the first: what the sum read
-// last still lies in L2.
+// last still lies in L2.  `partials` and `norm` are touched behind the wait
+// only; the tensors, which the launch before this one reads too, were written
+// before that one began.
 __global__ void __launch_bounds__(kNormThreads, kNormPerSm) norm_scale_kernel(const __grid_constant__ NormTable t, const double *partials,
-                                                                     unsigned count, float max_norm, float *norm)
+                                                                              unsigned count, float max_norm, float *norm)
 {
-    __shared__ double s_w[kNormThreads / 32];
+    __shared__ float s_scale;
     const int tid = threadIdx.x;
-    const double v = norm_of(partials, count, s_w, tid);
-    if (blockIdx.x == 0 && tid == 0 && norm != nullptr) *norm = static_cast<float>(v);
-    const double ratio = static_cast<double>(max_norm) / (v + kClipEps);
-    // a norm that is no number, or infinite, clips nothing
-    const float scale = ratio < 1.0 && v < __longlong_as_double(0x7ff0000000000000ll) ? static_cast<float>(ratio) : 1.0f;
+    float scale = 1.0f;
+    bool told = false;
     for (unsigned i = blockIdx.x; i < t.chunks; i += gridDim.x) {
         const unsigned chunk = t.chunks - 1 - i;
         const int tensor = tensor_of(t, chunk);
-        if (scale == 1.0f && t.in[tensor] == t.out[tensor]) continue;
         const unsigned index = chunk - (tensor > 0 ? t.end[tensor - 1] : 0u);
-        switch (static_cast<ValueType>(t.type[tensor])) {
-        case ValueType::F32: chunk_scale<float>(t, tensor, index, scale, tid); break;
-        case ValueType::F16: chunk_scale<__half>(t, tensor, index, scale, tid); break;
-        case ValueType::BF16: chunk_scale<__nv_bfloat16>(t, tensor, index, scale, tid); break;
+        const ValueType type = static_cast<ValueType>(t.type[tensor]);
+        Loaded l;
+        if (type == ValueType::F32)
+            chunk_load<4>(t, tensor, index, tid, l);
+        else
+            chunk_load<2>(t, tensor, index, tid, l);
+        if (!told) {
+            wait_primary_grid();
+            if (tid < 32) {
+                const double v = sqrt(warp_sum(partials, count, tid));
+                if (tid == 0) {
+                    if (blockIdx.x == 0 && norm != nullptr) *norm = static_cast<float>(v);
+                    const double ratio = static_cast<double>(max_norm) / (v + kClipEps);
+                    // a norm that is no number, or infinite, clips nothing
+                    s_scale = ratio < 1.0 && v < __longlong_as_double(0x7ff0000000000000ll) ? static_cast<float>(ratio) : 1.0f;
+                }
+            }
+            __syncthreads();
+            scale = s_scale;
+            told = true;
+        }
+        if (scale == 1.0f && t.in[tensor] == t.out[tensor]) continue;
+        switch (type) {
+        case ValueType::F32: chunk_store<float>(t, l, scale, tid); break;
+        case ValueType::F16: chunk_store<__half>(t, l, scale, tid); break;
+        case ValueType::BF16: chunk_store<__nv_bfloat16>(t, l, scale, tid); break;
         }
     }
 }
 
 unsigned size_of(ValueType type) { return type == ValueType::F32 ? 4u : 2u; }
+
+// The launches for the tables behind the first wait for what is before them as
+// any launch does.
+cudaError_t launch_scale(const NormTable &t, unsigned blocks, const double *work, unsigned partials, float max_norm,
+                         float *norm, cudaStream_t s)
+{
+    norm_scale_kernel<<<blocks, kNormThreads, 0, s>>>(t, work, partials, max_norm, norm);
+    return cudaGetLastError();
+}
 
 // The table of tensors [first, first + kNormTensors) of a call.
 bool fill(NormTable &t, const NormTensor *tensors, size_t first, size_t count)
@@ -288,15 +323,14 @@ cudaError_t launch_grad_norm(const NormTensor *tensors, size_t count, bool clip,
         for (size_t i = 0; i < count; i += kNormTensors) {
             if (!fill(t, tensors, i, count < i + kNormTensors ? count : i + kNormTensors)) return cudaErrorInvalidValue;
             if (t.chunks == 0) continue;
-            norm_scale_kernel<<<t.chunks < most ? t.chunks : most, kNormThreads, 0, s>>>(t, work, partials, max_norm,
-                                                                                      told ? nullptr : norm);
-            const cudaError_t e = cudaGetLastError();
+            const unsigned blocks = t.chunks < most ? t.chunks : most;
+            const cudaError_t e = told ? launch_scale(t, blocks, work, partials, max_norm, nullptr, s)
+                                       : launch_dependent(norm_scale_kernel, blocks, kNormThreads, s, t, work, partials, max_norm, norm);
             if (e != cudaSuccess) return e;
             told = true;
         }
     if (told) return cudaSuccess;
-    norm_kernel<<<1, kNormThreads, 0, s>>>(work, partials, norm);
-    return cudaGetLastError();
+    return launch_dependent(norm_kernel, 1, 32, s, work, partials, norm);
 }
 
 }  // namespace devscan
