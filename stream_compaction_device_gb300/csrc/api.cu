@@ -407,7 +407,7 @@ devscan_status gated_check(size_t rows, size_t tokens, size_t channels, const in
     if (starts == nullptr && rows * tokens > kMost) return DEVSCAN_ERR_INVALID;
     if (misaligned(starts, 4) || misaligned(slots, 4)) return DEVSCAN_ERR_INVALID;
     *out = {starts, slots, static_cast<int>(rows), static_cast<int>(channels), static_cast<int>(pool),
-            static_cast<unsigned>(tokens), 0, 0, 0};
+            static_cast<unsigned>(tokens), 0, 0, 0, 0};
     return DEVSCAN_OK;
 }
 

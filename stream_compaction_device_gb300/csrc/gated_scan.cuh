@@ -32,6 +32,8 @@
 // order that follows from the sizes alone.
 #pragma once
 
+#include <initializer_list>
+
 #include "cluster.cuh"
 #include "convert.cuh"
 #include "grid_sync.cuh"
@@ -51,11 +53,12 @@ constexpr int ring_bytes(int blocks) { return (228 << 10) / blocks - (18 << 10);
 // Tokens of a warp and round where the values of a lane and token have `bytes`
 // bytes: as many as two blocks per SM hold twice (long rows: fewer rounds), or
 // fewer, where rows are short.
-constexpr int tokens_per_round(int bytes, int copy, bool many)
+// `both`: the recurrence's a and b stay in registers.
+constexpr int tokens_per_round(int bytes, int copy, bool many, bool both)
 {
     const int most = ring_bytes(2) / (2 * kWarps * 32 * bytes) / 4 * 4;
-    const int some = bytes <= 8 && copy > 0 ? 12 : 8;
-    return copy == 0 || !many ? some : most;
+    const int some = bytes <= 8 && copy > 0 && !both ? 12 : 8;
+    return copy == 0 || !many ? some : both && most > 16 ? 16 : most;
 }
 
 // ---------------------------------------------------------------------------
@@ -137,40 +140,30 @@ template <int V> __device__ __forceinline__ Lanes<V> exp_decay(Lanes<V> g)
     return s;
 }
 
-// a = 1 / (1 + exp(-g)) and r = 1 - a: the smaller of the two is the quotient
-// t / (1 + t), t = exp(-|g|).  Both are kept as it, with g's sign.
-template <int V> __device__ __forceinline__ Lanes<V> sigmoid_kept(Lanes<V> g)
+// With u = exp(-g): 1 / (1 + u) and r = u / (1 + u).  Where u is at most 1 that
+// r is the smaller of the two and a is 1 - r, rounded once; elsewhere a is the
+// quotient.  (u ends at 2^126: a at 2^-126.)
+template <int V> __device__ __forceinline__ void sigmoid_decay(Lanes<V> g, Lanes<V> &a, Lanes<V> &r)
 {
-    const Lanes<V> scaled = g * all<V>(kLog2E);
+    Lanes<V> u = g * all<V>(-kLog2E);
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-        const float t = hard_exp2(-fabsf(scaled.v[k]));
-        g.v[k] = copysignf(t * hard_reciprocal(1.0f + t), g.v[k]);
-    }
-    return g;
+    for (int k = 0; k < V; ++k) asm("min.NaN.f32 %0, %1, %2;" : "=f"(u.v[k]) : "f"(hard_exp2(u.v[k])), "f"(0x1p126f));
+    a = u + all<V>(1.0f);
+#pragma unroll
+    for (int k = 0; k < V; ++k) a.v[k] = hard_reciprocal(a.v[k]);
+    r = u * a;
+    const Lanes<V> rest = fma(r, all<V>(-1.0f), all<V>(1.0f));
+#pragma unroll
+    for (int k = 0; k < V; ++k) a.v[k] = g.v[k] >= 0.0f ? rest.v[k] : a.v[k];
 }
 
-// What a token's gate is kept as, a from it, and what x is multiplied by.
-template <int KIND, int V> __device__ __forceinline__ Lanes<V> kept_of(Lanes<V> gate)
+// a, and what x is multiplied by (sigmoid only), from a token's gate.
+template <int KIND, int V> __device__ __forceinline__ void coefficients(Lanes<V> gate, Lanes<V> &a, Lanes<V> &r)
 {
-    if constexpr (KIND == kGateLog) return exp_decay(gate);
-    if constexpr (KIND == kGateSigmoid) return sigmoid_kept(gate);
-    return gate;
+    a = gate;
+    if constexpr (KIND == kGateLog) a = exp_decay(gate);
+    if constexpr (KIND == kGateSigmoid) sigmoid_decay(gate, a, r);
 }
-template <int KIND, int V> __device__ __forceinline__ void coefficients(Lanes<V> kept, Lanes<V> &a, Lanes<V> &r)
-{
-    a = kept;
-    if constexpr (KIND == kGateSigmoid) {
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const float small = fabsf(kept.v[k]), large = 1.0f - small;
-            const bool open = static_cast<int>(__float_as_uint(kept.v[k])) >= 0;   // g at least 0 (or a NaN)
-            a.v[k] = open ? large : small;
-            r.v[k] = open ? small : large;
-        }
-    }
-}
-template <int KIND> constexpr float kHold = KIND == kGateSigmoid ? 0.0f : 1.0f;   // kept for a = 1
 
 // ---------------------------------------------------------------------------
 // Rows and spans.
@@ -251,17 +244,17 @@ __device__ __forceinline__ float *state_of(const GatedRows &rows, float *states,
 // A warp's consecutive tokens n, n + 1, ... (DOWN: n, n - 1, ...).
 // ---------------------------------------------------------------------------
 struct Run {
-    unsigned n, row, t;   // the first token, its row of an array and its place there
+    unsigned n, row, t;   // the first token, its row in the arrays and its place there
     int count;
-    bool whole;           // all there, and in one row of an array
+    bool whole;           // all there, and in one row of the arrays
 };
 template <int L, bool DOWN> __device__ __forceinline__ Run run_of(const GatedRows &rows, unsigned n, int count)
 {
     Run r;
     r.n = n, r.count = count;
-    r.row = rows.starts == nullptr && rows.rows > 1 && count > 0 ? n / rows.tokens : 0u;
-    r.t = n - r.row * rows.tokens;
-    r.whole = count == L && (DOWN ? r.t + 1 >= L : r.t + L <= rows.tokens);
+    r.row = rows.per != rows.all() && count > 0 ? n / rows.per : 0u;
+    r.t = n - r.row * rows.per;
+    r.whole = count == L && (DOWN ? r.t + 1 >= L : r.t + L <= rows.per);
     return r;
 }
 __device__ __forceinline__ size_t element(const GatedArray &array, unsigned row, unsigned t)
@@ -282,15 +275,15 @@ __device__ __forceinline__ void walk(const GatedRows &rows, const GatedArray &ar
         }
         return;
     }
-    const size_t turn = array.row_stride - (rows.tokens - 1) * array.stride;   // modulo 2^64
+    const size_t turn = array.row_stride - (rows.per - 1) * array.stride;   // modulo 2^64
     unsigned t = r.t;
 #pragma unroll
     for (int i = 0; i < L; ++i) {
         if (i < r.count) fn(i, at);
-        const bool wrap = DOWN ? t == 0 : t + 1 == rows.tokens;
+        const bool wrap = DOWN ? t == 0 : t + 1 == rows.per;
         if (DOWN) {
             at -= wrap ? turn : array.stride;
-            t = wrap ? rows.tokens - 1 : t - 1;
+            t = wrap ? rows.per - 1 : t - 1;
         } else {
             at += wrap ? turn : array.stride;
             t = wrap ? 0 : t + 1;
@@ -340,7 +333,7 @@ __device__ __forceinline__ void copy_tokens(const GatedRows &rows, const GatedAr
         const int i = j * kAtOnce + i0;
         if (i >= r.count) break;
         const unsigned n = DOWN ? r.n - i : r.n + i;
-        const unsigned row = rows.starts == nullptr ? n / rows.tokens : 0u, t = n - row * rows.tokens;
+        const unsigned row = n / rows.per, t = n - row * rows.per;
         if (BACK > 0 && t < BACK) continue;   // nothing before it: not looked at
         const char *from = base + element(array, row, t - BACK) * size + piece * W;
 #pragma unroll
@@ -386,14 +379,25 @@ __device__ __forceinline__ Lanes<V> exchange(Exchange<V> &x, int turn, int block
     x.a[turn][warp][lane] = a, x.h[turn][warp][lane] = h;
     if (lane == 0) x.cut[turn][warp] = cut;
     __syncthreads();
+    const unsigned cuts = __ballot_sync(kFullMask, lane < kWarps && x.cut[turn][lane & (kWarps - 1)] != 0);
+    if (blocks == 1) {
+        Lanes<V> in = x.carry[turn][lane];
+        if (cuts == 0) {
+#pragma unroll
+            for (int w = 0; w < kWarps - 1; ++w)
+                if (w < warp) in = fma(x.a[turn][w][lane], in, x.h[turn][w][lane]);
+        } else {
+#pragma unroll 1
+            for (int w = 0; w < warp; ++w) in = follow((cuts >> w) & 1u, x.a[turn][w][lane], in, x.h[turn][w][lane]);
+        }
+        return in;
+    }
     // the map of the block's warps before this one, and of all of them
     Lanes<V> ba = all<V>(1.0f), bh = all<V>(0.0f), fa = ba, fh = bh;
-    const unsigned cuts = __ballot_sync(kFullMask, lane < kWarps && x.cut[turn][lane & (kWarps - 1)] != 0);
     if (cuts == 0) {
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             if (w == warp) ba = fa, bh = fh;
-            if (w >= warp && blocks == 1) break;
             const Lanes<V> wa = x.a[turn][w][lane];
             fh = fma(wa, fh, x.h[turn][w][lane]);
             fa = wa * fa;
@@ -408,7 +412,6 @@ __device__ __forceinline__ Lanes<V> exchange(Exchange<V> &x, int turn, int block
             fa = c ? wa : wa * fa;
         }
     }
-    if (blocks == 1) return follow((cuts & ((1u << warp) - 1u)) != 0, ba, x.carry[turn][lane], bh);
     if (warp < blocks) {   // warp q tells block q
         st_lanes<V>(cluster_addr(&x.all_a[turn][rank][lane], warp), fa);
         st_lanes<V>(cluster_addr(&x.all_h[turn][rank][lane], warp), fh);
@@ -478,11 +481,7 @@ __device__ __forceinline__ Edges edges_of(const GatedRows &rows, const Run &r, i
 {
     Edges e = {0, 0, 0, 0};
     const unsigned low = DOWN ? r.n - (L - 1) : r.n;   // where count == L
-    if (rows.starts == nullptr) {
-        if (r.whole && (DOWN ? r.t + 1 > L && r.t + 1 < rows.tokens : r.t > 0 && r.t + L < rows.tokens)) return e;
-    } else if (r.count == L && low > in.begin && low + L < in.end) {
-        return e;
-    }
+    if (r.count == L && low > in.begin && low + L < in.end) return e;
     const bool mine = lane < r.count;
     TokenPlace p = {0, true, false, false};
     if (mine) p = place_of(rows, DOWN ? r.n - lane : r.n + lane);
@@ -490,10 +489,12 @@ __device__ __forceinline__ Edges edges_of(const GatedRows &rows, const Run &r, i
     e.last = __ballot_sync(kFullMask, mine && p.last);
     e.outside = __ballot_sync(kFullMask, mine && !p.inside);
     e.row = p.row;
-    if (rows.starts != nullptr && r.count > 0) {
+    if (r.count > 0) {
         const bool some = __shfl_sync(kFullMask, p.inside, r.count - 1);   // the row that goes on
-        const int row = __shfl_sync(kFullMask, p.row, r.count - 1);
-        if (some) {
+        const unsigned row = static_cast<unsigned>(__shfl_sync(kFullMask, p.row, r.count - 1));
+        if (some && rows.starts == nullptr) {
+            in.begin = row * rows.tokens, in.end = in.begin + rows.tokens;
+        } else if (some) {
             in.begin = static_cast<unsigned>(__ldg(rows.starts + row));
             in.end = min(static_cast<unsigned>(__ldg(rows.starts + row + 1)), rows.all());
         }
@@ -563,27 +564,22 @@ template <typename X, typename G, int V, int L, int VALUES, int COPY> struct Rin
 };
 
 template <typename X, typename G, int V, int VALUES> constexpr int kLaneBytes = V * (VALUES * static_cast<int>(sizeof(X)) + static_cast<int>(sizeof(G)));
-template <typename X, typename G, int V, int VALUES, int COPY, bool MANY>
-using RingOf = Ring<X, G, V, tokens_per_round(kLaneBytes<X, G, V, VALUES>, COPY, MANY), VALUES, COPY>;
-template <typename X, typename G, int V, int COPY, bool MANY> using ForwardRing = RingOf<X, G, V, 1, COPY, MANY>;
+template <typename X, typename G, int V, int VALUES, int COPY, bool MANY, bool BOTH>
+using RingOf = Ring<X, G, V, tokens_per_round(kLaneBytes<X, G, V, VALUES>, COPY, MANY, BOTH), VALUES, COPY>;
 template <typename X, typename G, int V, int KIND, int COPY, bool MANY>
-using BackwardRing = RingOf<X, G, V, KIND == kGateSigmoid ? 3 : 2, COPY, MANY>;
+using ForwardRing = RingOf<X, G, V, 1, COPY, MANY, KIND == kGateSigmoid>;
+template <typename X, typename G, int V, int KIND, int COPY, bool MANY>
+using BackwardRing = RingOf<X, G, V, KIND == kGateSigmoid ? 3 : 2, COPY, MANY, false>;
 
 // ---------------------------------------------------------------------------
 // Forward.
 // ---------------------------------------------------------------------------
-// b of a token from x.
-template <int KIND, int V> __device__ __forceinline__ Lanes<V> given(Lanes<V> r, Lanes<V> x)
-{
-    if constexpr (KIND == kGateSigmoid) return r * x;
-    return x;
-}
-
 template <typename X, typename G, int V, int KIND, int COPY, bool MANY>
-__global__ void __launch_bounds__(kThreads, (ForwardRing<X, G, V, COPY, MANY>::kPerSm))
+__global__ void __launch_bounds__(kThreads, (ForwardRing<X, G, V, KIND, COPY, MANY>::kPerSm))
  gated_scan_kernel(const __grid_constant__ GatedScanCall p)
 {
-    using R = ForwardRing<X, G, V, COPY, MANY>;
+    constexpr bool SIGMOID = KIND == kGateSigmoid;
+    using R = ForwardRing<X, G, V, KIND, COPY, MANY>;
     constexpr int L = R::kTokens;
     using RX = typename R::RX;
     using RG = typename R::RG;
@@ -656,35 +652,45 @@ __global__ void __launch_bounds__(kThreads, (ForwardRing<X, G, V, COPY, MANY>::k
         const Edges e = edges_of<L, false>(p.rows, r, lane, in_row);
         const unsigned cut = e.first | e.outside;
         const bool plain = r.whole && (cut | e.last) == 0;
-        Lanes<V> kept[L], fa = all<V>(1.0f), h = all<V>(0.0f);
+        // sigmoid keeps b; the others take x from the ring again
+        Lanes<V> a[L], b[SIGMOID ? L : 1], fa = all<V>(1.0f), h = all<V>(0.0f);
 #pragma unroll
-        for (int i = 0; i < L; ++i) kept[i] = kept_of<KIND, V>(R::gate(stage, i, lane));
+        for (int i = 0; i < L; ++i) {
+            Lanes<V> rest;
+            coefficients<KIND, V>(R::gate(stage, i, lane), a[i], rest);
+            if constexpr (SIGMOID) b[i] = rest * R::value(stage, 0, i, lane);
+        }
+        auto given = [&](int i) {
+            if constexpr (SIGMOID)
+                return b[i];
+            else
+                return R::value(stage, 0, i, lane);
+        };
         if (plain) {
 #pragma unroll
             for (int i = 0; i < L; ++i) {
-                Lanes<V> a, rest;
-                coefficients<KIND, V>(kept[i], a, rest);
-                h = fma(a, h, given<KIND, V>(rest, R::value(stage, 0, i, lane)));
-                fa = fa * a;
+                h = fma(a[i], h, given(i));
+                fa = fa * a[i];
             }
-        } else {   // b is left in the ring: what it was made of may be overwritten before it is used again
+        } else {   // b stays in the ring, if not in registers: what it is made of may be overwritten before it is used again
 #pragma unroll
             for (int i = 0; i < L; ++i) {
-                Lanes<V> a, rest;
-                if (i >= r.count) kept[i] = all<V>(kHold<KIND>);
-                coefficients<KIND, V>(kept[i], a, rest);
-                Lanes<V> b = given<KIND, V>(rest, R::value(stage, 0, i, lane));
-                if (i >= r.count || ((e.outside >> i) & 1u)) b = all<V>(0.0f);
+                Lanes<V> now = given(i);
+                if (i >= r.count) a[i] = all<V>(1.0f);
+                if (i >= r.count || ((e.outside >> i) & 1u)) now = all<V>(0.0f);
                 if ((e.first >> i) & 1u) {
                     const float *from = state_of(p.rows, p.initial, e.row_of(i));
                     if (from != nullptr && live)
 #pragma unroll
-                        for (int k = 0; k < V; ++k) b.v[k] = fmaf(a.v[k], from[w.channel + k], b.v[k]);
+                        for (int k = 0; k < V; ++k) now.v[k] = fmaf(a[i].v[k], from[w.channel + k], now.v[k]);
                 }
-                R::put(stage, i, lane, b);
+                if constexpr (SIGMOID)
+                    b[i] = now;
+                else
+                    R::put(stage, i, lane, now);
                 const bool c = (cut >> i) & 1u;
-                h = follow(c, a, h, b);
-                fa = c ? all<V>(0.0f) : fa * a;
+                h = follow(c, a[i], h, now);
+                fa = c ? all<V>(0.0f) : fa * a[i];
             }
         }
         h = exchange<V>(s_x, step & 1, w.blocks, w.rank, warp, lane, fa, h, cut != 0);
@@ -692,9 +698,7 @@ __global__ void __launch_bounds__(kThreads, (ForwardRing<X, G, V, COPY, MANY>::k
             X *to = out + element(p.out, r.row, r.t);
 #pragma unroll
             for (int i = 0; i < L; ++i) {
-                Lanes<V> a, rest;
-                coefficients<KIND, V>(kept[i], a, rest);
-                h = fma(a, h, given<KIND, V>(rest, R::value(stage, 0, i, lane)));
+                h = fma(a[i], h, given(i));
                 if (live) *reinterpret_cast<RX *>(to) = pack<X, V>(h.v);
                 to += p.out.stride;
             }
@@ -704,15 +708,18 @@ __global__ void __launch_bounds__(kThreads, (ForwardRing<X, G, V, COPY, MANY>::k
         }
 #pragma unroll
         for (int i = 0; i < L; ++i) {
-            Lanes<V> a, rest;
-            coefficients<KIND, V>(kept[i], a, rest);
-            h = follow((cut >> i) & 1u, a, h, R::get(stage, i, lane));
-            kept[i] = h;
+            Lanes<V> now;
+            if constexpr (SIGMOID)
+                now = b[i];
+            else
+                now = R::get(stage, i, lane);
+            h = follow((cut >> i) & 1u, a[i], h, now);
+            a[i] = h;
         }
         if (step + 1 < rounds) hand_on<V>(s_x, (step + 1) & 1, w.blocks, w.rank, warp, lane, h);
         __syncwarp();   // the stage has been read
         if (live && r.count > 0)
-            walk<L, false>(p.rows, p.out, r, [&](int i, size_t at) { *reinterpret_cast<RX *>(out + at) = pack<X, V>(kept[i].v); });
+            walk<L, false>(p.rows, p.out, r, [&](int i, size_t at) { *reinterpret_cast<RX *>(out + at) = pack<X, V>(a[i].v); });
         if (p.final != nullptr) {
 #pragma unroll
             for (int i = 0; i < L; ++i) {
@@ -720,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, (ForwardRing<X, G, V, COPY, MANY>::k
                 float *to = state_of(p.rows, p.final, e.row_of(i));
                 if (to != nullptr && live)
 #pragma unroll
-                    for (int k = 0; k < V; ++k) to[w.channel + k] = kept[i].v[k];
+                    for (int k = 0; k < V; ++k) to[w.channel + k] = a[i].v[k];
             }
         }
     }
@@ -802,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, (BackwardRing<X, G, V, KIND, COPY, M
             walk<L, true>(p.rows, p.gate, r, [&](int i, size_t at) { rg[i % kKept] = *reinterpret_cast<const RG *>(gate + w.channel + at); });
             walk<L, true>(p.rows, p.y, r, [&](int i, size_t at) {
                 if (t > 0) ry[i % kKept] = *reinterpret_cast<const RX *>(y + w.channel + (at - p.y.stride));
-                t = t == 0 ? p.rows.tokens - 1 : t - 1;
+                t = t == 0 ? p.rows.per - 1 : t - 1;
             });
             if constexpr (SIGMOID)
                 walk<L, true>(p.rows, p.x, r, [&](int i, size_t at) { rx[i % kKept] = *reinterpret_cast<const RX *>(x + w.channel + at); });
@@ -832,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, (BackwardRing<X, G, V, KIND, COPY, M
         Lanes<V> a[L], rest[SIGMOID ? L : 1], d[L];
 #pragma unroll
         for (int i = 0; i < L; ++i) {
-            coefficients<KIND, V>(kept_of<KIND, V>(R::gate(stage, i, lane)), a[i], rest[SIGMOID ? i : 0]);
+            coefficients<KIND, V>(R::gate(stage, i, lane), a[i], rest[SIGMOID ? i : 0]);
             d[i] = R::value(stage, 0, i, lane);
         }
         const Edges e = edges_of<L, true>(p.rows, r, lane, in_row);
@@ -965,7 +972,7 @@ __global__ void __launch_bounds__(kStepThreads) gated_step_kernel(const __grid_c
 #pragma unroll
     for (int k = 0; k < N; ++k) {
         Lanes<1> a, rest;
-        coefficients<KIND, 1>(kept_of<KIND, 1>(Lanes<1>{gate[k]}), a, rest);
+        coefficients<KIND, 1>(Lanes<1>{gate[k]}, a, rest);
         if constexpr (KIND == kGateSigmoid) b[k] *= rest.v[0];
         if (from != nullptr) b[k] = fmaf(a.v[0], h0[k], b[k]);
     }
@@ -993,6 +1000,16 @@ struct Width {
     }
     int copy() const { return !whole ? 0 : all % 16 == 0 ? 16 : 4; }
 };
+
+// Tokens of a row as far as addresses go: where every array's rows lie behind
+// each other, all tokens are one.
+inline void lay_out(GatedRows &rows, std::initializer_list<const GatedArray *> arrays)
+{
+    bool flat = true;
+    for (const GatedArray *a : arrays) flat = flat && (a->data == nullptr || a->row_stride == rows.tokens * a->stride);
+    rows.per = flat || rows.starts != nullptr || rows.rows == 1 ? rows.all() : rows.tokens;
+    if (rows.per == 0) rows.per = 1;
+}
 
 // Spans and blocks per cluster.  Rows are spread first; a span's rows are then
 // spread over more blocks while the grid leaves places on the GPU empty and
@@ -1039,7 +1056,8 @@ template <typename X, typename G, int V, int KIND, int COPY, bool MANY>
 cudaError_t forward_of(GatedScanCall call, int sms, cudaStream_t s)
 {
     static std::atomic<unsigned long long> done;
-    using R = ForwardRing<X, G, V, COPY, MANY>;
+    using R = ForwardRing<X, G, V, KIND, COPY, MANY>;
+    lay_out(call.rows, {&call.x, &call.gate, &call.out});
     plan(call.rows, V, R::kTokens, R::kPerSm, sms);
     return launch_clusters(gated_scan_kernel<X, G, V, KIND, COPY, MANY>, call, R::kBytes, done, s);
 }
@@ -1092,6 +1110,7 @@ cudaError_t backward_of(GatedBackwardCall call, int sms, cudaStream_t s)
 {
     static std::atomic<unsigned long long> done;
     using R = BackwardRing<X, G, V, KIND, COPY, MANY>;
+    lay_out(call.rows, {&call.grad, &call.gate, &call.y, &call.grad_x, &call.grad_gate, KIND == kGateSigmoid ? &call.x : &call.y});
     plan(call.rows, V, R::kTokens, R::kPerSm, sms);
     return launch_clusters(gated_scan_backward_kernel<X, G, V, KIND, COPY, MANY>, call, R::kBytes, done, s);
 }

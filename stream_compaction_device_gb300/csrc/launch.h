@@ -202,6 +202,7 @@ struct GatedRows {
     const int32_t *slots;    // of the rows in the states; null: their own index
     int rows, channels, pool;
     unsigned tokens;         // per row, or packed in all
+    unsigned per;            // per row of the arrays, for addresses
     unsigned groups, spans;
     int blocks;
     __host__ __device__ unsigned all() const { return starts != nullptr ? tokens : tokens * static_cast<unsigned>(rows); }
