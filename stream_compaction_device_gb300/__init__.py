@@ -842,7 +842,7 @@ def _norm(tensors, out, max_norm, norm, work, stream):
     for word, values in enumerate((at, to, sizes, kinds)):
         table[word:4 * count:4] = array.array("Q", values)
     if norm is None:
-        norm = torch.empty(1, dtype=_F32, device="cuda")
+        norm = torch.empty((), dtype=_F32, device="cuda")
     need = _lib.norm_work_bytes(count)
     if work is None:
         work = torch.empty(need, dtype=torch.uint8, device="cuda")
@@ -866,7 +866,7 @@ def _norm(tensors, out, max_norm, norm, work, stream):
 def grad_norm(tensors, norm: torch.Tensor | None = None, work: torch.Tensor | None = None,
               stream=None) -> torch.Tensor:
     """2-norm over all elements of ``tensors`` (contiguous float32, float16 or
-    bfloat16, mixed as they come): one fp32 on the device.  Squares neither
+    bfloat16, mixed as they come): an fp32 scalar on the device.  Squares neither
     overflow nor vanish.  ``work`` may pass the scratch (any type,
     ``_lib.norm_work_bytes(len(tensors))`` bytes)."""
     return _norm(tensors, None, None, norm, work, stream)[0]
