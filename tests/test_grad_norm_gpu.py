@@ -132,7 +132,7 @@ def test_same_bits_streams_and_graphs(ds):
     for norm, out in results:
         assert torch.equal(norm, want[0]) and all(torch.equal(a, b) for a, b in zip(out, want[1]))
     for s in (streams[1], streams[1].cuda_stream):
-        norm = torch.zeros(1, device="cuda")
+        norm = torch.zeros((), device="cuda")
         torch.cuda.synchronize()
         ds.grad_norm(tensors, norm=norm, stream=s)
         streams[1].synchronize()

@@ -204,3 +204,44 @@ def test_threads(ds):
     for t in threads:
         t.join()
     assert not wrong
+
+
+def test_example_gradients(ds):
+    """The example's autograd functions against autograd through plain formulas
+    in 64 bits (rooms as in test_training_step), and that it runs."""
+    import importlib.util
+    import os
+
+    from conftest import ROOT
+    spec = importlib.util.spec_from_file_location("train_step", os.path.join(ROOT, "examples", "train_step.py"))
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    g = torch.Generator(device="cuda").manual_seed(11)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x, gate, grad = r(30, 12), r(30, 12), r(30, 12)
+    starts = torch.tensor([0, 11, 30], dtype=torch.int32, device="cuda")
+    leaves = [x.requires_grad_(), gate.requires_grad_()]
+    got = torch.autograd.grad((m.Recurrence.apply(*leaves, starts) * grad).sum(), leaves)
+    wide = [v.detach().double().requires_grad_() for v in leaves]
+    a, b, h = torch.sigmoid(wide[1]), torch.sigmoid(-wide[1]) * wide[0], []
+    for t in range(30):
+        h.append(b[t] if t in (0, 11) else a[t] * h[-1] + b[t])
+    want = torch.autograd.grad((torch.stack(h) * grad.double()).sum(), wide)
+    for u, v in zip(got, want):
+        assert (u.double() - v).abs().max() <= 400 * 2 ** -24 * v.abs().max()
+
+    ids = torch.randint(0, 4, (30, 2), generator=g, device="cuda")
+    _, _, order, places = ds.expert_sort(ids, 4, align=4)
+    weights = torch.rand(30, 2, generator=g, device="cuda").requires_grad_()
+    leaves = [x, weights]
+    scale = r(order.numel(), 1)
+    y = m.Combine.apply(m.Dispatch.apply(x, places, order) * scale, weights, places, order)
+    got = torch.autograd.grad((y * grad).sum(), leaves)
+    wide = [v.detach().double().requires_grad_() for v in leaves]
+    at = places.long()
+    plain = (wide[1][..., None] * wide[0][:, None] * scale.double()[at]).sum(1)
+    want = torch.autograd.grad((plain * grad.double()).sum(), wide)
+    for u, v in zip(got, want):
+        assert (u.double() - v).abs().max() <= 400 * 2 ** -24 * v.abs().max()
+    losses = m.train(3)
+    assert all(np.isfinite(losses))
