@@ -169,18 +169,35 @@ template <int KIND, int V> __device__ __forceinline__ void coefficients(Lanes<V>
 // Rows and spans.
 // ---------------------------------------------------------------------------
 
-// Index of the first of starts[0 .. count) that is at least `value` (`above`:
-// greater than it); count if none is.
-template <bool above>
-__device__ __forceinline__ int first_start(const int32_t *starts, int count, int value)
+// Index of the last row that begins at or before token n; -1 if none does.
+__device__ __forceinline__ int row_at(const GatedRows &rows, int n)
 {
-    int lo = 0, hi = count;
+    int lo = 0, hi = rows.rows + 1;
     while (lo < hi) {
-        const int mid = (lo + hi) >> 1, s = __ldg(starts + mid);
-        if (above ? s <= value : s < value)
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(rows.starts + mid) <= n)
             lo = mid + 1;
         else
             hi = mid;
+    }
+    return lo - 1;
+}
+
+// Index of the first of starts[0 .. count) that is at least `value`; count if
+// none is.  A warp looks at 32 places at once: what a launch waits for first is
+// two loads behind each other for a thousand rows, instead of ten.
+__device__ __forceinline__ int first_start(const int32_t *starts, int count, int value, int lane)
+{
+    int lo = 0, hi = count;
+    while (lo < hi) {
+        const int step = (hi - lo + 31) / 32;
+        const long long at = lo + static_cast<long long>(lane) * step;
+        const unsigned below = __ballot_sync(kFullMask, at < hi && __ldg(starts + at) < value);
+        const int many = __popc(below);   // of the places looked at
+        if (many == 0) return lo;
+        const long long last = lo + static_cast<long long>(many - 1) * step;   // the last of them that is below
+        lo = static_cast<int>(last + 1);
+        hi = static_cast<int>(last + step < hi ? last + step : hi);
     }
     return lo;
 }
@@ -195,7 +212,7 @@ __device__ __forceinline__ unsigned span_begin(const GatedRows &rows, unsigned j
     if (rows.starts == nullptr)
         return static_cast<unsigned>(static_cast<unsigned long long>(rows.rows) * j / rows.spans) * rows.tokens;
     const int share = static_cast<int>(static_cast<unsigned long long>(all) * j / rows.spans);
-    const int r = first_start<false>(rows.starts, rows.rows + 1, share);
+    const int r = first_start(rows.starts, rows.rows + 1, share, threadIdx.x & 31);
     if (r > rows.rows) return all;
     const unsigned at = static_cast<unsigned>(__ldg(rows.starts + r));   // >= share >= 0
     return at < all ? at : all;
@@ -215,7 +232,7 @@ __device__ __forceinline__ TokenPlace place_of(const GatedRows &rows, unsigned n
         return p;
     }
     // the last row that begins at or before n: of rows that begin alike, the one with tokens
-    p.row = first_start<true>(rows.starts, rows.rows + 1, static_cast<int>(n)) - 1;
+    p.row = row_at(rows, static_cast<int>(n));
     p.inside = p.row >= 0 && p.row < rows.rows;
     p.first = p.inside && __ldg(rows.starts + p.row) == static_cast<int>(n);
     p.last = p.inside && (__ldg(rows.starts + p.row + 1) == static_cast<int>(n + 1) || n + 1 == rows.all());
