@@ -10,6 +10,7 @@ array to the device, scans it and copies the result back.
 from __future__ import annotations
 
 import array
+import operator
 
 import torch
 
@@ -570,7 +571,7 @@ def _states(t, name: str, channels: int, pool: int, here: int):
         return None
     if t.get_device() != here:
         raise ValueError(f"{name} must be a CUDA tensor on the current device")
-    if t.dim() != 2 or t.shape[0] != pool or t.shape[1] != channels or not t.is_contiguous():
+    if t.shape != (pool, channels) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous [{pool}, {channels}]")
     if t.dtype is not _F32:
         raise TypeError(f"{name} must be float32")
@@ -715,6 +716,9 @@ def expert_sort(experts: torch.Tensor, num_experts: int, align: int = 1, rows: i
 
 def _check_rows(t: torch.Tensor, name: str, rows: int, width: int, dtype: torch.dtype, here: int) -> int:
     """A matrix of that size and device; returns its row stride."""
+    strides = t.stride()
+    if t.get_device() == here and t.dtype is dtype and t.shape == (rows, width) and strides[1] == 1 and strides[0] >= width:
+        return strides[0]
     if t.get_device() != here:
         raise ValueError(f"{name} must be a CUDA tensor on the current device")
     stride = _check_matrix(t, name)
@@ -815,6 +819,7 @@ def expert_combine_backward(grad: torch.Tensor, y: torch.Tensor, places: torch.T
 
 
 _TENSOR_TYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+_DTYPE_OF = operator.attrgetter("dtype")
 
 
 def _norm(tensors, out, max_norm, norm, work, stream):
@@ -824,10 +829,11 @@ def _norm(tensors, out, max_norm, norm, work, stream):
     if len(outs) != count:
         raise ValueError("out must hold a tensor for each of tensors")
     here = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
-    kinds = [_TENSOR_TYPE.get(t.dtype) for t in tensors]
-    if None in kinds:
-        raise TypeError(f"unsupported dtype {tensors[kinds.index(None)].dtype} (float32, float16, bfloat16)")
     of = torch.Tensor                              # a method for all tensors at once: there may be hundreds
+    dtypes = list(map(_DTYPE_OF, tensors))
+    kinds = list(map(_TENSOR_TYPE.get, dtypes))
+    if None in kinds:
+        raise TypeError(f"unsupported dtype {dtypes[kinds.index(None)]} (float32, float16, bfloat16)")
     sizes = list(map(of.numel, tensors))
     at = list(map(of.data_ptr, tensors))
     if count and (set(map(of.get_device, tensors)) != {here} or here < 0 or not all(map(of.is_contiguous, tensors))):
@@ -835,7 +841,7 @@ def _norm(tensors, out, max_norm, norm, work, stream):
     to = at
     if out is not None:
         if (count and set(map(of.get_device, outs)) != {here} or not all(map(of.is_contiguous, outs))
-                or list(map(of.numel, outs)) != sizes or [_TENSOR_TYPE.get(o.dtype) for o in outs] != kinds):
+                or list(map(of.numel, outs)) != sizes or list(map(_DTYPE_OF, outs)) != dtypes):
             raise ValueError("each of out must match its tensor in type, size and device, and be contiguous")
         to = list(map(of.data_ptr, outs))
     table = array.array("Q", bytes(32 * max(count, 1)))   # of devscan_tensor, four words each
