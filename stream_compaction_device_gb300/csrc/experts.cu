@@ -192,7 +192,8 @@ __global__ void __launch_bounds__(32 * WARPS, 1) expert_sort_kernel(const __grid
 // per choice; the warps behind those look through `order`, 32 rows each, for
 // rows of padding and clear them.  Every warp is a block: it ends, and makes room
 // for the next, when its own writes are out (16,384 x 8 rows of 4 KB: 115 us
-// with four warps to a block, 109 with one, 6.1 TB/s).
+// with four warps to a block, 109 with one, 6.1 TB/s).  Rows that are not made
+// of 16 bytes move in smaller pieces; an SM then needs more warps than blocks.
 // ---------------------------------------------------------------------------
 constexpr int kMoveWarps = 4;   // of a block that combines
 
@@ -203,13 +204,13 @@ __device__ __forceinline__ unsigned padding_rows(const int32_t *order, unsigned 
     return __ballot_sync(kFullMask, r < rows && order[r] == kOrderPadding);
 }
 
-template <typename V, int U>
-__global__ void __launch_bounds__(32) expert_dispatch_kernel(const __grid_constant__ ExpertMoveCall p,
-                                                                          unsigned vectors, unsigned runs)
+template <typename V, int U, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) expert_dispatch_kernel(const __grid_constant__ ExpertMoveCall p, unsigned vectors,
+                                                                     unsigned runs)
 {
     wait_primary_grid();   // a sort before this lets it start early
-    const int lane = threadIdx.x;
-    const size_t item = blockIdx.x;
+    const int lane = threadIdx.x & 31;
+    const size_t item = static_cast<size_t>(blockIdx.x) * WARPS + (threadIdx.x >> 5);
     const size_t moves = static_cast<size_t>(p.tokens) * runs;
     if (item < moves) {
         const unsigned t = static_cast<unsigned>(item / runs), run = static_cast<unsigned>(item % runs);
@@ -242,27 +243,29 @@ __global__ void __launch_bounds__(32) expert_dispatch_kernel(const __grid_consta
     }
 }
 
-template <typename V, int U>
+template <typename V, int U, int WARPS = sizeof(V) == 16 ? 1 : 4>
 cudaError_t dispatch(const ExpertMoveCall &call, cudaStream_t s)
 {
     const unsigned vectors = static_cast<unsigned>(call.row_bytes / sizeof(V));
     const unsigned runs = (vectors + 32 * U - 1) / (32 * U);
     const size_t items = static_cast<size_t>(call.tokens) * runs + (call.order != nullptr ? (call.rows + 31u) / 32 : 0);
     if (items == 0) return cudaSuccess;
-    if (items > INT32_MAX) return cudaErrorInvalidValue;
-    return launch_dependent(expert_dispatch_kernel<V, U>, static_cast<unsigned>(items), 32, s, call, vectors, runs);
+    const size_t blocks = (items + WARPS - 1) / WARPS;
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    return launch_dependent(expert_dispatch_kernel<V, U, WARPS>, static_cast<unsigned>(blocks), 32 * WARPS, s, call, vectors, runs);
 }
 
 // ---------------------------------------------------------------------------
 // Combine.  A warp takes 32 * V columns of a token and adds the rows of its
-// choices in their order, eight loads in flight, in fp32; one rounding.  Bound
+// choices in their order, eight loads in flight, in fp32; one rounding.  (Where
+// rows are not made of 16 bytes, U pieces of V values to a lane.)  Bound
 // by the two loads behind each other, of places and of rows: 32 warps to an SM
 // and small blocks (8,191 x 6 rows of 4 KB: 47 us with eight warps to a block
 // and 24 to an SM, 40 so, 5.8 TB/s).
 // ---------------------------------------------------------------------------
 constexpr int kAtOnce = 8;   // choices whose rows are in flight together
 
-template <typename T, int V>
+template <typename T, int V, int U>
 __global__ void __launch_bounds__(32 * kMoveWarps, 8) expert_combine_kernel(const __grid_constant__ ExpertCombineCall p,
                                                                          unsigned runs)
 {
@@ -271,33 +274,50 @@ __global__ void __launch_bounds__(32 * kMoveWarps, 8) expert_combine_kernel(cons
     const size_t item = static_cast<size_t>(blockIdx.x) * kMoveWarps + (threadIdx.x >> 5);
     if (item >= static_cast<size_t>(p.tokens) * runs) return;
     const unsigned t = static_cast<unsigned>(item / runs), run = static_cast<unsigned>(item % runs);
-    const unsigned c = (run * 32 + lane) * V;
-    const bool live = c < p.width;   // a whole number of lanes is
-    const T *y = static_cast<const T *>(p.y) + c;
+    constexpr int kRows = U > 1 ? kAtOnce / 2 : kAtOnce;   // whose pieces are in flight together
+    unsigned c[U];
+    bool live[U];   // a whole number of lanes is
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        c[u] = ((run * U + u) * 32 + lane) * V;
+        live[u] = c[u] < p.width;
+    }
+    const T *y = static_cast<const T *>(p.y);
     const size_t pair0 = static_cast<size_t>(t) * p.choices;
-    float sum[V] = {};
-    for (int k0 = 0; k0 < p.choices; k0 += kAtOnce) {
-        const bool have = lane < kAtOnce && k0 + lane < p.choices;
+    float sum[U][V] = {};
+    for (int k0 = 0; k0 < p.choices; k0 += kRows) {
+        const bool have = lane < kRows && k0 + lane < p.choices;
         const int place_here = have ? p.places[pair0 + k0 + lane] : -1;
         const float weight_here = have && p.weights != nullptr ? p.weights[pair0 + k0 + lane] : 1.0f;
-        R r[kAtOnce];
+        R r[kRows][U];
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
+        for (int j = 0; j < kRows; ++j) {
             const unsigned place = static_cast<unsigned>(__shfl_sync(kFullMask, place_here, j));
-            if (place < p.rows && live) r[j] = *reinterpret_cast<const R *>(y + place * p.y_stride);
+            const T *row = y + place * p.y_stride;
+            if (place >= p.rows) continue;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (live[u]) r[j][u] = *reinterpret_cast<const R *>(row + c[u]);
         }
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
+        for (int j = 0; j < kRows; ++j) {
             const unsigned place = static_cast<unsigned>(__shfl_sync(kFullMask, place_here, j));
             const float w = __shfl_sync(kFullMask, weight_here, j);
-            if (place >= p.rows || !live) continue;
-            float v[V];
-            unpack<T, V>(r[j], v);
+            if (place >= p.rows) continue;
 #pragma unroll
-            for (int i = 0; i < V; ++i) sum[i] = fmaf(w, v[i], sum[i]);
+            for (int u = 0; u < U; ++u) {
+                if (!live[u]) continue;
+                float v[V];
+                unpack<T, V>(r[j][u], v);
+#pragma unroll
+                for (int i = 0; i < V; ++i) sum[u][i] = fmaf(w, v[i], sum[u][i]);
+            }
         }
     }
-    if (live) *reinterpret_cast<R *>(static_cast<T *>(p.out) + t * p.out_stride + c) = pack<T, V>(sum);
+    T *out = static_cast<T *>(p.out) + t * p.out_stride;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (live[u]) *reinterpret_cast<R *>(out + c[u]) = pack<T, V>(sum[u]);
 }
 
 // ---------------------------------------------------------------------------
@@ -308,8 +328,8 @@ __global__ void __launch_bounds__(32 * kMoveWarps, 8) expert_combine_kernel(cons
 // ---------------------------------------------------------------------------
 constexpr int kBackWarps = 4;
 
-template <typename T, int V>
-__global__ void __launch_bounds__(32 * kBackWarps, 6) expert_combine_backward_kernel(
+template <typename T, int V, int U>
+__global__ void __launch_bounds__(32 * kBackWarps, U > 1 ? 4 : 6) expert_combine_backward_kernel(
     const __grid_constant__ ExpertCombineBackwardCall p)
 {
     using R = typename Raw<T, V>::type;
@@ -339,27 +359,43 @@ __global__ void __launch_bounds__(32 * kBackWarps, 6) expert_combine_backward_ke
             place[j] = static_cast<unsigned>(__shfl_sync(kFullMask, place_here, j));
             weight[j] = __shfl_sync(kFullMask, weight_here, j);
         }
-        for (unsigned c = threadIdx.x * V; c < p.width; c += 32 * kBackWarps * V) {
-            float g[V];
-            R r[kAtOnce];
-            if (p.grad_weights != nullptr)
+        constexpr unsigned kAcross = 32 * kBackWarps * V;   // columns that the block has at once
+        for (unsigned c0 = threadIdx.x * V; c0 < p.width; c0 += U * kAcross) {
+            R g[U];
 #pragma unroll
-                for (int j = 0; j < kAtOnce; ++j)
-                    if (place[j] < p.rows)
-                        r[j] = *reinterpret_cast<const R *>(static_cast<const T *>(p.y) + place[j] * p.y_stride + c);
-            unpack<T, V>(*reinterpret_cast<const R *>(grad + c), g);
+            for (int u = 0; u < U; ++u)
+                if (c0 + u * kAcross < p.width) g[u] = *reinterpret_cast<const R *>(grad + c0 + u * kAcross);
+            constexpr int kRows = U > 1 ? kAtOnce / 2 : kAtOnce;   // whose pieces are in flight together
 #pragma unroll
-            for (int j = 0; j < kAtOnce; ++j) {
-                if (place[j] >= p.rows) continue;
-                float v[V];
-                if (p.grad_weights != nullptr) {
-                    unpack<T, V>(r[j], v);
+            for (int j0 = 0; j0 < kAtOnce; j0 += kRows) {
+                R r[kRows][U];
+                if (p.grad_weights != nullptr)
 #pragma unroll
-                    for (int i = 0; i < V; ++i) sum[j] = fmaf(g[i], v[i], sum[j]);
+                    for (int j = 0; j < kRows; ++j)
+                        if (place[j0 + j] < p.rows)
+#pragma unroll
+                            for (int u = 0; u < U; ++u)
+                                if (c0 + u * kAcross < p.width)
+                                    r[j][u] = *reinterpret_cast<const R *>(static_cast<const T *>(p.y) + place[j0 + j] * p.y_stride + c0 + u * kAcross);
+#pragma unroll
+                for (int j = 0; j < kRows; ++j) {
+                    if (place[j0 + j] >= p.rows) continue;
+                    T *to = static_cast<T *>(p.grad_y) + place[j0 + j] * p.grad_y_stride + c0;
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        if (c0 + u * kAcross >= p.width) continue;
+                        float gv[V], v[V];
+                        unpack<T, V>(g[u], gv);
+                        if (p.grad_weights != nullptr) {
+                            unpack<T, V>(r[j][u], v);
+#pragma unroll
+                            for (int i = 0; i < V; ++i) sum[j0 + j] = fmaf(gv[i], v[i], sum[j0 + j]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < V; ++i) v[i] = weight[j0 + j] * gv[i];
+                        *reinterpret_cast<R *>(to + u * kAcross) = pack<T, V>(v);
+                    }
                 }
-#pragma unroll
-                for (int i = 0; i < V; ++i) v[i] = weight[j] * g[i];
-                *reinterpret_cast<R *>(static_cast<T *>(p.grad_y) + place[j] * p.grad_y_stride + c) = pack<T, V>(v);
             }
         }
         if (p.grad_weights == nullptr) continue;
@@ -416,48 +452,50 @@ template <typename Id, int WARPS> cudaError_t sort(ExpertSortCall call, cudaStre
     return cudaLaunchKernelEx(&cfg, kernel, call);
 }
 
-bool wide_rows(const void *p, size_t stride, size_t width, size_t size)
+bool rows_of(size_t unit, const void *p, size_t stride, size_t width, size_t size)
 {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * size % 16 == 0 && width * size % 16 == 0;
+    return reinterpret_cast<uintptr_t>(p) % unit == 0 && stride * size % unit == 0 && width * size % unit == 0;
 }
 
-template <typename T, int V>
+template <typename T, int V, int U>
 cudaError_t combine(const ExpertCombineCall &call, cudaStream_t s)
 {
-    const unsigned runs = (call.width + 32 * V - 1) / (32 * V);
+    const unsigned runs = (call.width + 32 * V * U - 1) / (32 * V * U);
     const size_t blocks = (static_cast<size_t>(call.tokens) * runs + kMoveWarps - 1) / kMoveWarps;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    expert_combine_kernel<T, V><<<static_cast<unsigned>(blocks), 32 * kMoveWarps, 0, s>>>(call, runs);
+    expert_combine_kernel<T, V, U><<<static_cast<unsigned>(blocks), 32 * kMoveWarps, 0, s>>>(call, runs);
     return cudaGetLastError();
 }
 template <typename T>
 cudaError_t combine_any(const ExpertCombineCall &call, cudaStream_t s)
 {
-    constexpr int V = 16 / sizeof(T);
-    if (wide_rows(call.y, call.y_stride, call.width, sizeof(T)) && wide_rows(call.out, call.out_stride, call.width, sizeof(T)))
-        return combine<T, V>(call, s);
-    return combine<T, 1>(call, s);
+    const auto made_of = [&](size_t unit) {
+        return rows_of(unit, call.y, call.y_stride, call.width, sizeof(T)) && rows_of(unit, call.out, call.out_stride, call.width, sizeof(T));
+    };
+    if (made_of(16)) return combine<T, 16 / sizeof(T), 1>(call, s);
+    return made_of(2 * sizeof(T)) ? combine<T, 2, 4>(call, s) : combine<T, 1, 4>(call, s);
 }
 
-template <typename T, int V>
+template <typename T, int V, int U>
 cudaError_t combine_backward(const ExpertCombineBackwardCall &call, cudaStream_t s)
 {
     const size_t blocks = static_cast<size_t>(call.tokens) +
                           (call.order != nullptr ? (call.rows + 32u * kBackWarps - 1) / (32 * kBackWarps) : 0);
     if (blocks == 0) return cudaSuccess;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    expert_combine_backward_kernel<T, V><<<static_cast<unsigned>(blocks), 32 * kBackWarps, 0, s>>>(call);
+    expert_combine_backward_kernel<T, V, U><<<static_cast<unsigned>(blocks), 32 * kBackWarps, 0, s>>>(call);
     return cudaGetLastError();
 }
 template <typename T>
 cudaError_t combine_backward_any(const ExpertCombineBackwardCall &call, cudaStream_t s)
 {
-    constexpr int V = 16 / sizeof(T);
-    const size_t w = call.width;
-    if (wide_rows(call.grad, call.grad_stride, w, sizeof(T)) && wide_rows(call.y, call.y_stride, w, sizeof(T)) &&
-        wide_rows(call.grad_y, call.grad_y_stride, w, sizeof(T)))
-        return combine_backward<T, V>(call, s);
-    return combine_backward<T, 1>(call, s);
+    const size_t w = call.width, n = sizeof(T);
+    const auto made_of = [&](size_t unit) {
+        return rows_of(unit, call.grad, call.grad_stride, w, n) && rows_of(unit, call.grad_y, call.grad_y_stride, w, n) &&
+               (call.grad_weights == nullptr || rows_of(unit, call.y, call.y_stride, w, n));
+    };
+    if (made_of(16)) return combine_backward<T, 16 / sizeof(T), 1>(call, s);
+    return made_of(2 * n) ? combine_backward<T, 2, 4>(call, s) : combine_backward<T, 1, 4>(call, s);
 }
 
 }  // namespace
@@ -481,9 +519,10 @@ cudaError_t launch_expert_dispatch(const ExpertMoveCall &call, cudaStream_t s)
         if (lanes >= size_t(1) << 20) return dispatch<uint4, 8>(call, s);
         return lanes >= size_t(1) << 17 ? dispatch<uint4, 4>(call, s) : dispatch<uint4, 1>(call, s);
     }
-    if (all % 4 == 0) return dispatch<unsigned, 4>(call, s);
-    if (all % 2 == 0) return dispatch<unsigned short, 4>(call, s);
-    return dispatch<unsigned char, 4>(call, s);
+    if (all % 8 == 0) return dispatch<uint2, 8>(call, s);
+    if (all % 4 == 0) return dispatch<unsigned, 8>(call, s);
+    if (all % 2 == 0) return dispatch<unsigned short, 8>(call, s);
+    return dispatch<unsigned char, 8>(call, s);
 }
 
 cudaError_t launch_expert_combine(ValueType type, const ExpertCombineCall &call, cudaStream_t s)

@@ -45,7 +45,7 @@ namespace gated {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr unsigned kStepThreads = 128;   // of a decode step's block
-constexpr int kMostBlocks = 8;   // of a cluster (the portable size)
+constexpr int kPortableBlocks = 8, kMostBlocks = 16;   // of a cluster
 constexpr int kMostPerSm = 3;   // blocks, where two stages of the ring fit
 // Shared memory for a block's ring where an SM holds `blocks`: of its 228 KB,
 // 1 KB and the exchange go off for each.
@@ -53,12 +53,14 @@ constexpr int ring_bytes(int blocks) { return (228 << 10) / blocks - (18 << 10);
 // Tokens of a warp and round where the values of a lane and token have `bytes`
 // bytes: as many as two blocks per SM hold twice (long rows: fewer rounds), or
 // fewer, where rows are short.
-// `both`: the recurrence's a and b stay in registers.
-constexpr int tokens_per_round(int bytes, int copy, bool many, bool both)
+// `both`: the recurrence's a and b stay in registers; `values`: arrays beside
+// the gates.  Without asynchronous copies it is registers that end it.
+constexpr int tokens_per_round(int bytes, int copy, bool many, bool both, int values)
 {
+    if (copy == 0) return !many ? 8 : values > 1 ? 12 : both ? 16 : 24;
     const int most = ring_bytes(2) / (2 * kWarps * 32 * bytes) / 4 * 4;
-    const int some = bytes <= 8 && copy > 0 && !both ? 12 : 8;
-    return copy == 0 || !many ? some : both && most > 16 ? 16 : most;
+    const int some = bytes <= 8 && !both ? 12 : 8;
+    return !many ? some : both && most > 16 ? 16 : most;
 }
 
 // ---------------------------------------------------------------------------
@@ -364,11 +366,11 @@ __device__ __forceinline__ void copy_tokens(const GatedRows &rows, const GatedAr
 // that comes into it.  The cluster's last warp hands on what goes out of it as
 // the next round's carry.
 // ---------------------------------------------------------------------------
-template <int V> struct Exchange {
+template <int V, int BLOCKS> struct Exchange {   // BLOCKS: the most of a cluster
     Lanes<V> a[2][kWarps][32], h[2][kWarps][32];                       // this block's warps
-    Lanes<V> all_a[2][kMostBlocks][32], all_h[2][kMostBlocks][32];     // the cluster's blocks
+    Lanes<V> all_a[2][BLOCKS][32], all_h[2][BLOCKS][32];     // the cluster's blocks
     Lanes<V> carry[2][32];
-    unsigned cut[2][kWarps], all_cut[2][kMostBlocks];                  // nonzero: the map forgets what comes in
+    unsigned cut[2][kWarps], all_cut[2][BLOCKS];                  // nonzero: the map forgets what comes in
 };
 
 template <int V> __device__ __forceinline__ Lanes<V> follow(bool cut, Lanes<V> a, Lanes<V> in, Lanes<V> h)
@@ -389,8 +391,8 @@ template <int V> __device__ __forceinline__ void st_lanes(uint32_t to, Lanes<V> 
 // Two buffers in turn are enough: a block writes a round's buffer after the
 // barrier of the round before, at which every reader of the round before that
 // has arrived.
-template <int V>
-__device__ __forceinline__ Lanes<V> exchange(Exchange<V> &x, int turn, int blocks, int rank, int warp, int lane,
+template <int V, int BLOCKS>
+__device__ __forceinline__ Lanes<V> exchange(Exchange<V, BLOCKS> &x, int turn, int blocks, int rank, int warp, int lane,
                                              Lanes<V> a, Lanes<V> h, bool cut)
 {
     x.a[turn][warp][lane] = a, x.h[turn][warp][lane] = h;
@@ -429,17 +431,20 @@ __device__ __forceinline__ Lanes<V> exchange(Exchange<V> &x, int turn, int block
             fa = c ? wa : wa * fa;
         }
     }
-    if (warp < blocks) {   // warp q tells block q
-        st_lanes<V>(cluster_addr(&x.all_a[turn][rank][lane], warp), fa);
-        st_lanes<V>(cluster_addr(&x.all_h[turn][rank][lane], warp), fh);
-        if (lane == 0) st_cluster(cluster_addr(&x.all_cut[turn][rank], warp), cuts);
+#pragma unroll
+    for (int q0 = 0; q0 < BLOCKS; q0 += kWarps) {   // warp q tells block q, and q + kWarps
+        const int q = q0 + warp;
+        if (q >= blocks) break;
+        st_lanes<V>(cluster_addr(&x.all_a[turn][rank][lane], q), fa);
+        st_lanes<V>(cluster_addr(&x.all_h[turn][rank][lane], q), fh);
+        if (lane == 0) st_cluster(cluster_addr(&x.all_cut[turn][rank], q), cuts);
     }
     cluster_sync();
     Lanes<V> in = x.carry[turn][lane];
-    const unsigned all_cuts = __ballot_sync(kFullMask, lane < blocks && x.all_cut[turn][lane & (kMostBlocks - 1)] != 0);
+    const unsigned all_cuts = __ballot_sync(kFullMask, lane < blocks && x.all_cut[turn][lane & (BLOCKS - 1)] != 0);
     if (all_cuts == 0) {
 #pragma unroll
-        for (int q = 0; q < kMostBlocks - 1; ++q)
+        for (int q = 0; q < BLOCKS - 1; ++q)
             if (q < rank) in = fma(x.all_a[turn][q][lane], in, x.all_h[turn][q][lane]);
     } else {
 #pragma unroll 1
@@ -451,8 +456,8 @@ __device__ __forceinline__ Lanes<V> exchange(Exchange<V> &x, int turn, int block
 
 // What goes out of the cluster's last warp.  Not after the last round: another
 // block may have left by then.
-template <int V>
-__device__ __forceinline__ void hand_on(Exchange<V> &x, int turn, int blocks, int rank, int warp, int lane, Lanes<V> h)
+template <int V, int BLOCKS>
+__device__ __forceinline__ void hand_on(Exchange<V, BLOCKS> &x, int turn, int blocks, int rank, int warp, int lane, Lanes<V> h)
 {
     if (rank != blocks - 1 || warp != kWarps - 1) return;
     if (blocks == 1) {
@@ -582,7 +587,7 @@ template <typename X, typename G, int V, int L, int VALUES, int COPY> struct Rin
 
 template <typename X, typename G, int V, int VALUES> constexpr int kLaneBytes = V * (VALUES * static_cast<int>(sizeof(X)) + static_cast<int>(sizeof(G)));
 template <typename X, typename G, int V, int VALUES, int COPY, bool MANY, bool BOTH>
-using RingOf = Ring<X, G, V, tokens_per_round(kLaneBytes<X, G, V, VALUES>, COPY, MANY, BOTH), VALUES, COPY>;
+using RingOf = Ring<X, G, V, tokens_per_round(kLaneBytes<X, G, V, VALUES>, COPY, MANY, BOTH, VALUES), VALUES, COPY>;
 template <typename X, typename G, int V, int KIND, int COPY, bool MANY>
 using ForwardRing = RingOf<X, G, V, 1, COPY, MANY, KIND == kGateSigmoid>;
 template <typename X, typename G, int V, int KIND, int COPY, bool MANY>
@@ -591,7 +596,7 @@ using BackwardRing = RingOf<X, G, V, KIND == kGateSigmoid ? 3 : 2, COPY, MANY, f
 // ---------------------------------------------------------------------------
 // Forward.
 // ---------------------------------------------------------------------------
-template <typename X, typename G, int V, int KIND, int COPY, bool MANY>
+template <typename X, typename G, int V, int KIND, int COPY, bool MANY, int BLOCKS>
 __global__ void __launch_bounds__(kThreads, (ForwardRing<X, G, V, KIND, COPY, MANY>::kPerSm))
  gated_scan_kernel(const __grid_constant__ GatedScanCall p)
 {
@@ -601,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, (ForwardRing<X, G, V, KIND, COPY, MA
     using RX = typename R::RX;
     using RG = typename R::RG;
     extern __shared__ __align__(16) char s_ring[];
-    __shared__ Exchange<V> s_x;
+    __shared__ Exchange<V, BLOCKS> s_x;
     const int lane = threadIdx.x & 31, warp = __shfl_sync(kFullMask, threadIdx.x >> 5, 0);
     const Work w = work_of(p.rows, V);
     const bool live = w.channel < p.rows.channels;   // a whole number of lanes is
@@ -710,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, (ForwardRing<X, G, V, KIND, COPY, MA
                 fa = c ? all<V>(0.0f) : fa * a[i];
             }
         }
-        h = exchange<V>(s_x, step & 1, w.blocks, w.rank, warp, lane, fa, h, cut != 0);
+        h = exchange(s_x, step & 1, w.blocks, w.rank, warp, lane, fa, h, cut != 0);
         if (plain) {
             X *to = out + element(p.out, r.row, r.t);
 #pragma unroll
@@ -719,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, (ForwardRing<X, G, V, KIND, COPY, MA
                 if (live) *reinterpret_cast<RX *>(to) = pack<X, V>(h.v);
                 to += p.out.stride;
             }
-            if (step + 1 < rounds) hand_on<V>(s_x, (step + 1) & 1, w.blocks, w.rank, warp, lane, h);
+            if (step + 1 < rounds) hand_on(s_x, (step + 1) & 1, w.blocks, w.rank, warp, lane, h);
             __syncwarp();   // the stage has been read
             continue;
         }
@@ -733,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, (ForwardRing<X, G, V, KIND, COPY, MA
             h = follow((cut >> i) & 1u, a[i], h, now);
             a[i] = h;
         }
-        if (step + 1 < rounds) hand_on<V>(s_x, (step + 1) & 1, w.blocks, w.rank, warp, lane, h);
+        if (step + 1 < rounds) hand_on(s_x, (step + 1) & 1, w.blocks, w.rank, warp, lane, h);
         __syncwarp();   // the stage has been read
         if (live && r.count > 0)
             walk<L, false>(p.rows, p.out, r, [&](int i, size_t at) { *reinterpret_cast<RX *>(out + at) = pack<X, V>(a[i].v); });
@@ -760,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, (ForwardRing<X, G, V, KIND, COPY, MA
 // h_{t-1} is what the forward call wrote, in its type.  It (and x) is taken
 // from the ring after the exchange, so that registers hold a, dh and r only.
 // ---------------------------------------------------------------------------
-template <typename X, typename G, int V, int KIND, int COPY, bool MANY>
+template <typename X, typename G, int V, int KIND, int COPY, bool MANY, int BLOCKS>
 __global__ void __launch_bounds__(kThreads, (BackwardRing<X, G, V, KIND, COPY, MANY>::kPerSm))
  gated_scan_backward_kernel(const __grid_constant__ GatedBackwardCall p)
 {
@@ -770,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, (BackwardRing<X, G, V, KIND, COPY, M
     using RX = typename R::RX;
     using RG = typename R::RG;
     extern __shared__ __align__(16) char s_ring[];
-    __shared__ Exchange<V> s_x;
+    __shared__ Exchange<V, BLOCKS> s_x;
     const int lane = threadIdx.x & 31, warp = __shfl_sync(kFullMask, threadIdx.x >> 5, 0);
     const Work w = work_of(p.rows, V);
     const bool live = w.channel < p.rows.channels;
@@ -887,7 +892,7 @@ __global__ void __launch_bounds__(kThreads, (BackwardRing<X, G, V, KIND, COPY, M
                 fa = c ? all<V>(0.0f) : fa * a[i];
             }
         }
-        f = exchange<V>(s_x, step & 1, w.blocks, w.rank, warp, lane, fa, f, cut != 0);
+        f = exchange(s_x, step & 1, w.blocks, w.rank, warp, lane, fa, f, cut != 0);
         // the gradients of token i from w = v and h_{t-1}
         auto gradients = [&](int i, Lanes<V> v, Lanes<V> before, Lanes<V> &gx, Lanes<V> &gg) {
             gx = v;
@@ -914,7 +919,7 @@ __global__ void __launch_bounds__(kThreads, (BackwardRing<X, G, V, KIND, COPY, M
                 }
                 to_x -= p.grad_x.stride, to_gate -= p.grad_gate.stride;
             }
-            if (step + 1 < rounds) hand_on<V>(s_x, (step + 1) & 1, w.blocks, w.rank, warp, lane, f);
+            if (step + 1 < rounds) hand_on(s_x, (step + 1) & 1, w.blocks, w.rank, warp, lane, f);
             __syncwarp();   // the stage has been read
             continue;
         }
@@ -938,7 +943,7 @@ __global__ void __launch_bounds__(kThreads, (BackwardRing<X, G, V, KIND, COPY, M
             gradients(i, v, before, gx, gg);
             a[i] = out ? all<V>(0.0f) : gx, d[i] = out ? all<V>(0.0f) : gg;
         }
-        if (step + 1 < rounds) hand_on<V>(s_x, (step + 1) & 1, w.blocks, w.rank, warp, lane, f);
+        if (step + 1 < rounds) hand_on(s_x, (step + 1) & 1, w.blocks, w.rank, warp, lane, f);
         if (live && r.count > 0) {
             walk<L, true>(p.rows, p.grad_x, r, [&](int i, size_t at) { *reinterpret_cast<RX *>(grad_x + at) = pack<X, V>(a[i].v); });
             walk<L, true>(p.rows, p.grad_gate, r, [&](int i, size_t at) { *reinterpret_cast<RG *>(grad_gate + at) = pack<G, V>(d[i].v); });
@@ -1033,7 +1038,7 @@ inline void lay_out(GatedRows &rows, std::initializer_list<const GatedArray *> a
 // and every block has a round's tokens.  (An exchange between blocks costs about
 // a fifth of a round: backward, 8 x 4096 x 4096, 266 us with one block for a
 // span and 319 with two.)
-inline void plan(GatedRows &rows, int per_lane, int tokens_per_warp, int places_per_sm, int sms)
+inline void plan(GatedRows &rows, int per_lane, int tokens_per_warp, int places_per_sm, bool many, int sms)
 {
     const size_t all = rows.all(), groups = (static_cast<size_t>(rows.channels) + 32 * per_lane - 1) / (32 * per_lane);
     const size_t places = static_cast<size_t>(sms) * places_per_sm, tile = static_cast<size_t>(kWarps) * tokens_per_warp;
@@ -1043,7 +1048,11 @@ inline void plan(GatedRows &rows, int per_lane, int tokens_per_warp, int places_
     if (spans > most) spans = most;
     if (spans < 1) spans = 1;
     size_t blocks = 1;
-    while (blocks < kMostBlocks && 2 * groups * spans * blocks <= places && spans * blocks * tile < all) blocks *= 2;
+    while (blocks < kPortableBlocks && 2 * groups * spans * blocks <= places && spans * blocks * tile < all) blocks *= 2;
+    // More than the portable size where all of them leave half of the SMs without a
+    // block (3 x 30,000 x 128 bf16: 57 us with eight blocks, 37 with sixteen).
+    if (many && blocks == kPortableBlocks && kMostBlocks * groups * spans <= static_cast<size_t>(sms) && spans * blocks * tile < all)
+        blocks = kMostBlocks;
     rows.groups = static_cast<unsigned>(groups), rows.spans = static_cast<unsigned>(spans);
     rows.blocks = static_cast<int>(blocks);
 }
@@ -1055,8 +1064,11 @@ inline bool many_tokens(const GatedRows &rows) { return rows.all() / static_cast
 template <typename Call>
 cudaError_t launch_clusters(void (*kernel)(Call), const Call &call, int ring, std::atomic<unsigned long long> &done, cudaStream_t s)
 {
-    const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), ring, done);
+    cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), ring, done);
     if (e != cudaSuccess) return e;
+    if (call.rows.blocks > kPortableBlocks &&
+        (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
+        return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(call.rows.groups * call.rows.spans * static_cast<unsigned>(call.rows.blocks));
     cfg.blockDim = dim3(kThreads);
@@ -1075,17 +1087,19 @@ cudaError_t launch_clusters(void (*kernel)(Call), const Call &call, int ring, st
 template <typename X, typename G, int V, int KIND, int COPY, bool MANY>
 cudaError_t forward_of(GatedScanCall call, int sms, cudaStream_t s)
 {
-    static std::atomic<unsigned long long> done;
+    static std::atomic<unsigned long long> done, more;
     using R = ForwardRing<X, G, V, KIND, COPY, MANY>;
     lay_out(call.rows, {&call.x, &call.gate, &call.out});
-    plan(call.rows, V, R::kTokens, R::kPerSm, sms);
-    return launch_clusters(gated_scan_kernel<X, G, V, KIND, COPY, MANY>, call, R::kBytes, done, s);
+    plan(call.rows, V, R::kTokens, R::kPerSm, MANY, sms);
+    if constexpr (MANY)
+        if (call.rows.blocks > kPortableBlocks)
+            return launch_clusters(gated_scan_kernel<X, G, V, KIND, COPY, MANY, kMostBlocks>, call, R::kBytes, more, s);
+    return launch_clusters(gated_scan_kernel<X, G, V, KIND, COPY, MANY, kPortableBlocks>, call, R::kBytes, done, s);
 }
 template <typename X, typename G, int V, int KIND, int COPY>
 cudaError_t forward(const GatedScanCall &call, int sms, cudaStream_t s)
 {
-    if constexpr (COPY > 0)
-        if (many_tokens(call.rows)) return forward_of<X, G, V, KIND, COPY, true>(call, sms, s);
+    if (many_tokens(call.rows)) return forward_of<X, G, V, KIND, COPY, true>(call, sms, s);
     return forward_of<X, G, V, KIND, COPY, false>(call, sms, s);
 }
 template <typename X, typename G, int N, int KIND>
@@ -1128,17 +1142,19 @@ cudaError_t forward_any(const GatedScanCall &call, int sms, cudaStream_t s)
 template <typename X, typename G, int V, int KIND, int COPY, bool MANY>
 cudaError_t backward_of(GatedBackwardCall call, int sms, cudaStream_t s)
 {
-    static std::atomic<unsigned long long> done;
+    static std::atomic<unsigned long long> done, more;
     using R = BackwardRing<X, G, V, KIND, COPY, MANY>;
     lay_out(call.rows, {&call.grad, &call.gate, &call.y, &call.grad_x, &call.grad_gate, KIND == kGateSigmoid ? &call.x : &call.y});
-    plan(call.rows, V, R::kTokens, R::kPerSm, sms);
-    return launch_clusters(gated_scan_backward_kernel<X, G, V, KIND, COPY, MANY>, call, R::kBytes, done, s);
+    plan(call.rows, V, R::kTokens, R::kPerSm, MANY, sms);
+    if constexpr (MANY)
+        if (call.rows.blocks > kPortableBlocks)
+            return launch_clusters(gated_scan_backward_kernel<X, G, V, KIND, COPY, MANY, kMostBlocks>, call, R::kBytes, more, s);
+    return launch_clusters(gated_scan_backward_kernel<X, G, V, KIND, COPY, MANY, kPortableBlocks>, call, R::kBytes, done, s);
 }
 template <typename X, typename G, int V, int KIND, int COPY>
 cudaError_t backward(const GatedBackwardCall &call, int sms, cudaStream_t s)
 {
-    if constexpr (COPY > 0)
-        if (many_tokens(call.rows)) return backward_of<X, G, V, KIND, COPY, true>(call, sms, s);
+    if (many_tokens(call.rows)) return backward_of<X, G, V, KIND, COPY, true>(call, sms, s);
     return backward_of<X, G, V, KIND, COPY, false>(call, sms, s);
 }
 template <typename X, typename G, int KIND>
