@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) expert_sort_kernel(const __grid
 // ---------------------------------------------------------------------------
 // Dispatch.  A warp takes a token's run of 32 * U vectors, reads it once and
 // writes it to each of the token's places, so that x is read once and not once
-// per choice; the warps behind those look through `order`, 32 rows each, for
+// per choice; the warps behind those look through `order`, eight rows each, for
 // rows of padding and clear them.  Every warp is a block: it ends, and makes room
 // for the next, when its own writes are out (16,384 x 8 rows of 4 KB: 115 us
 // with four warps to a block, 109 with one, 6.1 TB/s).  Rows that are not made
@@ -197,11 +197,12 @@ __global__ void __launch_bounds__(32 * WARPS, 1) expert_sort_kernel(const __grid
 // ---------------------------------------------------------------------------
 constexpr int kMoveWarps = 4;   // of a block that combines
 
-// The rows among order[r0 .. r0 + 32) that are padding, a bit each.
+// The rows among order[r0 .. r0 + kPadRows) that are padding, a bit each.
+constexpr int kPadRows = 8;
 __device__ __forceinline__ unsigned padding_rows(const int32_t *order, unsigned r0, unsigned rows, int lane)
 {
     const unsigned r = r0 + lane;
-    return __ballot_sync(kFullMask, r < rows && order[r] == kOrderPadding);
+    return __ballot_sync(kFullMask, lane < kPadRows && r < rows && order[r] == kOrderPadding);
 }
 
 template <typename V, int U, int WARPS>
@@ -235,7 +236,7 @@ __global__ void __launch_bounds__(32 * WARPS) expert_dispatch_kernel(const __gri
         }
         return;
     }
-    const size_t r0 = (item - moves) * 32;
+    const size_t r0 = (item - moves) * kPadRows;
     if (p.order == nullptr || r0 >= p.rows) return;
     for (unsigned found = padding_rows(p.order, static_cast<unsigned>(r0), p.rows, lane); found != 0; found &= found - 1) {
         V *to = reinterpret_cast<V *>(static_cast<char *>(p.to) + (r0 + __ffs(found) - 1) * p.to_stride);
@@ -248,7 +249,7 @@ cudaError_t dispatch(const ExpertMoveCall &call, cudaStream_t s)
 {
     const unsigned vectors = static_cast<unsigned>(call.row_bytes / sizeof(V));
     const unsigned runs = (vectors + 32 * U - 1) / (32 * U);
-    const size_t items = static_cast<size_t>(call.tokens) * runs + (call.order != nullptr ? (call.rows + 31u) / 32 : 0);
+    const size_t items = static_cast<size_t>(call.tokens) * runs + (call.order != nullptr ? (call.rows + kPadRows - 1u) / kPadRows : 0);
     if (items == 0) return cudaSuccess;
     const size_t blocks = (items + WARPS - 1) / WARPS;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
@@ -336,7 +337,7 @@ __global__ void __launch_bounds__(32 * kBackWarps, U > 1 ? 4 : 6) expert_combine
     __shared__ float s_sum[kBackWarps][kAtOnce];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (blockIdx.x >= p.tokens) {   // rows of padding
-        const size_t r0 = (static_cast<size_t>(blockIdx.x - p.tokens) * kBackWarps + warp) * 32;
+        const size_t r0 = (static_cast<size_t>(blockIdx.x - p.tokens) * kBackWarps + warp) * kPadRows;
         if (r0 >= p.rows) return;
         for (unsigned found = padding_rows(p.order, static_cast<unsigned>(r0), p.rows, lane); found != 0;
              found &= found - 1) {
@@ -480,7 +481,7 @@ template <typename T, int V, int U>
 cudaError_t combine_backward(const ExpertCombineBackwardCall &call, cudaStream_t s)
 {
     const size_t blocks = static_cast<size_t>(call.tokens) +
-                          (call.order != nullptr ? (call.rows + 32u * kBackWarps - 1) / (32 * kBackWarps) : 0);
+                          (call.order != nullptr ? (call.rows + kPadRows * kBackWarps - 1u) / (kPadRows * kBackWarps) : 0);
     if (blocks == 0) return cudaSuccess;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     expert_combine_backward_kernel<T, V, U><<<static_cast<unsigned>(blocks), 32 * kBackWarps, 0, s>>>(call);
