@@ -585,7 +585,8 @@ devscan_status gated_scan_backward_bf16(const uint16_t *grad, size_t grad_row_st
  * (expert_sort gives none) leave either's row.  No buffer that is written may
  * overlap another (DEVSCAN_ERR_INVALID).  No scratch; the same call gives the
  * same bits.  Rows that begin on 16 bytes and are a multiple of 16 bytes long
- * move fastest.
+ * move fastest.  expert_dispatch behind expert_sort on a stream is set up while
+ * the sort still runs.
  * ------------------------------------------------------------------------- */
 #define DEVSCAN_MAX_EXPERTS 1024
 
@@ -639,8 +640,9 @@ devscan_status expert_combine_backward_bf16(const uint16_t *grad, size_t grad_st
  *   work    : device scratch of the caller's, 8-byte aligned, of work_bytes >=
  *             DEVSCAN_NORM_WORK_BYTES(count); its content before and after
  *             means nothing, and two calls that may run at once need one each.
- * Two launches (for every 512 tensors).  Traffic: each tensor once for the
- * norm; to clip, once more and written, unless nothing is to be done in place.
+ * One launch for every 512 tensors, and one more for the norm or, to clip, for
+ * every 512 tensors.  Traffic: each tensor once for the norm; to clip, once more
+ * and written, unless nothing is to be done in place.
  * ------------------------------------------------------------------------- */
 typedef enum devscan_type { DEVSCAN_TYPE_F32 = 0, DEVSCAN_TYPE_F16 = 1, DEVSCAN_TYPE_BF16 = 2 } devscan_type;
 typedef struct devscan_tensor {

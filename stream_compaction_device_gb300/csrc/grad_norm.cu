@@ -15,7 +15,13 @@
 // fp32 and its shares in fp64.  Where a share's fp32 sum leaves the range in
 // which no square that matters is lost or overflows, the share is added again
 // in fp64 from its registers.  fp64 goes at two a clock and SM here, so one
-// warp folds what a block has, and one thread takes the root.
+// warp folds what a block has, and one thread takes the root (with all threads
+// doing so, 1.3 M fp32 in 40 tensors took 19.5 us instead of 7.7).
+//
+// What bounds it: memory.  1.5 G values in 300 tensors (5.9 GB in and out, read
+// once more for the norm) 1,422 us, 6.2 TB/s; the norm of 1 G bf16 321 us.
+// Blocks of 512 threads cost small calls 6 us; two or eight loads in flight
+// instead of four, large ones a third.
 #include <algorithm>
 
 #include "convert.cuh"
