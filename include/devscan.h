@@ -470,7 +470,8 @@ devscan_status sample_tokens_bf16(const uint16_t *logits, size_t rows, size_t vo
  *             outputs' tokens must not overlap).  gate has x's type, or with
  *             gate_f32 != 0 is fp32 (always so in the f32 calls).
  *   rows, tokens : rows of `tokens` each; tokens == 1 is a decode step (one
- *             launch without any exchange).  rows * tokens < INT32_MAX - 1;
+ *             launch without any exchange).  rows * tokens < INT32_MAX,
+ *             channels < INT32_MAX - 128;
  *   starts  : NULL, or device int32[rows + 1], not decreasing: the rows lie
  *             packed behind each other (slot_map's starts are such), token t of
  *             the packing at t * stride, row r being the tokens starts[r] ..
@@ -634,8 +635,8 @@ devscan_status expert_combine_backward_bf16(const uint16_t *grad, size_t grad_st
  *   tensors : HOST array of `count` (at most 2^24), read during the call; each
  *             has n elements of `type` at the device pointers in and out,
  *             aligned to the element.  out may be in, otherwise it overlaps
- *             nothing; the outs of two tensors must not overlap (not checked).
- *             grad_norm does not use out.
+ *             nothing; a tensor's out must overlap no other tensor's in or out
+ *             (not checked).  grad_norm does not use out.
  *   norm    : device float; max_norm: at least 0;
  *   work    : device scratch of the caller's, 8-byte aligned, of work_bytes >=
  *             DEVSCAN_NORM_WORK_BYTES(count); its content before and after

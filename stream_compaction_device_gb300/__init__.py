@@ -844,6 +844,10 @@ def _norm(tensors, out, max_norm, norm, work, stream):
                 or list(map(of.numel, outs)) != sizes or list(map(_DTYPE_OF, outs)) != dtypes):
             raise ValueError("each of out must match its tensor in type, size and device, and be contiguous")
         to = list(map(of.data_ptr, outs))
+    if max_norm is not None and len(set(to)) != count:
+        held = [p for p, n in zip(to, sizes) if n]
+        if len(set(held)) != len(held):
+            raise ValueError("a tensor is to be clipped twice")
     table = array.array("Q", bytes(32 * max(count, 1)))   # of devscan_tensor, four words each
     for word, values in enumerate((at, to, sizes, kinds)):
         table[word:4 * count:4] = array.array("Q", values)

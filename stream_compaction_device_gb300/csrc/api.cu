@@ -403,7 +403,8 @@ devscan_status gated_check(size_t rows, size_t tokens, size_t channels, const in
     if (kind != DEVSCAN_GATE_DECAY && kind != DEVSCAN_GATE_LOG && kind != DEVSCAN_GATE_SIGMOID)
         return DEVSCAN_ERR_INVALID;
     constexpr size_t kMost = static_cast<size_t>(INT32_MAX) - 1;
-    if (rows > kMost || tokens > kMost || channels > kMost || pool > kMost || channels < 1) return DEVSCAN_ERR_INVALID;
+    constexpr size_t kMostChannels = kMost - 128;   // the last lanes of the last warp are counted too
+    if (rows > kMost || tokens > kMost || channels > kMostChannels || pool > kMost || channels < 1) return DEVSCAN_ERR_INVALID;
     if (starts == nullptr && rows * tokens > kMost) return DEVSCAN_ERR_INVALID;
     if (misaligned(starts, 4) || misaligned(slots, 4)) return DEVSCAN_ERR_INVALID;
     *out = {starts, slots, static_cast<int>(rows), static_cast<int>(channels), static_cast<int>(pool),
@@ -611,9 +612,14 @@ try {
         const Span out[] = {{t.out, t.n * size}}, others[] = {{norm, 4}, {work, need}};
         if (written_overlap(out, others) || (t.out != t.in && written_overlap(out, in))) return DEVSCAN_ERR_INVALID;
     }
-    int sms = 0;
+    int sms = 0, dev = 0;
     const devscan_status st = current_sms(&sms);
     if (st != DEVSCAN_OK) return st;
+    if (cudaGetDevice(&dev) != cudaSuccess) return DEVSCAN_ERR_CUDA;
+    // The second launch starts beside the first and reads the tensors, so no other
+    // call's launch may come between them.
+    Hold hold;
+    hold_slot({dev, reinterpret_cast<uintptr_t>(stream)}, true, &hold);
     return from_cuda(launch_grad_norm(list.data(), count, clip, max_norm, norm, static_cast<double *>(work), sms, stream));
 } catch (const std::bad_alloc &) {
     return DEVSCAN_ERR_NOMEM;

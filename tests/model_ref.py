@@ -16,14 +16,15 @@ def as64(t):
 def decays(gate, kind):
     """(a, its relative room, what x is multiplied by, its relative room).
 
-    log: within 1/8 of 0, 1 + s is rounded once (u, or 2u above 1) from an s of
-    at most 0.134 with five roundings (1 u) and a series off by 2^-27: 4u.
+    log: within 1/16 of 0, 1 + s is rounded once (u, or 2u above 1) from an s of
+    at most 0.065 with four roundings (a quarter u) and a series off by 2^-26 (a
+    quarter u): below 4u.
     Elsewhere the hardware's exponential, off by 2 + 1.173 |g| units in the last
     place at most (2^-23 each).
-    sigmoid: t = exp(-|g|) has that error; 1 + t another half, the quotient two
-    units: small = t / (1 + t) is within (2 + 1.173 |g| + 0.5 + 2) 2^-23; large =
-    1 - small has small's error in absolute terms, less than that relative to
-    large, which is not the smaller, and a rounding."""
+    sigmoid: u = exp(-g) has that error; 1 + u another half unit, the reciprocal
+    one: 1 / (1 + u) and r = u / (1 + u), a rounding more, are within (2 + 1.173
+    |g| + 2) 2^-23; where u <= 1, a = 1 - r has r's error in absolute terms, less
+    than that relative to a, which is not the smaller, and a rounding."""
     g = gate
     if kind == "decay":
         return g, np.zeros_like(g), np.ones_like(g), np.zeros_like(g)

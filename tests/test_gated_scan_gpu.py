@@ -317,6 +317,21 @@ def test_far_offsets(ds):
     assert torch.equal(ds.gated_scan(x, gate, out=out)[0], ds.gated_scan(x.contiguous(), gate)[0])
 
 
+def test_most_tokens(ds):
+    """2^31 - 2 tokens in one row and in two: h = 2 - 2^-t exactly, from inputs that repeat themselves."""
+    n = 2**31 - 2
+    one, half = torch.ones(1, 1, device="cuda").expand(n, 1), torch.full((1, 1), 0.5, device="cuda").expand(n, 1)
+    out = torch.empty(n, 1, device="cuda")
+    starts = torch.tensor([0, 2**30 + 1, n], dtype=torch.int32, device="cuda")
+    for where, begins in ((None, [0]), (starts, [0, 2**30 + 1])):
+        out.zero_()
+        _, final = ds.gated_scan(one, half, starts=where, out=out)
+        assert (final == 2).all() and final.shape == (len(begins), 1)
+        for b in begins:
+            assert out[b:b + 4, 0].tolist() == [1.0, 1.5, 1.75, 1.875]
+        assert (out[-5:] == 2).all() and (out < 2).sum().item() == 24 * len(begins)
+
+
 def test_refusals(ds):
     x, g = torch.ones(2, 10, 8, device="cuda"), torch.ones(2, 10, 8, device="cuda")
     state, i32 = torch.ones(2, 8, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")

@@ -158,7 +158,7 @@ def test_refusals(ds):
            (ValueError, lambda: ds.clip_grad_norm([t], 1.0, out=[t[:9]])),
            (ValueError, lambda: ds.clip_grad_norm([t], 1.0, out=[t.half()])),
            (ValueError, lambda: ds.grad_norm([t], work=work)), (TypeError, lambda: ds.grad_norm([t], norm=t[:1].half())),
-           (ds.DevscanError, lambda: ds.grad_norm([t], norm=t[3:4])),
+           (ds.DevscanError, lambda: ds.grad_norm([t], norm=t[3:4])), (ValueError, lambda: ds.clip_grad_norm([t, t], 1.0)),
            (ds.DevscanError, lambda: ds.clip_grad_norm([t[:9]], 1.0, out=[t[1:]]))]
     for error, call in bad:
         with pytest.raises(error):

@@ -44,6 +44,7 @@ def test_gated_scan_refusals(lib):
         assert call(a9=0) == ERR_INVALID                               # no channels
         assert call(a14=3) == ERR_INVALID and call(a14=-1) == ERR_INVALID
         assert call(a7=2**31) == ERR_INVALID and call(a8=2**31) == ERR_INVALID
+        assert call(a9=2**31 - 2, a2=2**31, a17=2**31, a1=2**40, a16=2**40) == ERR_INVALID
         assert call(a7=2**20, a8=2**20) == ERR_INVALID                 # tokens past 32 bits
         assert call(a1=2**62) == ERR_INVALID and call(a2=2**62) == ERR_INVALID
         assert call(a17=7) == ERR_INVALID                              # output tokens overlap
