@@ -491,6 +491,7 @@ def sample_tokens(logits: torch.Tensor, noise: torch.Tensor | None = None, tempe
 
 _VALUES = {torch.float32: "f32", torch.float16: "f16", torch.bfloat16: "bf16"}
 _F32, _I32 = torch.float32, torch.int32
+_GATES = _lib.GATES
 
 
 def _value_suffix(t: torch.Tensor) -> str:
@@ -527,37 +528,39 @@ def _token_array(t: torch.Tensor, name: str, shape, dtype, here: int):
     """(address, row stride, token stride) of a tensor [rows, tokens, channels]
     or [tokens, channels] with neighbouring channels."""
     strides = t.stride()
+    if t.get_device() == here and t.dtype is dtype and t.shape == shape and (strides[-1] == 1 or shape[-1] == 1):
+        return t.data_ptr(), strides[0] if len(strides) == 3 else 0, strides[-2]
     if t.get_device() != here:
         raise ValueError(f"{name} must be a CUDA tensor on the current device")
     if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if strides[-1] != 1 and shape[-1] != 1:
-        raise ValueError(f"{name}'s channels must be contiguous")
-    return t.data_ptr(), strides[0] if len(strides) == 3 else 0, strides[-2]
+    raise ValueError(f"{name}'s channels must be contiguous")
 
 
 def _gated_rows(x: torch.Tensor, gate: torch.Tensor, starts, kind: str):
     """(rows, tokens, channels, the kind's number, whether the gates are fp32
     beside 16 bits)."""
-    number = _lib.GATES.get(kind)
+    number = _GATES.get(kind)
     if number is None:
         raise ValueError(f"unknown kind {kind!r} (decay, log, sigmoid)")
-    wide = gate.dtype is not x.dtype
-    if wide and gate.dtype is not _F32:
+    dtype = gate.dtype
+    wide = dtype is not x.dtype
+    if wide and dtype is not _F32:
         raise TypeError("gate must be float32 or of x's type")
-    if x.dim() == 3:
+    shape = x.shape
+    if len(shape) == 3:
         if starts is not None:
             raise ValueError("packed rows (starts) need [tokens, channels]")
-        rows, tokens, channels = x.shape
-    elif x.dim() == 2:
-        tokens, channels = x.shape
+        rows, tokens, channels = shape
+    elif len(shape) == 2:
+        tokens, channels = shape
         rows = 1
         if starts is not None:
-            if starts.numel() < 1:
-                raise ValueError("starts must hold rows + 1 elements")
             rows = starts.numel() - 1
+            if rows < 0:
+                raise ValueError("starts must hold rows + 1 elements")
     else:
         raise ValueError("x must be [rows, tokens, channels] or [tokens, channels]")
     if channels < 1:
@@ -569,13 +572,13 @@ def _states(t, name: str, channels: int, pool: int, here: int):
     """Address of fp32 states [pool, channels]; None for None."""
     if t is None:
         return None
+    if t.get_device() == here and t.dtype is _F32 and t.shape == (pool, channels) and t.is_contiguous():
+        return t.data_ptr()
     if t.get_device() != here:
         raise ValueError(f"{name} must be a CUDA tensor on the current device")
     if t.shape != (pool, channels) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous [{pool}, {channels}]")
-    if t.dtype is not _F32:
-        raise TypeError(f"{name} must be float32")
-    return t.data_ptr()
+    raise TypeError(f"{name} must be float32")
 
 
 def gated_scan(x: torch.Tensor, gate: torch.Tensor, starts: torch.Tensor | None = None,
@@ -613,12 +616,16 @@ def gated_scan(x: torch.Tensor, gate: torch.Tensor, starts: torch.Tensor | None 
     shape, dtype = x.shape, x.dtype
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=x.device)
+    x_at, x_row, x_token = _token_array(x, "x", shape, dtype, here)
+    gate_at, gate_row, gate_token = _token_array(gate, "gate", shape, gate.dtype, here)
+    out_at, out_row, out_token = _token_array(out, "out", shape, dtype, here)
+    states = _states(final, "final", channels, pool, here)
     status = getattr(load(), "gated_scan_" + suffix)(
-        *_token_array(x, "x", shape, dtype, here), *_token_array(gate, "gate", shape, gate.dtype, here), wide, rows,
-        tokens, channels, _vector(starts, "starts", _I32, rows + 1, here),
-        _states(initial, "initial", channels, pool, here), _vector(slots, "slots", _I32, rows, here), pool, number,
-        *_token_array(out, "out", shape, dtype, here), _states(final, "final", channels, pool, here),
-        _stream_handle(stream))
+        x_at, x_row, x_token, gate_at, gate_row, gate_token, wide, rows, tokens, channels,
+        None if starts is None else _vector(starts, "starts", _I32, rows + 1, here),
+        states if initial is final else _states(initial, "initial", channels, pool, here),
+        None if slots is None else _vector(slots, "slots", _I32, rows, here), pool, number, out_at, out_row, out_token,
+        states, _stream_handle(stream))
     if status:
         _lib.check(status, "gated_scan_" + suffix)
     return out, final
