@@ -386,10 +386,12 @@ bool check_values(Values *v, const GatedRows &rows, bool output)
 bool values_overlap(const Values &a, const Values &b, const GatedRows &rows)
 {
     if (a.bytes == 0 || b.bytes == 0 || !overlaps(a.array.data, a.bytes, b.array.data, b.bytes)) return false;
-    const size_t stride = a.array.stride * a.size, row = a.array.row_stride * a.size;
     const bool one_row = rows.starts != nullptr || rows.rows == 1;
-    if (rows.tokens < 2 || stride == 0 || stride != b.array.stride * b.size) return true;
-    if (!one_row && (row != b.array.row_stride * b.size || row % stride != 0)) return true;
+    if (one_row && rows.tokens < 2) return true;
+    const bool steps = rows.tokens == 1;   // rows of one token each: a row is a token
+    const size_t row = a.array.row_stride * a.size, row_b = b.array.row_stride * b.size;
+    const size_t stride = steps ? row : a.array.stride * a.size, stride_b = steps ? row_b : b.array.stride * b.size;
+    if (stride == 0 || stride != stride_b || (!one_row && (row != row_b || row % stride != 0))) return true;
     const uintptr_t x = reinterpret_cast<uintptr_t>(a.array.data), y = reinterpret_cast<uintptr_t>(b.array.data);
     const size_t shift = x <= y ? (y - x) % stride : (stride - (x - y) % stride) % stride;   // of b within a's token
     const size_t c = static_cast<size_t>(rows.channels);

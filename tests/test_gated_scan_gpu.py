@@ -307,6 +307,24 @@ def test_same_bits_and_streams(ds):
     assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("tokens", [1, 2])
+def test_arrays_side_by_side(ds, tokens):
+    """Inputs and outputs in one buffer, next to each other in every token: of a step, too."""
+    rng = np.random.default_rng(14)
+    buffer = cuda(rng.standard_normal((5, tokens, 5 * 16)), BF16)
+    parts = [buffer[..., 16 * i:16 * i + 16] for i in range(5)]
+    x, gate = parts[0].clone(), parts[2].clone()
+    want, _ = ds.gated_scan(x, gate, kind="sigmoid")
+    out, _ = ds.gated_scan(parts[0], parts[2], kind="sigmoid", out=parts[1])
+    assert torch.equal(out, want) and torch.equal(parts[0], x) and torch.equal(parts[2], gate)
+    back = ds.gated_scan_backward(x, x, gate, want, kind="sigmoid")
+    ds.gated_scan_backward(parts[0], parts[0], parts[2], parts[1], kind="sigmoid", grad_x=parts[4], grad_gate=parts[3])
+    assert torch.equal(parts[4], back[0]) and torch.equal(parts[3], back[1]) and torch.equal(parts[1], want)
+    for shift in (8, 24):
+        with pytest.raises(ds.DevscanError):
+            ds.gated_scan(parts[0], parts[2], kind="sigmoid", out=buffer[..., shift:shift + 16])
+
+
 def test_far_offsets(ds):
     """Elements behind 2^32 bytes and 2^31 elements."""
     wide = torch.zeros(40, 1 << 26, dtype=BF16, device="cuda")
