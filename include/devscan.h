@@ -626,9 +626,9 @@ devscan_status expert_combine_backward_bf16(const uint16_t *grad, size_t grad_st
  * The 2-norm over many tensors, and their clipping (the fold of P1 section
  * 四 over arrays that lie anywhere):
  *   *norm = sqrt(sum over all tensors and elements of in^2),
- *   out   = in min(1, max_norm / (norm + 1e-6)), rounded once.
- * A norm that is infinite or NaN clips nothing (out = in): the caller, who
- * reads it, decides.  Squares neither overflow nor vanish, whatever the
+ *   out   = in min(1, max_norm / (norm + 1e-6)), the factor in fp32, the product
+ * rounded once.  A norm that is infinite (in fp32, as it is given) or NaN clips
+ * nothing (out = in): the caller, who reads it, decides.  Squares neither overflow nor vanish, whatever the
  * values' size; sums are fp32 for 64 values and fp64 above, in a fixed order, so
  * that the same call gives the same bits.
  *

@@ -257,10 +257,11 @@ __global__ void __launch_bounds__(kNormThreads, kNormPerSm) norm_scale_kernel(co
             if (tid < 32) {
                 const double v = sqrt(warp_sum(partials, count, tid));
                 if (tid == 0) {
-                    if (blockIdx.x == 0 && norm != nullptr) *norm = static_cast<float>(v);
+                    const float told_norm = static_cast<float>(v);
+                    if (blockIdx.x == 0 && norm != nullptr) *norm = told_norm;
                     const double ratio = static_cast<double>(max_norm) / (v + kClipEps);
-                    // a norm that is no number, or infinite, clips nothing
-                    s_scale = ratio < 1.0 && v < __longlong_as_double(0x7ff0000000000000ll) ? static_cast<float>(ratio) : 1.0f;
+                    // a norm that is no number, or infinite as the caller reads it, clips nothing
+                    s_scale = ratio < 1.0 && told_norm < __int_as_float(0x7f800000) ? static_cast<float>(ratio) : 1.0f;
                 }
             }
             __syncthreads();

@@ -102,6 +102,16 @@ def test_not_finite(ds, bad, at):
     assert torch.equal(out.nan_to_num(5.0), keep.nan_to_num(5.0))
 
 
+def test_norm_past_fp32(ds):
+    """A norm of finite values that fp32 does not hold is given as infinite, and clips nothing."""
+    for n, whole in ((1, True), (300, False)):
+        t = torch.full((n,), 3e38, device="cuda")
+        keep = t.clone()
+        norm, _ = ds.clip_grad_norm([t], 1.0)
+        assert torch.isfinite(norm).item() is whole
+        assert torch.allclose(t, torch.ones_like(t)) if whole else torch.equal(t, keep)
+
+
 def test_nothing(ds):
     assert ds.grad_norm([]).item() == 0
     norm, out = ds.clip_grad_norm([torch.empty(0, device="cuda")], 1.0)
