@@ -862,9 +862,11 @@ def _norm(tensors, out, max_norm, norm, work, stream):
         norm = torch.empty((), dtype=_F32, device="cuda")
     need = _lib.norm_work_bytes(count)
     if work is None:
-        work = torch.empty(need, dtype=torch.uint8, device="cuda")
-        if stream is not None:   # the allocator may give it away once that stream is through with it
-            work.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+        if stream is None:
+            work = torch.empty(need, dtype=torch.uint8, device="cuda")
+        else:   # from that stream's memory: neither its last owner nor its next then runs beside the call
+            with torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))):
+                work = torch.empty(need, dtype=torch.uint8, device="cuda")
     here = _device_of(work, "work")
     if not work.is_contiguous():
         raise ValueError("work must be contiguous")

@@ -149,6 +149,19 @@ def test_same_bits_streams_and_graphs(ds):
         assert torch.equal(norm, want[0])
 
 
+def test_scratch_belongs_to_the_calls_stream(ds, monkeypatch):
+    """The call's own scratch is memory of the stream that it runs on, whichever is current."""
+    side, made, empty = torch.cuda.Stream(), [], torch.empty
+    t, norm = torch.ones(100, device="cuda"), torch.zeros((), device="cuda")
+    torch.cuda.synchronize()
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: (made.append(torch.cuda.current_stream().cuda_stream), empty(*a, **k))[1])
+    for stream, want in ((side, side.cuda_stream), (side.cuda_stream, side.cuda_stream), (None, torch.cuda.current_stream().cuda_stream)):
+        made.clear()
+        ds.grad_norm([t], norm=norm, stream=stream)
+        torch.cuda.synchronize()
+        assert made == [want] and norm.item() == 10
+
+
 def test_large(ds):
     """Elements behind 2^32 bytes."""
     t = torch.zeros((1 << 31) + 5, dtype=BF16, device="cuda")
