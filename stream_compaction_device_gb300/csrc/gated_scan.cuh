@@ -217,7 +217,8 @@ __device__ __forceinline__ int first_start(const int32_t *starts, int count, int
 }
 
 // Where span j begins: at the first row that begins at or behind its share of
-// the tokens.
+// the tokens, or, behind all rows (a padded batch, whose end is only cleared),
+// at the share itself.
 __device__ __forceinline__ unsigned span_begin(const GatedRows &rows, unsigned j)
 {
     const unsigned all = rows.all();
@@ -227,7 +228,7 @@ __device__ __forceinline__ unsigned span_begin(const GatedRows &rows, unsigned j
         return static_cast<unsigned>(static_cast<unsigned long long>(rows.rows) * j / rows.spans) * rows.tokens;
     const int share = static_cast<int>(static_cast<unsigned long long>(all) * j / rows.spans);
     const int r = first_start(rows.starts, rows.rows + 1, share, threadIdx.x & 31);
-    if (r > rows.rows) return all;
+    if (r > rows.rows) return static_cast<unsigned>(share);
     const unsigned at = static_cast<unsigned>(__ldg(rows.starts + r));   // >= share >= 0
     return at < all ? at : all;
 }
