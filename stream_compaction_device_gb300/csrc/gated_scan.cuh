@@ -484,6 +484,7 @@ __device__ __forceinline__ void hand_on(Exchange<V, BLOCKS> &x, int turn, int bl
 struct Work {
     int rank, blocks, channel;
     unsigned span, begin, end;
+    bool behind;   // all rows
 };
 __device__ __forceinline__ Work work_of(const GatedRows &rows, int per_lane)
 {
@@ -494,7 +495,17 @@ __device__ __forceinline__ Work work_of(const GatedRows &rows, int per_lane)
     w.channel = static_cast<int>((cluster % groups) * 32 + (threadIdx.x & 31)) * per_lane;
     w.begin = span_begin(rows, w.span), w.end = span_begin(rows, w.span + 1);
     if (w.end < w.begin) w.end = w.begin;   // only where starts decrease
+    w.behind = rows.starts != nullptr && static_cast<int>(w.begin) >= __ldg(rows.starts + rows.rows);
     return w;
+}
+
+// A span behind all rows becomes 0 and nothing of it is read.
+template <typename R, typename X>
+__device__ __forceinline__ void clear_span(const Work &w, const GatedArray &array, X *at)
+{
+    const unsigned warps = static_cast<unsigned>(w.blocks * kWarps);
+    for (unsigned n = w.begin + static_cast<unsigned>(w.rank) * kWarps + (threadIdx.x >> 5); n < w.end; n += warps)
+        *reinterpret_cast<R *>(at + element(array, 0, n)) = R{};
 }
 
 // Rows that begin or end among a warp's tokens, a bit per token; lane i knows
@@ -638,6 +649,10 @@ gated_scan_kernel(const __grid_constant__ GatedScanCall p)
             for (int k = 0; k < V; ++k) to[w.channel + k] = from != nullptr ? from[w.channel + k] : 0.0f;
         });
 
+    if (w.behind) {   // the whole cluster
+        if (live) clear_span<RX>(w, p.out, out);
+        return;
+    }
     const unsigned round = static_cast<unsigned>(w.blocks * kWarps * L);
     const unsigned rounds = (w.end - w.begin + round - 1) / round;
     const unsigned start = w.begin + static_cast<unsigned>((w.rank * kWarps + warp) * L);
@@ -809,6 +824,10 @@ gated_scan_backward_kernel(const __grid_constant__ GatedBackwardCall p)
             for (int k = 0; k < V; ++k) p.grad_initial[at + k] = p.grad_final != nullptr ? p.grad_final[at + k] : 0.0f;
         });
 
+    if (w.behind) {   // the whole cluster
+        if (live) clear_span<RX>(w, p.grad_x, grad_x), clear_span<RG>(w, p.grad_gate, grad_gate);
+        return;
+    }
     const unsigned round = static_cast<unsigned>(w.blocks * kWarps * L);
     const unsigned tokens = w.end - w.begin, rounds = (tokens + round - 1) / round;
     const unsigned start = static_cast<unsigned>((w.rank * kWarps + warp) * L);   // tokens of the span behind this warp's

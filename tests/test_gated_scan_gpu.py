@@ -122,6 +122,26 @@ def test_many_packed_rows(ds):
     check(ds, rng, len(one_long) - 1, 6000, 70, BF16, F32, "decay", starts=one_long, carry=True)
 
 
+@pytest.mark.parametrize("dtype,channels", [(F32, 36), (BF16, 33), (BF16, 64)])
+@pytest.mark.parametrize("real", [0, 50, 3000, 11999])
+def test_padded_batches(ds, real, dtype, channels):
+    """Tokens behind all rows get 0, whatever they hold and however many of them there are."""
+    rng = np.random.default_rng(real)
+    cuts = np.sort(rng.integers(0, real + 1, 59)).tolist()
+    starts = [0, *cuts, real]
+    check(ds, rng, 60, 12000, channels, dtype, dtype, "log", starts=starts, carry=True)
+    nan = float("nan")
+    x, gate = cuda(rng.standard_normal((12000, channels)), dtype), cuda(rng.standard_normal((12000, channels)), dtype)
+    x[real:], gate[real:] = nan, nan
+    where = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    out, final = ds.gated_scan(x, gate, starts=where, kind="sigmoid", out=torch.full_like(x, nan))
+    assert out.isfinite().all() and final.isfinite().all() and not out[real:].any()
+    out[real:] = nan
+    gx, gg, _ = ds.gated_scan_backward(x, x, gate, out, starts=where, kind="sigmoid", grad_x=torch.full_like(x, nan),
+                                       grad_gate=torch.full_like(x, nan))
+    assert gx.isfinite().all() and gg.isfinite().all() and not gx[real:].any() and not gg[real:].any()
+
+
 @pytest.mark.parametrize("tokens", [1, 5, 200])
 def test_states_in_a_pool(ds, tokens):
     """Slots of a larger pool, in place; a row without a state; other states stay."""
