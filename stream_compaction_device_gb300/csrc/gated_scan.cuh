@@ -262,11 +262,12 @@ __device__ __forceinline__ bool row_empty(const GatedRows &rows, int r)
     return a >= b;
 }
 
-// Row r's state in a pool; null where it has none.
+// Where row r's state lies in a pool, if below its size; that state, or null.
+__device__ __forceinline__ int slot_of(const GatedRows &rows, int r) { return rows.slots == nullptr ? r : __ldg(rows.slots + r); }
 __device__ __forceinline__ float *state_of(const GatedRows &rows, float *states, int r)
 {
     if (states == nullptr) return nullptr;
-    const int slot = rows.slots == nullptr ? r : __ldg(rows.slots + r);
+    const int slot = slot_of(rows, r);
     return static_cast<unsigned>(slot) < static_cast<unsigned>(rows.pool)
                ? states + static_cast<size_t>(slot) * rows.channels
                : nullptr;
@@ -548,16 +549,39 @@ __device__ __forceinline__ Edges edges_of(const GatedRows &rows, const Run &r, i
     return e;
 }
 
-// Rows without tokens: what goes in comes out, 0 where nothing does.  fn(row)
-// is called by a warp for each.
-template <typename Fn>
-__device__ __forceinline__ void empty_rows(const GatedRows &rows, const Work &w, Fn &&fn)
+// Rows without tokens: what goes in comes out, 0 where nothing does.  All spans'
+// warps share them, 32 rows at a time, of which a lane looks one up; those that
+// have a state are then copied, four in flight.
+template <int V>
+__device__ __forceinline__ void empty_rows(const GatedRows &rows, const Work &w, bool live, const float *from, float *to)
 {
-    if (w.span != 0) return;
-    const int lane = threadIdx.x & 31, warp = w.rank * kWarps + (threadIdx.x >> 5), warps = w.blocks * kWarps;
-    for (long long r0 = static_cast<long long>(warp) * 32; r0 < rows.rows; r0 += 32ll * warps) {
-        unsigned found = __ballot_sync(kFullMask, r0 + lane < rows.rows && row_empty(rows, static_cast<int>(r0 + lane)));
-        for (; found != 0; found &= found - 1) fn(static_cast<int>(r0) + __ffs(found) - 1);
+    if (to == nullptr || (rows.starts == nullptr && rows.tokens > 0)) return;
+    const unsigned lane = threadIdx.x & 31, warp = static_cast<unsigned>(w.rank) * kWarps + (threadIdx.x >> 5);
+    const long long turn = 32ll * rows.spans * w.blocks * kWarps;
+    for (long long r0 = 32ll * (static_cast<long long>(warp) * rows.spans + w.span); r0 < rows.rows; r0 += turn) {
+        const long long r = r0 + lane;
+        int slot = -1;
+        if (r < rows.rows && row_empty(rows, static_cast<int>(r))) slot = slot_of(rows, static_cast<int>(r));
+        unsigned found = __ballot_sync(kFullMask, static_cast<unsigned>(slot) < static_cast<unsigned>(rows.pool));
+        while (found != 0) {
+            float v[4][V] = {};
+            size_t at[4];
+            int many = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (found == 0) break;
+                at[i] = static_cast<size_t>(__shfl_sync(kFullMask, slot, __ffs(found) - 1)) * rows.channels + w.channel;
+                found &= found - 1, many = i + 1;
+                if (from != nullptr && live)
+#pragma unroll
+                    for (int k = 0; k < V; ++k) v[i][k] = from[at[i] + k];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < many && live)
+#pragma unroll
+                    for (int k = 0; k < V; ++k) to[at[i] + k] = v[i][k];
+        }
     }
 }
 
@@ -641,14 +665,7 @@ gated_scan_kernel(const __grid_constant__ GatedScanCall p)
     X *out = static_cast<X *>(p.out.data) + w.channel;
     char *const ring = s_ring + warp * R::kStages * R::kStage;
 
-    if (p.final != nullptr)
-        empty_rows(p.rows, w, [&](int r) {
-            float *to = state_of(p.rows, p.final, r);
-            const float *from = state_of(p.rows, p.initial, r);
-            if (to == nullptr || !live) return;
-            for (int k = 0; k < V; ++k) to[w.channel + k] = from != nullptr ? from[w.channel + k] : 0.0f;
-        });
-
+    empty_rows<V>(p.rows, w, live, p.initial, p.final);
     if (w.behind) {   // the whole cluster
         if (live) clear_span<RX>(w, p.out, out);
         return;
@@ -817,13 +834,7 @@ gated_scan_backward_kernel(const __grid_constant__ GatedBackwardCall p)
     G *grad_gate = static_cast<G *>(p.grad_gate.data) + w.channel;
     char *const ring = s_ring + warp * R::kStages * R::kStage;
 
-    if (p.grad_initial != nullptr)
-        empty_rows(p.rows, w, [&](int r) {
-            if (!live) return;
-            const size_t at = static_cast<size_t>(r) * p.rows.channels + w.channel;
-            for (int k = 0; k < V; ++k) p.grad_initial[at + k] = p.grad_final != nullptr ? p.grad_final[at + k] : 0.0f;
-        });
-
+    empty_rows<V>(p.rows, w, live, p.grad_final, p.grad_initial);
     if (w.behind) {   // the whole cluster
         if (live) clear_span<RX>(w, p.grad_x, grad_x), clear_span<RG>(w, p.grad_gate, grad_gate);
         return;
