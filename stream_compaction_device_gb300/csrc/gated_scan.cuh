@@ -29,7 +29,8 @@
 // are handed out first, since rows need no exchange; a row is spread over up to
 // sixteen blocks only where rows and channels alone do not fill the GPU.  No
 // block waits for another but at the cluster barrier, and the order of sums
-// follows from the call's sizes and starts.
+// follows from the call's sizes and starts.  Among packed rows, one longer than
+// half of all tokens has a launch of its own beside the others'.
 //
 // What bounds it (device time, share of the measured copy rate): 8 x 4096 x 4096
 // bf16 sigmoid 158 us forward (76%) and 266-270 us backward (90%): 52 and 91
@@ -41,7 +42,7 @@
 // for the writes in front of it, and fewer tokens fit in a round), 16 warps to a
 // block (304), a relaxed barrier (169, and not sound), the maps of a cluster's
 // blocks in dynamic shared memory (183).  Short packed rows leave spans uneven: 24
-// rows, 8191 x 1000 fp32 decay, 26 us (56%).
+// rows, 8191 x 1000 fp32 decay, 27 us (54%).
 #pragma once
 
 #include <initializer_list>
@@ -216,21 +217,45 @@ __device__ __forceinline__ int first_start(const int32_t *starts, int count, int
     return lo;
 }
 
-// Where span j begins: at the first row that begins at or behind its share of
-// the tokens, or, behind all rows (a padded batch, whose end is only cleared),
-// at the share itself.
-__device__ __forceinline__ unsigned span_begin(const GatedRows &rows, unsigned j)
+// A place between packed rows: the first row that begins at or behind `share`
+// of the tokens, or, behind all rows (a padded batch, whose end is only cleared),
+// the share itself.  And the long row, if it is one, in which the share lies.
+struct Cut {
+    unsigned at, row;   // where that row begins
+    bool is_long;
+};
+__device__ __forceinline__ Cut cut_at(const GatedRows &rows, unsigned share)
 {
-    const unsigned all = rows.all();
-    if (j == 0) return 0u;
-    if (j >= rows.spans) return all;
-    if (rows.starts == nullptr)
-        return static_cast<unsigned>(static_cast<unsigned long long>(rows.rows) * j / rows.spans) * rows.tokens;
-    const int share = static_cast<int>(static_cast<unsigned long long>(all) * j / rows.spans);
-    const int r = first_start(rows.starts, rows.rows + 1, share, threadIdx.x & 31);
-    if (r > rows.rows) return static_cast<unsigned>(share);
-    const unsigned at = static_cast<unsigned>(__ldg(rows.starts + r));   // >= share >= 0
-    return at < all ? at : all;
+    if (share == 0) return {0u, 0u, false};
+    const unsigned all = rows.all(), real = min(static_cast<unsigned>(max(__ldg(rows.starts + rows.rows), 0)), all);
+    const int r = first_start(rows.starts, rows.rows + 1, static_cast<int>(share), threadIdx.x & 31);
+    if (r > rows.rows) return {share, share, false};
+    Cut c;
+    c.at = min(static_cast<unsigned>(__ldg(rows.starts + r)), all);              // >= share > 0
+    c.row = r > 0 ? min(static_cast<unsigned>(max(__ldg(rows.starts + r - 1), 0)), c.at) : c.at;   // < share
+    c.is_long = rows.long_from != 0 && c.at - c.row >= rows.long_from && c.at - c.row > real / 2;
+    return c;
+}
+
+// The tokens of span j: whole rows, but for a row longer than half of all, which
+// is the only span of a launch of its own; the middle token is one of its.
+__device__ __forceinline__ void span_of(const GatedRows &rows, unsigned j, unsigned &begin, unsigned &end)
+{
+    if (rows.starts == nullptr) {
+        begin = static_cast<unsigned>(static_cast<unsigned long long>(rows.rows) * j / rows.spans) * rows.tokens;
+        end = static_cast<unsigned>(static_cast<unsigned long long>(rows.rows) * (j + 1) / rows.spans) * rows.tokens;
+        return;
+    }
+    if (rows.long_row) {
+        const Cut c = cut_at(rows, min(static_cast<unsigned>(max(__ldg(rows.starts + rows.rows), 0)), rows.all()) / 2 + 1);
+        begin = c.row, end = c.is_long ? c.at : c.row;
+        return;
+    }
+    const unsigned long long all = rows.all();
+    const unsigned from = static_cast<unsigned>(all * j / rows.spans), to = static_cast<unsigned>(all * (j + 1) / rows.spans);
+    const Cut last = cut_at(rows, to);
+    begin = cut_at(rows, from).at, end = last.is_long ? last.row : last.at;
+    if (end < begin) end = begin;   // the long row began before; or starts decrease
 }
 
 struct TokenPlace {
@@ -494,9 +519,8 @@ __device__ __forceinline__ Work work_of(const GatedRows &rows, int per_lane)
     const unsigned cluster = blockIdx.x / rows.blocks, groups = rows.groups;
     w.span = cluster / groups;
     w.channel = static_cast<int>((cluster % groups) * 32 + (threadIdx.x & 31)) * per_lane;
-    w.begin = span_begin(rows, w.span), w.end = span_begin(rows, w.span + 1);
-    if (w.end < w.begin) w.end = w.begin;   // only where starts decrease
-    w.behind = rows.starts != nullptr && static_cast<int>(w.begin) >= __ldg(rows.starts + rows.rows);
+    span_of(rows, w.span, w.begin, w.end);
+    w.behind = rows.starts != nullptr && !rows.long_row && static_cast<int>(w.begin) >= __ldg(rows.starts + rows.rows);
     return w;
 }
 
@@ -507,6 +531,13 @@ __device__ __forceinline__ void clear_span(const Work &w, const GatedArray &arra
     const unsigned warps = static_cast<unsigned>(w.blocks * kWarps);
     for (unsigned n = w.begin + static_cast<unsigned>(w.rank) * kWarps + (threadIdx.x >> 5); n < w.end; n += warps)
         *reinterpret_cast<R *>(at + element(array, 0, n)) = R{};
+}
+
+// The other rows' launch lets a long row's start beside it, which then must not
+// end before it.
+__device__ __forceinline__ void end_beside(const GatedRows &rows)
+{
+    if (rows.long_row && blockIdx.x == 0) wait_primary_grid();
 }
 
 // Rows that begin or end among a warp's tokens, a bit per token; lane i knows
@@ -555,7 +586,7 @@ __device__ __forceinline__ Edges edges_of(const GatedRows &rows, const Run &r, i
 template <int V>
 __device__ __forceinline__ void empty_rows(const GatedRows &rows, const Work &w, bool live, const float *from, float *to)
 {
-    if (to == nullptr || (rows.starts == nullptr && rows.tokens > 0)) return;
+    if (to == nullptr || rows.long_row || (rows.starts == nullptr && rows.tokens > 0)) return;
     const unsigned lane = threadIdx.x & 31, warp = static_cast<unsigned>(w.rank) * kWarps + (threadIdx.x >> 5);
     const long long turn = 32ll * rows.spans * w.blocks * kWarps;
     for (long long r0 = 32ll * (static_cast<long long>(warp) * rows.spans + w.span); r0 < rows.rows; r0 += turn) {
@@ -655,6 +686,7 @@ gated_scan_kernel(const __grid_constant__ GatedScanCall p)
     using RG = typename R::RG;
     extern __shared__ __align__(16) char s_ring[];
     __shared__ Exchange<V, BLOCKS> s_x;
+    if (p.rows.long_from != 0 && !p.rows.long_row) allow_dependent_launch();
     const int lane = threadIdx.x & 31, warp = __shfl_sync(kFullMask, threadIdx.x >> 5, 0);
     const Work w = work_of(p.rows, V);
     const bool live = w.channel < p.rows.channels;   // a whole number of lanes is
@@ -670,6 +702,7 @@ gated_scan_kernel(const __grid_constant__ GatedScanCall p)
         if (live) clear_span<RX>(w, p.out, out);
         return;
     }
+    if (p.rows.long_row && w.begin == w.end) return end_beside(p.rows);
     const unsigned round = static_cast<unsigned>(w.blocks * kWarps * L);
     const unsigned rounds = (w.end - w.begin + round - 1) / round;
     const unsigned start = w.begin + static_cast<unsigned>((w.rank * kWarps + warp) * L);
@@ -798,6 +831,7 @@ gated_scan_kernel(const __grid_constant__ GatedScanCall p)
             }
         }
     }
+    end_beside(p.rows);
 }
 
 // ---------------------------------------------------------------------------
@@ -821,6 +855,7 @@ gated_scan_backward_kernel(const __grid_constant__ GatedBackwardCall p)
     using RG = typename R::RG;
     extern __shared__ __align__(16) char s_ring[];
     __shared__ Exchange<V, BLOCKS> s_x;
+    if (p.rows.long_from != 0 && !p.rows.long_row) allow_dependent_launch();
     const int lane = threadIdx.x & 31, warp = __shfl_sync(kFullMask, threadIdx.x >> 5, 0);
     const Work w = work_of(p.rows, V);
     const bool live = w.channel < p.rows.channels;
@@ -839,6 +874,7 @@ gated_scan_backward_kernel(const __grid_constant__ GatedBackwardCall p)
         if (live) clear_span<RX>(w, p.grad_x, grad_x), clear_span<RG>(w, p.grad_gate, grad_gate);
         return;
     }
+    if (p.rows.long_row && w.begin == w.end) return end_beside(p.rows);
     const unsigned round = static_cast<unsigned>(w.blocks * kWarps * L);
     const unsigned tokens = w.end - w.begin, rounds = (tokens + round - 1) / round;
     const unsigned start = static_cast<unsigned>((w.rank * kWarps + warp) * L);   // tokens of the span behind this warp's
@@ -993,6 +1029,7 @@ gated_scan_backward_kernel(const __grid_constant__ GatedBackwardCall p)
         }
         __syncwarp();   // the stage has been read
     }
+    end_beside(p.rows);
 }
 
 // ---------------------------------------------------------------------------
@@ -1099,6 +1136,26 @@ inline void plan(GatedRows &rows, int per_lane, int tokens_per_warp, int places_
         blocks = kMostBlocks;
     rows.groups = static_cast<unsigned>(groups), rows.spans = static_cast<unsigned>(spans);
     rows.blocks = static_cast<int>(blocks);
+    rows.long_row = false, rows.long_from = 0;
+    // Packed rows may hold one that is longer than all others together (a prompt
+    // beside single tokens).  One span's blocks would go through it alone, so it
+    // has a launch of its own, with up to eight blocks to a cluster: 200 rows of one
+    // token and one of 8,000, 2048 bf16 log, 118 -> 48 us (backward 160 -> 58); 50 x 99 and
+    // 60,000 770 -> 211.  Where there is none the launch looks and leaves: 0.6 us (24
+    // rows, 8191 x 1000 fp32).  With it in front that was 1.9 (and 37 in the first
+    // case), and rows of a quarter of all were slower.  Not for rows that one span's
+    // blocks finish in eight rounds, nor where channels fill the GPU.
+    const size_t least = 8 * tile * blocks;
+    if (rows.starts != nullptr && spans > 1 && all >= least && blocks < kPortableBlocks && 4 * blocks * groups <= places)
+        rows.long_from = static_cast<unsigned>(least);
+}
+
+// A long row's own launch.
+inline void plan_long(GatedRows &rows, int places_per_sm, int sms)
+{
+    const size_t places = static_cast<size_t>(sms) * places_per_sm;
+    rows.long_row = true, rows.spans = 1;
+    while (rows.blocks < kPortableBlocks && 2 * rows.blocks * rows.groups <= places) rows.blocks *= 2;
 }
 
 // Whether rows are long enough for many tokens per round (forward, log: 16 x
@@ -1118,27 +1175,33 @@ cudaError_t launch_clusters(void (*kernel)(Call), const Call &call, int ring, st
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = static_cast<size_t>(ring);
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = static_cast<unsigned>(call.rows.blocks);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = call.rows.long_row ? 2 : 1;   // beside the others
     return cudaLaunchKernelEx(&cfg, kernel, call);
 }
 
 template <typename X, typename G, int V, int KIND, int COPY, bool MANY>
 cudaError_t forward_of(GatedScanCall call, int sms, cudaStream_t s)
 {
-    static std::atomic<unsigned long long> done, more;
+    static std::atomic<unsigned long long> done, more, longs;
     using R = ForwardRing<X, G, V, KIND, COPY, MANY>;
     lay_out(call.rows, {&call.x, &call.gate, &call.out});
     plan(call.rows, V, R::kTokens, R::kPerSm, MANY, sms);
     if constexpr (MANY)
         if (call.rows.blocks > kPortableBlocks)
             return launch_clusters(gated_scan_kernel<X, G, V, KIND, COPY, MANY, kMostBlocks>, call, R::kBytes, more, s);
-    return launch_clusters(gated_scan_kernel<X, G, V, KIND, COPY, MANY, kPortableBlocks>, call, R::kBytes, done, s);
+    const cudaError_t e = launch_clusters(gated_scan_kernel<X, G, V, KIND, COPY, MANY, kPortableBlocks>, call, R::kBytes, done, s);
+    if (e != cudaSuccess || call.rows.long_from == 0) return e;
+    using Long = ForwardRing<X, G, V, KIND, COPY, true>;
+    plan_long(call.rows, Long::kPerSm, sms);
+    return launch_clusters(gated_scan_kernel<X, G, V, KIND, COPY, true, kPortableBlocks>, call, Long::kBytes, longs, s);
 }
 template <typename X, typename G, int V, int KIND, int COPY>
 cudaError_t forward(const GatedScanCall &call, int sms, cudaStream_t s)
@@ -1186,14 +1249,18 @@ cudaError_t forward_any(const GatedScanCall &call, int sms, cudaStream_t s)
 template <typename X, typename G, int V, int KIND, int COPY, bool MANY>
 cudaError_t backward_of(GatedBackwardCall call, int sms, cudaStream_t s)
 {
-    static std::atomic<unsigned long long> done, more;
+    static std::atomic<unsigned long long> done, more, longs;
     using R = BackwardRing<X, G, V, KIND, COPY, MANY>;
     lay_out(call.rows, {&call.grad, &call.gate, &call.y, &call.grad_x, &call.grad_gate, KIND == kGateSigmoid ? &call.x : &call.y});
     plan(call.rows, V, R::kTokens, R::kPerSm, MANY, sms);
     if constexpr (MANY)
         if (call.rows.blocks > kPortableBlocks)
             return launch_clusters(gated_scan_backward_kernel<X, G, V, KIND, COPY, MANY, kMostBlocks>, call, R::kBytes, more, s);
-    return launch_clusters(gated_scan_backward_kernel<X, G, V, KIND, COPY, MANY, kPortableBlocks>, call, R::kBytes, done, s);
+    const cudaError_t e = launch_clusters(gated_scan_backward_kernel<X, G, V, KIND, COPY, MANY, kPortableBlocks>, call, R::kBytes, done, s);
+    if (e != cudaSuccess || call.rows.long_from == 0) return e;
+    using Long = BackwardRing<X, G, V, KIND, COPY, true>;
+    plan_long(call.rows, Long::kPerSm, sms);
+    return launch_clusters(gated_scan_backward_kernel<X, G, V, KIND, COPY, true, kPortableBlocks>, call, Long::kBytes, longs, s);
 }
 template <typename X, typename G, int V, int KIND, int COPY>
 cudaError_t backward(const GatedBackwardCall &call, int sms, cudaStream_t s)

@@ -205,6 +205,8 @@ struct GatedRows {
     unsigned per;            // per row of the arrays, for addresses
     unsigned groups, spans;
     int blocks;
+    unsigned long_from;      // a packed row of so many tokens, and more than half of all, has a launch of its own; 0: none
+    bool long_row;           // which this one is
     __host__ __device__ unsigned all() const { return starts != nullptr ? tokens : tokens * static_cast<unsigned>(rows); }
 };
 struct GatedArray {

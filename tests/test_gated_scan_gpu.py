@@ -142,6 +142,66 @@ def test_padded_batches(ds, real, dtype, channels):
     assert gx.isfinite().all() and gg.isfinite().all() and not gx[real:].any() and not gg[real:].any()
 
 
+@pytest.mark.parametrize("at", [0, 30, 59])
+@pytest.mark.parametrize("dtype,channels,kind", [(BF16, 640, "sigmoid"), (F32, 333, "decay"), (F16, 333, "log")])
+def test_one_long_row(ds, dtype, channels, kind, at):
+    """A row longer than all others, before, between and behind them; empty rows and a padded end beside it."""
+    rng = np.random.default_rng(at)
+    lengths = rng.integers(0, 4, 60)
+    lengths[at] = 6000
+    starts = np.concatenate([[0], np.cumsum(lengths)]).tolist()
+    check(ds, rng, 60, starts[-1], channels, dtype, dtype, kind, starts=starts, carry=True)
+    lengths[at] = 3100                                                  # just more than half, and just not
+    lengths[(at + 7) % 60] = 3050 - (lengths.sum() - lengths[(at + 7) % 60] - 3100)
+    for more in (0, 200):
+        lengths[(at + 7) % 60] += more
+        starts = np.concatenate([[0], np.cumsum(lengths)]).tolist()
+        check(ds, rng, 60, starts[-1] + 500, channels, dtype, dtype, kind, starts=starts, carry=at == 0)
+
+
+def test_one_long_row_that_is_cut(ds):
+    """Rows that begin in front of the tokens or go on behind them."""
+    rng = np.random.default_rng(15)
+    for starts in ([-50, 7000, *range(7001, 7060)], [*range(59), 9000], [*range(59), 8000, 9000], [1000, *range(1001, 1060), 9000]):
+        x, gate = cuda(rng.standard_normal((8000, 640)), BF16), cuda(rng.standard_normal((8000, 640)), BF16)
+        where = torch.tensor(starts, dtype=torch.int32, device="cuda")
+        out, final = ds.gated_scan(x, gate, starts=where, kind="sigmoid")
+        kept = [min(max(s, 0), 8000) for s in starts]
+        h, room, last, last_room = ref.scan(flat(x), flat(gate), "sigmoid", ref.rows_of(kept, 8000, len(kept) - 1))
+        ref.close(out, h, room, "out")
+        ref.close(final, last, last_room, "final")
+
+
+def test_long_row_streams_and_graphs(ds):
+    """Both launches stay in their stream's order, eager and captured."""
+    rng = np.random.default_rng(16)
+    starts = torch.tensor([*range(60), 9000], dtype=torch.int32, device="cuda")
+    x, gate = cuda(rng.standard_normal((9000, 640)), BF16), cuda(rng.standard_normal((9000, 640)), BF16)
+    want, last = ds.gated_scan(x, gate, starts=starts, kind="sigmoid")
+    once, _ = ds.gated_scan(want, gate, starts=starts, kind="sigmoid")
+    back = ds.gated_scan_backward(once, x, gate, want, starts=starts, kind="sigmoid")
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+
+    def steps():
+        out, final = ds.gated_scan(x, gate, starts=starts, kind="sigmoid")
+        twice, _ = ds.gated_scan(out, gate, starts=starts, kind="sigmoid")
+        return (out, final, twice, *ds.gated_scan_backward(twice, x, gate, out, starts=starts, kind="sigmoid")[:2])
+
+    with torch.cuda.graph(graph, stream=side):
+        captured = steps()
+    for _ in range(3):
+        for t in captured:
+            t.fill_(7)
+        graph.replay()
+        with torch.cuda.stream(side):
+            side.wait_stream(torch.cuda.default_stream())
+            eager = steps()
+        torch.cuda.synchronize()
+        for got in (captured, eager):
+            assert all(torch.equal(a, b) for a, b in zip(got, (want, last, once, *back[:2])))
+
+
 @pytest.mark.parametrize("tokens", [1, 5, 200])
 def test_states_in_a_pool(ds, tokens):
     """Slots of a larger pool, in place; a row without a state; other states stay."""
