@@ -14,7 +14,8 @@
 // Sums: a thread adds the squares of a chunk's share (64 values at most) in
 // fp32 and its shares in fp64.  Where a share's fp32 sum leaves the range in
 // which no square that matters is lost or overflows, the share is added again
-// in fp64 from its registers.  fp64 goes at two a clock and SM here, so one
+// with its values times a power of two (64 M values of 1e-25:
+// 73 us; 284 with that second sum in fp64).  fp64 goes at two a clock and SM here, so one
 // warp folds what a block has, and one thread takes the root (with all threads
 // doing so, 1.3 M fp32 in 40 tensors took 19.5 us instead of 7.7).
 //
@@ -99,8 +100,33 @@ __device__ __forceinline__ int tensor_of(const NormTable &t, unsigned chunk)
 }
 
 // Squares that count in fp32: sums in this range hold every square that is not
-// below 2^-60 of them, and none overflows on the way.
-constexpr float kLeastSum = 0x1p-80f, kMostSum = 0x1p120f;
+// below 2^-60 of them, and none overflows on the way.  Values whose sum is below
+// it are less than 2^-40 and at least 2^-149: times 2^96 their squares lie between
+// 2^-106 and 2^112.  Above it, times 2^-96, none passes 2^64, and what is lost is
+// below 2^-70 of the sum.  (Infinity and NaN stay what they are.)
+constexpr float kLeastSum = 0x1p-80f, kMostSum = 0x1p120f, kRaise = 0x1p96f, kLower = 0x1p-96f;
+
+// A share added again, of values times `scale`.  That is rare, so it is a loop that
+// reads them again (1.5 G values 1,422 us; from registers beside the first sum 1,478,
+// as a function 1,441).
+template <typename T> __device__ __forceinline__ float squares_again(const uint4 *vectors, unsigned count, int tid, float scale)
+{
+    constexpr int E = 16 / sizeof(T);
+    float sum[2] = {0.0f, 0.0f};
+#pragma unroll 1
+    for (int u = 0; u < kNormUnroll; ++u) {
+        const unsigned i = u * kNormThreads + tid;
+        if (i >= count) continue;
+        float v[E];
+        values_of<T>(vectors[i], v);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float s = v[e] * scale;
+            sum[e & 1] = fmaf(s, s, sum[e & 1]);
+        }
+    }
+    return sum[0] + sum[1];
+}
 
 template <typename T> __device__ __forceinline__ double chunk_squares(const NormTable &t, int tensor, unsigned index, int tid)
 {
@@ -128,14 +154,9 @@ template <typename T> __device__ __forceinline__ double chunk_squares(const Norm
         bool any = false;
 #pragma unroll
         for (int u = 0; u < kNormUnroll; ++u) any |= (q[u].x | q[u].y | q[u].z | q[u].w) != 0;
-        total = 0.0;
-        if (any)
-#pragma unroll
-            for (int u = 0; u < kNormUnroll; ++u) {
-                float v[E];
-                values_of<T>(q[u], v);
-                for (int e = 0; e < E; ++e) total = fma(static_cast<double>(v[e]), static_cast<double>(v[e]), total);
-            }
+        const bool raise = all < kLeastSum;
+        const double back = raise ? kLower : kRaise;
+        if (any) total = squares_again<T>(vectors, static_cast<unsigned>(c.vectors), tid, raise ? kRaise : kLower) * (back * back);
     }
     if (c.lead && static_cast<unsigned>(tid) < c.head) {
         const double v = to_float(base[tid]);

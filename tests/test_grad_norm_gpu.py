@@ -102,6 +102,19 @@ def test_not_finite(ds, bad, at):
     assert torch.equal(out.nan_to_num(5.0), keep.nan_to_num(5.0))
 
 
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+def test_range_in_whole_vectors(ds, dtype):
+    """Shares of a thread whose squares leave fp32, next to ordinary ones, at every size of value."""
+    exponents = range(-24, 16, 3) if dtype == F16 else range(-149, 128, 5) if dtype == F32 else range(-133, 128, 5)
+    for e in exponents:
+        t = torch.full((5000,), 2.0 ** e, dtype=torch.float64).to(dtype).cuda()
+        t[::3] *= -1
+        t[::7] = 0
+        for tensors in ([t], [t, torch.ones(4096, dtype=dtype, device="cuda")]):
+            want, room = ref.norm(tensors)
+            ref.close(ds.grad_norm(tensors), np.array([want]), np.array([room]), f"2^{e}")
+
+
 def test_norm_past_fp32(ds):
     """A norm of finite values that fp32 does not hold is given as infinite, and clips nothing."""
     for n, whole in ((1, True), (300, False)):
