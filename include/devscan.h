@@ -470,7 +470,7 @@ devscan_status sample_tokens_bf16(const uint16_t *logits, size_t rows, size_t vo
  *             outputs' tokens must not overlap).  gate has x's type, or with
  *             gate_f32 != 0 is fp32 (always so in the f32 calls).
  *   rows, tokens : rows of `tokens` each; tokens == 1 is a decode step (one
- *             launch without any exchange).  rows * tokens < INT32_MAX,
+ *             launch without any exchange, as for few tokens of many rows).  rows * tokens < INT32_MAX,
  *             channels < INT32_MAX - 128;
  *   starts  : NULL, or device int32[rows + 1], not decreasing: the rows lie
  *             packed behind each other (slot_map's starts are such), token t of

@@ -142,6 +142,39 @@ def test_padded_batches(ds, real, dtype, channels):
     assert gx.isfinite().all() and gg.isfinite().all() and not gx[real:].any() and not gg[real:].any()
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dtype,gate_dtype", TYPES)
+def test_few_tokens(ds, dtype, gate_dtype, kind):
+    """Rows of a few tokens, whose threads go through them: one row and many, whole vectors and not."""
+    rng = np.random.default_rng(17)
+    for rows, tokens, channels in ((1, 2, 136), (3, 3, 24), (70, 5, 1000), (130, 8, 64), (130, 9, 1024), (9, 32, 1030), (40, 33, 256),
+                                   (600, 4, 3)):
+        check(ds, rng, rows, tokens, channels, dtype, gate_dtype, kind, carry=rows % 2 == 0, backward=False)
+
+
+def test_few_tokens_in_place(ds):
+    """Over x, from and into a pool; a first gate without a state does not count; other tokens stay."""
+    rng = np.random.default_rng(18)
+    x, gate = cuda(rng.standard_normal((6, 12, 200)), BF16), cuda(rng.standard_normal((6, 12, 200)), BF16)
+    states, slots = cuda(rng.standard_normal((9, 200))), torch.tensor([3, -1, 8, 0, 9, 5], dtype=torch.int32, device="cuda")
+    gate[[1, 4], 5] = float("nan")
+    before, keep = states.clone(), x.clone()
+    at = x[:, 5:11]
+    out, final = ds.gated_scan(at, gate[:, 5:11], initial=states, slots=slots, kind="sigmoid", out=at)
+    assert final is states and torch.equal(x[:, :5], keep[:, :5]) and torch.equal(x[:, 11:], keep[:, 11:])
+    # without a state the first token's b = (1 - a) x has its own gate in it
+    assert out[[1, 4], 0].isnan().all()
+    rows, used = [0, 2, 3, 5], [3, 8, 0, 5]
+    spans = ref.rows_of(None, 6, 4)
+    h, room, last, last_room = ref.scan(flat(keep[rows, 5:11]), flat(gate[rows, 5:11]), "sigmoid", spans, ref.as64(before)[used])
+    ref.close(out[rows].reshape(-1, 200), h, room, "out")
+    ref.close(states[used], last, last_room, "states")
+    assert torch.equal(states[[1, 2, 4, 6, 7]], before[[1, 2, 4, 6, 7]])
+    gate[:, 5] = float("nan")
+    free = ds.gated_scan(keep[:, 5:11], gate[:, 5:11], kind="decay")[0]
+    assert torch.equal(free[:, 0], keep[:, 5]) and free.isfinite().all()
+
+
 @pytest.mark.parametrize("at", [0, 30, 59])
 @pytest.mark.parametrize("dtype,channels,kind", [(BF16, 640, "sigmoid"), (F32, 333, "decay"), (F16, 333, "log")])
 def test_one_long_row(ds, dtype, channels, kind, at):
