@@ -1191,8 +1191,10 @@ inline void plan(GatedRows &rows, int per_lane, int tokens_per_warp, int places_
     // 60,000 770 -> 211.  Where there is none the launch looks and leaves: 0.6 us (24
     // rows, 8191 x 1000 fp32).  With it in front that was 1.9 (and 37 in the first
     // case), and rows of a quarter of all were slower.  Not for rows that one span's
-    // blocks finish in eight rounds, nor where channels fill the GPU.
-    const size_t least = 8 * tile * blocks;
+    // blocks finish in eight rounds, nor where channels fill the GPU; nor for rows that
+    // are shorter than a span's share (beside a long padded end), since they need
+    // not reach a share's end, which is where spans leave them out.
+    const size_t share = (all + spans - 1) / spans, rounds = 8 * tile * blocks, least = rounds > share ? rounds : share;
     if (rows.starts != nullptr && spans > 1 && all >= least && blocks < kPortableBlocks && 4 * blocks * groups <= places)
         rows.long_from = static_cast<unsigned>(least);
 }

@@ -192,6 +192,22 @@ def test_one_long_row(ds, dtype, channels, kind, at):
         check(ds, rng, 60, starts[-1] + 500, channels, dtype, dtype, kind, starts=starts, carry=at == 0)
 
 
+def test_one_long_row_within_a_share(ds):
+    """A row longer than half of all that ends inside the first share of a padded batch, in place."""
+    rng = np.random.default_rng(19)
+    for starts, n, channels in (([0, 200, 4200, 4300, 4400, 4900, 5000], 36000, 640), ([0, 10, 910, 1000], 60000, 640),
+                                ([0, 5000, 5100], 30000, 256)):
+        rows = len(starts) - 1
+        x, gate = cuda(rng.standard_normal((n, channels)), BF16), cuda(rng.standard_normal((n, channels)), BF16)
+        states, where = cuda(rng.standard_normal((rows, channels))), torch.tensor(starts, dtype=torch.int32, device="cuda")
+        h, room, last, last_room = ref.scan(flat(x), flat(gate), "sigmoid", ref.rows_of(starts, n, rows), ref.as64(states))
+        for _ in range(3):
+            into, pool = x.clone(), states.clone()
+            ds.gated_scan(into, gate, starts=where, initial=pool, kind="sigmoid", out=into, final=pool)
+            ref.close(into, h, room, "out")
+            ref.close(pool, last, last_room, "states")
+
+
 def test_one_long_row_that_is_cut(ds):
     """Rows that begin in front of the tokens or go on behind them."""
     rng = np.random.default_rng(15)
