@@ -3,13 +3,20 @@ radix one-bit split as hand-written sm_103a CUDA kernels behind a C ABI.
 
 The functions below take CUDA tensors (PyTorch is used for device memory
 and streams only), pass their device pointers and the current CUDA stream
-to ``libdevscan.so`` and return.  All work is asynchronous on that stream.
+to ``libdevscan.so`` and return.  All work is asynchronous on that stream, or
+on the one that ``stream`` names (an object or a handle).  What a call makes for
+itself, outputs that it was not given among it, is memory of the stream that it
+runs on; that the tensors which it was given are ready there, and that what it
+returns is ready where it is used, the caller sees to, as with any torch
+operation on two streams.
 ``scan_host`` is the host-buffer entry: the library copies a pinned host
 array to the device, scans it and copies the result back.
 """
 from __future__ import annotations
 
 import array
+import contextlib
+import functools
 import operator
 
 import torch
@@ -45,6 +52,29 @@ def _stream_handle(stream) -> int:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _on(stream):
+    """Context in which torch works on that stream (None: on the current one)."""
+    if stream is None or _stream_handle(stream) == _stream_handle(None):
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        handle = int(stream)                 # 0 and 1 are the legacy default stream
+        stream = torch.cuda.ExternalStream(handle) if handle > 1 else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
+def _made_on(stream, make, *args, **kwargs) -> torch.Tensor:
+    """``make(*args, **kwargs)`` in the memory of that stream.  A block of the
+    current stream's may still be in use there by kernels of its last owner, and
+    goes to its next one as soon as it is freed, while the call runs on another."""
+    with _on(stream):
+        return make(*args, **kwargs)
+
+
+def _empty_on(stream):
+    """``torch.empty`` for what a call on that stream makes."""
+    return functools.partial(_made_on, stream, torch.empty)
+
+
 def _check_cuda(t: torch.Tensor, name: str) -> None:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -58,7 +88,7 @@ def _scan(direction: str, x: torch.Tensor, out, op: str, stream, dtype_override=
     if suffix is None:
         raise TypeError(f"unsupported dtype {x.dtype} (int32, uint32, float32)")
     if out is None:
-        out = torch.empty_like(x)
+        out = torch.empty_like(x) if stream is None else _made_on(stream, torch.empty_like, x)
     _check_cuda(out, "out")
     if out.numel() != x.numel() or out.dtype != x.dtype:
         raise ValueError("out must match x in size and dtype")
@@ -92,7 +122,7 @@ def _carry_scan(direction: str, x: torch.Tensor, carry: torch.Tensor | None, out
         if carry.dtype != x.dtype or carry.numel() < 1:
             raise ValueError("carry must be a device tensor of x's dtype holding one element")
     if out is None:
-        out = torch.empty_like(x)
+        out = torch.empty_like(x) if stream is None else _made_on(stream, torch.empty_like, x)
     _check_cuda(out, "out")
     if out.numel() != x.numel() or out.dtype != x.dtype:
         raise ValueError("out must match x in size and dtype")
@@ -123,8 +153,9 @@ def reduce(x: torch.Tensor, op: str = "add", out: torch.Tensor | None = None, st
     suffix = "u32" if as_uint32 else _SUFFIX.get(x.dtype)
     if suffix is None:
         raise TypeError(f"unsupported dtype {x.dtype} (int32, uint32, float32)")
+    empty = torch.empty if stream is None else _empty_on(stream)
     if out is None:
-        out = torch.empty(1, dtype=x.dtype, device=x.device)
+        out = empty(1, dtype=x.dtype, device=x.device)
     _check_cuda(out, "out")
     if out.dtype != x.dtype or out.numel() < 1:
         raise ValueError("out must hold one element of x's dtype")
@@ -160,7 +191,8 @@ def sharded_scan(shard: torch.Tensor, out: torch.Tensor | None = None, inclusive
     import torch.distributed as dist
     rank = dist.get_rank(group) if dist.is_available() and dist.is_initialized() else 0
     total = reduce(shard, op, stream=stream, as_uint32=as_uint32)
-    totals = exchange_totals(total, group)
+    with _on(stream):
+        totals = exchange_totals(total, group)
     carry = reduce(totals[:rank], op, stream=stream, as_uint32=as_uint32)
     fn = scan_inclusive_carry if inclusive else scan_exclusive_carry
     return fn(shard, carry, out, op=op, stream=stream, as_uint32=as_uint32)
@@ -185,7 +217,8 @@ def sharded_compact(values: torch.Tensor, flags: torch.Tensor | None = None, thr
         out, count = compact(values, flags, out, stream=stream)
     else:
         out, count = compact_greater(values, threshold, out, stream=stream)
-    counts = exchange_totals(count, group)
+    with _on(stream):
+        counts = exchange_totals(count, group)
     offset = reduce(counts[:rank], "add", stream=stream)
     total = reduce(counts, "add", stream=stream)
     return out, count, offset, total
@@ -200,7 +233,7 @@ def _segscan(direction: str, x: torch.Tensor, heads: torch.Tensor, out, op: str,
     if heads.dtype != torch.uint8 or heads.numel() != x.numel():
         raise ValueError("heads must be a uint8 tensor of x's length")
     if out is None:
-        out = torch.empty_like(x)
+        out = torch.empty_like(x) if stream is None else _made_on(stream, torch.empty_like, x)
     _check_cuda(out, "out")
     if out.numel() != x.numel() or out.dtype != x.dtype:
         raise ValueError("out must match x in size and dtype")
@@ -236,9 +269,10 @@ def compact(values: torch.Tensor, flags: torch.Tensor, out: torch.Tensor | None 
     if values.numel() != flags.numel():
         raise ValueError("values and flags differ in length")
     if out is None:
-        out = torch.empty_like(values)
+        out = torch.empty_like(values) if stream is None else _made_on(stream, torch.empty_like, values)
+    empty = torch.empty if stream is None else _empty_on(stream)
     if count is None:
-        count = torch.empty(1, dtype=torch.int32, device=values.device)
+        count = empty(1, dtype=torch.int32, device=values.device)
     _check_cuda(out, "out")
     _check_cuda(count, "count")
     _lib.check(load().compact_i32(values.data_ptr(), flags.data_ptr(), out.data_ptr(), count.data_ptr(),
@@ -255,9 +289,10 @@ def compact_greater(values: torch.Tensor, threshold: int, out: torch.Tensor | No
     if values.dtype != torch.int32:
         raise TypeError("values must be int32")
     if out is None:
-        out = torch.empty_like(values)
+        out = torch.empty_like(values) if stream is None else _made_on(stream, torch.empty_like, values)
+    empty = torch.empty if stream is None else _empty_on(stream)
     if count is None:
-        count = torch.empty(1, dtype=torch.int32, device=values.device)
+        count = empty(1, dtype=torch.int32, device=values.device)
     _check_cuda(out, "out")
     _check_cuda(count, "count")
     _lib.check(load().compact_gt_i32(values.data_ptr(), int(threshold), out.data_ptr(), count.data_ptr(),
@@ -275,11 +310,12 @@ def bracket_scan(weights: torch.Tensor, out: torch.Tensor | None = None, result:
     if weights.dtype != torch.int32:
         raise TypeError("weights must be int32")
     if store and out is None:
-        out = torch.empty_like(weights)
+        out = torch.empty_like(weights) if stream is None else _made_on(stream, torch.empty_like, weights)
     if not store:
         out = None
+    empty = torch.empty if stream is None else _empty_on(stream)
     if result is None:
-        result = torch.empty(2, dtype=torch.int32, device=weights.device)
+        result = empty(2, dtype=torch.int32, device=weights.device)
     _check_cuda(result, "result")
     if out is not None:
         _check_cuda(out, "out")
@@ -295,7 +331,7 @@ def split_bit(keys: torch.Tensor, bit: int, out: torch.Tensor | None = None, str
     if keys.element_size() != 4 or keys.is_floating_point():
         raise TypeError("keys must be a 32-bit integer tensor (bits read as uint32)")
     if out is None:
-        out = torch.empty_like(keys)
+        out = torch.empty_like(keys) if stream is None else _made_on(stream, torch.empty_like, keys)
     _check_cuda(out, "out")
     _lib.check(load().split_bit_u32(keys.data_ptr(), out.data_ptr(), int(bit), keys.numel(),
                                     _stream_handle(stream)), "split_bit_u32")
@@ -309,7 +345,7 @@ def radix_sort(keys: torch.Tensor, tmp: torch.Tensor | None = None, stream=None)
     if keys.element_size() != 4 or keys.is_floating_point():
         raise TypeError("keys must be a 32-bit integer tensor (bits read as uint32)")
     if tmp is None:
-        tmp = torch.empty_like(keys)
+        tmp = torch.empty_like(keys) if stream is None else _made_on(stream, torch.empty_like, keys)
     _check_cuda(tmp, "tmp")
     _lib.check(load().radix_sort_u32(keys.data_ptr(), tmp.data_ptr(), keys.numel(), _stream_handle(stream)),
                "radix_sort_u32")
@@ -323,7 +359,7 @@ def radix_sort_digits(keys: torch.Tensor, tmp: torch.Tensor | None = None, strea
     if keys.element_size() != 4 or keys.is_floating_point():
         raise TypeError("keys must be a 32-bit integer tensor (bits read as uint32)")
     if tmp is None:
-        tmp = torch.empty_like(keys)
+        tmp = torch.empty_like(keys) if stream is None else _made_on(stream, torch.empty_like, keys)
     _check_cuda(tmp, "tmp")
     _lib.check(load().radix_sort_digits_u32(keys.data_ptr(), tmp.data_ptr(), keys.numel(),
                                             _stream_handle(stream)), "radix_sort_digits_u32")
@@ -380,10 +416,11 @@ def block_table_extend(table: torch.Tensor, cached: torch.Tensor, fresh: torch.T
     stride = _check_table(table, page_size)
     rows, width = table.shape
     pool = pages.numel()
+    empty = torch.empty if stream is None else _empty_on(stream)
     if granted is None:
-        granted = torch.empty(rows, dtype=torch.uint8, device=table.device)
+        granted = empty(rows, dtype=torch.uint8, device=table.device)
     if left is None:
-        left = torch.empty(1, dtype=torch.int32, device=table.device)
+        left = empty(1, dtype=torch.int32, device=table.device)
     status = load().block_table_extend_i32(
         table.data_ptr(), stride, rows, width, _check_vector(cached, "cached", torch.int32, rows),
         _check_vector(fresh, "fresh", torch.int32, rows), int(page_size),
@@ -407,8 +444,9 @@ def slot_map(table: torch.Tensor, cached: torch.Tensor, fresh: torch.Tensor, pag
     tokens = int(tokens)
     if tokens < 0:
         raise ValueError("tokens must not be negative")
+    empty = torch.empty if stream is None else _empty_on(stream)
     if out is None:
-        new = lambda n, dtype: torch.empty(n, dtype=dtype, device=table.device)  # noqa: E731
+        new = lambda n, dtype: empty(n, dtype=dtype, device=table.device)  # noqa: E731
         out = (new(rows + 1, torch.int32), new(tokens, torch.int64), new(tokens, torch.int32),
                new(tokens, torch.int32))
     starts, slots, positions, row_ids = out
@@ -434,8 +472,9 @@ def block_table_release(table: torch.Tensor, cached: torch.Tensor, done: torch.T
     stride = _check_table(table, page_size)
     rows, width = table.shape
     pool = pages.numel()
+    empty = torch.empty if stream is None else _empty_on(stream)
     if left is None:
-        left = torch.empty(1, dtype=torch.int32, device=table.device)
+        left = empty(1, dtype=torch.int32, device=table.device)
     status = load().block_table_release_i32(
         table.data_ptr(), stride, rows, width, _check_vector(cached, "cached", torch.int32, rows),
         _check_vector(done, "done", torch.uint8, rows), int(page_size),
@@ -472,10 +511,11 @@ def sample_tokens(logits: torch.Tensor, noise: torch.Tensor | None = None, tempe
             raise TypeError("noise must be float32")
         if noise.shape != logits.shape:
             raise ValueError("noise must have the logits' shape")
+    empty = torch.empty if stream is None else _empty_on(stream)
     if out is None:
-        out = torch.empty(rows, dtype=torch.int32, device=logits.device)
+        out = empty(rows, dtype=torch.int32, device=logits.device)
     if logprobs is None:
-        logprobs = torch.empty(rows, dtype=torch.float32, device=logits.device)
+        logprobs = empty(rows, dtype=torch.float32, device=logits.device)
     f32, i32 = torch.float32, torch.int32
     status = getattr(load(), _SAMPLE_SYMBOL[logits.dtype])(
         logits.data_ptr(), rows, vocab, stride, None if noise is None else noise.data_ptr(), noise_stride,
@@ -603,9 +643,10 @@ def gated_scan(x: torch.Tensor, gate: torch.Tensor, starts: torch.Tensor | None 
     suffix = _value_suffix(x)
     here = _device_of(x, "x")
     rows, tokens, channels, number, wide = _gated_rows(x, gate, starts, kind)
+    empty = torch.empty if stream is None else _empty_on(stream)
     if final is None:
         if slots is None:
-            final = torch.empty(rows, channels, dtype=_F32, device=x.device)
+            final = empty(rows, channels, dtype=_F32, device=x.device)
         elif initial is None:
             raise ValueError("slots need initial or final to point into")
         else:
@@ -615,7 +656,7 @@ def gated_scan(x: torch.Tensor, gate: torch.Tensor, starts: torch.Tensor | None 
         raise ValueError(f"final must hold {rows} states")
     shape, dtype = x.shape, x.dtype
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=x.device)
+        out = empty(shape, dtype=dtype, device=x.device)
     x_at, x_row, x_token = _token_array(x, "x", shape, dtype, here)
     gate_at, gate_row, gate_token = _token_array(gate, "gate", shape, gate.dtype, here)
     out_at, out_row, out_token = _token_array(out, "out", shape, dtype, here)
@@ -649,12 +690,13 @@ def gated_scan_backward(grad: torch.Tensor, x: torch.Tensor | None, gate: torch.
     shape, dtype, device = y.shape, y.dtype, y.device
     if kind == "sigmoid" and x is None:
         raise ValueError("sigmoid needs x")
+    empty = torch.empty if stream is None else _empty_on(stream)
     if grad_x is None:
-        grad_x = torch.empty(shape, dtype=dtype, device=device)
+        grad_x = empty(shape, dtype=dtype, device=device)
     if grad_gate is None:
-        grad_gate = torch.empty(shape, dtype=gate.dtype, device=device)
+        grad_gate = empty(shape, dtype=gate.dtype, device=device)
     if grad_initial is None and initial is not None:
-        grad_initial = torch.empty(rows, channels, dtype=_F32, device=device)
+        grad_initial = empty(rows, channels, dtype=_F32, device=device)
     status = getattr(load(), "gated_scan_backward_" + suffix)(
         *_token_array(grad, "grad", shape, dtype, here),
         *((None, 0, 0) if x is None else _token_array(x, "x", shape, dtype, here)),
@@ -700,7 +742,8 @@ def expert_sort(experts: torch.Tensor, num_experts: int, align: int = 1, rows: i
     rows = int(rows)
     if rows < 0:
         raise ValueError("rows must not be negative")
-    device, empty = experts.device, torch.empty
+    device = experts.device
+    empty = torch.empty if stream is None else _empty_on(stream)
     if starts is None:
         starts = empty(num_experts + 1, dtype=_I32, device=device)
     if counts is None:
@@ -759,8 +802,9 @@ def expert_dispatch(x: torch.Tensor, places: torch.Tensor, order: torch.Tensor, 
     if x.dim() != 2 or x.shape[1] < 1:
         raise ValueError("x must be [tokens, width]")
     width, rows, size, dtype = x.shape[1], order.numel(), x.element_size(), x.dtype
+    empty = torch.empty if stream is None else _empty_on(stream)
     if out is None:
-        out = torch.empty(rows, width, dtype=dtype, device=x.device)
+        out = empty(rows, width, dtype=dtype, device=x.device)
     status = load().expert_dispatch(
         x.data_ptr(), _check_rows(x, "x", tokens, width, dtype, here) * size, width * size, tokens, choices,
         places.data_ptr(), rows, _vector(order, "order", _I32, rows, here), out.data_ptr(),
@@ -783,8 +827,9 @@ def expert_combine(y: torch.Tensor, places: torch.Tensor, weights: torch.Tensor 
         raise ValueError("y must be [rows, width]")
     rows, width = y.shape
     dtype = y.dtype
+    empty = torch.empty if stream is None else _empty_on(stream)
     if out is None:
-        out = torch.empty(tokens, width, dtype=dtype, device=y.device)
+        out = empty(tokens, width, dtype=dtype, device=y.device)
     status = getattr(load(), "expert_combine_" + suffix)(
         y.data_ptr(), _check_rows(y, "y", rows, width, dtype, here), rows, tokens, choices, width, places.data_ptr(),
         _vector(weights, "weights", _F32, tokens * choices, here), out.data_ptr(),
@@ -810,10 +855,11 @@ def expert_combine_backward(grad: torch.Tensor, y: torch.Tensor, places: torch.T
         raise ValueError("y must be [rows, width]")
     rows, width = y.shape
     dtype, pairs = y.dtype, tokens * choices
+    empty = torch.empty if stream is None else _empty_on(stream)
     if grad_y is None:
-        grad_y = torch.empty(rows, width, dtype=dtype, device=y.device)
+        grad_y = empty(rows, width, dtype=dtype, device=y.device)
     if grad_weights is None and weights is not None:
-        grad_weights = torch.empty(tokens, choices, dtype=_F32, device=y.device)
+        grad_weights = empty(tokens, choices, dtype=_F32, device=y.device)
     status = getattr(load(), "expert_combine_backward_" + suffix)(
         grad.data_ptr(), _check_rows(grad, "grad", tokens, width, dtype, here), y.data_ptr(),
         _check_rows(y, "y", rows, width, dtype, here), rows, tokens, choices, width, places.data_ptr(),
@@ -858,15 +904,12 @@ def _norm(tensors, out, max_norm, norm, work, stream):
     table = array.array("Q", bytes(32 * max(count, 1)))   # of devscan_tensor, four words each
     for word, values in enumerate((at, to, sizes, kinds)):
         table[word:4 * count:4] = array.array("Q", values)
+    empty = torch.empty if stream is None else _empty_on(stream)
     if norm is None:
-        norm = torch.empty((), dtype=_F32, device="cuda")
+        norm = empty((), dtype=_F32, device="cuda")
     need = _lib.norm_work_bytes(count)
     if work is None:
-        if stream is None:
-            work = torch.empty(need, dtype=torch.uint8, device="cuda")
-        else:   # from that stream's memory: neither its last owner nor its next then runs beside the call
-            with torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))):
-                work = torch.empty(need, dtype=torch.uint8, device="cuda")
+        work = empty(need, dtype=torch.uint8, device="cuda")
     here = _device_of(work, "work")
     if not work.is_contiguous():
         raise ValueError("work must be contiguous")
@@ -923,9 +966,10 @@ def scan_host(x_host: torch.Tensor, inclusive: bool = False, op: str = "add", de
     if suffix is None:
         raise TypeError(f"unsupported dtype {x_host.dtype} (int32, uint32, float32)")
     s = stream if stream is not None else torch.cuda.current_stream()
+    empty = torch.empty if stream is None else _empty_on(stream)
     if work is None:
-        d_in = torch.empty(x_host.shape, dtype=x_host.dtype, device=device)
-        d_out = torch.empty_like(d_in)
+        d_in = empty(x_host.shape, dtype=x_host.dtype, device=device)
+        d_out = _made_on(stream, torch.empty_like, d_in)
     else:
         d_in, d_out = work
         _check_cuda(d_in, "work[0]")
