@@ -475,7 +475,8 @@ devscan_status sample_tokens_bf16(const uint16_t *logits, size_t rows, size_t vo
  *   starts  : NULL, or device int32[rows + 1], not decreasing: the rows lie
  *             packed behind each other (slot_map's starts are such), token t of
  *             the packing at t * stride, row r being the tokens starts[r] ..
- *             starts[r + 1] - 1 of the `tokens` that there are.  Rows may be
+ *             starts[r + 1] - 1 of the `tokens` that there are, the first and
+ *             last of which are its own first and last.  Rows may be
  *             empty.  Tokens in no row (a padded batch) get 0 and are not
  *             otherwise looked at; row_strides are not used;
  *   initial : device float[pool][channels] or NULL (0): h before a row's

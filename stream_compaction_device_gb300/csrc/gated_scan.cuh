@@ -274,7 +274,8 @@ __device__ __forceinline__ TokenPlace place_of(const GatedRows &rows, unsigned n
     // the last row that begins at or before n: of rows that begin alike, the one with tokens
     p.row = row_at(rows, static_cast<int>(n));
     p.inside = p.row >= 0 && p.row < rows.rows;
-    p.first = p.inside && __ldg(rows.starts + p.row) == static_cast<int>(n);
+    // a row that begins in front of the tokens has its first one at 0
+    p.first = p.inside && max(__ldg(rows.starts + p.row), 0) == static_cast<int>(n);
     p.last = p.inside && (__ldg(rows.starts + p.row + 1) == static_cast<int>(n + 1) || n + 1 == rows.all());
     return p;
 }
@@ -573,7 +574,7 @@ __device__ __forceinline__ Edges edges_of(const GatedRows &rows, const Run &r, i
         if (some && rows.starts == nullptr) {
             in.begin = row * rows.tokens, in.end = in.begin + rows.tokens;
         } else if (some) {
-            in.begin = static_cast<unsigned>(__ldg(rows.starts + row));
+            in.begin = static_cast<unsigned>(max(__ldg(rows.starts + row), 0));
             in.end = min(static_cast<unsigned>(__ldg(rows.starts + row + 1)), rows.all());
         }
     }
