@@ -480,7 +480,8 @@ devscan_status sample_tokens_bf16(const uint16_t *logits, size_t rows, size_t vo
  *             empty.  Tokens in no row (a padded batch) get 0 and are not
  *             otherwise looked at; row_strides are not used;
  *   initial : device float[pool][channels] or NULL (0): h before a row's
- *             first token.  The first token's gate counts only with it;
+ *             first token.  Without it the first token's gate counts only in
+ *             sigmoid's b;
  *   final   : device float[pool][channels] or NULL: gets h after a row's last
  *             token; for an empty row, initial.  It may be `initial` itself;
  *   slots   : device int32[rows] or NULL: row r's state is at slots[r] in
@@ -500,7 +501,8 @@ devscan_status sample_tokens_bf16(const uint16_t *logits, size_t rows, size_t vo
  * first:
  *   grad_x = w (sigmoid: (1 - a) w),   f = a w (at last: grad_initial),
  *   grad_gate = w h' (decay), w h' a (log), w (h' - x) a (1 - a) (sigmoid),
- * h' being y of the token before, or initial.  x is read for sigmoid only (else
+ * h' being y of the token before, or initial; a first gate that does not count
+ * has the gradient 0, whatever it holds.  x is read for sigmoid only (else
  * it may be NULL).  States lie by row (no slots); tokens in no row get 0;
  * outputs overlap nothing but as above.
  *

@@ -31,3 +31,28 @@ def test_first_gates_in_front(ds, kind):  # noqa: F811
     gate[[0, 9]] = float("nan")
     out, final = ds.gated_scan(x, gate, starts=where, kind=kind)
     assert out.isfinite().all() and torch.equal(out, want) and torch.equal(final, last)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), 200.0])
+@pytest.mark.parametrize("kind", ["decay", "log"])
+@pytest.mark.parametrize("dtype,channels", [(F32, 40), (BF16, 64), (BF16, 33)])
+def test_gradients_of_first_gates(ds, dtype, channels, kind, bad):  # noqa: F811
+    """What does not count has no gradient, whatever it holds: the first gates of
+    rows without a state, of equal rows and of packed ones."""
+    rng = np.random.default_rng(3)
+    for starts in (None, [0, 1, 1, 60, 100]):
+        shape = (3, 100, channels) if starts is None else (110, channels)
+        x, gate = cuda(rng.standard_normal(shape), dtype), cuda(gates(rng, shape, kind), dtype)
+        grad = cuda(rng.standard_normal(shape), dtype)
+        where = None if starts is None else torch.tensor(starts, dtype=torch.int32, device="cuda")
+        first = (slice(None), 0) if starts is None else ([0, 1, 60],)
+        y = ds.gated_scan(x, gate, starts=where, kind=kind)[0]
+        want = ds.gated_scan_backward(grad, None, gate, y, starts=where, kind=kind)
+        assert not want[1][first].any()
+        gate[first] = bad
+        assert torch.equal(ds.gated_scan(x, gate, starts=where, kind=kind)[0], y)
+        got = ds.gated_scan_backward(grad, None, gate, y, starts=where, kind=kind)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        grad[first] = float("inf")
+        got = ds.gated_scan_backward(grad, None, gate, y, starts=where, kind=kind)
+        assert torch.equal(got[1], want[1])
