@@ -490,8 +490,8 @@ devscan_status sample_tokens_bf16(const uint16_t *logits, size_t rows, size_t vo
  *             they are.  Slots of two rows should differ; if not, which row's
  *             state remains is not defined.  NULL: r itself, pool >= rows.
  * out may be x itself, with its strides; otherwise it overlaps no other array,
- * except that arrays of the same strides may lie side by side in each
- * token (DEVSCAN_ERR_INVALID).  Pointers are aligned to their element.
+ * except that arrays of the same strides, batch-major or time-major, may lie
+ * side by side in each token (DEVSCAN_ERR_INVALID).  Pointers are aligned to their element.
  *
  * gated_scan_backward_T, from the gradients of out (grad, in its type) and of
  * final (grad_final, float[rows][channels] or NULL), gives those of x, gate

@@ -7,6 +7,7 @@
 #include <memory>
 #include <mutex>
 #include <new>
+#include <numeric>
 #include <utility>
 #include <vector>
 
@@ -382,20 +383,22 @@ bool check_values(Values *v, const GatedRows &rows, bool output)
 
 // Whether an output and another array may share memory: not where they lie
 // apart, nor where both have the same strides and their channels lie side by
-// side within a token's.
+// side within a token's: every token begins at a multiple of the strides'
+// common divisor, and modulo that the two are apart.  (Batch-major tokens are
+// their own stride apart, time-major ones their rows'.)
 bool values_overlap(const Values &a, const Values &b, const GatedRows &rows)
 {
     if (a.bytes == 0 || b.bytes == 0 || !overlaps(a.array.data, a.bytes, b.array.data, b.bytes)) return false;
-    const bool one_row = rows.starts != nullptr || rows.rows == 1;
-    if (one_row && rows.tokens < 2) return true;
-    const bool steps = rows.tokens == 1;   // rows of one token each: a row is a token
-    const size_t row = a.array.row_stride * a.size, row_b = b.array.row_stride * b.size;
-    const size_t stride = steps ? row : a.array.stride * a.size, stride_b = steps ? row_b : b.array.stride * b.size;
-    if (stride == 0 || stride != stride_b || (!one_row && (row != row_b || row % stride != 0))) return true;
+    const bool one_row = rows.starts != nullptr || rows.rows == 1, one_token = rows.tokens == 1;
+    if (one_row && one_token) return true;
+    const size_t row = one_row ? 0 : a.array.row_stride * a.size, row_b = one_row ? 0 : b.array.row_stride * b.size;
+    const size_t step = one_token ? 0 : a.array.stride * a.size, step_b = one_token ? 0 : b.array.stride * b.size;
+    const size_t apart = std::gcd(row, step);
+    if (apart == 0 || row != row_b || step != step_b) return true;
     const uintptr_t x = reinterpret_cast<uintptr_t>(a.array.data), y = reinterpret_cast<uintptr_t>(b.array.data);
-    const size_t shift = x <= y ? (y - x) % stride : (stride - (x - y) % stride) % stride;   // of b within a's token
+    const size_t shift = x <= y ? (y - x) % apart : (apart - (x - y) % apart) % apart;   // of b within a's token
     const size_t c = static_cast<size_t>(rows.channels);
-    return shift < c * a.size || shift + c * b.size > stride;
+    return shift < c * a.size || shift + c * b.size > apart;
 }
 
 // What forward and backward check alike.

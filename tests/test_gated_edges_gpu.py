@@ -56,3 +56,32 @@ def test_gradients_of_first_gates(ds, dtype, channels, kind, bad):  # noqa: F811
         grad[first] = float("inf")
         got = ds.gated_scan_backward(grad, None, gate, y, starts=where, kind=kind)
         assert torch.equal(got[1], want[1])
+
+
+def test_time_major_arrays_side_by_side(ds):  # noqa: F811
+    """Parts of one time-major projection, [tokens, rows, parts x channels], as
+    x, gate and outputs: the same strides, side by side in each token."""
+    rng = np.random.default_rng(5)
+    for tokens, rows, c in ((40, 3, 16), (5, 4, 24), (200, 2, 8)):
+        buffer = cuda(rng.standard_normal((tokens, rows, 5 * c)), BF16)
+        parts = [buffer[..., c * i:c * i + c].transpose(0, 1) for i in range(5)]
+        x, gate = parts[0].contiguous(), parts[2].contiguous()
+        want, _ = ds.gated_scan(x, gate, kind="sigmoid")
+        out, _ = ds.gated_scan(parts[0], parts[2], kind="sigmoid", out=parts[1])
+        assert torch.equal(out, want) and torch.equal(parts[0], x) and torch.equal(parts[2], gate)
+        back = ds.gated_scan_backward(x, x, gate, want, kind="sigmoid")
+        ds.gated_scan_backward(parts[0], parts[0], parts[2], parts[1], kind="sigmoid", grad_x=parts[4], grad_gate=parts[3])
+        assert torch.equal(parts[4], back[0]) and torch.equal(parts[3], back[1]) and torch.equal(parts[1], want)
+        for shift in (c // 2, c + c // 2, 4 * c + c // 2):      # across a neighbour, and into the next row's
+            if shift + c <= 5 * c:
+                with pytest.raises(ds.DevscanError):
+                    ds.gated_scan(parts[0], parts[2], kind="sigmoid", out=buffer[..., shift:shift + c].transpose(0, 1))
+        wide = buffer.reshape(tokens, -1)                       # the last part shifted into the next row's first
+        across = wide[:, 4 * c + c // 2:].as_strided((rows - 1, tokens, c), (5 * c, rows * 5 * c, 1))
+        x, gate = x[:-1], gate[:-1]
+        if rows > 2:
+            with pytest.raises(ds.DevscanError):
+                ds.gated_scan(parts[0][:-1], parts[2][:-1], kind="sigmoid", out=across)
+        else:                                                   # one row, and the next one's part is not given
+            want, _ = ds.gated_scan(x, gate, kind="sigmoid")
+            assert torch.equal(ds.gated_scan(parts[0][:-1], parts[2][:-1], kind="sigmoid", out=across)[0], want)
