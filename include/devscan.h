@@ -585,6 +585,8 @@ devscan_status gated_scan_backward_bf16(const uint16_t *grad, size_t grad_row_st
  * grad_weights may be NULL, and then y too.  Rows of which `order` (or NULL)
  * says -1 become 0, others are left as they were.
  *
+ * Calls whose tokens and an eighth of whose rows pass INT32_MAX together may be
+ * more than a launch holds, and are then refused (DEVSCAN_ERR_INVALID).
  * Places outside 0 .. rows - 1 count as none; two pairs with the same place
  * (expert_sort gives none) leave either's row.  No buffer that is written may
  * overlap another (DEVSCAN_ERR_INVALID).  No scratch; the same call gives the

@@ -535,6 +535,9 @@ bool expert_sizes(size_t tokens, size_t choices, size_t rows, size_t width)
            tokens * choices <= kMost;
 }
 
+// More tokens and rows than a grid has blocks are an argument's fault.
+devscan_status from_grid(cudaError_t e) { return e == cudaErrorInvalidConfiguration ? DEVSCAN_ERR_INVALID : from_cuda(e); }
+
 devscan_status expert_combine_common(ValueType type, const ExpertCombineCall &call, size_t rows, size_t tokens,
                                      size_t choices, size_t width, cudaStream_t stream)
 {
@@ -555,7 +558,7 @@ devscan_status expert_combine_common(ValueType type, const ExpertCombineCall &ca
     ExpertCombineCall c = call;
     c.rows = static_cast<unsigned>(rows), c.tokens = static_cast<unsigned>(tokens);
     c.width = static_cast<unsigned>(width), c.choices = static_cast<int>(choices);
-    return from_cuda(launch_expert_combine(type, c, stream));
+    return from_grid(launch_expert_combine(type, c, stream));
 }
 
 devscan_status expert_combine_backward_common(ValueType type, const ExpertCombineBackwardCall &call, size_t rows,
@@ -585,7 +588,7 @@ devscan_status expert_combine_backward_common(ValueType type, const ExpertCombin
     ExpertCombineBackwardCall c = call;
     c.rows = static_cast<unsigned>(rows), c.tokens = static_cast<unsigned>(tokens);
     c.width = static_cast<unsigned>(width), c.choices = static_cast<int>(choices);
-    return from_cuda(launch_expert_combine_backward(type, c, stream));
+    return from_grid(launch_expert_combine_backward(type, c, stream));
 }
 
 devscan_status norm_common(const devscan_tensor *tensors, size_t count, bool clip, float max_norm, float *norm, void *work,
@@ -1180,7 +1183,7 @@ devscan_status expert_dispatch(const void *x, size_t x_stride, size_t row_bytes,
     const Span written[] = {{out, out_bytes}};
     const Span read[] = {{x, x_bytes}, {places, tokens * choices * 4}, {order, rows * 4}};
     if (written_overlap(written, read)) return DEVSCAN_ERR_INVALID;
-    return from_cuda(launch_expert_dispatch({x, x_stride, row_bytes, static_cast<unsigned>(tokens),
+    return from_grid(launch_expert_dispatch({x, x_stride, row_bytes, static_cast<unsigned>(tokens),
                                              static_cast<unsigned>(rows), static_cast<int>(choices), places, order, out,
                                              out_stride},
                                             stream));

@@ -258,7 +258,7 @@ cudaError_t dispatch(const ExpertMoveCall &call, cudaStream_t s)
     const size_t items = static_cast<size_t>(call.tokens) * runs + (call.order != nullptr ? (call.rows + kPadRows - 1u) / kPadRows : 0);
     if (items == 0) return cudaSuccess;
     const size_t blocks = (items + WARPS - 1) / WARPS;
-    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
     return launch_dependent(expert_dispatch_kernel<V, U, WARPS>, static_cast<unsigned>(blocks), 32 * WARPS, s, call, vectors, runs);
 }
 
@@ -471,7 +471,7 @@ cudaError_t combine(const ExpertCombineCall &call, cudaStream_t s)
 {
     const unsigned runs = (call.width + 32 * V * U - 1) / (32 * V * U);
     const size_t blocks = (static_cast<size_t>(call.tokens) * runs + kMoveWarps - 1) / kMoveWarps;
-    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
     expert_combine_kernel<T, V, U><<<static_cast<unsigned>(blocks), 32 * kMoveWarps, 0, s>>>(call, runs);
     return cudaGetLastError();
 }
@@ -491,7 +491,7 @@ cudaError_t combine_backward(const ExpertCombineBackwardCall &call, cudaStream_t
     const size_t blocks = static_cast<size_t>(call.tokens) +
                           (call.order != nullptr ? (call.rows + kPadRows * kBackWarps - 1u) / (kPadRows * kBackWarps) : 0);
     if (blocks == 0) return cudaSuccess;
-    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
     expert_combine_backward_kernel<T, V, U><<<static_cast<unsigned>(blocks), 32 * kBackWarps, 0, s>>>(call);
     return cudaGetLastError();
 }
