@@ -51,6 +51,7 @@
 #include "convert.cuh"
 #include "grid_sync.cuh"
 #include "launch.h"
+#include "search.cuh"
 
 namespace devscan {
 namespace gated {
@@ -187,15 +188,7 @@ template <int KIND, int V> __device__ __forceinline__ void coefficients(Lanes<V>
 // Index of the last row that begins at or before token n; -1 if none does.
 __device__ __forceinline__ int row_at(const GatedRows &rows, int n)
 {
-    int lo = 0, hi = rows.rows + 1;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(rows.starts + mid) <= n)
-            lo = mid + 1;
-        else
-            hi = mid;
-    }
-    return lo - 1;
+    return first_not(rows.rows + 1, [&](int r) { return __ldg(rows.starts + r) <= n; }) - 1;
 }
 
 // Index of the first of starts[0 .. count) that is at least `value`; count if
@@ -203,18 +196,12 @@ __device__ __forceinline__ int row_at(const GatedRows &rows, int n)
 // two loads behind each other for a thousand rows, instead of ten.
 __device__ __forceinline__ int first_start(const int32_t *starts, int count, int value, int lane)
 {
-    int lo = 0, hi = count;
-    while (lo < hi) {
-        const int step = (hi - lo + 31) / 32;
-        const long long at = lo + static_cast<long long>(lane) * step;
-        const unsigned below = __ballot_sync(kFullMask, at < hi && __ldg(starts + at) < value);
-        const int many = __popc(below);   // of the places looked at
-        if (many == 0) return lo;
-        const long long last = lo + static_cast<long long>(many - 1) * step;   // the last of them that is below
-        lo = static_cast<int>(last + 1);
-        hi = static_cast<int>(last + step < hi ? last + step : hi);
+    Probes p = {0, count};
+    while (p.lo < p.hi) {
+        const long long at = p.place(lane);
+        p.narrow(__popc(__ballot_sync(kFullMask, at < p.hi && __ldg(starts + at) < value)));
     }
-    return lo;
+    return p.lo;
 }
 
 // A place between packed rows: the first row that begins at or behind `share`
