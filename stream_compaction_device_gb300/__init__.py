@@ -790,6 +790,17 @@ def _check_places(places: torch.Tensor, here: int):
     return tokens, choices
 
 
+def _per_pair(t, name: str, places: torch.Tensor, here: int):
+    """Address of fp32 values in the places' order: of their shape (apart from
+    dimensions of 1), or flat; None for None.  Another shape of as many elements,
+    such as [choices, tokens], would be read in an order that is not its own."""
+    if t is not None and t.shape != places.shape:
+        sizes = [n for n in t.shape if n != 1]
+        if len(sizes) > 1 and sizes != [n for n in places.shape if n != 1]:
+            raise ValueError(f"{name} must have the shape of places")
+    return _vector(t, name, _F32, places.numel(), here)
+
+
 def expert_dispatch(x: torch.Tensor, places: torch.Tensor, order: torch.Tensor, out: torch.Tensor | None = None,
                     stream=None) -> torch.Tensor:
     """Copy every token's row of ``x`` (any type, [tokens, width]) to its
@@ -832,7 +843,7 @@ def expert_combine(y: torch.Tensor, places: torch.Tensor, weights: torch.Tensor 
         out = empty(tokens, width, dtype=dtype, device=y.device)
     status = getattr(load(), "expert_combine_" + suffix)(
         y.data_ptr(), _check_rows(y, "y", rows, width, dtype, here), rows, tokens, choices, width, places.data_ptr(),
-        _vector(weights, "weights", _F32, tokens * choices, here), out.data_ptr(),
+        _per_pair(weights, "weights", places, here), out.data_ptr(),
         _check_rows(out, "out", tokens, width, dtype, here), _stream_handle(stream))
     if status:
         _lib.check(status, "expert_combine_" + suffix)
@@ -854,7 +865,7 @@ def expert_combine_backward(grad: torch.Tensor, y: torch.Tensor, places: torch.T
     if y.dim() != 2 or y.shape[1] < 1:
         raise ValueError("y must be [rows, width]")
     rows, width = y.shape
-    dtype, pairs = y.dtype, tokens * choices
+    dtype = y.dtype
     empty = torch.empty if stream is None else _empty_on(stream)
     if grad_y is None:
         grad_y = empty(rows, width, dtype=dtype, device=y.device)
@@ -863,9 +874,9 @@ def expert_combine_backward(grad: torch.Tensor, y: torch.Tensor, places: torch.T
     status = getattr(load(), "expert_combine_backward_" + suffix)(
         grad.data_ptr(), _check_rows(grad, "grad", tokens, width, dtype, here), y.data_ptr(),
         _check_rows(y, "y", rows, width, dtype, here), rows, tokens, choices, width, places.data_ptr(),
-        _vector(weights, "weights", _F32, pairs, here), _vector(order, "order", _I32, rows, here), grad_y.data_ptr(),
+        _per_pair(weights, "weights", places, here), _vector(order, "order", _I32, rows, here), grad_y.data_ptr(),
         _check_rows(grad_y, "grad_y", rows, width, dtype, here),
-        _vector(grad_weights, "grad_weights", _F32, pairs, here), _stream_handle(stream))
+        _per_pair(grad_weights, "grad_weights", places, here), _stream_handle(stream))
     if status:
         _lib.check(status, "expert_combine_backward_" + suffix)
     return grad_y, grad_weights
