@@ -82,12 +82,14 @@ class Model(torch.nn.Module):
         width = x.shape[1]
         x = x + Recurrence.apply(both[:, :width], both[:, width:] + 2, starts)
         top, ids = (x @ self.router).topk(self.choices, dim=1)
-        # every expert gets the same number of rows, so that one batched product has them all
-        first, _, order, places = ds.expert_sort(ids, self.experts, align=self.rows, rows=self.experts * self.rows)
+        # every expert's product has the same number of rows, so that one batched product has them all; one
+        # without tokens has no rows of its own, and takes a row of zeros behind the others
+        first, counts, order, places = ds.expert_sort(ids, self.experts, align=self.rows, rows=self.experts * self.rows)
         xs = Dispatch.apply(x, places, order)
-        at = (first[:-1, None].long() + torch.arange(self.rows, device=x.device)).clamp(max=xs.shape[0] - 1)
+        xs = torch.cat([xs, xs.new_zeros(1, width)])
+        at = torch.where(counts[:, None] > 0, first[:-1, None].long() + torch.arange(self.rows, device=x.device), len(xs) - 1)
         ys = torch.bmm(torch.relu(torch.bmm(xs[at], self.up)), self.down)
-        back = torch.zeros_like(xs).index_copy(0, at.reshape(-1), ys.reshape(-1, width))
+        back = torch.zeros_like(xs).index_copy(0, at.reshape(-1), ys.reshape(-1, width))[:-1]
         x = x + Combine.apply(back, torch.softmax(top, 1), places, order)
         return x @ self.head
 
