@@ -8,7 +8,8 @@ on the one that ``stream`` names (an object or a handle).  What a call makes for
 itself, outputs that it was not given among it, is memory of the stream that it
 runs on; that the tensors which it was given are ready there, and that what it
 returns is ready where it is used, the caller sees to, as with any torch
-operation on two streams.
+operation on two streams.  No call is an autograd function: results carry no
+graph, and the calls of a model's layers warn where a gradient is lost with that.
 ``scan_host`` is the host-buffer entry: the library copies a pinned host
 array to the device, scans it and copies the result back.
 """
@@ -18,6 +19,7 @@ import array
 import contextlib
 import functools
 import operator
+import warnings
 
 import torch
 
@@ -541,6 +543,17 @@ def _value_suffix(t: torch.Tensor) -> str:
     return suffix
 
 
+def _no_graph(name: str, *tensors) -> None:
+    """Tells of a gradient that is lost: the calls are no autograd functions."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                warnings.warn(f"{name} has no autograd graph: its result does not lead back to tensors that require a "
+                              "gradient (call it in the forward and backward of a torch.autograd.Function, or under "
+                              "torch.no_grad)", stacklevel=3)
+                return
+
+
 def _device_of(t: torch.Tensor, name: str) -> int:
     """The device of a call that begins with that tensor: the current one,
     whose stream it takes."""
@@ -637,11 +650,13 @@ def gated_scan(x: torch.Tensor, gate: torch.Tensor, starts: torch.Tensor | None 
     ``final``, which takes h after their last token.  One token per row is the
     decode step.
 
+    Carries no autograd graph; its gradients are :func:`gated_scan_backward`'s.
     Returns (out, final).  ``out`` may be ``x`` itself and ``final`` may be
     ``initial`` itself; without ``final``, rows with slots leave their states in
     ``initial``, and others in a new tensor."""
     suffix = _value_suffix(x)
     here = _device_of(x, "x")
+    _no_graph("gated_scan", x, gate, initial)
     rows, tokens, channels, number, wide = _gated_rows(x, gate, starts, kind)
     empty = torch.empty if stream is None else _empty_on(stream)
     if final is None:
@@ -686,6 +701,7 @@ def gated_scan_backward(grad: torch.Tensor, x: torch.Tensor | None, gate: torch.
     tensor for it."""
     suffix = _value_suffix(y)
     here = _device_of(y, "y")
+    _no_graph("gated_scan_backward", grad, x, gate, y, initial, grad_final)
     rows, tokens, channels, number, wide = _gated_rows(y, gate, starts, kind)
     shape, dtype, device = y.shape, y.dtype, y.device
     if kind == "sigmoid" and x is None:
@@ -809,6 +825,7 @@ def expert_dispatch(x: torch.Tensor, places: torch.Tensor, order: torch.Tensor, 
     there).  Returns ``out`` [rows, width].  The gradient of x is
     ``expert_combine`` of out's, without weights."""
     here = _device_of(x, "x")
+    _no_graph("expert_dispatch", x)
     tokens, choices = _check_places(places, here)
     if x.dim() != 2 or x.shape[1] < 1:
         raise ValueError("x must be [tokens, width]")
@@ -833,6 +850,7 @@ def expert_combine(y: torch.Tensor, places: torch.Tensor, weights: torch.Tensor 
     token without any place gets 0."""
     suffix = _value_suffix(y)
     here = _device_of(y, "y")
+    _no_graph("expert_combine", y, weights)
     tokens, choices = _check_places(places, here)
     if y.dim() != 2 or y.shape[1] < 1:
         raise ValueError("y must be [rows, width]")
@@ -861,6 +879,7 @@ def expert_combine_backward(grad: torch.Tensor, y: torch.Tensor, places: torch.T
     there are neither ``weights`` nor a tensor for it."""
     suffix = _value_suffix(y)
     here = _device_of(y, "y")
+    _no_graph("expert_combine_backward", grad, y, weights)
     tokens, choices = _check_places(places, here)
     if y.dim() != 2 or y.shape[1] < 1:
         raise ValueError("y must be [rows, width]")
@@ -939,8 +958,8 @@ def _norm(tensors, out, max_norm, norm, work, stream):
 def grad_norm(tensors, norm: torch.Tensor | None = None, work: torch.Tensor | None = None,
               stream=None) -> torch.Tensor:
     """2-norm over all elements of ``tensors`` (contiguous float32, float16 or
-    bfloat16, mixed as they come): an fp32 scalar on the device.  Squares neither
-    overflow nor vanish.  ``work`` may pass the scratch (any type,
+    bfloat16, mixed as they come): an fp32 scalar on the device, without an autograd
+    graph.  Squares neither overflow nor vanish.  ``work`` may pass the scratch (any type,
     ``_lib.norm_work_bytes(len(tensors))`` bytes)."""
     return _norm(tensors, None, None, norm, work, stream)[0]
 
