@@ -85,3 +85,59 @@ def test_time_major_arrays_side_by_side(ds):  # noqa: F811
         else:                                                   # one row, and the next one's part is not given
             want, _ = ds.gated_scan(x, gate, kind="sigmoid")
             assert torch.equal(ds.gated_scan(parts[0][:-1], parts[2][:-1], kind="sigmoid", out=across)[0], want)
+
+
+def test_errors_do_not_lean(ds):  # noqa: F811
+    """60,000 tokens through decays next to 1, all terms positive.  Errors that
+    are as often up as down: with memories of M tokens the state's relative error
+    is a sum of M / 2 tokens' worth of independent roundings, of the decay (next
+    to 1 from below: at most 2^-25, variance 2^-50 / 3) and of the running value
+    (at most 2^-24: 2^-48 / 3), a standard deviation of 2^-24 sqrt(5 M / 24).
+    Five of those; log: M = 2,000, and for its series four roundings of values of
+    10^-3 at most, M / 2 of them; sigmoid: M = 1,740, and the hardware's
+    exponential, which may lean by (3 + 1.2 |g|) 2^-23 in b and as much, times
+    M (1 - a), in a.  A decay off to one side by a tenth of 2^-24 is 1.2e-5 and
+    1.0e-5 off."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    n, c = 60000, 64
+    x = torch.randn(1, n, c, generator=g, device="cuda").abs_()
+    for kind, memory, lean in (("log", 2000, 1000 * 4 * 1e-3 * 2.0 ** -24), ("sigmoid", 1740, 2 * (3 + 1.2 * 8) * 2.0 ** -23)):
+        gate = torch.rand(1, n, c, generator=g, device="cuda")
+        gate = -gate * 1e-3 if kind == "log" else 7 + gate
+        final = ds.gated_scan(x, gate, kind=kind)[1]
+        a = torch.exp(gate.double()) if kind == "log" else torch.sigmoid(gate.double())
+        b = x.double() * (1 if kind == "log" else torch.sigmoid(-gate.double()))
+        h = torch.zeros(c, dtype=torch.float64, device="cuda")
+        for t in range(n):
+            h = a[0, t] * h + b[0, t]
+        error = (final[0].double() - h) / h
+        limit = 5 * 2.0 ** -24 * (5 * memory / 24) ** 0.5 + lean
+        assert error.abs().max().item() < limit < 1e-5, (kind, error.abs().max().item(), limit)
+
+
+def test_what_rounded_outputs_cost_the_gates(ds):  # noqa: F811
+    """The backward call takes h as it was rounded to the output's type.  Where x
+    moves slowly h' - x is small beside h', and the gate's gradient is then off
+    by at most |w| a (1 - a) half |h'| from that of the recurrence that is not
+    rounded: more than its own rounding in 16 bits, nothing to speak of in 32."""
+    rng = np.random.default_rng(8)
+    rows, tokens, channels = 1, 400, 32
+    shape = (rows, tokens, channels)
+    slow = 1 + 0.02 * np.sin(np.arange(tokens) / 40)[None, :, None] + 0.002 * rng.standard_normal(shape)
+    shares = {}
+    for dtype in (F32, F16, BF16):
+        x, gate, grad = cuda(slow, dtype), cuda(rng.standard_normal(shape) + 1, F32), cuda(rng.standard_normal(shape), dtype)
+        spans = ref.rows_of(None, tokens, rows)
+        initial = torch.ones(1, channels, device="cuda")
+        y = ds.gated_scan(x, gate, initial=initial, kind="sigmoid")[0]
+        got = ds.gated_scan_backward(grad, x, gate, y, initial=initial, kind="sigmoid")[1]
+        h, h_room, _, _ = ref.scan(flat(x), flat(gate), "sigmoid", spans, np.ones((1, channels)))
+        value, room = ref.scan_backward(flat(grad), flat(x), flat(gate), h, "sigmoid", spans, np.ones((1, channels)))["gate"]
+        a = 1 / (1 + np.exp(-flat(gate)))
+        w = np.abs(ref.scan_backward(flat(grad), flat(x), flat(gate), h, "sigmoid", spans)["x"][0]) / (1 - a)
+        before = np.vstack([np.zeros((1, channels)), ref.HALF[dtype] * np.abs(h[:-1]) + h_room[:-1] * 2])   # the state is fp32
+        cost = w * a * (1 - a) * before
+        ref.close(got.reshape(-1, channels), value, room + cost, f"{dtype}")
+        error = np.abs(ref.as64(got)[0] - value)
+        shares[dtype] = np.linalg.norm(error) / np.linalg.norm(value)
+    assert shares[F32] < 1e-4 < shares[BF16], shares
