@@ -141,3 +141,36 @@ def test_what_rounded_outputs_cost_the_gates(ds):  # noqa: F811
         error = np.abs(ref.as64(got)[0] - value)
         shares[dtype] = np.linalg.norm(error) / np.linalg.norm(value)
     assert shares[F32] < 1e-4 < shares[BF16], shares
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("how", ["shared", "drawn"])
+def test_decays_that_repeat(ds, how, dtype):  # noqa: F811
+    """Decays next to 1 that all tokens share, or that 16 bits leave few of: what
+    is rounded alike in every run of tokens does not add up.  A run (24 tokens
+    forward, 16 backward, of long rows) leaves one rounding of its product, and the
+    product of the runs one more, each of variance 2^-50 / 3 over the channels,
+    which have decays of their own; a channel's memory of M <= 4,900 tokens adds
+    M / 24 (16) of them, all alike: the error's norm over the channels is at most
+    that of the longest memory, beside which independent roundings (2^-24 sqrt(5 M
+    / 24) as in test_errors_do_not_lean, of which the runs' sums have a part) are
+    small; both are in the limit.  Multiplied up token by token, (1 - 2^-11)^24
+    alone is 4 times 2^-24 off."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    n, c = 20000, 256
+    slow = torch.exp(torch.rand(c, generator=g, device="cuda") * 5 - 8.5)
+    noise = torch.ones(1, n, c, device="cuda") if how == "shared" else 2 * torch.rand(1, n, c, generator=g, device="cuda")
+    gate = torch.exp(-slow * noise).to(dtype)
+    x = torch.rand(1, n, c, generator=g, device="cuda").to(dtype)
+    y, final = ds.gated_scan(x, gate)
+    state = torch.zeros(1, c, device="cuda")
+    back = ds.gated_scan_backward(x, None, gate, y, initial=state)[2]
+    a, b = gate[0].double(), x[0].double()
+    h, f = torch.zeros(c, dtype=torch.float64, device="cuda"), torch.zeros(c, dtype=torch.float64, device="cuda")
+    for t in range(n):
+        h = a[t] * h + b[t]
+        f = a[n - 1 - t] * (f + b[n - 1 - t])
+    for got, want, run in ((final[0], h, 24), (back[0], f, 16)):
+        limit = 4900 / run * (2 / 3) ** 0.5 * 2.0 ** -25 + 2.0 ** -24 * (5 * 4900 / 24) ** 0.5 / 4
+        error = ((got.double() - want).norm() / want.norm()).item()
+        assert error < limit, (how, dtype, run, error, limit)
