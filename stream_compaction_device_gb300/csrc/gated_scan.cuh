@@ -1027,14 +1027,14 @@ gated_scan_backward_kernel(const __grid_constant__ GatedBackwardCall p)
             __syncwarp();   // the stage has been read
             continue;
         }
+        // no gradient for first gates without a state: not 0 times an infinity or NaN
+        const unsigned no_gate = e.outside | (!SIGMOID && p.initial == nullptr ? e.first : 0u);
 #pragma unroll
         for (int i = 0; i < L; ++i) {
-            const bool out = (e.outside >> i) & 1u;
             Lanes<V> v = d[i] + f, before = R::value(stage, 1, i, lane), gx, gg;
 #pragma unroll
             for (int k = 0; k < V; ++k) v.v[k] = (cut >> i) & 1u ? d[i].v[k] : v.v[k];
             f = a[i] * v;
-            bool unused = false;   // a first gate without a state: no 0 times an infinity or NaN
             if ((e.first >> i) & 1u) {
                 const int row = e.row_of(i);
                 const float *from = state_of(p.rows, p.initial, row);
@@ -1044,10 +1044,9 @@ gated_scan_backward_kernel(const __grid_constant__ GatedBackwardCall p)
                     if (p.grad_initial != nullptr && live)
                         p.grad_initial[static_cast<size_t>(row) * p.rows.channels + w.channel + k] = f.v[k];
                 }
-                unused = !SIGMOID && from == nullptr;
             }
             gradients(i, v, before, gx, gg);
-            a[i] = out ? all<V>(0.0f) : gx, d[i] = out || unused ? all<V>(0.0f) : gg;
+            a[i] = (e.outside >> i) & 1u ? all<V>(0.0f) : gx, d[i] = (no_gate >> i) & 1u ? all<V>(0.0f) : gg;
         }
         if (step + 1 < rounds) hand_on(s_x, (step + 1) & 1, w.blocks, w.rank, warp, lane, f);
         if (live && r.count > 0) {
