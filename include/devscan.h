@@ -461,7 +461,7 @@ devscan_status sample_tokens_bf16(const uint16_t *logits, size_t rows, size_t vo
  *   DEVSCAN_GATE_LOG     : a = exp(gate),               b = x;
  *   DEVSCAN_GATE_SIGMOID : a = 1 / (1 + exp(-gate)),    b = (1 - a) x.
  * out is h in x's type; the recurrence itself runs in fp32.  Gates are meant
- * to have |a| <= 1: products of up to 1,024 of them are formed, and where one
+ * to have |a| <= 1: products of up to 192 of them are formed, and where one
  * overflows so may what is 0 times it.
  *
  *   x, gate, out : device arrays of rows of tokens of `channels` neighbouring
@@ -504,7 +504,11 @@ devscan_status sample_tokens_bf16(const uint16_t *logits, size_t rows, size_t vo
  * h' being y of the token before, or initial; a first gate that does not count
  * has the gradient 0, whatever it holds.  x is read for sigmoid only (else
  * it may be NULL).  States lie by row (no slots); tokens in no row get 0;
- * outputs overlap nothing but as above.
+ * outputs overlap nothing but as above.  Since h' is y, and so rounded to y's type,
+ * a sigmoid gate's gradient is off by up to |w| a (1 - a) half a step of |h'|: where
+ * x moves slowly, and h' - x is small beside h', that may be much of it in 16 bits
+ * (x that moves by 2% around 1: 9% of the gradient's norm in fp16, 47% in bf16, 2e-5
+ * in fp32; random x: 9e-5, 8e-4, 1e-7).
  *
  * Traffic: each value once.  No scratch; the same call gives the same bits.
  * ------------------------------------------------------------------------- */
@@ -587,6 +591,7 @@ devscan_status gated_scan_backward_bf16(const uint16_t *grad, size_t grad_row_st
  *
  * Calls whose tokens and an eighth of whose rows pass INT32_MAX together may be
  * more than a launch holds, and are then refused (DEVSCAN_ERR_INVALID).
+ * `order` and `places` are one sort's; those of two go together unnoticed.
  * Places outside 0 .. rows - 1 count as none; two pairs with the same place
  * (expert_sort gives none) leave either's row.  No buffer that is written may
  * overlap another (DEVSCAN_ERR_INVALID).  No scratch; the same call gives the
@@ -634,7 +639,7 @@ devscan_status expert_combine_backward_bf16(const uint16_t *grad, size_t grad_st
  *   out   = in min(1, max_norm / (norm + 1e-6)), the factor in fp32, the product
  * rounded once.  A norm that is infinite (in fp32, as it is given) or NaN clips
  * nothing (out = in): the caller, who reads it, decides.  Squares neither overflow nor vanish, whatever the
- * values' size; sums are fp32 for 64 values and fp64 above, in a fixed order, so
+ * values' size; sums are fp32 for 32 values at most and fp64 above, in a fixed order, so
  * that the same call gives the same bits.
  *
  *   tensors : HOST array of `count` (at most 2^24), read during the call; each

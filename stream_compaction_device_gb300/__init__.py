@@ -643,7 +643,8 @@ def gated_scan(x: torch.Tensor, gate: torch.Tensor, starts: torch.Tensor | None 
 
     ``x`` (float32, float16 or bfloat16) is [rows, tokens, channels], or
     [tokens, channels]: one row, or with ``starts`` (int32, rows + 1, as
-    ``slot_map`` gives them) packed rows; tokens in no row get 0.  ``gate`` has
+    ``slot_map`` gives them) packed rows, of those tokens that there are; tokens in
+    no row get 0.  ``gate`` has
     x's shape, and its type or float32.  Only the channels need to be
     contiguous.  ``initial`` (fp32 [states, channels]) holds the rows' h before
     their first token; ``slots`` (int32 per row) says where in it, and in
@@ -968,7 +969,8 @@ def clip_grad_norm(tensors, max_norm: float, out=None, norm: torch.Tensor | None
                    work: torch.Tensor | None = None, stream=None):
     """Scale ``tensors`` by min(1, max_norm / (norm + 1e-6)), norm being that of
     :func:`grad_norm` over all of them; in place, or into the tensors of
-    ``out``.  A norm that is infinite or NaN clips nothing.  Returns (norm, the
+    ``out``.  Tensors that are written must not overlap others in part (that is
+    not checked).  A norm that is infinite or NaN clips nothing.  Returns (norm, the
     list of clipped tensors); nothing is read back to the host."""
     max_norm = float(max_norm)
     if not max_norm >= 0:

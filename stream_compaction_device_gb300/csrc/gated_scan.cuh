@@ -34,8 +34,8 @@
 //
 // What bounds it (device time, share of the measured copy rate): 8 x 4096 x 4096
 // bf16 sigmoid 158 us forward (76%) and 266-270 us backward (90%): 52 and 91
-// instructions per warp and token, with issue slots 62% busy; decay, at 37, is
-// nearer to memory.  One row of 65,536 x 2048 bf16 log 171 us (70%): eight
+// instructions per warp and token, with issue slots 62% busy; decay, at 38, is
+// nearer to memory (135 us, 89%).  One row of 65,536 x 2048 bf16 log 171 us (70%): eight
 // blocks to a cluster, and every round waits for the slowest of 64 warps
 // (barrier stalls first, issue slots 48% busy).  Measured and dropped there: a
 // round finished while the next is begun (223 us: the barrier's release waits
@@ -1060,8 +1060,8 @@ gated_scan_backward_kernel(const __grid_constant__ GatedBackwardCall p)
 
 // ---------------------------------------------------------------------------
 // One token per row: a thread per N channels of a row, 16 bytes of x where that
-// is aligned (512 x 4096 bf16 with fp32 states: 4.9 us, 89% of the copy rate, and
-// 7.7 with 4 bytes).
+// is aligned (512 x 4096 bf16 with fp32 states, 29 MB: 7.1 us from memory, 62% of the
+// copy rate; where L2 holds them 4.3, and 7.7 with 4 bytes).
 // ---------------------------------------------------------------------------
 template <typename T, int N> constexpr int kPiece = N * sizeof(T) > 16 ? 16 / static_cast<int>(sizeof(T)) : N;   // values of an access
 template <typename T, int N> __device__ __forceinline__ void load_values(const T *from, float (&v)[N])
@@ -1111,7 +1111,8 @@ __global__ void __launch_bounds__(kStepThreads) gated_step_kernel(const __grid_c
 
 // A few tokens per row (a draft's, checked at once): a thread goes through its
 // channels' tokens, four of them in flight (512 rows x 4096 bf16 sigmoid with
-// states: 2 tokens 7.3 us, 4 11.4, 16 58; clusters took 20.5, 29 and 84).
+// states, where L2 holds them: 2 tokens 7.0 us, 4 10.4, 16 59; clusters took 20.5,
+// 29 and 84.  From memory 12.1, 19.0 and 58).
 constexpr int kFewAtOnce = 4;
 template <typename X, typename G, int N, int KIND>
 __global__ void __launch_bounds__(kStepThreads) gated_few_kernel(const __grid_constant__ GatedScanCall p, unsigned lanes, unsigned blocks_per_row,
@@ -1235,6 +1236,7 @@ inline void plan_long(GatedRows &rows, int places_per_sm, int sms)
 
 // Whether rows are long enough for many tokens per round (forward, log: 16 x
 // 1024 x 4096 bf16 90 us with many and 76 with few; 2 x 8192 x 1024 32 and 37).
+// Packed rows go by their average: the host does not know their lengths.
 inline bool many_tokens(const GatedRows &rows) { return rows.all() / static_cast<unsigned>(rows.rows > 0 ? rows.rows : 1) >= 2048; }
 
 template <typename Call>
@@ -1298,7 +1300,7 @@ cudaError_t step(const GatedScanCall &call, cudaStream_t s)
     return cudaGetLastError();
 }
 // Whether a thread per channels goes through a row's tokens: where they are few,
-// or rows make up for it (sigmoid, clusters against this: 1 x 8 x 4096 bf16 4.7 and
+// or rows make up for it (sigmoid, inputs in L2, clusters against this: 1 x 8 x 4096 bf16 4.7 and
 // 4.3 us, 1 x 16 4.5 and 6.8, 8 x 32 6.9 and 11.2; 64 x 32 x 1024 12.0 and 11.5, 64 x 32
 // x 4096 22.5 and 13.0, 64 x 64 35.7 and 47.5).
 inline bool few_tokens(const GatedRows &rows, size_t lanes)

@@ -11,7 +11,7 @@
 // launch is a programmatic dependent: its blocks start as the first one's end
 // and load their first chunk before they wait for the norm.
 //
-// Sums: a thread adds the squares of a chunk's share (64 values at most) in
+// Sums: a thread adds the squares of a chunk's share (32 values of 16 bits, 16 of 32) in
 // fp32 and its shares in fp64.  Where a share's fp32 sum leaves the range in
 // which no square that matters is lost or overflows, the share is added again
 // with its values times a power of two (64 M values of 1e-25:
