@@ -143,9 +143,11 @@ def test_what_rounded_outputs_cost_the_gates(ds):  # noqa: F811
     assert shares[F32] < 1e-4 < shares[BF16], shares
 
 
-@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("dtype,gate_dtype,sign", [(F32, F32, "plus"), (F32, F32, "minus"), (F32, F32, "in turn"), (F16, F16, "plus"),
+                                                   (F16, F16, "minus"), (F16, F16, "in turn"), (BF16, BF16, "plus"),
+                                                   (BF16, BF16, "minus"), (BF16, F32, "plus")])
 @pytest.mark.parametrize("how", ["shared", "drawn"])
-def test_decays_that_repeat(ds, how, dtype):  # noqa: F811
+def test_decays_that_repeat(ds, how, dtype, gate_dtype, sign):  # noqa: F811
     """Decays next to 1 that all tokens share, or that 16 bits leave few of: what
     is rounded alike in every run of tokens does not add up.  A run (24 tokens
     forward, 16 backward, of long rows) leaves one rounding of its product, and the
@@ -160,7 +162,10 @@ def test_decays_that_repeat(ds, how, dtype):  # noqa: F811
     n, c = 20000, 256
     slow = torch.exp(torch.rand(c, generator=g, device="cuda") * 5 - 8.5)
     noise = torch.ones(1, n, c, device="cuda") if how == "shared" else 2 * torch.rand(1, n, c, generator=g, device="cuda")
-    gate = torch.exp(-slow * noise).to(dtype)
+    gate = torch.exp(-slow * noise)
+    if sign != "plus":
+        gate[:, ::1 if sign == "minus" else 2] *= -1
+    gate = gate.to(gate_dtype)
     x = torch.rand(1, n, c, generator=g, device="cuda").to(dtype)
     y, final = ds.gated_scan(x, gate)
     state = torch.zeros(1, c, device="cuda")
@@ -173,4 +178,4 @@ def test_decays_that_repeat(ds, how, dtype):  # noqa: F811
     for got, want, run in ((final[0], h, 24), (back[0], f, 16)):
         limit = 4900 / run * (2 / 3) ** 0.5 * 2.0 ** -25 + 2.0 ** -24 * (5 * 4900 / 24) ** 0.5 / 4
         error = ((got.double() - want).norm() / want.norm()).item()
-        assert error < limit, (how, dtype, run, error, limit)
+        assert error < limit, (how, dtype, sign, run, error, limit)
